@@ -526,6 +526,198 @@ typedef struct {
 
 kda_status_t kda_prep(const kda_prep_args* args, void* stream);
 
+/*
+ * Full attention beside the recurrence, and the paged cache it reads.
+ *
+ * "From KV Cache to Depth Attention", Technical Details: the stack
+ * interleaves KDA layers with full-attention layers (3:1), which keep a
+ * key and a value for every token.  These calls run such a layer's attention
+ * with grouped heads: H query heads share H_kv key heads (H a multiple of
+ * H_kv, query head h reads key head h / (H / H_kv)), all of head_dim
+ * channels.  For query row i at position p_i of its sequence
+ *
+ *   o_i = sum_{j <= p_i} w_ij v_j,   w_ij = softmax over j <= p_i of scale q_i . k_j
+ *
+ * A row that may attend nothing (p_i < 0) gets o = 0.  A value or key at a
+ * position a row may not attend never reaches that row through its weight,
+ * which is exactly 0 there; whatever the cache or the packed tensors hold
+ * behind a sequence's end (infinities and NaN among it) changes nothing.
+ * Softmax statistics and sums are fp32; with bf16 inputs the weights are
+ * rounded to bf16 before they multiply v (the tensor cores' operand type),
+ * an error of at most 2^-8 of each weight, as o's own rounding to bf16.
+ *
+ * The paged cache.  k_cache and v_cache are [num_pages, page_size, H_kv,
+ * head_dim] in in_dtype.  page_size is a power of two in 16..1024.  A pool of
+ * num_rows rows (one per request the host tracks, as the state pool of the
+ * decode has slots) holds the requests' pages: block_table [num_rows,
+ * max_pages] int32 and kv_lens [num_rows] int64.  Position x of row r lives
+ * in slot block_table[r][x / page_size] * page_size + x % page_size, a slot
+ * being an index into the caches seen as [num_pages * page_size, H_kv,
+ * head_dim].  One step of a serving host:
+ *
+ *   kda_kv_plan     pages and slots for the new tokens, kv_lens advanced
+ *   kda_kv_write    the new k and v rows into their slots
+ *   kda_attn_paged  the new tokens over everything cached, themselves included
+ *   kda_kv_release  (for finished requests) their pages back to the free list
+ *
+ * `rows` names the row of each request of the batch (request s is row s if
+ * NULL); a negative row skips the request.
+ *
+ * `status` of these calls: device int32 or NULL, into which the kernels OR
+ * flags (never cleared by the library): 1 (malformed cu_seqlens), 8 (bounded
+ * wait expired), 32 (a malformed row, length, page or slot), 64 (the free
+ * list ran out), 128 (a sequence longer than max_seqlen).
+ */
+#define KDA_ATTN_MAX_GROUP 128 /* largest num_heads / num_kv_heads */
+
+/*
+ * Causal attention over packed whole prompts: sequence s holds tokens
+ * [cu_seqlens[s], cu_seqlens[s+1]), p_i is the token's index in it.  A
+ * malformed sequence (flag 1) is skipped; rows of o behind the last sequence
+ * are left as they were.
+ */
+typedef struct {
+  int32_t num_seqs;            /* N >= 1                                          */
+  int32_t num_heads;           /* H query heads                                   */
+  int32_t num_kv_heads;        /* H_kv, divides H; H / H_kv <= KDA_ATTN_MAX_GROUP */
+  int32_t head_dim;            /* in {16, 32, 64, 128, 256}                       */
+  int64_t total_tokens;        /* T, host-known upper bound of cu_seqlens[N]      */
+  const int64_t* cu_seqlens;   /* device [N+1], cu[0] = 0, non-decreasing         */
+  kda_dtype_t in_dtype;        /* dtype of q, k, v and o                          */
+  const void* q;               /* device [T, H, head_dim]                         */
+  const void* k;               /* device [T, H_kv, head_dim]                      */
+  const void* v;               /* device [T, H_kv, head_dim]                      */
+  float scale;                 /* of the logits, usually 1 / sqrt(head_dim)       */
+  void* o;                     /* device [T, H, head_dim]                         */
+  int32_t* status;             /* device int32 or NULL (see above)                */
+} kda_attn_prefill_args;
+
+/* Device workspace bytes (host-side fields only); 0 if the arguments are
+ * invalid.  Contents need not be initialised; not to be used by two calls in
+ * flight. */
+size_t kda_attn_prefill_workspace_size(const kda_attn_prefill_args* args);
+kda_status_t kda_attn_prefill(const kda_attn_prefill_args* args, void* ws, size_t ws_bytes,
+                              void* stream);
+
+/*
+ * Attention of each request's new tokens (one or a chunk) over the paged
+ * cache, which already holds them: of the L_s = cu_seqlens[s+1] -
+ * cu_seqlens[s] new tokens of request s, in row r with n = kv_lens[r] cached
+ * positions, token i is at position p_i = n - L_s + i.  A request with a
+ * malformed row or length is skipped (flag 32; 128 when L_s > max_seqlen); a
+ * block-table entry outside the cache is flagged (32) and read as a page of
+ * zeros.  Entries past a request's last position are never read.
+ */
+typedef struct {
+  int32_t num_seqs;            /* N >= 1 requests                                 */
+  int32_t num_heads, num_kv_heads, head_dim; /* as above                          */
+  int64_t total_tokens;        /* T, host-known upper bound of cu_seqlens[N]      */
+  const int64_t* cu_seqlens;   /* device [N+1] over the new tokens                */
+  int32_t max_seqlen;          /* host-known upper bound of every L_s; 0 = T      */
+  kda_dtype_t in_dtype;        /* dtype of q, the caches and o                    */
+  const void* q;               /* device [T, H, head_dim]                         */
+  const void* k_cache;         /* device [num_pages, page_size, H_kv, head_dim]   */
+  const void* v_cache;
+  int32_t num_pages, page_size;
+  const int32_t* block_table;  /* device [num_rows, max_pages]                    */
+  const int64_t* kv_lens;      /* device [num_rows], new tokens included          */
+  int32_t num_rows, max_pages;
+  const int32_t* rows;         /* device [N] or NULL                              */
+  float scale;
+  void* o;                     /* device [T, H, head_dim]                         */
+  int32_t* status;
+} kda_attn_paged_args;
+
+size_t kda_attn_paged_workspace_size(const kda_attn_paged_args* args);
+kda_status_t kda_attn_paged(const kda_attn_paged_args* args, void* ws, size_t ws_bytes,
+                            void* stream);
+
+/*
+ * Pages and slots for the new tokens of a batch.  Request s (row r) has
+ * c = kv_lens_in[r] cached positions and L_s new tokens.  It needs
+ * ceil((c + L_s) / page_size) - ceil(c / page_size) more pages; the j-th of
+ * them is free_pages[count - 1 - (e_s + j)], with count = *free_count_in and
+ * e_s the pages needed by the requests before it.  The call writes them into
+ * block_table, the slot of every new token into slot_map (-1 for the tokens of
+ * a skipped or refused request and for those at or past cu_seqlens[N]),
+ * c + L_s into kv_lens_out[r] and the pages left into *free_count_out.
+ *   - A request whose pages end past the free list is refused (flag 64):
+ *     nothing of it is planned, kv_lens_out[r] = c.  Requests that need no
+ *     page are still served.
+ *   - So is a request (flag 32) with a row outside the pool, c outside
+ *     [0, max_pages * page_size], c + L_s past it, or a row that an earlier
+ *     request of the batch names; and (flag 1) one with malformed
+ *     cu_seqlens.
+ *   - The outputs may be the inputs (kv_lens_out == kv_lens_in, free_count_out
+ *     == free_count_in); where they are not, rows outside the batch are not
+ *     written.  free_pages itself is not changed.
+ */
+typedef struct {
+  int32_t num_seqs;            /* N >= 1                                          */
+  int64_t total_tokens;        /* T entries of slot_map                           */
+  const int64_t* cu_seqlens;   /* device [N+1]                                    */
+  int32_t page_size, num_pages;
+  int32_t num_rows, max_pages;
+  const int32_t* rows;         /* device [N] or NULL                              */
+  int32_t* block_table;        /* device [num_rows, max_pages], entries added     */
+  const int64_t* kv_lens_in;   /* device [num_rows]                               */
+  int64_t* kv_lens_out;        /* device [num_rows]                               */
+  const int32_t* free_pages;   /* device [num_pages], the first count are free    */
+  const int32_t* free_count_in;/* device [1]                                      */
+  int32_t* free_count_out;     /* device [1]                                      */
+  int64_t* slot_map;           /* device [T]                                      */
+  int32_t* status;
+} kda_kv_plan_args;
+
+size_t kda_kv_plan_workspace_size(const kda_kv_plan_args* args);
+kda_status_t kda_kv_plan(const kda_kv_plan_args* args, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Pages of finished requests back to the free list: for every row in `rows`,
+ * in order, its ceil(kv_lens[r] / page_size) pages are appended to free_pages
+ * from *free_count on, which advances, and kv_lens[r] becomes 0.  A row named
+ * twice is released once; a row outside the pool or with a malformed length,
+ * and rows whose pages would pass num_pages, are left alone (flag 32);
+ * negative rows are skipped.
+ */
+typedef struct {
+  int32_t num_release;         /* M >= 0 entries of rows                          */
+  int32_t page_size, num_pages;
+  int32_t num_rows, max_pages;
+  const int32_t* rows;         /* device [M]                                      */
+  const int32_t* block_table;  /* device [num_rows, max_pages]                    */
+  int64_t* kv_lens;            /* device [num_rows]                               */
+  int32_t* free_pages;         /* device [num_pages]                              */
+  int32_t* free_count;         /* device [1]                                      */
+  int32_t* status;
+} kda_kv_release_args;
+
+size_t kda_kv_release_workspace_size(const kda_kv_release_args* args);
+kda_status_t kda_kv_release(const kda_kv_release_args* args, void* ws, size_t ws_bytes,
+                            void* stream);
+
+/*
+ * The new keys and values into their slots: k_cache[slot_map[t]] = k[t],
+ * v_cache[slot_map[t]] = v[t], the caches seen as [num_slots, H_kv, head_dim].
+ * A negative slot skips the token; a slot at or past num_slots is flagged
+ * (32) and skipped.  Two tokens must not share a slot (which of them stays
+ * is then not defined).
+ */
+typedef struct {
+  int64_t total_tokens;        /* T >= 0                                          */
+  int32_t num_kv_heads, head_dim;
+  kda_dtype_t in_dtype;
+  const void* k;               /* device [T, H_kv, head_dim]                      */
+  const void* v;
+  const int64_t* slot_map;     /* device [T]                                      */
+  int64_t num_slots;           /* num_pages * page_size                           */
+  void* k_cache;
+  void* v_cache;
+  int32_t* status;
+} kda_kv_write_args;
+
+kda_status_t kda_kv_write(const kda_kv_write_args* args, void* stream);
+
 /* Static description of a status code. */
 const char* kda_status_string(kda_status_t status);
 

@@ -7,7 +7,9 @@ built, or no CUDA device is present, the calls raise.
 
 The names follow the C ABI: ``kda_prefill``, ``kda_prefill_workspace_size``,
 ``kda_prefill_device_status``, ``kda_snapshot_plan``, ``kda_decode_step``,
-``kda_prep``, ``kda_status_string``, ``kda_prefill_host`` (host buffers).
+``kda_prep``, ``kda_status_string``, ``kda_prefill_host`` (host buffers), and
+for the full-attention layers ``kda_attn_prefill``, ``kda_attn_paged``,
+``kda_kv_plan``, ``kda_kv_write``, ``kda_kv_release``.
 ``prefill`` and ``prefill_host`` are conveniences that allocate outputs and
 workspace with torch and call ``kda_prefill`` / ``kda_prefill_host``.
 """
@@ -39,7 +41,10 @@ EXPORTED = ("kda_prefill_workspace_size", "kda_prefill", "kda_prefill_noalloc",
             "kda_prefix_cache_create", "kda_prefix_cache_destroy", "kda_prefix_cache_entries",
             "kda_prefix_cache_lookup", "kda_prefix_cache_reserve",
             "kda_prefill_device_status", "kda_snapshot_plan", "kda_decode_step", "kda_prep",
-            "kda_status_string", "kda_version", "kda_prefill_schedule")
+            "kda_status_string", "kda_version", "kda_prefill_schedule",
+            "kda_attn_prefill_workspace_size", "kda_attn_prefill", "kda_attn_paged_workspace_size",
+            "kda_attn_paged", "kda_kv_plan_workspace_size", "kda_kv_plan",
+            "kda_kv_release_workspace_size", "kda_kv_release", "kda_kv_write")
 NOALLOC_SCRATCH_BYTES = 64 << 20  # fixed workspace behind kda_prefill_noalloc
 
 
@@ -99,6 +104,44 @@ class PrepArgs(ctypes.Structure):
                 ("layer", ctypes.POINTER(LayerArgs))]
 
 
+class AttnPrefillArgs(ctypes.Structure):
+    _fields_ = [("num_seqs", c_i32), ("num_heads", c_i32), ("num_kv_heads", c_i32),
+                ("head_dim", c_i32), ("total_tokens", c_i64), ("cu_seqlens", c_vp),
+                ("in_dtype", ctypes.c_int), ("q", c_vp), ("k", c_vp), ("v", c_vp),
+                ("scale", c_f32), ("o", c_vp), ("status", c_vp)]
+
+
+class AttnPagedArgs(ctypes.Structure):
+    _fields_ = [("num_seqs", c_i32), ("num_heads", c_i32), ("num_kv_heads", c_i32),
+                ("head_dim", c_i32), ("total_tokens", c_i64), ("cu_seqlens", c_vp),
+                ("max_seqlen", c_i32), ("in_dtype", ctypes.c_int), ("q", c_vp),
+                ("k_cache", c_vp), ("v_cache", c_vp), ("num_pages", c_i32), ("page_size", c_i32),
+                ("block_table", c_vp), ("kv_lens", c_vp), ("num_rows", c_i32),
+                ("max_pages", c_i32), ("rows", c_vp), ("scale", c_f32), ("o", c_vp),
+                ("status", c_vp)]
+
+
+class KvPlanArgs(ctypes.Structure):
+    _fields_ = [("num_seqs", c_i32), ("total_tokens", c_i64), ("cu_seqlens", c_vp),
+                ("page_size", c_i32), ("num_pages", c_i32), ("num_rows", c_i32),
+                ("max_pages", c_i32), ("rows", c_vp), ("block_table", c_vp),
+                ("kv_lens_in", c_vp), ("kv_lens_out", c_vp), ("free_pages", c_vp),
+                ("free_count_in", c_vp), ("free_count_out", c_vp), ("slot_map", c_vp),
+                ("status", c_vp)]
+
+
+class KvReleaseArgs(ctypes.Structure):
+    _fields_ = [("num_release", c_i32), ("page_size", c_i32), ("num_pages", c_i32),
+                ("num_rows", c_i32), ("max_pages", c_i32), ("rows", c_vp), ("block_table", c_vp),
+                ("kv_lens", c_vp), ("free_pages", c_vp), ("free_count", c_vp), ("status", c_vp)]
+
+
+class KvWriteArgs(ctypes.Structure):
+    _fields_ = [("total_tokens", c_i64), ("num_kv_heads", c_i32), ("head_dim", c_i32),
+                ("in_dtype", ctypes.c_int), ("k", c_vp), ("v", c_vp), ("slot_map", c_vp),
+                ("num_slots", c_i64), ("k_cache", c_vp), ("v_cache", c_vp), ("status", c_vp)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -148,6 +191,14 @@ def lib() -> ctypes.CDLL:
             L.kda_decode_step.restype = ctypes.c_int
             L.kda_prep.argtypes = [ctypes.POINTER(PrepArgs), c_vp]
             L.kda_prep.restype = ctypes.c_int
+            for name, args in (("kda_attn_prefill", AttnPrefillArgs), ("kda_attn_paged", AttnPagedArgs),
+                               ("kda_kv_plan", KvPlanArgs), ("kda_kv_release", KvReleaseArgs)):
+                size, call = getattr(L, name + "_workspace_size"), getattr(L, name)
+                size.argtypes, size.restype = [ctypes.POINTER(args)], ctypes.c_size_t
+                call.argtypes = [ctypes.POINTER(args), c_vp, ctypes.c_size_t, c_vp]
+                call.restype = ctypes.c_int
+            L.kda_kv_write.argtypes = [ctypes.POINTER(KvWriteArgs), c_vp]
+            L.kda_kv_write.restype = ctypes.c_int
             L.kda_status_string.argtypes = [ctypes.c_int]
             L.kda_status_string.restype = ctypes.c_char_p
             L.kda_version.restype = ctypes.c_char_p
@@ -781,3 +832,289 @@ def prep(q, k, g, b, cu_seqlens, stream=None, **conv):
     beta = torch.empty(T, H, **f)
     kda_prep(q, k, g, b, cu_seqlens, qhat, khat, G, beta, stream=stream, **conv)
     return qhat, khat, G, beta
+
+
+# ----------------------------------------------------------------- full attention and its cache
+def _same_device(**tensors):
+    """The device of the tensors given (None entries left out); all must share one."""
+    dev = first = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if dev is None:
+            dev, first = t.device, name
+        elif t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, {first} on {dev}")
+    return dev
+
+
+def _shape(name, t, want):
+    if tuple(t.shape) != tuple(want):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(want)}")
+
+
+def _launch(fn, what, device, args, workspace, stream):
+    """Calls a C entry on ``stream`` (None: the current stream of the tensors'
+    device) with that device current."""
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _launch(fn, what, device, args, workspace, stream)
+    if workspace is None:
+        _check(fn(ctypes.byref(args), _stream(stream)), what)
+    else:
+        _check(fn(ctypes.byref(args), workspace.data_ptr(), workspace.numel(), _stream(stream)), what)
+
+
+class _CacheCall:
+    """What the planned calls share: the argument block, the workspace and the
+    status word are made once; ``run()`` only launches kernels."""
+    _name = ""
+
+    def _plan(self, device, args, keep, status):
+        self._device, self.args, self._keep = device, args, keep
+        self.status = torch.zeros(1, dtype=torch.int32, device=device) if status is None else status
+        if self.status.numel() < 1:
+            raise ValueError("status needs one int32")
+        _same_device(status=self.status, other=keep[0])
+        args.status = _ptr(self.status, torch.int32, "status")
+        self._fn, self.workspace = getattr(lib(), self._name), None
+        size = getattr(lib(), self._name + "_workspace_size", None) if self._name != "kda_kv_write" else None
+        if size is not None:
+            nbytes = int(size(ctypes.byref(args)))
+            if nbytes == 0:
+                # the call itself reports why, before any launch
+                _check(self._fn(ctypes.byref(args), None, 0, None), self._name)
+            self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+    def run(self, stream=None):
+        _launch(self._fn, self._name, self._device, self.args, self.workspace, stream)
+        return self
+
+    def device_status(self) -> int:
+        """The flags raised so far (synchronises); see include/kda.h."""
+        return int(self.status.item())
+
+
+def _heads(q, k, names):
+    if q.dim() != 3:
+        raise ValueError(f"q must be [T, H, D], got {tuple(q.shape)}")
+    H, D = q.shape[1:]
+    Hkv = k.shape[-2]
+    if Hkv < 1 or H % Hkv:
+        raise ValueError(f"{H} query heads are no multiple of {Hkv} key heads ({names})")
+    return q.shape[0], H, Hkv, D
+
+
+def _cu(cu_seqlens):
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError(f"cu_seqlens must be [N + 1] with N >= 1, got {tuple(cu_seqlens.shape)}")
+    return cu_seqlens.numel() - 1
+
+
+class AttnPrefill(_CacheCall):
+    """Planned ``kda_attn_prefill``: causal attention over packed prompts, q
+    [T, H, D], k and v [T, H_kv, D]; ``o`` [T, H, D] is allocated unless given.
+    scale defaults to D^-1/2."""
+    _name = "kda_attn_prefill"
+
+    def __init__(self, q, k, v, cu_seqlens, *, scale=None, o=None, status=None):
+        if k.dim() != 3:
+            raise ValueError(f"k must be [T, H_kv, D], got {tuple(k.shape)}")
+        T, H, Hkv, D = _heads(q, k, "q, k")
+        _shape("k", k, (T, Hkv, D))
+        _shape("v", v, (T, Hkv, D))
+        N = _cu(cu_seqlens)
+        dev = _same_device(q=q, k=k, v=v, cu_seqlens=cu_seqlens, o=o)
+        self.o = torch.empty_like(q, memory_format=torch.contiguous_format) if o is None else o
+        _shape("o", self.o, (T, H, D))
+        a, dt = AttnPrefillArgs(), q.dtype
+        a.num_seqs, a.num_heads, a.num_kv_heads, a.head_dim, a.total_tokens = N, H, Hkv, D, T
+        a.cu_seqlens = _ptr(cu_seqlens, torch.int64, "cu_seqlens")
+        a.in_dtype = _dtype_code(dt)
+        a.q, a.k, a.v = _ptr(q, dt, "q"), _ptr(k, dt, "k"), _ptr(v, dt, "v")
+        a.o = _ptr(self.o, dt, "o")
+        a.scale = float(D ** -0.5 if scale is None else scale)
+        self._plan(dev, a, (q, k, v, cu_seqlens, o), status)
+
+
+class AttnPaged(_CacheCall):
+    """Planned ``kda_attn_paged``: each request's new tokens q [T, H, D] over
+    the paged cache [num_pages, page_size, H_kv, D] that holds them already.
+    block_table [rows, max_pages] int32, kv_lens [rows] int64 (new tokens
+    included), rows [N] int32 names each request's row (None: request s is row
+    s).  max_seqlen: a bound on one request's new tokens (0: T); 1 for a decode
+    step."""
+    _name = "kda_attn_paged"
+
+    def __init__(self, q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, *, rows=None,
+                 max_seqlen=0, scale=None, o=None, status=None):
+        if k_cache.dim() != 4:
+            raise ValueError(f"k_cache must be [pages, page_size, H_kv, D], got {tuple(k_cache.shape)}")
+        T, H, Hkv, D = _heads(q, k_cache, "q, k_cache")
+        P, page = k_cache.shape[:2]
+        _shape("k_cache", k_cache, (P, page, Hkv, D))
+        _shape("v_cache", v_cache, (P, page, Hkv, D))
+        N = _cu(cu_seqlens)
+        if block_table.dim() != 2:
+            raise ValueError(f"block_table must be [rows, max_pages], got {tuple(block_table.shape)}")
+        R, M = block_table.shape
+        _shape("kv_lens", kv_lens, (R,))
+        if rows is not None:
+            _shape("rows", rows, (N,))
+        elif R < N:
+            raise ValueError(f"{N} requests but {R} rows in block_table")
+        dev = _same_device(q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, kv_lens=kv_lens,
+                           cu_seqlens=cu_seqlens, rows=rows, o=o)
+        self.o = torch.empty_like(q, memory_format=torch.contiguous_format) if o is None else o
+        _shape("o", self.o, (T, H, D))
+        a, dt = AttnPagedArgs(), q.dtype
+        a.num_seqs, a.num_heads, a.num_kv_heads, a.head_dim, a.total_tokens = N, H, Hkv, D, T
+        a.cu_seqlens = _ptr(cu_seqlens, torch.int64, "cu_seqlens")
+        a.max_seqlen, a.in_dtype = int(max_seqlen), _dtype_code(dt)
+        a.q, a.o = _ptr(q, dt, "q"), _ptr(self.o, dt, "o")
+        a.k_cache, a.v_cache = _ptr(k_cache, dt, "k_cache"), _ptr(v_cache, dt, "v_cache")
+        a.num_pages, a.page_size = P, page
+        a.block_table = _ptr(block_table, torch.int32, "block_table")
+        a.kv_lens = _ptr(kv_lens, torch.int64, "kv_lens")
+        a.num_rows, a.max_pages = R, M
+        a.rows = _ptr(rows, torch.int32, "rows")
+        a.scale = float(D ** -0.5 if scale is None else scale)
+        self._plan(dev, a, (q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, rows, o), status)
+
+
+class KvPlan(_CacheCall):
+    """Planned ``kda_kv_plan``: pages and slots for ``total_tokens`` new tokens
+    (a host-known bound of cu_seqlens[N]).  block_table [rows, max_pages] int32
+    and free_pages [num_pages] int32 with free_count [1] int32 are the pool;
+    kv_lens [rows] int64 counts what is cached.  By default kv_lens and
+    free_count advance in place; slot_map [total_tokens] int64 is allocated
+    unless given."""
+    _name = "kda_kv_plan"
+
+    def __init__(self, cu_seqlens, total_tokens, block_table, kv_lens, free_pages, free_count, *,
+                 page_size, rows=None, kv_lens_out=None, free_count_out=None, slot_map=None, status=None):
+        N = _cu(cu_seqlens)
+        if block_table.dim() != 2:
+            raise ValueError(f"block_table must be [rows, max_pages], got {tuple(block_table.shape)}")
+        R, M = block_table.shape
+        self.kv_lens_out = kv_lens if kv_lens_out is None else kv_lens_out
+        self.free_count_out = free_count if free_count_out is None else free_count_out
+        dev = _same_device(cu_seqlens=cu_seqlens, block_table=block_table, kv_lens=kv_lens,
+                           free_pages=free_pages, free_count=free_count, rows=rows,
+                           kv_lens_out=kv_lens_out, free_count_out=free_count_out, slot_map=slot_map)
+        self.slot_map = (torch.empty(int(total_tokens), dtype=torch.int64, device=dev)
+                         if slot_map is None else slot_map)
+        _shape("kv_lens", kv_lens, (R,))
+        _shape("kv_lens_out", self.kv_lens_out, (R,))
+        _shape("slot_map", self.slot_map, (int(total_tokens),))
+        _shape("free_count", free_count, (1,))
+        _shape("free_count_out", self.free_count_out, (1,))
+        if free_pages.dim() != 1:
+            raise ValueError(f"free_pages must be [num_pages], got {tuple(free_pages.shape)}")
+        if rows is not None:
+            _shape("rows", rows, (N,))
+        elif R < N:
+            raise ValueError(f"{N} requests but {R} rows in block_table")
+        a = KvPlanArgs()
+        a.num_seqs, a.total_tokens = N, int(total_tokens)
+        a.cu_seqlens = _ptr(cu_seqlens, torch.int64, "cu_seqlens")
+        a.page_size, a.num_pages, a.num_rows, a.max_pages = int(page_size), free_pages.numel(), R, M
+        a.rows = _ptr(rows, torch.int32, "rows")
+        a.block_table = _ptr(block_table, torch.int32, "block_table")
+        a.kv_lens_in = _ptr(kv_lens, torch.int64, "kv_lens")
+        a.kv_lens_out = _ptr(self.kv_lens_out, torch.int64, "kv_lens_out")
+        a.free_pages = _ptr(free_pages, torch.int32, "free_pages")
+        a.free_count_in = _ptr(free_count, torch.int32, "free_count")
+        a.free_count_out = _ptr(self.free_count_out, torch.int32, "free_count_out")
+        a.slot_map = _ptr(self.slot_map, torch.int64, "slot_map")
+        self._plan(dev, a, (cu_seqlens, block_table, kv_lens, free_pages, free_count, rows, self.kv_lens_out,
+                            self.free_count_out, self.slot_map), status)
+
+
+class KvRelease(_CacheCall):
+    """Planned ``kda_kv_release``: the pages of ``rows`` [M] int32 back to the
+    free list, their kv_lens to 0."""
+    _name = "kda_kv_release"
+
+    def __init__(self, rows, block_table, kv_lens, free_pages, free_count, *, page_size, status=None):
+        if rows.dim() != 1 or block_table.dim() != 2 or free_pages.dim() != 1:
+            raise ValueError("rows must be [M], block_table [rows, max_pages], free_pages [num_pages]")
+        R, M = block_table.shape
+        _shape("kv_lens", kv_lens, (R,))
+        _shape("free_count", free_count, (1,))
+        dev = _same_device(rows=rows, block_table=block_table, kv_lens=kv_lens, free_pages=free_pages,
+                           free_count=free_count)
+        a = KvReleaseArgs()
+        a.num_release, a.page_size, a.num_pages = rows.numel(), int(page_size), free_pages.numel()
+        a.num_rows, a.max_pages = R, M
+        a.rows = _ptr(rows, torch.int32, "rows")
+        a.block_table = _ptr(block_table, torch.int32, "block_table")
+        a.kv_lens = _ptr(kv_lens, torch.int64, "kv_lens")
+        a.free_pages = _ptr(free_pages, torch.int32, "free_pages")
+        a.free_count = _ptr(free_count, torch.int32, "free_count")
+        self._plan(dev, a, (rows, block_table, kv_lens, free_pages, free_count), status)
+
+
+class KvWrite(_CacheCall):
+    """Planned ``kda_kv_write``: k, v [T, H_kv, D] into the slots slot_map [T]
+    of the caches [num_pages, page_size, H_kv, D]."""
+    _name = "kda_kv_write"
+
+    def __init__(self, k, v, slot_map, k_cache, v_cache, *, status=None):
+        if k.dim() != 3 or k_cache.dim() != 4:
+            raise ValueError("k must be [T, H_kv, D] and k_cache [pages, page_size, H_kv, D]")
+        T, Hkv, D = k.shape
+        P, page = k_cache.shape[:2]
+        _shape("v", v, (T, Hkv, D))
+        _shape("k_cache", k_cache, (P, page, Hkv, D))
+        _shape("v_cache", v_cache, (P, page, Hkv, D))
+        _shape("slot_map", slot_map, (T,))
+        dev = _same_device(k=k, v=v, slot_map=slot_map, k_cache=k_cache, v_cache=v_cache)
+        a, dt = KvWriteArgs(), k.dtype
+        a.total_tokens, a.num_kv_heads, a.head_dim = T, Hkv, D
+        a.in_dtype = _dtype_code(dt)
+        a.k, a.v = _ptr(k, dt, "k"), _ptr(v, dt, "v")
+        a.slot_map = _ptr(slot_map, torch.int64, "slot_map")
+        a.num_slots = P * page
+        a.k_cache, a.v_cache = _ptr(k_cache, dt, "k_cache"), _ptr(v_cache, dt, "v_cache")
+        self._plan(dev, a, (k, v, slot_map, k_cache, v_cache), status)
+
+
+def _run_on(make, stream):
+    """Makes a planned call and runs it on ``stream``; what it allocates
+    belongs to that stream, so it is zeroed before the kernels and not reused
+    before they end."""
+    if stream is None:
+        return make().run()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(stream):
+        return make().run(stream)
+
+
+def attn_prefill(q, k, v, cu_seqlens, *, stream=None, **kw):
+    """Allocates, runs and returns o (see AttnPrefill)."""
+    return _run_on(lambda: AttnPrefill(q, k, v, cu_seqlens, **kw), stream).o
+
+
+def attn_paged(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, *, stream=None, **kw):
+    """Allocates, runs and returns o (see AttnPaged)."""
+    return _run_on(lambda: AttnPaged(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, **kw), stream).o
+
+
+def kv_plan(cu_seqlens, total_tokens, block_table, kv_lens, free_pages, free_count, *, stream=None, **kw):
+    """Runs kda_kv_plan and returns slot_map (see KvPlan)."""
+    return _run_on(lambda: KvPlan(cu_seqlens, total_tokens, block_table, kv_lens, free_pages, free_count, **kw),
+                   stream).slot_map
+
+
+def kv_release(rows, block_table, kv_lens, free_pages, free_count, *, stream=None, **kw):
+    """Runs kda_kv_release (see KvRelease)."""
+    _run_on(lambda: KvRelease(rows, block_table, kv_lens, free_pages, free_count, **kw), stream)
+
+
+def kv_write(k, v, slot_map, k_cache, v_cache, *, stream=None, **kw):
+    """Runs kda_kv_write (see KvWrite)."""
+    _run_on(lambda: KvWrite(k, v, slot_map, k_cache, v_cache, **kw), stream)
