@@ -1,7 +1,7 @@
 // kda_attn_api.cu -- the extern "C" entry points of the full attention and its
 // paged cache: argument validation, workspace sizes and the choice of path.
 // Declarations and contracts are in include/kda.h.
-#include "kda_attn.cuh"
+#include "kda_attn_tc.cuh"
 
 namespace kda {
 namespace {
@@ -28,6 +28,10 @@ kda_status_t validate_heads(int32_t H, int32_t Hkv, int32_t D, kda_dtype_t dt) {
 
 // token indices are int32 coordinates in the kernels' copies and grids
 bool tokens_ok(int64_t T) { return T < ((int64_t)1 << 30); }
+// so are the positions of a row
+bool positions_ok(int32_t max_pages, int32_t page_size) {
+  return (int64_t)max_pages * page_size < ((int64_t)1 << 31) - 1024;
+}
 
 kda_status_t validate(const kda_attn_prefill_args* a) {
   if (!a || a->num_seqs < 1 || a->total_tokens < 0 || !a->cu_seqlens) return KDA_ERR_INVALID_ARG;
@@ -46,6 +50,7 @@ kda_status_t validate(const kda_attn_paged_args* a) {
   if (!a->rows && a->num_rows < a->num_seqs) return KDA_ERR_INVALID_ARG;
   if (a->total_tokens > 0 && (!a->q || !a->o || !a->kv_lens || !a->block_table || !a->k_cache || !a->v_cache))
     return KDA_ERR_INVALID_ARG;
+  if (!positions_ok(a->max_pages, a->page_size)) return KDA_ERR_UNSUPPORTED;
   return tokens_ok(a->total_tokens) ? KDA_OK : KDA_ERR_UNSUPPORTED;
 }
 
@@ -96,21 +101,20 @@ AttnParams params(const kda_attn_paged_args* a) {
   return p;
 }
 
-size_t attn_workspace(const AttnParams& p) {
-  (void)p;
-  return 256;
-}
+size_t attn_workspace(const AttnParams& p) { return attn_tc_fits(p) ? attn_tc_workspace(p) : 256; }
 
 kda_status_t run_attn(const AttnParams& p, void* ws, size_t ws_bytes, void* stream) {
   if (!ws || ws_bytes < attn_workspace(p) || misaligned(ws)) return KDA_ERR_WORKSPACE;
   if (p.total_tokens == 0) return KDA_OK;
-  return from_cuda(launch_attn_simt(p, static_cast<cudaStream_t>(stream)));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return from_cuda(attn_tc_fits(p) ? launch_attn_tc(p, ws, s) : launch_attn_simt(p, s));
 }
 
 kda_status_t validate(const kda_kv_plan_args* a) {
   if (!a || a->num_seqs < 1 || a->total_tokens < 0 || !a->cu_seqlens) return KDA_ERR_INVALID_ARG;
   if (a->num_pages < 0 || a->num_rows < 0 || a->max_pages < 0) return KDA_ERR_INVALID_ARG;
-  if (!page_ok(a->page_size) || !tokens_ok(a->total_tokens)) return KDA_ERR_UNSUPPORTED;
+  if (!page_ok(a->page_size) || !tokens_ok(a->total_tokens) || !positions_ok(a->max_pages, a->page_size))
+    return KDA_ERR_UNSUPPORTED;
   if (!a->rows && a->num_rows < a->num_seqs) return KDA_ERR_INVALID_ARG;
   if (!a->free_count_in || !a->free_count_out) return KDA_ERR_INVALID_ARG;
   if (a->num_rows > 0 && (!a->kv_lens_in || !a->kv_lens_out)) return KDA_ERR_INVALID_ARG;
@@ -123,7 +127,7 @@ kda_status_t validate(const kda_kv_plan_args* a) {
 kda_status_t validate(const kda_kv_release_args* a) {
   if (!a || a->num_release < 0) return KDA_ERR_INVALID_ARG;
   if (a->num_pages < 0 || a->num_rows < 0 || a->max_pages < 0) return KDA_ERR_INVALID_ARG;
-  if (!page_ok(a->page_size)) return KDA_ERR_UNSUPPORTED;
+  if (!page_ok(a->page_size) || !positions_ok(a->max_pages, a->page_size)) return KDA_ERR_UNSUPPORTED;
   if (a->num_release > 0 && (!a->rows || !a->free_count)) return KDA_ERR_INVALID_ARG;
   if (a->num_rows > 0 && !a->kv_lens) return KDA_ERR_INVALID_ARG;
   if (a->num_rows > 0 && a->max_pages > 0 && !a->block_table) return KDA_ERR_INVALID_ARG;

@@ -1,0 +1,861 @@
+// kda_attn_tc.cu -- causal attention with grouped heads on the tcgen05 tensor
+// cores: bf16, heads of up to 128 channels, packed prompts or the paged cache.
+//
+// Rows.  The rows of a key head's G query heads are packed, row = token * G +
+// head, so that one pass over K and V serves them all.  An item is two row
+// tiles of 128 rows (floor(128 / G) tokens each) of one (sequence, key head),
+// or a piece of its keys; a persistent CTA per SM takes items, the costliest
+// first (attn_plan_kernel sorts them).
+//
+// Per key tile of 128 positions and row tile, with the logits in base 2,
+// x = (scale / ln 2) q.k:
+//
+//   S = Q K^T            tcgen05, fp32 in TMEM
+//   m' = max(m, max x)   l = l 2^(m - m') + sum 2^(x - m')     one thread a row
+//   P = 2^(x - m')       rounded to bf16, into S's columns of TMEM
+//   O = O 2^(m - m') + P V   tcgen05, A from TMEM
+//
+// The reference m of a row follows its maximum only once that has risen by
+// more than 2^kLazyLog2: until then the weights are taken against the old
+// reference (at most 2^kLazyLog2 each, the same relative rounding), and O
+// needs no rescaling pass.  o = O / l at the end, so the choice changes no
+// result beyond rounding.
+//
+// Warps: 0-3 and 4-7 hold the softmax of the two row tiles (thread = row =
+// TMEM lane), 8 issues the copies, 9 the MMAs (10 and 11 only complete the
+// warpgroup that gives its registers to the softmax).  While one tile's softmax
+// runs, the tensor core works on the other tile.  The MMAs of a CTA are issued by
+// one thread and execute in issue order, so S of the next key tile may be
+// issued right behind the P V that reads P from the same columns.
+//
+// Masked places.  Logits past a row's position are replaced by -inf before
+// they are used, so K may hold anything there.  V meets weights of exactly 0,
+// which would still turn infinities and NaN into NaN: a key tile that ends
+// behind the sequence has its remaining V rows zeroed in shared memory, and
+// in a tile with positions that some row of the item may not attend,
+// non-finite values of V are zeroed too; the epilogue then puts them back
+// into the rows that do attend them (a slow path no finite input takes).
+#include "kda_attn_tc.cuh"
+
+namespace kda {
+namespace {
+
+using namespace tc;
+
+constexpr int kTile = 128;       // rows of a row tile, positions of a key tile
+constexpr int kThreads = 384;    // two softmax warpgroups; copies and MMAs
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLazyLog2 = 8.f;
+constexpr uint32_t kTmemCols = 512;
+
+template <int DP>
+struct Shape {
+  static constexpr int NH = DP / 64;                        // 128-byte column blocks of a tile
+  static constexpr uint32_t kBlock = kTile * 128;           // bytes of one block
+  static constexpr uint32_t kTileBytes = NH * kBlock;
+  static constexpr int kStages = DP == 128 ? 5 : 8;
+  static constexpr uint32_t kQ = 0;                         // two row tiles
+  static constexpr uint32_t kRing = 2 * kTileBytes;
+  static constexpr uint32_t kBars = kRing + kStages * kTileBytes;
+  static constexpr uint32_t kBytes = kBars + 512;
+};
+
+struct Bars {
+  uint64_t full[8], empty[8];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2];
+  uint64_t fix, drain;
+  uint32_t dead;      // a wait expired: every role winds down
+  uint32_t tmem;
+  // the CTA's k-th item with key tiles: non-finite values were taken out of its
+  // V tiles (index k % 4; the copies run at most two such items ahead of the
+  // epilogue, held back by Q's row tiles)
+  uint32_t poison[4];
+};
+static_assert(sizeof(Bars) <= 512, "barrier block");
+
+// Waits for `parity` of `bar`; false once any wait of the CTA has expired
+// (kWaitLimitNs), so that the roles end together.
+__device__ __forceinline__ bool wait_or_dead(uint64_t* bar, uint32_t parity, uint32_t* dead) {
+  const uint32_t a = smem_u32(bar);
+  uint64_t t0 = 0;
+  for (uint32_t it = 0;; ++it) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(done)
+        : "r"(a), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if (it == 0) {
+      t0 = globaltimer_ns();
+    } else if ((it & 63) == 0) {
+      if (*reinterpret_cast<volatile uint32_t*>(dead)) return false;
+      if (globaltimer_ns() - t0 > kWaitLimitNs) {
+        *reinterpret_cast<volatile uint32_t*>(dead) = 1;
+        return false;
+      }
+    }
+  }
+}
+
+// What every role derives from an item
+struct Geo {
+  int rows[2];   // valid rows of each row tile
+  int n[2];      // key tiles of each
+  int nmax;
+  int kt0;       // first key tile
+  int fix_from;  // first key tile with a position some row may not attend, or past the sequence
+};
+__device__ __forceinline__ Geo geometry(const AttnItem& it, int G, int tpt) {
+  Geo g;
+  g.kt0 = it.kt0;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int tok = min(tpt, max(0, it.ntok - t * tpt));
+    g.rows[t] = tok * G;
+    const int end = tok > 0 ? max(0, min(it.kv_len, it.pos0 + t * tpt + tok)) : 0;
+    g.n[t] = max(0, min(it.kt1, (end + kTile - 1) / kTile) - it.kt0);
+  }
+  g.nmax = max(g.n[0], g.n[1]);
+  const int first = it.pos0 + 1;
+  g.fix_from = first <= 0 ? 0 : first / kTile;
+  return g;
+}
+
+// The CTA's i-th item: items go round the CTAs back and forth, so that the
+// sorted costs even out.
+__device__ __forceinline__ int64_t nth_item(int i) {
+  const int64_t g = gridDim.x, c = blockIdx.x;
+  return (int64_t)i * g + ((i & 1) ? g - 1 - c : c);
+}
+
+// ------------------------------------------------------------------ copies
+template <int DP>
+__device__ void load_role(const AttnParams& p, const TcArgs& a, const CUtensorMap* mq, const CUtensorMap* mk,
+                          const CUtensorMap* mv, char* sm, Bars* b, int64_t total, int tpt) {
+  using S = Shape<DP>;
+  const int lane = threadIdx.x & 31;
+  uint32_t n = 0;            // tiles copied so far
+  uint32_t nq[2] = {0, 0};   // q tiles copied so far
+  uint32_t nfix = 0, busy_items = 0;
+  bool ok = true;
+  const int box = a.box_tokens, boxes = kTile / box;
+  const uint32_t box_bytes = (uint32_t)box * 128u;
+  for (int i = 0; ok; ++i) {
+    const int64_t w = nth_item(i);
+    if (w >= total) break;
+    const AttnItem it = a.items[w / p.Hkv];
+    const int h = (int)(w % p.Hkv);
+    const Geo g = geometry(it, p.G, tpt);
+    if (g.nmax == 0) continue;
+    uint32_t* poison = &b->poison[busy_items++ & 3];
+    if (lane == 0) *poison = 0;
+    // key tile kt of K or V into the next stage
+    auto load_tile = [&](const CUtensorMap* m, int kt, bool fix) {
+      const uint32_t st = n % S::kStages;
+      char* dst = sm + S::kRing + st * S::kTileBytes;
+      const int x0 = kt * kTile;
+      // this lane's box: its page, read before the wait
+      const int nb = min(boxes, (it.kv_len - x0 + box - 1) / box);
+      int c2 = it.base + x0 + lane * box, c3 = 0;
+      if (p.block_table && lane < nb) {
+        const int x = x0 + lane * box;
+        int page = p.block_table[(int64_t)it.base * p.max_pages + (x >> p.page_shift)];
+        if (page < 0 || page >= p.num_pages) {
+          attn_flag(p.status, kFlagBadCache);
+          page = p.num_pages;  // outside the map: filled with zeros
+        }
+        c2 = x & ((1 << p.page_shift) - 1);
+        c3 = page;
+      }
+      ok = wait_or_dead(&b->empty[st], ((n / S::kStages) & 1) ^ 1, &b->dead);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return;
+      uint64_t* bar = fix ? &b->fix : &b->full[st];
+      if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)nb * box_bytes * S::NH);
+      __syncwarp();
+      if (lane < nb)
+#pragma unroll
+        for (int c = 0; c < S::NH; ++c) tma_4d(dst + c * S::kBlock + lane * box_bytes, m, 64 * c, h, c2, c3, bar);
+      if (fix) {
+        // in place: rows behind the sequence to zero, non-finite values out
+        ok = wait_or_dead(&b->fix, nfix & 1, &b->dead);
+        ok = __all_sync(0xffffffffu, ok);
+        ++nfix;
+        if (!ok) return;
+        const int live = min(kTile, it.kv_len - x0);
+        bool bad = false;
+        if (it.ntok > 1) {
+#pragma unroll 4
+          for (int v = lane; v < live * 8 * S::NH; v += 32) {
+            uint4* q4 = reinterpret_cast<uint4*>(dst + (v / (live * 8)) * S::kBlock) + v % (live * 8);
+            const uint4 x = *q4;
+            // an exponent of all ones carries into the sign's place
+            const uint32_t t = (((x.x & 0x7f807f80u) + 0x00800080u) | ((x.y & 0x7f807f80u) + 0x00800080u) |
+                                ((x.z & 0x7f807f80u) + 0x00800080u) | ((x.w & 0x7f807f80u) + 0x00800080u)) &
+                               0x80008000u;
+            if (t) {
+              bad = true;
+              *q4 = make_uint4(finite_only(x.x), finite_only(x.y), finite_only(x.z), finite_only(x.w));
+            }
+          }
+        }
+        for (int v = live * 8 + lane; v < kTile * 8; v += 32)
+#pragma unroll
+          for (int c = 0; c < S::NH; ++c)
+            *(reinterpret_cast<uint4*>(dst + c * S::kBlock) + v) = make_uint4(0, 0, 0, 0);
+        if (bad) *reinterpret_cast<volatile uint32_t*>(poison) = 1;
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b->full[st]);
+      }
+      ++n;
+    };
+    for (int t = 0; t < 2 && ok; ++t) {
+      if (g.n[t] == 0) continue;
+      ok = wait_or_dead(&b->q_empty[t], (nq[t] & 1) ^ 1, &b->dead);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&b->q_full[t], (uint32_t)(tpt * p.G) * 128u * S::NH);
+#pragma unroll
+        for (int c = 0; c < S::NH; ++c)
+          tma_3d(sm + S::kQ + t * S::kTileBytes + c * S::kBlock, mq, 64 * c, h * p.G, it.tok0 + t * tpt,
+                 &b->q_full[t]);
+      }
+      ++nq[t];
+      __syncwarp();
+    }
+    for (int j = 0; j < g.nmax && ok; ++j) {
+      const int kt = g.kt0 + j;
+      load_tile(mk, kt, false);
+      if (ok) load_tile(mv, kt, kt >= g.fix_from);
+    }
+  }
+  // no copy of its own is in flight when a CTA that gave up exits
+  if (!ok) {
+    for (uint32_t k = n > S::kStages ? n - S::kStages : 0; k < n; ++k)
+      mbar_wait(&b->full[k % S::kStages], (k / S::kStages) & 1, kWaitLimitNs);
+    for (int t = 0; t < 2; ++t)
+      if (nq[t] > 0) mbar_wait(&b->q_full[t], (nq[t] - 1) & 1, kWaitLimitNs);
+    if (nfix > 0) mbar_wait(&b->fix, (nfix - 1) & 1, kWaitLimitNs);
+  }
+}
+
+// ------------------------------------------------------------------ MMAs
+template <int DP>
+__device__ void mma_role(const AttnParams& p, const TcArgs& a, char* sm, Bars* b, int64_t total, int tpt) {
+  using S = Shape<DP>;
+  const uint32_t tmem = b->tmem;
+  const uint32_t id_qk = idesc_bf16(kTile, kTile), id_pv = idesc_bf16(kTile, DP, 0, 1);
+  const uint32_t q0 = smem_u32(sm + S::kQ), r0 = smem_u32(sm + S::kRing);
+  uint32_t n = 0, nq[2] = {0, 0}, np[2] = {0, 0};
+  uint32_t* dead = &b->dead;
+  auto full = [&](uint32_t k) { return wait_or_dead(&b->full[k % S::kStages], (k / S::kStages) & 1, dead); };
+  auto qk = [&](int t, uint32_t k) {
+    const uint32_t kb = r0 + (k % S::kStages) * S::kTileBytes, qb = q0 + t * S::kTileBytes;
+#pragma unroll
+    for (int s = 0; s < DP / 16; ++s) {
+      const uint32_t off = (s / 4) * S::kBlock + (s % 4) * 32;
+      mma_bf16(tmem + t * kTile, sdesc_sw128(qb + off, 16, 1024), sdesc_sw128(kb + off, 16, 1024), id_qk, s > 0);
+    }
+    mma_commit(&b->s_full[t]);
+  };
+  auto pv = [&](int t, uint32_t k, bool first) {
+    const uint32_t vb = r0 + (k % S::kStages) * S::kTileBytes;
+#pragma unroll
+    for (int s = 0; s < kTile / 16; ++s)
+      mma_bf16_ts(tmem + 2 * kTile + t * DP, tmem + t * kTile + s * 8, sdesc_sw128(vb + s * 2048, S::kBlock, 1024),
+                  id_pv, !first || s > 0);
+  };
+  bool ok = true;
+  for (int i = 0; ok; ++i) {
+    const int64_t w = nth_item(i);
+    if (w >= total) break;
+    const AttnItem it = a.items[w / p.Hkv];
+    const Geo g = geometry(it, p.G, tpt);
+    if (g.nmax == 0) continue;
+    if (!(ok = full(n))) break;
+    for (int t = 0; t < 2 && ok; ++t) {
+      if (g.n[t] == 0) continue;
+      if (!(ok = wait_or_dead(&b->q_full[t], nq[t] & 1, dead))) break;
+      ++nq[t];
+      fence_after_sync();
+      qk(t, n);
+      if (g.n[t] == 1) mma_commit(&b->q_empty[t]);
+    }
+    if (!ok) break;
+    mma_commit(&b->empty[n % S::kStages]);
+    ++n;
+    for (int j = 0; j < g.nmax && ok; ++j) {
+      const uint32_t vk = n, kk = n + 1;
+      bool have_v = false, have_k = false;
+      for (int t = 0; t < 2; ++t) {
+        if (j >= g.n[t]) continue;
+        if (!have_v && !(ok = full(vk))) break;
+        have_v = true;
+        if (!(ok = wait_or_dead(&b->p_full[t], np[t] & 1, dead))) break;
+        ++np[t];
+        fence_after_sync();
+        pv(t, vk, j == 0);
+        if (j + 1 < g.n[t]) {
+          if (!have_k && !(ok = full(kk))) break;
+          have_k = true;
+          fence_after_sync();
+          qk(t, kk);
+          if (j + 2 == g.n[t]) mma_commit(&b->q_empty[t]);
+        } else {
+          mma_commit(&b->o_full[t]);
+        }
+      }
+      if (!ok) break;
+      mma_commit(&b->empty[vk % S::kStages]);
+      ++n;
+      if (j + 1 < g.nmax) {
+        mma_commit(&b->empty[kk % S::kStages]);
+        ++n;
+      }
+    }
+  }
+  // no MMA and no arrival of one is left in flight
+  mma_commit(&b->drain);
+  mbar_wait(&b->drain, 0, kWaitLimitNs);
+}
+
+// ------------------------------------------------------------------ softmax and outputs
+// The non-finite values taken out of an item's V tiles, put back into one row
+// (slow path): every channel that an attended position poisons takes its
+// infinity, or NaN where it meets both signs or a NaN.
+__device__ __noinline__ float poison_of(const __nv_bfloat16* v, int64_t stride, const int32_t* pages, int num_pages,
+                                        int shift, int from, int limit) {
+  bool pos = false, neg = false, nan = false;
+  for (int x = from; x <= limit; ++x) {
+    int64_t at = x;
+    if (pages) {
+      const int32_t page = pages[x >> shift];
+      if (page < 0 || page >= num_pages) continue;
+      at = ((int64_t)page << shift) + (x & ((1 << shift) - 1));
+    }
+    const float y = __bfloat162float(v[at * stride]);
+    pos |= y == INFINITY;
+    neg |= y == -INFINITY;
+    nan |= y != y;
+  }
+  return nan || (pos && neg) ? NAN : pos ? INFINITY : neg ? -INFINITY : 0.f;
+}
+
+template <int DP>
+__device__ void softmax_role(const AttnParams& p, const TcArgs& a, Bars* b, int64_t total, int tpt) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int t = warp >> 2, row = (warp & 3) * 32 + lane;
+  uint32_t* dead = &b->dead;
+  const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+  const uint32_t s_col = b->tmem + lanes + t * kTile, o_col = b->tmem + lanes + 2 * kTile + t * DP;
+  const float sc = p.scale * kLog2e;
+  uint32_t ns = 0, no = 0, busy_items = 0;
+  for (int i = 0;; ++i) {
+    const int64_t w = nth_item(i);
+    if (w >= total) return;
+    const AttnItem it = a.items[w / p.Hkv];
+    const int h = (int)(w % p.Hkv);
+    const Geo g = geometry(it, p.G, tpt);
+    const int rows = g.rows[t], n = g.n[t];
+    const uint32_t* poisoned = &b->poison[busy_items & 3];
+    busy_items += g.nmax > 0;
+    if (rows == 0) continue;
+    const int tok = row / p.G;  // within the row tile
+    const int limit = it.pos0 + t * tpt + tok;
+    const int mask_from = it.pos0 + t * tpt + 1 <= 0 ? 0 : (it.pos0 + t * tpt + 1) / kTile;
+    const bool busy = (warp & 3) * 32 < rows;  // a warp without rows only keeps step
+    float m = -INFINITY, l = 0.f;
+    for (int j = 0; j < n; ++j) {
+      if (!__all_sync(0xffffffffu, wait_or_dead(&b->s_full[t], ns & 1, dead))) return;
+      ++ns;
+      fence_after_sync();
+      if (busy) {
+        float s[kTile];
+#pragma unroll
+        for (int c = 0; c < kTile; c += 32) tmem_ld32(s_col + c, s + c);
+        tmem_ld_wait();
+        const int kt = g.kt0 + j;
+        if (kt >= mask_from) {
+          const int last = min(limit, it.kv_len - 1) - kt * kTile;
+#pragma unroll
+          for (int c = 0; c < kTile; ++c) s[c] = c <= last ? s[c] : -INFINITY;
+        }
+        float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int c = 4; c < kTile; c += 8) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            mx[u] = c + u + 4 < kTile ? fmaxf(mx[u], fmaxf(s[c + u], s[c + u + 4])) : fmaxf(mx[u], s[c + u]);
+        }
+        const float x = sc * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        // the reference moves with the first finite maximum, then only past the threshold
+        const bool move = x > m + kLazyLog2 || (m == -INFINITY && x > m);
+        const bool scale_o = move && m != -INFINITY;
+        if (__any_sync(0xffffffffu, scale_o)) {
+          const float f = scale_o ? exp2_fast(m - x) : 1.f;
+          l *= f;
+#pragma unroll
+          for (int c = 0; c < DP; c += 32) {
+            float o[32];
+            tmem_ld32(o_col + c, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int u = 0; u < 32; ++u) o[u] *= f;
+            tmem_st32(o_col + c, reinterpret_cast<const uint32_t*>(o));
+          }
+        }
+        if (move) m = x;
+        const float ref = m == -INFINITY ? 0.f : m;
+        const float2 sc2 = make_float2(sc, sc), ref2 = make_float2(-ref, -ref);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int c = 0; c < kTile; c += 64) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int u = 0; u < 32; ++u) {
+            float2 e = fma2(make_float2(s[c + 2 * u], s[c + 2 * u + 1]), sc2, ref2);
+            e.x = exp2_fast(e.x);
+            e.y = exp2_fast(e.y);
+            sum[u & 1] = add2(sum[u & 1], e);
+            pk[u] = pack2(e.x, e.y);
+          }
+          tmem_st32(s_col + c / 2, pk);
+        }
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        tmem_st_wait();
+      }
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&b->p_full[t]);
+    }
+    // o = O / l, or the piece's O with its m and l
+    if (n > 0) {
+      if (!__all_sync(0xffffffffu, wait_or_dead(&b->o_full[t], no & 1, dead))) return;
+      ++no;
+      fence_after_sync();
+    }
+    if (!busy) continue;
+    const bool poison = n > 0 && *reinterpret_cast<const volatile uint32_t*>(poisoned) != 0;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int gq = row - tok * p.G;
+    const bool mine = row < rows;
+    const int64_t orow = ((int64_t)(it.tok0 + t * tpt + tok) * p.H + (int64_t)h * p.G + gq) * p.D;
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) + orow;
+    const int64_t prow = it.slot < 0 ? 0 : ((int64_t)it.slot * p.Hkv + h) * (2 * kTile) + t * kTile + row;
+#pragma unroll 1
+    for (int c = 0; c < DP; c += 32) {
+      float x[32];
+      if (n > 0) {
+        tmem_ld32(o_col + c, x);
+        tmem_ld_wait();
+      } else {
+#pragma unroll
+        for (int u = 0; u < 32; ++u) x[u] = 0.f;
+      }
+      if (mine && c < p.D) {
+        const float f = it.slot < 0 ? inv : 1.f;
+#pragma unroll
+        for (int u = 0; u < 32; ++u) x[u] *= f;
+        if (poison) {
+          const int from = max(g.kt0, g.fix_from) * kTile, to = min(limit, min(it.kv_len, it.kt1 * kTile) - 1);
+          const int64_t stride = (int64_t)p.Hkv * p.D;
+          const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v) + (int64_t)h * p.D + c +
+                                   (p.block_table ? 0 : it.base * stride);
+          const int32_t* pages = p.block_table ? p.block_table + (int64_t)it.base * p.max_pages : nullptr;
+#pragma unroll
+          for (int u = 0; u < 32; ++u) {
+            if (c + u >= p.D) break;
+            const float y = poison_of(v + u, stride, pages, p.num_pages, p.page_shift, from, to);
+            if (y != 0.f) x[u] += y;  // a NaN already there stays
+          }
+        }
+        if (it.slot < 0) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int u = 0; u < 16; ++u) pk[u] = pack2(x[2 * u], x[2 * u + 1]);
+#pragma unroll
+          for (int u = 0; u < 16; u += 4)
+            if (c + 2 * u < p.D) *reinterpret_cast<uint4*>(o + c + 2 * u) = make_uint4(pk[u], pk[u + 1], pk[u + 2], pk[u + 3]);
+        } else {
+          float* part = a.part_o + prow * DP + c;
+#pragma unroll
+          for (int u = 0; u < 32; u += 4) *reinterpret_cast<float4*>(part + u) = make_float4(x[u], x[u + 1], x[u + 2], x[u + 3]);
+        }
+      }
+      __syncwarp();
+    }
+    if (mine && it.slot >= 0) a.part_ml[prow] = make_float2(m, l);
+    // these reads of O come before the arrival that lets the next item's P V write it
+    fence_before_sync();
+  }
+}
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_tc(const AttnParams p, const TcArgs a, const __grid_constant__ CUtensorMap mq,
+            const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+  using S = Shape<DP>;
+  extern __shared__ __align__(1024) char sm[];
+  Bars* b = reinterpret_cast<Bars*>(sm + S::kBars);
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 8; ++s) {
+      mbar_init(&b->full[s], 1);
+      mbar_init(&b->empty[s], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&b->q_full[t], 1);
+      mbar_init(&b->q_empty[t], 1);
+      mbar_init(&b->s_full[t], 1);
+      mbar_init(&b->p_full[t], 4);
+      mbar_init(&b->o_full[t], 1);
+    }
+    mbar_init(&b->fix, 1);
+    mbar_init(&b->drain, 1);
+    b->dead = 0;
+    mbar_init_fence();
+  }
+  if (warp == 9) tmem_alloc(&b->tmem, kTmemCols);
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  pdl_wait();  // the plan
+  const int tpt = kTile / p.G;
+  const int64_t total = (int64_t)a.head->items * p.Hkv;
+  // registers: 168 a thread at launch (384 x 168 = 64,512); a softmax thread
+  // holds a row of 128 logits: 2 x 128 x 208 + 128 x 80 = 63,488
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    softmax_role<DP>(p, a, b, total, tpt);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (warp == 8) load_role<DP>(p, a, &mq, &mk, &mv, sm, b, total, tpt);
+    else if (warp == 9 && (threadIdx.x & 31) == 0) mma_role<DP>(p, a, sm, b, total, tpt);
+  }
+  __syncwarp();
+  fence_before_sync();
+  __syncthreads();
+  if (threadIdx.x == 0 && b->dead) attn_flag(p.status, kFlagTimeout);
+  if (warp == 9) tmem_dealloc(b->tmem, kTmemCols);
+}
+
+// ------------------------------------------------------------------ planning
+constexpr int kPlanThreads = 1024;
+constexpr int kBuckets = 2560;
+
+// costs up to 255 keep their own bucket, larger ones their seven leading bits
+__device__ __forceinline__ int bucket_of(int cost) {
+  if (cost < 256) return cost;
+  const int e = 31 - __clz(cost) - 7;
+  return (e << 7) + (cost >> e);
+}
+
+__device__ int64_t plan_scan(int64_t x, int64_t* part, int64_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) part[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int64_t y = part[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t z = __shfl_up_sync(0xffffffffu, y, o);
+      if (lane >= o) y += z;
+    }
+    part[lane] = y;
+  }
+  __syncthreads();
+  if (warp > 0) x += part[warp - 1];
+  *total = part[31];
+  __syncthreads();
+  return x;
+}
+
+// One CTA: the items of the call from the device-side lengths, sorted by
+// their key tiles, costliest first.  When they are too few to fill the GPU
+// (split_sms > 0) an item's key tiles are cut into pieces of about equal
+// share, and the list of what to join is left for attn_join.
+__global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnParams p, const TcArgs a, int tpi) {
+  __shared__ int64_t part[32];
+  __shared__ int hist[kBuckets];
+  __shared__ unsigned long long cost_sum;
+  const int tid = threadIdx.x;
+  pdl_launch_dependents();
+  for (int i = tid; i < kBuckets; i += kPlanThreads) hist[i] = 0;
+  if (tid == 0) cost_sum = 0;
+  __syncthreads();
+  auto item = [&](const AttnSeq& s, int64_t tile) {
+    AttnItem it;
+    it.tok0 = (int32_t)(s.tok0 + tile * tpi);
+    it.ntok = (int32_t)min((int64_t)tpi, s.len - tile * tpi);
+    it.base = p.block_table ? s.row : (int32_t)s.tok0;
+    it.pos0 = (int32_t)(s.kv_len - s.len + tile * tpi);
+    it.kv_len = (int32_t)s.kv_len;
+    it.kt0 = 0;
+    const int end = max(0, min(it.kv_len, it.pos0 + it.ntok));
+    it.kt1 = (end + kTile - 1) / kTile;
+    it.slot = -1;
+    return it;
+  };
+  // the sequences' tiles, prefix sums in seq_begin; the cost of all
+  int64_t n_tiles = 0;
+  for (int base = 0; base < p.num_seqs; base += kPlanThreads) {
+    const int s = base + tid;
+    int64_t n = 0, total;
+    AttnSeq q{};
+    if (s < p.num_seqs) {
+      q = attn_seq(p, s);
+      if (q.flag) attn_flag(p.status, q.flag);
+      n = ((int64_t)q.len + tpi - 1) / tpi;
+    }
+    const int64_t end = plan_scan(n, part, &total);
+    if (s < p.num_seqs) a.seq_begin[s] = n_tiles + end - n;
+    n_tiles += total;
+  }
+  n_tiles = min(n_tiles, a.max_items);
+  __syncthreads();
+  auto seq_of = [&](int64_t x) {
+    int lo = 0, hi = p.num_seqs - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (a.seq_begin[mid] <= x) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+  };
+  const bool split = a.split_sms > 0 && n_tiles * p.Hkv < 2 * (int64_t)a.split_sms;
+  int piece = INT32_MAX;
+  if (split) {
+    unsigned long long c = 0;
+    for (int64_t x = tid; x < n_tiles; x += kPlanThreads) {
+      const int s = seq_of(x);
+      c += (unsigned long long)item(attn_seq(p, s), x - a.seq_begin[s]).kt1;
+    }
+    atomicAdd(&cost_sum, c);
+    __syncthreads();
+    const int64_t share = ((int64_t)cost_sum * p.Hkv + a.split_sms - 1) / a.split_sms;
+    piece = (int)max((int64_t)kMinPiece, share);
+  }
+  // pieces of tile x: how many, and each one's key tiles
+  auto pieces = [&](const AttnItem& it) { return it.kt1 <= piece ? 1 : (it.kt1 + piece - 1) / piece; };
+  for (int64_t x = tid; x < n_tiles; x += kPlanThreads) {
+    const int s = seq_of(x);
+    const AttnItem it = item(attn_seq(p, s), x - a.seq_begin[s]);
+    const int np = pieces(it);
+    for (int k = 0; k < np; ++k) {
+      const int64_t k0 = (int64_t)it.kt1 * k / np, k1 = (int64_t)it.kt1 * (k + 1) / np;
+      atomicAdd(&hist[bucket_of((int)(k1 - k0))], 1);
+    }
+  }
+  __syncthreads();
+  // hist[b] becomes the first place of bucket b: costlier buckets go first
+  int64_t before = 0;
+  for (int base = 0; base < kBuckets; base += kPlanThreads) {
+    const int bkt = kBuckets - 1 - (base + tid);
+    int64_t total;
+    const int64_t n = bkt >= 0 ? hist[bkt] : 0;
+    const int64_t end = plan_scan(n, part, &total);
+    if (bkt >= 0) hist[bkt] = (int)(before + end - n);
+    before += total;
+  }
+  __syncthreads();
+  int64_t slots = 0, joins = 0;
+  for (int64_t base = 0; base < n_tiles; base += kPlanThreads) {
+    const int64_t x = base + tid;
+    AttnItem it{};
+    int np = 0;
+    if (x < n_tiles) {
+      const int s = seq_of(x);
+      it = item(attn_seq(p, s), x - a.seq_begin[s]);
+      np = pieces(it);
+    }
+    int64_t slot0 = 0, join = 0;
+    if (split) {  // partial results in tile order, whatever the order of the atomics below
+      int64_t total;
+      const int64_t mine = np > 1 ? np : 0;
+      slot0 = slots + plan_scan(mine, part, &total) - mine;
+      slots += total;
+      const int64_t one = np > 1;
+      join = joins + plan_scan(one, part, &total) - one;
+      joins += total;
+    }
+    if (np > 1) {
+      a.joins[join] = AttnJoin{it.tok0, it.ntok, (int32_t)slot0, np};
+    }
+    const int kt1 = it.kt1;
+    for (int k = 0; k < np; ++k) {
+      it.kt0 = (int)((int64_t)kt1 * k / np);
+      it.kt1 = (int)((int64_t)kt1 * (k + 1) / np);
+      it.slot = np > 1 ? (int32_t)(slot0 + k) : -1;
+      a.items[atomicAdd(&hist[bucket_of(it.kt1 - it.kt0)], 1)] = it;
+    }
+  }
+  if (tid == 0) {
+    a.head->items = (int32_t)before;
+    a.head->joins = (int32_t)joins;
+  }
+}
+
+// The pieces of a cut item joined: with M = max m_k, o = sum 2^(m_k - M) O_k /
+// sum 2^(m_k - M) l_k, in piece order.  A warp per row.
+template <int DP>
+__global__ void __launch_bounds__(256) attn_join(const AttnParams p, const TcArgs a, int tpt) {
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t pairs = (int64_t)a.head->joins * p.Hkv;
+  constexpr int V = DP / 32;
+  for (int64_t w = blockIdx.x; w < pairs * 32; w += gridDim.x) {
+    const AttnJoin jn = a.joins[w / 32 / p.Hkv];
+    const int h = (int)(w / 32 % p.Hkv), r = (int)(w % 32) * 8 + warp;
+    const int t = r / kTile, row = r % kTile, tok = t * tpt + row / p.G;
+    if (row >= tpt * p.G || tok >= jn.ntok) continue;
+    float M = -INFINITY;
+    for (int k = 0; k < jn.pieces; ++k)
+      M = fmaxf(M, a.part_ml[((int64_t)(jn.slot + k) * p.Hkv + h) * (2 * kTile) + r].x);
+    if (M == -INFINITY) M = 0.f;
+    float l = 0.f, o[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) o[v] = 0.f;
+    for (int k = 0; k < jn.pieces; ++k) {
+      const int64_t at = ((int64_t)(jn.slot + k) * p.Hkv + h) * (2 * kTile) + r;
+      const float2 ml = a.part_ml[at];
+      const float f = exp2_fast(ml.x - M);
+      l += f * ml.y;
+#pragma unroll
+      for (int v = 0; v < V; ++v) o[v] = fmaf(f, a.part_o[at * DP + v * 32 + lane], o[v]);
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    __nv_bfloat16* out =
+        static_cast<__nv_bfloat16*>(p.o) + ((int64_t)(jn.tok0 + tok) * p.H + (int64_t)h * p.G + row % p.G) * p.D;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (v * 32 + lane < p.D) out[v * 32 + lane] = __float2bfloat16_rn(o[v] * inv);
+  }
+}
+
+// ------------------------------------------------------------------ host
+bool encode_q(CUtensorMap* m, const AttnParams& p, int tpt) {
+  const EncodeTiledFn enc = encode_tiled();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)p.D, (cuuint64_t)p.H, (cuuint64_t)p.total_tokens};
+  const cuuint64_t strides[2] = {(cuuint64_t)p.D * 2, (cuuint64_t)p.H * p.D * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)tpt};
+  const cuuint32_t elem[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p.q), dims, strides, box, elem,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// K or V as [pages][positions][Hkv][D] (packed: one page of all tokens), box
+// {64 channels, 1 head, `box` positions, 1 page}; what lies outside reads as zeros
+bool encode_kv(CUtensorMap* m, const AttnParams& p, const void* base, int box) {
+  const EncodeTiledFn enc = encode_tiled();
+  if (!enc) return false;
+  const bool paged = p.block_table != nullptr;
+  const cuuint64_t page = paged ? (cuuint64_t)1 << p.page_shift : (cuuint64_t)p.total_tokens;
+  const cuuint64_t row = (cuuint64_t)p.Hkv * p.D * 2;
+  const cuuint64_t dims[4] = {(cuuint64_t)p.D, (cuuint64_t)p.Hkv, page, paged ? (cuuint64_t)p.num_pages : 1};
+  const cuuint64_t strides[3] = {(cuuint64_t)p.D * 2, row, row * page};
+  const cuuint32_t bx[4] = {64, 1, (cuuint32_t)box, 1};
+  const cuuint32_t elem[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, bx, elem,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int padded(int D) { return D <= 64 ? 64 : 128; }
+
+struct TcLayout {
+  size_t head, seq_begin, items, joins, ml, o, total;
+  int64_t max_items, max_pieces;
+  bool split;
+};
+TcLayout layout(const AttnParams& p) {
+  TcLayout L{};
+  const int tpi = 2 * (kTile / p.G);
+  L.max_items = (p.total_tokens + tpi - 1) / tpi + p.num_seqs;
+  // pieces only where the whole batch cannot fill the GPU: at most two per SM
+  // are whole items, and the cuts add one per SM
+  L.split = p.block_table && (p.total_tokens + tpi - 1) / tpi * p.Hkv < 2 * kSplitSms;
+  L.max_pieces = L.split ? 3 * (int64_t)kSplitSms / p.Hkv + 1 : 0;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = align_up(off + bytes, 256);
+    return at;
+  };
+  L.head = take(sizeof(AttnHead));
+  L.seq_begin = take(sizeof(int64_t) * p.num_seqs);
+  L.items = take(sizeof(AttnItem) * (size_t)(L.max_items + L.max_pieces));
+  if (L.split) {
+    L.joins = take(sizeof(AttnJoin) * (size_t)(2 * kSplitSms));
+    const size_t rows = (size_t)L.max_pieces * p.Hkv * 2 * kTile;
+    L.ml = take(rows * sizeof(float2));
+    L.o = take(rows * padded(p.D) * sizeof(float));
+  }
+  L.total = off;
+  return L;
+}
+
+template <int DP>
+cudaError_t launch_dp(const AttnParams& p, const TcLayout& L, char* w, cudaStream_t stream) {
+  using S = Shape<DP>;
+  const int tpt = kTile / p.G, page = p.block_table ? 1 << p.page_shift : kTile;
+  TcArgs a{};
+  a.head = reinterpret_cast<AttnHead*>(w + L.head);
+  a.seq_begin = reinterpret_cast<int64_t*>(w + L.seq_begin);
+  a.items = reinterpret_cast<AttnItem*>(w + L.items);
+  a.max_items = L.max_items;
+  a.box_tokens = page < kTile ? page : kTile;
+  if (L.split) {
+    a.split_sms = kSplitSms;
+    a.joins = reinterpret_cast<AttnJoin*>(w + L.joins);
+    a.part_ml = reinterpret_cast<float2*>(w + L.ml);
+    a.part_o = reinterpret_cast<float*>(w + L.o);
+  }
+  CUtensorMap mq, mk, mv;
+  if (!encode_q(&mq, p, tpt) || !encode_kv(&mk, p, p.k, a.box_tokens) || !encode_kv(&mv, p, p.v, a.box_tokens))
+    return cudaErrorInvalidValue;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(attn_tc<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kBytes);
+  if (e != cudaSuccess) return e;
+  attn_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p, a, 2 * tpt);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const int64_t most = (L.max_items + L.max_pieces) * p.Hkv;
+  e = launch_maybe_dependent(true, attn_tc<DP>, dim3((unsigned)(most < sms ? most : sms)), dim3(kThreads),
+                             (size_t)S::kBytes, stream, p, a, mq, mk, mv);
+  if (e != cudaSuccess || !L.split) return e;
+  return launch_maybe_dependent(true, attn_join<DP>, dim3((unsigned)(4 * sms)), dim3(256), 0, stream, p, a, tpt);
+}
+
+}  // namespace
+
+// bf16, up to 128 channels (narrower heads run zero-padded to 64 or 128 by the
+// copies), a positive finite scale (the running maximum is taken before the
+// scaling), and what the tensor maps need: 16-byte aligned bases and indices
+// inside int32.  Everything else runs on the CUDA cores.
+bool attn_tc_fits(const AttnParams& p) {
+  auto al16 = [](const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15) == 0; };
+  return p.dt == KDA_BF16 && p.D <= 128 && p.scale > 0.f && p.scale <= 3.4e38f && al16(p.q) && al16(p.k) &&
+         al16(p.v) && al16(p.o) && (!p.block_table || p.num_pages > 0);
+}
+size_t attn_tc_workspace(const AttnParams& p) { return layout(p).total; }
+cudaError_t launch_attn_tc(const AttnParams& p, void* ws, cudaStream_t stream) {
+  const TcLayout L = layout(p);
+  char* w = static_cast<char*>(ws);
+  return p.D <= 64 ? launch_dp<64>(p, L, w, stream) : launch_dp<128>(p, L, w, stream);
+}
+
+}  // namespace kda

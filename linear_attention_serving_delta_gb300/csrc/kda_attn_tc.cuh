@@ -1,0 +1,152 @@
+// kda_attn_tc.cuh -- plan records and PTX helpers of the tensor-core attention.
+//
+// Shared-memory operands here are 128-byte swizzled: a tile is stored in
+// blocks of 64 channels, each [rows][64] bf16 with rows of 128 bytes whose
+// eight 16-byte pieces are permuted by row % 8 (what a tensor-map copy with
+// CU_TENSOR_MAP_SWIZZLE_128B writes).  As a K-major operand (Q, K) the 8-row
+// groups are 1024 bytes apart and 16 channels are 32 bytes; as an MN-major
+// one (V, whose tokens are the contraction) the 64-channel blocks are the
+// leading stride, and 16 tokens are 2048 bytes.
+#pragma once
+
+#include "kda_attn.cuh"
+#include "kda_tc.cuh"
+
+namespace kda {
+
+// The SMs the cut into pieces is sized for, and the fewest key tiles a piece has
+constexpr int kSplitSms = 152;
+constexpr int kMinPiece = 4;
+
+// One unit of work (for each key head): ntok tokens from packed token tok0 on,
+// the first at position pos0, over the key tiles [kt0, kt1) of a sequence of
+// kv_len positions.  base: the sequence's first packed token (prompts) or its
+// row of the block table.  slot >= 0: a piece, its partial result's place.
+struct AttnItem {
+  int32_t tok0, ntok, base, pos0, kv_len, kt0, kt1, slot;
+};
+struct AttnJoin {
+  int32_t tok0, ntok, slot, pieces;
+};
+struct AttnHead {
+  int32_t items, joins;
+};
+struct TcArgs {
+  AttnHead* head;
+  int64_t* seq_begin;   // [N] first tile of each sequence
+  AttnItem* items;
+  int64_t max_items;    // tiles the workspace has room for
+  int32_t box_tokens;   // positions per copy
+  int32_t split_sms;    // > 0: items may be cut into pieces
+  AttnJoin* joins;
+  float2* part_ml;      // [pieces][Hkv][256] (m, l)
+  float* part_o;        // [pieces][Hkv][256][DP]
+};
+
+namespace tc {
+
+// descriptor of a 128-byte swizzled operand (see above)
+__device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return sdesc(saddr, lbo, sbo) | ((uint64_t)2 << 61);
+}
+
+// D[tmem] (+)= A[tmem] * B[smem], A bf16 in 32-bit columns of two
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// 32 lanes x 32 columns of 32-bit data (see tmem_ld16 / tmem_st16)
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+      "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+      "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// Tensor-map copies into shared memory, completion counted in bytes on `bar`.
+// The innermost coordinate is a multiple of 64 bf16 here (TMA wants 16 bytes).
+__device__ __forceinline__ void tma_3d(void* dst, const CUtensorMap* m, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(smem_u32(dst)),
+      "l"(m), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma_4d(void* dst, const CUtensorMap* m, int x, int y, int z, int w, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(smem_u32(dst)),
+      "l"(m), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// 2^x with the hardware approximation (relative error about 2^-22), 0 below 2^-126
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// two fp32 operations per instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return d;
+}
+// two floats to bf16, `lo` in the low half
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// two bf16, each zeroed if it is infinite or NaN
+__device__ __forceinline__ uint32_t finite_only(uint32_t w) {
+  if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+  if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
+  return w;
+}
+
+}  // namespace tc
+
+bool attn_tc_fits(const AttnParams& p);
+size_t attn_tc_workspace(const AttnParams& p);
+cudaError_t launch_attn_tc(const AttnParams& p, void* ws, cudaStream_t stream);
+
+}  // namespace kda
