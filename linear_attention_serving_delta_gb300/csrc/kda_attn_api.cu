@@ -101,12 +101,17 @@ AttnParams params(const kda_attn_paged_args* a) {
   return p;
 }
 
-size_t attn_workspace(const AttnParams& p) { return attn_tc_fits(p) ? attn_tc_workspace(p) : 256; }
+// A few rows a request: the streaming kernel; else the tensor cores; else the
+// CUDA cores.
+size_t attn_workspace(const AttnParams& p) {
+  return attn_rows_fits(p) ? attn_rows_workspace(p) : attn_tc_fits(p) ? attn_tc_workspace(p) : 256;
+}
 
 kda_status_t run_attn(const AttnParams& p, void* ws, size_t ws_bytes, void* stream) {
   if (!ws || ws_bytes < attn_workspace(p) || misaligned(ws)) return KDA_ERR_WORKSPACE;
   if (p.total_tokens == 0) return KDA_OK;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (attn_rows_fits(p)) return from_cuda(launch_attn_rows(p, ws, s));
   return from_cuda(attn_tc_fits(p) ? launch_attn_tc(p, ws, s) : launch_attn_simt(p, s));
 }
 

@@ -1,0 +1,798 @@
+// kda_attn_rows.cu -- attention of a few rows per request over the paged
+// cache: single tokens, or a few of them, of at most 16 rows with their group
+// of query heads (row = token * G + head).
+//
+// Such a step reads every cached key and value once and does little with
+// them, so the kernel is a stream: it is bound by HBM.  The key tiles of all
+// (request, key head) pairs form one line of work, pair after pair, and every
+// CTA of a grid that fills the GPU takes an equal stretch of it, whatever the
+// requests' lengths.  A pair inside one stretch is finished there; one that
+// crosses stretches leaves its parts (unnormalised output, running maximum m
+// and sum l, fp32) for attn_rows_join, which adds them in line order:
+//   M = max m_k,  o = sum 2^(m_k - M) O_k / sum 2^(m_k - M) l_k.
+//
+// In a CTA one warp copies tiles into a ring (tensor-map copies, a box per
+// page, 128-byte swizzle) and four warps each take a quarter of a tile's keys
+// with softmax statistics of their own, joined at the end of a pair.  bf16:
+// 16 keys a warp on mma.sync (a 128-row tcgen05 tile would be 7/8 padding
+// here, and the tensor cores wait for memory either way); the weights are
+// rounded to bf16, as P V's operand.  fp32: 8 keys a warp on FMAs.
+#include "kda_attn_tc.cuh"
+
+namespace kda {
+namespace {
+
+using namespace tc;
+
+constexpr int kWarps = 4;                      // consumers
+constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kMaxRows = 16;
+constexpr int kMinTiles = 4;                   // shortest stretch of a CTA
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLazyLog2 = 8.f;  // how far the maximum may rise before O is rescaled
+
+template <typename T, int DP>
+struct Shape {
+  static constexpr int KT = sizeof(T) == 2 ? 64 : 32;      // keys of a tile
+  static constexpr int NB = DP * (int)sizeof(T) / 128;     // 128-byte blocks of a row
+  static constexpr uint32_t kBlock = KT * 128;
+  static constexpr uint32_t kKV = 2 * NB * kBlock;         // K, then V; also the joining warps' scratch
+  static constexpr uint32_t kQBlock = kMaxRows * 128;      // bf16: q of a pair, with its first tile
+  static constexpr uint32_t kStage = kKV + (sizeof(T) == 2 ? NB * kQBlock : 0);
+  static constexpr int CTAS = kKV <= 32768 ? 2 : 1;
+  static constexpr int kStages = kKV <= 8192 ? 8 : kKV <= 16384 ? 5 : 3;
+  static constexpr uint32_t kQ = kStages * kStage;         // fp32: the pair's q rows, plain
+  static constexpr uint32_t kTail = kQ + (sizeof(T) == 4 ? kMaxRows * DP * 4 : 0);
+  static constexpr uint32_t kBytes = kTail + 2048 + 1024;  // barriers; slack to align the base
+};
+static_assert(Shape<__nv_bfloat16, 128>::kKV >= kWarps * kMaxRows * 128 * 4, "the warps' outputs fit a stage");
+static_assert(Shape<float, 128>::kKV >= kWarps * kMaxRows * 128 * 4, "the warps' outputs fit a stage");
+static_assert(2 * (Shape<__nv_bfloat16, 128>::kBytes + 1024) <= 233472, "two CTAs per SM");
+static_assert(2 * (Shape<float, 128>::kBytes + 1024) <= 233472, "two CTAs per SM");
+static_assert(Shape<float, 256>::kBytes <= 232448 && Shape<__nv_bfloat16, 256>::kBytes <= 232448, "one CTA");
+
+// A tile in the ring, for its consumers
+struct Tile {
+  int32_t tok0, len, kv_len, head;
+  int32_t x0;     // position of its first key
+  int32_t first;  // of the pair in this stretch
+  int32_t last;
+  int32_t slot;   // at the last tile: where the part goes, or -1 (the pair is whole)
+};
+
+struct Tail {
+  uint64_t full[8], empty[8];
+  uint64_t join[2];
+  uint32_t dead;
+  uint32_t pad;
+  Tile tile[8];
+  float2 ml[kWarps][kMaxRows];
+  int64_t sum[kWarps + 1];
+  int64_t found[2];
+};
+static_assert(sizeof(Tail) <= 2048, "tail block");
+
+struct RowsJoin {
+  int32_t parts;  // 0: nothing to join
+  int32_t tok0, len, head;
+};
+struct RowsArgs {
+  RowsJoin* joins;  // [grid]
+  float2* ml;       // [2 grid][16]
+  float* o;         // [2 grid][16][DP]
+  int32_t box;      // positions per copy
+  int32_t q_tokens; // tokens of q per copy
+};
+
+template <typename T, int DP>
+__device__ __forceinline__ int tiles_of(const AttnSeq& q) {
+  constexpr int KT = Shape<T, DP>::KT;
+  if (q.len == 0) return 0;
+  return q.kv_len <= KT ? 1 : (int)((q.kv_len + KT - 1) / KT);  // a pair without keys still writes its zeros
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t* r, uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t* r, uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a));
+}
+__device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// byte offset of 16-byte piece c of row r in swizzled blocks of `block` bytes
+__device__ __forceinline__ uint32_t sw_off(int r, int c, uint32_t block) {
+  return (uint32_t)(c >> 3) * block + (uint32_t)r * 128u + (uint32_t)(((c & 7) ^ (r & 7)) << 4);
+}
+
+// One quarter-tile's work and its running state, bf16
+template <int DP>
+struct RowsBf16 {
+  using S = Shape<__nv_bfloat16, DP>;
+  static constexpr int NK = DP / 16, NV = DP / 8;
+  uint32_t q[NK][4];
+  float o[NV][4], m[2], l[2];
+
+  __device__ void start(const char* stage, float*, int lane) {
+    const uint32_t qs = smem_u32(stage + S::kKV);
+#pragma unroll
+    for (int k = 0; k < NK; ++k)
+      ldsm4(q[k], qs + sw_off((lane & 7) + ((lane >> 3) & 1) * 8, 2 * k + (lane >> 4), S::kQBlock));
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[v][e] = 0.f;
+    m[0] = m[1] = -INFINITY;
+    l[0] = l[1] = 0.f;
+  }
+
+  __device__ void step(char* stage, const float*, const Tile& t, int G, float sc, int warp, int lane) {
+    const int x0 = t.x0 + 16 * warp;  // this warp's keys
+    if (x0 >= t.kv_len) return;
+    const uint32_t ks = smem_u32(stage);
+    char* vs = stage + S::NB * S::kBlock;
+    const int live = min(16, t.kv_len - x0);
+    bool poison = false;
+    const int from = t.kv_len - t.len;  // position of the first row
+    const bool masked = x0 + 15 > from;
+    if (masked) {
+      // rows of V behind the sequence to zero; non-finite values that some row may not attend
+      for (int i = lane; i < 16 * S::NB * 8; i += 32) {
+        const int r = i / (S::NB * 8), c = i % (S::NB * 8);
+        uint4* x = reinterpret_cast<uint4*>(vs + sw_off(16 * warp + r, c, S::kBlock));
+        if (r >= live) *x = make_uint4(0, 0, 0, 0);
+        else if (t.len > 1) {
+          const uint4 y = *x;
+          poison |= ((((y.x & 0x7f807f80u) + 0x00800080u) | ((y.y & 0x7f807f80u) + 0x00800080u) |
+                      ((y.z & 0x7f807f80u) + 0x00800080u) | ((y.w & 0x7f807f80u) + 0x00800080u)) & 0x80008000u) != 0;
+        }
+      }
+      poison = __any_sync(0xffffffffu, poison);
+    }
+    float s[2][4];
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+#pragma unroll
+    for (int k = 0; k < NK; ++k) {
+      uint32_t b[4];
+      ldsm4(b, ks + sw_off(16 * warp + (lane & 7) + (lane >> 4) * 8, 2 * k + ((lane >> 3) & 1), S::kBlock));
+      mma16816(s[0], q[k], b[0], b[1]);
+      mma16816(s[1], q[k], b[2], b[3]);
+    }
+    const int r0 = lane >> 2, c0 = 2 * (lane & 3);
+    int limit[2];
+    if (masked) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) limit[h] = min(t.kv_len - 1, from + (r0 + 8 * h) / G) - x0;
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (8 * n + c0 + (e & 1) > limit[e >> 1]) s[n][e] = -INFINITY;
+    }
+    float x[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      x[h] = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
+      x[h] = fmaxf(x[h], __shfl_xor_sync(0xffffffffu, x[h], 1));
+      x[h] = sc * fmaxf(x[h], __shfl_xor_sync(0xffffffffu, x[h], 2));
+    }
+    bool move[2], scale[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      move[h] = x[h] > m[h] + kLazyLog2 || (m[h] == -INFINITY && x[h] > m[h]);
+      scale[h] = move[h] && m[h] != -INFINITY;
+    }
+    if (__any_sync(0xffffffffu, scale[0] || scale[1])) {
+      const float f0 = scale[0] ? exp2_fast(m[0] - x[0]) : 1.f, f1 = scale[1] ? exp2_fast(m[1] - x[1]) : 1.f;
+      l[0] *= f0;
+      l[1] *= f1;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        o[v][0] *= f0;
+        o[v][1] *= f0;
+        o[v][2] *= f1;
+        o[v][3] *= f1;
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (move[h]) m[h] = x[h];
+    const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s[n][e] = exp2_fast(fmaf(s[n][e], sc, -ref[e >> 1]));
+        l[e >> 1] += s[n][e];
+      }
+    if (masked && poison) {  // key by key, into the rows that attend it
+      const float* p0 = &s[0][0];
+      for (int k = 0; k < live; ++k) {
+        const int src = (lane & ~3) | ((k & 7) >> 1);
+        float w[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float y = 0.f;
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {  // the score's register, by a fixed index
+            const int n = z >> 1, e = z & 1;
+            const float c = __shfl_sync(0xffffffffu, p0[4 * n + 2 * h + e], src);
+            if (n == (k >> 3) && e == (k & 1)) y = c;
+          }
+          w[h] = __bfloat162float(__float2bfloat16_rn(y));
+        }
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          const uint32_t y = *reinterpret_cast<const uint32_t*>(vs + sw_off(16 * warp + k, v, S::kBlock) + 4 * (lane & 3));
+          const float y0 = __uint_as_float(y << 16), y1 = __uint_as_float(y & 0xffff0000u);
+          if (k <= limit[0]) {
+            o[v][0] = fmaf(w[0], y0, o[v][0]);
+            o[v][1] = fmaf(w[0], y1, o[v][1]);
+          }
+          if (k <= limit[1]) {
+            o[v][2] = fmaf(w[1], y0, o[v][2]);
+            o[v][3] = fmaf(w[1], y1, o[v][3]);
+          }
+        }
+      }
+      return;
+    }
+    __syncwarp();  // V's zeroed rows
+    const uint32_t a[4] = {pack2(s[0][0], s[0][1]), pack2(s[0][2], s[0][3]), pack2(s[1][0], s[1][1]),
+                           pack2(s[1][2], s[1][3])};
+    const uint32_t va = smem_u32(vs);
+#pragma unroll
+    for (int v = 0; v < NV; v += 2) {
+      uint32_t b[4];
+      ldsm4t(b, va + sw_off(16 * warp + (lane & 15), v + (lane >> 4), S::kBlock));
+      mma16816(o[v], a, b[0], b[1]);
+      mma16816(o[v + 1], a, b[2], b[3]);
+    }
+  }
+
+  // m and l of the warp's rows; then its output times f[row half] into scratch [16][DP]
+  __device__ void stats(float2* ml, int lane) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+      if ((lane & 3) == 0) ml[(lane >> 2) + 8 * h] = make_float2(m[h], l[h]);
+    }
+  }
+  __device__ void put(float* scratch, const float2 (*ml)[kMaxRows], int rows, int lane) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = (lane >> 2) + 8 * h;
+      if (r >= rows) continue;
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w][r].x);
+      const float f = exp2_fast(m[h] - (M == -INFINITY ? 0.f : M));
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        *reinterpret_cast<float2*>(scratch + r * DP + 8 * v + 2 * (lane & 3)) =
+            make_float2(o[v][2 * h] * f, o[v][2 * h + 1] * f);
+    }
+  }
+};
+
+// The same in fp32: a lane holds one key and a quarter of its channels for the
+// scores, then DP / 32 channels of the output
+template <int DP, int RT_>
+struct RowsF32 {
+  using S = Shape<float, DP>;
+  static constexpr int RT = RT_, NC = DP / 32 > 4 ? 4 : DP / 32, NG = DP / 32 / NC;  // channels: NG groups of NC
+  float o[RT][NG * NC], m[RT], l[RT];
+
+  __device__ void start(const char* stage, float* qs, int lane) {
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+#pragma unroll
+      for (int c = 0; c < NG * NC; ++c) o[r][c] = 0.f;
+      m[r] = -INFINITY;
+      l[r] = 0.f;
+    }
+    (void)stage;
+    (void)qs;
+    (void)lane;
+  }
+  // the pair's q rows, by all consumers; rows it does not have are zeros
+  static __device__ void load_q(const AttnParams& p, const Tile& t, float* qs, int tid) {
+    const float* q = static_cast<const float*>(p.q);
+    for (int i = tid; i < RT * DP; i += 32 * kWarps) {
+      const int r = i / DP, c = i % DP;
+      qs[i] = r < t.len * p.G && c < p.D
+                  ? q[((int64_t)(t.tok0 + r / p.G) * p.H + (int64_t)t.head * p.G + r % p.G) * p.D + c]
+                  : 0.f;
+    }
+  }
+
+  __device__ void step(char* stage, const float* qs, const Tile& t, int G, float sc, int warp, int lane) {
+    const int x0 = t.x0 + 8 * warp;
+    if (x0 >= t.kv_len) return;
+    const int live = min(8, t.kv_len - x0), from = t.kv_len - t.len;
+    const bool masked = x0 + 7 > from;
+    const int i = lane >> 2, qd = lane & 3;
+    const int key = ((i & 1) << 2) | (i >> 1);  // lanes of a load phase four keys apart: no bank conflict
+    float s[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) s[r] = 0.f;
+#pragma unroll 2
+    for (int c = qd; c < DP / 4; c += 4) {
+      const float4 k4 = *reinterpret_cast<const float4*>(stage + sw_off(8 * warp + key, c, S::kBlock));
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        const float4 q4 = *reinterpret_cast<const float4*>(qs + r * DP + 4 * c);
+        s[r] = fmaf(q4.x, k4.x, fmaf(q4.y, k4.y, fmaf(q4.z, k4.z, fmaf(q4.w, k4.w, s[r]))));
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      s[r] += __shfl_xor_sync(0xffffffffu, s[r], 1);
+      s[r] += __shfl_xor_sync(0xffffffffu, s[r], 2);
+      s[r] *= sc;
+      if (masked && x0 + key > min(t.kv_len - 1, from + r / G)) s[r] = -INFINITY;
+      float x = s[r];
+      x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+      x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+      x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+      if (x > m[r]) {  // uniform in the warp
+        const float f = exp2f(m[r] - x);
+        l[r] *= f;
+#pragma unroll
+        for (int c = 0; c < NG * NC; ++c) o[r][c] *= f;
+        m[r] = x;
+      }
+      s[r] = exp2f(s[r] - (m[r] == -INFINITY ? 0.f : m[r]));
+      l[r] += s[r];
+    }
+    const char* vs = stage + S::NB * S::kBlock;
+    for (int k = 0; k < live; ++k) {
+      float v[NG * NC];
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        const int ch = g * 128 + lane * NC;  // first channel of this lane's group
+        const char* a = vs + sw_off(8 * warp + k, ch >> 2, S::kBlock) + (ch & 3) * 4;
+        if (NC == 4) {
+          const float4 y = *reinterpret_cast<const float4*>(a);
+          v[g * NC] = y.x;
+          v[g * NC + 1 % NC] = y.y;
+          v[g * NC + 2 % NC] = y.z;
+          v[g * NC + 3 % NC] = y.w;
+        } else {
+#pragma unroll
+          for (int c = 0; c < NC; ++c) v[g * NC + c] = *reinterpret_cast<const float*>(a + 4 * c);
+        }
+      }
+      const int src = (((k & 3) << 1) | (k >> 2)) << 2;  // a lane that holds key k
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        const float w = __shfl_sync(0xffffffffu, s[r], src);
+        if (!masked || x0 + k <= from + r / G) {  // a masked key's value stays out even where it is not finite
+#pragma unroll
+          for (int c = 0; c < NG * NC; ++c) o[r][c] = fmaf(w, v[c], o[r][c]);
+        }
+      }
+    }
+  }
+  __device__ void stats(float2* ml, int lane) {
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      float x = l[r];
+      x += __shfl_xor_sync(0xffffffffu, x, 4);
+      x += __shfl_xor_sync(0xffffffffu, x, 8);
+      x += __shfl_xor_sync(0xffffffffu, x, 16);
+      if (lane == 0) ml[r] = make_float2(m[r], x);
+    }
+  }
+  __device__ void put(float* scratch, const float2 (*ml)[kMaxRows], int rows, int lane) {
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      if (r >= rows) break;
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w][r].x);
+      const float f = exp2f(m[r] - (M == -INFINITY ? 0.f : M));
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int c = 0; c < NC; ++c) scratch[r * DP + g * 128 + lane * NC + c] = o[r][g * NC + c] * f;
+    }
+  }
+};
+
+template <typename T, int DP, typename Work>
+__global__ void __launch_bounds__(kThreads, Shape<T, DP>::CTAS)
+    attn_rows(const AttnParams p, const RowsArgs a, const __grid_constant__ CUtensorMap mq,
+              const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+  using S = Shape<T, DP>;
+  constexpr int KT = S::KT;
+  extern __shared__ char raw[];
+  char* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  Tail* b = reinterpret_cast<Tail*>(sm + S::kTail);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int s = 0; s < S::kStages; ++s) {
+      mbar_init(&b->full[s], 1);
+      mbar_init(&b->empty[s], kWarps);
+    }
+    mbar_init(&b->join[0], kWarps);
+    mbar_init(&b->join[1], kWarps);
+    b->dead = 0;
+    b->found[0] = -1;
+    mbar_init_fence();
+  }
+  pdl_wait();
+
+  // the line of work: its length, this CTA's stretch, and where that starts
+  int64_t W = 0, u0 = 0, u1 = 0, before = 0;
+  int64_t first_seq = -1, first_off = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    before = 0;
+    for (int base = 0; base < p.num_seqs; base += kThreads) {
+      const int s = base + tid;
+      int64_t n = 0;
+      if (s < p.num_seqs) {
+        const AttnSeq q = attn_seq(p, s);
+        if (pass == 0 && q.flag && blockIdx.x == 0) attn_flag(p.status, q.flag);
+        n = (int64_t)tiles_of<T, DP>(q) * p.Hkv;
+      }
+      int64_t x = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      __syncthreads();
+      if (lane == 31) b->sum[warp] = x;
+      __syncthreads();
+      int64_t total = 0;
+#pragma unroll
+      for (int w = 0; w <= kWarps; ++w) {
+        if (w < warp) x += b->sum[w];
+        total += b->sum[w];
+      }
+      if (pass == 1 && n > 0 && u0 >= before + x - n && u0 < before + x) {
+        b->found[0] = s;
+        b->found[1] = u0 - (before + x - n);
+      }
+      before += total;
+      if (pass == 1 && u0 < before) break;
+    }
+    if (pass == 0) {
+      W = before;
+      const int64_t share = (W + gridDim.x - 1) / gridDim.x;
+      const int64_t per = share > kMinTiles ? share : kMinTiles;
+      u0 = min(W, per * blockIdx.x);
+      u1 = min(W, u0 + per);
+      first_off = per;
+      if (u0 == u1) {
+        if (tid == 0) a.joins[blockIdx.x].parts = 0;
+        return;
+      }
+    }
+  }
+  __syncthreads();
+  const int64_t per = first_off;
+  first_seq = b->found[0];
+  first_off = b->found[1];
+
+  if (warp == kWarps) {
+    // ---- copies
+    int base = (int)first_seq, cur = 0;  // 32 requests at a time, one a lane
+    AttnSeq mine{};
+    int mine_n = 0;
+    auto fetch = [&](int at) {
+      base = at;
+      mine = AttnSeq{};
+      mine_n = 0;
+      if (at + lane < p.num_seqs) {
+        mine = attn_seq(p, at + lane);
+        mine_n = tiles_of<T, DP>(mine);
+      }
+    };
+    fetch(base);
+    int n = __shfl_sync(0xffffffffu, mine_n, 0);
+    int head = (int)(first_off / n), tile = (int)(first_off % n);
+    bool seg_first = true;
+    int seg_tile0 = tile;
+    bool ok = true;
+    uint32_t k = 0;
+    if (lane == 0) a.joins[blockIdx.x].parts = 0;
+    const uint32_t box_bytes = (uint32_t)a.box * 128u;
+    for (int64_t u = u0; u < u1 && ok; ++u, ++k) {
+      const int tok0 = (int)__shfl_sync(0xffffffffu, mine.tok0, cur), len = __shfl_sync(0xffffffffu, mine.len, cur);
+      const int kv = (int)__shfl_sync(0xffffffffu, mine.kv_len, cur), row = __shfl_sync(0xffffffffu, mine.row, cur);
+      const int x0 = tile * KT;
+      const int nb = max(0, min(KT / a.box, (kv - x0 + a.box - 1) / a.box));
+      int c2 = 0, c3 = 0;
+      if (lane < nb) {
+        const int x = x0 + lane * a.box;
+        int page = p.block_table[(int64_t)row * p.max_pages + (x >> p.page_shift)];
+        if (page < 0 || page >= p.num_pages) {
+          attn_flag(p.status, kFlagBadCache);
+          page = p.num_pages;  // outside the map: filled with zeros
+        }
+        c2 = x & ((1 << p.page_shift) - 1);
+        c3 = page;
+      }
+      const uint32_t st = k % S::kStages;
+      ok = __all_sync(0xffffffffu, wait_or_dead(&b->empty[st], ((k / S::kStages) & 1) ^ 1, &b->dead));
+      if (!ok) break;
+      char* dst = sm + st * S::kStage;
+      const bool last = u + 1 == u1 || tile + 1 == n;
+      if (lane == 0) {
+        Tile t;
+        t.tok0 = tok0;
+        t.len = len;
+        t.kv_len = kv;
+        t.head = head;
+        t.x0 = x0;
+        t.first = seg_first;
+        t.last = last;
+        t.slot = -1;
+        if (last && (seg_tile0 > 0 || tile + 1 < n)) {
+          t.slot = 2 * (int)blockIdx.x + (seg_tile0 == 0);
+          if (seg_tile0 == 0)  // the pair starts here: its other parts are the next stretches' first ones
+            a.joins[blockIdx.x] =
+                RowsJoin{(int)((u - tile + n - 1) / per - blockIdx.x + 1), tok0, len, head};
+        }
+        b->tile[st] = t;
+        const uint32_t bytes = (uint32_t)nb * box_bytes * 2 * S::NB +
+                               (sizeof(T) == 2 && seg_first ? (uint32_t)(a.q_tokens * p.G) * 128u * S::NB : 0u);
+        mbar_arrive_expect_tx(&b->full[st], bytes);
+        if (sizeof(T) == 2 && seg_first)
+#pragma unroll
+          for (int c = 0; c < S::NB; ++c)
+            tma_3d(dst + S::kKV + c * S::kQBlock, &mq, c * (128 / (int)sizeof(T)), head * p.G, tok0, &b->full[st]);
+      }
+      __syncwarp();
+      if (lane < nb)
+#pragma unroll
+        for (int c = 0; c < S::NB; ++c) {
+          const int ch = c * (128 / (int)sizeof(T));
+          tma_4d(dst + c * S::kBlock + lane * box_bytes, &mk, ch, head, c2, c3, &b->full[st]);
+          tma_4d(dst + (S::NB + c) * S::kBlock + lane * box_bytes, &mv, ch, head, c2, c3, &b->full[st]);
+        }
+      // the next tile of the line
+      seg_first = last;
+      if (++tile == n) {
+        tile = 0;
+        if (++head == p.Hkv) {
+          head = 0;
+          if (u + 1 < u1) {
+            do {
+              if (++cur == 32) {
+                cur = 0;
+                fetch(base + 32);
+              }
+              n = __shfl_sync(0xffffffffu, mine_n, cur);
+            } while (n == 0 && base + cur < p.num_seqs);
+          }
+        }
+      }
+      if (seg_first) seg_tile0 = tile;
+    }
+    if (!ok)  // no copy in flight when a CTA that gave up exits
+      for (uint32_t i = k > (uint32_t)S::kStages ? k - S::kStages : 0; i < k; ++i)
+        mbar_wait(&b->full[i % S::kStages], (i / S::kStages) & 1, kWaitLimitNs);
+  } else {
+    // ---- scores, softmax, output
+    Work w;
+    float* qs = reinterpret_cast<float*>(sm + S::kQ);
+    const float sc = p.scale * kLog2e;
+    uint32_t joins = 0;
+    uint32_t k = 0;
+    for (int64_t u = u0; u < u1; ++u, ++k) {
+      const uint32_t st = k % S::kStages;
+      char* stage = sm + st * S::kStage;
+      if (!__all_sync(0xffffffffu, wait_or_dead(&b->full[st], (k / S::kStages) & 1, &b->dead))) break;
+      const Tile t = b->tile[st];
+      if (t.first) {
+        if constexpr (sizeof(T) == 4) {
+          // (the last pair's readers of qs are done: they met at its join)
+          Work::load_q(p, t, qs, tid);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&b->join[0]);
+          if (!__all_sync(0xffffffffu, wait_or_dead(&b->join[0], joins & 1, &b->dead))) break;
+          if (lane == 0) mbar_arrive(&b->join[1]);
+          if (!__all_sync(0xffffffffu, wait_or_dead(&b->join[1], joins & 1, &b->dead))) break;
+          ++joins;
+        }
+        w.start(stage, qs, lane);
+      }
+      w.step(stage, qs, t, p.G, sc, warp, lane);
+      if (t.last) {
+        const int rows = t.len * p.G;
+        w.stats(b->ml[warp], lane);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b->join[0]);
+        if (!__all_sync(0xffffffffu, wait_or_dead(&b->join[0], joins & 1, &b->dead))) break;
+        // every warp is done with this stage's K and V: it holds the outputs now
+        float* scratch = reinterpret_cast<float*>(stage);
+        w.put(scratch + warp * kMaxRows * DP, b->ml, rows, lane);
+        // each row's M and l over the warps, before another pair's replace them;
+        // a thread's output quads are STEPS pieces of the [16][DP] tile
+        constexpr int VEC = DP / 4, STEPS = kMaxRows * VEC / (32 * kWarps);
+        float M[STEPS], L[STEPS];
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+          const int r = (i * 32 * kWarps + tid) / VEC;
+          M[i] = -INFINITY;
+          L[i] = 0.f;
+          if (r >= rows) continue;
+#pragma unroll
+          for (int z = 0; z < kWarps; ++z) M[i] = fmaxf(M[i], b->ml[z][r].x);
+#pragma unroll
+          for (int z = 0; z < kWarps; ++z)
+            L[i] += exp2f(b->ml[z][r].x - (M[i] == -INFINITY ? 0.f : M[i])) * b->ml[z][r].y;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b->join[1]);
+        if (!__all_sync(0xffffffffu, wait_or_dead(&b->join[1], joins & 1, &b->dead))) break;
+        ++joins;
+        T* out = static_cast<T*>(p.o);
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+          const int e = i * 32 * kWarps + tid, r = e / VEC, c = (e % VEC) * 4;
+          if (r >= rows) continue;
+          float4 x = *reinterpret_cast<const float4*>(scratch + r * DP + c);
+#pragma unroll
+          for (int z = 1; z < kWarps; ++z) {
+            const float4 y = *reinterpret_cast<const float4*>(scratch + (z * kMaxRows + r) * DP + c);
+            x.x += y.x;
+            x.y += y.y;
+            x.z += y.z;
+            x.w += y.w;
+          }
+          if (t.slot >= 0) {
+            *reinterpret_cast<float4*>(a.o + ((int64_t)t.slot * kMaxRows + r) * DP + c) = x;
+            if (c == 0) a.ml[t.slot * kMaxRows + r] = make_float2(M[i], L[i]);
+          } else if (c < p.D) {
+            const int64_t at =
+                ((int64_t)(t.tok0 + r / p.G) * p.H + (int64_t)t.head * p.G + r % p.G) * p.D + c;
+            const float f = L[i] == 0.f ? 0.f : 1.f / L[i];
+            if constexpr (sizeof(T) == 2)
+              *reinterpret_cast<uint2*>(out + at) = make_uint2(pack2(x.x * f, x.y * f), pack2(x.z * f, x.w * f));
+            else
+              *reinterpret_cast<float4*>(out + at) = make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
+          }
+        }
+      }
+      // generic accesses of the stage before the copies that refill it
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&b->empty[st]);
+    }
+  }
+  __syncthreads();
+  if (tid == 0 && b->dead) attn_flag(p.status, kFlagTimeout);
+}
+
+// The pairs that cross stretches, a CTA per stretch and row: parts
+// 2 c + 1, 2 (c + 1), 2 (c + 2), ..  A thread per channel.
+template <typename T, int DP>
+__global__ void __launch_bounds__(DP) attn_rows_join(const AttnParams p, const RowsArgs a) {
+  pdl_wait();
+  const RowsJoin jn = a.joins[blockIdx.x];
+  const int r = blockIdx.y, c = threadIdx.x;
+  if (jn.parts == 0 || r >= jn.len * p.G) return;
+  const int s0 = 2 * (int)blockIdx.x;
+  auto slot = [&](int k) { return k == 0 ? s0 + 1 : s0 + 2 * k; };
+  float M = -INFINITY;
+  for (int k = 0; k < jn.parts; ++k) M = fmaxf(M, a.ml[slot(k) * kMaxRows + r].x);
+  if (M == -INFINITY) M = 0.f;
+  float l = 0.f, o = 0.f;
+#pragma unroll 4
+  for (int k = 0; k < jn.parts; ++k) {
+    const float2 ml = a.ml[slot(k) * kMaxRows + r];
+    const float f = exp2f(ml.x - M);
+    l = fmaf(f, ml.y, l);
+    o = fmaf(f, a.o[((int64_t)slot(k) * kMaxRows + r) * DP + c], o);
+  }
+  if (c < p.D)
+    st_out(static_cast<T*>(p.o),
+           ((int64_t)(jn.tok0 + r / p.G) * p.H + (int64_t)jn.head * p.G + r % p.G) * p.D + c,
+           l == 0.f ? 0.f : o / l);
+}
+
+// ------------------------------------------------------------------ host
+bool encode(CUtensorMap* m, const AttnParams& p, const void* base, bool q, int box) {
+  const EncodeTiledFn enc = encode_tiled();
+  if (!enc) return false;
+  const bool half = p.dt == KDA_BF16;
+  const cuuint64_t es = half ? 2 : 4, page = (cuuint64_t)1 << p.page_shift;
+  const cuuint64_t heads = q ? p.H : p.Hkv, row = heads * p.D * es;
+  const cuuint64_t dims[4] = {(cuuint64_t)p.D, heads, q ? (cuuint64_t)p.total_tokens : page, (cuuint64_t)p.num_pages};
+  const cuuint64_t strides[3] = {p.D * es, row, row * page};
+  const cuuint32_t bx[4] = {(cuuint32_t)(128 / es), q ? (cuuint32_t)p.G : 1u, (cuuint32_t)box, 1};
+  const cuuint32_t elem[4] = {1, 1, 1, 1};
+  return enc(m, half ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, q ? 3 : 4,
+             const_cast<void*>(base), dims, strides, bx, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int kMaxGrid = 2 * 192;  // two CTAs on each of up to 192 SMs
+
+int padded(const AttnParams& p) {
+  const int low = p.dt == KDA_BF16 ? 64 : 32;
+  return p.D < low ? low : p.D;
+}
+
+template <typename T, int DP, typename Work>
+cudaError_t launch_w(const AttnParams& p, char* w, cudaStream_t stream) {
+  using S = Shape<T, DP>;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  auto kernel = attn_rows<T, DP, Work>;
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kBytes);
+  if (e != cudaSuccess) return e;
+  const int grid = sms * S::CTAS < kMaxGrid ? sms * S::CTAS : kMaxGrid;
+  RowsArgs a{};
+  a.joins = reinterpret_cast<RowsJoin*>(w);
+  a.ml = reinterpret_cast<float2*>(w + align_up(sizeof(RowsJoin) * kMaxGrid, 256));
+  a.o = reinterpret_cast<float*>(a.ml + 2 * kMaxGrid * kMaxRows);
+  const int page = 1 << p.page_shift;
+  a.box = page < S::KT ? page : S::KT;
+  a.q_tokens = (int)p.max_seqlen;
+  CUtensorMap mq, mk, mv;
+  if (!encode(&mq, p, p.q, true, a.q_tokens) || !encode(&mk, p, p.k, false, a.box) ||
+      !encode(&mv, p, p.v, false, a.box))
+    return cudaErrorInvalidValue;
+  kernel<<<grid, kThreads, S::kBytes, stream>>>(p, a, mq, mk, mv);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_maybe_dependent(true, attn_rows_join<T, DP>, dim3((unsigned)grid, (unsigned)(p.max_seqlen * p.G)),
+                                dim3(DP), 0, stream, p, a);
+}
+
+template <int DP>
+cudaError_t launch_f32(const AttnParams& p, char* w, cudaStream_t stream) {
+  const int64_t rows = p.max_seqlen * p.G;
+  if (rows <= 4) return launch_w<float, DP, RowsF32<DP, 4>>(p, w, stream);
+  if (rows <= 8) return launch_w<float, DP, RowsF32<DP, 8>>(p, w, stream);
+  return launch_w<float, DP, RowsF32<DP, 16>>(p, w, stream);
+}
+
+}  // namespace
+
+// At most 16 rows a request, a positive finite scale (the running maximum is
+// taken before the scaling), 16-byte aligned bases for the tensor maps.
+bool attn_rows_fits(const AttnParams& p) {
+  auto al16 = [](const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15) == 0; };
+  return p.block_table && p.max_seqlen * p.G <= kMaxRows && p.scale > 0.f && p.scale <= 3.4e38f && al16(p.q) &&
+         al16(p.k) && al16(p.v) && al16(p.o) && p.num_pages > 0;
+}
+size_t attn_rows_workspace(const AttnParams& p) {
+  return align_up(sizeof(RowsJoin) * kMaxGrid, 256) + 2 * kMaxGrid * kMaxRows * (sizeof(float2) + padded(p) * 4);
+}
+cudaError_t launch_attn_rows(const AttnParams& p, void* ws, cudaStream_t stream) {
+  char* w = static_cast<char*>(ws);
+  if (p.dt == KDA_BF16) {
+    switch (padded(p)) {
+      case 64: return launch_w<__nv_bfloat16, 64, RowsBf16<64>>(p, w, stream);
+      case 128: return launch_w<__nv_bfloat16, 128, RowsBf16<128>>(p, w, stream);
+      default: return launch_w<__nv_bfloat16, 256, RowsBf16<256>>(p, w, stream);
+    }
+  }
+  switch (padded(p)) {
+    case 32: return launch_f32<32>(p, w, stream);
+    case 64: return launch_f32<64>(p, w, stream);
+    case 128: return launch_f32<128>(p, w, stream);
+    default: return launch_f32<256>(p, w, stream);
+  }
+}
+
+}  // namespace kda

@@ -73,33 +73,6 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 512, "barrier block");
 
-// Waits for `parity` of `bar`; false once any wait of the CTA has expired
-// (kWaitLimitNs), so that the roles end together.
-__device__ __forceinline__ bool wait_or_dead(uint64_t* bar, uint32_t parity, uint32_t* dead) {
-  const uint32_t a = smem_u32(bar);
-  uint64_t t0 = 0;
-  for (uint32_t it = 0;; ++it) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}\n"
-        : "=r"(done)
-        : "r"(a), "r"(parity)
-        : "memory");
-    if (done) return true;
-    if (it == 0) {
-      t0 = globaltimer_ns();
-    } else if ((it & 63) == 0) {
-      if (*reinterpret_cast<volatile uint32_t*>(dead)) return false;
-      if (globaltimer_ns() - t0 > kWaitLimitNs) {
-        *reinterpret_cast<volatile uint32_t*>(dead) = 1;
-        return false;
-      }
-    }
-  }
-}
-
 // What every role derives from an item
 struct Geo {
   int rows[2];   // valid rows of each row tile

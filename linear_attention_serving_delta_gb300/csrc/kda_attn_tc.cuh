@@ -1,4 +1,5 @@
-// kda_attn_tc.cuh -- plan records and PTX helpers of the tensor-core attention.
+// kda_attn_tc.cuh -- plan records and PTX helpers of the tensor-core attention
+// and of the attention of a few rows.
 //
 // Shared-memory operands here are 128-byte swizzled: a tile is stored in
 // blocks of 64 channels, each [rows][64] bf16 with rows of 128 bytes whose
@@ -92,6 +93,33 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+// Waits for `parity` of `bar`; false once any wait of the CTA has expired
+// (kWaitLimitNs), so that the roles end together.
+__device__ __forceinline__ bool wait_or_dead(uint64_t* bar, uint32_t parity, uint32_t* dead) {
+  const uint32_t a = smem_u32(bar);
+  uint64_t t0 = 0;
+  for (uint32_t it = 0;; ++it) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(done)
+        : "r"(a), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if (it == 0) {
+      t0 = globaltimer_ns();
+    } else if ((it & 63) == 0) {
+      if (*reinterpret_cast<volatile uint32_t*>(dead)) return false;
+      if (globaltimer_ns() - t0 > kWaitLimitNs) {
+        *reinterpret_cast<volatile uint32_t*>(dead) = 1;
+        return false;
+      }
+    }
+  }
+}
+
 // Tensor-map copies into shared memory, completion counted in bytes on `bar`.
 // The innermost coordinate is a multiple of 64 bf16 here (TMA wants 16 bytes).
 __device__ __forceinline__ void tma_3d(void* dst, const CUtensorMap* m, int x, int y, int z, uint64_t* bar) {
@@ -148,5 +176,9 @@ __device__ __forceinline__ uint32_t finite_only(uint32_t w) {
 bool attn_tc_fits(const AttnParams& p);
 size_t attn_tc_workspace(const AttnParams& p);
 cudaError_t launch_attn_tc(const AttnParams& p, void* ws, cudaStream_t stream);
+
+bool attn_rows_fits(const AttnParams& p);
+size_t attn_rows_workspace(const AttnParams& p);
+cudaError_t launch_attn_rows(const AttnParams& p, void* ws, cudaStream_t stream);
 
 }  // namespace kda
