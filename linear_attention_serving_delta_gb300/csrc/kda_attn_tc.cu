@@ -15,18 +15,17 @@
 //   P = 2^(x - m')       rounded to bf16, into S's columns of TMEM
 //   O = O 2^(m - m') + P V   tcgen05, A from TMEM
 //
-// The reference m of a row follows its maximum only once that has risen by
-// more than 2^kLazyLog2: until then the weights are taken against the old
-// reference (at most 2^kLazyLog2 each, the same relative rounding), and O
-// needs no rescaling pass.  o = O / l at the end, so the choice changes no
-// result beyond rounding.
+// The reference m of a row follows its maximum only once weights taken against
+// the old one would pass 2^kLazyLog2 (the same relative rounding): most tiles
+// need no rescaling pass over O, and of their first half not even the maximum.
+// o = O / l at the end, so the choice changes no result beyond rounding.
 //
 // Warps: 0-3 and 4-7 hold the softmax of the two row tiles (thread = row =
-// TMEM lane), 8 issues the copies, 9 the MMAs (10 and 11 only complete the
-// warpgroup that gives its registers to the softmax).  While one tile's softmax
-// runs, the tensor core works on the other tile.  The MMAs of a CTA are issued by
-// one thread and execute in issue order, so S of the next key tile may be
-// issued right behind the P V that reads P from the same columns.
+// TMEM lane), 9 and 10 issue the MMAs of one row tile each, 8 copies Q and K, 11
+// V.  While one tile's softmax runs, the tensor core works on the other tile.
+// The MMAs of a row tile are issued by one thread and execute in issue order, so S of
+// the next key tile may be issued right behind the P V that reads P from the
+// same columns.
 //
 // Masked places.  Logits past a row's position are replaced by -inf before
 // they are used, so K may hold anything there.  V meets weights of exactly 0,
@@ -46,6 +45,7 @@ constexpr int kTile = 128;       // rows of a row tile, positions of a key tile
 constexpr int kThreads = 384;    // two softmax warpgroups; copies and MMAs
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazyLog2 = 8.f;
+constexpr float kLazySum = 256.f;  // 2^kLazyLog2
 constexpr uint32_t kTmemCols = 512;
 
 template <int DP>
@@ -53,18 +53,21 @@ struct Shape {
   static constexpr int NH = DP / 64;                        // 128-byte column blocks of a tile
   static constexpr uint32_t kBlock = kTile * 128;           // bytes of one block
   static constexpr uint32_t kTileBytes = NH * kBlock;
-  static constexpr int kStages = DP == 128 ? 5 : 8;
+  // K's ring is one deeper: K of a tile is needed right behind P V of the one before
+  static constexpr int kKStages = DP == 128 ? 3 : 4, kVStages = DP == 128 ? 2 : 4;
   static constexpr uint32_t kQ = 0;                         // two row tiles
-  static constexpr uint32_t kRing = 2 * kTileBytes;
-  static constexpr uint32_t kBars = kRing + kStages * kTileBytes;
+  static constexpr uint32_t kK = 2 * kTileBytes;
+  static constexpr uint32_t kV = kK + kKStages * kTileBytes;
+  static constexpr uint32_t kBars = kV + kVStages * kTileBytes;
   static constexpr uint32_t kBytes = kBars + 512;
 };
 
 struct Bars {
-  uint64_t full[8], empty[8];
-  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2];
-  uint64_t fix, drain;
+  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], o_full[2];
+  uint64_t fix, drain[2];
   uint32_t dead;      // a wait expired: every role winds down
+  uint32_t turn;      // held by the MMA warp whose burst is being issued
   uint32_t tmem;
   // the CTA's k-th item with key tiles: non-finite values were taken out of its
   // V tiles (index k % 4; the copies run at most two such items ahead of the
@@ -105,17 +108,111 @@ __device__ __forceinline__ int64_t nth_item(int i) {
 }
 
 // ------------------------------------------------------------------ copies
+// A stage of a ring and its phase
+template <int N>
+struct Ring {
+  uint32_t st = 0, ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++st == N) {
+      st = 0;
+      ph ^= 1;
+    }
+  }
+};
+
+// Key tile x0.. of K or V for the whole warp, a box a lane: c2, c3 are the
+// box's coordinates in the map, n how many boxes hold positions.
+struct Boxes {
+  int c2, c3, n;
+};
+__device__ __forceinline__ Boxes boxes_of(const AttnParams& p, const AttnItem& it, int x0, int shift, int lane) {
+  Boxes r;
+  r.n = min(kTile >> shift, (it.kv_len - x0 + (1 << shift) - 1) >> shift);
+  const int x = x0 + (lane << shift);
+  r.c2 = it.base + x;
+  r.c3 = 0;
+  if (p.block_table) {
+    int page = p.num_pages;
+    if (lane < r.n) {
+      page = p.block_table[(int64_t)it.base * p.max_pages + (x >> p.page_shift)];
+      if (page < 0 || page >= p.num_pages) {
+        attn_flag(p.status, kFlagBadCache);
+        page = p.num_pages;  // outside the map: filled with zeros
+      }
+    }
+    r.c2 = x & ((1 << p.page_shift) - 1);
+    r.c3 = page;
+  }
+  return r;
+}
 template <int DP>
-__device__ void load_role(const AttnParams& p, const TcArgs& a, const CUtensorMap* mq, const CUtensorMap* mk,
-                          const CUtensorMap* mv, char* sm, Bars* b, int64_t total, int tpt) {
+__device__ __forceinline__ void copy_boxes(const CUtensorMap* m, char* dst, const Boxes& bx, int shift, int h, int lane,
+                                           uint64_t* bar) {
+  using S = Shape<DP>;
+  const uint32_t box_bytes = 128u << shift;
+  if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)bx.n * box_bytes * S::NH);
+  __syncwarp();
+  if (lane < bx.n)
+#pragma unroll
+    for (int c = 0; c < S::NH; ++c) tma_4d(dst + c * S::kBlock + lane * box_bytes, m, 64 * c, h, bx.c2, bx.c3, bar);
+}
+
+// Q's row tiles and K
+template <int DP>
+__device__ void load_k_role(const AttnParams& p, const TcArgs& a, const CUtensorMap* mq, const CUtensorMap* mk,
+                            char* sm, Bars* b, int64_t total, int tpt) {
   using S = Shape<DP>;
   const int lane = threadIdx.x & 31;
-  uint32_t n = 0;            // tiles copied so far
-  uint32_t nq[2] = {0, 0};   // q tiles copied so far
-  uint32_t nfix = 0, busy_items = 0;
+  Ring<S::kKStages> ring;
+  uint32_t n = 0, nq[2] = {0, 0};
   bool ok = true;
-  const int box = a.box_tokens, boxes = kTile / box;
-  const uint32_t box_bytes = (uint32_t)box * 128u;
+  for (int i = 0; ok; ++i) {
+    const int64_t w = nth_item(i);
+    if (w >= total) break;
+    const AttnItem it = a.items[w / p.Hkv];
+    const int h = (int)(w % p.Hkv);
+    const Geo g = geometry(it, p.G, tpt);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      if (g.n[t] == 0 || !ok) continue;
+      ok = __all_sync(0xffffffffu, wait_or_dead(&b->q_empty[t], (nq[t] & 1) ^ 1, &b->dead));
+      if (!ok) continue;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&b->q_full[t], (uint32_t)(tpt * p.G) * 128u * S::NH);
+#pragma unroll
+        for (int c = 0; c < S::NH; ++c)
+          tma_3d(sm + S::kQ + t * S::kTileBytes + c * S::kBlock, mq, 64 * c, h * p.G, it.tok0 + t * tpt,
+                 &b->q_full[t]);
+      }
+      ++nq[t];
+    }
+    for (int j = 0; j < g.nmax && ok; ++j) {
+      const Boxes bx = boxes_of(p, it, (g.kt0 + j) * kTile, a.box_shift, lane);
+      ok = __all_sync(0xffffffffu, wait_or_dead(&b->k_empty[ring.st], ring.ph ^ 1, &b->dead));
+      if (!ok) break;
+      copy_boxes<DP>(mk, sm + S::kK + ring.st * S::kTileBytes, bx, a.box_shift, h, lane, &b->k_full[ring.st]);
+      ring.next();
+      ++n;
+    }
+  }
+  // no copy of its own is in flight when a CTA that gave up exits
+  if (!ok) {
+    for (uint32_t k = n > S::kKStages ? n - S::kKStages : 0; k < n; ++k)
+      mbar_wait(&b->k_full[k % S::kKStages], (k / S::kKStages) & 1, kWaitLimitNs);
+    for (int t = 0; t < 2; ++t)
+      if (nq[t] > 0) mbar_wait(&b->q_full[t], (nq[t] - 1) & 1, kWaitLimitNs);
+  }
+}
+
+// V, and what has to be put right in it
+template <int DP>
+__device__ void load_v_role(const AttnParams& p, const TcArgs& a, const CUtensorMap* mv, char* sm, Bars* b,
+                            int64_t total, int tpt) {
+  using S = Shape<DP>;
+  const int lane = threadIdx.x & 31;
+  Ring<S::kVStages> ring;
+  uint32_t n = 0, nfix = 0, busy_items = 0;
+  bool ok = true;
   for (int i = 0; ok; ++i) {
     const int64_t w = nth_item(i);
     if (w >= total) break;
@@ -125,123 +222,126 @@ __device__ void load_role(const AttnParams& p, const TcArgs& a, const CUtensorMa
     if (g.nmax == 0) continue;
     uint32_t* poison = &b->poison[busy_items++ & 3];
     if (lane == 0) *poison = 0;
-    // key tile kt of K or V into the next stage
-    auto load_tile = [&](const CUtensorMap* m, int kt, bool fix) {
-      const uint32_t st = n % S::kStages;
-      char* dst = sm + S::kRing + st * S::kTileBytes;
-      const int x0 = kt * kTile;
-      // this lane's box: its page, read before the wait
-      const int nb = min(boxes, (it.kv_len - x0 + box - 1) / box);
-      int c2 = it.base + x0 + lane * box, c3 = 0;
-      if (p.block_table && lane < nb) {
-        const int x = x0 + lane * box;
-        int page = p.block_table[(int64_t)it.base * p.max_pages + (x >> p.page_shift)];
-        if (page < 0 || page >= p.num_pages) {
-          attn_flag(p.status, kFlagBadCache);
-          page = p.num_pages;  // outside the map: filled with zeros
-        }
-        c2 = x & ((1 << p.page_shift) - 1);
-        c3 = page;
-      }
-      ok = wait_or_dead(&b->empty[st], ((n / S::kStages) & 1) ^ 1, &b->dead);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) return;
-      uint64_t* bar = fix ? &b->fix : &b->full[st];
-      if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)nb * box_bytes * S::NH);
-      __syncwarp();
-      if (lane < nb)
-#pragma unroll
-        for (int c = 0; c < S::NH; ++c) tma_4d(dst + c * S::kBlock + lane * box_bytes, m, 64 * c, h, c2, c3, bar);
+    for (int j = 0; j < g.nmax; ++j) {
+      const int kt = g.kt0 + j, x0 = kt * kTile;
+      const bool fix = kt >= g.fix_from;
+      const Boxes bx = boxes_of(p, it, x0, a.box_shift, lane);
+      char* dst = sm + S::kV + ring.st * S::kTileBytes;
+      ok = __all_sync(0xffffffffu, wait_or_dead(&b->v_empty[ring.st], ring.ph ^ 1, &b->dead));
+      if (!ok) break;
+      copy_boxes<DP>(mv, dst, bx, a.box_shift, h, lane, fix ? &b->fix : &b->v_full[ring.st]);
       if (fix) {
         // in place: rows behind the sequence to zero, non-finite values out
-        ok = wait_or_dead(&b->fix, nfix & 1, &b->dead);
-        ok = __all_sync(0xffffffffu, ok);
+        ok = __all_sync(0xffffffffu, wait_or_dead(&b->fix, nfix & 1, &b->dead));
         ++nfix;
-        if (!ok) return;
-        const int live = min(kTile, it.kv_len - x0);
+        if (!ok) break;
+        const int live = min(kTile, it.kv_len - x0) * 8;  // 16-byte pieces of a block
         bool bad = false;
-        if (it.ntok > 1) {
-#pragma unroll 4
-          for (int v = lane; v < live * 8 * S::NH; v += 32) {
-            uint4* q4 = reinterpret_cast<uint4*>(dst + (v / (live * 8)) * S::kBlock) + v % (live * 8);
-            const uint4 x = *q4;
-            // an exponent of all ones carries into the sign's place
-            const uint32_t t = (((x.x & 0x7f807f80u) + 0x00800080u) | ((x.y & 0x7f807f80u) + 0x00800080u) |
-                                ((x.z & 0x7f807f80u) + 0x00800080u) | ((x.w & 0x7f807f80u) + 0x00800080u)) &
-                               0x80008000u;
-            if (t) {
-              bad = true;
-              *q4 = make_uint4(finite_only(x.x), finite_only(x.y), finite_only(x.z), finite_only(x.w));
+#pragma unroll
+        for (int c = 0; c < S::NH; ++c) {
+          uint4* blk = reinterpret_cast<uint4*>(dst + c * S::kBlock);
+          if (it.ntok > 1) {
+#pragma unroll 8
+            for (int v = lane; v < live; v += 32) {
+              const uint4 x = blk[v];
+              // an exponent of all ones carries into the sign's place
+              const uint32_t t = (((x.x & 0x7f807f80u) + 0x00800080u) | ((x.y & 0x7f807f80u) + 0x00800080u) |
+                                  ((x.z & 0x7f807f80u) + 0x00800080u) | ((x.w & 0x7f807f80u) + 0x00800080u)) &
+                                 0x80008000u;
+              if (t) {
+                bad = true;
+                blk[v] = make_uint4(finite_only(x.x), finite_only(x.y), finite_only(x.z), finite_only(x.w));
+              }
             }
           }
+          for (int v = live + lane; v < kTile * 8; v += 32) blk[v] = make_uint4(0, 0, 0, 0);
         }
-        for (int v = live * 8 + lane; v < kTile * 8; v += 32)
-#pragma unroll
-          for (int c = 0; c < S::NH; ++c)
-            *(reinterpret_cast<uint4*>(dst + c * S::kBlock) + v) = make_uint4(0, 0, 0, 0);
         if (bad) *reinterpret_cast<volatile uint32_t*>(poison) = 1;
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&b->full[st]);
+        if (lane == 0) mbar_arrive(&b->v_full[ring.st]);
       }
+      ring.next();
       ++n;
-    };
-    for (int t = 0; t < 2 && ok; ++t) {
-      if (g.n[t] == 0) continue;
-      ok = wait_or_dead(&b->q_empty[t], (nq[t] & 1) ^ 1, &b->dead);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&b->q_full[t], (uint32_t)(tpt * p.G) * 128u * S::NH);
-#pragma unroll
-        for (int c = 0; c < S::NH; ++c)
-          tma_3d(sm + S::kQ + t * S::kTileBytes + c * S::kBlock, mq, 64 * c, h * p.G, it.tok0 + t * tpt,
-                 &b->q_full[t]);
-      }
-      ++nq[t];
-      __syncwarp();
-    }
-    for (int j = 0; j < g.nmax && ok; ++j) {
-      const int kt = g.kt0 + j;
-      load_tile(mk, kt, false);
-      if (ok) load_tile(mv, kt, kt >= g.fix_from);
     }
   }
-  // no copy of its own is in flight when a CTA that gave up exits
   if (!ok) {
-    for (uint32_t k = n > S::kStages ? n - S::kStages : 0; k < n; ++k)
-      mbar_wait(&b->full[k % S::kStages], (k / S::kStages) & 1, kWaitLimitNs);
-    for (int t = 0; t < 2; ++t)
-      if (nq[t] > 0) mbar_wait(&b->q_full[t], (nq[t] - 1) & 1, kWaitLimitNs);
+    for (uint32_t k = n > S::kVStages ? n - S::kVStages : 0; k < n; ++k)
+      mbar_wait(&b->v_full[k % S::kVStages], (k / S::kVStages) & 1, kWaitLimitNs);
     if (nfix > 0) mbar_wait(&b->fix, (nfix - 1) & 1, kWaitLimitNs);
   }
 }
 
 // ------------------------------------------------------------------ MMAs
+// A warp for each row tile: what one waits for, the other's MMAs cover (a wait
+// behind S's MMAs costs the tensor core 50-100 cycles when one warp issues
+// both tiles' work).  The whole warp walks the items, so that descriptors stay
+// in uniform registers; one lane issues.
 template <int DP>
-__device__ void mma_role(const AttnParams& p, const TcArgs& a, char* sm, Bars* b, int64_t total, int tpt) {
+__device__ void mma_role(const AttnParams& p, const TcArgs& a, char* sm, Bars* b, int64_t total, int tpt, int t) {
   using S = Shape<DP>;
-  const uint32_t tmem = b->tmem;
-  const uint32_t id_qk = idesc_bf16(kTile, kTile), id_pv = idesc_bf16(kTile, DP, 0, 1);
-  const uint32_t q0 = smem_u32(sm + S::kQ), r0 = smem_u32(sm + S::kRing);
-  uint32_t n = 0, nq[2] = {0, 0}, np[2] = {0, 0};
+  const uint32_t tmem = __shfl_sync(0xffffffffu, b->tmem, 0);
+  const uint32_t ts = tmem + t * kTile, to = tmem + 2 * kTile + t * DP;
+  constexpr uint32_t id_qk = idesc_bf16(kTile, kTile), id_pv = idesc_bf16(kTile, DP, 0, 1);
+  const uint64_t qd = sdesc_sw128(smem_u32(sm + S::kQ + t * S::kTileBytes), 16, 1024),
+                 k0 = sdesc_sw128(smem_u32(sm + S::kK), 16, 1024),
+                 v0 = sdesc_sw128(smem_u32(sm + S::kV), S::kBlock, 1024);
+  const bool issue = elect_one();
+  Ring<S::kKStages> kr;
+  Ring<S::kVStages> vr;
+  uint32_t nq = 0, np = 0;
   uint32_t* dead = &b->dead;
-  auto full = [&](uint32_t k) { return wait_or_dead(&b->full[k % S::kStages], (k / S::kStages) & 1, dead); };
-  auto qk = [&](int t, uint32_t k) {
-    const uint32_t kb = r0 + (k % S::kStages) * S::kTileBytes, qb = q0 + t * S::kTileBytes;
-#pragma unroll
-    for (int s = 0; s < DP / 16; ++s) {
-      const uint32_t off = (s / 4) * S::kBlock + (s % 4) * 32;
-      mma_bf16(tmem + t * kTile, sdesc_sw128(qb + off, 16, 1024), sdesc_sw128(kb + off, 16, 1024), id_qk, s > 0);
-    }
-    mma_commit(&b->s_full[t]);
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait_or_dead(bar, parity, dead)) != 0;
   };
-  auto pv = [&](int t, uint32_t k, bool first) {
-    const uint32_t vb = r0 + (k % S::kStages) * S::kTileBytes;
+  // this row tile's share of a stage is done: with its MMAs, or at once
+  auto release = [&](uint64_t* empty, bool used) {
+    if (issue) {
+      if (used) mma_commit(empty);
+      else mbar_arrive(empty);
+    }
+  };
+  auto qk = [&](uint32_t stage) {
+    const uint64_t kd = k0 + (uint64_t)(stage * (S::kTileBytes >> 4));
+    if (issue) {
 #pragma unroll
-    for (int s = 0; s < kTile / 16; ++s)
-      mma_bf16_ts(tmem + 2 * kTile + t * DP, tmem + t * kTile + s * 8, sdesc_sw128(vb + s * 2048, S::kBlock, 1024),
-                  id_pv, !first || s > 0);
+      for (int s = 0; s < DP / 16; ++s) {
+        const uint32_t off = ((s / 4) * S::kBlock + (s % 4) * 32) >> 4;
+        mma_bf16(ts, qd + off, kd + off, id_qk, s > 0);
+      }
+      mma_commit(&b->s_full[t]);
+    }
+  };
+  // P V over half of the key tile
+  auto pv = [&](uint32_t stage, int half, bool first) {
+    const uint64_t vd = v0 + (uint64_t)(stage * (S::kTileBytes >> 4) + half * (4 * 2048 >> 4));
+    if (issue) {
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        mma_bf16_ts(to, ts + half * 32 + s * 8, vd + s * (2048 >> 4), id_pv, !first || s > 0);
+    }
+  };
+  // One row tile's burst (P V, then S of the next key tile) at a time: bursts
+  // that interleave end together, and so do the softmaxes behind them, each
+  // slower for the other (8192 tokens, 32 heads of 128: 368 us, 418 without).
+  // If the holder waits for P's second half and gives up, so does the other.
+  auto take = [&] {
+    bool mine = true;
+    if (issue) {
+      uint64_t t0 = 0;
+      for (uint32_t it = 0; atomicCAS_block(&b->turn, 0u, 1u) != 0u; ++it) {
+        if (it == 0) t0 = globaltimer_ns();
+        else if ((it & 63) == 0 && globaltimer_ns() - t0 > kWaitLimitNs) {
+          *reinterpret_cast<volatile uint32_t*>(dead) = 1;
+          mine = false;
+          break;
+        }
+      }
+    }
+    return __all_sync(0xffffffffu, mine) != 0;
+  };
+  auto give = [&] {
+    if (issue) atomicExch_block(&b->turn, 0u);
   };
   bool ok = true;
   for (int i = 0; ok; ++i) {
@@ -249,52 +349,54 @@ __device__ void mma_role(const AttnParams& p, const TcArgs& a, char* sm, Bars* b
     if (w >= total) break;
     const AttnItem it = a.items[w / p.Hkv];
     const Geo g = geometry(it, p.G, tpt);
+    const int n = t == 0 ? g.n[0] : g.n[1];
     if (g.nmax == 0) continue;
-    if (!(ok = full(n))) break;
-    for (int t = 0; t < 2 && ok; ++t) {
-      if (g.n[t] == 0) continue;
-      if (!(ok = wait_or_dead(&b->q_full[t], nq[t] & 1, dead))) break;
-      ++nq[t];
+    if (!(ok = wait(&b->k_full[kr.st], kr.ph))) break;
+    if (n > 0) {
+      if (!(ok = wait(&b->q_full[t], nq & 1))) break;
+      ++nq;
       fence_after_sync();
-      qk(t, n);
-      if (g.n[t] == 1) mma_commit(&b->q_empty[t]);
+      qk(kr.st);
+      if (n == 1 && issue) mma_commit(&b->q_empty[t]);
     }
-    if (!ok) break;
-    mma_commit(&b->empty[n % S::kStages]);
-    ++n;
-    for (int j = 0; j < g.nmax && ok; ++j) {
-      const uint32_t vk = n, kk = n + 1;
-      bool have_v = false, have_k = false;
-      for (int t = 0; t < 2; ++t) {
-        if (j >= g.n[t]) continue;
-        if (!have_v && !(ok = full(vk))) break;
-        have_v = true;
-        if (!(ok = wait_or_dead(&b->p_full[t], np[t] & 1, dead))) break;
-        ++np[t];
+    release(&b->k_empty[kr.st], n > 0);
+    kr.next();
+    for (int j = 0; j < g.nmax; ++j) {
+      if (!(ok = wait(&b->v_full[vr.st], vr.ph))) break;
+      const bool more = j + 1 < g.nmax;
+      if (more && !(ok = wait(&b->k_full[kr.st], kr.ph))) break;
+      if (j < n) {
+        if (!(ok = wait(&b->p_half[t], np & 1))) break;
+        if (!(ok = take())) break;
         fence_after_sync();
-        pv(t, vk, j == 0);
-        if (j + 1 < g.n[t]) {
-          if (!have_k && !(ok = full(kk))) break;
-          have_k = true;
-          fence_after_sync();
-          qk(t, kk);
-          if (j + 2 == g.n[t]) mma_commit(&b->q_empty[t]);
+        pv(vr.st, 0, j == 0);
+        if (!(ok = wait(&b->p_full[t], np & 1))) break;
+        ++np;
+        fence_after_sync();
+        pv(vr.st, 1, false);
+        if (j + 1 < n) {
+          release(&b->v_empty[vr.st], true);
+          qk(kr.st);
+          give();
+          if (j + 2 == n && issue) mma_commit(&b->q_empty[t]);
         } else {
-          mma_commit(&b->o_full[t]);
+          give();
+          if (issue) mma_commit(&b->o_full[t]);
+          release(&b->v_empty[vr.st], true);
         }
+      } else {
+        release(&b->v_empty[vr.st], false);
       }
-      if (!ok) break;
-      mma_commit(&b->empty[vk % S::kStages]);
-      ++n;
-      if (j + 1 < g.nmax) {
-        mma_commit(&b->empty[kk % S::kStages]);
-        ++n;
+      vr.next();
+      if (more) {
+        release(&b->k_empty[kr.st], j + 1 < n);
+        kr.next();
       }
     }
   }
   // no MMA and no arrival of one is left in flight
-  mma_commit(&b->drain);
-  mbar_wait(&b->drain, 0, kWaitLimitNs);
+  if (issue) mma_commit(&b->drain[t]);
+  mbar_wait(&b->drain[t], 0, kWaitLimitNs);
 }
 
 // ------------------------------------------------------------------ softmax and outputs
@@ -328,11 +430,20 @@ __device__ void softmax_role(const AttnParams& p, const TcArgs& a, Bars* b, int6
   const uint32_t s_col = b->tmem + lanes + t * kTile, o_col = b->tmem + lanes + 2 * kTile + t * DP;
   const float sc = p.scale * kLog2e;
   uint32_t ns = 0, no = 0, busy_items = 0;
+  AttnItem ahead{};  // the next item, read during the one before
+  int h_ahead = 0;
+  auto fetch = [&](int64_t w) {
+    if (w < total) {
+      ahead = a.items[w / p.Hkv];
+      h_ahead = (int)(w % p.Hkv);
+    }
+  };
+  fetch(nth_item(0));
   for (int i = 0;; ++i) {
-    const int64_t w = nth_item(i);
-    if (w >= total) return;
-    const AttnItem it = a.items[w / p.Hkv];
-    const int h = (int)(w % p.Hkv);
+    if (nth_item(i) >= total) return;
+    const AttnItem it = ahead;
+    const int h = h_ahead;
+    fetch(nth_item(i + 1));
     const Geo g = geometry(it, p.G, tpt);
     const int rows = g.rows[t], n = g.n[t];
     const uint32_t* poisoned = &b->poison[busy_items & 3];
@@ -358,49 +469,72 @@ __device__ void softmax_role(const AttnParams& p, const TcArgs& a, Bars* b, int6
 #pragma unroll
           for (int c = 0; c < kTile; ++c) s[c] = c <= last ? s[c] : -INFINITY;
         }
-        float mx[4] = {s[0], s[1], s[2], s[3]};
+        // The first half's weights against the old reference, beside the
+        // maximum of the second half.  If their sum, or that maximum, has
+        // risen too far for some row of the warp, the reference moves and they
+        // are taken again (the first tile, and seldom after).
+        uint32_t pk[32];
+        float2 sum[2];
+        sum[0] = sum[1] = make_float2(0.f, 0.f);
+        auto weight = [&](const float* y, int u, float2 sc2, float2 ref2) {
+          float2 e = fma2(make_float2(y[2 * u], y[2 * u + 1]), sc2, ref2);
+          e.x = exp2_fast(e.x);
+          e.y = exp2_fast(e.y);
+          sum[u & 1] = add2(sum[u & 1], e);
+          pk[u] = pack2(e.x, e.y);
+        };
+        const float2 sc2 = make_float2(sc, sc);
+        float2 ref2 = make_float2(-m, -m);
+        if (m == -INFINITY) ref2 = make_float2(0.f, 0.f);
+        float mx[4] = {s[64], s[65], s[66], s[67]};
 #pragma unroll
-        for (int c = 4; c < kTile; c += 8) {
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            mx[u] = c + u + 4 < kTile ? fmaxf(mx[u], fmaxf(s[c + u], s[c + u + 4])) : fmaxf(mx[u], s[c + u]);
+        for (int u = 0; u < 32; ++u) {
+          weight(s, u, sc2, ref2);
+          mx[u & 3] = fmaxf(mx[u & 3], fmaxf(s[64 + 2 * u], s[65 + 2 * u]));
         }
-        const float x = sc * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        // the reference moves with the first finite maximum, then only past the threshold
-        const bool move = x > m + kLazyLog2 || (m == -INFINITY && x > m);
-        const bool scale_o = move && m != -INFINITY;
-        if (__any_sync(0xffffffffu, scale_o)) {
-          const float f = scale_o ? exp2_fast(m - x) : 1.f;
-          l *= f;
+        const float x2 = sc * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        const float s1 = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        // (a sum that is no number, or an infinite one, asks for the maximum too)
+        const bool far = !(s1 <= kLazySum) || x2 > m + kLazyLog2 || m == -INFINITY;
+        if (__any_sync(0xffffffffu, far)) {
 #pragma unroll
-          for (int c = 0; c < DP; c += 32) {
-            float o[32];
-            tmem_ld32(o_col + c, o);
-            tmem_ld_wait();
+          for (int u = 0; u < 32; ++u) mx[u & 3] = fmaxf(mx[u & 3], fmaxf(s[2 * u], s[2 * u + 1]));
+          const float x = sc * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          const bool move = x > m;
+          const bool scale_o = move && m != -INFINITY;
+          if (__any_sync(0xffffffffu, scale_o)) {
+            const float f = scale_o ? exp2_fast(m - x) : 1.f;
+            l *= f;
+#pragma unroll 1
+            for (int c = 0; c < DP; c += 32) {
+              float o[32];
+              tmem_ld32(o_col + c, o);
+              tmem_ld_wait();
 #pragma unroll
-            for (int u = 0; u < 32; ++u) o[u] *= f;
-            tmem_st32(o_col + c, reinterpret_cast<const uint32_t*>(o));
+              for (int u = 0; u < 32; ++u) o[u] *= f;
+              tmem_st32(o_col + c, reinterpret_cast<const uint32_t*>(o));
+            }
           }
-        }
-        if (move) m = x;
-        const float ref = m == -INFINITY ? 0.f : m;
-        const float2 sc2 = make_float2(sc, sc), ref2 = make_float2(-ref, -ref);
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-        for (int c = 0; c < kTile; c += 64) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int u = 0; u < 32; ++u) {
-            float2 e = fma2(make_float2(s[c + 2 * u], s[c + 2 * u + 1]), sc2, ref2);
-            e.x = exp2_fast(e.x);
-            e.y = exp2_fast(e.y);
-            sum[u & 1] = add2(sum[u & 1], e);
-            pk[u] = pack2(e.x, e.y);
+          if (move) {
+            m = x;
+            ref2 = make_float2(-m, -m);
           }
-          tmem_st32(s_col + c / 2, pk);
+          sum[0] = sum[1] = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int u = 0; u < 32; ++u) weight(s, u, sc2, ref2);
         }
+        tmem_st32(s_col, pk);
+        tmem_st_wait();
+        fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b->p_half[t]);
+#pragma unroll
+        for (int u = 0; u < 32; ++u) weight(s + 64, u, sc2, ref2);
+        tmem_st32(s_col + 32, pk);
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         tmem_st_wait();
+      } else {
+        if (lane == 0) mbar_arrive(&b->p_half[t]);
       }
       fence_before_sync();
       __syncwarp();
@@ -452,8 +586,8 @@ __device__ void softmax_role(const AttnParams& p, const TcArgs& a, Bars* b, int6
 #pragma unroll
           for (int u = 0; u < 16; ++u) pk[u] = pack2(x[2 * u], x[2 * u + 1]);
 #pragma unroll
-          for (int u = 0; u < 16; u += 4)
-            if (c + 2 * u < p.D) *reinterpret_cast<uint4*>(o + c + 2 * u) = make_uint4(pk[u], pk[u + 1], pk[u + 2], pk[u + 3]);
+          for (int u = 0; u < 16; u += 8)
+            if (c + 2 * u < p.D) st_32b(o + c + 2 * u, pk + u, a.o_wide);
         } else {
           float* part = a.part_o + prow * DP + c;
 #pragma unroll
@@ -477,20 +611,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   Bars* b = reinterpret_cast<Bars*>(sm + S::kBars);
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < 8; ++s) {
-      mbar_init(&b->full[s], 1);
-      mbar_init(&b->empty[s], 1);
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&b->k_full[s], 1);
+      mbar_init(&b->k_empty[s], 2);
+      mbar_init(&b->v_full[s], 1);
+      mbar_init(&b->v_empty[s], 2);
     }
     for (int t = 0; t < 2; ++t) {
+      mbar_init(&b->drain[t], 1);
       mbar_init(&b->q_full[t], 1);
       mbar_init(&b->q_empty[t], 1);
       mbar_init(&b->s_full[t], 1);
+      mbar_init(&b->p_half[t], 4);
       mbar_init(&b->p_full[t], 4);
       mbar_init(&b->o_full[t], 1);
     }
     mbar_init(&b->fix, 1);
-    mbar_init(&b->drain, 1);
     b->dead = 0;
+    b->turn = 0;
     mbar_init_fence();
   }
   if (warp == 9) tmem_alloc(&b->tmem, kTmemCols);
@@ -507,8 +645,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     softmax_role<DP>(p, a, b, total, tpt);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    if (warp == 8) load_role<DP>(p, a, &mq, &mk, &mv, sm, b, total, tpt);
-    else if (warp == 9 && (threadIdx.x & 31) == 0) mma_role<DP>(p, a, sm, b, total, tpt);
+    if (warp == 8) load_k_role<DP>(p, a, &mq, &mk, sm, b, total, tpt);
+    else if (warp == 11) load_v_role<DP>(p, a, &mv, sm, b, total, tpt);
+    else mma_role<DP>(p, a, sm, b, total, tpt, warp - 9);
   }
   __syncwarp();
   fence_before_sync();
@@ -781,13 +920,14 @@ TcLayout layout(const AttnParams& p) {
 template <int DP>
 cudaError_t launch_dp(const AttnParams& p, const TcLayout& L, char* w, cudaStream_t stream) {
   using S = Shape<DP>;
-  const int tpt = kTile / p.G, page = p.block_table ? 1 << p.page_shift : kTile;
+  const int tpt = kTile / p.G;
   TcArgs a{};
   a.head = reinterpret_cast<AttnHead*>(w + L.head);
   a.seq_begin = reinterpret_cast<int64_t*>(w + L.seq_begin);
   a.items = reinterpret_cast<AttnItem*>(w + L.items);
   a.max_items = L.max_items;
-  a.box_tokens = page < kTile ? page : kTile;
+  a.box_shift = p.block_table && p.page_shift < 7 ? p.page_shift : 7;
+  a.o_wide = (reinterpret_cast<uintptr_t>(p.o) & 31) == 0;
   if (L.split) {
     a.split_sms = kSplitSms;
     a.joins = reinterpret_cast<AttnJoin*>(w + L.joins);
@@ -795,7 +935,7 @@ cudaError_t launch_dp(const AttnParams& p, const TcLayout& L, char* w, cudaStrea
     a.part_o = reinterpret_cast<float*>(w + L.o);
   }
   CUtensorMap mq, mk, mv;
-  if (!encode_q(&mq, p, tpt) || !encode_kv(&mk, p, p.k, a.box_tokens) || !encode_kv(&mv, p, p.v, a.box_tokens))
+  if (!encode_q(&mq, p, tpt) || !encode_kv(&mk, p, p.k, 1 << a.box_shift) || !encode_kv(&mv, p, p.v, 1 << a.box_shift))
     return cudaErrorInvalidValue;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);

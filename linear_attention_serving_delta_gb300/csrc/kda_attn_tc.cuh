@@ -37,7 +37,8 @@ struct TcArgs {
   int64_t* seq_begin;   // [N] first tile of each sequence
   AttnItem* items;
   int64_t max_items;    // tiles the workspace has room for
-  int32_t box_tokens;   // positions per copy
+  int32_t box_shift;    // log2 of the positions per copy
+  int32_t o_wide;       // o is 32-byte aligned
   int32_t split_sms;    // > 0: items may be cut into pieces
   AttnJoin* joins;
   float2* part_ml;      // [pieces][Hkv][256] (m, l)
@@ -89,28 +90,34 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
       : "memory");
 }
 
+// true in one lane of the (converged) warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(r));
+  return r != 0;
+}
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 // Waits for `parity` of `bar`; false once any wait of the CTA has expired
 // (kWaitLimitNs), so that the roles end together.
-__device__ __forceinline__ bool wait_or_dead(uint64_t* bar, uint32_t parity, uint32_t* dead) {
-  const uint32_t a = smem_u32(bar);
-  uint64_t t0 = 0;
-  for (uint32_t it = 0;; ++it) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}\n"
-        : "=r"(done)
-        : "r"(a), "r"(parity)
-        : "memory");
-    if (done) return true;
-    if (it == 0) {
-      t0 = globaltimer_ns();
-    } else if ((it & 63) == 0) {
+__device__ __forceinline__ bool mbar_done(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+__device__ __forceinline__ bool wait_or_dead_slow(uint64_t* bar, uint32_t parity, uint32_t* dead) {
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_done(bar, parity)) return true;
+    if ((it & 63) == 0) {
       if (*reinterpret_cast<volatile uint32_t*>(dead)) return false;
       if (globaltimer_ns() - t0 > kWaitLimitNs) {
         *reinterpret_cast<volatile uint32_t*>(dead) = 1;
@@ -118,6 +125,11 @@ __device__ __forceinline__ bool wait_or_dead(uint64_t* bar, uint32_t parity, uin
       }
     }
   }
+}
+__device__ __forceinline__ bool wait_or_dead(uint64_t* bar, uint32_t parity, uint32_t* dead) {
+  if (mbar_done(bar, parity)) return true;
+  if (mbar_done(bar, parity)) return true;  // (each suspends for a while)
+  return wait_or_dead_slow(bar, parity, dead);
 }
 
 // Tensor-map copies into shared memory, completion counted in bytes on `bar`.
@@ -163,6 +175,17 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+// 32 bytes to global memory, in one store (a whole sector) where p is 32-byte aligned
+__device__ __forceinline__ void st_32b(void* p, const uint32_t* v, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
 }
 // two bf16, each zeroed if it is infinite or NaN
 __device__ __forceinline__ uint32_t finite_only(uint32_t w) {
