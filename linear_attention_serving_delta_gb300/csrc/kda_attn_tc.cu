@@ -44,6 +44,7 @@ using namespace tc;
 constexpr int kTile = 128;       // rows of a row tile, positions of a key tile
 constexpr int kThreads = 384;    // two softmax warpgroups; copies and MMAs
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kFirst = 64;       // positions of P handed over first
 constexpr float kLazyLog2 = 8.f;
 constexpr float kLazySum = 256.f;  // 2^kLazyLog2
 constexpr uint32_t kTmemCols = 512;
@@ -53,8 +54,8 @@ struct Shape {
   static constexpr int NH = DP / 64;                        // 128-byte column blocks of a tile
   static constexpr uint32_t kBlock = kTile * 128;           // bytes of one block
   static constexpr uint32_t kTileBytes = NH * kBlock;
-  // K's ring is one deeper: K of a tile is needed right behind P V of the one before
-  static constexpr int kKStages = DP == 128 ? 3 : 4, kVStages = DP == 128 ? 2 : 4;
+  // V's ring is one deeper: some of its tiles are put right in place before use
+  static constexpr int kKStages = DP == 128 ? 2 : 4, kVStages = DP == 128 ? 3 : 4;
   static constexpr uint32_t kQ = 0;                         // two row tiles
   static constexpr uint32_t kK = 2 * kTileBytes;
   static constexpr uint32_t kV = kK + kKStages * kTileBytes;
@@ -235,14 +236,15 @@ __device__ void load_v_role(const AttnParams& p, const TcArgs& a, const CUtensor
         ok = __all_sync(0xffffffffu, wait_or_dead(&b->fix, nfix & 1, &b->dead));
         ++nfix;
         if (!ok) break;
-        const int live = min(kTile, it.kv_len - x0) * 8;  // 16-byte pieces of a block
+        // in 16-byte pieces of a block: the rows some row may not attend, the end of the sequence
+        const int from = max(0, it.pos0 + 1 - x0) * 8, live = min(kTile, it.kv_len - x0) * 8;
         bool bad = false;
 #pragma unroll
         for (int c = 0; c < S::NH; ++c) {
           uint4* blk = reinterpret_cast<uint4*>(dst + c * S::kBlock);
           if (it.ntok > 1) {
 #pragma unroll 8
-            for (int v = lane; v < live; v += 32) {
+            for (int v = from + lane; v < live; v += 32) {
               const uint4 x = blk[v];
               // an exponent of all ones carries into the sign's place
               const uint32_t t = (((x.x & 0x7f807f80u) + 0x00800080u) | ((x.y & 0x7f807f80u) + 0x00800080u) |
@@ -301,7 +303,10 @@ __device__ void mma_role(const AttnParams& p, const TcArgs& a, char* sm, Bars* b
       else mbar_arrive(empty);
     }
   };
-  auto qk = [&](uint32_t stage) {
+  auto give = [&] {
+    if (issue) atomicExch_block(&b->turn, 0u);
+  };
+  auto qk = [&](uint32_t stage, bool held) {
     const uint64_t kd = k0 + (uint64_t)(stage * (S::kTileBytes >> 4));
     if (issue) {
 #pragma unroll
@@ -309,16 +314,22 @@ __device__ void mma_role(const AttnParams& p, const TcArgs& a, char* sm, Bars* b
         const uint32_t off = ((s / 4) * S::kBlock + (s % 4) * 32) >> 4;
         mma_bf16(ts, qd + off, kd + off, id_qk, s > 0);
       }
+      if (held) give();
       mma_commit(&b->s_full[t]);
     }
   };
-  // P V over half of the key tile
-  auto pv = [&](uint32_t stage, int half, bool first) {
-    const uint64_t vd = v0 + (uint64_t)(stage * (S::kTileBytes >> 4) + half * (4 * 2048 >> 4));
+  // P V over the first kFirst positions of the key tile, or the others
+  auto pv = [&](uint32_t stage, bool rest, bool first) {
+    const uint64_t vd = v0 + (uint64_t)(stage * (S::kTileBytes >> 4));
     if (issue) {
+      if (!rest) {
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
-        mma_bf16_ts(to, ts + half * 32 + s * 8, vd + s * (2048 >> 4), id_pv, !first || s > 0);
+        for (int s = 0; s < kFirst / 16; ++s)
+          mma_bf16_ts(to, ts + s * 8, vd + s * (2048 >> 4), id_pv, !first || s > 0);
+      } else {
+#pragma unroll
+        for (int s = kFirst / 16; s < kTile / 16; ++s) mma_bf16_ts(to, ts + s * 8, vd + s * (2048 >> 4), id_pv, 1);
+      }
     }
   };
   // One row tile's burst (P V, then S of the next key tile) at a time: bursts
@@ -340,9 +351,6 @@ __device__ void mma_role(const AttnParams& p, const TcArgs& a, char* sm, Bars* b
     }
     return __all_sync(0xffffffffu, mine) != 0;
   };
-  auto give = [&] {
-    if (issue) atomicExch_block(&b->turn, 0u);
-  };
   bool ok = true;
   for (int i = 0; ok; ++i) {
     const int64_t w = nth_item(i);
@@ -356,7 +364,7 @@ __device__ void mma_role(const AttnParams& p, const TcArgs& a, char* sm, Bars* b
       if (!(ok = wait(&b->q_full[t], nq & 1))) break;
       ++nq;
       fence_after_sync();
-      qk(kr.st);
+      qk(kr.st, false);
       if (n == 1 && issue) mma_commit(&b->q_empty[t]);
     }
     release(&b->k_empty[kr.st], n > 0);
@@ -369,15 +377,14 @@ __device__ void mma_role(const AttnParams& p, const TcArgs& a, char* sm, Bars* b
         if (!(ok = wait(&b->p_half[t], np & 1))) break;
         if (!(ok = take())) break;
         fence_after_sync();
-        pv(vr.st, 0, j == 0);
+        pv(vr.st, false, j == 0);
         if (!(ok = wait(&b->p_full[t], np & 1))) break;
         ++np;
         fence_after_sync();
-        pv(vr.st, 1, false);
+        pv(vr.st, true, false);
         if (j + 1 < n) {
           release(&b->v_empty[vr.st], true);
-          qk(kr.st);
-          give();
+          qk(kr.st, true);
           if (j + 2 == n && issue) mma_commit(&b->q_empty[t]);
         } else {
           give();
@@ -473,7 +480,7 @@ __device__ void softmax_role(const AttnParams& p, const TcArgs& a, Bars* b, int6
         // maximum of the second half.  If their sum, or that maximum, has
         // risen too far for some row of the warp, the reference moves and they
         // are taken again (the first tile, and seldom after).
-        uint32_t pk[32];
+        uint32_t pk[kFirst / 2];
         float2 sum[2];
         sum[0] = sum[1] = make_float2(0.f, 0.f);
         auto weight = [&](const float* y, int u, float2 sc2, float2 ref2) {
@@ -486,11 +493,11 @@ __device__ void softmax_role(const AttnParams& p, const TcArgs& a, Bars* b, int6
         const float2 sc2 = make_float2(sc, sc);
         float2 ref2 = make_float2(-m, -m);
         if (m == -INFINITY) ref2 = make_float2(0.f, 0.f);
-        float mx[4] = {s[64], s[65], s[66], s[67]};
+        float mx[4] = {s[kFirst], s[kFirst + 1], s[kFirst + 2], s[kFirst + 3]};
 #pragma unroll
-        for (int u = 0; u < 32; ++u) {
+        for (int u = 0; u < kFirst / 2; ++u) {
           weight(s, u, sc2, ref2);
-          mx[u & 3] = fmaxf(mx[u & 3], fmaxf(s[64 + 2 * u], s[65 + 2 * u]));
+          if (kFirst + 2 * u < kTile) mx[u & 3] = fmaxf(mx[u & 3], fmaxf(s[kFirst + 2 * u], s[kFirst + 2 * u + 1]));
         }
         const float x2 = sc * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         const float s1 = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
@@ -498,7 +505,7 @@ __device__ void softmax_role(const AttnParams& p, const TcArgs& a, Bars* b, int6
         const bool far = !(s1 <= kLazySum) || x2 > m + kLazyLog2 || m == -INFINITY;
         if (__any_sync(0xffffffffu, far)) {
 #pragma unroll
-          for (int u = 0; u < 32; ++u) mx[u & 3] = fmaxf(mx[u & 3], fmaxf(s[2 * u], s[2 * u + 1]));
+          for (int u = 0; u < kFirst / 2; ++u) mx[u & 3] = fmaxf(mx[u & 3], fmaxf(s[2 * u], s[2 * u + 1]));
           const float x = sc * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
           const bool move = x > m;
           const bool scale_o = move && m != -INFINITY;
@@ -521,16 +528,18 @@ __device__ void softmax_role(const AttnParams& p, const TcArgs& a, Bars* b, int6
           }
           sum[0] = sum[1] = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int u = 0; u < 32; ++u) weight(s, u, sc2, ref2);
+          for (int u = 0; u < kFirst / 2; ++u) weight(s, u, sc2, ref2);
         }
         tmem_st32(s_col, pk);
+        if constexpr (kFirst == 96) tmem_st16(s_col + 32, reinterpret_cast<const float*>(pk + 32));
         tmem_st_wait();
         fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&b->p_half[t]);
 #pragma unroll
-        for (int u = 0; u < 32; ++u) weight(s + 64, u, sc2, ref2);
-        tmem_st32(s_col + 32, pk);
+        for (int u = 0; u < (kTile - kFirst) / 2; ++u) weight(s + kFirst, u, sc2, ref2);
+        if constexpr (kFirst == 96) tmem_st16(s_col + 48, reinterpret_cast<const float*>(pk));
+        else tmem_st32(s_col + 32, pk);
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         tmem_st_wait();
       } else {
@@ -569,7 +578,7 @@ __device__ void softmax_role(const AttnParams& p, const TcArgs& a, Bars* b, int6
 #pragma unroll
         for (int u = 0; u < 32; ++u) x[u] *= f;
         if (poison) {
-          const int from = max(g.kt0, g.fix_from) * kTile, to = min(limit, min(it.kv_len, it.kt1 * kTile) - 1);
+          const int from = max(g.kt0 * kTile, it.pos0 + 1), to = min(limit, min(it.kv_len, it.kt1 * kTile) - 1);
           const int64_t stride = (int64_t)p.Hkv * p.D;
           const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v) + (int64_t)h * p.D + c +
                                    (p.block_table ? 0 : it.base * stride);
@@ -753,7 +762,8 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnParam
     }
     atomicAdd(&cost_sum, c);
     __syncthreads();
-    const int64_t share = ((int64_t)cost_sum * p.Hkv + a.split_sms - 1) / a.split_sms;
+    const int64_t parts = (int64_t)kPiecesPerSm * a.split_sms;
+    const int64_t share = ((int64_t)cost_sum * p.Hkv + parts - 1) / parts;
     piece = (int)max((int64_t)kMinPiece, share);
   }
   // pieces of tile x: how many, and each one's key tiles
@@ -895,9 +905,9 @@ TcLayout layout(const AttnParams& p) {
   const int tpi = 2 * (kTile / p.G);
   L.max_items = (p.total_tokens + tpi - 1) / tpi + p.num_seqs;
   // pieces only where the whole batch cannot fill the GPU: at most two per SM
-  // are whole items, and the cuts add one per SM
+  // are whole items, and the cuts add kPiecesPerSm
   L.split = p.block_table && (p.total_tokens + tpi - 1) / tpi * p.Hkv < 2 * kSplitSms;
-  L.max_pieces = L.split ? 3 * (int64_t)kSplitSms / p.Hkv + 1 : 0;
+  L.max_pieces = L.split ? (2 + kPiecesPerSm) * (int64_t)kSplitSms / p.Hkv + 1 : 0;
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t at = off;

@@ -15,8 +15,10 @@
 
 namespace kda {
 
-// The SMs the cut into pieces is sized for, and the fewest key tiles a piece has
+// The SMs the cut into pieces is sized for, the pieces an SM gets (their costs
+// even out over several), and the fewest key tiles a piece has
 constexpr int kSplitSms = 152;
+constexpr int kPiecesPerSm = 1;
 constexpr int kMinPiece = 4;
 
 // One unit of work (for each key head): ntok tokens from packed token tok0 on,
