@@ -1,22 +1,27 @@
-// kda_attn_rows.cu -- attention of a few rows per request over the paged
-// cache: single tokens, or a few of them, of at most 16 rows with their group
-// of query heads (row = token * G + head).
+// kda_attn_rows.cu -- attention by blocks of at most 16 rows: single tokens (or
+// a few) over the paged cache in both types, and everything in fp32 or with
+// heads of 256 channels.
 //
-// Such a step reads every cached key and value once and does little with
-// them, so the kernel is a stream: it is bound by HBM.  The key tiles of all
-// (request, key head) pairs form one line of work, pair after pair, and every
-// CTA of a grid that fills the GPU takes an equal stretch of it, whatever the
-// requests' lengths.  A pair inside one stretch is finished there; one that
-// crosses stretches leaves its parts (unnormalised output, running maximum m
-// and sum l, fp32) for attn_rows_join, which adds them in line order:
-//   M = max m_k,  o = sum 2^(m_k - M) O_k / sum 2^(m_k - M) l_k.
+// A block's rows are those of one key head: row = token * gb + head, with gb
+// = min(G, 16) of its G query heads and as many tokens (a power of two) as fit
+// 16 rows.  For single tokens that reads every cached key and value once and
+// does little with them, so the kernel is a stream, bound by HBM; fp32 blocks
+// of a prompt are bound by the FMA units instead.
+//
+// The key tiles of all blocks form one line of work, sequence after sequence,
+// head after head, and every CTA of a grid that fills the GPU takes an equal
+// stretch of it, whatever the lengths.  A block inside one stretch is finished
+// there; one that crosses stretches leaves its parts (unnormalised output,
+// running maximum m and sum l, fp32) for attn_rows_join, which adds them in
+// line order:  M = max m_k,  o = sum 2^(m_k - M) O_k / sum 2^(m_k - M) l_k.
 //
 // In a CTA one warp copies tiles into a ring (tensor-map copies, a box per
 // page, 128-byte swizzle) and four warps each take a quarter of a tile's keys
-// with softmax statistics of their own, joined at the end of a pair.  bf16:
-// 16 keys a warp on mma.sync (a 128-row tcgen05 tile would be 7/8 padding
-// here, and the tensor cores wait for memory either way); the weights are
-// rounded to bf16, as P V's operand.  fp32: 8 keys a warp on FMAs.
+// with softmax statistics of their own, joined at the end of a block.  bf16:
+// 16 keys a warp on mma.sync (a 128-row tcgen05 tile would be 7/8 padding for
+// single tokens, and the tensor cores wait for memory either way); the
+// weights are rounded to bf16, as P V's operand.  fp32: the same with every
+// operand in three bf16 parts; 8 keys a warp on FMAs for heads of 256.
 #include "kda_attn_tc.cuh"
 
 namespace kda {
@@ -33,7 +38,7 @@ constexpr float kLazyLog2 = 8.f;  // how far the maximum may rise before O is re
 
 template <typename T, int DP>
 struct Shape {
-  static constexpr int KT = sizeof(T) == 2 ? 64 : 32;      // keys of a tile
+  static constexpr int KT = sizeof(T) == 2 || DP <= 128 ? 64 : 32;  // keys of a tile
   static constexpr int NB = DP * (int)sizeof(T) / 128;     // 128-byte blocks of a row
   static constexpr uint32_t kBlock = KT * 128;
   static constexpr uint32_t kKV = 2 * NB * kBlock;         // K, then V; also the joining warps' scratch
@@ -42,22 +47,24 @@ struct Shape {
   static constexpr int CTAS = kKV <= 32768 ? 2 : 1;
   static constexpr int kStages = kKV <= 8192 ? 8 : kKV <= 16384 ? 5 : 3;
   static constexpr uint32_t kQ = kStages * kStage;         // fp32: the pair's q rows, plain
-  static constexpr uint32_t kTail = kQ + (sizeof(T) == 4 ? kMaxRows * DP * 4 : 0);
+  static constexpr uint32_t kQPlane = (DP + 63) / 64 * kMaxRows * 128;  // fp32: a bf16 part of q (split3)
+  static constexpr uint32_t kTail = kQ + (sizeof(T) == 2 ? 0 : DP <= 128 ? 3 * kQPlane : kMaxRows * DP * 4);
   static constexpr uint32_t kBytes = kTail + 2048 + 1024;  // barriers; slack to align the base
 };
 static_assert(Shape<__nv_bfloat16, 128>::kKV >= kWarps * kMaxRows * 128 * 4, "the warps' outputs fit a stage");
 static_assert(Shape<float, 128>::kKV >= kWarps * kMaxRows * 128 * 4, "the warps' outputs fit a stage");
 static_assert(2 * (Shape<__nv_bfloat16, 128>::kBytes + 1024) <= 233472, "two CTAs per SM");
-static_assert(2 * (Shape<float, 128>::kBytes + 1024) <= 233472, "two CTAs per SM");
-static_assert(Shape<float, 256>::kBytes <= 232448 && Shape<__nv_bfloat16, 256>::kBytes <= 232448, "one CTA");
+static_assert(2 * (Shape<float, 64>::kBytes + 1024) <= 233472, "two CTAs per SM");
+static_assert(Shape<float, 256>::kBytes <= 232448 && Shape<float, 128>::kBytes <= 232448 && Shape<__nv_bfloat16, 256>::kBytes <= 232448, "one CTA");
 
 // A tile in the ring, for its consumers
 struct Tile {
-  int32_t tok0, len, kv_len, head;
-  int32_t x0;     // position of its first key
-  int32_t first;  // of the pair in this stretch
-  int32_t last;
-  int32_t slot;   // at the last tile: where the part goes, or -1 (the pair is whole)
+  int32_t tok0, head0;  // packed token and query head of the block's first row
+  int32_t rows, gb;     // rows of the block, query heads of a token in it
+  int32_t pos0, end;    // position of its first token; keys its last one attends
+  int32_t x0;           // position of the tile's first key
+  int32_t first, last;  // of the block in this stretch
+  int32_t slot;         // at the last tile: where the part goes, or -1 (the block is whole)
 };
 
 struct Tail {
@@ -74,22 +81,59 @@ static_assert(sizeof(Tail) <= 2048, "tail block");
 
 struct RowsJoin {
   int32_t parts;  // 0: nothing to join
-  int32_t tok0, len, head;
+  int32_t tok0, head0, rows, gb;
 };
 struct RowsArgs {
-  RowsJoin* joins;  // [grid]
-  float2* ml;       // [2 grid][16]
-  float* o;         // [2 grid][16][DP]
-  int32_t box;      // positions per copy
-  int32_t q_tokens; // tokens of q per copy
+  RowsJoin* joins;   // [grid]
+  float2* ml;        // [2 grid][16]
+  float* o;          // [2 grid][16][DP]
+  int32_t box_shift; // log2 of the positions per copy
+  int32_t q_shift;   // log2 of a block's tokens
+  int32_t parts;     // blocks of a token's G heads
 };
 
-template <typename T, int DP>
-__device__ __forceinline__ int tiles_of(const AttnSeq& q) {
-  constexpr int KT = Shape<T, DP>::KT;
-  if (q.len == 0) return 0;
-  return q.kv_len <= KT ? 1 : (int)((q.kv_len + KT - 1) / KT);  // a pair without keys still writes its zeros
-}
+// The blocks of a sequence for one head (part): n of them, block i with
+// tiles(i) = max(1, ceil((pos + (i + 1) q) / KT)) key tiles, q = 2^q_shift
+// tokens each, pos the position of the first token.  (The last block may count
+// a tile without keys; a block without keys still writes its zeros.)  With R =
+// KT / q and d = floor((pos + KT - 1) / q) + 1 that is max(1, floor((d + i) / R)),
+// and sum_{j < n} floor(j / R) = R t (t - 1) / 2 + t (n - t R) for t = floor(n / R).
+template <int KT>
+struct Blocks {
+  int64_t n, d;
+  int rs;  // log2 R
+  __device__ __forceinline__ Blocks(const AttnSeq& s, int q_shift) {
+    n = ((int64_t)s.len + (1 << q_shift) - 1) >> q_shift;
+    d = ((s.kv_len - s.len + KT - 1) >> q_shift) + 1;
+    rs = 31 - __clz(KT) - q_shift;
+  }
+  __device__ __forceinline__ int tiles(int64_t i) const { return (int)max((int64_t)1, (d + i) >> rs); }
+  __device__ __forceinline__ int64_t sum(int64_t m) const {
+    const int64_t t = m >> rs;
+    return (t * (t - 1) / 2 << rs) + t * (m - (t << rs));
+  }
+  __device__ __forceinline__ int64_t ones() const {  // blocks before the formula passes 1
+    return min(n, max((int64_t)0, ((int64_t)1 << rs) - d));
+  }
+  __device__ __forceinline__ int64_t total() const { return ones() + sum(d + n) - sum(d + ones()); }
+  // the block that holds tile r of the head, and r's index in it
+  __device__ void find(int64_t r, int64_t* block, int* tile) const {
+    const int64_t o = ones();
+    if (r < o) {
+      *block = r;
+      *tile = 0;
+      return;
+    }
+    const int64_t y = r - o + sum(d + o);
+    // largest t with R t (t - 1) / 2 <= y
+    int64_t t = (int64_t)((1.0 + sqrt(1.0 + 8.0 * (double)y / (double)(1 << rs))) / 2.0);
+    while ((t * (t - 1) / 2 << rs) > y) --t;
+    while ((t * (t + 1) / 2 << rs) <= y) ++t;
+    const int64_t z = y - (t * (t - 1) / 2 << rs), m = z / t;
+    *block = (t << rs) + m - d;
+    *tile = (int)(z - m * t);
+  }
+};
 
 __device__ __forceinline__ void ldsm4(uint32_t* r, uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -112,6 +156,23 @@ __device__ __forceinline__ uint32_t sw_off(int r, int c, uint32_t block) {
   return (uint32_t)(c >> 3) * block + (uint32_t)r * 128u + (uint32_t)(((c & 7) ^ (r & 7)) << 4);
 }
 
+// The weights of key k for the two rows of a lane, from the accumulator layout
+// p[n][e] of a 16 x 16 tile (every lane of the warp calls)
+__device__ __forceinline__ void weight_of(const float* p, int k, int lane, float* w) {
+  const int src = (lane & ~3) | ((k & 7) >> 1);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    w[h] = 0.f;
+#pragma unroll
+    for (int z = 0; z < 4; ++z) {  // its register, by a fixed index
+      const int n = z >> 1, e = z & 1;
+      const float c = __shfl_sync(0xffffffffu, p[4 * n + 2 * h + e], src);
+      if (n == (k >> 3) && e == (k & 1)) w[h] = c;
+    }
+  }
+}
+__device__ __forceinline__ bool finite(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
+
 // One quarter-tile's work and its running state, bf16
 template <int DP>
 struct RowsBf16 {
@@ -133,22 +194,21 @@ struct RowsBf16 {
     l[0] = l[1] = 0.f;
   }
 
-  __device__ void step(char* stage, const float*, const Tile& t, int G, float sc, int warp, int lane) {
+  __device__ void step(char* stage, const float*, const Tile& t, float sc, int warp, int lane) {
     const int x0 = t.x0 + 16 * warp;  // this warp's keys
-    if (x0 >= t.kv_len) return;
+    if (x0 >= t.end) return;
     const uint32_t ks = smem_u32(stage);
     char* vs = stage + S::NB * S::kBlock;
-    const int live = min(16, t.kv_len - x0);
+    const int live = min(16, t.end - x0);
     bool poison = false;
-    const int from = t.kv_len - t.len;  // position of the first row
-    const bool masked = x0 + 15 > from;
+    const bool masked = x0 + 15 > t.pos0;
     if (masked) {
-      // rows of V behind the sequence to zero; non-finite values that some row may not attend
+      // rows of V behind the block's last key to zero; non-finite values that some row may not attend
       for (int i = lane; i < 16 * S::NB * 8; i += 32) {
         const int r = i / (S::NB * 8), c = i % (S::NB * 8);
         uint4* x = reinterpret_cast<uint4*>(vs + sw_off(16 * warp + r, c, S::kBlock));
         if (r >= live) *x = make_uint4(0, 0, 0, 0);
-        else if (t.len > 1) {
+        else if (t.rows > t.gb) {
           const uint4 y = *x;
           poison |= ((((y.x & 0x7f807f80u) + 0x00800080u) | ((y.y & 0x7f807f80u) + 0x00800080u) |
                       ((y.z & 0x7f807f80u) + 0x00800080u) | ((y.w & 0x7f807f80u) + 0x00800080u)) & 0x80008000u) != 0;
@@ -172,7 +232,7 @@ struct RowsBf16 {
     int limit[2];
     if (masked) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) limit[h] = min(t.kv_len - 1, from + (r0 + 8 * h) / G) - x0;
+      for (int h = 0; h < 2; ++h) limit[h] = min(t.end - 1, t.pos0 + (r0 + 8 * h) / t.gb) - x0;
 #pragma unroll
       for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -215,37 +275,29 @@ struct RowsBf16 {
         s[n][e] = exp2_fast(fmaf(s[n][e], sc, -ref[e >> 1]));
         l[e >> 1] += s[n][e];
       }
-    if (masked && poison) {  // key by key, into the rows that attend it
+    if (masked && poison) {  // the non-finite values alone into the rows that attend them, then zeros for them
       const float* p0 = &s[0][0];
       for (int k = 0; k < live; ++k) {
-        const int src = (lane & ~3) | ((k & 7) >> 1);
         float w[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float y = 0.f;
-#pragma unroll
-          for (int z = 0; z < 4; ++z) {  // the score's register, by a fixed index
-            const int n = z >> 1, e = z & 1;
-            const float c = __shfl_sync(0xffffffffu, p0[4 * n + 2 * h + e], src);
-            if (n == (k >> 3) && e == (k & 1)) y = c;
-          }
-          w[h] = __bfloat162float(__float2bfloat16_rn(y));
-        }
+        weight_of(p0, k, lane, w);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
           const uint32_t y = *reinterpret_cast<const uint32_t*>(vs + sw_off(16 * warp + k, v, S::kBlock) + 4 * (lane & 3));
-          const float y0 = __uint_as_float(y << 16), y1 = __uint_as_float(y & 0xffff0000u);
-          if (k <= limit[0]) {
-            o[v][0] = fmaf(w[0], y0, o[v][0]);
-            o[v][1] = fmaf(w[0], y1, o[v][1]);
-          }
-          if (k <= limit[1]) {
-            o[v][2] = fmaf(w[1], y0, o[v][2]);
-            o[v][3] = fmaf(w[1], y1, o[v][3]);
-          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if (k <= limit[h]) {
+              if ((y & 0x7f80u) == 0x7f80u) o[v][2 * h] = fmaf(w[h], __uint_as_float(y << 16), o[v][2 * h]);
+              if ((y & 0x7f800000u) == 0x7f800000u)
+                o[v][2 * h + 1] = fmaf(w[h], __uint_as_float(y & 0xffff0000u), o[v][2 * h + 1]);
+            }
         }
       }
-      return;
+      __syncwarp();
+      for (int i = lane; i < 16 * S::NB * 8; i += 32) {
+        uint4* x4 = reinterpret_cast<uint4*>(vs + sw_off(16 * warp + i / (S::NB * 8), i % (S::NB * 8), S::kBlock));
+        const uint4 y = *x4;
+        *x4 = make_uint4(finite_only(y.x), finite_only(y.y), finite_only(y.z), finite_only(y.w));
+      }
     }
     __syncwarp();  // V's zeroed rows
     const uint32_t a[4] = {pack2(s[0][0], s[0][1]), pack2(s[0][2], s[0][3]), pack2(s[1][0], s[1][1]),
@@ -286,7 +338,236 @@ struct RowsBf16 {
   }
 };
 
-// The same in fp32: a lane holds one key and a quarter of its channels for the
+// x = h + m + l to fp32 precision, each part bf16: h is x cut to 8 bits (so it
+// never overflows), m and l round what is left, |x - h - m - l| <= 2^-23 |x|.
+// An infinity or NaN stays in h alone.  Two values at a time.
+struct Split {
+  uint32_t h, m, l;
+};
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ Split split3(float x, float y) {
+  Split s;
+  const uint32_t bx = __float_as_uint(x) & 0xffff0000u, by = __float_as_uint(y) & 0xffff0000u;
+  s.h = (bx >> 16) | by;
+  // (a NaN whose payload the cut loses would turn into an infinity)
+  if (x != x) s.h |= 0x7fffu;
+  if (y != y) s.h |= 0x7fff0000u;
+  float rx = x - __uint_as_float(bx), ry = y - __uint_as_float(by);
+  rx = rx == rx ? rx : 0.f;
+  ry = ry == ry ? ry : 0.f;
+  s.m = pack2(rx, ry);
+  s.l = pack2(rx - bf_lo(s.m), ry - bf_hi(s.m));
+  return s;
+}
+
+// The same in fp32, up to 128 channels, on the same instructions: every operand
+// is split into three bf16 parts (split3) and a product takes the six pairs
+// that matter, h h, h m, m h, h l, l h and m m; what is left out is below
+// 2^-22 of it, as an fp32 rounding or two.
+template <int DP>
+struct RowsF32x3 {
+  using S = Shape<float, DP>;
+  static constexpr int NK = DP / 16, NV = DP / 8;
+  float o[NV][4], m[2], l[2];
+
+  __device__ void start(const char*, float*, int) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[v][e] = 0.f;
+    m[0] = m[1] = -INFINITY;
+    l[0] = l[1] = 0.f;
+  }
+  // the block's q rows, split, by all consumers; rows it does not have are zeros
+  static __device__ void load_q(const AttnParams& p, const Tile& t, float* qs, int tid) {
+    const float* q = static_cast<const float*>(p.q);
+    char* base = reinterpret_cast<char*>(qs);
+    for (int i = tid; i < kMaxRows * DP / 2; i += 32 * kWarps) {
+      const int r = i / (DP / 2), c = 2 * (i % (DP / 2));
+      float2 x = make_float2(0.f, 0.f);
+      if (r < t.rows && c < p.D)
+        x = *reinterpret_cast<const float2*>(q + ((int64_t)(t.tok0 + r / t.gb) * p.H + t.head0 + r % t.gb) * p.D + c);
+      const Split y = split3(x.x, x.y);
+      const uint32_t off = sw_off(r, c >> 3, S::kQBlock) + (c & 7) * 2;
+      *reinterpret_cast<uint32_t*>(base + off) = y.h;
+      *reinterpret_cast<uint32_t*>(base + S::kQPlane + off) = y.m;
+      *reinterpret_cast<uint32_t*>(base + 2 * S::kQPlane + off) = y.l;
+    }
+  }
+
+  __device__ void step(char* stage, const float* qs, const Tile& t, float sc, int warp, int lane) {
+    const int x0 = t.x0 + 16 * warp;  // this warp's keys
+    if (x0 >= t.end) return;
+    char* vs = stage + S::NB * S::kBlock;
+    const int live = min(16, t.end - x0);
+    bool poison = false;
+    const bool masked = x0 + 15 > t.pos0;
+    if (masked) {
+      // rows of V behind the block's last key to zero; non-finite values that some row may not attend
+      for (int i = lane; i < 16 * S::NB * 8; i += 32) {
+        const int r = i / (S::NB * 8), c = i % (S::NB * 8);
+        uint4* x = reinterpret_cast<uint4*>(vs + sw_off(16 * warp + r, c, S::kBlock));
+        if (r >= live) {
+          *x = make_uint4(0, 0, 0, 0);
+        } else if (t.rows > t.gb) {
+          const uint4 y = *x;
+          poison |= ((((y.x & 0x7f800000u) + 0x00800000u) | ((y.y & 0x7f800000u) + 0x00800000u) |
+                      ((y.z & 0x7f800000u) + 0x00800000u) | ((y.w & 0x7f800000u) + 0x00800000u)) & 0x80000000u) != 0;
+        }
+      }
+      poison = __any_sync(0xffffffffu, poison);
+    }
+    const int r0 = lane >> 2, q2 = lane & 3;
+    float s[2][4], sx[2][4];  // h h apart from the smaller products
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[n][e] = sx[n][e] = 0.f;
+    const uint32_t qa = smem_u32(qs);
+#pragma unroll 2
+    for (int k = 0; k < NK; ++k) {
+      uint32_t ah[4], am[4], al[4];
+      const uint32_t off = sw_off((lane & 7) + ((lane >> 3) & 1) * 8, 2 * k + (lane >> 4), S::kQBlock);
+      ldsm4(ah, qa + off);
+      ldsm4(am, qa + S::kQPlane + off);
+      ldsm4(al, qa + 2 * S::kQPlane + off);
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const int row = 16 * warp + 8 * n + r0;
+        const float2 x = *reinterpret_cast<const float2*>(stage + sw_off(row, 4 * k + (q2 >> 1), S::kBlock) + (q2 & 1) * 8);
+        const float2 y = *reinterpret_cast<const float2*>(stage + sw_off(row, 4 * k + 2 + (q2 >> 1), S::kBlock) + (q2 & 1) * 8);
+        const Split b0 = split3(x.x, x.y), b1 = split3(y.x, y.y);
+        mma16816(s[n], ah, b0.h, b1.h);
+        mma16816(sx[n], ah, b0.l, b1.l);
+        mma16816(sx[n], al, b0.h, b1.h);
+        mma16816(sx[n], am, b0.m, b1.m);
+        mma16816(sx[n], ah, b0.m, b1.m);
+        mma16816(sx[n], am, b0.h, b1.h);
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[n][e] += sx[n][e];
+    const int c0 = 2 * q2;
+    int limit[2];
+    if (masked) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) limit[h] = min(t.end - 1, t.pos0 + (r0 + 8 * h) / t.gb) - x0;
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (8 * n + c0 + (e & 1) > limit[e >> 1]) s[n][e] = -INFINITY;
+    }
+    float x[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      x[h] = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
+      x[h] = fmaxf(x[h], __shfl_xor_sync(0xffffffffu, x[h], 1));
+      x[h] = sc * fmaxf(x[h], __shfl_xor_sync(0xffffffffu, x[h], 2));
+    }
+    const bool up = x[0] > m[0] || x[1] > m[1];
+    if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (!(x[h] > m[h])) x[h] = m[h];
+        const float f = m[h] == -INFINITY ? 1.f : exp2f(m[h] - x[h]);
+        m[h] = x[h];
+        l[h] *= f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          o[v][2 * h] *= f;
+          o[v][2 * h + 1] *= f;
+        }
+      }
+    }
+    const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s[n][e] = exp2f(fmaf(s[n][e], sc, -ref[e >> 1]));
+        l[e >> 1] += s[n][e];
+      }
+    if (masked && poison) {  // as for bf16
+      const float* p0 = &s[0][0];
+      for (int k = 0; k < live; ++k) {
+        float w[2];
+        weight_of(p0, k, lane, w);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          const float2 y = *reinterpret_cast<const float2*>(vs + sw_off(16 * warp + k, 2 * v + (q2 >> 1), S::kBlock) + (q2 & 1) * 8);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if (k <= limit[h]) {
+              if (!finite(y.x)) o[v][2 * h] = fmaf(w[h], y.x, o[v][2 * h]);
+              if (!finite(y.y)) o[v][2 * h + 1] = fmaf(w[h], y.y, o[v][2 * h + 1]);
+            }
+        }
+      }
+      __syncwarp();
+      for (int i = lane; i < 16 * S::NB * 8; i += 32) {
+        float4* x4 = reinterpret_cast<float4*>(vs + sw_off(16 * warp + i / (S::NB * 8), i % (S::NB * 8), S::kBlock));
+        const float4 y = *x4;
+        *x4 = make_float4(finite(y.x) ? y.x : 0.f, finite(y.y) ? y.y : 0.f, finite(y.z) ? y.z : 0.f,
+                          finite(y.w) ? y.w : 0.f);
+      }
+    }
+    __syncwarp();  // V's zeroed rows
+    uint32_t ah[4], am[4], al[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const Split y = split3(s[i >> 1][2 * (i & 1)], s[i >> 1][2 * (i & 1) + 1]);
+      ah[i] = y.h;
+      am[i] = y.m;
+      al[i] = y.l;
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      // keys 2 q2, + 1, + 8, + 9 of channel 8 v + r0
+      float y[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        y[i] = *reinterpret_cast<const float*>(
+            vs + sw_off(16 * warp + 2 * q2 + (i & 1) + 8 * (i >> 1), 2 * v + (r0 >> 2), S::kBlock) + (r0 & 3) * 4);
+      const Split b0 = split3(y[0], y[1]), b1 = split3(y[2], y[3]);
+      mma16816(o[v], ah, b0.l, b1.l);
+      mma16816(o[v], al, b0.h, b1.h);
+      mma16816(o[v], am, b0.m, b1.m);
+      mma16816(o[v], ah, b0.m, b1.m);
+      mma16816(o[v], am, b0.h, b1.h);
+      mma16816(o[v], ah, b0.h, b1.h);
+    }
+  }
+  __device__ void stats(float2* ml, int lane) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+      if ((lane & 3) == 0) ml[(lane >> 2) + 8 * h] = make_float2(m[h], l[h]);
+    }
+  }
+  __device__ void put(float* scratch, const float2 (*ml)[kMaxRows], int rows, int lane) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = (lane >> 2) + 8 * h;
+      if (r >= rows) continue;
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w][r].x);
+      const float f = exp2f(m[h] - (M == -INFINITY ? 0.f : M));
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        *reinterpret_cast<float2*>(scratch + r * DP + 8 * v + 2 * (lane & 3)) =
+            make_float2(o[v][2 * h] * f, o[v][2 * h + 1] * f);
+    }
+  }
+};
+
+// fp32 with 256 channels: FMAs, 8 keys a warp.  A lane holds one key and a
+// quarter of its channels for the
 // scores, then DP / 32 channels of the output
 template <int DP, int RT_>
 struct RowsF32 {
@@ -306,22 +587,22 @@ struct RowsF32 {
     (void)qs;
     (void)lane;
   }
-  // the pair's q rows, by all consumers; rows it does not have are zeros
+  // the block's q rows, by all consumers; rows it does not have are zeros
   static __device__ void load_q(const AttnParams& p, const Tile& t, float* qs, int tid) {
     const float* q = static_cast<const float*>(p.q);
     for (int i = tid; i < RT * DP; i += 32 * kWarps) {
       const int r = i / DP, c = i % DP;
-      qs[i] = r < t.len * p.G && c < p.D
-                  ? q[((int64_t)(t.tok0 + r / p.G) * p.H + (int64_t)t.head * p.G + r % p.G) * p.D + c]
+      qs[i] = r < t.rows && c < p.D
+                  ? q[((int64_t)(t.tok0 + r / t.gb) * p.H + t.head0 + r % t.gb) * p.D + c]
                   : 0.f;
     }
   }
 
-  __device__ void step(char* stage, const float* qs, const Tile& t, int G, float sc, int warp, int lane) {
+  __device__ void step(char* stage, const float* qs, const Tile& t, float sc, int warp, int lane) {
     const int x0 = t.x0 + 8 * warp;
-    if (x0 >= t.kv_len) return;
-    const int live = min(8, t.kv_len - x0), from = t.kv_len - t.len;
-    const bool masked = x0 + 7 > from;
+    if (x0 >= t.end) return;
+    const int live = min(8, t.end - x0);
+    const bool masked = x0 + 7 > t.pos0;
     const int i = lane >> 2, qd = lane & 3;
     const int key = ((i & 1) << 2) | (i >> 1);  // lanes of a load phase four keys apart: no bank conflict
     float s[RT];
@@ -341,7 +622,7 @@ struct RowsF32 {
       s[r] += __shfl_xor_sync(0xffffffffu, s[r], 1);
       s[r] += __shfl_xor_sync(0xffffffffu, s[r], 2);
       s[r] *= sc;
-      if (masked && x0 + key > min(t.kv_len - 1, from + r / G)) s[r] = -INFINITY;
+      if (masked && x0 + key > min(t.end - 1, t.pos0 + r / t.gb)) s[r] = -INFINITY;
       float x = s[r];
       x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
       x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
@@ -378,7 +659,7 @@ struct RowsF32 {
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
         const float w = __shfl_sync(0xffffffffu, s[r], src);
-        if (!masked || x0 + k <= from + r / G) {  // a masked key's value stays out even where it is not finite
+        if (!masked || x0 + k <= t.pos0 + r / t.gb) {  // a masked key's value stays out even where it is not finite
 #pragma unroll
           for (int c = 0; c < NG * NC; ++c) o[r][c] = fmaf(w, v[c], o[r][c]);
         }
@@ -445,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, DP>::CTAS)
       if (s < p.num_seqs) {
         const AttnSeq q = attn_seq(p, s);
         if (pass == 0 && q.flag && blockIdx.x == 0) attn_flag(p.status, q.flag);
-        n = (int64_t)tiles_of<T, DP>(q) * p.Hkv;
+        if (q.len > 0) n = Blocks<KT>(q, a.q_shift).total() * p.Hkv * a.parts;
       }
       int64_t x = n;
 #pragma unroll
@@ -489,39 +770,51 @@ __global__ void __launch_bounds__(kThreads, Shape<T, DP>::CTAS)
 
   if (warp == kWarps) {
     // ---- copies
-    int base = (int)first_seq, cur = 0;  // 32 requests at a time, one a lane
+    int base = (int)first_seq, cur = 0;  // 32 sequences at a time, one a lane
     AttnSeq mine{};
-    int mine_n = 0;
     auto fetch = [&](int at) {
       base = at;
       mine = AttnSeq{};
-      mine_n = 0;
-      if (at + lane < p.num_seqs) {
-        mine = attn_seq(p, at + lane);
-        mine_n = tiles_of<T, DP>(mine);
-      }
+      if (at + lane < p.num_seqs) mine = attn_seq(p, at + lane);
     };
     fetch(base);
-    int n = __shfl_sync(0xffffffffu, mine_n, 0);
-    int head = (int)(first_off / n), tile = (int)(first_off % n);
+    AttnSeq sq;
+    auto seq = [&] {
+      sq.tok0 = __shfl_sync(0xffffffffu, mine.tok0, cur);
+      sq.len = __shfl_sync(0xffffffffu, mine.len, cur);
+      sq.kv_len = __shfl_sync(0xffffffffu, mine.kv_len, cur);
+      sq.row = __shfl_sync(0xffffffffu, mine.row, cur);
+    };
+    seq();
+    Blocks<KT> bl(sq, a.q_shift);
+    const int64_t per_head = bl.total();
+    int head = (int)(first_off / per_head), tile;  // head: key head * parts + part
+    int64_t block;
+    bl.find(first_off - head * per_head, &block, &tile);
+    int n = bl.tiles(block);
     bool seg_first = true;
     int seg_tile0 = tile;
     bool ok = true;
     uint32_t k = 0;
     if (lane == 0) a.joins[blockIdx.x].parts = 0;
-    const uint32_t box_bytes = (uint32_t)a.box * 128u;
+    const uint32_t box_bytes = 128u << a.box_shift;
+    const int box = 1 << a.box_shift, qt = 1 << a.q_shift, gmax = min(p.G, kMaxRows);
     for (int64_t u = u0; u < u1 && ok; ++u, ++k) {
-      const int tok0 = (int)__shfl_sync(0xffffffffu, mine.tok0, cur), len = __shfl_sync(0xffffffffu, mine.len, cur);
-      const int kv = (int)__shfl_sync(0xffffffffu, mine.kv_len, cur), row = __shfl_sync(0xffffffffu, mine.row, cur);
+      const int kvh = a.parts == 1 ? head : head / a.parts, part = a.parts == 1 ? 0 : head - kvh * a.parts;
+      const int t0 = (int)block << a.q_shift, ntok = min(qt, sq.len - t0);
+      const int pos0 = (int)sq.kv_len - sq.len + t0, end = max(0, min((int)sq.kv_len, pos0 + ntok));
       const int x0 = tile * KT;
-      const int nb = max(0, min(KT / a.box, (kv - x0 + a.box - 1) / a.box));
-      int c2 = 0, c3 = 0;
-      if (lane < nb) {
-        const int x = x0 + lane * a.box;
-        int page = p.block_table[(int64_t)row * p.max_pages + (x >> p.page_shift)];
-        if (page < 0 || page >= p.num_pages) {
-          attn_flag(p.status, kFlagBadCache);
-          page = p.num_pages;  // outside the map: filled with zeros
+      const int nb = max(0, min(KT >> a.box_shift, (end - x0 + box - 1) >> a.box_shift));
+      const int x = x0 + (lane << a.box_shift);
+      int c2 = (int)sq.tok0 + x, c3 = 0;
+      if (p.block_table) {
+        int page = p.num_pages;
+        if (lane < nb) {
+          page = p.block_table[(int64_t)sq.row * p.max_pages + (x >> p.page_shift)];
+          if (page < 0 || page >= p.num_pages) {
+            attn_flag(p.status, kFlagBadCache);
+            page = p.num_pages;  // outside the map: filled with zeros
+          }
         }
         c2 = x & ((1 << p.page_shift) - 1);
         c3 = page;
@@ -533,53 +826,59 @@ __global__ void __launch_bounds__(kThreads, Shape<T, DP>::CTAS)
       const bool last = u + 1 == u1 || tile + 1 == n;
       if (lane == 0) {
         Tile t;
-        t.tok0 = tok0;
-        t.len = len;
-        t.kv_len = kv;
-        t.head = head;
+        t.tok0 = (int)sq.tok0 + t0;
+        t.head0 = kvh * p.G + part * kMaxRows;
+        t.gb = a.parts == 1 ? p.G : min(kMaxRows, p.G - part * kMaxRows);
+        t.rows = ntok * t.gb;
+        t.pos0 = pos0;
+        t.end = end;
         t.x0 = x0;
         t.first = seg_first;
         t.last = last;
         t.slot = -1;
         if (last && (seg_tile0 > 0 || tile + 1 < n)) {
           t.slot = 2 * (int)blockIdx.x + (seg_tile0 == 0);
-          if (seg_tile0 == 0)  // the pair starts here: its other parts are the next stretches' first ones
-            a.joins[blockIdx.x] =
-                RowsJoin{(int)((u - tile + n - 1) / per - blockIdx.x + 1), tok0, len, head};
+          if (seg_tile0 == 0)  // the block starts here: its other parts are the next stretches' first ones
+            a.joins[blockIdx.x] = RowsJoin{(int)((u - tile + n - 1) / per - blockIdx.x + 1), t.tok0, t.head0, t.rows, t.gb};
         }
         b->tile[st] = t;
         const uint32_t bytes = (uint32_t)nb * box_bytes * 2 * S::NB +
-                               (sizeof(T) == 2 && seg_first ? (uint32_t)(a.q_tokens * p.G) * 128u * S::NB : 0u);
+                               (sizeof(T) == 2 && seg_first ? (uint32_t)(qt * gmax) * 128u * S::NB : 0u);
         mbar_arrive_expect_tx(&b->full[st], bytes);
         if (sizeof(T) == 2 && seg_first)
 #pragma unroll
           for (int c = 0; c < S::NB; ++c)
-            tma_3d(dst + S::kKV + c * S::kQBlock, &mq, c * (128 / (int)sizeof(T)), head * p.G, tok0, &b->full[st]);
+            tma_3d(dst + S::kKV + c * S::kQBlock, &mq, c * (128 / (int)sizeof(T)), t.head0, t.tok0, &b->full[st]);
       }
       __syncwarp();
       if (lane < nb)
 #pragma unroll
         for (int c = 0; c < S::NB; ++c) {
           const int ch = c * (128 / (int)sizeof(T));
-          tma_4d(dst + c * S::kBlock + lane * box_bytes, &mk, ch, head, c2, c3, &b->full[st]);
-          tma_4d(dst + (S::NB + c) * S::kBlock + lane * box_bytes, &mv, ch, head, c2, c3, &b->full[st]);
+          tma_4d(dst + c * S::kBlock + lane * box_bytes, &mk, ch, kvh, c2, c3, &b->full[st]);
+          tma_4d(dst + (S::NB + c) * S::kBlock + lane * box_bytes, &mv, ch, kvh, c2, c3, &b->full[st]);
         }
       // the next tile of the line
       seg_first = last;
       if (++tile == n) {
         tile = 0;
-        if (++head == p.Hkv) {
-          head = 0;
-          if (u + 1 < u1) {
-            do {
-              if (++cur == 32) {
-                cur = 0;
-                fetch(base + 32);
-              }
-              n = __shfl_sync(0xffffffffu, mine_n, cur);
-            } while (n == 0 && base + cur < p.num_seqs);
+        if (++block == bl.n) {
+          block = 0;
+          if (++head == p.Hkv * a.parts) {
+            head = 0;
+            if (u + 1 < u1) {
+              do {
+                if (++cur == 32) {
+                  cur = 0;
+                  fetch(base + 32);
+                }
+                seq();
+              } while (sq.len == 0 && base + cur < p.num_seqs);
+              bl = Blocks<KT>(sq, a.q_shift);
+            }
           }
         }
+        n = bl.tiles(block);
       }
       if (seg_first) seg_tile0 = tile;
     }
@@ -611,9 +910,9 @@ __global__ void __launch_bounds__(kThreads, Shape<T, DP>::CTAS)
         }
         w.start(stage, qs, lane);
       }
-      w.step(stage, qs, t, p.G, sc, warp, lane);
+      w.step(stage, qs, t, sc, warp, lane);
       if (t.last) {
-        const int rows = t.len * p.G;
+        const int rows = t.rows;
         w.stats(b->ml[warp], lane);
         __syncwarp();
         if (lane == 0) mbar_arrive(&b->join[0]);
@@ -660,7 +959,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, DP>::CTAS)
             if (c == 0) a.ml[t.slot * kMaxRows + r] = make_float2(M[i], L[i]);
           } else if (c < p.D) {
             const int64_t at =
-                ((int64_t)(t.tok0 + r / p.G) * p.H + (int64_t)t.head * p.G + r % p.G) * p.D + c;
+                ((int64_t)(t.tok0 + r / t.gb) * p.H + t.head0 + r % t.gb) * p.D + c;
             const float f = L[i] == 0.f ? 0.f : 1.f / L[i];
             if constexpr (sizeof(T) == 2)
               *reinterpret_cast<uint2*>(out + at) = make_uint2(pack2(x.x * f, x.y * f), pack2(x.z * f, x.w * f));
@@ -679,14 +978,14 @@ __global__ void __launch_bounds__(kThreads, Shape<T, DP>::CTAS)
   if (tid == 0 && b->dead) attn_flag(p.status, kFlagTimeout);
 }
 
-// The pairs that cross stretches, a CTA per stretch and row: parts
+// The blocks that cross stretches, a CTA per stretch and row: parts
 // 2 c + 1, 2 (c + 1), 2 (c + 2), ..  A thread per channel.
 template <typename T, int DP>
 __global__ void __launch_bounds__(DP) attn_rows_join(const AttnParams p, const RowsArgs a) {
   pdl_wait();
   const RowsJoin jn = a.joins[blockIdx.x];
   const int r = blockIdx.y, c = threadIdx.x;
-  if (jn.parts == 0 || r >= jn.len * p.G) return;
+  if (jn.parts == 0 || r >= jn.rows) return;
   const int s0 = 2 * (int)blockIdx.x;
   auto slot = [&](int k) { return k == 0 ? s0 + 1 : s0 + 2 * k; };
   float M = -INFINITY;
@@ -702,20 +1001,21 @@ __global__ void __launch_bounds__(DP) attn_rows_join(const AttnParams p, const R
   }
   if (c < p.D)
     st_out(static_cast<T*>(p.o),
-           ((int64_t)(jn.tok0 + r / p.G) * p.H + (int64_t)jn.head * p.G + r % p.G) * p.D + c,
+           ((int64_t)(jn.tok0 + r / jn.gb) * p.H + jn.head0 + r % jn.gb) * p.D + c,
            l == 0.f ? 0.f : o / l);
 }
 
 // ------------------------------------------------------------------ host
-bool encode(CUtensorMap* m, const AttnParams& p, const void* base, bool q, int box) {
+// q, or K or V as [pages][positions][Hkv][D] (packed: one page of all tokens)
+bool encode(CUtensorMap* m, const AttnParams& p, const void* base, bool q, int heads, int box) {
   const EncodeTiledFn enc = encode_tiled();
   if (!enc) return false;
-  const bool half = p.dt == KDA_BF16;
-  const cuuint64_t es = half ? 2 : 4, page = (cuuint64_t)1 << p.page_shift;
-  const cuuint64_t heads = q ? p.H : p.Hkv, row = heads * p.D * es;
-  const cuuint64_t dims[4] = {(cuuint64_t)p.D, heads, q ? (cuuint64_t)p.total_tokens : page, (cuuint64_t)p.num_pages};
+  const bool half = p.dt == KDA_BF16, paged = !q && p.block_table;
+  const cuuint64_t es = half ? 2 : 4, page = paged ? (cuuint64_t)1 << p.page_shift : (cuuint64_t)p.total_tokens;
+  const cuuint64_t nh = q ? p.H : p.Hkv, row = nh * p.D * es;
+  const cuuint64_t dims[4] = {(cuuint64_t)p.D, nh, page, paged ? (cuuint64_t)p.num_pages : 1};
   const cuuint64_t strides[3] = {p.D * es, row, row * page};
-  const cuuint32_t bx[4] = {(cuuint32_t)(128 / es), q ? (cuuint32_t)p.G : 1u, (cuuint32_t)box, 1};
+  const cuuint32_t bx[4] = {(cuuint32_t)(128 / es), (cuuint32_t)heads, (cuuint32_t)box, 1};
   const cuuint32_t elem[4] = {1, 1, 1, 1};
   return enc(m, half ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, q ? 3 : 4,
              const_cast<void*>(base), dims, strides, bx, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -728,6 +1028,13 @@ constexpr int kMaxGrid = 2 * 192;  // two CTAs on each of up to 192 SMs
 int padded(const AttnParams& p) {
   const int low = p.dt == KDA_BF16 ? 64 : 32;
   return p.D < low ? low : p.D;
+}
+
+// Tokens of a block, log2: as many as 16 rows hold and a sequence may have
+int block_shift(const AttnParams& p) {
+  int s = 0;
+  while ((2 << s) * p.G <= kMaxRows && (1 << s) < p.max_seqlen) ++s;
+  return s;
 }
 
 template <typename T, int DP, typename Work>
@@ -744,23 +1051,25 @@ cudaError_t launch_w(const AttnParams& p, char* w, cudaStream_t stream) {
   a.joins = reinterpret_cast<RowsJoin*>(w);
   a.ml = reinterpret_cast<float2*>(w + align_up(sizeof(RowsJoin) * kMaxGrid, 256));
   a.o = reinterpret_cast<float*>(a.ml + 2 * kMaxGrid * kMaxRows);
-  const int page = 1 << p.page_shift;
-  a.box = page < S::KT ? page : S::KT;
-  a.q_tokens = (int)p.max_seqlen;
+  constexpr int kt_shift = S::KT == 64 ? 6 : 5;
+  a.box_shift = p.block_table && p.page_shift < kt_shift ? p.page_shift : kt_shift;
+  a.q_shift = block_shift(p);
+  a.parts = (p.G + kMaxRows - 1) / kMaxRows;
+  const int heads = p.G < kMaxRows ? p.G : kMaxRows;
   CUtensorMap mq, mk, mv;
-  if (!encode(&mq, p, p.q, true, a.q_tokens) || !encode(&mk, p, p.k, false, a.box) ||
-      !encode(&mv, p, p.v, false, a.box))
+  if (!encode(&mq, p, p.q, true, heads, 1 << a.q_shift) || !encode(&mk, p, p.k, false, 1, 1 << a.box_shift) ||
+      !encode(&mv, p, p.v, false, 1, 1 << a.box_shift))
     return cudaErrorInvalidValue;
   kernel<<<grid, kThreads, S::kBytes, stream>>>(p, a, mq, mk, mv);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_maybe_dependent(true, attn_rows_join<T, DP>, dim3((unsigned)grid, (unsigned)(p.max_seqlen * p.G)),
+  return launch_maybe_dependent(true, attn_rows_join<T, DP>, dim3((unsigned)grid, (unsigned)(heads << a.q_shift)),
                                 dim3(DP), 0, stream, p, a);
 }
 
 template <int DP>
 cudaError_t launch_f32(const AttnParams& p, char* w, cudaStream_t stream) {
-  const int64_t rows = p.max_seqlen * p.G;
+  const int rows = (p.G < kMaxRows ? p.G : kMaxRows) << block_shift(p);
   if (rows <= 4) return launch_w<float, DP, RowsF32<DP, 4>>(p, w, stream);
   if (rows <= 8) return launch_w<float, DP, RowsF32<DP, 8>>(p, w, stream);
   return launch_w<float, DP, RowsF32<DP, 16>>(p, w, stream);
@@ -768,12 +1077,15 @@ cudaError_t launch_f32(const AttnParams& p, char* w, cudaStream_t stream) {
 
 }  // namespace
 
-// At most 16 rows a request, a positive finite scale (the running maximum is
-// taken before the scaling), 16-byte aligned bases for the tensor maps.
+// Single tokens, or as few as 16 rows hold, over the cache (more rows of bf16
+// go to the tensor cores' 128-row tiles); all of fp32 and of 256 channels.  A
+// positive finite scale (the running maximum is taken before the scaling),
+// 16-byte aligned bases for the tensor maps.
 bool attn_rows_fits(const AttnParams& p) {
   auto al16 = [](const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15) == 0; };
-  return p.block_table && p.max_seqlen * p.G <= kMaxRows && p.scale > 0.f && p.scale <= 3.4e38f && al16(p.q) &&
-         al16(p.k) && al16(p.v) && al16(p.o) && p.num_pages > 0;
+  const bool few = p.block_table && p.max_seqlen * p.G <= kMaxRows;
+  return (few || p.dt == KDA_F32 || p.D == 256) && p.scale > 0.f && p.scale <= 3.4e38f && al16(p.q) && al16(p.k) &&
+         al16(p.v) && al16(p.o) && (!p.block_table || p.num_pages > 0);
 }
 size_t attn_rows_workspace(const AttnParams& p) {
   return align_up(sizeof(RowsJoin) * kMaxGrid, 256) + 2 * kMaxGrid * kMaxRows * (sizeof(float2) + padded(p) * 4);
@@ -788,9 +1100,9 @@ cudaError_t launch_attn_rows(const AttnParams& p, void* ws, cudaStream_t stream)
     }
   }
   switch (padded(p)) {
-    case 32: return launch_f32<32>(p, w, stream);
-    case 64: return launch_f32<64>(p, w, stream);
-    case 128: return launch_f32<128>(p, w, stream);
+    case 32: return launch_w<float, 32, RowsF32x3<32>>(p, w, stream);
+    case 64: return launch_w<float, 64, RowsF32x3<64>>(p, w, stream);
+    case 128: return launch_w<float, 128, RowsF32x3<128>>(p, w, stream);
     default: return launch_f32<256>(p, w, stream);
   }
 }
