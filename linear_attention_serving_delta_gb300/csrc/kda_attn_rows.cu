@@ -714,6 +714,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, DP>::CTAS)
     mbar_init_fence();
   }
   pdl_wait();
+  pdl_launch_dependents();  // the join's launch overlaps the work (it waits for the end of it)
 
   // the line of work: its length, this CTA's stretch, and where that starts
   int64_t W = 0, u0 = 0, u1 = 0, before = 0;
@@ -978,31 +979,39 @@ __global__ void __launch_bounds__(kThreads, Shape<T, DP>::CTAS)
   if (tid == 0 && b->dead) attn_flag(p.status, kFlagTimeout);
 }
 
-// The blocks that cross stretches, a CTA per stretch and row: parts
-// 2 c + 1, 2 (c + 1), 2 (c + 2), ..  A thread per channel.
+// The blocks that cross stretches: parts 2 c + 1, 2 (c + 1), 2 (c + 2), .. of
+// stretch c.  A warp per row, DP / 32 channels a lane.
+constexpr int kJoinWarps = 4;
 template <typename T, int DP>
-__global__ void __launch_bounds__(DP) attn_rows_join(const AttnParams p, const RowsArgs a) {
+__global__ void __launch_bounds__(32 * kJoinWarps) attn_rows_join(const AttnParams p, const RowsArgs a) {
   pdl_wait();
   const RowsJoin jn = a.joins[blockIdx.x];
-  const int r = blockIdx.y, c = threadIdx.x;
+  const int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (jn.parts == 0 || r >= jn.rows) return;
+  constexpr int V = DP / 32;
   const int s0 = 2 * (int)blockIdx.x;
-  auto slot = [&](int k) { return k == 0 ? s0 + 1 : s0 + 2 * k; };
+  auto slot = [&](int k) { return (k == 0 ? s0 + 1 : s0 + 2 * k) * kMaxRows + r; };
   float M = -INFINITY;
-  for (int k = 0; k < jn.parts; ++k) M = fmaxf(M, a.ml[slot(k) * kMaxRows + r].x);
+  for (int k = lane; k < jn.parts; k += 32) M = fmaxf(M, a.ml[slot(k)].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   if (M == -INFINITY) M = 0.f;
-  float l = 0.f, o = 0.f;
+  float l = 0.f, o[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) o[v] = 0.f;
 #pragma unroll 4
   for (int k = 0; k < jn.parts; ++k) {
-    const float2 ml = a.ml[slot(k) * kMaxRows + r];
+    const float2 ml = a.ml[slot(k)];
     const float f = exp2f(ml.x - M);
     l = fmaf(f, ml.y, l);
-    o = fmaf(f, a.o[((int64_t)slot(k) * kMaxRows + r) * DP + c], o);
+#pragma unroll
+    for (int v = 0; v < V; ++v) o[v] = fmaf(f, a.o[(int64_t)slot(k) * DP + 32 * v + lane], o[v]);
   }
-  if (c < p.D)
-    st_out(static_cast<T*>(p.o),
-           ((int64_t)(jn.tok0 + r / jn.gb) * p.H + jn.head0 + r % jn.gb) * p.D + c,
-           l == 0.f ? 0.f : o / l);
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int64_t at = ((int64_t)(jn.tok0 + r / jn.gb) * p.H + jn.head0 + r % jn.gb) * p.D;
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    if (32 * v + lane < p.D) st_out(static_cast<T*>(p.o), at + 32 * v + lane, o[v] * inv);
 }
 
 // ------------------------------------------------------------------ host
@@ -1046,7 +1055,12 @@ cudaError_t launch_w(const AttnParams& p, char* w, cudaStream_t stream) {
   auto kernel = attn_rows<T, DP, Work>;
   if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kBytes);
   if (e != cudaSuccess) return e;
-  const int grid = sms * S::CTAS < kMaxGrid ? sms * S::CTAS : kMaxGrid;
+  // no more CTAs than stretches of kMinTiles that the longest rows could fill
+  const int64_t keys = p.block_table ? (int64_t)p.max_pages << p.page_shift : p.total_tokens;
+  const int64_t blocks = ((p.total_tokens >> block_shift(p)) + p.num_seqs) * ((p.G + kMaxRows - 1) / kMaxRows) * p.Hkv;
+  const int64_t most = blocks < kMaxGrid * kMinTiles ? (blocks * (keys / S::KT + 2) + kMinTiles - 1) / kMinTiles : kMaxGrid;
+  int grid = sms * S::CTAS < kMaxGrid ? sms * S::CTAS : kMaxGrid;
+  if (most < grid) grid = (int)most;
   RowsArgs a{};
   a.joins = reinterpret_cast<RowsJoin*>(w);
   a.ml = reinterpret_cast<float2*>(w + align_up(sizeof(RowsJoin) * kMaxGrid, 256));
@@ -1060,11 +1074,12 @@ cudaError_t launch_w(const AttnParams& p, char* w, cudaStream_t stream) {
   if (!encode(&mq, p, p.q, true, heads, 1 << a.q_shift) || !encode(&mk, p, p.k, false, 1, 1 << a.box_shift) ||
       !encode(&mv, p, p.v, false, 1, 1 << a.box_shift))
     return cudaErrorInvalidValue;
-  kernel<<<grid, kThreads, S::kBytes, stream>>>(p, a, mq, mk, mv);
-  e = cudaGetLastError();
+  e = launch_maybe_dependent(true, kernel, dim3((unsigned)grid), dim3(kThreads), (size_t)S::kBytes, stream, p, a, mq, mk,
+                             mv);
   if (e != cudaSuccess) return e;
-  return launch_maybe_dependent(true, attn_rows_join<T, DP>, dim3((unsigned)grid, (unsigned)(heads << a.q_shift)),
-                                dim3(DP), 0, stream, p, a);
+  return launch_maybe_dependent(true, attn_rows_join<T, DP>,
+                                dim3((unsigned)grid, (unsigned)((heads << a.q_shift) + kJoinWarps - 1) / kJoinWarps),
+                                dim3(32 * kJoinWarps), 0, stream, p, a);
 }
 
 template <int DP>

@@ -68,6 +68,8 @@ struct Bars {
   uint64_t q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], o_full[2];
   uint64_t fix, drain[2];
   uint32_t dead;      // a wait expired: every role winds down
+  uint32_t own;       // a call that plans for itself: this CTA has an item
+  int32_t plan[kThreads / 32];
   uint32_t turn;      // held by the MMA warp whose burst is being issued
   uint32_t tmem;
   // the CTA's k-th item with key tiles: non-finite values were taken out of its
@@ -99,6 +101,10 @@ __device__ __forceinline__ Geo geometry(const AttnItem& it, int G, int tpt) {
   const int first = it.pos0 + 1;
   g.fix_from = first <= 0 ? 0 : first / kTile;
   return g;
+}
+
+__device__ __forceinline__ const AttnItem& item_at(const TcArgs& a, int64_t w, int Hkv) {
+  return a.items[a.self_plan ? w : w / Hkv];
 }
 
 // The CTA's i-th item: items go round the CTAs back and forth, so that the
@@ -170,7 +176,7 @@ __device__ void load_k_role(const AttnParams& p, const TcArgs& a, const CUtensor
   for (int i = 0; ok; ++i) {
     const int64_t w = nth_item(i);
     if (w >= total) break;
-    const AttnItem it = a.items[w / p.Hkv];
+    const AttnItem it = item_at(a, w, p.Hkv);
     const int h = (int)(w % p.Hkv);
     const Geo g = geometry(it, p.G, tpt);
 #pragma unroll
@@ -217,7 +223,7 @@ __device__ void load_v_role(const AttnParams& p, const TcArgs& a, const CUtensor
   for (int i = 0; ok; ++i) {
     const int64_t w = nth_item(i);
     if (w >= total) break;
-    const AttnItem it = a.items[w / p.Hkv];
+    const AttnItem it = item_at(a, w, p.Hkv);
     const int h = (int)(w % p.Hkv);
     const Geo g = geometry(it, p.G, tpt);
     if (g.nmax == 0) continue;
@@ -355,7 +361,7 @@ __device__ void mma_role(const AttnParams& p, const TcArgs& a, char* sm, Bars* b
   for (int i = 0; ok; ++i) {
     const int64_t w = nth_item(i);
     if (w >= total) break;
-    const AttnItem it = a.items[w / p.Hkv];
+    const AttnItem it = item_at(a, w, p.Hkv);
     const Geo g = geometry(it, p.G, tpt);
     const int n = t == 0 ? g.n[0] : g.n[1];
     if (g.nmax == 0) continue;
@@ -441,7 +447,7 @@ __device__ void softmax_role(const AttnParams& p, const TcArgs& a, Bars* b, int6
   int h_ahead = 0;
   auto fetch = [&](int64_t w) {
     if (w < total) {
-      ahead = a.items[w / p.Hkv];
+      ahead = item_at(a, w, p.Hkv);
       h_ahead = (int)(w % p.Hkv);
     }
   };
@@ -611,6 +617,60 @@ __device__ void softmax_role(const AttnParams& p, const TcArgs& a, Bars* b, int6
   }
 }
 
+__device__ __forceinline__ AttnItem make_item(const AttnParams& p, const AttnSeq& s, int64_t tile, int tpi) {
+  AttnItem it;
+  it.tok0 = (int32_t)(s.tok0 + tile * tpi);
+  it.ntok = (int32_t)min((int64_t)tpi, s.len - tile * tpi);
+  it.base = p.block_table ? s.row : (int32_t)s.tok0;
+  it.pos0 = (int32_t)(s.kv_len - s.len + tile * tpi);
+  it.kv_len = (int32_t)s.kv_len;
+  it.kt0 = 0;
+  it.kt1 = (max(0, min(it.kv_len, it.pos0 + it.ntok)) + kTile - 1) / kTile;
+  it.slot = -1;
+  return it;
+}
+
+// Small calls plan for themselves: no more items than CTAs, so the order does
+// not matter and CTA w needs item w alone, which the thread of its sequence
+// leaves in the workspace.  Returns whether there is one (for every thread).
+__device__ bool plan_own_item(const AttnParams& p, const TcArgs& a, Bars* b, int tpi) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t want = blockIdx.x / p.Hkv;
+  int64_t before = 0;
+  for (int base = 0; base < p.num_seqs; base += kThreads) {
+    const int s = base + tid;
+    AttnSeq q{};
+    int n = 0;
+    if (s < p.num_seqs) {
+      q = attn_seq(p, s);
+      if (q.flag && blockIdx.x == 0) attn_flag(p.status, q.flag);
+      n = (q.len + tpi - 1) / tpi;
+    }
+    int x = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) b->plan[warp] = x;
+    __syncthreads();
+    int total = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) x += b->plan[w];
+      total += b->plan[w];
+    }
+    const int64_t first = before + x - n;
+    if (n > 0 && want >= first && want < first + n) {
+      a.items[blockIdx.x] = make_item(p, q, want - first, tpi);
+      b->own = 1;
+    }
+    before += total;
+    __syncthreads();
+  }
+  return *reinterpret_cast<volatile uint32_t*>(&b->own) != 0;
+}
+
 template <int DP>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tc(const AttnParams p, const TcArgs a, const __grid_constant__ CUtensorMap mq,
@@ -637,6 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&b->fix, 1);
     b->dead = 0;
+    b->own = 0;
     b->turn = 0;
     mbar_init_fence();
   }
@@ -644,9 +705,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
-  pdl_wait();  // the plan
+  pdl_wait();  // the plan, or what came before
   const int tpt = kTile / p.G;
-  const int64_t total = (int64_t)a.head->items * p.Hkv;
+  const int64_t total =
+      a.self_plan ? (plan_own_item(p, a, b, 2 * tpt) ? blockIdx.x + 1 : 0) : (int64_t)a.head->items * p.Hkv;
   // registers: 168 a thread at launch (384 x 168 = 64,512); a softmax thread
   // holds a row of 128 logits: 2 x 128 x 208 + 128 x 80 = 63,488
   if (warp < 8) {
@@ -668,6 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ------------------------------------------------------------------ planning
 constexpr int kPlanThreads = 1024;
 constexpr int kBuckets = 2560;
+constexpr int kPlanSeqs = 640;
 
 // costs up to 255 keep their own bucket, larger ones their seven leading bits
 __device__ __forceinline__ int bucket_of(int cost) {
@@ -709,25 +772,15 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnParam
   __shared__ int64_t part[32];
   __shared__ int hist[kBuckets];
   __shared__ unsigned long long cost_sum;
+  __shared__ AttnSeq sm_seq[kPlanSeqs];       // the sequences, for batches of up to kPlanSeqs
+  __shared__ int32_t sm_begin[kPlanSeqs];
   const int tid = threadIdx.x;
+  const bool near = p.num_seqs <= kPlanSeqs;
   pdl_launch_dependents();
+  pdl_wait();
   for (int i = tid; i < kBuckets; i += kPlanThreads) hist[i] = 0;
   if (tid == 0) cost_sum = 0;
-  __syncthreads();
-  auto item = [&](const AttnSeq& s, int64_t tile) {
-    AttnItem it;
-    it.tok0 = (int32_t)(s.tok0 + tile * tpi);
-    it.ntok = (int32_t)min((int64_t)tpi, s.len - tile * tpi);
-    it.base = p.block_table ? s.row : (int32_t)s.tok0;
-    it.pos0 = (int32_t)(s.kv_len - s.len + tile * tpi);
-    it.kv_len = (int32_t)s.kv_len;
-    it.kt0 = 0;
-    const int end = max(0, min(it.kv_len, it.pos0 + it.ntok));
-    it.kt1 = (end + kTile - 1) / kTile;
-    it.slot = -1;
-    return it;
-  };
-  // the sequences' tiles, prefix sums in seq_begin; the cost of all
+  // the sequences' tiles and their prefix sums
   int64_t n_tiles = 0;
   for (int base = 0; base < p.num_seqs; base += kPlanThreads) {
     const int s = base + tid;
@@ -739,38 +792,42 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnParam
       n = ((int64_t)q.len + tpi - 1) / tpi;
     }
     const int64_t end = plan_scan(n, part, &total);
-    if (s < p.num_seqs) a.seq_begin[s] = n_tiles + end - n;
+    if (s < p.num_seqs) {
+      if (near) {
+        sm_seq[s] = q;
+        sm_begin[s] = (int32_t)(n_tiles + end - n);
+      } else {
+        a.seq_begin[s] = n_tiles + end - n;
+      }
+    }
     n_tiles += total;
   }
   n_tiles = min(n_tiles, a.max_items);
   __syncthreads();
-  auto seq_of = [&](int64_t x) {
+  auto tile_item = [&](int64_t x) {
     int lo = 0, hi = p.num_seqs - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (a.seq_begin[mid] <= x) lo = mid; else hi = mid - 1;
+      if ((near ? (int64_t)sm_begin[mid] : a.seq_begin[mid]) <= x) lo = mid; else hi = mid - 1;
     }
-    return lo;
+    return near ? make_item(p, sm_seq[lo], x - sm_begin[lo], tpi)
+                : make_item(p, attn_seq(p, lo), x - a.seq_begin[lo], tpi);
   };
   const bool split = a.split_sms > 0 && n_tiles * p.Hkv < 2 * (int64_t)a.split_sms;
   int piece = INT32_MAX;
   if (split) {
     unsigned long long c = 0;
-    for (int64_t x = tid; x < n_tiles; x += kPlanThreads) {
-      const int s = seq_of(x);
-      c += (unsigned long long)item(attn_seq(p, s), x - a.seq_begin[s]).kt1;
-    }
-    atomicAdd(&cost_sum, c);
+    for (int64_t x = tid; x < n_tiles; x += kPlanThreads) c += (unsigned long long)tile_item(x).kt1;
+    if (c) atomicAdd(&cost_sum, c);
     __syncthreads();
     const int64_t parts = (int64_t)kPiecesPerSm * a.split_sms;
     const int64_t share = ((int64_t)cost_sum * p.Hkv + parts - 1) / parts;
     piece = (int)max((int64_t)kMinPiece, share);
   }
-  // pieces of tile x: how many, and each one's key tiles
+  // pieces of an item: how many, and each one's key tiles
   auto pieces = [&](const AttnItem& it) { return it.kt1 <= piece ? 1 : (it.kt1 + piece - 1) / piece; };
   for (int64_t x = tid; x < n_tiles; x += kPlanThreads) {
-    const int s = seq_of(x);
-    const AttnItem it = item(attn_seq(p, s), x - a.seq_begin[s]);
+    const AttnItem it = tile_item(x);
     const int np = pieces(it);
     for (int k = 0; k < np; ++k) {
       const int64_t k0 = (int64_t)it.kt1 * k / np, k1 = (int64_t)it.kt1 * (k + 1) / np;
@@ -778,15 +835,24 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnParam
     }
   }
   __syncthreads();
-  // hist[b] becomes the first place of bucket b: costlier buckets go first
-  int64_t before = 0;
-  for (int base = 0; base < kBuckets; base += kPlanThreads) {
-    const int bkt = kBuckets - 1 - (base + tid);
-    int64_t total;
-    const int64_t n = bkt >= 0 ? hist[bkt] : 0;
-    const int64_t end = plan_scan(n, part, &total);
-    if (bkt >= 0) hist[bkt] = (int)(before + end - n);
-    before += total;
+  // hist[b] becomes the first place of bucket b: costlier buckets go first.
+  // A thread sums kBuckets / kPlanThreads neighbours.
+  constexpr int kPer = (kBuckets + kPlanThreads - 1) / kPlanThreads;
+  int mine[kPer];
+  int64_t n = 0, total;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int bkt = kBuckets - 1 - (tid * kPer + i);
+    mine[i] = bkt >= 0 ? hist[bkt] : 0;
+    n += mine[i];
+  }
+  int64_t at = plan_scan(n, part, &total) - n;
+  const int64_t items = total;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int bkt = kBuckets - 1 - (tid * kPer + i);
+    if (bkt >= 0) hist[bkt] = (int)at;
+    at += mine[i];
   }
   __syncthreads();
   int64_t slots = 0, joins = 0;
@@ -795,23 +861,19 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnParam
     AttnItem it{};
     int np = 0;
     if (x < n_tiles) {
-      const int s = seq_of(x);
-      it = item(attn_seq(p, s), x - a.seq_begin[s]);
+      it = tile_item(x);
       np = pieces(it);
     }
     int64_t slot0 = 0, join = 0;
     if (split) {  // partial results in tile order, whatever the order of the atomics below
-      int64_t total;
-      const int64_t mine = np > 1 ? np : 0;
-      slot0 = slots + plan_scan(mine, part, &total) - mine;
+      const int64_t cut = np > 1 ? np : 0;
+      slot0 = slots + plan_scan(cut, part, &total) - cut;
       slots += total;
       const int64_t one = np > 1;
       join = joins + plan_scan(one, part, &total) - one;
       joins += total;
     }
-    if (np > 1) {
-      a.joins[join] = AttnJoin{it.tok0, it.ntok, (int32_t)slot0, np};
-    }
+    if (np > 1) a.joins[join] = AttnJoin{it.tok0, it.ntok, (int32_t)slot0, np};
     const int kt1 = it.kt1;
     for (int k = 0; k < np; ++k) {
       it.kt0 = (int)((int64_t)kt1 * k / np);
@@ -821,7 +883,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnParam
     }
   }
   if (tid == 0) {
-    a.head->items = (int32_t)before;
+    a.head->items = (int32_t)items;
     a.head->joins = (int32_t)joins;
   }
 }
@@ -898,7 +960,7 @@ int padded(int D) { return D <= 64 ? 64 : 128; }
 struct TcLayout {
   size_t head, seq_begin, items, joins, ml, o, total;
   int64_t max_items, max_pieces;
-  bool split;
+  bool split, self_plan;
 };
 TcLayout layout(const AttnParams& p) {
   TcLayout L{};
@@ -907,6 +969,11 @@ TcLayout layout(const AttnParams& p) {
   // pieces only where the whole batch cannot fill the GPU: at most two per SM
   // are whole items, and the cuts add kPiecesPerSm
   L.split = p.block_table && (p.total_tokens + tpi - 1) / tpi * p.Hkv < 2 * kSplitSms;
+  // a call whose items cannot outnumber the SMs plans for itself, unless long
+  // key ranges are better cut
+  const int64_t keys = p.block_table ? (int64_t)p.max_pages << p.page_shift : p.total_tokens;
+  L.self_plan = L.max_items * p.Hkv <= kSplitSms && (!L.split || keys <= kSelfPlanKeys);
+  if (L.self_plan) L.split = false;
   L.max_pieces = L.split ? (2 + kPiecesPerSm) * (int64_t)kSplitSms / p.Hkv + 1 : 0;
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -916,7 +983,7 @@ TcLayout layout(const AttnParams& p) {
   };
   L.head = take(sizeof(AttnHead));
   L.seq_begin = take(sizeof(int64_t) * p.num_seqs);
-  L.items = take(sizeof(AttnItem) * (size_t)(L.max_items + L.max_pieces));
+  L.items = take(sizeof(AttnItem) * (size_t)(L.self_plan ? L.max_items * p.Hkv : L.max_items + L.max_pieces));
   if (L.split) {
     L.joins = take(sizeof(AttnJoin) * (size_t)(2 * kSplitSms));
     const size_t rows = (size_t)L.max_pieces * p.Hkv * 2 * kTile;
@@ -953,10 +1020,13 @@ cudaError_t launch_dp(const AttnParams& p, const TcLayout& L, char* w, cudaStrea
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(attn_tc<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kBytes);
   if (e != cudaSuccess) return e;
-  attn_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p, a, 2 * tpt);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
   const int64_t most = (L.max_items + L.max_pieces) * p.Hkv;
+  a.self_plan = L.self_plan && L.max_items * p.Hkv <= sms;
+  if (a.self_plan)
+    return launch_maybe_dependent(true, attn_tc<DP>, dim3((unsigned)(L.max_items * p.Hkv)), dim3(kThreads),
+                                  (size_t)S::kBytes, stream, p, a, mq, mk, mv);
+  e = launch_maybe_dependent(true, attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p, a, 2 * tpt);
+  if (e != cudaSuccess) return e;
   e = launch_maybe_dependent(true, attn_tc<DP>, dim3((unsigned)(most < sms ? most : sms)), dim3(kThreads),
                              (size_t)S::kBytes, stream, p, a, mq, mk, mv);
   if (e != cudaSuccess || !L.split) return e;

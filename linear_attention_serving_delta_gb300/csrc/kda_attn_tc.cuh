@@ -20,6 +20,8 @@ namespace kda {
 constexpr int kSplitSms = 152;
 constexpr int kPiecesPerSm = 1;
 constexpr int kMinPiece = 4;
+// Rows of up to this many positions are not worth cutting in a small call
+constexpr int kSelfPlanKeys = 2048;
 
 // One unit of work (for each key head): ntok tokens from packed token tok0 on,
 // the first at position pos0, over the key tiles [kt0, kt1) of a sequence of
@@ -40,6 +42,7 @@ struct TcArgs {
   AttnItem* items;
   int64_t max_items;    // tiles the workspace has room for
   int32_t box_shift;    // log2 of the positions per copy
+  int32_t self_plan;    // every CTA finds its one item
   int32_t o_wide;       // o is 32-byte aligned
   int32_t split_sms;    // > 0: items may be cut into pieces
   AttnJoin* joins;

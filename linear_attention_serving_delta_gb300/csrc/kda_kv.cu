@@ -8,8 +8,15 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int64_t kNoPlan = -1;
+// The first request that names a row is found in shared memory for pools of up
+// to this many rows, in the workspace beyond.
+constexpr int kSharedRows = 4096;
+// A batch of up to kOneLaunchTokens tokens of up to kPlanThreads requests takes
+// its slots in the planning CTA itself, from shared memory: one launch, where a
+// second one costs more than the CTA's few passes.
+constexpr int64_t kOneLaunchTokens = 4096;
 
-// What the planning kernel leaves for the slot map
+// What the planning CTA leaves for the slot map, in the workspace
 struct KvWs {
   int32_t* owner;   // [num_rows] the first request of the batch that names the row
   int64_t* first;   // [N] e_s, or kNoPlan for a skipped or refused request
@@ -17,21 +24,20 @@ struct KvWs {
   int32_t* count;   // [1] pages on the free list before the call
 };
 
-__host__ __device__ KvWs kv_ws(void* ws, int64_t n, int64_t rows) {
+KvWs kv_ws(void* ws, int64_t n) {
   KvWs w;
   char* c = static_cast<char*>(ws);
   w.count = reinterpret_cast<int32_t*>(c);
   w.first = reinterpret_cast<int64_t*>(c + 256);
   w.ctx = w.first + n;
   w.owner = reinterpret_cast<int32_t*>(w.ctx + n);
-  (void)rows;
   return w;
 }
 
-// Inclusive sum over the block's threads (kPlanThreads of them); *total gets
-// the sum of all.  `part` is shared, 32 entries.
+// Inclusive sum over the block's threads; *total gets the sum of all.  `part`
+// is shared, 32 entries, and free again at the next barrier.
 __device__ int64_t block_scan(int64_t x, int64_t* part, int64_t* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
@@ -39,87 +45,85 @@ __device__ int64_t block_scan(int64_t x, int64_t* part, int64_t* total) {
   }
   if (lane == 31) part[warp] = x;
   __syncthreads();
-  if (warp == 0) {
-    int64_t y = part[lane];
+  int64_t y = lane < warps ? part[lane] : 0;  // every warp adds up the warps before it
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t z = __shfl_up_sync(0xffffffffu, y, o);
-      if (lane >= o) y += z;
-    }
-    part[lane] = y;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t z = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) y += z;
   }
-  __syncthreads();
-  if (warp > 0) x += part[warp - 1];
-  *total = part[31];
-  __syncthreads();
-  return x;
+  *total = __shfl_sync(0xffffffffu, y, 31);
+  const int64_t before = __shfl_sync(0xffffffffu, y, warp > 0 ? warp - 1 : 0);
+  return warp > 0 ? x + before : x;
 }
 
 __device__ __forceinline__ int64_t ceil_shift(int64_t x, int s) { return (x + ((int64_t)1 << s) - 1) >> s; }
 
-// The slot of new token t (and, at a page's first token, the page's table entry)
-__device__ void plan_token(const kda_kv_plan_args& a, const KvWs& w, int shift, int64_t t) {
-  const int32_t s = seq_of_token(a.cu_seqlens, a.num_seqs, t);
-  const int64_t b = a.cu_seqlens[s], e = a.cu_seqlens[s + 1];
-  int64_t slot = -1;
-  const int64_t first = w.first[s];
-  if (t >= b && t < e && first != kNoPlan) {
-    const int32_t r = a.rows ? a.rows[s] : s;
-    const int64_t c = w.ctx[s], pos = c + (t - b);
-    const int64_t have = ceil_shift(c, shift), j = pos >> shift;
-    const int64_t off = pos & (((int64_t)1 << shift) - 1);
-    int32_t* entry = a.block_table + (int64_t)r * a.max_pages + j;
-    int32_t page;
-    if (j >= have) {
-      page = a.free_pages[*w.count - 1 - (first + (j - have))];
-      if (off == 0) *entry = page;
-    } else {
-      page = *entry;
-    }
-    if (page >= 0 && page < a.num_pages) slot = ((int64_t)page << shift) + off;
-    else attn_flag(a.status, kFlagBadCache);
+// owner[r] = the first entry of rows[0..n) that is r, for every r named there
+__device__ void find_owners(const int32_t* rows, int32_t n, int32_t num_rows, int32_t* owner) {
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const int32_t r = rows[i];
+    if (r >= 0 && r < num_rows) owner[r] = INT32_MAX;
   }
-  a.slot_map[t] = slot;
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const int32_t r = rows[i];
+    if (r >= 0 && r < num_rows) atomicMin(&owner[r], i);
+  }
+  __syncthreads();
+}
+
+// The slot of new token t of request s (and, at a page's first token, the
+// page's table entry); c: cached before, first: e_s
+__device__ int64_t plan_slot(const kda_kv_plan_args& a, int shift, int64_t count, int64_t t, int32_t s, int64_t b,
+                             int64_t c, int64_t first) {
+  const int32_t r = a.rows ? a.rows[s] : s;
+  const int64_t pos = c + (t - b), have = ceil_shift(c, shift), j = pos >> shift;
+  const int64_t off = pos & (((int64_t)1 << shift) - 1);
+  int32_t* entry = a.block_table + (int64_t)r * a.max_pages + j;
+  int32_t page;
+  if (j >= have) {
+    page = a.free_pages[count - 1 - (first + (j - have))];
+    if (off == 0) *entry = page;
+  } else {
+    page = *entry;
+  }
+  if (page >= 0 && page < a.num_pages) return ((int64_t)page << shift) + off;
+  attn_flag(a.status, kFlagBadCache);
+  return -1;
 }
 
 // One CTA: the pages each request needs, their prefix sum over the batch, and
 // which requests the free list can serve.  Bound by its chain of dependent
-// global loads (row, length, owner), a few microseconds whatever the batch.
-// With `tokens` it goes on to the slots (small batches: one launch).
-__global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(kda_kv_plan_args a, KvWs w, int shift, int tokens) {
-  __shared__ int64_t part[32];
-  const int tid = threadIdx.x;
+// global loads (row, length, page), a few microseconds whatever the batch.
+// kSlots: it goes on to the slots (one request a thread at most).
+template <bool kSlots>
+__global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(kda_kv_plan_args a, KvWs w, int shift) {
+  __shared__ int64_t part[2][32];
+  __shared__ int64_t sm_cu[kSlots ? kPlanThreads + 1 : 1], sm_first[kSlots ? kPlanThreads : 1],
+      sm_ctx[kSlots ? kPlanThreads : 1];
+  extern __shared__ int32_t sm_owner[];
+  const int tid = threadIdx.x, threads = blockDim.x;
   int32_t count = *a.free_count_in;
+  int32_t* owner = a.num_rows <= kSharedRows ? sm_owner : w.owner;
+  if (a.rows) find_owners(a.rows, a.num_seqs, a.num_rows, owner);
   if (count < 0 || count > a.num_pages) {
     if (tid == 0) attn_flag(a.status, kFlagBadCache);
     count = 0;
   }
-  // the first request that names a row owns it
-  if (a.rows) {
-    for (int s = tid; s < a.num_seqs; s += kPlanThreads) {
-      const int32_t r = a.rows[s];
-      if (r >= 0 && r < a.num_rows) w.owner[r] = INT32_MAX;
-    }
-    __syncthreads();
-    for (int s = tid; s < a.num_seqs; s += kPlanThreads) {
-      const int32_t r = a.rows[s];
-      if (r >= 0 && r < a.num_rows) atomicMin(&w.owner[r], s);
-    }
-    __syncthreads();
-  }
   int64_t before = 0, served = 0;
-  for (int base = 0; base < a.num_seqs; base += kPlanThreads) {
+  for (int base = 0; base < a.num_seqs; base += threads) {
     const int s = base + tid;
-    int64_t need = 0, c = 0, len = 0;
+    int64_t need = 0, c = 0, len = 0, b = 0;
     int32_t r = -1;
     bool ok = false;
     if (s < a.num_seqs) {
       r = a.rows ? a.rows[s] : s;
-      const int64_t b = a.cu_seqlens[s], e = a.cu_seqlens[s + 1];
+      b = a.cu_seqlens[s];
+      const int64_t e = a.cu_seqlens[s + 1];
       len = e - b;
       if (b < 0 || e < b || e > a.total_tokens || (s == 0 && b != 0)) {
         attn_flag(a.status, kFlagBadSeqlens);
-      } else if (r >= a.num_rows || (r >= 0 && a.rows && *(volatile int32_t*)&w.owner[r] != s)) {
+      } else if (r >= a.num_rows || (r >= 0 && a.rows && owner[r] != s)) {
         attn_flag(a.status, kFlagBadCache);
         r = -1;  // the owner's length stays as the owner leaves it
       } else if (r >= 0) {
@@ -128,60 +132,73 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(kda_kv_plan_args 
         if (!ok) attn_flag(a.status, kFlagBadCache);
       }
       if (ok) need = ceil_shift(c + len, shift) - ceil_shift(c, shift);
+      if (kSlots) {
+        sm_cu[s] = b;
+        if (s + 1 == a.num_seqs) sm_cu[s + 1] = e;
+      }
     }
-    int64_t total;
-    const int64_t end = before + block_scan(need, part, &total);
+    int64_t total, all;
+    const int64_t end = before + block_scan(need, part[0], &total);
     if (s < a.num_seqs) {
       if (ok && need > 0 && end > count) {
         ok = false;
         attn_flag(a.status, kFlagNoPages);
       }
-      w.first[s] = ok ? end - need : kNoPlan;
-      w.ctx[s] = c;
+      const int64_t first = ok ? end - need : kNoPlan;
+      if (kSlots) {
+        sm_first[s] = first;
+        sm_ctx[s] = c;
+      } else {
+        w.first[s] = first;
+        w.ctx[s] = c;
+      }
       if (ok) a.kv_lens_out[r] = c + len;
       else if (r >= 0 && a.kv_lens_out != a.kv_lens_in) a.kv_lens_out[r] = a.kv_lens_in[r];
     }
-    // the served ones that need pages come first among those that do
-    block_scan(ok ? need : 0, part, &total);
-    served += total;
-    int64_t all;
-    block_scan(need, part, &all);
-    before += all;
+    block_scan(ok ? need : 0, part[1], &all);
+    before += total;
+    served += all;
+    if (base + threads < a.num_seqs) __syncthreads();  // `part` again
   }
   if (tid == 0) {
-    *w.count = count;
     *a.free_count_out = count - (int32_t)served;
+    if (!kSlots) *w.count = count;
   }
-  if (!tokens) return;
-  __syncthreads();
-  for (int64_t t = tid; t < a.total_tokens; t += kPlanThreads) plan_token(a, w, shift, t);
+  if constexpr (kSlots) {
+    __syncthreads();
+    for (int64_t t = tid; t < a.total_tokens; t += threads) {
+      // the request of the token: a decode batch has one token each
+      int32_t s = t < a.num_seqs && sm_cu[t] == t && sm_cu[t + 1] > t ? (int32_t)t : seq_of_token(sm_cu, a.num_seqs, t);
+      const int64_t b = sm_cu[s], first = sm_first[s];
+      a.slot_map[t] = t >= b && t < sm_cu[s + 1] && first != kNoPlan
+                          ? plan_slot(a, shift, count, t, s, b, sm_ctx[s], first)
+                          : -1;
+    }
+  }
 }
 
 __global__ void __launch_bounds__(256) kv_slots_kernel(kda_kv_plan_args a, KvWs w, int shift) {
   const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (t >= a.total_tokens) return;
+  const int32_t s = seq_of_token(a.cu_seqlens, a.num_seqs, t);
+  const int64_t b = a.cu_seqlens[s], e = a.cu_seqlens[s + 1];
   pdl_wait();
-  if (t < a.total_tokens) plan_token(a, w, shift, t);
+  const int64_t first = w.first[s];
+  a.slot_map[t] = t >= b && t < e && first != kNoPlan ? plan_slot(a, shift, *w.count, t, s, b, w.ctx[s], first) : -1;
 }
 
 __global__ void __launch_bounds__(kPlanThreads) kv_release_kernel(kda_kv_release_args a, KvWs w, int shift) {
-  __shared__ int64_t part[32];
+  __shared__ int64_t part[2][32];
+  extern __shared__ int32_t sm_owner[];
   const int tid = threadIdx.x;
   int64_t count = *a.free_count;
+  int32_t* owner = a.num_rows <= kSharedRows ? sm_owner : w.owner;
   __syncthreads();
   if (count < 0 || count > a.num_pages) {
     if (tid == 0) attn_flag(a.status, kFlagBadCache);
     return;
   }
-  for (int i = tid; i < a.num_release; i += kPlanThreads) {
-    const int32_t r = a.rows[i];
-    if (r >= 0 && r < a.num_rows) w.owner[r] = INT32_MAX;
-  }
-  __syncthreads();
-  for (int i = tid; i < a.num_release; i += kPlanThreads) {
-    const int32_t r = a.rows[i];
-    if (r >= 0 && r < a.num_rows) atomicMin(&w.owner[r], i);
-  }
-  __syncthreads();
+  find_owners(a.rows, a.num_release, a.num_rows, owner);
   for (int base = 0; base < a.num_release; base += kPlanThreads) {
     const int i = base + tid;
     int64_t n = 0;
@@ -191,7 +208,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_release_kernel(kda_kv_release
       if (r >= a.num_rows) {
         attn_flag(a.status, kFlagBadCache);
         r = -1;
-      } else if (r >= 0 && *(volatile int32_t*)&w.owner[r] == i) {
+      } else if (r >= 0 && owner[r] == i) {
         const int64_t len = a.kv_lens[r];
         if (len < 0 || len > ((int64_t)a.max_pages << shift)) {
           attn_flag(a.status, kFlagBadCache);
@@ -204,7 +221,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_release_kernel(kda_kv_release
       }
     }
     int64_t total;
-    int64_t at = count + block_scan(n, part, &total) - n;
+    const int64_t at = count + block_scan(n, part[0], &total) - n;
     if (n > 0 && at + n > a.num_pages) {
       attn_flag(a.status, kFlagBadCache);
       r = -1;
@@ -214,8 +231,9 @@ __global__ void __launch_bounds__(kPlanThreads) kv_release_kernel(kda_kv_release
       a.kv_lens[r] = 0;
       for (int64_t j = 0; j < n; ++j) a.free_pages[at + j] = a.block_table[(int64_t)r * a.max_pages + j];
     }
-    block_scan(n, part, &total);
+    block_scan(n, part[1], &total);
     count += total;
+    __syncthreads();  // `part` again
   }
   if (tid == 0) *a.free_count = (int32_t)count;
 }
@@ -252,9 +270,7 @@ int shift_of(int32_t page_size) {
   return s;
 }
 
-// Batches up to this many tokens take their slots in the planning CTA itself:
-// one launch, where a second one costs more than the CTA's few passes.
-constexpr int64_t kOneLaunchTokens = 4096;
+size_t owner_bytes(int32_t rows) { return rows <= kSharedRows ? (size_t)rows * sizeof(int32_t) : 0; }
 
 }  // namespace
 
@@ -263,19 +279,21 @@ size_t kv_plan_workspace(int64_t n, int64_t rows) {
 }
 
 cudaError_t launch_kv_plan(const kda_kv_plan_args& a, void* ws, cudaStream_t stream) {
-  const KvWs w = kv_ws(ws, a.num_seqs, a.num_rows);
+  const KvWs w = kv_ws(ws, a.num_seqs);
   const int shift = shift_of(a.page_size);
-  const int one = a.total_tokens <= kOneLaunchTokens;
-  kv_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a, w, shift, one);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || one) return e;
+  const bool one = a.total_tokens <= kOneLaunchTokens && a.num_seqs <= kPlanThreads;
+  const int64_t most = one && a.total_tokens > a.num_seqs ? a.total_tokens : a.num_seqs;
+  const int threads = most >= kPlanThreads ? kPlanThreads : (int)(most + 31) / 32 * 32;
+  (one ? kv_plan_kernel<true> : kv_plan_kernel<false>)<<<1, threads, owner_bytes(a.num_rows), stream>>>(a, w, shift);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || one || a.total_tokens == 0) return e;
   return launch_maybe_dependent(true, kv_slots_kernel, dim3((unsigned)((a.total_tokens + 255) / 256)), dim3(256), 0,
                                 stream, a, w, shift);
 }
 
 cudaError_t launch_kv_release(const kda_kv_release_args& a, void* ws, cudaStream_t stream) {
   if (a.num_release == 0) return cudaSuccess;
-  kv_release_kernel<<<1, kPlanThreads, 0, stream>>>(a, kv_ws(ws, 0, a.num_rows), shift_of(a.page_size));
+  kv_release_kernel<<<1, kPlanThreads, owner_bytes(a.num_rows), stream>>>(a, kv_ws(ws, 0), shift_of(a.page_size));
   return cudaGetLastError();
 }
 

@@ -855,18 +855,6 @@ def _shape(name, t, want):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(want)}")
 
 
-def _launch(fn, what, device, args, workspace, stream):
-    """Calls a C entry on ``stream`` (None: the current stream of the tensors'
-    device) with that device current."""
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return _launch(fn, what, device, args, workspace, stream)
-    if workspace is None:
-        _check(fn(ctypes.byref(args), _stream(stream)), what)
-    else:
-        _check(fn(ctypes.byref(args), workspace.data_ptr(), workspace.numel(), _stream(stream)), what)
-
-
 class _CacheCall:
     """What the planned calls share: the argument block, the workspace and the
     status word are made once; ``run()`` only launches kernels."""
@@ -887,9 +875,22 @@ class _CacheCall:
                 # the call itself reports why, before any launch
                 _check(self._fn(ctypes.byref(args), None, 0, None), self._name)
             self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        # the C arguments before the stream, made once
+        self._call = (ctypes.byref(args),)
+        if self.workspace is not None:
+            self._call += (self.workspace.data_ptr(), self.workspace.numel())
 
     def run(self, stream=None):
-        _launch(self._fn, self._name, self._device, self.args, self.workspace, stream)
+        """Launches on ``stream`` (None: the current stream of the tensors' device)."""
+        index = self._device.index
+        if index != torch.cuda.current_device():
+            with torch.cuda.device(index):
+                return self.run(stream)
+        # (the raw handle: torch.cuda.current_stream() alone costs 3 us)
+        s = torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
+        status = self._fn(*self._call, s)
+        if status != KDA_OK:
+            raise KdaError(status, self._name)
         return self
 
     def device_status(self) -> int:
