@@ -32,7 +32,7 @@ using namespace tc;
 constexpr int kWarps = 4;                      // consumers
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kMaxRows = 16;
-constexpr int kMinTiles = 4;                   // shortest stretch of a CTA
+constexpr int kMinTiles = 1;                   // shortest stretch of a CTA
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazyLog2 = 8.f;  // how far the maximum may rise before O is rescaled
 
@@ -75,7 +75,10 @@ struct Tail {
   Tile tile[8];
   float2 ml[kWarps][kMaxRows];
   int64_t sum[kWarps + 1];
-  int64_t found[2];
+  int64_t found;   // where in its sequence's tiles the stretch starts
+  int32_t found_at;
+  int32_t pad2;
+  AttnSeq found_seq;
 };
 static_assert(sizeof(Tail) <= 2048, "tail block");
 
@@ -91,6 +94,11 @@ struct RowsArgs {
   int32_t q_shift;   // log2 of a block's tokens
   int32_t parts;     // blocks of a token's G heads
 };
+
+// a / b for a >= 0, b > 0: the quick way where both are small
+__device__ __forceinline__ int64_t div_any(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
 
 // The blocks of a sequence for one head (part): n of them, block i with
 // tiles(i) = max(1, ceil((pos + (i + 1) q) / KT)) key tiles, q = 2^q_shift
@@ -115,9 +123,14 @@ struct Blocks {
   __device__ __forceinline__ int64_t ones() const {  // blocks before the formula passes 1
     return min(n, max((int64_t)0, ((int64_t)1 << rs) - d));
   }
-  __device__ __forceinline__ int64_t total() const { return ones() + sum(d + n) - sum(d + ones()); }
+  __device__ __forceinline__ int64_t total() const { return n == 1 ? tiles(0) : ones() + sum(d + n) - sum(d + ones()); }
   // the block that holds tile r of the head, and r's index in it
   __device__ void find(int64_t r, int64_t* block, int* tile) const {
+    if (n == 1) {
+      *block = 0;
+      *tile = (int)r;
+      return;
+    }
     const int64_t o = ones();
     if (r < o) {
       *block = r;
@@ -126,10 +139,11 @@ struct Blocks {
     }
     const int64_t y = r - o + sum(d + o);
     // largest t with R t (t - 1) / 2 <= y
-    int64_t t = (int64_t)((1.0 + sqrt(1.0 + 8.0 * (double)y / (double)(1 << rs))) / 2.0);
+    int64_t t = (int64_t)((1.f + sqrtf(1.f + 8.f * (float)y / (float)(1 << rs))) * 0.5f);
+    if (t < 1) t = 1;
     while ((t * (t - 1) / 2 << rs) > y) --t;
     while ((t * (t + 1) / 2 << rs) <= y) ++t;
-    const int64_t z = y - (t * (t - 1) / 2 << rs), m = z / t;
+    const int64_t z = y - (t * (t - 1) / 2 << rs), m = div_any(z, t);
     *block = (t << rs) + m - d;
     *tile = (int)(z - m * t);
   }
@@ -710,22 +724,27 @@ __global__ void __launch_bounds__(kThreads, Shape<T, DP>::CTAS)
     mbar_init(&b->join[0], kWarps);
     mbar_init(&b->join[1], kWarps);
     b->dead = 0;
-    b->found[0] = -1;
     mbar_init_fence();
+  }
+  if (tid == 32) {
+    prefetch_map(&mk);
+    prefetch_map(&mv);
+    if (sizeof(T) == 2) prefetch_map(&mq);
   }
   pdl_wait();
   pdl_launch_dependents();  // the join's launch overlaps the work (it waits for the end of it)
 
   // the line of work: its length, this CTA's stretch, and where that starts
-  int64_t W = 0, u0 = 0, u1 = 0, before = 0;
-  int64_t first_seq = -1, first_off = 0;
+  int64_t u0 = 0, u1 = 0, per = 0;
+  const bool one = p.num_seqs <= kThreads;  // the batch in one go: its tiles are counted once
   for (int pass = 0; pass < 2; ++pass) {
-    before = 0;
+    int64_t before = 0;
     for (int base = 0; base < p.num_seqs; base += kThreads) {
       const int s = base + tid;
       int64_t n = 0;
+      AttnSeq q{};
       if (s < p.num_seqs) {
-        const AttnSeq q = attn_seq(p, s);
+        q = attn_seq(p, s);
         if (pass == 0 && q.flag && blockIdx.x == 0) attn_flag(p.status, q.flag);
         if (q.len > 0) n = Blocks<KT>(q, a.q_shift).total() * p.Hkv * a.parts;
       }
@@ -744,52 +763,54 @@ __global__ void __launch_bounds__(kThreads, Shape<T, DP>::CTAS)
         if (w < warp) x += b->sum[w];
         total += b->sum[w];
       }
-      if (pass == 1 && n > 0 && u0 >= before + x - n && u0 < before + x) {
-        b->found[0] = s;
-        b->found[1] = u0 - (before + x - n);
+      if (pass == 0 && one) {
+        const int64_t share = div_any(total + gridDim.x - 1, gridDim.x);
+        per = share > kMinTiles ? share : kMinTiles;
+        u0 = min(total, per * blockIdx.x);
+        u1 = min(total, u0 + per);
+      }
+      if ((pass == 1 || one) && n > 0 && u0 >= before + x - n && u0 < before + x) {
+        b->found = u0 - (before + x - n);
+        b->found_at = s;
+        b->found_seq = q;
       }
       before += total;
       if (pass == 1 && u0 < before) break;
     }
-    if (pass == 0) {
-      W = before;
-      const int64_t share = (W + gridDim.x - 1) / gridDim.x;
-      const int64_t per = share > kMinTiles ? share : kMinTiles;
-      u0 = min(W, per * blockIdx.x);
-      u1 = min(W, u0 + per);
-      first_off = per;
-      if (u0 == u1) {
-        if (tid == 0) a.joins[blockIdx.x].parts = 0;
-        return;
-      }
+    if (pass == 0 && !one) {
+      const int64_t share = div_any(before + gridDim.x - 1, gridDim.x);
+      per = share > kMinTiles ? share : kMinTiles;
+      u0 = min(before, per * blockIdx.x);
+      u1 = min(before, u0 + per);
     }
+    if (u0 == u1) {
+      if (tid == 0) a.joins[blockIdx.x].parts = 0;
+      return;
+    }
+    if (one) break;
   }
   __syncthreads();
-  const int64_t per = first_off;
-  first_seq = b->found[0];
-  first_off = b->found[1];
+  const int64_t first_off = b->found;
 
   if (warp == kWarps) {
     // ---- copies
-    int base = (int)first_seq, cur = 0;  // 32 sequences at a time, one a lane
+    int base = b->found_at, cur = 0;  // sequences behind the first: 32 at a time, one a lane
     AttnSeq mine{};
     auto fetch = [&](int at) {
       base = at;
       mine = AttnSeq{};
       if (at + lane < p.num_seqs) mine = attn_seq(p, at + lane);
     };
-    fetch(base);
-    AttnSeq sq;
+    AttnSeq sq = b->found_seq;
     auto seq = [&] {
       sq.tok0 = __shfl_sync(0xffffffffu, mine.tok0, cur);
       sq.len = __shfl_sync(0xffffffffu, mine.len, cur);
       sq.kv_len = __shfl_sync(0xffffffffu, mine.kv_len, cur);
       sq.row = __shfl_sync(0xffffffffu, mine.row, cur);
     };
-    seq();
     Blocks<KT> bl(sq, a.q_shift);
     const int64_t per_head = bl.total();
-    int head = (int)(first_off / per_head), tile;  // head: key head * parts + part
+    int head = (int)div_any(first_off, per_head), tile;  // head: key head * parts + part
     int64_t block;
     bl.find(first_off - head * per_head, &block, &tile);
     int n = bl.tiles(block);
@@ -840,7 +861,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, DP>::CTAS)
         if (last && (seg_tile0 > 0 || tile + 1 < n)) {
           t.slot = 2 * (int)blockIdx.x + (seg_tile0 == 0);
           if (seg_tile0 == 0)  // the block starts here: its other parts are the next stretches' first ones
-            a.joins[blockIdx.x] = RowsJoin{(int)((u - tile + n - 1) / per - blockIdx.x + 1), t.tok0, t.head0, t.rows, t.gb};
+            a.joins[blockIdx.x] = RowsJoin{(int)div_any(u - tile + n - 1, per) - (int)blockIdx.x + 1, t.tok0, t.head0, t.rows, t.gb};
         }
         b->tile[st] = t;
         const uint32_t bytes = (uint32_t)nb * box_bytes * 2 * S::NB +
@@ -859,6 +880,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, DP>::CTAS)
           tma_4d(dst + c * S::kBlock + lane * box_bytes, &mk, ch, kvh, c2, c3, &b->full[st]);
           tma_4d(dst + (S::NB + c) * S::kBlock + lane * box_bytes, &mv, ch, kvh, c2, c3, &b->full[st]);
         }
+      if (k == 0) fetch(base);  // (the first sequence again, and those behind it)
       // the next tile of the line
       seg_first = last;
       if (++tile == n) {

@@ -701,6 +701,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     b->turn = 0;
     mbar_init_fence();
   }
+  if (threadIdx.x == 32) {
+    prefetch_map(&mq);
+    prefetch_map(&mk);
+    prefetch_map(&mv);
+  }
   if (warp == 9) tmem_alloc(&b->tmem, kTmemCols);
   fence_before_sync();
   __syncthreads();

@@ -154,6 +154,10 @@ __device__ __forceinline__ void tma_4d(void* dst, const CUtensorMap* m, int x, i
       : "memory");
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+}
+
 // 2^x with the hardware approximation (relative error about 2^-22), 0 below 2^-126
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
