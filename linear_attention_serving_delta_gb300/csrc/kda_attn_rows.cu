@@ -1,12 +1,12 @@
-// kda_attn_rows.cu -- attention by blocks of at most 16 rows: single tokens (or
+// kda_attn_rows.cu -- attention by blocks of at most 16 rows (32 in fp32): single tokens (or
 // a few) over the paged cache in both types, and everything in fp32 or with
 // heads of 256 channels.
 //
 // A block's rows are those of one key head: row = token * gb + head, with gb
-// = min(G, 16) of its G query heads and as many tokens (a power of two) as fit
-// 16 rows.  For single tokens that reads every cached key and value once and
+// = min(G, 16 or 32) of its G query heads and as many tokens (a power of two) as fit
+// a block.  For single tokens that reads every cached key and value once and
 // does little with them, so the kernel is a stream, bound by HBM; fp32 blocks
-// of a prompt are bound by the FMA units instead.
+// of a prompt are bound by the splitting of their operands instead.
 //
 // The key tiles of all blocks form one line of work, sequence after sequence,
 // head after head, and every CTA of a grid that fills the GPU takes an equal
@@ -21,7 +21,7 @@
 // 16 keys a warp on mma.sync (a 128-row tcgen05 tile would be 7/8 padding for
 // single tokens, and the tensor cores wait for memory either way); the
 // weights are rounded to bf16, as P V's operand.  fp32: the same with every
-// operand in three bf16 parts; 8 keys a warp on FMAs for heads of 256.
+// operand in three bf16 parts.
 #include "kda_attn_tc.cuh"
 
 namespace kda {
@@ -31,31 +31,32 @@ using namespace tc;
 
 constexpr int kWarps = 4;                      // consumers
 constexpr int kThreads = 32 * (kWarps + 1);
-constexpr int kMaxRows = 16;
+constexpr int kMaxRows = 32;                   // most rows of a block (16, or 32 in fp32)
 constexpr int kMinTiles = 1;                   // shortest stretch of a CTA
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazyLog2 = 8.f;  // how far the maximum may rise before O is rescaled
 
-template <typename T, int DP>
+template <typename T, int DP, int R>
 struct Shape {
   static constexpr int KT = sizeof(T) == 2 || DP <= 128 ? 64 : 32;  // keys of a tile
   static constexpr int NB = DP * (int)sizeof(T) / 128;     // 128-byte blocks of a row
   static constexpr uint32_t kBlock = KT * 128;
   static constexpr uint32_t kKV = 2 * NB * kBlock;         // K, then V; also the joining warps' scratch
-  static constexpr uint32_t kQBlock = kMaxRows * 128;      // bf16: q of a pair, with its first tile
+  static constexpr uint32_t kQBlock = R * 128;      // bf16: q of a pair, with its first tile
   static constexpr uint32_t kStage = kKV + (sizeof(T) == 2 ? NB * kQBlock : 0);
   static constexpr int CTAS = kKV <= 32768 ? 2 : 1;
   static constexpr int kStages = kKV <= 8192 ? 8 : kKV <= 16384 ? 5 : 3;
   static constexpr uint32_t kQ = kStages * kStage;         // fp32: the pair's q rows, plain
-  static constexpr uint32_t kQPlane = (DP + 63) / 64 * kMaxRows * 128;  // fp32: a bf16 part of q (split3)
-  static constexpr uint32_t kTail = kQ + (sizeof(T) == 2 ? 0 : DP <= 128 ? 3 * kQPlane : kMaxRows * DP * 4);
+  static constexpr uint32_t kQPlane = (DP + 63) / 64 * kQBlock;  // fp32: a bf16 part of q (split3)
+  static constexpr uint32_t kTail = kQ + (sizeof(T) == 2 ? 0 : 3 * kQPlane);
   static constexpr uint32_t kBytes = kTail + 2048 + 1024;  // barriers; slack to align the base
 };
-static_assert(Shape<__nv_bfloat16, 128>::kKV >= kWarps * kMaxRows * 128 * 4, "the warps' outputs fit a stage");
-static_assert(Shape<float, 128>::kKV >= kWarps * kMaxRows * 128 * 4, "the warps' outputs fit a stage");
-static_assert(2 * (Shape<__nv_bfloat16, 128>::kBytes + 1024) <= 233472, "two CTAs per SM");
-static_assert(2 * (Shape<float, 64>::kBytes + 1024) <= 233472, "two CTAs per SM");
-static_assert(Shape<float, 256>::kBytes <= 232448 && Shape<float, 128>::kBytes <= 232448 && Shape<__nv_bfloat16, 256>::kBytes <= 232448, "one CTA");
+template <typename T, int DP, int R>
+constexpr bool shape_ok() {
+  using S = Shape<T, DP, R>;
+  return S::kKV >= kWarps * R * DP * 4                                  // the warps' outputs fit a stage
+         && S::CTAS * (S::kBytes + 1024) <= 233472 && S::kBytes <= 232448;
+}
 
 // A tile in the ring, for its consumers
 struct Tile {
@@ -88,8 +89,8 @@ struct RowsJoin {
 };
 struct RowsArgs {
   RowsJoin* joins;   // [grid]
-  float2* ml;        // [2 grid][16]
-  float* o;          // [2 grid][16][DP]
+  float2* ml;        // [2 grid][kMaxRows]
+  float* o;          // [2 grid][kMaxRows][DP]
   int32_t box_shift; // log2 of the positions per copy
   int32_t q_shift;   // log2 of a block's tokens
   int32_t parts;     // blocks of a token's G heads
@@ -165,20 +166,33 @@ __device__ __forceinline__ void mma16816(float* d, const uint32_t* a, uint32_t b
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// the same over 8 keys, and by the number of keys
+__device__ __forceinline__ void mma1688(float* d, const uint32_t* a, uint32_t b0) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(b0));
+}
+template <int NT>
+__device__ __forceinline__ void mma_keys(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  if constexpr (NT == 2) mma16816(d, a, b0, b1);
+  else mma1688(d, a, b0);
+}
 // byte offset of 16-byte piece c of row r in swizzled blocks of `block` bytes
 __device__ __forceinline__ uint32_t sw_off(int r, int c, uint32_t block) {
   return (uint32_t)(c >> 3) * block + (uint32_t)r * 128u + (uint32_t)(((c & 7) ^ (r & 7)) << 4);
 }
 
 // The weights of key k for the two rows of a lane, from the accumulator layout
-// p[n][e] of a 16 x 16 tile (every lane of the warp calls)
+// p[n][e] of a 16 x 8 NT tile (every lane of the warp calls)
+template <int NT>
 __device__ __forceinline__ void weight_of(const float* p, int k, int lane, float* w) {
   const int src = (lane & ~3) | ((k & 7) >> 1);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     w[h] = 0.f;
 #pragma unroll
-    for (int z = 0; z < 4; ++z) {  // its register, by a fixed index
+    for (int z = 0; z < 2 * NT; ++z) {  // its register, by a fixed index
       const int n = z >> 1, e = z & 1;
       const float c = __shfl_sync(0xffffffffu, p[4 * n + 2 * h + e], src);
       if (n == (k >> 3) && e == (k & 1)) w[h] = c;
@@ -190,7 +204,8 @@ __device__ __forceinline__ bool finite(float x) { return (__float_as_uint(x) & 0
 // One quarter-tile's work and its running state, bf16
 template <int DP>
 struct RowsBf16 {
-  using S = Shape<__nv_bfloat16, DP>;
+  static constexpr int kRows = 16;
+  using S = Shape<__nv_bfloat16, DP, kRows>;
   static constexpr int NK = DP / 16, NV = DP / 8;
   uint32_t q[NK][4];
   float o[NV][4], m[2], l[2];
@@ -293,7 +308,7 @@ struct RowsBf16 {
       const float* p0 = &s[0][0];
       for (int k = 0; k < live; ++k) {
         float w[2];
-        weight_of(p0, k, lane, w);
+        weight_of<2>(p0, k, lane, w);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
           const uint32_t y = *reinterpret_cast<const uint32_t*>(vs + sw_off(16 * warp + k, v, S::kBlock) + 4 * (lane & 3));
@@ -375,29 +390,36 @@ __device__ __forceinline__ Split split3(float x, float y) {
   return s;
 }
 
-// The same in fp32, up to 128 channels, on the same instructions: every operand
-// is split into three bf16 parts (split3) and a product takes the six pairs
-// that matter, h h, h m, m h, h l, l h and m m; what is left out is below
-// 2^-22 of it, as an fp32 rounding or two.
-template <int DP>
-struct RowsF32x3 {
-  using S = Shape<float, DP>;
-  static constexpr int NK = DP / 16, NV = DP / 8;
-  float o[NV][4], m[2], l[2];
+// The same in fp32 on the same instructions: every operand is split into three
+// bf16 parts (split3) and a product takes the six pairs that matter, h h, h m,
+// m h, h l, l h and m m; what is left out is below 2^-22 of it, as an fp32
+// rounding or two.  KW keys a warp; MT tiles of 16 rows, which share the
+// splitting of K and V (more work than the products).
+template <int DP, int KW, int MT>
+struct RowsF32 {
+  static constexpr int kRows = 16 * MT;
+  using S = Shape<float, DP, kRows>;
+  static_assert(KW * kWarps == S::KT, "a warp's share of a tile");
+  static constexpr int NK = DP / 16, NV = DP / 8, NT = KW / 8;
+  float o[MT][NV][4], m[MT][2], l[MT][2];
 
   __device__ void start(const char*, float*, int) {
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
+    for (int t = 0; t < MT; ++t) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[v][e] = 0.f;
-    m[0] = m[1] = -INFINITY;
-    l[0] = l[1] = 0.f;
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[t][v][e] = 0.f;
+      m[t][0] = m[t][1] = -INFINITY;
+      l[t][0] = l[t][1] = 0.f;
+    }
   }
   // the block's q rows, split, by all consumers; rows it does not have are zeros
   static __device__ void load_q(const AttnParams& p, const Tile& t, float* qs, int tid) {
     const float* q = static_cast<const float*>(p.q);
     char* base = reinterpret_cast<char*>(qs);
-    for (int i = tid; i < kMaxRows * DP / 2; i += 32 * kWarps) {
+#pragma unroll 4
+    for (int i = tid; i < kRows * DP / 2; i += 32 * kWarps) {
       const int r = i / (DP / 2), c = 2 * (i % (DP / 2));
       float2 x = make_float2(0.f, 0.f);
       if (r < t.rows && c < p.D)
@@ -411,17 +433,17 @@ struct RowsF32x3 {
   }
 
   __device__ void step(char* stage, const float* qs, const Tile& t, float sc, int warp, int lane) {
-    const int x0 = t.x0 + 16 * warp;  // this warp's keys
+    const int x0 = t.x0 + KW * warp;  // this warp's keys
     if (x0 >= t.end) return;
     char* vs = stage + S::NB * S::kBlock;
-    const int live = min(16, t.end - x0);
+    const int live = min(KW, t.end - x0);
     bool poison = false;
-    const bool masked = x0 + 15 > t.pos0;
+    const bool masked = x0 + KW - 1 > t.pos0;
     if (masked) {
       // rows of V behind the block's last key to zero; non-finite values that some row may not attend
-      for (int i = lane; i < 16 * S::NB * 8; i += 32) {
+      for (int i = lane; i < KW * S::NB * 8; i += 32) {
         const int r = i / (S::NB * 8), c = i % (S::NB * 8);
-        uint4* x = reinterpret_cast<uint4*>(vs + sw_off(16 * warp + r, c, S::kBlock));
+        uint4* x = reinterpret_cast<uint4*>(vs + sw_off(KW * warp + r, c, S::kBlock));
         if (r >= live) {
           *x = make_uint4(0, 0, 0, 0);
         } else if (t.rows > t.gb) {
@@ -433,284 +455,182 @@ struct RowsF32x3 {
       poison = __any_sync(0xffffffffu, poison);
     }
     const int r0 = lane >> 2, q2 = lane & 3;
-    float s[2][4], sx[2][4];  // h h apart from the smaller products
+    float s[MT][NT][4], sx[MT][NT][4];  // h h apart from the smaller products
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[n][e] = sx[n][e] = 0.f;
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[i][n][e] = sx[i][n][e] = 0.f;
     const uint32_t qa = smem_u32(qs);
 #pragma unroll 2
     for (int k = 0; k < NK; ++k) {
-      uint32_t ah[4], am[4], al[4];
-      const uint32_t off = sw_off((lane & 7) + ((lane >> 3) & 1) * 8, 2 * k + (lane >> 4), S::kQBlock);
-      ldsm4(ah, qa + off);
-      ldsm4(am, qa + S::kQPlane + off);
-      ldsm4(al, qa + 2 * S::kQPlane + off);
+      uint32_t ah[MT][4], am[MT][4], al[MT][4];
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        const int row = 16 * warp + 8 * n + r0;
+      for (int i = 0; i < MT; ++i) {
+        const uint32_t off = sw_off(16 * i + (lane & 7) + ((lane >> 3) & 1) * 8, 2 * k + (lane >> 4), S::kQBlock);
+        ldsm4(ah[i], qa + off);
+        ldsm4(am[i], qa + S::kQPlane + off);
+        ldsm4(al[i], qa + 2 * S::kQPlane + off);
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int row = KW * warp + 8 * n + r0;
         const float2 x = *reinterpret_cast<const float2*>(stage + sw_off(row, 4 * k + (q2 >> 1), S::kBlock) + (q2 & 1) * 8);
         const float2 y = *reinterpret_cast<const float2*>(stage + sw_off(row, 4 * k + 2 + (q2 >> 1), S::kBlock) + (q2 & 1) * 8);
         const Split b0 = split3(x.x, x.y), b1 = split3(y.x, y.y);
-        mma16816(s[n], ah, b0.h, b1.h);
-        mma16816(sx[n], ah, b0.l, b1.l);
-        mma16816(sx[n], al, b0.h, b1.h);
-        mma16816(sx[n], am, b0.m, b1.m);
-        mma16816(sx[n], ah, b0.m, b1.m);
-        mma16816(sx[n], am, b0.h, b1.h);
-      }
-    }
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[n][e] += sx[n][e];
-    const int c0 = 2 * q2;
-    int limit[2];
-    if (masked) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) limit[h] = min(t.end - 1, t.pos0 + (r0 + 8 * h) / t.gb) - x0;
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (8 * n + c0 + (e & 1) > limit[e >> 1]) s[n][e] = -INFINITY;
-    }
-    float x[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      x[h] = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
-      x[h] = fmaxf(x[h], __shfl_xor_sync(0xffffffffu, x[h], 1));
-      x[h] = sc * fmaxf(x[h], __shfl_xor_sync(0xffffffffu, x[h], 2));
-    }
-    const bool up = x[0] > m[0] || x[1] > m[1];
-    if (__any_sync(0xffffffffu, up)) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (!(x[h] > m[h])) x[h] = m[h];
-        const float f = m[h] == -INFINITY ? 1.f : exp2f(m[h] - x[h]);
-        m[h] = x[h];
-        l[h] *= f;
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          o[v][2 * h] *= f;
-          o[v][2 * h + 1] *= f;
+        for (int i = 0; i < MT; ++i) {
+          mma16816(s[i][n], ah[i], b0.h, b1.h);
+          mma16816(sx[i][n], ah[i], b0.l, b1.l);
+          mma16816(sx[i][n], al[i], b0.h, b1.h);
+          mma16816(sx[i][n], am[i], b0.m, b1.m);
+          mma16816(sx[i][n], ah[i], b0.m, b1.m);
+          mma16816(sx[i][n], am[i], b0.h, b1.h);
         }
       }
     }
-    const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+    int limit[MT][2];
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+    for (int i = 0; i < MT; ++i) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        s[n][e] = exp2f(fmaf(s[n][e], sc, -ref[e >> 1]));
-        l[e >> 1] += s[n][e];
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[i][n][e] += sx[i][n][e];
+      if (masked) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) limit[i][h] = min(t.end - 1, t.pos0 + (16 * i + r0 + 8 * h) / t.gb) - x0;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (8 * n + 2 * q2 + (e & 1) > limit[i][e >> 1]) s[i][n][e] = -INFINITY;
       }
-    if (masked && poison) {  // as for bf16
-      const float* p0 = &s[0][0];
-      for (int k = 0; k < live; ++k) {
-        float w[2];
-        weight_of(p0, k, lane, w);
+      float x[2];
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          const float2 y = *reinterpret_cast<const float2*>(vs + sw_off(16 * warp + k, 2 * v + (q2 >> 1), S::kBlock) + (q2 & 1) * 8);
+      for (int h = 0; h < 2; ++h) {
+        x[h] = fmaxf(s[i][0][2 * h], s[i][0][2 * h + 1]);
+        if (NT == 2) x[h] = fmaxf(x[h], fmaxf(s[i][NT - 1][2 * h], s[i][NT - 1][2 * h + 1]));
+        x[h] = fmaxf(x[h], __shfl_xor_sync(0xffffffffu, x[h], 1));
+        x[h] = sc * fmaxf(x[h], __shfl_xor_sync(0xffffffffu, x[h], 2));
+      }
+      if (__any_sync(0xffffffffu, x[0] > m[i][0] || x[1] > m[i][1])) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            if (k <= limit[h]) {
-              if (!finite(y.x)) o[v][2 * h] = fmaf(w[h], y.x, o[v][2 * h]);
-              if (!finite(y.y)) o[v][2 * h + 1] = fmaf(w[h], y.y, o[v][2 * h + 1]);
-            }
+        for (int h = 0; h < 2; ++h) {
+          if (!(x[h] > m[i][h])) x[h] = m[i][h];
+          const float f = m[i][h] == -INFINITY ? 1.f : exp2f(m[i][h] - x[h]);
+          m[i][h] = x[h];
+          l[i][h] *= f;
+#pragma unroll
+          for (int v = 0; v < NV; ++v) {
+            o[i][v][2 * h] *= f;
+            o[i][v][2 * h + 1] *= f;
+          }
+        }
+      }
+      const float ref[2] = {m[i][0] == -INFINITY ? 0.f : m[i][0], m[i][1] == -INFINITY ? 0.f : m[i][1]};
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[i][n][e] = exp2f(fmaf(s[i][n][e], sc, -ref[e >> 1]));
+          l[i][e >> 1] += s[i][n][e];
+        }
+    }
+    if (masked && poison) {  // the non-finite values alone into the rows that attend them, then zeros for them
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        for (int k = 0; k < live; ++k) {
+          float w[2];
+          weight_of<NT>(&s[i][0][0], k, lane, w);
+#pragma unroll
+          for (int v = 0; v < NV; ++v) {
+            const float2 y = *reinterpret_cast<const float2*>(vs + sw_off(KW * warp + k, 2 * v + (q2 >> 1), S::kBlock) + (q2 & 1) * 8);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              if (k <= limit[i][h]) {
+                if (!finite(y.x)) o[i][v][2 * h] = fmaf(w[h], y.x, o[i][v][2 * h]);
+                if (!finite(y.y)) o[i][v][2 * h + 1] = fmaf(w[h], y.y, o[i][v][2 * h + 1]);
+              }
+          }
         }
       }
       __syncwarp();
-      for (int i = lane; i < 16 * S::NB * 8; i += 32) {
-        float4* x4 = reinterpret_cast<float4*>(vs + sw_off(16 * warp + i / (S::NB * 8), i % (S::NB * 8), S::kBlock));
+      for (int i = lane; i < KW * S::NB * 8; i += 32) {
+        float4* x4 = reinterpret_cast<float4*>(vs + sw_off(KW * warp + i / (S::NB * 8), i % (S::NB * 8), S::kBlock));
         const float4 y = *x4;
         *x4 = make_float4(finite(y.x) ? y.x : 0.f, finite(y.y) ? y.y : 0.f, finite(y.z) ? y.z : 0.f,
                           finite(y.w) ? y.w : 0.f);
       }
     }
     __syncwarp();  // V's zeroed rows
-    uint32_t ah[4], am[4], al[4];
+    uint32_t ah[MT][2 * NT], am[MT][2 * NT], al[MT][2 * NT];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const Split y = split3(s[i >> 1][2 * (i & 1)], s[i >> 1][2 * (i & 1) + 1]);
-      ah[i] = y.h;
-      am[i] = y.m;
-      al[i] = y.l;
-    }
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int z = 0; z < 2 * NT; ++z) {
+        const Split y = split3(s[i][z >> 1][2 * (z & 1)], s[i][z >> 1][2 * (z & 1) + 1]);
+        ah[i][z] = y.h;
+        am[i][z] = y.m;
+        al[i][z] = y.l;
+      }
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      // keys 2 q2, + 1, + 8, + 9 of channel 8 v + r0
-      float y[4];
+      // keys 2 q2, + 1 (, + 8, + 9) of channel 8 v + r0
+      float y[2 * NT];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 2 * NT; ++i)
         y[i] = *reinterpret_cast<const float*>(
-            vs + sw_off(16 * warp + 2 * q2 + (i & 1) + 8 * (i >> 1), 2 * v + (r0 >> 2), S::kBlock) + (r0 & 3) * 4);
-      const Split b0 = split3(y[0], y[1]), b1 = split3(y[2], y[3]);
-      mma16816(o[v], ah, b0.l, b1.l);
-      mma16816(o[v], al, b0.h, b1.h);
-      mma16816(o[v], am, b0.m, b1.m);
-      mma16816(o[v], ah, b0.m, b1.m);
-      mma16816(o[v], am, b0.h, b1.h);
-      mma16816(o[v], ah, b0.h, b1.h);
-    }
-  }
-  __device__ void stats(float2* ml, int lane) {
+            vs + sw_off(KW * warp + 2 * q2 + (i & 1) + 8 * (i >> 1), 2 * v + (r0 >> 2), S::kBlock) + (r0 & 3) * 4);
+      const Split b0 = split3(y[0], y[1]), b1 = split3(y[2 * NT - 2], y[2 * NT - 1]);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-      if ((lane & 3) == 0) ml[(lane >> 2) + 8 * h] = make_float2(m[h], l[h]);
-    }
-  }
-  __device__ void put(float* scratch, const float2 (*ml)[kMaxRows], int rows, int lane) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = (lane >> 2) + 8 * h;
-      if (r >= rows) continue;
-      float M = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w][r].x);
-      const float f = exp2f(m[h] - (M == -INFINITY ? 0.f : M));
-#pragma unroll
-      for (int v = 0; v < NV; ++v)
-        *reinterpret_cast<float2*>(scratch + r * DP + 8 * v + 2 * (lane & 3)) =
-            make_float2(o[v][2 * h] * f, o[v][2 * h + 1] * f);
-    }
-  }
-};
-
-// fp32 with 256 channels: FMAs, 8 keys a warp.  A lane holds one key and a
-// quarter of its channels for the
-// scores, then DP / 32 channels of the output
-template <int DP, int RT_>
-struct RowsF32 {
-  using S = Shape<float, DP>;
-  static constexpr int RT = RT_, NC = DP / 32 > 4 ? 4 : DP / 32, NG = DP / 32 / NC;  // channels: NG groups of NC
-  float o[RT][NG * NC], m[RT], l[RT];
-
-  __device__ void start(const char* stage, float* qs, int lane) {
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-#pragma unroll
-      for (int c = 0; c < NG * NC; ++c) o[r][c] = 0.f;
-      m[r] = -INFINITY;
-      l[r] = 0.f;
-    }
-    (void)stage;
-    (void)qs;
-    (void)lane;
-  }
-  // the block's q rows, by all consumers; rows it does not have are zeros
-  static __device__ void load_q(const AttnParams& p, const Tile& t, float* qs, int tid) {
-    const float* q = static_cast<const float*>(p.q);
-    for (int i = tid; i < RT * DP; i += 32 * kWarps) {
-      const int r = i / DP, c = i % DP;
-      qs[i] = r < t.rows && c < p.D
-                  ? q[((int64_t)(t.tok0 + r / t.gb) * p.H + t.head0 + r % t.gb) * p.D + c]
-                  : 0.f;
-    }
-  }
-
-  __device__ void step(char* stage, const float* qs, const Tile& t, float sc, int warp, int lane) {
-    const int x0 = t.x0 + 8 * warp;
-    if (x0 >= t.end) return;
-    const int live = min(8, t.end - x0);
-    const bool masked = x0 + 7 > t.pos0;
-    const int i = lane >> 2, qd = lane & 3;
-    const int key = ((i & 1) << 2) | (i >> 1);  // lanes of a load phase four keys apart: no bank conflict
-    float s[RT];
-#pragma unroll
-    for (int r = 0; r < RT; ++r) s[r] = 0.f;
-#pragma unroll 2
-    for (int c = qd; c < DP / 4; c += 4) {
-      const float4 k4 = *reinterpret_cast<const float4*>(stage + sw_off(8 * warp + key, c, S::kBlock));
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        const float4 q4 = *reinterpret_cast<const float4*>(qs + r * DP + 4 * c);
-        s[r] = fmaf(q4.x, k4.x, fmaf(q4.y, k4.y, fmaf(q4.z, k4.z, fmaf(q4.w, k4.w, s[r]))));
-      }
-    }
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      s[r] += __shfl_xor_sync(0xffffffffu, s[r], 1);
-      s[r] += __shfl_xor_sync(0xffffffffu, s[r], 2);
-      s[r] *= sc;
-      if (masked && x0 + key > min(t.end - 1, t.pos0 + r / t.gb)) s[r] = -INFINITY;
-      float x = s[r];
-      x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-      x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-      x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-      if (x > m[r]) {  // uniform in the warp
-        const float f = exp2f(m[r] - x);
-        l[r] *= f;
-#pragma unroll
-        for (int c = 0; c < NG * NC; ++c) o[r][c] *= f;
-        m[r] = x;
-      }
-      s[r] = exp2f(s[r] - (m[r] == -INFINITY ? 0.f : m[r]));
-      l[r] += s[r];
-    }
-    const char* vs = stage + S::NB * S::kBlock;
-    for (int k = 0; k < live; ++k) {
-      float v[NG * NC];
-#pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        const int ch = g * 128 + lane * NC;  // first channel of this lane's group
-        const char* a = vs + sw_off(8 * warp + k, ch >> 2, S::kBlock) + (ch & 3) * 4;
-        if (NC == 4) {
-          const float4 y = *reinterpret_cast<const float4*>(a);
-          v[g * NC] = y.x;
-          v[g * NC + 1 % NC] = y.y;
-          v[g * NC + 2 % NC] = y.z;
-          v[g * NC + 3 % NC] = y.w;
-        } else {
-#pragma unroll
-          for (int c = 0; c < NC; ++c) v[g * NC + c] = *reinterpret_cast<const float*>(a + 4 * c);
-        }
-      }
-      const int src = (((k & 3) << 1) | (k >> 2)) << 2;  // a lane that holds key k
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        const float w = __shfl_sync(0xffffffffu, s[r], src);
-        if (!masked || x0 + k <= t.pos0 + r / t.gb) {  // a masked key's value stays out even where it is not finite
-#pragma unroll
-          for (int c = 0; c < NG * NC; ++c) o[r][c] = fmaf(w, v[c], o[r][c]);
-        }
+      for (int i = 0; i < MT; ++i) {
+        mma_keys<NT>(o[i][v], ah[i], b0.l, b1.l);
+        mma_keys<NT>(o[i][v], al[i], b0.h, b1.h);
+        mma_keys<NT>(o[i][v], am[i], b0.m, b1.m);
+        mma_keys<NT>(o[i][v], ah[i], b0.m, b1.m);
+        mma_keys<NT>(o[i][v], am[i], b0.h, b1.h);
+        mma_keys<NT>(o[i][v], ah[i], b0.h, b1.h);
       }
     }
   }
   __device__ void stats(float2* ml, int lane) {
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      float x = l[r];
-      x += __shfl_xor_sync(0xffffffffu, x, 4);
-      x += __shfl_xor_sync(0xffffffffu, x, 8);
-      x += __shfl_xor_sync(0xffffffffu, x, 16);
-      if (lane == 0) ml[r] = make_float2(m[r], x);
-    }
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float x = l[i][h];
+        x += __shfl_xor_sync(0xffffffffu, x, 1);
+        x += __shfl_xor_sync(0xffffffffu, x, 2);
+        if ((lane & 3) == 0) ml[16 * i + (lane >> 2) + 8 * h] = make_float2(m[i][h], x);
+      }
   }
   __device__ void put(float* scratch, const float2 (*ml)[kMaxRows], int rows, int lane) {
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      if (r >= rows) break;
-      float M = -INFINITY;
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w][r].x);
-      const float f = exp2f(m[r] - (M == -INFINITY ? 0.f : M));
+      for (int h = 0; h < 2; ++h) {
+        const int r = 16 * i + (lane >> 2) + 8 * h;
+        if (r >= rows) continue;
+        float M = -INFINITY;
 #pragma unroll
-      for (int g = 0; g < NG; ++g)
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w][r].x);
+        const float f = exp2f(m[i][h] - (M == -INFINITY ? 0.f : M));
 #pragma unroll
-        for (int c = 0; c < NC; ++c) scratch[r * DP + g * 128 + lane * NC + c] = o[r][g * NC + c] * f;
-    }
+        for (int v = 0; v < NV; ++v)
+          *reinterpret_cast<float2*>(scratch + r * DP + 8 * v + 2 * (lane & 3)) =
+              make_float2(o[i][v][2 * h] * f, o[i][v][2 * h + 1] * f);
+      }
   }
 };
 
 template <typename T, int DP, typename Work>
-__global__ void __launch_bounds__(kThreads, Shape<T, DP>::CTAS)
+__global__ void __launch_bounds__(kThreads, Shape<T, DP, Work::kRows>::CTAS)
     attn_rows(const AttnParams p, const RowsArgs a, const __grid_constant__ CUtensorMap mq,
               const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
-  using S = Shape<T, DP>;
+  using S = Shape<T, DP, Work::kRows>;
+  static_assert(shape_ok<T, DP, Work::kRows>(), "shared memory");
+  constexpr int R = Work::kRows;
   constexpr int KT = S::KT;
   extern __shared__ char raw[];
   char* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
@@ -820,7 +740,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, DP>::CTAS)
     uint32_t k = 0;
     if (lane == 0) a.joins[blockIdx.x].parts = 0;
     const uint32_t box_bytes = 128u << a.box_shift;
-    const int box = 1 << a.box_shift, qt = 1 << a.q_shift, gmax = min(p.G, kMaxRows);
+    const int box = 1 << a.box_shift, qt = 1 << a.q_shift, gmax = min(p.G, R);
     for (int64_t u = u0; u < u1 && ok; ++u, ++k) {
       const int kvh = a.parts == 1 ? head : head / a.parts, part = a.parts == 1 ? 0 : head - kvh * a.parts;
       const int t0 = (int)block << a.q_shift, ntok = min(qt, sq.len - t0);
@@ -849,8 +769,8 @@ __global__ void __launch_bounds__(kThreads, Shape<T, DP>::CTAS)
       if (lane == 0) {
         Tile t;
         t.tok0 = (int)sq.tok0 + t0;
-        t.head0 = kvh * p.G + part * kMaxRows;
-        t.gb = a.parts == 1 ? p.G : min(kMaxRows, p.G - part * kMaxRows);
+        t.head0 = kvh * p.G + part * R;
+        t.gb = a.parts == 1 ? p.G : min(R, p.G - part * R);
         t.rows = ntok * t.gb;
         t.pos0 = pos0;
         t.end = end;
@@ -942,10 +862,10 @@ __global__ void __launch_bounds__(kThreads, Shape<T, DP>::CTAS)
         if (!__all_sync(0xffffffffu, wait_or_dead(&b->join[0], joins & 1, &b->dead))) break;
         // every warp is done with this stage's K and V: it holds the outputs now
         float* scratch = reinterpret_cast<float*>(stage);
-        w.put(scratch + warp * kMaxRows * DP, b->ml, rows, lane);
+        w.put(scratch + warp * R * DP, b->ml, rows, lane);
         // each row's M and l over the warps, before another pair's replace them;
-        // a thread's output quads are STEPS pieces of the [16][DP] tile
-        constexpr int VEC = DP / 4, STEPS = kMaxRows * VEC / (32 * kWarps);
+        // a thread's output quads are STEPS pieces of the [R][DP] tile
+        constexpr int VEC = DP / 4, STEPS = R * VEC / (32 * kWarps);
         float M[STEPS], L[STEPS];
 #pragma unroll
         for (int i = 0; i < STEPS; ++i) {
@@ -971,7 +891,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, DP>::CTAS)
           float4 x = *reinterpret_cast<const float4*>(scratch + r * DP + c);
 #pragma unroll
           for (int z = 1; z < kWarps; ++z) {
-            const float4 y = *reinterpret_cast<const float4*>(scratch + (z * kMaxRows + r) * DP + c);
+            const float4 y = *reinterpret_cast<const float4*>(scratch + (z * R + r) * DP + c);
             x.x += y.x;
             x.y += y.y;
             x.z += y.z;
@@ -1002,13 +922,16 @@ __global__ void __launch_bounds__(kThreads, Shape<T, DP>::CTAS)
 }
 
 // The blocks that cross stretches: parts 2 c + 1, 2 (c + 1), 2 (c + 2), .. of
-// stretch c.  A warp per row, DP / 32 channels a lane.
-constexpr int kJoinWarps = 4;
+// stretch c.  A CTA per row, the parts dealt to its warps, which are then added
+// in their order.
+constexpr int kJoinWarps = 8;
 template <typename T, int DP>
 __global__ void __launch_bounds__(32 * kJoinWarps) attn_rows_join(const AttnParams p, const RowsArgs a) {
+  __shared__ float sm_o[kJoinWarps][DP];
+  __shared__ float sm_l[kJoinWarps];
   pdl_wait();
   const RowsJoin jn = a.joins[blockIdx.x];
-  const int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int r = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (jn.parts == 0 || r >= jn.rows) return;
   constexpr int V = DP / 32;
   const int s0 = 2 * (int)blockIdx.x;
@@ -1022,18 +945,27 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_rows_join(const AttnPara
 #pragma unroll
   for (int v = 0; v < V; ++v) o[v] = 0.f;
 #pragma unroll 4
-  for (int k = 0; k < jn.parts; ++k) {
+  for (int k = warp; k < jn.parts; k += kJoinWarps) {
     const float2 ml = a.ml[slot(k)];
     const float f = exp2f(ml.x - M);
     l = fmaf(f, ml.y, l);
 #pragma unroll
     for (int v = 0; v < V; ++v) o[v] = fmaf(f, a.o[(int64_t)slot(k) * DP + 32 * v + lane], o[v]);
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  const int64_t at = ((int64_t)(jn.tok0 + r / jn.gb) * p.H + jn.head0 + r % jn.gb) * p.D;
 #pragma unroll
-  for (int v = 0; v < V; ++v)
-    if (32 * v + lane < p.D) st_out(static_cast<T*>(p.o), at + 32 * v + lane, o[v] * inv);
+  for (int v = 0; v < V; ++v) sm_o[warp][32 * v + lane] = o[v];
+  if (lane == 0) sm_l[warp] = l;
+  __syncthreads();
+  const int64_t at = ((int64_t)(jn.tok0 + r / jn.gb) * p.H + jn.head0 + r % jn.gb) * p.D;
+  float sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) sum += sm_l[w];
+  for (int c = threadIdx.x; c < p.D; c += 32 * kJoinWarps) {
+    float x = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) x += sm_o[w][c];
+    st_out(static_cast<T*>(p.o), at + c, sum == 0.f ? 0.f : x / sum);
+  }
 }
 
 // ------------------------------------------------------------------ host
@@ -1061,16 +993,17 @@ int padded(const AttnParams& p) {
   return p.D < low ? low : p.D;
 }
 
-// Tokens of a block, log2: as many as 16 rows hold and a sequence may have
-int block_shift(const AttnParams& p) {
+// Tokens of a block, log2: as many as its rows hold and a sequence may have
+int block_shift(const AttnParams& p, int rows) {
   int s = 0;
-  while ((2 << s) * p.G <= kMaxRows && (1 << s) < p.max_seqlen) ++s;
+  while ((2 << s) * p.G <= rows && (1 << s) < p.max_seqlen) ++s;
   return s;
 }
 
 template <typename T, int DP, typename Work>
 cudaError_t launch_w(const AttnParams& p, char* w, cudaStream_t stream) {
-  using S = Shape<T, DP>;
+  constexpr int R = Work::kRows;
+  using S = Shape<T, DP, R>;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -1079,7 +1012,7 @@ cudaError_t launch_w(const AttnParams& p, char* w, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   // no more CTAs than stretches of kMinTiles that the longest rows could fill
   const int64_t keys = p.block_table ? (int64_t)p.max_pages << p.page_shift : p.total_tokens;
-  const int64_t blocks = ((p.total_tokens >> block_shift(p)) + p.num_seqs) * ((p.G + kMaxRows - 1) / kMaxRows) * p.Hkv;
+  const int64_t blocks = ((p.total_tokens >> block_shift(p, R)) + p.num_seqs) * ((p.G + R - 1) / R) * p.Hkv;
   const int64_t most = blocks < kMaxGrid * kMinTiles ? (blocks * (keys / S::KT + 2) + kMinTiles - 1) / kMinTiles : kMaxGrid;
   int grid = sms * S::CTAS < kMaxGrid ? sms * S::CTAS : kMaxGrid;
   if (most < grid) grid = (int)most;
@@ -1089,9 +1022,9 @@ cudaError_t launch_w(const AttnParams& p, char* w, cudaStream_t stream) {
   a.o = reinterpret_cast<float*>(a.ml + 2 * kMaxGrid * kMaxRows);
   constexpr int kt_shift = S::KT == 64 ? 6 : 5;
   a.box_shift = p.block_table && p.page_shift < kt_shift ? p.page_shift : kt_shift;
-  a.q_shift = block_shift(p);
-  a.parts = (p.G + kMaxRows - 1) / kMaxRows;
-  const int heads = p.G < kMaxRows ? p.G : kMaxRows;
+  a.q_shift = block_shift(p, R);
+  a.parts = (p.G + R - 1) / R;
+  const int heads = p.G < R ? p.G : R;
   CUtensorMap mq, mk, mv;
   if (!encode(&mq, p, p.q, true, heads, 1 << a.q_shift) || !encode(&mk, p, p.k, false, 1, 1 << a.box_shift) ||
       !encode(&mv, p, p.v, false, 1, 1 << a.box_shift))
@@ -1100,16 +1033,15 @@ cudaError_t launch_w(const AttnParams& p, char* w, cudaStream_t stream) {
                              mv);
   if (e != cudaSuccess) return e;
   return launch_maybe_dependent(true, attn_rows_join<T, DP>,
-                                dim3((unsigned)grid, (unsigned)((heads << a.q_shift) + kJoinWarps - 1) / kJoinWarps),
+                                dim3((unsigned)grid, (unsigned)(heads << a.q_shift)),
                                 dim3(32 * kJoinWarps), 0, stream, p, a);
 }
 
+// fp32: 32 rows where a sequence has them, else 16
 template <int DP>
 cudaError_t launch_f32(const AttnParams& p, char* w, cudaStream_t stream) {
-  const int rows = (p.G < kMaxRows ? p.G : kMaxRows) << block_shift(p);
-  if (rows <= 4) return launch_w<float, DP, RowsF32<DP, 4>>(p, w, stream);
-  if (rows <= 8) return launch_w<float, DP, RowsF32<DP, 8>>(p, w, stream);
-  return launch_w<float, DP, RowsF32<DP, 16>>(p, w, stream);
+  if (p.max_seqlen * p.G > 16) return launch_w<float, DP, RowsF32<DP, 16, 2>>(p, w, stream);
+  return launch_w<float, DP, RowsF32<DP, 16, 1>>(p, w, stream);
 }
 
 }  // namespace
@@ -1120,7 +1052,7 @@ cudaError_t launch_f32(const AttnParams& p, char* w, cudaStream_t stream) {
 // 16-byte aligned bases for the tensor maps.
 bool attn_rows_fits(const AttnParams& p) {
   auto al16 = [](const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15) == 0; };
-  const bool few = p.block_table && p.max_seqlen * p.G <= kMaxRows;
+  const bool few = p.block_table && p.max_seqlen * p.G <= 16;
   return (few || p.dt == KDA_F32 || p.D == 256) && p.scale > 0.f && p.scale <= 3.4e38f && al16(p.q) && al16(p.k) &&
          al16(p.v) && al16(p.o) && (!p.block_table || p.num_pages > 0);
 }
@@ -1137,10 +1069,10 @@ cudaError_t launch_attn_rows(const AttnParams& p, void* ws, cudaStream_t stream)
     }
   }
   switch (padded(p)) {
-    case 32: return launch_w<float, 32, RowsF32x3<32>>(p, w, stream);
-    case 64: return launch_w<float, 64, RowsF32x3<64>>(p, w, stream);
-    case 128: return launch_w<float, 128, RowsF32x3<128>>(p, w, stream);
-    default: return launch_f32<256>(p, w, stream);
+    case 32: return launch_f32<32>(p, w, stream);
+    case 64: return launch_f32<64>(p, w, stream);
+    case 128: return launch_f32<128>(p, w, stream);
+    default: return launch_w<float, 256, RowsF32<256, 8, 1>>(p, w, stream);
   }
 }
 
