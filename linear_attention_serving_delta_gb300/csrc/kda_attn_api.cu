@@ -101,18 +101,40 @@ AttnParams params(const kda_attn_paged_args* a) {
   return p;
 }
 
-// A few rows a request: the streaming kernel; else the tensor cores; else the
-// CUDA cores.
+// The path of a call: single tokens and a few rows on the streaming kernel,
+// more on the tensor cores' row tiles (two a CTA; one for heads of 256 channels
+// and fp32), fp32 heads of 256 channels on the streaming kernel again, and what
+// none of them takes (odd alignment, a scale that is not positive) on the CUDA
+// cores.
+enum class AttnPath { kRows, kTc, kTc1, kSimt };
+AttnPath attn_path(const AttnParams& p) {
+  const bool few = p.block_table && p.max_seqlen * p.G <= 16;
+  if (few && attn_rows_fits(p)) return AttnPath::kRows;
+  if (attn_tc_fits(p)) return AttnPath::kTc;
+  if (attn_tc1_fits(p)) return AttnPath::kTc1;
+  return attn_rows_fits(p) ? AttnPath::kRows : AttnPath::kSimt;
+}
 size_t attn_workspace(const AttnParams& p) {
-  return attn_rows_fits(p) ? attn_rows_workspace(p) : attn_tc_fits(p) ? attn_tc_workspace(p) : 256;
+  switch (attn_path(p)) {
+    case AttnPath::kRows: return attn_rows_workspace(p);
+    case AttnPath::kTc: return attn_tc_workspace(p);
+    case AttnPath::kTc1: return attn_tc1_workspace(p);
+    case AttnPath::kSimt: break;
+  }
+  return 256;
 }
 
 kda_status_t run_attn(const AttnParams& p, void* ws, size_t ws_bytes, void* stream) {
   if (!ws || ws_bytes < attn_workspace(p) || misaligned(ws)) return KDA_ERR_WORKSPACE;
   if (p.total_tokens == 0) return KDA_OK;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (attn_rows_fits(p)) return from_cuda(launch_attn_rows(p, ws, s));
-  return from_cuda(attn_tc_fits(p) ? launch_attn_tc(p, ws, s) : launch_attn_simt(p, s));
+  switch (attn_path(p)) {
+    case AttnPath::kRows: return from_cuda(launch_attn_rows(p, ws, s));
+    case AttnPath::kTc: return from_cuda(launch_attn_tc(p, ws, s));
+    case AttnPath::kTc1: return from_cuda(launch_attn_tc1(p, ws, s));
+    case AttnPath::kSimt: break;
+  }
+  return from_cuda(launch_attn_simt(p, s));
 }
 
 kda_status_t validate(const kda_kv_plan_args* a) {

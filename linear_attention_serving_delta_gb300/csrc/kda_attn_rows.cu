@@ -178,11 +178,6 @@ __device__ __forceinline__ void mma_keys(float* d, const uint32_t* a, uint32_t b
   if constexpr (NT == 2) mma16816(d, a, b0, b1);
   else mma1688(d, a, b0);
 }
-// byte offset of 16-byte piece c of row r in swizzled blocks of `block` bytes
-__device__ __forceinline__ uint32_t sw_off(int r, int c, uint32_t block) {
-  return (uint32_t)(c >> 3) * block + (uint32_t)r * 128u + (uint32_t)(((c & 7) ^ (r & 7)) << 4);
-}
-
 // The weights of key k for the two rows of a lane, from the accumulator layout
 // p[n][e] of a 16 x 8 NT tile (every lane of the warp calls)
 template <int NT>
@@ -366,29 +361,6 @@ struct RowsBf16 {
     }
   }
 };
-
-// x = h + m + l to fp32 precision, each part bf16: h is x cut to 8 bits (so it
-// never overflows), m and l round what is left, |x - h - m - l| <= 2^-23 |x|.
-// An infinity or NaN stays in h alone.  Two values at a time.
-struct Split {
-  uint32_t h, m, l;
-};
-__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-__device__ __forceinline__ Split split3(float x, float y) {
-  Split s;
-  const uint32_t bx = __float_as_uint(x) & 0xffff0000u, by = __float_as_uint(y) & 0xffff0000u;
-  s.h = (bx >> 16) | by;
-  // (a NaN whose payload the cut loses would turn into an infinity)
-  if (x != x) s.h |= 0x7fffu;
-  if (y != y) s.h |= 0x7fff0000u;
-  float rx = x - __uint_as_float(bx), ry = y - __uint_as_float(by);
-  rx = rx == rx ? rx : 0.f;
-  ry = ry == ry ? ry : 0.f;
-  s.m = pack2(rx, ry);
-  s.l = pack2(rx - bf_lo(s.m), ry - bf_hi(s.m));
-  return s;
-}
 
 // The same in fp32 on the same instructions: every operand is split into three
 // bf16 parts (split3) and a product takes the six pairs that matter, h h, h m,
@@ -969,23 +941,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_rows_join(const AttnPara
 }
 
 // ------------------------------------------------------------------ host
-// q, or K or V as [pages][positions][Hkv][D] (packed: one page of all tokens)
-bool encode(CUtensorMap* m, const AttnParams& p, const void* base, bool q, int heads, int box) {
-  const EncodeTiledFn enc = encode_tiled();
-  if (!enc) return false;
-  const bool half = p.dt == KDA_BF16, paged = !q && p.block_table;
-  const cuuint64_t es = half ? 2 : 4, page = paged ? (cuuint64_t)1 << p.page_shift : (cuuint64_t)p.total_tokens;
-  const cuuint64_t nh = q ? p.H : p.Hkv, row = nh * p.D * es;
-  const cuuint64_t dims[4] = {(cuuint64_t)p.D, nh, page, paged ? (cuuint64_t)p.num_pages : 1};
-  const cuuint64_t strides[3] = {p.D * es, row, row * page};
-  const cuuint32_t bx[4] = {(cuuint32_t)(128 / es), (cuuint32_t)heads, (cuuint32_t)box, 1};
-  const cuuint32_t elem[4] = {1, 1, 1, 1};
-  return enc(m, half ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, q ? 3 : 4,
-             const_cast<void*>(base), dims, strides, bx, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 constexpr int kMaxGrid = 2 * 192;  // two CTAs on each of up to 192 SMs
 
 int padded(const AttnParams& p) {
@@ -1026,8 +981,8 @@ cudaError_t launch_w(const AttnParams& p, char* w, cudaStream_t stream) {
   a.parts = (p.G + R - 1) / R;
   const int heads = p.G < R ? p.G : R;
   CUtensorMap mq, mk, mv;
-  if (!encode(&mq, p, p.q, true, heads, 1 << a.q_shift) || !encode(&mk, p, p.k, false, 1, 1 << a.box_shift) ||
-      !encode(&mv, p, p.v, false, 1, 1 << a.box_shift))
+  if (!attn_map(&mq, p, p.q, true, heads, 1 << a.q_shift) || !attn_map(&mk, p, p.k, false, 1, 1 << a.box_shift) ||
+      !attn_map(&mv, p, p.v, false, 1, 1 << a.box_shift))
     return cudaErrorInvalidValue;
   e = launch_maybe_dependent(true, kernel, dim3((unsigned)grid), dim3(kThreads), (size_t)S::kBytes, stream, p, a, mq, mk,
                              mv);

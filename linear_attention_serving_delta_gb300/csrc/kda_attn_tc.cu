@@ -73,9 +73,9 @@ struct Bars {
   uint32_t turn;      // held by the MMA warp whose burst is being issued
   uint32_t tmem;
   // the CTA's k-th item with key tiles: non-finite values were taken out of its
-  // V tiles (index k % 4; the copies run at most two such items ahead of the
-  // epilogue, held back by Q's row tiles)
-  uint32_t poison[4];
+  // V tiles (index k % 8; V's ring lets the copies begin at most five such
+  // items ahead of the epilogue)
+  uint32_t poison[8];
 };
 static_assert(sizeof(Bars) <= 512, "barrier block");
 
@@ -103,55 +103,7 @@ __device__ __forceinline__ Geo geometry(const AttnItem& it, int G, int tpt) {
   return g;
 }
 
-__device__ __forceinline__ const AttnItem& item_at(const TcArgs& a, int64_t w, int Hkv) {
-  return a.items[a.self_plan ? w : w / Hkv];
-}
-
-// The CTA's i-th item: items go round the CTAs back and forth, so that the
-// sorted costs even out.
-__device__ __forceinline__ int64_t nth_item(int i) {
-  const int64_t g = gridDim.x, c = blockIdx.x;
-  return (int64_t)i * g + ((i & 1) ? g - 1 - c : c);
-}
-
 // ------------------------------------------------------------------ copies
-// A stage of a ring and its phase
-template <int N>
-struct Ring {
-  uint32_t st = 0, ph = 0;
-  __device__ __forceinline__ void next() {
-    if (++st == N) {
-      st = 0;
-      ph ^= 1;
-    }
-  }
-};
-
-// Key tile x0.. of K or V for the whole warp, a box a lane: c2, c3 are the
-// box's coordinates in the map, n how many boxes hold positions.
-struct Boxes {
-  int c2, c3, n;
-};
-__device__ __forceinline__ Boxes boxes_of(const AttnParams& p, const AttnItem& it, int x0, int shift, int lane) {
-  Boxes r;
-  r.n = min(kTile >> shift, (it.kv_len - x0 + (1 << shift) - 1) >> shift);
-  const int x = x0 + (lane << shift);
-  r.c2 = it.base + x;
-  r.c3 = 0;
-  if (p.block_table) {
-    int page = p.num_pages;
-    if (lane < r.n) {
-      page = p.block_table[(int64_t)it.base * p.max_pages + (x >> p.page_shift)];
-      if (page < 0 || page >= p.num_pages) {
-        attn_flag(p.status, kFlagBadCache);
-        page = p.num_pages;  // outside the map: filled with zeros
-      }
-    }
-    r.c2 = x & ((1 << p.page_shift) - 1);
-    r.c3 = page;
-  }
-  return r;
-}
 template <int DP>
 __device__ __forceinline__ void copy_boxes(const CUtensorMap* m, char* dst, const Boxes& bx, int shift, int h, int lane,
                                            uint64_t* bar) {
@@ -194,7 +146,7 @@ __device__ void load_k_role(const AttnParams& p, const TcArgs& a, const CUtensor
       ++nq[t];
     }
     for (int j = 0; j < g.nmax && ok; ++j) {
-      const Boxes bx = boxes_of(p, it, (g.kt0 + j) * kTile, a.box_shift, lane);
+      const Boxes bx = boxes_of(p, it, (g.kt0 + j) * kTile, kTile, a.box_shift, lane);
       ok = __all_sync(0xffffffffu, wait_or_dead(&b->k_empty[ring.st], ring.ph ^ 1, &b->dead));
       if (!ok) break;
       copy_boxes<DP>(mk, sm + S::kK + ring.st * S::kTileBytes, bx, a.box_shift, h, lane, &b->k_full[ring.st]);
@@ -227,12 +179,12 @@ __device__ void load_v_role(const AttnParams& p, const TcArgs& a, const CUtensor
     const int h = (int)(w % p.Hkv);
     const Geo g = geometry(it, p.G, tpt);
     if (g.nmax == 0) continue;
-    uint32_t* poison = &b->poison[busy_items++ & 3];
+    uint32_t* poison = &b->poison[busy_items++ & 7];
     if (lane == 0) *poison = 0;
     for (int j = 0; j < g.nmax; ++j) {
       const int kt = g.kt0 + j, x0 = kt * kTile;
       const bool fix = kt >= g.fix_from;
-      const Boxes bx = boxes_of(p, it, x0, a.box_shift, lane);
+      const Boxes bx = boxes_of(p, it, x0, kTile, a.box_shift, lane);
       char* dst = sm + S::kV + ring.st * S::kTileBytes;
       ok = __all_sync(0xffffffffu, wait_or_dead(&b->v_empty[ring.st], ring.ph ^ 1, &b->dead));
       if (!ok) break;
@@ -459,7 +411,7 @@ __device__ void softmax_role(const AttnParams& p, const TcArgs& a, Bars* b, int6
     fetch(nth_item(i + 1));
     const Geo g = geometry(it, p.G, tpt);
     const int rows = g.rows[t], n = g.n[t];
-    const uint32_t* poisoned = &b->poison[busy_items & 3];
+    const uint32_t* poisoned = &b->poison[busy_items & 7];
     busy_items += g.nmax > 0;
     if (rows == 0) continue;
     const int tok = row / p.G;  // within the row tile
@@ -617,24 +569,11 @@ __device__ void softmax_role(const AttnParams& p, const TcArgs& a, Bars* b, int6
   }
 }
 
-__device__ __forceinline__ AttnItem make_item(const AttnParams& p, const AttnSeq& s, int64_t tile, int tpi) {
-  AttnItem it;
-  it.tok0 = (int32_t)(s.tok0 + tile * tpi);
-  it.ntok = (int32_t)min((int64_t)tpi, s.len - tile * tpi);
-  it.base = p.block_table ? s.row : (int32_t)s.tok0;
-  it.pos0 = (int32_t)(s.kv_len - s.len + tile * tpi);
-  it.kv_len = (int32_t)s.kv_len;
-  it.kt0 = 0;
-  it.kt1 = (max(0, min(it.kv_len, it.pos0 + it.ntok)) + kTile - 1) / kTile;
-  it.slot = -1;
-  return it;
-}
-
 // Small calls plan for themselves: no more items than CTAs, so the order does
 // not matter and CTA w needs item w alone, which the thread of its sequence
 // leaves in the workspace.  Returns whether there is one (for every thread).
-__device__ bool plan_own_item(const AttnParams& p, const TcArgs& a, Bars* b, int tpi) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+__device__ bool plan_own_item(const AttnParams& p, const TcArgs& a, Bars* b) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, tpi = a.row_tiles * a.tpt;
   const int64_t want = blockIdx.x / p.Hkv;
   int64_t before = 0;
   for (int base = 0; base < p.num_seqs; base += kThreads) {
@@ -662,7 +601,7 @@ __device__ bool plan_own_item(const AttnParams& p, const TcArgs& a, Bars* b, int
     }
     const int64_t first = before + x - n;
     if (n > 0 && want >= first && want < first + n) {
-      a.items[blockIdx.x] = make_item(p, q, want - first, tpi);
+      a.items[blockIdx.x] = make_item(p, a, q, want - first);
       b->own = 1;
     }
     before += total;
@@ -713,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();  // the plan, or what came before
   const int tpt = kTile / p.G;
   const int64_t total =
-      a.self_plan ? (plan_own_item(p, a, b, 2 * tpt) ? blockIdx.x + 1 : 0) : (int64_t)a.head->items * p.Hkv;
+      a.self_plan ? (plan_own_item(p, a, b) ? blockIdx.x + 1 : 0) : (int64_t)a.head->items * p.Hkv;
   // registers: 168 a thread at launch (384 x 168 = 64,512); a softmax thread
   // holds a row of 128 logits: 2 x 128 x 208 + 128 x 80 = 63,488
   if (warp < 8) {
@@ -732,292 +671,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 9) tmem_dealloc(b->tmem, kTmemCols);
 }
 
-// ------------------------------------------------------------------ planning
-constexpr int kPlanThreads = 1024;
-constexpr int kBuckets = 2560;
-constexpr int kPlanSeqs = 640;
-
-// costs up to 255 keep their own bucket, larger ones their seven leading bits
-__device__ __forceinline__ int bucket_of(int cost) {
-  if (cost < 256) return cost;
-  const int e = 31 - __clz(cost) - 7;
-  return (e << 7) + (cost >> e);
-}
-
-__device__ int64_t plan_scan(int64_t x, int64_t* part, int64_t* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) part[warp] = x;
-  __syncthreads();
-  if (warp == 0) {
-    int64_t y = part[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t z = __shfl_up_sync(0xffffffffu, y, o);
-      if (lane >= o) y += z;
-    }
-    part[lane] = y;
-  }
-  __syncthreads();
-  if (warp > 0) x += part[warp - 1];
-  *total = part[31];
-  __syncthreads();
-  return x;
-}
-
-// One CTA: the items of the call from the device-side lengths, sorted by
-// their key tiles, costliest first.  When they are too few to fill the GPU
-// (split_sms > 0) an item's key tiles are cut into pieces of about equal
-// share, and the list of what to join is left for attn_join.
-__global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnParams p, const TcArgs a, int tpi) {
-  __shared__ int64_t part[32];
-  __shared__ int hist[kBuckets];
-  __shared__ unsigned long long cost_sum;
-  __shared__ AttnSeq sm_seq[kPlanSeqs];       // the sequences, for batches of up to kPlanSeqs
-  __shared__ int32_t sm_begin[kPlanSeqs];
-  const int tid = threadIdx.x;
-  const bool near = p.num_seqs <= kPlanSeqs;
-  pdl_launch_dependents();
-  pdl_wait();
-  for (int i = tid; i < kBuckets; i += kPlanThreads) hist[i] = 0;
-  if (tid == 0) cost_sum = 0;
-  // the sequences' tiles and their prefix sums
-  int64_t n_tiles = 0;
-  for (int base = 0; base < p.num_seqs; base += kPlanThreads) {
-    const int s = base + tid;
-    int64_t n = 0, total;
-    AttnSeq q{};
-    if (s < p.num_seqs) {
-      q = attn_seq(p, s);
-      if (q.flag) attn_flag(p.status, q.flag);
-      n = ((int64_t)q.len + tpi - 1) / tpi;
-    }
-    const int64_t end = plan_scan(n, part, &total);
-    if (s < p.num_seqs) {
-      if (near) {
-        sm_seq[s] = q;
-        sm_begin[s] = (int32_t)(n_tiles + end - n);
-      } else {
-        a.seq_begin[s] = n_tiles + end - n;
-      }
-    }
-    n_tiles += total;
-  }
-  n_tiles = min(n_tiles, a.max_items);
-  __syncthreads();
-  auto tile_item = [&](int64_t x) {
-    int lo = 0, hi = p.num_seqs - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if ((near ? (int64_t)sm_begin[mid] : a.seq_begin[mid]) <= x) lo = mid; else hi = mid - 1;
-    }
-    return near ? make_item(p, sm_seq[lo], x - sm_begin[lo], tpi)
-                : make_item(p, attn_seq(p, lo), x - a.seq_begin[lo], tpi);
-  };
-  const bool split = a.split_sms > 0 && n_tiles * p.Hkv < 2 * (int64_t)a.split_sms;
-  int piece = INT32_MAX;
-  if (split) {
-    unsigned long long c = 0;
-    for (int64_t x = tid; x < n_tiles; x += kPlanThreads) c += (unsigned long long)tile_item(x).kt1;
-    if (c) atomicAdd(&cost_sum, c);
-    __syncthreads();
-    const int64_t parts = (int64_t)kPiecesPerSm * a.split_sms;
-    const int64_t share = ((int64_t)cost_sum * p.Hkv + parts - 1) / parts;
-    piece = (int)max((int64_t)kMinPiece, share);
-  }
-  // pieces of an item: how many, and each one's key tiles
-  auto pieces = [&](const AttnItem& it) { return it.kt1 <= piece ? 1 : (it.kt1 + piece - 1) / piece; };
-  for (int64_t x = tid; x < n_tiles; x += kPlanThreads) {
-    const AttnItem it = tile_item(x);
-    const int np = pieces(it);
-    for (int k = 0; k < np; ++k) {
-      const int64_t k0 = (int64_t)it.kt1 * k / np, k1 = (int64_t)it.kt1 * (k + 1) / np;
-      atomicAdd(&hist[bucket_of((int)(k1 - k0))], 1);
-    }
-  }
-  __syncthreads();
-  // hist[b] becomes the first place of bucket b: costlier buckets go first.
-  // A thread sums kBuckets / kPlanThreads neighbours.
-  constexpr int kPer = (kBuckets + kPlanThreads - 1) / kPlanThreads;
-  int mine[kPer];
-  int64_t n = 0, total;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int bkt = kBuckets - 1 - (tid * kPer + i);
-    mine[i] = bkt >= 0 ? hist[bkt] : 0;
-    n += mine[i];
-  }
-  int64_t at = plan_scan(n, part, &total) - n;
-  const int64_t items = total;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int bkt = kBuckets - 1 - (tid * kPer + i);
-    if (bkt >= 0) hist[bkt] = (int)at;
-    at += mine[i];
-  }
-  __syncthreads();
-  int64_t slots = 0, joins = 0;
-  for (int64_t base = 0; base < n_tiles; base += kPlanThreads) {
-    const int64_t x = base + tid;
-    AttnItem it{};
-    int np = 0;
-    if (x < n_tiles) {
-      it = tile_item(x);
-      np = pieces(it);
-    }
-    int64_t slot0 = 0, join = 0;
-    if (split) {  // partial results in tile order, whatever the order of the atomics below
-      const int64_t cut = np > 1 ? np : 0;
-      slot0 = slots + plan_scan(cut, part, &total) - cut;
-      slots += total;
-      const int64_t one = np > 1;
-      join = joins + plan_scan(one, part, &total) - one;
-      joins += total;
-    }
-    if (np > 1) a.joins[join] = AttnJoin{it.tok0, it.ntok, (int32_t)slot0, np};
-    const int kt1 = it.kt1;
-    for (int k = 0; k < np; ++k) {
-      it.kt0 = (int)((int64_t)kt1 * k / np);
-      it.kt1 = (int)((int64_t)kt1 * (k + 1) / np);
-      it.slot = np > 1 ? (int32_t)(slot0 + k) : -1;
-      a.items[atomicAdd(&hist[bucket_of(it.kt1 - it.kt0)], 1)] = it;
-    }
-  }
-  if (tid == 0) {
-    a.head->items = (int32_t)items;
-    a.head->joins = (int32_t)joins;
-  }
-}
-
-// The pieces of a cut item joined: with M = max m_k, o = sum 2^(m_k - M) O_k /
-// sum 2^(m_k - M) l_k, in piece order.  A warp per row.
-template <int DP>
-__global__ void __launch_bounds__(256) attn_join(const AttnParams p, const TcArgs a, int tpt) {
-  pdl_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t pairs = (int64_t)a.head->joins * p.Hkv;
-  constexpr int V = DP / 32;
-  for (int64_t w = blockIdx.x; w < pairs * 32; w += gridDim.x) {
-    const AttnJoin jn = a.joins[w / 32 / p.Hkv];
-    const int h = (int)(w / 32 % p.Hkv), r = (int)(w % 32) * 8 + warp;
-    const int t = r / kTile, row = r % kTile, tok = t * tpt + row / p.G;
-    if (row >= tpt * p.G || tok >= jn.ntok) continue;
-    float M = -INFINITY;
-    for (int k = 0; k < jn.pieces; ++k)
-      M = fmaxf(M, a.part_ml[((int64_t)(jn.slot + k) * p.Hkv + h) * (2 * kTile) + r].x);
-    if (M == -INFINITY) M = 0.f;
-    float l = 0.f, o[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) o[v] = 0.f;
-    for (int k = 0; k < jn.pieces; ++k) {
-      const int64_t at = ((int64_t)(jn.slot + k) * p.Hkv + h) * (2 * kTile) + r;
-      const float2 ml = a.part_ml[at];
-      const float f = exp2_fast(ml.x - M);
-      l += f * ml.y;
-#pragma unroll
-      for (int v = 0; v < V; ++v) o[v] = fmaf(f, a.part_o[at * DP + v * 32 + lane], o[v]);
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    __nv_bfloat16* out =
-        static_cast<__nv_bfloat16*>(p.o) + ((int64_t)(jn.tok0 + tok) * p.H + (int64_t)h * p.G + row % p.G) * p.D;
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (v * 32 + lane < p.D) out[v * 32 + lane] = __float2bfloat16_rn(o[v] * inv);
-  }
-}
-
 // ------------------------------------------------------------------ host
-bool encode_q(CUtensorMap* m, const AttnParams& p, int tpt) {
-  const EncodeTiledFn enc = encode_tiled();
-  if (!enc) return false;
-  const cuuint64_t dims[3] = {(cuuint64_t)p.D, (cuuint64_t)p.H, (cuuint64_t)p.total_tokens};
-  const cuuint64_t strides[2] = {(cuuint64_t)p.D * 2, (cuuint64_t)p.H * p.D * 2};
-  const cuuint32_t box[3] = {64, (cuuint32_t)p.G, (cuuint32_t)tpt};
-  const cuuint32_t elem[3] = {1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p.q), dims, strides, box, elem,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// K or V as [pages][positions][Hkv][D] (packed: one page of all tokens), box
-// {64 channels, 1 head, `box` positions, 1 page}; what lies outside reads as zeros
-bool encode_kv(CUtensorMap* m, const AttnParams& p, const void* base, int box) {
-  const EncodeTiledFn enc = encode_tiled();
-  if (!enc) return false;
-  const bool paged = p.block_table != nullptr;
-  const cuuint64_t page = paged ? (cuuint64_t)1 << p.page_shift : (cuuint64_t)p.total_tokens;
-  const cuuint64_t row = (cuuint64_t)p.Hkv * p.D * 2;
-  const cuuint64_t dims[4] = {(cuuint64_t)p.D, (cuuint64_t)p.Hkv, page, paged ? (cuuint64_t)p.num_pages : 1};
-  const cuuint64_t strides[3] = {(cuuint64_t)p.D * 2, row, row * page};
-  const cuuint32_t bx[4] = {64, 1, (cuuint32_t)box, 1};
-  const cuuint32_t elem[4] = {1, 1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, bx, elem,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
+constexpr int kKeyShift = 7;  // log2 of kTile
 int padded(int D) { return D <= 64 ? 64 : 128; }
 
-struct TcLayout {
-  size_t head, seq_begin, items, joins, ml, o, total;
-  int64_t max_items, max_pieces;
-  bool split, self_plan;
-};
-TcLayout layout(const AttnParams& p) {
-  TcLayout L{};
-  const int tpi = 2 * (kTile / p.G);
-  L.max_items = (p.total_tokens + tpi - 1) / tpi + p.num_seqs;
-  // pieces only where the whole batch cannot fill the GPU: at most two per SM
-  // are whole items, and the cuts add kPiecesPerSm
-  L.split = p.block_table && (p.total_tokens + tpi - 1) / tpi * p.Hkv < 2 * kSplitSms;
-  // a call whose items cannot outnumber the SMs plans for itself, unless long
-  // key ranges are better cut
-  const int64_t keys = p.block_table ? (int64_t)p.max_pages << p.page_shift : p.total_tokens;
-  L.self_plan = L.max_items * p.Hkv <= kSplitSms && (!L.split || keys <= kSelfPlanKeys);
-  if (L.self_plan) L.split = false;
-  L.max_pieces = L.split ? (2 + kPiecesPerSm) * (int64_t)kSplitSms / p.Hkv + 1 : 0;
-  size_t off = 0;
-  auto take = [&](size_t bytes) {
-    const size_t at = off;
-    off = align_up(off + bytes, 256);
-    return at;
-  };
-  L.head = take(sizeof(AttnHead));
-  L.seq_begin = take(sizeof(int64_t) * p.num_seqs);
-  L.items = take(sizeof(AttnItem) * (size_t)(L.self_plan ? L.max_items * p.Hkv : L.max_items + L.max_pieces));
-  if (L.split) {
-    L.joins = take(sizeof(AttnJoin) * (size_t)(2 * kSplitSms));
-    const size_t rows = (size_t)L.max_pieces * p.Hkv * 2 * kTile;
-    L.ml = take(rows * sizeof(float2));
-    L.o = take(rows * padded(p.D) * sizeof(float));
-  }
-  L.total = off;
-  return L;
-}
-
 template <int DP>
-cudaError_t launch_dp(const AttnParams& p, const TcLayout& L, char* w, cudaStream_t stream) {
+cudaError_t launch_dp(const AttnParams& p, const TcLayout& L, void* ws, cudaStream_t stream) {
   using S = Shape<DP>;
-  const int tpt = kTile / p.G;
-  TcArgs a{};
-  a.head = reinterpret_cast<AttnHead*>(w + L.head);
-  a.seq_begin = reinterpret_cast<int64_t*>(w + L.seq_begin);
-  a.items = reinterpret_cast<AttnItem*>(w + L.items);
-  a.max_items = L.max_items;
-  a.box_shift = p.block_table && p.page_shift < 7 ? p.page_shift : 7;
-  a.o_wide = (reinterpret_cast<uintptr_t>(p.o) & 31) == 0;
-  if (L.split) {
-    a.split_sms = kSplitSms;
-    a.joins = reinterpret_cast<AttnJoin*>(w + L.joins);
-    a.part_ml = reinterpret_cast<float2*>(w + L.ml);
-    a.part_o = reinterpret_cast<float*>(w + L.o);
-  }
+  TcArgs a = tc_args(p, L, 2, kKeyShift, ws);
   CUtensorMap mq, mk, mv;
-  if (!encode_q(&mq, p, tpt) || !encode_kv(&mk, p, p.k, 1 << a.box_shift) || !encode_kv(&mv, p, p.v, 1 << a.box_shift))
+  if (!attn_map(&mq, p, p.q, true, p.G, a.tpt) || !attn_map(&mk, p, p.k, false, 1, 1 << a.box_shift) ||
+      !attn_map(&mv, p, p.v, false, 1, 1 << a.box_shift))
     return cudaErrorInvalidValue;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1030,12 +694,11 @@ cudaError_t launch_dp(const AttnParams& p, const TcLayout& L, char* w, cudaStrea
   if (a.self_plan)
     return launch_maybe_dependent(true, attn_tc<DP>, dim3((unsigned)(L.max_items * p.Hkv)), dim3(kThreads),
                                   (size_t)S::kBytes, stream, p, a, mq, mk, mv);
-  e = launch_maybe_dependent(true, attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p, a, 2 * tpt);
+  e = launch_attn_plan(p, a, stream);
   if (e != cudaSuccess) return e;
   e = launch_maybe_dependent(true, attn_tc<DP>, dim3((unsigned)(most < sms ? most : sms)), dim3(kThreads),
                              (size_t)S::kBytes, stream, p, a, mq, mk, mv);
-  if (e != cudaSuccess || !L.split) return e;
-  return launch_maybe_dependent(true, attn_join<DP>, dim3((unsigned)(4 * sms)), dim3(256), 0, stream, p, a, tpt);
+  return e != cudaSuccess || !L.split ? e : launch_attn_join(p, a, DP, sms, stream);
 }
 
 }  // namespace
@@ -1049,11 +712,10 @@ bool attn_tc_fits(const AttnParams& p) {
   return p.dt == KDA_BF16 && p.D <= 128 && p.scale > 0.f && p.scale <= 3.4e38f && al16(p.q) && al16(p.k) &&
          al16(p.v) && al16(p.o) && (!p.block_table || p.num_pages > 0);
 }
-size_t attn_tc_workspace(const AttnParams& p) { return layout(p).total; }
+size_t attn_tc_workspace(const AttnParams& p) { return tc_layout(p, 2, padded(p.D), true).total; }
 cudaError_t launch_attn_tc(const AttnParams& p, void* ws, cudaStream_t stream) {
-  const TcLayout L = layout(p);
-  char* w = static_cast<char*>(ws);
-  return p.D <= 64 ? launch_dp<64>(p, L, w, stream) : launch_dp<128>(p, L, w, stream);
+  const TcLayout L = tc_layout(p, 2, padded(p.D), true);
+  return p.D <= 64 ? launch_dp<64>(p, L, ws, stream) : launch_dp<128>(p, L, ws, stream);
 }
 
 }  // namespace kda

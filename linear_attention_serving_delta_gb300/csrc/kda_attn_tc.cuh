@@ -10,6 +10,8 @@
 // leading stride, and 16 tokens are 2048 bytes.
 #pragma once
 
+#include <type_traits>
+
 #include "kda_attn.cuh"
 #include "kda_tc.cuh"
 
@@ -17,6 +19,10 @@ namespace kda {
 
 // The SMs the cut into pieces is sized for, the pieces an SM gets (their costs
 // even out over several), and the fewest key tiles a piece has
+// Requests of up to this many rows a key head take blocks of 16 or 32 rows where
+// a 128-row tile has one row tile per CTA only
+constexpr int kFewRows = 32;
+constexpr int kRowTile = 128;  // rows of a row tile
 constexpr int kSplitSms = 152;
 constexpr int kPiecesPerSm = 1;
 constexpr int kMinPiece = 4;
@@ -41,14 +47,86 @@ struct TcArgs {
   int64_t* seq_begin;   // [N] first tile of each sequence
   AttnItem* items;
   int64_t max_items;    // tiles the workspace has room for
+  int32_t row_tiles;    // row tiles of an item
+  int32_t tpt;          // tokens of a row tile
+  int32_t kt_shift;     // log2 of a key tile's positions
   int32_t box_shift;    // log2 of the positions per copy
   int32_t self_plan;    // every CTA finds its one item
   int32_t o_wide;       // o is 32-byte aligned
   int32_t split_sms;    // > 0: items may be cut into pieces
   AttnJoin* joins;
-  float2* part_ml;      // [pieces][Hkv][256] (m, l)
-  float* part_o;        // [pieces][Hkv][256][DP]
+  float2* part_ml;      // [pieces][Hkv][row_tiles * 128] (m, l)
+  float* part_o;        // [pieces][Hkv][row_tiles * 128][DP]
 };
+
+struct TcLayout {
+  size_t head, seq_begin, items, joins, ml, o, total;
+  int64_t max_items, max_pieces;
+  bool split, self_plan;
+};
+
+// Tile `tile` (of row_tiles x tpt tokens) of sequence s, over all of its keys
+__device__ __forceinline__ AttnItem make_item(const AttnParams& p, const TcArgs& a, const AttnSeq& s, int64_t tile) {
+  const int tpi = a.row_tiles * a.tpt;
+  AttnItem it;
+  it.tok0 = (int32_t)(s.tok0 + tile * tpi);
+  it.ntok = (int32_t)min((int64_t)tpi, s.len - tile * tpi);
+  it.base = p.block_table ? s.row : (int32_t)s.tok0;
+  it.pos0 = (int32_t)(s.kv_len - s.len + tile * tpi);
+  it.kv_len = (int32_t)s.kv_len;
+  it.kt0 = 0;
+  it.kt1 = (max(0, min(it.kv_len, it.pos0 + it.ntok)) + (1 << a.kt_shift) - 1) >> a.kt_shift;
+  it.slot = -1;
+  return it;
+}
+__device__ __forceinline__ const AttnItem& item_at(const TcArgs& a, int64_t w, int Hkv) {
+  return a.items[a.self_plan ? w : w / Hkv];
+}
+
+// The CTA's i-th item: items go round the CTAs back and forth, so that the
+// sorted costs even out.
+__device__ __forceinline__ int64_t nth_item(int i) {
+  const int64_t g = gridDim.x, c = blockIdx.x;
+  return (int64_t)i * g + ((i & 1) ? g - 1 - c : c);
+}
+
+// A stage of a ring and its phase
+template <int N>
+struct Ring {
+  uint32_t st = 0, ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++st == N) {
+      st = 0;
+      ph ^= 1;
+    }
+  }
+};
+
+// Key tile x0.. of K or V for the whole warp, a box a lane: c2, c3 are the
+// box's coordinates in the map, n how many boxes hold positions.
+struct Boxes {
+  int c2, c3, n;
+};
+__device__ __forceinline__ Boxes boxes_of(const AttnParams& p, const AttnItem& it, int x0, int keys, int shift, int lane) {
+  Boxes r;
+  r.n = min(keys >> shift, (it.kv_len - x0 + (1 << shift) - 1) >> shift);
+  const int x = x0 + (lane << shift);
+  r.c2 = it.base + x;
+  r.c3 = 0;
+  if (p.block_table) {
+    int page = p.num_pages;
+    if (lane < r.n) {
+      page = p.block_table[(int64_t)it.base * p.max_pages + (x >> p.page_shift)];
+      if (page < 0 || page >= p.num_pages) {
+        attn_flag(p.status, kFlagBadCache);
+        page = p.num_pages;  // outside the map: filled with zeros
+      }
+    }
+    r.c2 = x & ((1 << p.page_shift) - 1);
+    r.c3 = page;
+  }
+  return r;
+}
 
 namespace tc {
 
@@ -203,11 +281,55 @@ __device__ __forceinline__ uint32_t finite_only(uint32_t w) {
   return w;
 }
 
+// byte offset of 16-byte piece c of row r in swizzled blocks of `block` bytes
+__device__ __forceinline__ uint32_t sw_off(int r, int c, uint32_t block) {
+  return (uint32_t)(c >> 3) * block + (uint32_t)r * 128u + (uint32_t)(((c & 7) ^ (r & 7)) << 4);
+}
+
+// x = h + m + l to fp32 precision, each part bf16: h is x cut to 8 bits (so it
+// never overflows), m and l round what is left, |x - h - m - l| <= 2^-23 |x|.
+// An infinity or NaN stays in h alone.  Two values at a time.
+struct Split {
+  uint32_t h, m, l;
+};
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ Split split3(float x, float y) {
+  Split s;
+  const uint32_t bx = __float_as_uint(x) & 0xffff0000u, by = __float_as_uint(y) & 0xffff0000u;
+  s.h = (bx >> 16) | by;
+  // (a NaN whose payload the cut loses would turn into an infinity)
+  if (x != x) s.h |= 0x7fffu;
+  if (y != y) s.h |= 0x7fff0000u;
+  float rx = x - __uint_as_float(bx), ry = y - __uint_as_float(by);
+  rx = rx == rx ? rx : 0.f;
+  ry = ry == ry ? ry : 0.f;
+  s.m = pack2(rx, ry);
+  s.l = pack2(rx - bf_lo(s.m), ry - bf_hi(s.m));
+  return s;
+}
+
 }  // namespace tc
+
+// Workspace, arguments and launches of the plan and of the joining of pieces.
+// row_tiles: of an item; dp: padded channels; kt_shift: log2 of a key tile.
+TcLayout tc_layout(const AttnParams& p, int row_tiles, int dp, bool may_self_plan);
+TcArgs tc_args(const AttnParams& p, const TcLayout& L, int row_tiles, int kt_shift, void* ws);
+cudaError_t launch_attn_plan(const AttnParams& p, const TcArgs& a, cudaStream_t stream);
+cudaError_t launch_attn_join(const AttnParams& p, const TcArgs& a, int dp, int sms, cudaStream_t stream);
+
+// Tensor map of q, or of K or V as [pages][positions][Hkv][D] (packed: one page
+// of all tokens), box {128 bytes of channels, `heads`, `box` positions (, 1
+// page)}, 128-byte swizzle; what lies outside reads as zeros.
+bool attn_map(CUtensorMap* m, const AttnParams& p, const void* base, bool q, int heads, int box);
 
 bool attn_tc_fits(const AttnParams& p);
 size_t attn_tc_workspace(const AttnParams& p);
 cudaError_t launch_attn_tc(const AttnParams& p, void* ws, cudaStream_t stream);
+
+bool attn_tc1_fits(const AttnParams& p);
+size_t attn_tc1_workspace(const AttnParams& p);
+cudaError_t launch_attn_tc1(const AttnParams& p, void* ws, cudaStream_t stream);
 
 bool attn_rows_fits(const AttnParams& p);
 size_t attn_rows_workspace(const AttnParams& p);
