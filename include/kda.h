@@ -541,7 +541,9 @@ kda_status_t kda_prep(const kda_prep_args* args, void* stream);
  * A row that may attend nothing (p_i < 0) gets o = 0.  A value or key at a
  * position a row may not attend never reaches that row through its weight,
  * which is exactly 0 there; whatever the cache or the packed tensors hold
- * behind a sequence's end (infinities and NaN among it) changes nothing.
+ * behind a sequence's end (infinities and NaN among it) changes nothing.  An
+ * infinite value makes its channel infinite in the rows that attend it; an
+ * infinite or NaN key, or query, may make NaN of the rows that meet it.
  * Softmax statistics and sums are fp32; with bf16 inputs the weights are
  * rounded to bf16 before they multiply v (the tensor cores' operand type),
  * an error of at most 2^-8 of each weight, as o's own rounding to bf16.

@@ -270,7 +270,7 @@ cudaError_t launch_attn_plan(const AttnParams& p, const TcArgs& a, cudaStream_t 
   return launch_maybe_dependent(true, attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p, a);
 }
 cudaError_t launch_attn_join(const AttnParams& p, const TcArgs& a, int dp, int sms, cudaStream_t stream) {
-  const dim3 grid((unsigned)(4 * sms));
+  const dim3 grid((unsigned)(16 * sms));
   return p.dt == KDA_BF16 ? join_t<__nv_bfloat16>(p, a, dp, grid, stream) : join_t<float>(p, a, dp, grid, stream);
 }
 

@@ -411,29 +411,35 @@ struct RowsF32 {
     const int live = min(KW, t.end - x0);
     bool poison = false;
     const bool masked = x0 + KW - 1 > t.pos0;
-    if (masked) {
-      // rows of V behind the block's last key to zero; non-finite values that some row may not attend
-      for (int i = lane; i < KW * S::NB * 8; i += 32) {
-        const int r = i / (S::NB * 8), c = i % (S::NB * 8);
-        uint4* x = reinterpret_cast<uint4*>(vs + sw_off(KW * warp + r, c, S::kBlock));
-        if (r >= live) {
-          *x = make_uint4(0, 0, 0, 0);
-        } else if (t.rows > t.gb) {
-          const uint4 y = *x;
-          poison |= ((((y.x & 0x7f800000u) + 0x00800000u) | ((y.y & 0x7f800000u) + 0x00800000u) |
-                      ((y.z & 0x7f800000u) + 0x00800000u) | ((y.w & 0x7f800000u) + 0x00800000u)) & 0x80000000u) != 0;
-        }
+    // rows of V behind the block's last key to zero; non-finite values are
+    // looked for in every tile (split, they would meet parts that are 0)
+    for (int i = lane; i < KW * S::NB * 8; i += 32) {
+      const int r = i / (S::NB * 8), c = i % (S::NB * 8);
+      uint4* x = reinterpret_cast<uint4*>(vs + sw_off(KW * warp + r, c, S::kBlock));
+      if (r >= live) {
+        *x = make_uint4(0, 0, 0, 0);
+      } else {
+        const uint4 y = *x;
+        poison |= ((((y.x & 0x7f800000u) + 0x00800000u) | ((y.y & 0x7f800000u) + 0x00800000u) |
+                    ((y.z & 0x7f800000u) + 0x00800000u) | ((y.w & 0x7f800000u) + 0x00800000u)) & 0x80000000u) != 0;
       }
-      poison = __any_sync(0xffffffffu, poison);
     }
+    poison = __any_sync(0xffffffffu, poison);
     const int r0 = lane >> 2, q2 = lane & 3;
-    float s[MT][NT][4], sx[MT][NT][4];  // h h apart from the smaller products
+    // h h apart from the smaller products; these in two sums where a single
+    // accumulator tile would make one long chain of dependent products
+    constexpr int XS = MT * NT == 1 ? 2 : 1;
+    float s[MT][NT][4], sx[XS][MT][NT][4];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[i][n][e] = sx[i][n][e] = 0.f;
+        for (int e = 0; e < 4; ++e) {
+          s[i][n][e] = 0.f;
+#pragma unroll
+          for (int z = 0; z < XS; ++z) sx[z][i][n][e] = 0.f;
+        }
     const uint32_t qa = smem_u32(qs);
 #pragma unroll 2
     for (int k = 0; k < NK; ++k) {
@@ -454,11 +460,11 @@ struct RowsF32 {
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
           mma16816(s[i][n], ah[i], b0.h, b1.h);
-          mma16816(sx[i][n], ah[i], b0.l, b1.l);
-          mma16816(sx[i][n], al[i], b0.h, b1.h);
-          mma16816(sx[i][n], am[i], b0.m, b1.m);
-          mma16816(sx[i][n], ah[i], b0.m, b1.m);
-          mma16816(sx[i][n], am[i], b0.h, b1.h);
+          mma16816(sx[0][i][n], ah[i], b0.l, b1.l);
+          mma16816(sx[0][i][n], al[i], b0.h, b1.h);
+          mma16816(sx[0][i][n], am[i], b0.m, b1.m);
+          mma16816(sx[XS - 1][i][n], ah[i], b0.m, b1.m);
+          mma16816(sx[XS - 1][i][n], am[i], b0.h, b1.h);
         }
       }
     }
@@ -468,7 +474,8 @@ struct RowsF32 {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[i][n][e] += sx[i][n][e];
+        for (int e = 0; e < 4; ++e) s[i][n][e] += XS == 2 ? sx[0][i][n][e] + sx[XS - 1][i][n][e] : sx[0][i][n][e];
+      limit[i][0] = limit[i][1] = KW - 1;
       if (masked) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) limit[i][h] = min(t.end - 1, t.pos0 + (16 * i + r0 + 8 * h) / t.gb) - x0;
@@ -509,7 +516,7 @@ struct RowsF32 {
           l[i][e >> 1] += s[i][n][e];
         }
     }
-    if (masked && poison) {  // the non-finite values alone into the rows that attend them, then zeros for them
+    if (poison) {  // the non-finite values alone into the rows that attend them, then zeros for them
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
         for (int k = 0; k < live; ++k) {

@@ -105,9 +105,17 @@ def test_scales_and_sharp_rows(dtype, scale, sharp):
     run_prompt([300, 40], 4, 2, 64, dtype, seed=3, scale=scale, sharp=sharp)
 
 
-@pytest.mark.parametrize("D,H,Hkv", [(128, 8, 2), (64, 4, 4)])
-def test_longer_prompts(D, H, Hkv):
-    run_prompt([2500, 1111], H, Hkv, D, "bf16", seed=9)
+@pytest.mark.parametrize("D,H,Hkv,dtype", [(128, 8, 2, "bf16"), (64, 4, 4, "bf16"), (256, 6, 2, "bf16"),
+                                           (128, 8, 2, "f32"), (64, 4, 4, "f32"), (32, 8, 2, "f32"), (256, 6, 2, "f32")])
+def test_longer_prompts(D, H, Hkv, dtype):
+    run_prompt([2500, 1111], H, Hkv, D, dtype, seed=9)
+
+
+@pytest.mark.parametrize("D,dtype", [(128, "bf16"), (256, "bf16"), (64, "f32")])
+def test_many_short_prompts(D, dtype):
+    """More sequences than a CTA plans at once, among them empty ones."""
+    lens = [(7 * i) % 5 for i in range(1300)]
+    run_prompt(lens, 4, 2, D, dtype, seed=10)
 
 
 def test_rising_logits():
@@ -151,7 +159,7 @@ def test_a_neighbour_with_infinities_changes_nothing(dtype, D):
         check(o[b:e], *reference(q[b:e], k[b:e], v[b:e], 0, D ** -0.5, dtype))
 
 
-@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("bf16", 64), ("bf16", 256), ("f32", 128)])
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("bf16", 64), ("bf16", 256), ("f32", 128), ("f32", 256)])
 @pytest.mark.parametrize("at", [0, 5, 100, 299])
 def test_later_tokens_never_reach_earlier_rows(dtype, D, at):
     """Infinities and NaN from position `at` on: the rows before it are as they were."""
@@ -273,6 +281,22 @@ def test_long_contexts_of_few_requests(page, new):
     run_paged([5000, 777], [new, 1], 8, 2, 128, page, "bf16", seed=page + new)
     run_paged([4097], [new], 4, 1, 64, page, "bf16", seed=page + new)
     run_paged([2000], [new], 4, 2, 64, page, "f32", seed=page + new)
+    run_paged([3000, 100], [new, new], 8, 2, 256, page, "bf16", seed=page + new)
+    run_paged([1500, 900], [new, 1], 8, 2, 128, page, "f32", seed=page + new)
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("bf16", 256), ("f32", 128), ("f32", 256)])
+def test_a_chunk_beside_decoding_requests(dtype, D):
+    run_paged([3000, 17, 900, 2500, 0, 64], [200, 1, 1, 1, 1, 3], 8, 2, D, 32, dtype, seed=D)
+
+
+@pytest.mark.parametrize("dtype,D,new", [("bf16", 128, 1), ("bf16", 64, 1), ("f32", 64, 1), ("f32", 64, 20)])
+def test_many_requests(dtype, D, new):
+    """More requests than a CTA plans at once, with skipped and empty ones between."""
+    n = 700
+    ctx = [(13 * i) % 90 for i in range(n)]
+    lens = [0 if i % 7 == 3 else 1 + i % new for i in range(n)]
+    run_paged(ctx, lens, 4, 2, D, 16, dtype, seed=new)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -337,6 +361,33 @@ def test_rows_before_the_first_position_are_zero(dtype, D):
         assert (a.o[b:b + dead] == 0).all()
         if have[i]:
             check(a.o[b + dead:e], *reference(q[b + dead:e], p.K[i], p.V[i], 0, D ** -0.5, dtype))
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 64), ("bf16", 128), ("bf16", 256), ("f32", 64), ("f32", 128), ("f32", 256)])
+@pytest.mark.parametrize("new", [3, 60])
+def test_infinite_values_reach_the_rows_that_attend_them(dtype, D, new):
+    """One infinite value, and one NaN, in the cache: their channels in the rows from there on, nothing else."""
+    ctx = 150
+    p = Pool([ctx], [new], 2, D, 16, dtype, 6)
+    q = rand(gen(12), new, 4, D, dtype=dtype)
+    cu = cu_of([new]).cuda()
+
+    def put(x, head, c, value):
+        page, off = int(p.table[0, x // 16]), x % 16
+        p.v[page, off, head, c] = value
+
+    put(ctx + 1, 0, 5, float("inf"))       # among the new tokens
+    put(ctx + new - 1, 1, 7, float("nan"))
+    p.V[0][ctx + 1, 0, 5] = 0
+    p.V[0][ctx + new - 1, 1, 7] = 0
+    a = kda.AttnPaged(q, p.k, p.v, p.table, p.lens, cu, max_seqlen=new).run()
+    ref, tol = reference(q, p.K[0], p.V[0], ctx, D ** -0.5, dtype)
+    o = a.o.clone()
+    assert torch.isposinf(o[1:, 0:2, 5]).all() and torch.isfinite(o[0, 0:2, 5]).all()
+    assert torch.isnan(o[-1, 2:4, 7]).all() and torch.isfinite(o[:-1, 2:4, 7]).all()
+    o[1:, 0:2, 5], o[-1, 2:4, 7] = 0, 0
+    tol[1:, 0:2, 5], tol[-1, 2:4, 7] = 1e9, 1e9
+    check(o, ref, tol)
 
 
 def test_slots_past_32_bit_offsets():
