@@ -564,12 +564,17 @@ struct RowsF32 {
       const Split b0 = split3(y[0], y[1]), b1 = split3(y[2 * NT - 2], y[2 * NT - 1]);
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
-        mma_keys<NT>(o[i][v], ah[i], b0.l, b1.l);
-        mma_keys<NT>(o[i][v], al[i], b0.h, b1.h);
-        mma_keys<NT>(o[i][v], am[i], b0.m, b1.m);
-        mma_keys<NT>(o[i][v], ah[i], b0.m, b1.m);
-        mma_keys<NT>(o[i][v], am[i], b0.h, b1.h);
-        mma_keys<NT>(o[i][v], ah[i], b0.h, b1.h);
+        // from zero, and added rounded to nearest: the tensor cores' own
+        // accumulation cuts, a bias that grows with the tiles
+        float y4[4] = {0.f, 0.f, 0.f, 0.f};
+        mma_keys<NT>(y4, ah[i], b0.l, b1.l);
+        mma_keys<NT>(y4, al[i], b0.h, b1.h);
+        mma_keys<NT>(y4, am[i], b0.m, b1.m);
+        mma_keys<NT>(y4, ah[i], b0.m, b1.m);
+        mma_keys<NT>(y4, am[i], b0.h, b1.h);
+        mma_keys<NT>(y4, ah[i], b0.h, b1.h);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][v][e] += y4[e];
       }
     }
   }

@@ -24,7 +24,7 @@ namespace kda {
 constexpr int kFewRows = 32;
 constexpr int kRowTile = 128;  // rows of a row tile
 constexpr int kSplitSms = 152;
-constexpr int kPiecesPerSm = 1;
+constexpr int kPiecesPerSm = 2;
 constexpr int kMinPiece = 4;
 // Rows of up to this many positions are not worth cutting in a small call
 constexpr int kSelfPlanKeys = 2048;
