@@ -413,68 +413,84 @@ struct RowsF32 {
     const bool masked = x0 + KW - 1 > t.pos0;
     // rows of V behind the block's last key to zero; non-finite values are
     // looked for in every tile (split, they would meet parts that are 0)
-    for (int i = lane; i < KW * S::NB * 8; i += 32) {
-      const int r = i / (S::NB * 8), c = i % (S::NB * 8);
-      uint4* x = reinterpret_cast<uint4*>(vs + sw_off(KW * warp + r, c, S::kBlock));
-      if (r >= live) {
-        *x = make_uint4(0, 0, 0, 0);
-      } else {
-        const uint4 y = *x;
-        poison |= ((((y.x & 0x7f800000u) + 0x00800000u) | ((y.y & 0x7f800000u) + 0x00800000u) |
-                    ((y.z & 0x7f800000u) + 0x00800000u) | ((y.w & 0x7f800000u) + 0x00800000u)) & 0x80000000u) != 0;
-      }
+    if (live < KW) {
+      for (int i = live * S::NB * 8 + lane; i < KW * S::NB * 8; i += 32)
+        *reinterpret_cast<uint4*>(vs + sw_off(KW * warp + i / (S::NB * 8), i % (S::NB * 8), S::kBlock)) =
+            make_uint4(0, 0, 0, 0);
+      __syncwarp();
     }
+    uint32_t seen = 0;
+#pragma unroll 8
+    for (int i = lane; i < KW * S::NB * 8; i += 32) {
+      const uint4 y = *reinterpret_cast<const uint4*>(vs + sw_off(KW * warp + i / (S::NB * 8), i % (S::NB * 8), S::kBlock));
+      seen |= ((y.x & 0x7f800000u) + 0x00800000u) | ((y.y & 0x7f800000u) + 0x00800000u) |
+              ((y.z & 0x7f800000u) + 0x00800000u) | ((y.w & 0x7f800000u) + 0x00800000u);
+    }
+    poison = (seen & 0x80000000u) != 0;
     poison = __any_sync(0xffffffffu, poison);
     const int r0 = lane >> 2, q2 = lane & 3;
-    // h h apart from the smaller products; these in two sums where a single
-    // accumulator tile would make one long chain of dependent products
-    constexpr int XS = MT * NT == 1 ? 2 : 1;
-    float s[MT][NT][4], sx[XS][MT][NT][4];
+    // h h apart from the smaller products, and (one key tile of 8) even from odd
+    // steps: products that follow one another are of different sums
+    constexpr int KS = MT * NT == 1 ? 2 : 1;
+    float s[MT][NT][4], sh[KS][MT][NT][4], sx[KS][2][MT][NT][4];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int z = 0; z < KS; ++z) sh[z][i][n][e] = sx[z][0][i][n][e] = sx[z][1][i][n][e] = 0.f;
+    const uint32_t qa = smem_u32(qs);
+#pragma unroll (MT == 1 ? 4 / KS : 1)
+    for (int k0 = 0; k0 < NK; k0 += KS) {
+#pragma unroll
+      for (int z = 0; z < KS; ++z) {
+        const int k = k0 + z;
+        uint32_t ah[MT][4], am[MT][4], al[MT][4];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          const uint32_t off = sw_off(16 * i + (lane & 7) + ((lane >> 3) & 1) * 8, 2 * k + (lane >> 4), S::kQBlock);
+          ldsm4(ah[i], qa + off);
+          ldsm4(am[i], qa + S::kQPlane + off);
+          ldsm4(al[i], qa + 2 * S::kQPlane + off);
+        }
+        Split b0[NT], b1[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const int row = KW * warp + 8 * n + r0;
+          const float2 x = *reinterpret_cast<const float2*>(stage + sw_off(row, 4 * k + (q2 >> 1), S::kBlock) + (q2 & 1) * 8);
+          const float2 y = *reinterpret_cast<const float2*>(stage + sw_off(row, 4 * k + 2 + (q2 >> 1), S::kBlock) + (q2 & 1) * 8);
+          b0[n] = split3(x.x, x.y);
+          b1[n] = split3(y.x, y.y);
+        }
+#pragma unroll
+        for (int r = 0; r < 3; ++r)
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              if (r == 0) mma16816(sx[z][0][i][n], ah[i], b0[n].l, b1[n].l);
+              if (r == 1) mma16816(sx[z][0][i][n], al[i], b0[n].h, b1[n].h);
+              if (r == 2) mma16816(sx[z][0][i][n], am[i], b0[n].m, b1[n].m);
+              if (r == 0) mma16816(sh[z][i][n], ah[i], b0[n].h, b1[n].h);
+              if (r == 1) mma16816(sx[z][1][i][n], ah[i], b0[n].m, b1[n].m);
+              if (r == 2) mma16816(sx[z][1][i][n], am[i], b0[n].h, b1[n].h);
+            }
+      }
+    }
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          s[i][n][e] = 0.f;
-#pragma unroll
-          for (int z = 0; z < XS; ++z) sx[z][i][n][e] = 0.f;
+          s[i][n][e] = (sx[0][0][i][n][e] + sx[0][1][i][n][e]) + sh[0][i][n][e];
+          if (KS == 2) s[i][n][e] += (sx[KS - 1][0][i][n][e] + sx[KS - 1][1][i][n][e]) + sh[KS - 1][i][n][e];
         }
-    const uint32_t qa = smem_u32(qs);
-#pragma unroll 2
-    for (int k = 0; k < NK; ++k) {
-      uint32_t ah[MT][4], am[MT][4], al[MT][4];
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const uint32_t off = sw_off(16 * i + (lane & 7) + ((lane >> 3) & 1) * 8, 2 * k + (lane >> 4), S::kQBlock);
-        ldsm4(ah[i], qa + off);
-        ldsm4(am[i], qa + S::kQPlane + off);
-        ldsm4(al[i], qa + 2 * S::kQPlane + off);
-      }
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int row = KW * warp + 8 * n + r0;
-        const float2 x = *reinterpret_cast<const float2*>(stage + sw_off(row, 4 * k + (q2 >> 1), S::kBlock) + (q2 & 1) * 8);
-        const float2 y = *reinterpret_cast<const float2*>(stage + sw_off(row, 4 * k + 2 + (q2 >> 1), S::kBlock) + (q2 & 1) * 8);
-        const Split b0 = split3(x.x, x.y), b1 = split3(y.x, y.y);
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          mma16816(s[i][n], ah[i], b0.h, b1.h);
-          mma16816(sx[0][i][n], ah[i], b0.l, b1.l);
-          mma16816(sx[0][i][n], al[i], b0.h, b1.h);
-          mma16816(sx[0][i][n], am[i], b0.m, b1.m);
-          mma16816(sx[XS - 1][i][n], ah[i], b0.m, b1.m);
-          mma16816(sx[XS - 1][i][n], am[i], b0.h, b1.h);
-        }
-      }
-    }
     int limit[MT][2];
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[i][n][e] += XS == 2 ? sx[0][i][n][e] + sx[XS - 1][i][n][e] : sx[0][i][n][e];
       limit[i][0] = limit[i][1] = KW - 1;
       if (masked) {
 #pragma unroll
@@ -553,29 +569,49 @@ struct RowsF32 {
         am[i][z] = y.m;
         al[i][z] = y.l;
       }
+    // VG groups of 8 channels at a time: products that follow one another are
+    // of different sums (one after the other on one sum, their latency would rule)
+    constexpr int VG = 4 / MT;
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      // keys 2 q2, + 1 (, + 8, + 9) of channel 8 v + r0
-      float y[2 * NT];
+    for (int v = 0; v < NV; v += VG) {
+      Split b0[VG], b1[VG];
 #pragma unroll
-      for (int i = 0; i < 2 * NT; ++i)
-        y[i] = *reinterpret_cast<const float*>(
-            vs + sw_off(KW * warp + 2 * q2 + (i & 1) + 8 * (i >> 1), 2 * v + (r0 >> 2), S::kBlock) + (r0 & 3) * 4);
-      const Split b0 = split3(y[0], y[1]), b1 = split3(y[2 * NT - 2], y[2 * NT - 1]);
+      for (int g = 0; g < VG; ++g) {
+        // keys 2 q2, + 1 (, + 8, + 9) of channel 8 (v + g) + r0
+        float y[2 * NT];
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        // from zero, and added rounded to nearest: the tensor cores' own
-        // accumulation cuts, a bias that grows with the tiles
-        float y4[4] = {0.f, 0.f, 0.f, 0.f};
-        mma_keys<NT>(y4, ah[i], b0.l, b1.l);
-        mma_keys<NT>(y4, al[i], b0.h, b1.h);
-        mma_keys<NT>(y4, am[i], b0.m, b1.m);
-        mma_keys<NT>(y4, ah[i], b0.m, b1.m);
-        mma_keys<NT>(y4, am[i], b0.h, b1.h);
-        mma_keys<NT>(y4, ah[i], b0.h, b1.h);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[i][v][e] += y4[e];
+        for (int i = 0; i < 2 * NT; ++i)
+          y[i] = *reinterpret_cast<const float*>(
+              vs + sw_off(KW * warp + 2 * q2 + (i & 1) + 8 * (i >> 1), 2 * (v + g) + (r0 >> 2), S::kBlock) + (r0 & 3) * 4);
+        b0[g] = split3(y[0], y[1]);
+        b1[g] = split3(y[2 * NT - 2], y[2 * NT - 1]);
       }
+      // from zero, and added rounded to nearest: the tensor cores' own
+      // accumulation cuts, a bias that grows with the tiles
+      float y4[MT][VG][4];
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int g = 0; g < VG; ++g)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y4[i][g][e] = 0.f;
+#pragma unroll
+      for (int z = 0; z < 6; ++z)
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int g = 0; g < VG; ++g) {
+            const uint32_t* x = z == 1 ? al[i] : z == 2 || z == 4 ? am[i] : ah[i];
+            const uint32_t c0 = z == 0 ? b0[g].l : z == 2 || z == 3 ? b0[g].m : b0[g].h;
+            const uint32_t c1 = z == 0 ? b1[g].l : z == 2 || z == 3 ? b1[g].m : b1[g].h;
+            mma_keys<NT>(y4[i][g], x, c0, c1);
+          }
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int g = 0; g < VG; ++g)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[i][v + g][e] += y4[i][g][e];
     }
   }
   __device__ void stats(float2* ml, int lane) {
