@@ -22,6 +22,8 @@
 // single tokens, and the tensor cores wait for memory either way); the
 // weights are rounded to bf16, as P V's operand.  fp32: the same with every
 // operand in three bf16 parts.
+#include <algorithm>
+
 #include "kda_attn_tc.cuh"
 
 namespace kda {
@@ -66,6 +68,8 @@ struct Tile {
   int32_t x0;           // position of the tile's first key
   int32_t first, last;  // of the block in this stretch
   int32_t slot;         // at the last tile: where the part goes, or -1 (the block is whole)
+  int32_t base;         // first packed token of the sequence, or its row of the block table
+  int32_t kvh;          // key head
 };
 
 struct Tail {
@@ -78,7 +82,7 @@ struct Tail {
   int64_t sum[kWarps + 1];
   int64_t found;   // where in its sequence's tiles the stretch starts
   int32_t found_at;
-  int32_t pad2;
+  int32_t poison[3];  // positions whose non-finite values were taken out of the block's V
   AttnSeq found_seq;
 };
 static_assert(sizeof(Tail) <= 2048, "tail block");
@@ -97,8 +101,9 @@ struct RowsArgs {
 };
 
 // a / b for a >= 0, b > 0: the quick way where both are small
+__device__ __noinline__ int64_t div_large(int64_t a, int64_t b) { return a / b; }
 __device__ __forceinline__ int64_t div_any(int64_t a, int64_t b) {
-  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : div_large(a, b);
 }
 
 // The blocks of a sequence for one head (part): n of them, block i with
@@ -178,23 +183,35 @@ __device__ __forceinline__ void mma_keys(float* d, const uint32_t* a, uint32_t b
   if constexpr (NT == 2) mma16816(d, a, b0, b1);
   else mma1688(d, a, b0);
 }
-// The weights of key k for the two rows of a lane, from the accumulator layout
-// p[n][e] of a 16 x 8 NT tile (every lane of the warp calls)
-template <int NT>
-__device__ __forceinline__ void weight_of(const float* p, int k, int lane, float* w) {
-  const int src = (lane & ~3) | ((k & 7) >> 1);
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    w[h] = 0.f;
-#pragma unroll
-    for (int z = 0; z < 2 * NT; ++z) {  // its register, by a fixed index
-      const int n = z >> 1, e = z & 1;
-      const float c = __shfl_sync(0xffffffffu, p[4 * n + 2 * h + e], src);
-      if (n == (k >> 3) && e == (k & 1)) w[h] = c;
+// Non-finite values among keys [key0, key0 + n) of a V tile (x0: position of the
+// tile's first key) become zeros; range takes in the positions they had.  The
+// block's outputs get them back when they are written (poison_of).
+template <typename T, int NB>
+__device__ __noinline__ void take_out(char* vs, uint32_t block, int key0, int n, int x0, int32_t* range, int lane) {
+  int lo = INT32_MAX, hi = -1;
+#pragma unroll 1
+  for (int i = lane; i < n * NB * 8; i += 32) {
+    const int r = key0 + i / (NB * 8);
+    uint4* at = reinterpret_cast<uint4*>(vs + sw_off(r, i % (NB * 8), block));
+    const uint4 x = *at;
+    uint4 y;
+    if constexpr (sizeof(T) == 2) {
+      y = make_uint4(finite_only(x.x), finite_only(x.y), finite_only(x.z), finite_only(x.w));
+    } else {
+      auto keep = [](uint32_t v) { return (v & 0x7f800000u) == 0x7f800000u ? 0u : v; };
+      y = make_uint4(keep(x.x), keep(x.y), keep(x.z), keep(x.w));
+    }
+    if (x.x != y.x || x.y != y.y || x.z != y.z || x.w != y.w) {
+      *at = y;
+      lo = min(lo, x0 + r);
+      hi = max(hi, x0 + r);
     }
   }
+  if (hi >= 0) {
+    atomicMin_block(&range[0], lo);
+    atomicMax_block(&range[1], hi);
+  }
 }
-__device__ __forceinline__ bool finite(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
 
 // One quarter-tile's work and its running state, bf16
 template <int DP>
@@ -218,7 +235,7 @@ struct RowsBf16 {
     l[0] = l[1] = 0.f;
   }
 
-  __device__ void step(char* stage, const float*, const Tile& t, float sc, int warp, int lane) {
+  __device__ void step(char* stage, const float*, const Tile& t, float sc, int32_t* range, int warp, int lane) {
     const int x0 = t.x0 + 16 * warp;  // this warp's keys
     if (x0 >= t.end) return;
     const uint32_t ks = smem_u32(stage);
@@ -299,30 +316,7 @@ struct RowsBf16 {
         s[n][e] = exp2_fast(fmaf(s[n][e], sc, -ref[e >> 1]));
         l[e >> 1] += s[n][e];
       }
-    if (masked && poison) {  // the non-finite values alone into the rows that attend them, then zeros for them
-      const float* p0 = &s[0][0];
-      for (int k = 0; k < live; ++k) {
-        float w[2];
-        weight_of<2>(p0, k, lane, w);
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          const uint32_t y = *reinterpret_cast<const uint32_t*>(vs + sw_off(16 * warp + k, v, S::kBlock) + 4 * (lane & 3));
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            if (k <= limit[h]) {
-              if ((y & 0x7f80u) == 0x7f80u) o[v][2 * h] = fmaf(w[h], __uint_as_float(y << 16), o[v][2 * h]);
-              if ((y & 0x7f800000u) == 0x7f800000u)
-                o[v][2 * h + 1] = fmaf(w[h], __uint_as_float(y & 0xffff0000u), o[v][2 * h + 1]);
-            }
-        }
-      }
-      __syncwarp();
-      for (int i = lane; i < 16 * S::NB * 8; i += 32) {
-        uint4* x4 = reinterpret_cast<uint4*>(vs + sw_off(16 * warp + i / (S::NB * 8), i % (S::NB * 8), S::kBlock));
-        const uint4 y = *x4;
-        *x4 = make_uint4(finite_only(y.x), finite_only(y.y), finite_only(y.z), finite_only(y.w));
-      }
-    }
+    if (masked && poison) take_out<__nv_bfloat16, S::NB>(vs, S::kBlock, 16 * warp, 16, t.x0, range, lane);
     __syncwarp();  // V's zeroed rows
     const uint32_t a[4] = {pack2(s[0][0], s[0][1]), pack2(s[0][2], s[0][3]), pack2(s[1][0], s[1][1]),
                            pack2(s[1][2], s[1][3])};
@@ -404,7 +398,7 @@ struct RowsF32 {
     }
   }
 
-  __device__ void step(char* stage, const float* qs, const Tile& t, float sc, int warp, int lane) {
+  __device__ void step(char* stage, const float* qs, const Tile& t, float sc, int32_t* range, int warp, int lane) {
     const int x0 = t.x0 + KW * warp;  // this warp's keys
     if (x0 >= t.end) return;
     char* vs = stage + S::NB * S::kBlock;
@@ -532,32 +526,7 @@ struct RowsF32 {
           l[i][e >> 1] += s[i][n][e];
         }
     }
-    if (poison) {  // the non-finite values alone into the rows that attend them, then zeros for them
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        for (int k = 0; k < live; ++k) {
-          float w[2];
-          weight_of<NT>(&s[i][0][0], k, lane, w);
-#pragma unroll
-          for (int v = 0; v < NV; ++v) {
-            const float2 y = *reinterpret_cast<const float2*>(vs + sw_off(KW * warp + k, 2 * v + (q2 >> 1), S::kBlock) + (q2 & 1) * 8);
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              if (k <= limit[i][h]) {
-                if (!finite(y.x)) o[i][v][2 * h] = fmaf(w[h], y.x, o[i][v][2 * h]);
-                if (!finite(y.y)) o[i][v][2 * h + 1] = fmaf(w[h], y.y, o[i][v][2 * h + 1]);
-              }
-          }
-        }
-      }
-      __syncwarp();
-      for (int i = lane; i < KW * S::NB * 8; i += 32) {
-        float4* x4 = reinterpret_cast<float4*>(vs + sw_off(KW * warp + i / (S::NB * 8), i % (S::NB * 8), S::kBlock));
-        const float4 y = *x4;
-        *x4 = make_float4(finite(y.x) ? y.x : 0.f, finite(y.y) ? y.y : 0.f, finite(y.z) ? y.z : 0.f,
-                          finite(y.w) ? y.w : 0.f);
-      }
-    }
+    if (poison) take_out<float, S::NB>(vs, S::kBlock, KW * warp, KW, t.x0, range, lane);
     __syncwarp();  // V's zeroed rows
     uint32_t ah[MT][2 * NT], am[MT][2 * NT], al[MT][2 * NT];
 #pragma unroll
@@ -664,6 +633,8 @@ __global__ void __launch_bounds__(kThreads, Shape<T, DP, Work::kRows>::CTAS)
     mbar_init(&b->join[0], kWarps);
     mbar_init(&b->join[1], kWarps);
     b->dead = 0;
+    b->poison[0] = INT32_MAX;
+    b->poison[1] = -1;
     mbar_init_fence();
   }
   if (tid == 32) {
@@ -795,6 +766,8 @@ __global__ void __launch_bounds__(kThreads, Shape<T, DP, Work::kRows>::CTAS)
         t.pos0 = pos0;
         t.end = end;
         t.x0 = x0;
+        t.base = p.block_table ? sq.row : (int)sq.tok0;
+        t.kvh = kvh;
         t.first = seg_first;
         t.last = last;
         t.slot = -1;
@@ -873,7 +846,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, DP, Work::kRows>::CTAS)
         }
         w.start(stage, qs, lane);
       }
-      w.step(stage, qs, t, sc, warp, lane);
+      w.step(stage, qs, t, sc, b->poison, warp, lane);
       if (t.last) {
         const int rows = t.rows;
         w.stats(b->ml[warp], lane);
@@ -904,6 +877,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, DP, Work::kRows>::CTAS)
         if (!__all_sync(0xffffffffu, wait_or_dead(&b->join[1], joins & 1, &b->dead))) break;
         ++joins;
         T* out = static_cast<T*>(p.o);
+        const bool poisoned = *reinterpret_cast<volatile int32_t*>(&b->poison[1]) >= 0;
 #pragma unroll
         for (int i = 0; i < STEPS; ++i) {
           const int e = i * 32 * kWarps + tid, r = e / VEC, c = (e % VEC) * 4;
@@ -916,6 +890,22 @@ __global__ void __launch_bounds__(kThreads, Shape<T, DP, Work::kRows>::CTAS)
             x.y += y.y;
             x.z += y.z;
             x.w += y.w;
+          }
+          if (poisoned) {
+            const int64_t stride = (int64_t)p.Hkv * p.D;
+            const T* v = static_cast<const T*>(p.v) + (int64_t)t.kvh * p.D + c + (p.block_table ? 0 : t.base * stride);
+            const int32_t* pages = p.block_table ? p.block_table + (int64_t)t.base * p.max_pages : nullptr;
+            const int to = min(b->poison[1], min(t.end - 1, t.pos0 + r / t.gb));
+#pragma unroll 1
+            for (int u = 0; u < 4 && c + u < p.D; ++u) {
+              const float z = poison_of(v + u, stride, pages, p.num_pages, p.page_shift, b->poison[0], to);
+              const float y = u == 0 ? x.x : u == 1 ? x.y : u == 2 ? x.z : x.w;
+              const float s = z != 0.f ? y + z : y;  // a NaN already there stays
+              if (u == 0) x.x = s;
+              else if (u == 1) x.y = s;
+              else if (u == 2) x.z = s;
+              else x.w = s;
+            }
           }
           if (t.slot >= 0) {
             *reinterpret_cast<float4*>(a.o + ((int64_t)t.slot * kMaxRows + r) * DP + c) = x;
@@ -942,49 +932,52 @@ __global__ void __launch_bounds__(kThreads, Shape<T, DP, Work::kRows>::CTAS)
 }
 
 // The blocks that cross stretches: parts 2 c + 1, 2 (c + 1), 2 (c + 2), .. of
-// stretch c.  A CTA per row, the parts dealt to its warps, which are then added
-// in their order.
-constexpr int kJoinWarps = 8;
+// stretch c.  A CTA per row at a time, the parts dealt to its warps, which are
+// then added in their order.
+constexpr int kJoinWarps = 8, kJoinRows = 16;
 template <typename T, int DP>
 __global__ void __launch_bounds__(32 * kJoinWarps) attn_rows_join(const AttnParams p, const RowsArgs a) {
   __shared__ float sm_o[kJoinWarps][DP];
   __shared__ float sm_l[kJoinWarps];
   pdl_wait();
   const RowsJoin jn = a.joins[blockIdx.x];
-  const int r = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (jn.parts == 0 || r >= jn.rows) return;
+  if (jn.parts == 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int V = DP / 32;
   const int s0 = 2 * (int)blockIdx.x;
-  auto slot = [&](int k) { return (k == 0 ? s0 + 1 : s0 + 2 * k) * kMaxRows + r; };
-  float M = -INFINITY;
-  for (int k = lane; k < jn.parts; k += 32) M = fmaxf(M, a.ml[slot(k)].x);
+  for (int r = blockIdx.y; r < jn.rows; r += gridDim.y) {
+    auto slot = [&](int k) { return (k == 0 ? s0 + 1 : s0 + 2 * k) * kMaxRows + r; };
+    float M = -INFINITY;
+    for (int k = lane; k < jn.parts; k += 32) M = fmaxf(M, a.ml[slot(k)].x);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  if (M == -INFINITY) M = 0.f;
-  float l = 0.f, o[V];
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    if (M == -INFINITY) M = 0.f;
+    float l = 0.f, o[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) o[v] = 0.f;
+    for (int v = 0; v < V; ++v) o[v] = 0.f;
 #pragma unroll 4
-  for (int k = warp; k < jn.parts; k += kJoinWarps) {
-    const float2 ml = a.ml[slot(k)];
-    const float f = exp2f(ml.x - M);
-    l = fmaf(f, ml.y, l);
+    for (int k = warp; k < jn.parts; k += kJoinWarps) {
+      const float2 ml = a.ml[slot(k)];
+      const float f = exp2f(ml.x - M);
+      l = fmaf(f, ml.y, l);
 #pragma unroll
-    for (int v = 0; v < V; ++v) o[v] = fmaf(f, a.o[(int64_t)slot(k) * DP + 32 * v + lane], o[v]);
-  }
+      for (int v = 0; v < V; ++v) o[v] = fmaf(f, a.o[(int64_t)slot(k) * DP + 32 * v + lane], o[v]);
+    }
+    __syncthreads();  // the row before is written
 #pragma unroll
-  for (int v = 0; v < V; ++v) sm_o[warp][32 * v + lane] = o[v];
-  if (lane == 0) sm_l[warp] = l;
-  __syncthreads();
-  const int64_t at = ((int64_t)(jn.tok0 + r / jn.gb) * p.H + jn.head0 + r % jn.gb) * p.D;
-  float sum = 0.f;
+    for (int v = 0; v < V; ++v) sm_o[warp][32 * v + lane] = o[v];
+    if (lane == 0) sm_l[warp] = l;
+    __syncthreads();
+    const int64_t at = ((int64_t)(jn.tok0 + r / jn.gb) * p.H + jn.head0 + r % jn.gb) * p.D;
+    float sum = 0.f;
 #pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) sum += sm_l[w];
-  for (int c = threadIdx.x; c < p.D; c += 32 * kJoinWarps) {
-    float x = 0.f;
+    for (int w = 0; w < kJoinWarps; ++w) sum += sm_l[w];
+    for (int c = threadIdx.x; c < p.D; c += 32 * kJoinWarps) {
+      float x = 0.f;
 #pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) x += sm_o[w][c];
-    st_out(static_cast<T*>(p.o), at + c, sum == 0.f ? 0.f : x / sum);
+      for (int w = 0; w < kJoinWarps; ++w) x += sm_o[w][c];
+      st_out(static_cast<T*>(p.o), at + c, sum == 0.f ? 0.f : x / sum);
+    }
   }
 }
 
@@ -1036,7 +1029,7 @@ cudaError_t launch_w(const AttnParams& p, char* w, cudaStream_t stream) {
                              mv);
   if (e != cudaSuccess) return e;
   return launch_maybe_dependent(true, attn_rows_join<T, DP>,
-                                dim3((unsigned)grid, (unsigned)(heads << a.q_shift)),
+                                dim3((unsigned)grid, (unsigned)std::min(heads << a.q_shift, kJoinRows)),
                                 dim3(32 * kJoinWarps), 0, stream, p, a);
 }
 

@@ -365,27 +365,6 @@ __device__ void mma_role(const AttnParams& p, const TcArgs& a, char* sm, Bars* b
 }
 
 // ------------------------------------------------------------------ softmax and outputs
-// The non-finite values taken out of an item's V tiles, put back into one row
-// (slow path): every channel that an attended position poisons takes its
-// infinity, or NaN where it meets both signs or a NaN.
-__device__ __noinline__ float poison_of(const __nv_bfloat16* v, int64_t stride, const int32_t* pages, int num_pages,
-                                        int shift, int from, int limit) {
-  bool pos = false, neg = false, nan = false;
-  for (int x = from; x <= limit; ++x) {
-    int64_t at = x;
-    if (pages) {
-      const int32_t page = pages[x >> shift];
-      if (page < 0 || page >= num_pages) continue;
-      at = ((int64_t)page << shift) + (x & ((1 << shift) - 1));
-    }
-    const float y = __bfloat162float(v[at * stride]);
-    pos |= y == INFINITY;
-    neg |= y == -INFINITY;
-    nan |= y != y;
-  }
-  return nan || (pos && neg) ? NAN : pos ? INFINITY : neg ? -INFINITY : 0.f;
-}
-
 template <int DP>
 __device__ void softmax_role(const AttnParams& p, const TcArgs& a, Bars* b, int64_t total, int tpt) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

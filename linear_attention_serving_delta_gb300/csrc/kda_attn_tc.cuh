@@ -128,6 +128,28 @@ __device__ __forceinline__ Boxes boxes_of(const AttnParams& p, const AttnItem& i
   return r;
 }
 
+// The non-finite values taken out of V tiles, put back into one channel of one
+// row (slow path): what the attended positions from..limit give it, an infinity,
+// or NaN where both signs or a NaN meet; 0 for none.
+template <typename T>
+static __device__ __noinline__ float poison_of(const T* v, int64_t stride, const int32_t* pages, int num_pages, int shift,
+                                        int from, int limit) {
+  bool pos = false, neg = false, nan = false;
+  for (int x = from; x <= limit; ++x) {
+    int64_t at = x;
+    if (pages) {
+      const int32_t page = pages[x >> shift];
+      if (page < 0 || page >= num_pages) continue;
+      at = ((int64_t)page << shift) + (x & ((1 << shift) - 1));
+    }
+    const float y = ld_in(v, at * stride);
+    pos |= y == INFINITY;
+    neg |= y == -INFINITY;
+    nan |= y != y;
+  }
+  return nan || (pos && neg) ? NAN : pos ? INFINITY : neg ? -INFINITY : 0.f;
+}
+
 namespace tc {
 
 // descriptor of a 128-byte swizzled operand (see above)

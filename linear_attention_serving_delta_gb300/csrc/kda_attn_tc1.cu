@@ -452,26 +452,6 @@ __device__ void mma_role(const AttnParams& p, const TcArgs& a, char* sm, Bars* b
 }
 
 // ------------------------------------------------------------------ softmax and outputs
-// The non-finite values taken out of V, put back into one row (slow path): see kda_attn_tc.cu
-template <typename T>
-__device__ __noinline__ float poison_of(const T* v, int64_t stride, const int32_t* pages, int num_pages, int shift,
-                                        int from, int limit) {
-  bool pos = false, neg = false, nan = false;
-  for (int x = from; x <= limit; ++x) {
-    int64_t at = x;
-    if (pages) {
-      const int32_t page = pages[x >> shift];
-      if (page < 0 || page >= num_pages) continue;
-      at = ((int64_t)page << shift) + (x & ((1 << shift) - 1));
-    }
-    const float y = ld_in(v, at * stride);
-    pos |= y == INFINITY;
-    neg |= y == -INFINITY;
-    nan |= y != y;
-  }
-  return nan || (pos && neg) ? NAN : pos ? INFINITY : neg ? -INFINITY : 0.f;
-}
-
 template <int NP, int DP>
 __device__ void softmax_role(const AttnParams& p, const TcArgs& a, Bars* b, int64_t total) {
   using S = Shape<NP, DP>;
