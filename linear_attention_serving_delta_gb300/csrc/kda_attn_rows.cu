@@ -82,7 +82,7 @@ struct Tail {
   int64_t sum[kWarps + 1];
   int64_t found;   // where in its sequence's tiles the stretch starts
   int32_t found_at;
-  int32_t poison[3];  // positions whose non-finite values were taken out of the block's V
+  int32_t poison[3][2];  // positions whose non-finite values were taken out of a block's V: its k-th in turn
   AttnSeq found_seq;
 };
 static_assert(sizeof(Tail) <= 2048, "tail block");
@@ -633,8 +633,10 @@ __global__ void __launch_bounds__(kThreads, Shape<T, DP, Work::kRows>::CTAS)
     mbar_init(&b->join[0], kWarps);
     mbar_init(&b->join[1], kWarps);
     b->dead = 0;
-    b->poison[0] = INT32_MAX;
-    b->poison[1] = -1;
+    for (int s = 0; s < 3; ++s) {
+      b->poison[s][0] = INT32_MAX;
+      b->poison[s][1] = -1;
+    }
     mbar_init_fence();
   }
   if (tid == 32) {
@@ -827,6 +829,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, DP, Work::kRows>::CTAS)
     float* qs = reinterpret_cast<float*>(sm + S::kQ);
     const float sc = p.scale * kLog2e;
     uint32_t joins = 0;
+    int block = 0;  // of the blocks of the stretch, modulo 3
     uint32_t k = 0;
     for (int64_t u = u0; u < u1; ++u, ++k) {
       const uint32_t st = k % S::kStages;
@@ -846,7 +849,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, DP, Work::kRows>::CTAS)
         }
         w.start(stage, qs, lane);
       }
-      w.step(stage, qs, t, sc, b->poison, warp, lane);
+      w.step(stage, qs, t, sc, b->poison[block], warp, lane);
       if (t.last) {
         const int rows = t.rows;
         w.stats(b->ml[warp], lane);
@@ -877,7 +880,8 @@ __global__ void __launch_bounds__(kThreads, Shape<T, DP, Work::kRows>::CTAS)
         if (!__all_sync(0xffffffffu, wait_or_dead(&b->join[1], joins & 1, &b->dead))) break;
         ++joins;
         T* out = static_cast<T*>(p.o);
-        const bool poisoned = *reinterpret_cast<volatile int32_t*>(&b->poison[1]) >= 0;
+        const int32_t* range = b->poison[block];
+        const bool poisoned = *reinterpret_cast<const volatile int32_t*>(&range[1]) >= 0;
 #pragma unroll
         for (int i = 0; i < STEPS; ++i) {
           const int e = i * 32 * kWarps + tid, r = e / VEC, c = (e % VEC) * 4;
@@ -895,10 +899,10 @@ __global__ void __launch_bounds__(kThreads, Shape<T, DP, Work::kRows>::CTAS)
             const int64_t stride = (int64_t)p.Hkv * p.D;
             const T* v = static_cast<const T*>(p.v) + (int64_t)t.kvh * p.D + c + (p.block_table ? 0 : t.base * stride);
             const int32_t* pages = p.block_table ? p.block_table + (int64_t)t.base * p.max_pages : nullptr;
-            const int to = min(b->poison[1], min(t.end - 1, t.pos0 + r / t.gb));
+            const int to = min(range[1], min(t.end - 1, t.pos0 + r / t.gb));
 #pragma unroll 1
             for (int u = 0; u < 4 && c + u < p.D; ++u) {
-              const float z = poison_of(v + u, stride, pages, p.num_pages, p.page_shift, b->poison[0], to);
+              const float z = poison_of(v + u, stride, pages, p.num_pages, p.page_shift, range[0], to);
               const float y = u == 0 ? x.x : u == 1 ? x.y : u == 2 ? x.z : x.w;
               const float s = z != 0.f ? y + z : y;  // a NaN already there stays
               if (u == 0) x.x = s;
@@ -920,6 +924,14 @@ __global__ void __launch_bounds__(kThreads, Shape<T, DP, Work::kRows>::CTAS)
               *reinterpret_cast<float4*>(out + at) = make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
           }
         }
+        // the word of the block after next is free: all warps are past the block
+        // before this one, and none starts that one before this thread's next join
+        const int next = block == 0 ? 2 : block - 1;
+        if (tid == 0) {
+          b->poison[next][0] = INT32_MAX;
+          b->poison[next][1] = -1;
+        }
+        block = block == 2 ? 0 : block + 1;
       }
       // generic accesses of the stage before the copies that refill it
       fence_async_smem();

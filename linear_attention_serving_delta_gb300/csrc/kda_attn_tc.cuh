@@ -146,6 +146,7 @@ static __device__ __noinline__ float poison_of(const T* v, int64_t stride, const
     pos |= y == INFINITY;
     neg |= y == -INFINITY;
     nan |= y != y;
+    if (nan || (pos && neg)) break;
   }
   return nan || (pos && neg) ? NAN : pos ? INFINITY : neg ? -INFINITY : 0.f;
 }
