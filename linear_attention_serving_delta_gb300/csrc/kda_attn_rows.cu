@@ -22,6 +22,10 @@
 // single tokens, and the tensor cores wait for memory either way); the
 // weights are rounded to bf16, as P V's operand.  fp32: the same with every
 // operand in three bf16 parts.
+//
+// Measured on GB300, 32 query heads over 8 of 128 channels, bf16: one token each
+// of 256 requests over 64..8191 keys 634 us (6.7 TB/s, the measured copy
+// rate), one token over 131,072 keys 90 us (5.9 TB/s).
 #include <algorithm>
 
 #include "kda_attn_tc.cuh"

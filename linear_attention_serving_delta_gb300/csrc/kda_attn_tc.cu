@@ -34,6 +34,11 @@
 // in a tile with positions that some row of the item may not attend,
 // non-finite values of V are zeroed too; the epilogue then puts them back
 // into the rows that do attend them (a slow path no finite input takes).
+//
+// Bound by the tensor core and by the softmax between S and P V.  Measured on
+// GB300: one prompt of 8192 tokens, 32 query heads over 8 of 128 channels, 339 us
+// (1.62 PFLOP/s, the tensor pipe 71% busy); 182k tokens of 8 prompts 24.9 ms
+// (1.42 PFLOP/s under the power cap).
 #include "kda_attn_tc.cuh"
 
 namespace kda {

@@ -17,10 +17,12 @@
 
 namespace kda {
 
-// The SMs the cut into pieces is sized for, the pieces an SM gets (their costs
-// even out over several), and the fewest key tiles a piece has
+// The SMs the cut into pieces is sized for, the pieces an SM gets (a chunk of 512
+// tokens over 32k keys beside eight requests: one 328 us, two 277, three 297,
+// four 300), and the fewest key tiles a piece has
 // Requests of up to this many rows a key head take blocks of 16 or 32 rows where
-// a 128-row tile has one row tile per CTA only
+// a CTA would have one row tile only (fp32, 20 rows of 7 requests: 23 us, 34 on
+// the row tiles)
 constexpr int kFewRows = 32;
 constexpr int kRowTile = 128;  // rows of a row tile
 constexpr int kSplitSms = 152;

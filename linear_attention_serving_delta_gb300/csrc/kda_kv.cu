@@ -94,7 +94,9 @@ __device__ int64_t plan_slot(const kda_kv_plan_args& a, int shift, int64_t count
 
 // One CTA: the pages each request needs, their prefix sum over the batch, and
 // which requests the free list can serve.  Bound by its chain of dependent
-// global loads (row, length, page), a few microseconds whatever the batch.
+// global loads (row, length, page), a few microseconds whatever the batch (256
+// requests with their slots: 6.1 us; 7.7 with the owners and the slots' inputs
+// in global memory).
 // kSlots: it goes on to the slots (one request a thread at most).
 template <bool kSlots>
 __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(kda_kv_plan_args a, KvWs w, int shift) {
@@ -239,7 +241,9 @@ __global__ void __launch_bounds__(kPlanThreads) kv_release_kernel(kda_kv_release
 }
 
 // One warp per token: the row of k, then that of v, in units of V.  Moves
-// every byte once; bound by HBM on large batches, by latency on a decode's.
+// every byte once; bound by HBM on large batches (110,353 tokens of 8 x 128
+// bf16: 141 us, 6.4 TB/s, 96% of the measured copy rate), by latency on a
+// decode's (256 tokens: 4.1 us).
 template <typename V>
 __global__ void __launch_bounds__(256) kv_write_kernel(kda_kv_write_args a, int64_t row_units) {
   const int64_t warps = (int64_t)gridDim.x * 8;

@@ -104,7 +104,8 @@ HEADS = [(dict(num_heads=0), INVALID), (dict(num_kv_heads=0), INVALID), (dict(nu
          (dict(total_tokens=-1), INVALID), (dict(total_tokens=1 << 30), UNSUPPORTED),
          (dict(cu_seqlens=None), INVALID), (dict(q=None), INVALID), (dict(o=None), INVALID)]
 PAGES = [(dict(page_size=8), UNSUPPORTED), (dict(page_size=48), UNSUPPORTED), (dict(page_size=2048), UNSUPPORTED),
-         (dict(num_pages=-1), INVALID), (dict(num_rows=-1), INVALID), (dict(max_pages=-1), INVALID)]
+         (dict(num_pages=-1), INVALID), (dict(num_rows=-1), INVALID), (dict(max_pages=-1), INVALID),
+         (dict(max_pages=1 << 27), UNSUPPORTED)]  # positions past int32
 
 
 @pytest.mark.parametrize("over,status", HEADS + [(dict(k=None), INVALID), (dict(v=None), INVALID)])

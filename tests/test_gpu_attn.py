@@ -390,6 +390,58 @@ def test_infinite_values_reach_the_rows_that_attend_them(dtype, D, new):
     check(o, ref, tol)
 
 
+@pytest.mark.parametrize("G", [16, 17, 20, 33, 40, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_group_sizes_of_wide_heads(G, dtype):
+    """A token's group of heads cut into blocks of 16 or 32 rows."""
+    run_prompt([40, 3], G, 1, 256, dtype, seed=G)
+    run_paged([100, 7, 900], [1, 1, 1], 2 * G, 2, 256, 16, dtype, seed=G)
+    run_paged([100, 7, 900], [1, 2, 1], G, 1, 64, 16, dtype, seed=G)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [0.0, -0.2, 1e-6])
+@pytest.mark.parametrize("new", [1, 30])
+def test_scales_over_the_cache(dtype, scale, new):
+    run_paged([300, 20], [new, 1], 8, 2, 64, 16, dtype, seed=new, scale=scale)
+
+
+def test_unaligned_cache():
+    g = gen(13)
+    p = Pool([200, 31], [3, 20], 2, 64, 16, "bf16", 14)
+    k = torch.empty(p.k.numel() + 1, device="cuda", dtype=torch.bfloat16)[1:].view(p.k.shape).copy_(p.k)
+    v = torch.empty(p.v.numel() + 1, device="cuda", dtype=torch.bfloat16)[1:].view(p.v.shape).copy_(p.v)
+    q = rand(g, 23, 8, 64)
+    o = kda.attn_paged(q, k, v, p.table, p.lens, cu_of([3, 20]).cuda())
+    check(o[:3], *reference(q[:3], p.K[0], p.V[0], 200, 0.125, "bf16"))
+    check(o[3:], *reference(q[3:], p.K[1], p.V[1], 31, 0.125, "bf16"))
+
+
+def test_prompts_in_a_graph():
+    """A captured call follows its inputs, lengths among them."""
+    for D, dtype in ((64, "bf16"), (128, "bf16"), (256, "bf16"), (64, "f32")):
+        g = gen(15)
+        T = 900
+        q, k, v = rand(g, T, 8, D, dtype=dtype), rand(g, T, 2, D, dtype=dtype), rand(g, T, 2, D, dtype=dtype)
+        cu = cu_of([300, 500]).cuda()
+        a = kda.AttnPrefill(q, k, v, cu)
+        a.run()
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            a.run()
+        for lens in ([300, 500], [1, 899], [450, 450], [0, 10]):
+            cu.copy_(cu_of(lens))
+            v.copy_(rand(g, T, 2, D, dtype=dtype))
+            a.o.fill_(9)
+            graph.replay()
+            b = lens[0]
+            for x, y in ((0, b), (b, b + lens[1])):
+                if x < y:
+                    check(a.o[x:y], *reference(q[x:y], k[x:y], v[x:y], 0, D ** -0.5, dtype))
+            assert (a.o[sum(lens):] == 9).all()
+
+
 def test_slots_past_32_bit_offsets():
     """A cache of more than 2^32 elements, pages at its far end."""
     Hkv, D, page = 8, 128, 64

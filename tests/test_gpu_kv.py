@@ -97,6 +97,22 @@ def test_plan(n, new, ctx, page, in_place):
     run_plan(cu_of(lens), sum(lens), table, kv, free, count, page, rows, in_place)
 
 
+def test_plan_and_release_in_a_large_pool():
+    """More rows than the owners found in shared memory; a row named twice."""
+    R, page = 9000, 16
+    cached = [i % 40 for i in range(R)]
+    table, kv, free, count = pool(R, 5, page, cached, sum(-(-c // page) for c in cached) + 60, 8)
+    rows = torch.tensor([8999, 5, 4096, 4095, 5, 8191, 7000], dtype=torch.int32)
+    run_plan(cu_of([3, 20, 1, 17, 4, 0, 30]), 75, table, kv, free, count, page, rows, in_place=True)
+    d = [x.cuda() for x in (rows, table, kv, free)]
+    cnt = torch.tensor([count], dtype=torch.int32, device="cuda")
+    assert kda.KvRelease(*d, cnt, page_size=page).run().device_status() == 0
+    want = free[:count].tolist()
+    for r in (8999, 5, 4096, 4095, 8191, 7000):
+        want += table[r, :-(-cached[r] // page)].tolist()
+    assert int(cnt) == len(want) and d[3][:len(want)].tolist() == want
+
+
 def test_plan_without_rows_and_with_padding():
     """Request s is row s; the slot map is longer than the batch's tokens."""
     table, kv, free, count = pool(4, 8, 16, [0, 16, 15, 33], 40, 1)
