@@ -101,15 +101,14 @@ AttnParams params(const kda_attn_paged_args* a) {
   return p;
 }
 
-// The path of a call: single tokens and a few rows on the streaming kernel,
+// The path of a call: few rows a request (few_rows) on the streaming kernel,
 // more on the tensor cores' row tiles (two a CTA; one for heads of 256 channels
 // and fp32), fp32 heads of 256 channels on the streaming kernel again, and what
 // none of them takes (odd alignment, a scale that is not positive) on the CUDA
 // cores.
 enum class AttnPath { kRows, kTc, kTc1, kSimt };
 AttnPath attn_path(const AttnParams& p) {
-  const bool few = p.block_table && p.max_seqlen * p.G <= 16;
-  if (few && attn_rows_fits(p)) return AttnPath::kRows;
+  if (few_rows(p) && attn_rows_fits(p)) return AttnPath::kRows;
   if (attn_tc_fits(p)) return AttnPath::kTc;
   if (attn_tc1_fits(p)) return AttnPath::kTc1;
   return attn_rows_fits(p) ? AttnPath::kRows : AttnPath::kSimt;

@@ -1064,8 +1064,7 @@ cudaError_t launch_f32(const AttnParams& p, char* w, cudaStream_t stream) {
 // 16-byte aligned bases for the tensor maps.
 bool attn_rows_fits(const AttnParams& p) {
   auto al16 = [](const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15) == 0; };
-  const bool few = p.block_table && p.max_seqlen * p.G <= 16;
-  return (few || p.dt == KDA_F32 || p.D == 256) && p.scale > 0.f && p.scale <= 3.4e38f && al16(p.q) && al16(p.k) &&
+  return (few_rows(p) || p.dt == KDA_F32 || p.D == 256) && p.scale > 0.f && p.scale <= 3.4e38f && al16(p.q) && al16(p.k) &&
          al16(p.v) && al16(p.o) && (!p.block_table || p.num_pages > 0);
 }
 size_t attn_rows_workspace(const AttnParams& p) {

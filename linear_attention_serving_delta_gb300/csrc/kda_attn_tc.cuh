@@ -20,6 +20,12 @@ namespace kda {
 // The SMs the cut into pieces is sized for, the pieces an SM gets (a chunk of 512
 // tokens over 32k keys beside eight requests: one 328 us, two 277, three 297,
 // four 300), and the fewest key tiles a piece has
+// Over the cache, requests of up to kTinyRows rows a key head take the streaming
+// kernel's blocks, and so do a few blocks of rows over short tables: a 128-row
+// tile's chain of steps would take longer (163 requests of 1..40 tokens over
+// tables of 320 positions 38 us, 48 on the row tiles; 100 requests of 32 rows over
+// 960 positions 73 and 58).
+constexpr int kTinyRows = 16, kShortRows = 64, kShortKeys = 512;
 // Requests of up to this many rows a key head take blocks of 16 or 32 rows where
 // a CTA would have one row tile only (fp32, 20 rows of 7 requests: 23 us, 34 on
 // the row tiles)
@@ -338,6 +344,12 @@ __device__ __forceinline__ Split split3(float x, float y) {
 
 // Workspace, arguments and launches of the plan and of the joining of pieces.
 // row_tiles: of an item; dp: padded channels; kt_shift: log2 of a key tile.
+inline bool few_rows(const AttnParams& p) {
+  const int64_t rows = p.max_seqlen * p.G;
+  return p.block_table &&
+         (rows <= kTinyRows || (rows <= kShortRows && ((int64_t)p.max_pages << p.page_shift) <= kShortKeys));
+}
+
 TcLayout tc_layout(const AttnParams& p, int row_tiles, int dp, bool may_self_plan);
 TcArgs tc_args(const AttnParams& p, const TcLayout& L, int row_tiles, int kt_shift, void* ws);
 cudaError_t launch_attn_plan(const AttnParams& p, const TcArgs& a, cudaStream_t stream);
