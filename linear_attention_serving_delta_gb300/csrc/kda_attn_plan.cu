@@ -214,7 +214,7 @@ cudaError_t join_t(const AttnParams& p, const TcArgs& a, int dp, dim3 grid, cuda
 
 }  // namespace
 
-TcLayout tc_layout(const AttnParams& p, int row_tiles, int dp, bool may_self_plan) {
+TcLayout tc_layout(const AttnParams& p, int row_tiles, int dp) {
   TcLayout L{};
   const int tpi = row_tiles * (kRowTile / p.G);
   L.max_items = (p.total_tokens + tpi - 1) / tpi + p.num_seqs;
@@ -224,7 +224,7 @@ TcLayout tc_layout(const AttnParams& p, int row_tiles, int dp, bool may_self_pla
   // a call whose items cannot outnumber the SMs plans for itself, unless long
   // key ranges are better cut
   const int64_t keys = p.block_table ? (int64_t)p.max_pages << p.page_shift : p.total_tokens;
-  L.self_plan = may_self_plan && L.max_items * p.Hkv <= kSplitSms && (!L.split || keys <= kSelfPlanKeys);
+  L.self_plan = L.max_items * p.Hkv <= kSplitSms && (!L.split || keys <= kSelfPlanKeys);
   if (L.self_plan) L.split = false;
   L.max_pieces = L.split ? (2 + kPiecesPerSm) * (int64_t)kSplitSms / p.Hkv + 1 : 0;
   size_t off = 0;

@@ -73,8 +73,7 @@ struct Bars {
   uint64_t q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], o_full[2];
   uint64_t fix, drain[2];
   uint32_t dead;      // a wait expired: every role winds down
-  uint32_t own;       // a call that plans for itself: this CTA has an item
-  int32_t plan[kThreads / 32];
+  OwnPlan plan;
   uint32_t turn;      // held by the MMA warp whose burst is being issued
   uint32_t tmem;
   // the CTA's k-th item with key tiles: non-finite values were taken out of its
@@ -553,47 +552,6 @@ __device__ void softmax_role(const AttnParams& p, const TcArgs& a, Bars* b, int6
   }
 }
 
-// Small calls plan for themselves: no more items than CTAs, so the order does
-// not matter and CTA w needs item w alone, which the thread of its sequence
-// leaves in the workspace.  Returns whether there is one (for every thread).
-__device__ bool plan_own_item(const AttnParams& p, const TcArgs& a, Bars* b) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, tpi = a.row_tiles * a.tpt;
-  const int64_t want = blockIdx.x / p.Hkv;
-  int64_t before = 0;
-  for (int base = 0; base < p.num_seqs; base += kThreads) {
-    const int s = base + tid;
-    AttnSeq q{};
-    int n = 0;
-    if (s < p.num_seqs) {
-      q = attn_seq(p, s);
-      if (q.flag && blockIdx.x == 0) attn_flag(p.status, q.flag);
-      n = (q.len + tpi - 1) / tpi;
-    }
-    int x = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (lane == 31) b->plan[warp] = x;
-    __syncthreads();
-    int total = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) x += b->plan[w];
-      total += b->plan[w];
-    }
-    const int64_t first = before + x - n;
-    if (n > 0 && want >= first && want < first + n) {
-      a.items[blockIdx.x] = make_item(p, a, q, want - first);
-      b->own = 1;
-    }
-    before += total;
-    __syncthreads();
-  }
-  return *reinterpret_cast<volatile uint32_t*>(&b->own) != 0;
-}
-
 template <int DP>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tc(const AttnParams p, const TcArgs a, const __grid_constant__ CUtensorMap mq,
@@ -620,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&b->fix, 1);
     b->dead = 0;
-    b->own = 0;
+    b->plan.own = 0;
     b->turn = 0;
     mbar_init_fence();
   }
@@ -636,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();  // the plan, or what came before
   const int tpt = kTile / p.G;
   const int64_t total =
-      a.self_plan ? (plan_own_item(p, a, b) ? blockIdx.x + 1 : 0) : (int64_t)a.head->items * p.Hkv;
+      a.self_plan ? (plan_own_item<kThreads>(p, a, &b->plan) ? blockIdx.x + 1 : 0) : (int64_t)a.head->items * p.Hkv;
   // registers: 168 a thread at launch (384 x 168 = 64,512); a softmax thread
   // holds a row of 128 logits: 2 x 128 x 208 + 128 x 80 = 63,488
   if (warp < 8) {
@@ -696,9 +654,9 @@ bool attn_tc_fits(const AttnParams& p) {
   return p.dt == KDA_BF16 && p.D <= 128 && p.scale > 0.f && p.scale <= 3.4e38f && al16(p.q) && al16(p.k) &&
          al16(p.v) && al16(p.o) && (!p.block_table || p.num_pages > 0);
 }
-size_t attn_tc_workspace(const AttnParams& p) { return tc_layout(p, 2, padded(p.D), true).total; }
+size_t attn_tc_workspace(const AttnParams& p) { return tc_layout(p, 2, padded(p.D)).total; }
 cudaError_t launch_attn_tc(const AttnParams& p, void* ws, cudaStream_t stream) {
-  const TcLayout L = tc_layout(p, 2, padded(p.D), true);
+  const TcLayout L = tc_layout(p, 2, padded(p.D));
   return p.D <= 64 ? launch_dp<64>(p, L, ws, stream) : launch_dp<128>(p, L, ws, stream);
 }
 

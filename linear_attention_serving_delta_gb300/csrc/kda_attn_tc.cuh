@@ -136,6 +136,52 @@ __device__ __forceinline__ Boxes boxes_of(const AttnParams& p, const AttnItem& i
   return r;
 }
 
+struct OwnPlan {
+  uint32_t own;     // this CTA has an item; 0 at the start
+  int32_t sum[12];  // of the warps
+};
+// Small calls plan for themselves: no more items than CTAs, so the order does
+// not matter and CTA w needs item w alone, which the thread of its sequence
+// leaves in the workspace.  Returns whether there is one (for every thread).
+template <int THREADS>
+__device__ bool plan_own_item(const AttnParams& p, const TcArgs& a, OwnPlan* b) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, tpi = a.row_tiles * a.tpt;
+  const int64_t want = blockIdx.x / p.Hkv;
+  int64_t before = 0;
+  for (int base = 0; base < p.num_seqs; base += THREADS) {
+    const int s = base + tid;
+    AttnSeq q{};
+    int n = 0;
+    if (s < p.num_seqs) {
+      q = attn_seq(p, s);
+      if (q.flag && blockIdx.x == 0) attn_flag(p.status, q.flag);
+      n = (q.len + tpi - 1) / tpi;
+    }
+    int x = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) b->sum[warp] = x;
+    __syncthreads();
+    int total = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+      if (w < warp) x += b->sum[w];
+      total += b->sum[w];
+    }
+    const int64_t first = before + x - n;
+    if (n > 0 && want >= first && want < first + n) {
+      a.items[blockIdx.x] = make_item(p, a, q, want - first);
+      b->own = 1;
+    }
+    before += total;
+    __syncthreads();
+  }
+  return *reinterpret_cast<volatile uint32_t*>(&b->own) != 0;
+}
+
 // The non-finite values taken out of V tiles, put back into one channel of one
 // row (slow path): what the attended positions from..limit give it, an infinity,
 // or NaN where both signs or a NaN meet; 0 for none.
@@ -350,7 +396,7 @@ inline bool few_rows(const AttnParams& p) {
          (rows <= kTinyRows || (rows <= kShortRows && ((int64_t)p.max_pages << p.page_shift) <= kShortKeys));
 }
 
-TcLayout tc_layout(const AttnParams& p, int row_tiles, int dp, bool may_self_plan);
+TcLayout tc_layout(const AttnParams& p, int row_tiles, int dp);
 TcArgs tc_args(const AttnParams& p, const TcLayout& L, int row_tiles, int kt_shift, void* ws);
 cudaError_t launch_attn_plan(const AttnParams& p, const TcArgs& a, cudaStream_t stream);
 cudaError_t launch_attn_join(const AttnParams& p, const TcArgs& a, int dp, int sms, cudaStream_t stream);

@@ -67,6 +67,7 @@ struct Bars {
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], h_full[8], h_empty[8];
   uint64_t q_full, q_empty, s_full[2], p_full[2], pv_done[2], fix, drain;
   uint32_t dead, tmem;
+  OwnPlan plan;
   // the CTA's k-th item with key tiles (index k % 8): the positions whose
   // non-finite values were taken out of V
   int32_t poison_from[8], poison_to[8];
@@ -690,6 +691,7 @@ __global__ void __launch_bounds__(Shape<NP, DP>::kThreads, 1)
       b->poison_to[s] = -1;
     }
     b->dead = 0;
+    b->plan.own = 0;
     mbar_init_fence();
   }
   if (threadIdx.x == 32) {
@@ -701,8 +703,9 @@ __global__ void __launch_bounds__(Shape<NP, DP>::kThreads, 1)
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
-  pdl_wait();  // the plan
-  const int64_t total = (int64_t)a.head->items * p.Hkv;
+  pdl_wait();  // the plan, or what came before
+  const int64_t total = a.self_plan ? (plan_own_item<S::kThreads>(p, a, &b->plan) ? blockIdx.x + 1 : 0)
+                                    : (int64_t)a.head->items * p.Hkv;
   if (warp < 4) softmax_role<NP, DP>(p, a, b, total);
   else if (warp == 5) mma_role<NP, DP>(p, a, sm, b, total);
   else if constexpr (NP == 1) {
@@ -722,7 +725,7 @@ __global__ void __launch_bounds__(Shape<NP, DP>::kThreads, 1)
 template <int NP, int DP>
 cudaError_t launch_np(const AttnParams& p, void* ws, cudaStream_t stream) {
   using S = Shape<NP, DP>;
-  const TcLayout L = tc_layout(p, 1, DP, false);
+  const TcLayout L = tc_layout(p, 1, DP);
   TcArgs a = tc_args(p, L, 1, kKeyShift, ws);
   const int box = 1 << (NP == 1 || a.box_shift < 5 ? a.box_shift : 5);
   CUtensorMap mq, mk, mv;
@@ -734,7 +737,8 @@ cudaError_t launch_np(const AttnParams& p, void* ws, cudaStream_t stream) {
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   auto kernel = attn_tc1<NP, DP>;
   if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kBytes);
-  if (e == cudaSuccess) e = launch_attn_plan(p, a, stream);
+  a.self_plan = L.self_plan && L.max_items * p.Hkv <= sms;
+  if (e == cudaSuccess && !a.self_plan) e = launch_attn_plan(p, a, stream);
   if (e != cudaSuccess) return e;
   const int64_t most = (L.max_items + L.max_pieces) * p.Hkv;
   e = launch_maybe_dependent(true, kernel, dim3((unsigned)(most < sms ? most : sms)), dim3(S::kThreads),
@@ -754,7 +758,7 @@ bool attn_tc1_fits(const AttnParams& p) {
          al16(p.v) && al16(p.o) && (!p.block_table || p.num_pages > 0);
 }
 size_t attn_tc1_workspace(const AttnParams& p) {
-  return tc_layout(p, 1, p.dt == KDA_BF16 ? 256 : p.D <= 64 ? 64 : 128, false).total;
+  return tc_layout(p, 1, p.dt == KDA_BF16 ? 256 : p.D <= 64 ? 64 : 128).total;
 }
 cudaError_t launch_attn_tc1(const AttnParams& p, void* ws, cudaStream_t stream) {
   if (p.dt == KDA_BF16) return launch_np<1, 256>(p, ws, stream);

@@ -95,8 +95,8 @@ __device__ int64_t plan_slot(const kda_kv_plan_args& a, int shift, int64_t count
 // One CTA: the pages each request needs, their prefix sum over the batch, and
 // which requests the free list can serve.  Bound by its chain of dependent
 // global loads (row, length, page), a few microseconds whatever the batch (256
-// requests with their slots: 6.1 us; 7.7 with the owners and the slots' inputs
-// in global memory).
+// requests with their slots: 3.5 us; 6.1 as a plain launch, 7.7 with the owners
+// and the slots' inputs in global memory).
 // kSlots: it goes on to the slots (one request a thread at most).
 template <bool kSlots>
 __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(kda_kv_plan_args a, KvWs w, int shift) {
@@ -105,6 +105,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(kda_kv_plan_args 
       sm_ctx[kSlots ? kPlanThreads : 1];
   extern __shared__ int32_t sm_owner[];
   const int tid = threadIdx.x, threads = blockDim.x;
+  pdl_wait();
   int32_t count = *a.free_count_in;
   int32_t* owner = a.num_rows <= kSharedRows ? sm_owner : w.owner;
   if (a.rows) find_owners(a.rows, a.num_seqs, a.num_rows, owner);
@@ -181,10 +182,10 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(kda_kv_plan_args 
 
 __global__ void __launch_bounds__(256) kv_slots_kernel(kda_kv_plan_args a, KvWs w, int shift) {
   const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  pdl_wait();
   if (t >= a.total_tokens) return;
   const int32_t s = seq_of_token(a.cu_seqlens, a.num_seqs, t);
   const int64_t b = a.cu_seqlens[s], e = a.cu_seqlens[s + 1];
-  pdl_wait();
   const int64_t first = w.first[s];
   a.slot_map[t] = t >= b && t < e && first != kNoPlan ? plan_slot(a, shift, *w.count, t, s, b, w.ctx[s], first) : -1;
 }
@@ -193,6 +194,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_release_kernel(kda_kv_release
   __shared__ int64_t part[2][32];
   extern __shared__ int32_t sm_owner[];
   const int tid = threadIdx.x;
+  pdl_wait();
   int64_t count = *a.free_count;
   int32_t* owner = a.num_rows <= kSharedRows ? sm_owner : w.owner;
   __syncthreads();
@@ -242,12 +244,13 @@ __global__ void __launch_bounds__(kPlanThreads) kv_release_kernel(kda_kv_release
 
 // One warp per token: the row of k, then that of v, in units of V.  Moves
 // every byte once; bound by HBM on large batches (110,353 tokens of 8 x 128
-// bf16: 141 us, 6.4 TB/s, 96% of the measured copy rate), by latency on a
-// decode's (256 tokens: 4.1 us).
+// bf16: 138 us, 6.6 TB/s, 98% of the measured copy rate), by latency on a
+// decode's (256 tokens: 2.9 us, 4.1 as a plain launch).
 template <typename V>
 __global__ void __launch_bounds__(256) kv_write_kernel(kda_kv_write_args a, int64_t row_units) {
   const int64_t warps = (int64_t)gridDim.x * 8;
   const int lane = threadIdx.x & 31;
+  pdl_wait();
   for (int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); t < a.total_tokens; t += warps) {
     const int64_t slot = a.slot_map[t];
     if (slot < 0) continue;
@@ -288,8 +291,9 @@ cudaError_t launch_kv_plan(const kda_kv_plan_args& a, void* ws, cudaStream_t str
   const bool one = a.total_tokens <= kOneLaunchTokens && a.num_seqs <= kPlanThreads;
   const int64_t most = one && a.total_tokens > a.num_seqs ? a.total_tokens : a.num_seqs;
   const int threads = most >= kPlanThreads ? kPlanThreads : (int)(most + 31) / 32 * 32;
-  (one ? kv_plan_kernel<true> : kv_plan_kernel<false>)<<<1, threads, owner_bytes(a.num_rows), stream>>>(a, w, shift);
-  const cudaError_t e = cudaGetLastError();
+  // (each of these as the programmatic dependent of what precedes it: its launch overlaps that one's end)
+  const cudaError_t e = launch_maybe_dependent(true, one ? kv_plan_kernel<true> : kv_plan_kernel<false>, dim3(1),
+                                               dim3(threads), owner_bytes(a.num_rows), stream, a, w, shift);
   if (e != cudaSuccess || one || a.total_tokens == 0) return e;
   return launch_maybe_dependent(true, kv_slots_kernel, dim3((unsigned)((a.total_tokens + 255) / 256)), dim3(256), 0,
                                 stream, a, w, shift);
@@ -297,8 +301,8 @@ cudaError_t launch_kv_plan(const kda_kv_plan_args& a, void* ws, cudaStream_t str
 
 cudaError_t launch_kv_release(const kda_kv_release_args& a, void* ws, cudaStream_t stream) {
   if (a.num_release == 0) return cudaSuccess;
-  kv_release_kernel<<<1, kPlanThreads, owner_bytes(a.num_rows), stream>>>(a, kv_ws(ws, 0), shift_of(a.page_size));
-  return cudaGetLastError();
+  return launch_maybe_dependent(true, kv_release_kernel, dim3(1), dim3(kPlanThreads), owner_bytes(a.num_rows), stream, a,
+                                kv_ws(ws, 0), shift_of(a.page_size));
 }
 
 cudaError_t launch_kv_write(const kda_kv_write_args& a, cudaStream_t stream) {
@@ -309,11 +313,9 @@ cudaError_t launch_kv_write(const kda_kv_write_args& a, cudaStream_t stream) {
   int64_t ctas = (a.total_tokens + 7) / 8;
   if (ctas > 152 * 8) ctas = 152 * 8;
   // rows are multiples of 32 bytes (16 channels of 2 bytes); an unaligned base takes 2-byte units
-  if ((all & 15) == 0)
-    kv_write_kernel<uint4><<<(unsigned)ctas, 256, 0, stream>>>(a, bytes / 16);
-  else
-    kv_write_kernel<uint16_t><<<(unsigned)ctas, 256, 0, stream>>>(a, bytes / 2);
-  return cudaGetLastError();
+  const bool wide = (all & 15) == 0;
+  return launch_maybe_dependent(true, wide ? kv_write_kernel<uint4> : kv_write_kernel<uint16_t>, dim3((unsigned)ctas),
+                                dim3(256), 0, stream, a, bytes / (wide ? 16 : 2));
 }
 
 }  // namespace kda
