@@ -49,7 +49,7 @@ using namespace tc;
 constexpr int kTile = 128;       // rows of a row tile, positions of a key tile
 constexpr int kThreads = 384;    // two softmax warpgroups; copies and MMAs
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kFirst = 64;       // positions of P handed over first
+constexpr int kFirst = kTile / 2;  // positions of P handed over first
 constexpr float kLazyLog2 = 8.f;
 constexpr float kLazySum = 256.f;  // 2^kLazyLog2
 constexpr uint32_t kTmemCols = 512;
@@ -438,7 +438,7 @@ __device__ void softmax_role(const AttnParams& p, const TcArgs& a, Bars* b, int6
 #pragma unroll
         for (int u = 0; u < kFirst / 2; ++u) {
           weight(s, u, sc2, ref2);
-          if (kFirst + 2 * u < kTile) mx[u & 3] = fmaxf(mx[u & 3], fmaxf(s[kFirst + 2 * u], s[kFirst + 2 * u + 1]));
+          mx[u & 3] = fmaxf(mx[u & 3], fmaxf(s[kFirst + 2 * u], s[kFirst + 2 * u + 1]));
         }
         const float x2 = sc * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         const float s1 = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
@@ -472,15 +472,13 @@ __device__ void softmax_role(const AttnParams& p, const TcArgs& a, Bars* b, int6
           for (int u = 0; u < kFirst / 2; ++u) weight(s, u, sc2, ref2);
         }
         tmem_st32(s_col, pk);
-        if constexpr (kFirst == 96) tmem_st16(s_col + 32, reinterpret_cast<const float*>(pk + 32));
         tmem_st_wait();
         fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&b->p_half[t]);
 #pragma unroll
         for (int u = 0; u < (kTile - kFirst) / 2; ++u) weight(s + kFirst, u, sc2, ref2);
-        if constexpr (kFirst == 96) tmem_st16(s_col + 48, reinterpret_cast<const float*>(pk));
-        else tmem_st32(s_col + 32, pk);
+        tmem_st32(s_col + 32, pk);
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         tmem_st_wait();
       } else {
