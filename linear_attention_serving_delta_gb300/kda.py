@@ -857,7 +857,9 @@ def _shape(name, t, want):
 
 class _CacheCall:
     """What the planned calls share: the argument block, the workspace and the
-    status word are made once; ``run()`` only launches kernels."""
+    status word are made once, on the current stream; ``run()`` only launches
+    kernels.  Another stream waits for that one before its first run, and two
+    runs of one planned call do not overlap (they share its workspace)."""
     _name = ""
 
     def _plan(self, device, args, keep, status):
