@@ -178,6 +178,22 @@ def test_release(M):
     assert d[3][:len(want)].tolist() == want and torch.equal(d[2].cpu(), lens)
 
 
+def test_release_of_long_rows():
+    # more pages than one pass of the threads takes, next to rows of none and of one
+    page, R = 16, 5
+    cached = [100_000, 0, 1, 70_000, 16 * 1024]
+    table, kv, free, count = pool(R, 6250, page, cached, sum(-(-c // page) for c in cached) + 7, 9)
+    rows = torch.tensor([3, 1, 4, 0, 2], dtype=torch.int32)
+    d = [x.cuda() for x in (rows, table, kv, free)]
+    cnt = torch.tensor([count], dtype=torch.int32, device="cuda")
+    a = kda.KvRelease(*d, cnt, page_size=page).run()
+    want = free[:count].tolist()
+    for r in rows.tolist():
+        want += table[r, :-(-cached[r] // page)].tolist()
+    assert a.device_status() == 0 and int(cnt) == len(want) and d[2].tolist() == [0] * R
+    assert d[3][:len(want)].tolist() == want
+
+
 def test_release_of_malformed_rows():
     table, kv, free, count = pool(5, 8, 16, [20, 40, 1 << 40, 0, 100], 30, 7)
     rows = torch.tensor([1, -1, 1, 9, 2, 3, 0, 1], dtype=torch.int32)
