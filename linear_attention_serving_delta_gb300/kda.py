@@ -975,7 +975,7 @@ class AttnPaged(_CacheCall):
         a, dt = AttnPagedArgs(), q.dtype
         a.num_seqs, a.num_heads, a.num_kv_heads, a.head_dim, a.total_tokens = N, H, Hkv, D, T
         a.cu_seqlens = _ptr(cu_seqlens, torch.int64, "cu_seqlens")
-        a.max_seqlen, a.in_dtype = int(max_seqlen), _dtype_code(dt)
+        a.max_seqlen, a.in_dtype = min(int(max_seqlen), T), _dtype_code(dt)
         a.q, a.o = _ptr(q, dt, "q"), _ptr(self.o, dt, "o")
         a.k_cache, a.v_cache = _ptr(k_cache, dt, "k_cache"), _ptr(v_cache, dt, "v_cache")
         a.num_pages, a.page_size = P, page

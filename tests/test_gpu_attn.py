@@ -406,6 +406,11 @@ def test_scales_over_the_cache(dtype, scale, new):
     run_paged([300, 20], [new, 1], 8, 2, 64, 16, dtype, seed=new, scale=scale)
 
 
+@pytest.mark.parametrize("bound", [40, 1 << 31, (1 << 32) + 1])
+def test_a_loose_bound_on_the_new_tokens(bound):
+    run_paged([30, 500], [3, 40], 8, 2, 64, 16, "bf16", seed=5, max_seqlen=bound)
+
+
 def test_unaligned_cache():
     g = gen(13)
     p = Pool([200, 31], [3, 20], 2, 64, 16, "bf16", 14)
