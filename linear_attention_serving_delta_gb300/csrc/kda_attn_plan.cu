@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnParam
     if (s < p.num_seqs) {
       if (near) {
         sm_seq[s] = q;
-        sm_begin[s] = (int32_t)(n_tiles + end - n);
+        sm_begin[s] = (int32_t)min(n_tiles + end - n, (int64_t)INT32_MAX);  // (past max_items: not looked up)
       } else {
         a.seq_begin[s] = n_tiles + end - n;
       }
