@@ -124,11 +124,12 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(kda_kv_plan_args 
       b = a.cu_seqlens[s];
       const int64_t e = a.cu_seqlens[s + 1];
       len = e - b;
+      if (r >= a.num_rows || (r >= 0 && a.rows && owner[r] != s)) {
+        attn_flag(a.status, kFlagBadCache);
+        r = -1;  // no row of the pool; the owner's length stays as the owner leaves it
+      }
       if (b < 0 || e < b || e > a.total_tokens || (s == 0 && b != 0)) {
         attn_flag(a.status, kFlagBadSeqlens);
-      } else if (r >= a.num_rows || (r >= 0 && a.rows && owner[r] != s)) {
-        attn_flag(a.status, kFlagBadCache);
-        r = -1;  // the owner's length stays as the owner leaves it
       } else if (r >= 0) {
         c = a.kv_lens_in[r];
         ok = c >= 0 && c + len <= ((int64_t)a.max_pages << shift) && c + len >= c;

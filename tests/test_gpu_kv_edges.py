@@ -1,0 +1,33 @@
+"""The paged cache's bookkeeping on malformed batches and full lists: what is
+refused leaves every pool entry as it was, what is served is whole.
+"""
+import pytest
+import torch
+
+from linear_attention_serving_delta_gb300 import kda
+from test_gpu_kv import pool
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("R", [3, 4500])
+def test_malformed_seqlens_beside_malformed_rows(R):
+    """A request with malformed cu_seqlens whose row lies behind the pool, or is another request's: lengths
+    that are written apart from those read get nothing from it, nor does what stands around them."""
+    cached = [5 + i % 30 for i in range(R)]
+    table, kv, free, count = pool(R, 8, 16, cached, sum(-(-c // 16) for c in cached) + 9, 11)
+    # what stands behind (and before) the pool's rows, in the lengths read and in those written
+    around = torch.arange(40_000, 40_000 + R + 64)
+    lens_in, lens_out = around.clone().cuda(), (around + 100_000).cuda()
+    lens_in[32:32 + R] = kv.cuda()
+    for row in (R, R + 20, 1):  # (the first request's row is 1)
+        before_in, before_out = lens_in.clone(), lens_out.clone()
+        cu = torch.tensor([0, 20, 15]).cuda()
+        cnt = torch.tensor([count], dtype=torch.int32, device="cuda")
+        p = kda.KvPlan(cu, 40, table.cuda(), lens_in[32:32 + R], free.cuda(), cnt, page_size=16,
+                       rows=torch.tensor([1, row], dtype=torch.int32, device="cuda"),
+                       kv_lens_out=lens_out[32:32 + R], free_count_out=torch.full_like(cnt, -1)).run()
+        assert p.device_status() == 1 | 32
+        before_out[32 + 1] = cached[1] + 20
+        assert torch.equal(lens_in, before_in) and torch.equal(lens_out, before_out)
+        assert (p.slot_map[:20] >= 0).all() and (p.slot_map[20:] == -1).all()
