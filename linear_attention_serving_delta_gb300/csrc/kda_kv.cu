@@ -132,7 +132,8 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(kda_kv_plan_args 
         attn_flag(a.status, kFlagBadSeqlens);
       } else if (r >= 0) {
         c = a.kv_lens_in[r];
-        ok = c >= 0 && c + len <= ((int64_t)a.max_pages << shift) && c + len >= c;
+        const int64_t most = (int64_t)a.max_pages << shift;
+        ok = c >= 0 && c <= most && len <= most - c;  // (c + len may pass 64 bits)
         if (!ok) attn_flag(a.status, kFlagBadCache);
       }
       if (ok) need = ceil_shift(c + len, shift) - ceil_shift(c, shift);

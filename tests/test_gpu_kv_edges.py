@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from linear_attention_serving_delta_gb300 import kda
+from test_gpu_attn import cu_of
 from test_gpu_kv import pool
 
 pytestmark = pytest.mark.gpu
@@ -31,3 +32,21 @@ def test_malformed_seqlens_beside_malformed_rows(R):
         before_out[32 + 1] = cached[1] + 20
         assert torch.equal(lens_in, before_in) and torch.equal(lens_out, before_out)
         assert (p.slot_map[:20] >= 0).all() and (p.slot_map[20:] == -1).all()
+
+
+@pytest.mark.parametrize("n", [1, 1500])
+def test_plan_of_lengths_next_to_64_bits(n):
+    """Cached lengths to which no new token can be added within 64 bits: refused as any that the table cannot hold."""
+    top = 2 ** 63 - 1
+    table, kv, free, count = pool(n + 3, 5, 16, [7] * (n + 3), 2 * n + 20, 12)
+    bad = torch.tensor([top, top - 1, 5 * 16 + 1])
+    kv[n:] = bad
+    cu = cu_of([1] * n + [2, 2, 0])
+    T = int(cu[-1])
+    d = [x.cuda() for x in (cu, table, kv, free)]
+    out = torch.full_like(d[2], -3)
+    p = kda.KvPlan(d[0], T, d[1], d[2], d[3], torch.tensor([count], dtype=torch.int32, device="cuda"), page_size=16,
+                   kv_lens_out=out).run()
+    assert p.device_status() == 32 and int(p.free_count_out) == count
+    assert torch.equal(d[1].cpu(), table) and torch.equal(out.cpu(), torch.cat([torch.full((n,), 8), bad]))
+    assert (p.slot_map[n:] == -1).all() and (p.slot_map[:n] >= 0).all()
