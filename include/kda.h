@@ -648,8 +648,8 @@ kda_status_t kda_attn_paged(const kda_attn_paged_args* args, void* ws, size_t ws
  *     page are still served.
  *   - So is a request (flag 32) with a row outside the pool, c outside
  *     [0, max_pages * page_size], c + L_s past it, or a row that an earlier
- *     request of the batch names; and (flag 1) one with malformed
- *     cu_seqlens.
+ *     request of the batch names; and (flag 1) the first one with malformed
+ *     cu_seqlens and every one behind it, whose tokens cannot be told apart.
  *   - The outputs may be the inputs (kv_lens_out == kv_lens_in, free_count_out
  *     == free_count_in); where they are not, rows outside the batch are not
  *     written.  free_pages itself is not changed.

@@ -21,7 +21,7 @@ struct KvWs {
   int32_t* owner;   // [num_rows] the first request of the batch that names the row
   int64_t* first;   // [N] e_s, or kNoPlan for a skipped or refused request
   int64_t* ctx;     // [N] positions cached before the call
-  int32_t* count;   // [1] pages on the free list before the call
+  int32_t* count;   // [2] pages on the free list before the call; requests before malformed cu_seqlens
 };
 
 KvWs kv_ws(void* ws, int64_t n) {
@@ -103,8 +103,11 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(kda_kv_plan_args 
   __shared__ int64_t part[2][32];
   __shared__ int64_t sm_cu[kSlots ? kPlanThreads + 1 : 1], sm_first[kSlots ? kPlanThreads : 1],
       sm_ctx[kSlots ? kPlanThreads : 1];
+  __shared__ int32_t sm_good;  // requests before the first with malformed cu_seqlens
   extern __shared__ int32_t sm_owner[];
   const int tid = threadIdx.x, threads = blockDim.x;
+  if (tid == 0) sm_good = a.num_seqs;
+  __syncthreads();
   pdl_wait();
   int32_t count = *a.free_count_in;
   int32_t* owner = a.num_rows <= kSharedRows ? sm_owner : w.owner;
@@ -130,6 +133,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(kda_kv_plan_args 
       }
       if (b < 0 || e < b || e > a.total_tokens || (s == 0 && b != 0)) {
         attn_flag(a.status, kFlagBadSeqlens);
+        atomicMin(&sm_good, s);
       } else if (r >= 0) {
         c = a.kv_lens_in[r];
         const int64_t most = (int64_t)a.max_pages << shift;
@@ -145,6 +149,9 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(kda_kv_plan_args 
     int64_t total, all;
     const int64_t end = before + block_scan(need, part[0], &total);
     if (s < a.num_seqs) {
+      // behind malformed offsets a token's request cannot be told (what these
+      // requests need stands behind all that is served in the prefix sum)
+      if (s >= *reinterpret_cast<volatile int32_t*>(&sm_good)) ok = false;
       if (ok && need > 0 && end > count) {
         ok = false;
         attn_flag(a.status, kFlagNoPages);
@@ -167,13 +174,17 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(kda_kv_plan_args 
   }
   if (tid == 0) {
     *a.free_count_out = count - (int32_t)served;
-    if (!kSlots) *w.count = count;
+    if (!kSlots) {
+      w.count[0] = count;
+      w.count[1] = sm_good;
+    }
   }
   if constexpr (kSlots) {
     __syncthreads();
+    const int32_t good = sm_good;
     for (int64_t t = tid; t < a.total_tokens; t += threads) {
       // the request of the token: a decode batch has one token each
-      int32_t s = t < a.num_seqs && sm_cu[t] == t && sm_cu[t + 1] > t ? (int32_t)t : seq_of_token(sm_cu, a.num_seqs, t);
+      int32_t s = t < good && sm_cu[t] == t && sm_cu[t + 1] > t ? (int32_t)t : seq_of_token(sm_cu, good, t);
       const int64_t b = sm_cu[s], first = sm_first[s];
       a.slot_map[t] = t >= b && t < sm_cu[s + 1] && first != kNoPlan
                           ? plan_slot(a, shift, count, t, s, b, sm_ctx[s], first)
@@ -186,10 +197,10 @@ __global__ void __launch_bounds__(256) kv_slots_kernel(kda_kv_plan_args a, KvWs 
   const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
   pdl_wait();
   if (t >= a.total_tokens) return;
-  const int32_t s = seq_of_token(a.cu_seqlens, a.num_seqs, t);
+  const int32_t s = seq_of_token(a.cu_seqlens, w.count[1], t);
   const int64_t b = a.cu_seqlens[s], e = a.cu_seqlens[s + 1];
   const int64_t first = w.first[s];
-  a.slot_map[t] = t >= b && t < e && first != kNoPlan ? plan_slot(a, shift, *w.count, t, s, b, w.ctx[s], first) : -1;
+  a.slot_map[t] = t >= b && t < e && first != kNoPlan ? plan_slot(a, shift, w.count[0], t, s, b, w.ctx[s], first) : -1;
 }
 
 // One CTA: the pages each row gives back and their prefix sum, then the pages

@@ -6,7 +6,7 @@ import torch
 
 from linear_attention_serving_delta_gb300 import kda
 from test_gpu_attn import cu_of
-from test_gpu_kv import pool
+from test_gpu_kv import plan_by_hand, pool
 
 pytestmark = pytest.mark.gpu
 
@@ -50,3 +50,19 @@ def test_plan_of_lengths_next_to_64_bits(n):
     assert p.device_status() == 32 and int(p.free_count_out) == count
     assert torch.equal(d[1].cpu(), table) and torch.equal(out.cpu(), torch.cat([torch.full((n,), 8), bad]))
     assert (p.slot_map[n:] == -1).all() and (p.slot_map[:n] >= 0).all()
+
+
+@pytest.mark.parametrize("T", [40, 6000])
+@pytest.mark.parametrize("cu,good", [([0, 10, 7, 30], 1), ([0, 20, 5, 8, 30], 1), ([0, 4, 9, 41000, 12, 30], 2),
+                                     ([0, 16, 32, 31, 40], 2), ([2, 10, 30], 0), ([0, 18, -3, 20], 1)])
+def test_nothing_behind_malformed_seqlens_is_planned(cu, good, T):
+    """The first malformed request and those behind it are refused; those before it are served whole."""
+    n = len(cu) - 1
+    table, kv, free, count = pool(n, 8, 16, [3, 20, 5, 0, 17][:n], 30, 4)
+    d = [x.cuda() for x in (torch.tensor(cu), table, kv, free)]
+    p = kda.KvPlan(d[0], T, d[1], d[2], d[3], torch.tensor([count], dtype=torch.int32, device="cuda"),
+                   page_size=16).run()
+    want = plan_by_hand(cu[:good + 1] if good else [0], T, table, kv, free, count, 16, None)
+    assert p.device_status() == 1
+    assert torch.equal(d[1].cpu(), want[0]) and torch.equal(p.slot_map.cpu(), want[1])
+    assert torch.equal(d[2].cpu(), want[2]) and int(p.free_count_out) == want[3]
