@@ -199,6 +199,7 @@ __device__ void load_v_role(const AttnParams& p, const TcArgs& a, const CUtensor
         ++nfix;
         if (!ok) break;
         // in 16-byte pieces of a block: the rows some row may not attend, the end of the sequence
+        // (an item holds two tokens where its sequence does: one of a single token is the sequence's last)
         const int from = max(0, it.pos0 + 1 - x0) * 8, live = min(kTile, it.kv_len - x0) * 8;
         bool bad = false;
 #pragma unroll

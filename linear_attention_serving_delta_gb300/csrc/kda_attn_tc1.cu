@@ -172,23 +172,23 @@ __device__ void load_v_bf16(const AttnParams& p, const TcArgs& a, const CUtensor
         ok = warp_wait<1, DP>(&b->fix, nfix & 1, &b->dead);
         ++nfix;
         if (!ok) break;
-        // in 16-byte pieces of a block: the rows some row may not attend, the end of the sequence
-        const int from = max(0, it.pos0 + 1 - x0) * 8, live = min(kKeys, it.kv_len - x0) * 8;
+        // in 16-byte pieces of a block: the rows some row may not attend, and the
+        // first that none may (a sequence's later tokens stand there too)
+        const int from = max(0, it.pos0 + 1 - x0) * 8,
+                  live = min(kKeys, min(it.kv_len, it.pos0 + it.ntok) - x0) * 8;
         bool bad = false;
 #pragma unroll
         for (int c = 0; c < S::NB; ++c) {
           uint4* blk = reinterpret_cast<uint4*>(dst + c * S::kKBlock);
-          if (it.ntok > 1) {
 #pragma unroll 4
-            for (int v = from + lane; v < live; v += 32) {
-              const uint4 x = blk[v];
-              const uint32_t t = (((x.x & 0x7f807f80u) + 0x00800080u) | ((x.y & 0x7f807f80u) + 0x00800080u) |
-                                  ((x.z & 0x7f807f80u) + 0x00800080u) | ((x.w & 0x7f807f80u) + 0x00800080u)) &
-                                 0x80008000u;
-              if (t) {
-                bad = true;
-                blk[v] = make_uint4(finite_only(x.x), finite_only(x.y), finite_only(x.z), finite_only(x.w));
-              }
+          for (int v = from + lane; v < live; v += 32) {
+            const uint4 x = blk[v];
+            const uint32_t t = (((x.x & 0x7f807f80u) + 0x00800080u) | ((x.y & 0x7f807f80u) + 0x00800080u) |
+                                ((x.z & 0x7f807f80u) + 0x00800080u) | ((x.w & 0x7f807f80u) + 0x00800080u)) &
+                               0x80008000u;
+            if (t) {
+              bad = true;
+              blk[v] = make_uint4(finite_only(x.x), finite_only(x.y), finite_only(x.z), finite_only(x.w));
             }
           }
           for (int v = live + lane; v < kKeys * 8; v += 32) blk[v] = make_uint4(0, 0, 0, 0);
