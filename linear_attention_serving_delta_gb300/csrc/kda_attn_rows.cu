@@ -76,6 +76,17 @@ struct Tile {
   int32_t kvh;          // key head
 };
 
+// The non-finite values taken out of a block's V: the positions past its first
+// token's that had some, and for those that all of its rows attend the channels
+// with +inf, -inf and NaN, a bit each
+struct Poison {
+  int32_t from, to;
+  uint32_t seen;
+  uint32_t bits[3][8];
+};
+constexpr int kPoisonWords = sizeof(Poison) / 4;
+__device__ __forceinline__ int32_t no_poison(int word) { return word == 0 ? INT32_MAX : word == 1 ? -1 : 0; }
+
 struct Tail {
   uint64_t full[8], empty[8];
   uint64_t join[2];
@@ -86,7 +97,7 @@ struct Tail {
   int64_t sum[kWarps + 1];
   int64_t found;   // where in its sequence's tiles the stretch starts
   int32_t found_at;
-  int32_t poison[3][2];  // positions whose non-finite values were taken out of a block's V: its k-th in turn
+  Poison poison[3];  // of the CTA's k-th block, in turn
   AttnSeq found_seq;
 };
 static_assert(sizeof(Tail) <= 2048, "tail block");
@@ -188,10 +199,11 @@ __device__ __forceinline__ void mma_keys(float* d, const uint32_t* a, uint32_t b
   else mma1688(d, a, b0);
 }
 // Non-finite values among keys [key0, key0 + n) of a V tile (x0: position of the
-// tile's first key) become zeros; range takes in the positions they had.  The
-// block's outputs get them back when they are written (poison_of).
+// tile's first key) become zeros and are noted in ps (pos0: the last position that
+// all rows attend).  The block's outputs get them back when they are written.
 template <typename T, int NB>
-__device__ __noinline__ void take_out(char* vs, uint32_t block, int key0, int n, int x0, int32_t* range, int lane) {
+__device__ __noinline__ void take_out(char* vs, uint32_t block, int key0, int n, int x0, int pos0, Poison* ps, int lane) {
+  constexpr int E = 16 / (int)sizeof(T);
   int lo = INT32_MAX, hi = -1;
 #pragma unroll 1
   for (int i = lane; i < n * NB * 8; i += 32) {
@@ -205,15 +217,26 @@ __device__ __noinline__ void take_out(char* vs, uint32_t block, int key0, int n,
       auto keep = [](uint32_t v) { return (v & 0x7f800000u) == 0x7f800000u ? 0u : v; };
       y = make_uint4(keep(x.x), keep(x.y), keep(x.z), keep(x.w));
     }
-    if (x.x != y.x || x.y != y.y || x.z != y.z || x.w != y.w) {
-      *at = y;
+    if (x.x == y.x && x.y == y.y && x.z == y.z && x.w == y.w) continue;
+    *at = y;
+    if (x0 + r > pos0) {
       lo = min(lo, x0 + r);
       hi = max(hi, x0 + r);
+    } else {
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float f = E == 4 ? __uint_as_float(w[e & 3]) : e & 1 ? bf_hi(w[e / 2 & 3]) : bf_lo(w[e / 2 & 3]);
+        const int ch = i % (NB * 8) * E + e;
+        if ((__float_as_uint(f) & 0x7f800000u) == 0x7f800000u)
+          atomicOr_block(&ps->bits[poison_kind(f)][ch >> 5], 1u << (ch & 31));
+      }
     }
+    *reinterpret_cast<volatile uint32_t*>(&ps->seen) = 1;
   }
   if (hi >= 0) {
-    atomicMin_block(&range[0], lo);
-    atomicMax_block(&range[1], hi);
+    atomicMin_block(&ps->from, lo);
+    atomicMax_block(&ps->to, hi);
   }
 }
 
@@ -239,7 +262,7 @@ struct RowsBf16 {
     l[0] = l[1] = 0.f;
   }
 
-  __device__ void step(char* stage, const float*, const Tile& t, float sc, int32_t* range, int warp, int lane) {
+  __device__ void step(char* stage, const float*, const Tile& t, float sc, Poison* ps, int warp, int lane) {
     const int x0 = t.x0 + 16 * warp;  // this warp's keys
     if (x0 >= t.end) return;
     const uint32_t ks = smem_u32(stage);
@@ -320,7 +343,7 @@ struct RowsBf16 {
         s[n][e] = exp2_fast(fmaf(s[n][e], sc, -ref[e >> 1]));
         l[e >> 1] += s[n][e];
       }
-    if (masked && poison) take_out<__nv_bfloat16, S::NB>(vs, S::kBlock, 16 * warp, 16, t.x0, range, lane);
+    if (masked && poison) take_out<__nv_bfloat16, S::NB>(vs, S::kBlock, 16 * warp, 16, t.x0, t.pos0, ps, lane);
     __syncwarp();  // V's zeroed rows
     const uint32_t a[4] = {pack2(s[0][0], s[0][1]), pack2(s[0][2], s[0][3]), pack2(s[1][0], s[1][1]),
                            pack2(s[1][2], s[1][3])};
@@ -402,7 +425,7 @@ struct RowsF32 {
     }
   }
 
-  __device__ void step(char* stage, const float* qs, const Tile& t, float sc, int32_t* range, int warp, int lane) {
+  __device__ void step(char* stage, const float* qs, const Tile& t, float sc, Poison* ps, int warp, int lane) {
     const int x0 = t.x0 + KW * warp;  // this warp's keys
     if (x0 >= t.end) return;
     char* vs = stage + S::NB * S::kBlock;
@@ -530,7 +553,7 @@ struct RowsF32 {
           l[i][e >> 1] += s[i][n][e];
         }
     }
-    if (poison) take_out<float, S::NB>(vs, S::kBlock, KW * warp, KW, t.x0, range, lane);
+    if (poison) take_out<float, S::NB>(vs, S::kBlock, KW * warp, KW, t.x0, t.pos0, ps, lane);
     __syncwarp();  // V's zeroed rows
     uint32_t ah[MT][2 * NT], am[MT][2 * NT], al[MT][2 * NT];
 #pragma unroll
@@ -637,12 +660,9 @@ __global__ void __launch_bounds__(kThreads, Shape<T, DP, Work::kRows>::CTAS)
     mbar_init(&b->join[0], kWarps);
     mbar_init(&b->join[1], kWarps);
     b->dead = 0;
-    for (int s = 0; s < 3; ++s) {
-      b->poison[s][0] = INT32_MAX;
-      b->poison[s][1] = -1;
-    }
     mbar_init_fence();
   }
+  if (tid < 3 * kPoisonWords) reinterpret_cast<int32_t*>(b->poison)[tid] = no_poison(tid % kPoisonWords);
   if (tid == 32) {
     prefetch_map(&mk);
     prefetch_map(&mv);
@@ -853,7 +873,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, DP, Work::kRows>::CTAS)
         }
         w.start(stage, qs, lane);
       }
-      w.step(stage, qs, t, sc, b->poison[block], warp, lane);
+      w.step(stage, qs, t, sc, &b->poison[block], warp, lane);
       if (t.last) {
         const int rows = t.rows;
         w.stats(b->ml[warp], lane);
@@ -884,8 +904,8 @@ __global__ void __launch_bounds__(kThreads, Shape<T, DP, Work::kRows>::CTAS)
         if (!__all_sync(0xffffffffu, wait_or_dead(&b->join[1], joins & 1, &b->dead))) break;
         ++joins;
         T* out = static_cast<T*>(p.o);
-        const int32_t* range = b->poison[block];
-        const bool poisoned = *reinterpret_cast<const volatile int32_t*>(&range[1]) >= 0;
+        const Poison* ps = &b->poison[block];
+        const bool poisoned = *reinterpret_cast<const volatile uint32_t*>(&ps->seen) != 0;
 #pragma unroll
         for (int i = 0; i < STEPS; ++i) {
           const int e = i * 32 * kWarps + tid, r = e / VEC, c = (e % VEC) * 4;
@@ -903,10 +923,13 @@ __global__ void __launch_bounds__(kThreads, Shape<T, DP, Work::kRows>::CTAS)
             const int64_t stride = (int64_t)p.Hkv * p.D;
             const T* v = static_cast<const T*>(p.v) + (int64_t)t.kvh * p.D + c + (p.block_table ? 0 : t.base * stride);
             const int32_t* pages = p.block_table ? p.block_table + (int64_t)t.base * p.max_pages : nullptr;
-            const int to = min(range[1], min(t.end - 1, t.pos0 + r / t.gb));
+            const int to = min(ps->to, min(t.end - 1, t.pos0 + r / t.gb));
 #pragma unroll 1
             for (int u = 0; u < 4 && c + u < p.D; ++u) {
-              const float z = poison_of(v + u, stride, pages, p.num_pages, p.page_shift, range[0], to);
+              const int ch = c + u;
+              auto bit = [&](int kind) { return (ps->bits[kind][ch >> 5] >> (ch & 31) & 1) != 0; };
+              const float z = poison_value(bit(0), bit(1), bit(2)) +
+                              poison_of(v + u, stride, pages, p.num_pages, p.page_shift, ps->from, to);
               const float y = u == 0 ? x.x : u == 1 ? x.y : u == 2 ? x.z : x.w;
               const float s = z != 0.f ? y + z : y;  // a NaN already there stays
               if (u == 0) x.x = s;
@@ -931,10 +954,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, DP, Work::kRows>::CTAS)
         // the word of the block after next is free: all warps are past the block
         // before this one, and none starts that one before this thread's next join
         const int next = block == 0 ? 2 : block - 1;
-        if (tid == 0) {
-          b->poison[next][0] = INT32_MAX;
-          b->poison[next][1] = -1;
-        }
+        if (tid < kPoisonWords) reinterpret_cast<int32_t*>(&b->poison[next])[tid] = no_poison(tid);
         block = block == 2 ? 0 : block + 1;
       }
       // generic accesses of the stage before the copies that refill it

@@ -76,10 +76,10 @@ struct Bars {
   OwnPlan plan;
   uint32_t turn;      // held by the MMA warp whose burst is being issued
   uint32_t tmem;
-  // the CTA's k-th item with key tiles: non-finite values were taken out of its
-  // V tiles (index k % 8; V's ring lets the copies begin at most five such
-  // items ahead of the epilogue)
-  uint32_t poison[8];
+  // the CTA's k-th item with key tiles: the channels in which non-finite values
+  // were taken out of its V tiles, a bit each (index k % 8; V's ring lets the copies
+  // begin at most five such items ahead of the epilogue)
+  uint32_t poison[8][4];
 };
 static_assert(sizeof(Bars) <= 512, "barrier block");
 
@@ -183,8 +183,8 @@ __device__ void load_v_role(const AttnParams& p, const TcArgs& a, const CUtensor
     const int h = (int)(w % p.Hkv);
     const Geo g = geometry(it, p.G, tpt);
     if (g.nmax == 0) continue;
-    uint32_t* poison = &b->poison[busy_items++ & 7];
-    if (lane == 0) *poison = 0;
+    uint32_t* poison = b->poison[busy_items++ & 7];
+    if (lane < 4) poison[lane] = 0;  // (before the copies' __syncwarp)
     for (int j = 0; j < g.nmax; ++j) {
       const int kt = g.kt0 + j, x0 = kt * kTile;
       const bool fix = kt >= g.fix_from;
@@ -201,7 +201,6 @@ __device__ void load_v_role(const AttnParams& p, const TcArgs& a, const CUtensor
         // in 16-byte pieces of a block: the rows some row may not attend, the end of the sequence
         // (an item holds two tokens where its sequence does: one of a single token is the sequence's last)
         const int from = max(0, it.pos0 + 1 - x0) * 8, live = min(kTile, it.kv_len - x0) * 8;
-        bool bad = false;
 #pragma unroll
         for (int c = 0; c < S::NH; ++c) {
           uint4* blk = reinterpret_cast<uint4*>(dst + c * S::kBlock);
@@ -214,14 +213,13 @@ __device__ void load_v_role(const AttnParams& p, const TcArgs& a, const CUtensor
                                   ((x.z & 0x7f807f80u) + 0x00800080u) | ((x.w & 0x7f807f80u) + 0x00800080u)) &
                                  0x80008000u;
               if (t) {
-                bad = true;
+                mark_channels(poison, c, v, x);
                 blk[v] = make_uint4(finite_only(x.x), finite_only(x.y), finite_only(x.z), finite_only(x.w));
               }
             }
           }
           for (int v = live + lane; v < kTile * 8; v += 32) blk[v] = make_uint4(0, 0, 0, 0);
         }
-        if (bad) *reinterpret_cast<volatile uint32_t*>(poison) = 1;
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&b->v_full[ring.st]);
@@ -395,7 +393,7 @@ __device__ void softmax_role(const AttnParams& p, const TcArgs& a, Bars* b, int6
     fetch(nth_item(i + 1));
     const Geo g = geometry(it, p.G, tpt);
     const int rows = g.rows[t], n = g.n[t];
-    const uint32_t* poisoned = &b->poison[busy_items & 7];
+    const uint32_t* poisoned = b->poison[busy_items & 7];
     busy_items += g.nmax > 0;
     if (rows == 0) continue;
     const int tok = row / p.G;  // within the row tile
@@ -496,7 +494,6 @@ __device__ void softmax_role(const AttnParams& p, const TcArgs& a, Bars* b, int6
       fence_after_sync();
     }
     if (!busy) continue;
-    const bool poison = n > 0 && *reinterpret_cast<const volatile uint32_t*>(poisoned) != 0;
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const int gq = row - tok * p.G;
     const bool mine = row < rows;
@@ -517,6 +514,7 @@ __device__ void softmax_role(const AttnParams& p, const TcArgs& a, Bars* b, int6
         const float f = it.slot < 0 ? inv : 1.f;
 #pragma unroll
         for (int u = 0; u < 32; ++u) x[u] *= f;
+        const uint32_t poison = n > 0 ? reinterpret_cast<const volatile uint32_t*>(poisoned)[c >> 5] : 0;
         if (poison) {
           const int from = max(g.kt0 * kTile, it.pos0 + 1), to = min(limit, min(it.kv_len, it.kt1 * kTile) - 1);
           const int64_t stride = (int64_t)p.Hkv * p.D;
@@ -525,7 +523,7 @@ __device__ void softmax_role(const AttnParams& p, const TcArgs& a, Bars* b, int6
           const int32_t* pages = p.block_table ? p.block_table + (int64_t)it.base * p.max_pages : nullptr;
 #pragma unroll
           for (int u = 0; u < 32; ++u) {
-            if (c + u >= p.D) break;
+            if (!(poison >> u & 1)) continue;
             const float y = poison_of(v + u, stride, pages, p.num_pages, p.page_shift, from, to);
             if (y != 0.f) x[u] += y;  // a NaN already there stays
           }

@@ -182,9 +182,17 @@ __device__ bool plan_own_item(const AttnParams& p, const TcArgs& a, OwnPlan* b) 
   return *reinterpret_cast<volatile uint32_t*>(&b->own) != 0;
 }
 
-// The non-finite values taken out of V tiles, put back into one channel of one
-// row (slow path): what the attended positions from..limit give it, an infinity,
-// or NaN where both signs or a NaN meet; 0 for none.
+// The non-finite values taken out of V tiles come back at the output (slow
+// path).  What a channel of a row gets: an infinity, or NaN where both signs or
+// a NaN meet; 0 for none.
+__device__ __forceinline__ float poison_value(bool pos, bool neg, bool nan) {
+  return nan || (pos && neg) ? NAN : pos ? INFINITY : neg ? -INFINITY : 0.f;
+}
+// The kind of a non-finite value, as an index of a row of bits: +inf, -inf, NaN
+__device__ __forceinline__ int poison_kind(float x) { return x != x ? 2 : x < 0.f ? 1 : 0; }
+// From the cache itself, over the positions from..limit: those that some rows of
+// a tile may attend and others may not, no more than its tokens (a longer way,
+// one load after the other, would outlast the CTA's other waits).
 template <typename T>
 static __device__ __noinline__ float poison_of(const T* v, int64_t stride, const int32_t* pages, int num_pages, int shift,
                                         int from, int limit) {
@@ -202,7 +210,7 @@ static __device__ __noinline__ float poison_of(const T* v, int64_t stride, const
     nan |= y != y;
     if (nan || (pos && neg)) break;
   }
-  return nan || (pos && neg) ? NAN : pos ? INFINITY : neg ? -INFINITY : 0.f;
+  return poison_value(pos, neg, nan);
 }
 
 namespace tc {
@@ -356,6 +364,20 @@ __device__ __forceinline__ uint32_t finite_only(uint32_t w) {
   if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
   if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
   return w;
+}
+
+// which of eight bf16 are infinite or NaN, a bit each
+__device__ __forceinline__ uint32_t nonfinite8(uint4 x) {
+  auto two = [](uint32_t w) {
+    return ((w & 0x7f80u) == 0x7f80u ? 1u : 0u) | ((w & 0x7f800000u) == 0x7f800000u ? 2u : 0u);
+  };
+  return two(x.x) | two(x.y) << 2 | two(x.z) << 4 | two(x.w) << 6;
+}
+// the same piece v of a swizzled block (64 channels from `block` x 64 on) marked in a
+// bit for each channel
+__device__ __forceinline__ void mark_channels(uint32_t* words, int block, int v, uint4 x) {
+  const int piece = (v & 7) ^ ((v >> 3) & 7);
+  atomicOr_block(&words[2 * block + (piece >> 2)], nonfinite8(x) << (8 * (piece & 3)));
 }
 
 // byte offset of 16-byte piece c of row r in swizzled blocks of `block` bytes

@@ -68,9 +68,12 @@ struct Bars {
   uint64_t q_full, q_empty, s_full[2], p_full[2], pv_done[2], fix, drain;
   uint32_t dead, tmem;
   OwnPlan plan;
-  // the CTA's k-th item with key tiles (index k % 8): the positions whose
-  // non-finite values were taken out of V
+  // the CTA's k-th item with key tiles (index k % 8): the positions past its first
+  // token's whose non-finite values were taken out of V, and their channels, a bit
+  // each; (fp32) three more rows of bits for the positions that all of its rows
+  // attend, the channels with +inf, -inf and NaN there
   int32_t poison_from[8], poison_to[8];
+  uint32_t poison[8][16];
 };
 static_assert(sizeof(Bars) <= 1024, "barrier block");
 
@@ -161,6 +164,7 @@ __device__ void load_v_bf16(const AttnParams& p, const TcArgs& a, const CUtensor
     if (g.n <= 0) continue;
     const int slot = busy++ & 7;
     if (lane == 0) b->poison_to[slot] = -1;
+    if (lane < 8) b->poison[slot][lane] = 0;  // (before the copies' __syncwarp)
     for (int j = 0; j < g.n; ++j) {
       const int kt = g.kt0 + j, x0 = kt * kKeys;
       const bool fix = kt >= g.fix_from;
@@ -188,6 +192,7 @@ __device__ void load_v_bf16(const AttnParams& p, const TcArgs& a, const CUtensor
                                0x80008000u;
             if (t) {
               bad = true;
+              mark_channels(b->poison[slot], c, v, x);
               blk[v] = make_uint4(finite_only(x.x), finite_only(x.y), finite_only(x.z), finite_only(x.w));
             }
           }
@@ -283,6 +288,7 @@ __device__ void split_role(const AttnParams& p, const TcArgs& a, char* sm, Bars*
       b->poison_from[(busy + 3) & 7] = INT32_MAX;
       b->poison_to[(busy + 3) & 7] = -1;
     }
+    if (tid < 16) b->poison[(busy + 3) & 7][tid] = 0;
     ++busy;
     if (!warp_wait<3, DP>(&b->q_empty, (nq & 1) ^ 1, &b->dead)) return;
     ++nq;
@@ -334,9 +340,15 @@ __device__ void split_role(const AttnParams& p, const TcArgs& a, char* sm, Bars*
             for (int u = 0; u < 8; ++u) {
               if (r >= live) x[u] = 0.f;
               if ((__float_as_uint(x[u]) & 0x7f800000u) == 0x7f800000u) {
+                const int ch = 8 * c + u;
+                if (x0 + r <= it.pos0) {
+                  atomicOr_block(&b->poison[slot][4 + 4 * poison_kind(x[u]) + (ch >> 5)], 1u << (ch & 31));
+                } else {
+                  atomicOr_block(&b->poison[slot][ch >> 5], 1u << (ch & 31));
+                  lo = min(lo, x0 + r);
+                  hi = max(hi, x0 + r);
+                }
                 x[u] = 0.f;
-                lo = min(lo, x0 + r);
-                hi = max(hi, x0 + r);
               }
             }
           }
@@ -590,7 +602,6 @@ __device__ void softmax_role(const AttnParams& p, const TcArgs& a, Bars* b, int6
                 to = n > 0 ? min(*reinterpret_cast<volatile int32_t*>(&b->poison_to[slot]),
                                  min(limit, min(it.kv_len, it.kt1 * kKeys) - 1))
                            : -1;
-      const bool poison = n > 0 && *reinterpret_cast<volatile int32_t*>(&b->poison_to[slot]) >= 0;
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const int gq = row - tok * p.G;
       const bool live = row < g.rows;
@@ -617,14 +628,20 @@ __device__ void softmax_role(const AttnParams& p, const TcArgs& a, Bars* b, int6
           const float f = it.slot < 0 ? inv : 1.f;
 #pragma unroll
           for (int u = 0; u < 32; ++u) x[u] *= f;
-          if (poison) {
+          const volatile uint32_t* bits = b->poison[slot] + (c >> 5);
+          const uint32_t some = n > 0 ? bits[0] : 0;  // channels with such values that some rows attend
+          uint32_t all[3] = {0, 0, 0};                // and that all rows do
+          if (NP == 3 && n > 0)
+#pragma unroll
+            for (int z = 0; z < 3; ++z) all[z] = bits[4 + 4 * z];
+          if (some | all[0] | all[1] | all[2]) {
             const int64_t stride = (int64_t)p.Hkv * p.D;
             const T* v = static_cast<const T*>(p.v) + (int64_t)h * p.D + c + (p.block_table ? 0 : it.base * stride);
             const int32_t* pages = p.block_table ? p.block_table + (int64_t)it.base * p.max_pages : nullptr;
 #pragma unroll
             for (int u = 0; u < 32; ++u) {
-              if (c + u >= p.D) break;
-              const float z = poison_of(v + u, stride, pages, p.num_pages, p.page_shift, from, to);
+              float z = poison_value(all[0] >> u & 1, all[1] >> u & 1, all[2] >> u & 1);
+              if (some >> u & 1) z += poison_of(v + u, stride, pages, p.num_pages, p.page_shift, from, to);
               if (z != 0.f) x[u] += z;  // a NaN already there stays
             }
           }
@@ -689,6 +706,7 @@ __global__ void __launch_bounds__(Shape<NP, DP>::kThreads, 1)
     for (int s = 0; s < 8; ++s) {
       b->poison_from[s] = INT32_MAX;
       b->poison_to[s] = -1;
+      for (int z = 0; z < 16; ++z) b->poison[s][z] = 0;
     }
     b->dead = 0;
     b->plan.own = 0;

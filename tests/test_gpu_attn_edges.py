@@ -42,3 +42,89 @@ def test_later_tokens_of_a_chunk_never_reach_wide_groups(D, dtype, G):
     o = kda.attn_paged(q, p.k, p.v, p.table, p.lens, cu)
     check(o[:at], *reference(q[:at], p.K[0][:ctx + at], p.V[0][:ctx + at], ctx, D ** -0.5, dtype))
     assert torch.equal(o[:at], clean[:at]) and torch.isnan(o[at:].float()).all()
+
+
+# ------------------------------------------------------------------ values that are not finite
+def check_classes(o, q, k, v, pos0, scale, dtype):
+    """Each output's kind is that of the values its row attends in its channel: NaN for a NaN or both
+    infinities, an infinity for one, and otherwise finite, with the tolerance of the same values without
+    the others' (zeros in their place)."""
+    H, G = q.shape[1], q.shape[1] // v.shape[1]
+    last = torch.arange(pos0, pos0 + q.shape[0], device=q.device).clamp(max=v.shape[0] - 1)
+
+    def any_up_to(hit):  # [m, Hkv, D] -> [n, H, D]: one such value at or before the row's position
+        return (hit.cumsum(0) > 0)[last].repeat_interleave(G, 1)
+
+    pos, neg = any_up_to(torch.isposinf(v)), any_up_to(torch.isneginf(v))
+    nan = any_up_to(torch.isnan(v)) | (pos & neg)
+    assert torch.equal(torch.isnan(o), nan)
+    assert torch.equal(torch.isposinf(o), pos & ~nan) and torch.equal(torch.isneginf(o), neg & ~nan)
+    ref, tol = reference(q, k, torch.where(torch.isfinite(v), v, torch.zeros_like(v)), pos0, scale, dtype)
+    finite = torch.isfinite(o)
+    check(torch.where(finite, o, torch.zeros_like(o)), torch.where(finite, ref, torch.zeros_like(ref)),
+          torch.where(finite, tol, torch.ones_like(tol)))
+
+
+def strew(v, seed, share):
+    """Infinities of both signs and NaN in a share of v's places, in half of the channels."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    where = torch.rand(v.shape, generator=g, device="cuda") < share
+    where[..., ::2] = False
+    kind = torch.randint(0, 5, v.shape, generator=g, device="cuda")
+    for z, x in enumerate(("inf", "inf", "-inf", "-inf", "nan")):
+        v[where & (kind == z)] = float(x)
+
+
+KINDS = [(4, 2, 64, "bf16"), (8, 2, 128, "bf16"), (6, 2, 32, "bf16"), (4, 2, 256, "bf16"), (130, 2, 256, "bf16"),
+         (4, 2, 64, "f32"), (8, 2, 128, "f32"), (100, 1, 128, "f32"), (4, 2, 32, "f32"), (4, 1, 256, "f32")]
+
+
+@pytest.mark.parametrize("H,Hkv,D,dtype", KINDS)
+@pytest.mark.parametrize("share", [0.0005, 0.01])
+def test_strewn_values_in_prompts(H, Hkv, D, dtype, share):
+    g = gen(H + D)
+    lens = [330, 1, 95]
+    T = sum(lens)
+    q, k, v = rand(g, T, H, D, dtype=dtype), rand(g, T, Hkv, D, dtype=dtype), rand(g, T, Hkv, D, dtype=dtype)
+    strew(v, H, share)
+    cu = cu_of(lens)
+    a = kda.AttnPrefill(q, k, v, cu.cuda()).run()
+    assert a.device_status() == 0
+    for b, e in zip(cu.tolist(), cu.tolist()[1:]):
+        check_classes(a.o[b:e], q[b:e], k[b:e], v[b:e], 0, D ** -0.5, dtype)
+
+
+@pytest.mark.parametrize("H,Hkv,D,dtype", KINDS)
+@pytest.mark.parametrize("ctx,new", [([150, 700], [60, 3]), ([5000, 40], [20, 1]), ([3000, 900, 16], [1, 1, 1])])
+def test_strewn_values_in_the_cache(H, Hkv, D, dtype, ctx, new):
+    p = Pool(ctx, new, Hkv, D, 16, dtype, 3)
+    for i, (c, n) in enumerate(zip(ctx, new)):
+        strew(p.V[i], i, 0.001)
+        x = torch.arange(c + n)
+        slot = (p.table[i].cpu().long()[x // 16] * 16 + x % 16).cuda()
+        p.v.view(-1, Hkv, D)[slot] = p.V[i]
+    cu = cu_of(new)
+    q = rand(gen(H), sum(new), H, D, dtype=dtype)
+    a = kda.AttnPaged(q, p.k, p.v, p.table, p.lens, cu.cuda(), max_seqlen=max(new)).run()
+    assert a.device_status() == 0
+    for i, c in enumerate(ctx):
+        b, e = int(cu[i]), int(cu[i + 1])
+        check_classes(a.o[b:e], q[b:e], p.K[i], p.V[i], c, D ** -0.5, dtype)
+
+
+@pytest.mark.parametrize("T,D,dtype", [(45_000, 128, "f32"), (45_000, 64, "f32"), (12_000, 256, "f32"),
+                                       (45_000, 128, "bf16")])
+def test_two_infinities_far_apart(T, D, dtype):
+    """One near each end of a long prompt: their rows get them, the call ends without a flag, and the prompt
+    beside it is whole."""
+    g = gen(D)
+    lens = [T, 300]
+    n = sum(lens)
+    q, k, v = rand(g, n, 1, D, dtype=dtype), rand(g, n, 1, D, dtype=dtype), rand(g, n, 1, D, dtype=dtype)
+    v[3, 0, 5] = float("inf")
+    v[T - 3, 0, 9] = -float("inf")
+    a = kda.AttnPrefill(q, k, v, cu_of(lens).cuda()).run()
+    assert a.device_status() == 0
+    for b, e in ((0, 70), (T // 2, T // 2 + 70), (T - 70, T)):
+        check_classes(a.o[b:e], q[b:e], k[:e], v[:e], b, D ** -0.5, dtype)
+    check_classes(a.o[T:], q[T:], k[T:], v[T:], 0, D ** -0.5, dtype)
