@@ -244,11 +244,24 @@ __global__ void __launch_bounds__(kPlanThreads) kv_release_kernel(kda_kv_release
       }
     }
     int64_t total;
-    const int64_t at = count + block_scan(n, part[0], &total) - n;
-    if (n > 0 && at + n > a.num_pages) {
-      attn_flag(a.status, kFlagBadCache);
-      r = -1;
-      n = 0;
+    block_scan(n, part[0], &total);
+    if (count + total > a.num_pages) {  // (an over-full list: row by row, a row that does not fit is passed over)
+      sm_end[tid] = n;
+      __syncthreads();
+      if (tid == 0) {
+        int64_t at = count;
+        for (int x = 0; x < kPlanThreads; ++x) {
+          if (at + sm_end[x] > a.num_pages) sm_end[x] = -1;
+          else at += sm_end[x];
+        }
+      }
+      __syncthreads();
+      if (sm_end[tid] < 0) {
+        attn_flag(a.status, kFlagBadCache);
+        r = -1;
+        n = 0;
+      }
+      __syncthreads();  // sm_end again
     }
     if (r >= 0) a.kv_lens[r] = 0;
     sm_end[tid] = block_scan(n, part[1], &total);

@@ -66,3 +66,36 @@ def test_nothing_behind_malformed_seqlens_is_planned(cu, good, T):
     assert p.device_status() == 1
     assert torch.equal(d[1].cpu(), want[0]) and torch.equal(p.slot_map.cpu(), want[1])
     assert torch.equal(d[2].cpu(), want[2]) and int(p.free_count_out) == want[3]
+
+
+# ------------------------------------------------------------------ a free list that cannot take every page
+def release_by_hand(rows, table, kv, free, count, page):
+    free, kv, cap = free[:count].tolist(), kv.clone(), len(free)
+    refused = False
+    for r in rows:
+        n = -(-int(kv[r]) // page)
+        if len(free) + n > cap:
+            refused = True
+            continue
+        free += table[r, :n].tolist()
+        kv[r] = 0
+    return free, kv, refused
+
+
+@pytest.mark.parametrize("M,room", [(3, 4), (40, 25), (1500, 900), (1500, 3700)])
+def test_release_into_a_full_list_takes_every_row_that_fits(M, room):
+    page = 16
+    g = torch.Generator().manual_seed(M)
+    cached = torch.randint(0, 6 * page, (M,), generator=g).tolist()
+    cached[0] = 6 * page  # the first row is refused where there is no room for it
+    num = sum(-(-c // page) for c in cached) + 40
+    table, kv, free, _ = pool(M, 8, page, cached, num, 3)
+    count = num - room
+    free = torch.where(free < 0, torch.arange(num).int(), free)
+    rows = torch.arange(M).int()
+    want = release_by_hand(rows.tolist(), table, kv, free, count, page)
+    d = [x.cuda() for x in (rows, table, kv, free)]
+    cnt = torch.tensor([count], dtype=torch.int32, device="cuda")
+    a = kda.KvRelease(*d, cnt, page_size=page).run()
+    assert want[2] and a.device_status() == 32
+    assert int(cnt) == len(want[0]) and d[3][:len(want[0])].tolist() == want[0] and torch.equal(d[2].cpu(), want[1])
