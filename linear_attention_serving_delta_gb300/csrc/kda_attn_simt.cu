@@ -37,9 +37,10 @@ __device__ TileRef find_tile(const AttnParams& p, int64_t idx, int per, int64_t*
     const int s = base + tid;
     int64_t n = 0;
     if (s < p.num_seqs) {
-      const int64_t len = p.cu_seqlens[s + 1] - p.cu_seqlens[s];
-      // malformed sequences get one tile (it raises the flag), long ones no more than the bound allows
-      n = len <= 0 ? (len < 0) : (len > p.max_seqlen ? 1 : (len + per - 1) / per);
+      const int64_t b = p.cu_seqlens[s], e = p.cu_seqlens[s + 1];
+      // malformed sequences get one tile (it raises the flag), whatever they claim: the grid has room for no more
+      const bool ok = b >= 0 && e >= b && e <= p.total_tokens && (s > 0 || b == 0) && e - b <= p.max_seqlen;
+      n = ok ? (e - b + per - 1) / per : 1;
     }
     int64_t x = n;
 #pragma unroll

@@ -128,3 +128,17 @@ def test_two_infinities_far_apart(T, D, dtype):
     for b, e in ((0, 70), (T // 2, T // 2 + 70), (T - 70, T)):
         check_classes(a.o[b:e], q[b:e], k[:e], v[:e], b, D ** -0.5, dtype)
     check_classes(a.o[T:], q[T:], k[T:], v[T:], 0, D ** -0.5, dtype)
+
+
+@pytest.mark.parametrize("scale", [-0.3, 0.125])
+@pytest.mark.parametrize("cu", [[-80, 10, 100], [10, 10, 100], [-1000, -90, 5, 100]])
+def test_a_malformed_first_sequence_leaves_the_others_whole(cu, scale):
+    """The well-formed sequence behind it is attended to its last token, on the CUDA cores and the tensor cores."""
+    g = gen(3)
+    T, G, D = 100, 64, 64
+    q, k, v = rand(g, T, G, D), rand(g, T, 1, D), rand(g, T, 1, D)
+    a = kda.AttnPrefill(q, k, v, torch.tensor(cu).cuda(), scale=scale, o=torch.full_like(q, 7.0)).run()
+    assert a.device_status() == 1
+    b, e = cu[-2:]
+    check(a.o[b:e], *reference(q[b:e], k[b:e], v[b:e], 0, scale, "bf16"))
+    assert (a.o[:b] == 7).all()
