@@ -855,6 +855,14 @@ def _shape(name, t, want):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(want)}")
 
 
+def _i32(name, x):
+    """x as the argument blocks hold it; ctypes would keep the low 32 bits of any other."""
+    x = int(x)
+    if not -(1 << 31) <= x < 1 << 31:
+        raise ValueError(f"{name} does not fit 32 bits: {x}")
+    return x
+
+
 class _CacheCall:
     """What the planned calls share: the argument block, the workspace and the
     status word are made once, on the current stream; ``run()`` only launches
@@ -975,7 +983,7 @@ class AttnPaged(_CacheCall):
         a, dt = AttnPagedArgs(), q.dtype
         a.num_seqs, a.num_heads, a.num_kv_heads, a.head_dim, a.total_tokens = N, H, Hkv, D, T
         a.cu_seqlens = _ptr(cu_seqlens, torch.int64, "cu_seqlens")
-        a.max_seqlen, a.in_dtype = min(int(max_seqlen), T), _dtype_code(dt)
+        a.max_seqlen, a.in_dtype = _i32("max_seqlen", min(int(max_seqlen), T)), _dtype_code(dt)
         a.q, a.o = _ptr(q, dt, "q"), _ptr(self.o, dt, "o")
         a.k_cache, a.v_cache = _ptr(k_cache, dt, "k_cache"), _ptr(v_cache, dt, "v_cache")
         a.num_pages, a.page_size = P, page
@@ -998,7 +1006,7 @@ class KvPlan(_CacheCall):
 
     def __init__(self, cu_seqlens, total_tokens, block_table, kv_lens, free_pages, free_count, *,
                  page_size, rows=None, kv_lens_out=None, free_count_out=None, slot_map=None, status=None):
-        N = _cu(cu_seqlens)
+        N, page_size = _cu(cu_seqlens), _i32("page_size", page_size)
         if block_table.dim() != 2:
             raise ValueError(f"block_table must be [rows, max_pages], got {tuple(block_table.shape)}")
         R, M = block_table.shape
@@ -1023,7 +1031,7 @@ class KvPlan(_CacheCall):
         a = KvPlanArgs()
         a.num_seqs, a.total_tokens = N, int(total_tokens)
         a.cu_seqlens = _ptr(cu_seqlens, torch.int64, "cu_seqlens")
-        a.page_size, a.num_pages, a.num_rows, a.max_pages = int(page_size), free_pages.numel(), R, M
+        a.page_size, a.num_pages, a.num_rows, a.max_pages = page_size, free_pages.numel(), R, M
         a.rows = _ptr(rows, torch.int32, "rows")
         a.block_table = _ptr(block_table, torch.int32, "block_table")
         a.kv_lens_in = _ptr(kv_lens, torch.int64, "kv_lens")
@@ -1044,13 +1052,13 @@ class KvRelease(_CacheCall):
     def __init__(self, rows, block_table, kv_lens, free_pages, free_count, *, page_size, status=None):
         if rows.dim() != 1 or block_table.dim() != 2 or free_pages.dim() != 1:
             raise ValueError("rows must be [M], block_table [rows, max_pages], free_pages [num_pages]")
-        R, M = block_table.shape
+        (R, M), page_size = block_table.shape, _i32("page_size", page_size)
         _shape("kv_lens", kv_lens, (R,))
         _shape("free_count", free_count, (1,))
         dev = _same_device(rows=rows, block_table=block_table, kv_lens=kv_lens, free_pages=free_pages,
                            free_count=free_count)
         a = KvReleaseArgs()
-        a.num_release, a.page_size, a.num_pages = rows.numel(), int(page_size), free_pages.numel()
+        a.num_release, a.page_size, a.num_pages = rows.numel(), page_size, free_pages.numel()
         a.num_rows, a.max_pages = R, M
         a.rows = _ptr(rows, torch.int32, "rows")
         a.block_table = _ptr(block_table, torch.int32, "block_table")
