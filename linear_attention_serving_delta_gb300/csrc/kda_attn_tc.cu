@@ -418,8 +418,10 @@ __device__ void softmax_role(const AttnParams& p, const TcArgs& a, Bars* b, int6
         }
         // The first half's weights against the old reference, beside the
         // maximum of the second half.  If their sum, or that maximum, has
-        // risen too far for some row of the warp, the reference moves and they
-        // are taken again (the first tile, and seldom after).
+        // risen too far for some row of the warp, they are taken again (the
+        // first tile, and seldom after), and the reference of that row moves: of
+        // no other one, which may be another token's, or none's with whatever
+        // shared memory held for its query.
         uint32_t pk[kFirst / 2];
         float2 sum[2];
         sum[0] = sum[1] = make_float2(0.f, 0.f);
@@ -447,7 +449,7 @@ __device__ void softmax_role(const AttnParams& p, const TcArgs& a, Bars* b, int6
 #pragma unroll
           for (int u = 0; u < kFirst / 2; ++u) mx[u & 3] = fmaxf(mx[u & 3], fmaxf(s[2 * u], s[2 * u + 1]));
           const float x = sc * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          const bool move = x > m;
+          const bool move = far && x > m;
           const bool scale_o = move && m != -INFINITY;
           if (__any_sync(0xffffffffu, scale_o)) {
             const float f = scale_o ? exp2_fast(m - x) : 1.f;

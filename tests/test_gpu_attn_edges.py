@@ -142,3 +142,60 @@ def test_a_malformed_first_sequence_leaves_the_others_whole(cu, scale):
     b, e = cu[-2:]
     check(a.o[b:e], *reference(q[b:e], k[b:e], v[b:e], 0, scale, "bf16"))
     assert (a.o[:b] == 7).all()
+
+
+# ------------------------------------------------------------------ rows by themselves
+ROWS = [(3, 64, "bf16"), (5, 128, "bf16"), (12, 128, "bf16"), (20, 64, "bf16"), (33, 128, "bf16"), (90, 32, "bf16"),
+        (4, 128, "bf16"), (5, 256, "bf16"), (5, 128, "f32"), (20, 64, "f32"), (5, 256, "f32")]
+
+
+@pytest.mark.parametrize("G,D,dtype", ROWS)
+@pytest.mark.parametrize("paged", [False, True])
+def test_same_bits_whatever_ran_before(G, D, dtype, paged):
+    """Rows of a tile that no token fills hold what an earlier call left in shared memory: it changes nothing."""
+    g = gen(G)
+    ctx, new = [700, 90], [120, 31]
+    T = sum(new)
+    q = rand(g, T, G, D, dtype=dtype)
+    if paged:
+        p = Pool(ctx, new, 1, D, 32, dtype, 5)
+        a = kda.AttnPaged(q, p.k, p.v, p.table, p.lens, cu_of(new).cuda())
+    else:
+        k, v = rand(g, T, 1, D, dtype=dtype), rand(g, T, 1, D, dtype=dtype)
+        a = kda.AttnPrefill(q, k, v, cu_of(new).cuda())
+    big = rand(g, 3000, 128, D, dtype=dtype)
+    kb = rand(g, 3000, 1, D, dtype=dtype)
+    first = a.run().o.clone()
+    for fill in (3.0, 40.0, float("nan")):
+        kda.attn_prefill(big * fill, kb, kb, cu_of([3000]).cuda())
+        assert torch.equal(a.run().o, first)
+
+
+@pytest.mark.parametrize("G,D,dtype", ROWS)
+def test_a_query_changes_its_own_rows_only(G, D, dtype):
+    """The other tokens' rows keep their bits, whatever the query of one holds."""
+    g = gen(G + 1)
+    T, at = 700, 431
+    q, k, v = rand(g, T, 2 * G, D, dtype=dtype), rand(g, T, 2, D, dtype=dtype), rand(g, T, 2, D, dtype=dtype)
+    cu = cu_of([T]).cuda()
+    first = kda.attn_prefill(q, k, v, cu)
+    for x in (30.0, float("inf"), float("nan")):
+        other = q.clone()
+        other[at] *= x
+        o = kda.attn_prefill(other, k, v, cu)
+        assert torch.equal(o[:at], first[:at]) and torch.equal(o[at + 1:], first[at + 1:])
+
+
+@pytest.mark.parametrize("G,D,dtype", ROWS)
+def test_a_later_key_changes_no_earlier_row(G, D, dtype):
+    """Keys past a row's position, NaN among them, leave its bits as they were."""
+    g = gen(G + 2)
+    T, at = 700, 431
+    q, k, v = rand(g, T, 2 * G, D, dtype=dtype), rand(g, T, 2, D, dtype=dtype), rand(g, T, 2, D, dtype=dtype)
+    cu = cu_of([T]).cuda()
+    first = kda.attn_prefill(q, k, v, cu)
+    for x in (30.0, float("inf"), float("nan")):
+        other = k.clone()
+        other[at] *= x
+        o = kda.attn_prefill(q, other, v, cu)
+        assert torch.equal(o[:at], first[:at])
