@@ -240,6 +240,24 @@ __device__ __noinline__ void take_out(char* vs, uint32_t block, int key0, int n,
   }
 }
 
+// Channels c.. of one row's output with what was taken out of its block's V given
+// back (slow path); last: the last position that the row attends.
+template <typename T>
+__device__ __noinline__ float4 put_back(float4 x, const Poison& ps, const T* v, int64_t stride, const int32_t* pages,
+                                        int num_pages, int shift, int last, int c, int D) {
+  float y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int ch = c + u;
+    if (ch >= D) break;
+    auto bit = [&](int kind) { return (ps.bits[kind][ch >> 5] >> (ch & 31) & 1) != 0; };
+    const float z = poison_value(bit(0), bit(1), bit(2)) +
+                    poison_of(v + ch, stride, pages, num_pages, shift, ps.from, min(ps.to, last));
+    if (z != 0.f) y[u] += z;  // a NaN already there stays
+  }
+  return make_float4(y[0], y[1], y[2], y[3]);
+}
+
 // One quarter-tile's work and its running state, bf16
 template <int DP>
 struct RowsBf16 {
@@ -921,22 +939,9 @@ __global__ void __launch_bounds__(kThreads, Shape<T, DP, Work::kRows>::CTAS)
           }
           if (poisoned) {
             const int64_t stride = (int64_t)p.Hkv * p.D;
-            const T* v = static_cast<const T*>(p.v) + (int64_t)t.kvh * p.D + c + (p.block_table ? 0 : t.base * stride);
-            const int32_t* pages = p.block_table ? p.block_table + (int64_t)t.base * p.max_pages : nullptr;
-            const int to = min(ps->to, min(t.end - 1, t.pos0 + r / t.gb));
-#pragma unroll 1
-            for (int u = 0; u < 4 && c + u < p.D; ++u) {
-              const int ch = c + u;
-              auto bit = [&](int kind) { return (ps->bits[kind][ch >> 5] >> (ch & 31) & 1) != 0; };
-              const float z = poison_value(bit(0), bit(1), bit(2)) +
-                              poison_of(v + u, stride, pages, p.num_pages, p.page_shift, ps->from, to);
-              const float y = u == 0 ? x.x : u == 1 ? x.y : u == 2 ? x.z : x.w;
-              const float s = z != 0.f ? y + z : y;  // a NaN already there stays
-              if (u == 0) x.x = s;
-              else if (u == 1) x.y = s;
-              else if (u == 2) x.z = s;
-              else x.w = s;
-            }
+            x = put_back(x, *ps, static_cast<const T*>(p.v) + (int64_t)t.kvh * p.D + (p.block_table ? 0 : t.base * stride),
+                         stride, p.block_table ? p.block_table + (int64_t)t.base * p.max_pages : nullptr, p.num_pages,
+                         p.page_shift, min(t.end - 1, t.pos0 + r / t.gb), c, p.D);
           }
           if (t.slot >= 0) {
             *reinterpret_cast<float4*>(a.o + ((int64_t)t.slot * kMaxRows + r) * DP + c) = x;

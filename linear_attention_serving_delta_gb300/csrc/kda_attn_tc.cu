@@ -201,25 +201,18 @@ __device__ void load_v_role(const AttnParams& p, const TcArgs& a, const CUtensor
         // in 16-byte pieces of a block: the rows some row may not attend, the end of the sequence
         // (an item holds two tokens where its sequence does: one of a single token is the sequence's last)
         const int from = max(0, it.pos0 + 1 - x0) * 8, live = min(kTile, it.kv_len - x0) * 8;
+        uint32_t seen = 0;
 #pragma unroll
         for (int c = 0; c < S::NH; ++c) {
           uint4* blk = reinterpret_cast<uint4*>(dst + c * S::kBlock);
           if (it.ntok > 1) {
 #pragma unroll 8
-            for (int v = from + lane; v < live; v += 32) {
-              const uint4 x = blk[v];
-              // an exponent of all ones carries into the sign's place
-              const uint32_t t = (((x.x & 0x7f807f80u) + 0x00800080u) | ((x.y & 0x7f807f80u) + 0x00800080u) |
-                                  ((x.z & 0x7f807f80u) + 0x00800080u) | ((x.w & 0x7f807f80u) + 0x00800080u)) &
-                                 0x80008000u;
-              if (t) {
-                mark_channels(poison, c, v, x);
-                blk[v] = make_uint4(finite_only(x.x), finite_only(x.y), finite_only(x.z), finite_only(x.w));
-              }
-            }
+            for (int v = from + lane; v < live; v += 32) seen |= exponents_full(blk[v]);
           }
           for (int v = live + lane; v < kTile * 8; v += 32) blk[v] = make_uint4(0, 0, 0, 0);
         }
+        if (__any_sync(0xffffffffu, (seen & 0x80008000u) != 0))
+          take_out_bf16(dst, S::kBlock, S::NH, from, live, poison);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&b->v_full[ring.st]);

@@ -373,11 +373,29 @@ __device__ __forceinline__ uint32_t nonfinite8(uint4 x) {
   };
   return two(x.x) | two(x.y) << 2 | two(x.z) << 4 | two(x.w) << 6;
 }
-// the same piece v of a swizzled block (64 channels from `block` x 64 on) marked in a
-// bit for each channel
-__device__ __forceinline__ void mark_channels(uint32_t* words, int block, int v, uint4 x) {
-  const int piece = (v & 7) ^ ((v >> 3) & 7);
-  atomicOr_block(&words[2 * block + (piece >> 2)], nonfinite8(x) << (8 * (piece & 3)));
+// Non-finite bf16 values among the 16-byte pieces [from, live) of the `blocks`
+// swizzled blocks of a V tile (`bytes` apart, 64 channels each) become zeros, and
+// their channels' bits of `words` are set: the whole warp, where the search found some.
+static __device__ __noinline__ void take_out_bf16(char* tile, uint32_t bytes, int blocks, int from, int live,
+                                                  uint32_t* words) {
+  for (int c = 0; c < blocks; ++c) {
+    uint4* blk = reinterpret_cast<uint4*>(tile + c * bytes);
+#pragma unroll 1
+    for (int v = from + (threadIdx.x & 31); v < live; v += 32) {
+      const uint4 x = blk[v];
+      const uint32_t bad = nonfinite8(x);
+      if (!bad) continue;
+      const int piece = (v & 7) ^ ((v >> 3) & 7);
+      atomicOr_block(&words[2 * c + (piece >> 2)], bad << (8 * (piece & 3)));
+      blk[v] = make_uint4(finite_only(x.x), finite_only(x.y), finite_only(x.z), finite_only(x.w));
+    }
+  }
+}
+// the search: bits 15 and 31 tell whether one of eight bf16 has an exponent of all
+// ones (which carries into the sign's place)
+__device__ __forceinline__ uint32_t exponents_full(uint4 x) {
+  return ((x.x & 0x7f807f80u) + 0x00800080u) | ((x.y & 0x7f807f80u) + 0x00800080u) |
+         ((x.z & 0x7f807f80u) + 0x00800080u) | ((x.w & 0x7f807f80u) + 0x00800080u);
 }
 
 // byte offset of 16-byte piece c of row r in swizzled blocks of `block` bytes

@@ -73,7 +73,7 @@ struct Bars {
   // each; (fp32) three more rows of bits for the positions that all of its rows
   // attend, the channels with +inf, -inf and NaN there
   int32_t poison_from[8], poison_to[8];
-  uint32_t poison[8][16];
+  uint32_t poison_seen[8], poison[8][16];
 };
 static_assert(sizeof(Bars) <= 1024, "barrier block");
 
@@ -163,7 +163,7 @@ __device__ void load_v_bf16(const AttnParams& p, const TcArgs& a, const CUtensor
     const Geo g = geometry(it, p.G);
     if (g.n <= 0) continue;
     const int slot = busy++ & 7;
-    if (lane == 0) b->poison_to[slot] = -1;
+    if (lane == 0) b->poison_to[slot] = -1, b->poison_seen[slot] = 0;
     if (lane < 8) b->poison[slot][lane] = 0;  // (before the copies' __syncwarp)
     for (int j = 0; j < g.n; ++j) {
       const int kt = g.kt0 + j, x0 = kt * kKeys;
@@ -180,27 +180,20 @@ __device__ void load_v_bf16(const AttnParams& p, const TcArgs& a, const CUtensor
         // first that none may (a sequence's later tokens stand there too)
         const int from = max(0, it.pos0 + 1 - x0) * 8,
                   live = min(kKeys, min(it.kv_len, it.pos0 + it.ntok) - x0) * 8;
-        bool bad = false;
+        uint32_t seen = 0;
 #pragma unroll
         for (int c = 0; c < S::NB; ++c) {
           uint4* blk = reinterpret_cast<uint4*>(dst + c * S::kKBlock);
 #pragma unroll 4
-          for (int v = from + lane; v < live; v += 32) {
-            const uint4 x = blk[v];
-            const uint32_t t = (((x.x & 0x7f807f80u) + 0x00800080u) | ((x.y & 0x7f807f80u) + 0x00800080u) |
-                                ((x.z & 0x7f807f80u) + 0x00800080u) | ((x.w & 0x7f807f80u) + 0x00800080u)) &
-                               0x80008000u;
-            if (t) {
-              bad = true;
-              mark_channels(b->poison[slot], c, v, x);
-              blk[v] = make_uint4(finite_only(x.x), finite_only(x.y), finite_only(x.z), finite_only(x.w));
-            }
-          }
+          for (int v = from + lane; v < live; v += 32) seen |= exponents_full(blk[v]);
           for (int v = live + lane; v < kKeys * 8; v += 32) blk[v] = make_uint4(0, 0, 0, 0);
         }
-        if (__any_sync(0xffffffffu, bad) && lane == 0) {
+        const bool bad = __any_sync(0xffffffffu, (seen & 0x80008000u) != 0);
+        if (bad) take_out_bf16(dst, S::kKBlock, S::NB, from, live, b->poison[slot]);
+        if (bad && lane == 0) {
           if (b->poison_to[slot] < 0) b->poison_from[slot] = max(x0, it.pos0 + 1);
           b->poison_to[slot] = x0 + kKeys - 1;
+          b->poison_seen[slot] = 1;
         }
         fence_async_smem();
         __syncwarp();
@@ -264,6 +257,33 @@ __device__ void load_f32(const AttnParams& p, const TcArgs& a, const CUtensorMap
       mbar_wait(&b->h_full[k % S::kHalfStages], (k / S::kHalfStages) & 1, kWaitLimitNs);
 }
 
+// The non-finite values of half a tile of fp32 V, noted by the thread that took them
+// out (slow path): rows below `live` of the staged half from position x0 on; pos0: the
+// last position that all rows attend.
+template <int DP>
+static __device__ __noinline__ void note_poison(Bars* b, int slot, const char* in, int tid, int x0, int live, int pos0) {
+  using S = Shape<3, DP>;
+#pragma unroll 1
+  for (int z = tid; z < S::kHalfKeys * DP / 8; z += 128) {
+    const int r = z % S::kHalfKeys, x = x0 + r;
+    if (r >= live) continue;
+#pragma unroll 1
+    for (int u = 0; u < 8; ++u) {
+      const int ch = z / S::kHalfKeys * 8 + u;
+      const float y = *reinterpret_cast<const float*>(in + sw_off(r, ch >> 2, S::kHalfBlock) + (ch & 3) * 4);
+      if ((__float_as_uint(y) & 0x7f800000u) != 0x7f800000u) continue;
+      *reinterpret_cast<volatile uint32_t*>(&b->poison_seen[slot]) = 1;
+      if (x <= pos0) {
+        atomicOr_block(&b->poison[slot][4 + 4 * poison_kind(y) + (ch >> 5)], 1u << (ch & 31));
+      } else {
+        atomicOr_block(&b->poison[slot][ch >> 5], 1u << (ch & 31));
+        atomicMin_block(&b->poison_from[slot], x);
+        atomicMax_block(&b->poison_to[slot], x);
+      }
+    }
+  }
+}
+
 // The four splitting warps: Q's rows, then the tiles, from fp32 into three
 // bf16 operands.  V: zeros behind the sequence, non-finite values taken out.
 template <int DP>
@@ -287,6 +307,7 @@ __device__ void split_role(const AttnParams& p, const TcArgs& a, char* sm, Bars*
     if (tid == 0) {
       b->poison_from[(busy + 3) & 7] = INT32_MAX;
       b->poison_to[(busy + 3) & 7] = -1;
+      b->poison_seen[(busy + 3) & 7] = 0;
     }
     if (tid < 16) b->poison[(busy + 3) & 7][tid] = 0;
     ++busy;
@@ -320,12 +341,12 @@ __device__ void split_role(const AttnParams& p, const TcArgs& a, char* sm, Bars*
       uint64_t* full = v ? &b->v_full[vr.st] : &b->k_full[kr.st];
       if (!warp_wait<3, DP>(empty, (v ? vr.ph : kr.ph) ^ 1, &b->dead)) return false;
       char* out = sm + (v ? S::kV + vr.st * S::kOperand : S::kK + kr.st * S::kOperand);
-      int lo = INT32_MAX, hi = -1;
       for (int half = 0; half < 2; ++half) {
         const int x0 = (g.kt0 + j) * kKeys + half * S::kHalfKeys;
         if (!warp_wait<3, DP>(&b->h_full[ring.st], ring.ph, &b->dead)) return false;
         const char* in = sm + S::kStaging + ring.st * S::kHalf;
         const int live = it.kv_len - x0;
+        int seen = 0;
 #pragma unroll 2
         for (int z = tid; z < S::kHalfKeys * C8; z += 128) {
           // lanes along the rows: 16-byte pieces of eight swizzled rows meet no bank twice
@@ -340,15 +361,8 @@ __device__ void split_role(const AttnParams& p, const TcArgs& a, char* sm, Bars*
             for (int u = 0; u < 8; ++u) {
               if (r >= live) x[u] = 0.f;
               if ((__float_as_uint(x[u]) & 0x7f800000u) == 0x7f800000u) {
-                const int ch = 8 * c + u;
-                if (x0 + r <= it.pos0) {
-                  atomicOr_block(&b->poison[slot][4 + 4 * poison_kind(x[u]) + (ch >> 5)], 1u << (ch & 31));
-                } else {
-                  atomicOr_block(&b->poison[slot][ch >> 5], 1u << (ch & 31));
-                  lo = min(lo, x0 + r);
-                  hi = max(hi, x0 + r);
-                }
                 x[u] = 0.f;
+                seen = 1;
               }
             }
           }
@@ -360,14 +374,11 @@ __device__ void split_role(const AttnParams& p, const TcArgs& a, char* sm, Bars*
           *reinterpret_cast<uint4*>(dst + S::kPlane) = make_uint4(s[0].m, s[1].m, s[2].m, s[3].m);
           *reinterpret_cast<uint4*>(dst + 2 * S::kPlane) = make_uint4(s[0].l, s[1].l, s[2].l, s[3].l);
         }
+        if (seen) note_poison<DP>(b, slot, in, tid, x0, live, it.pos0);
         fence_async_smem();  // reads of the staging before its next copy, writes before the MMAs
         __syncwarp();
         if (lane == 0) mbar_arrive(&b->h_empty[ring.st]);
         ring.next();
-      }
-      if (hi >= 0) {
-        atomicMin_block(&b->poison_from[slot], lo);
-        atomicMax_block(&b->poison_to[slot], hi);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(full);
@@ -598,10 +609,7 @@ __device__ void softmax_role(const AttnParams& p, const TcArgs& a, Bars* b, int6
     // o = O / l, or the piece's O with its m and l
     if (n > 0 && !pv_wait(np - 1)) return;
     if (busy) {
-      const int from = *reinterpret_cast<volatile int32_t*>(&b->poison_from[slot]),
-                to = n > 0 ? min(*reinterpret_cast<volatile int32_t*>(&b->poison_to[slot]),
-                                 min(limit, min(it.kv_len, it.kt1 * kKeys) - 1))
-                           : -1;
+      const bool poison = n > 0 && *reinterpret_cast<volatile uint32_t*>(&b->poison_seen[slot]) != 0;
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const int gq = row - tok * p.G;
       const bool live = row < g.rows;
@@ -628,13 +636,16 @@ __device__ void softmax_role(const AttnParams& p, const TcArgs& a, Bars* b, int6
           const float f = it.slot < 0 ? inv : 1.f;
 #pragma unroll
           for (int u = 0; u < 32; ++u) x[u] *= f;
-          const volatile uint32_t* bits = b->poison[slot] + (c >> 5);
-          const uint32_t some = n > 0 ? bits[0] : 0;  // channels with such values that some rows attend
-          uint32_t all[3] = {0, 0, 0};                // and that all rows do
-          if (NP == 3 && n > 0)
+          if (poison) {
+            const volatile uint32_t* bits = b->poison[slot] + (c >> 5);
+            const uint32_t some = bits[0];  // channels with such values that some rows attend
+            uint32_t all[3] = {0, 0, 0};    // and that all rows do
+            if (NP == 3)
 #pragma unroll
-            for (int z = 0; z < 3; ++z) all[z] = bits[4 + 4 * z];
-          if (some | all[0] | all[1] | all[2]) {
+              for (int z = 0; z < 3; ++z) all[z] = bits[4 + 4 * z];
+            const int from = *reinterpret_cast<volatile int32_t*>(&b->poison_from[slot]),
+                      to = min(*reinterpret_cast<volatile int32_t*>(&b->poison_to[slot]),
+                               min(limit, min(it.kv_len, it.kt1 * kKeys) - 1));
             const int64_t stride = (int64_t)p.Hkv * p.D;
             const T* v = static_cast<const T*>(p.v) + (int64_t)h * p.D + c + (p.block_table ? 0 : it.base * stride);
             const int32_t* pages = p.block_table ? p.block_table + (int64_t)it.base * p.max_pages : nullptr;
@@ -706,12 +717,13 @@ __global__ void __launch_bounds__(Shape<NP, DP>::kThreads, 1)
     for (int s = 0; s < 8; ++s) {
       b->poison_from[s] = INT32_MAX;
       b->poison_to[s] = -1;
-      for (int z = 0; z < 16; ++z) b->poison[s][z] = 0;
+      b->poison_seen[s] = 0;
     }
     b->dead = 0;
     b->plan.own = 0;
     mbar_init_fence();
   }
+  if (threadIdx.x >= 64 && threadIdx.x < 64 + 8 * 16) (&b->poison[0][0])[threadIdx.x - 64] = 0;
   if (threadIdx.x == 32) {
     if (NP == 1) prefetch_map(&mq);
     prefetch_map(&mk);
