@@ -36,12 +36,7 @@ __device__ TileRef find_tile(const AttnParams& p, int64_t idx, int per, int64_t*
   for (int base = 0; base < p.num_seqs; base += kThreads) {
     const int s = base + tid;
     int64_t n = 0;
-    if (s < p.num_seqs) {
-      const int64_t b = p.cu_seqlens[s], e = p.cu_seqlens[s + 1];
-      // malformed sequences get one tile (it raises the flag), whatever they claim: the grid has room for no more
-      const bool ok = b >= 0 && e >= b && e <= p.total_tokens && (s > 0 || b == 0) && e - b <= p.max_seqlen;
-      n = ok ? (e - b + per - 1) / per : 1;
-    }
+    if (s < p.num_seqs) n = ((int64_t)attn_seq(p, s).len + per - 1) / per;
     int64_t x = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -92,12 +87,15 @@ __global__ void __launch_bounds__(kThreads) attn_simt(AttnParams p) {
   // (G > kRows: a tile is kRows of one token's G rows)
   const int parts = (G + kRows - 1) / kRows;
   const int part = blockIdx.x % parts;
+  if (blockIdx.x == 0 && blockIdx.y == 0)  // flags of malformed sequences, which have no tiles
+    for (int s = tid; s < p.num_seqs; s += kThreads) {
+      const int32_t flag = attn_seq(p, s).flag;
+      if (flag) attn_flag(p.status, flag);
+    }
   const TileRef ref = find_tile(p, blockIdx.x / parts, per, sh);
   if (ref.seq < 0) return;
   const AttnSeq sq = attn_seq(p, ref.seq);
-  if (sq.flag && tid == 0 && blockIdx.y == 0) attn_flag(p.status, sq.flag);
   const int64_t t0 = ref.tile * per;
-  if (t0 >= sq.len) return;
   const int ntok = (int)min((int64_t)per, sq.len - t0);
   const int nrows = min(kRows, ntok * G - part * kRows);  // rows of this tile
   const int kvh = blockIdx.y;

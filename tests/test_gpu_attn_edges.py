@@ -199,3 +199,18 @@ def test_a_later_key_changes_no_earlier_row(G, D, dtype):
         other[at] *= x
         o = kda.attn_prefill(q, other, v, cu)
         assert torch.equal(o[:at], first[:at])
+
+
+@pytest.mark.parametrize("scale", [-0.3, 0.125])
+@pytest.mark.parametrize("dtype,D", [("bf16", 64), ("bf16", 256), ("f32", 128)])
+@pytest.mark.parametrize("new", [1, 40])
+def test_malformed_requests_without_tokens_are_flagged(new, dtype, D, scale):
+    """A row outside the pool, or a length that the table cannot hold, of a request that brings no token."""
+    for row, length in ((9, 20), (0, 1 << 40)):
+        p = Pool([20, 30], [0, new], 2, D, 16, dtype, 2)
+        p.lens[0] = length
+        q = rand(gen(1), new, 4, D, dtype=dtype)
+        a = kda.AttnPaged(q, p.k, p.v, p.table, p.lens, cu_of([0, new]).cuda(), scale=scale, max_seqlen=new,
+                          rows=torch.tensor([row, 1], dtype=torch.int32, device="cuda")).run()
+        assert a.device_status() == 32
+        check(a.o, *reference(q, p.K[1], p.V[1], 30, scale, dtype))
