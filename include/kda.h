@@ -529,12 +529,14 @@ kda_status_t kda_prep(const kda_prep_args* args, void* stream);
 /*
  * Full attention beside the recurrence, and the paged cache it reads.
  *
- * "From KV Cache to Depth Attention", Technical Details: the stack
- * interleaves KDA layers with full-attention layers (3:1), which keep a
- * key and a value for every token.  These calls run such a layer's attention
- * with grouped heads: H query heads share H_kv key heads (H a multiple of
- * H_kv, query head h reads key head h / (H / H_kv)), all of head_dim
- * channels.  For query row i at position p_i of its sequence
+ * Hybrid stacks interleave linear layers with full-attention layers, which
+ * keep a key and a value for every token.  These calls run such a layer's
+ * attention with grouped heads: H query heads share H_kv key heads (H a
+ * multiple of H_kv, query head h reads key head h / (H / H_kv)), all of
+ * head_dim channels.  (The stack of "From KV Cache to Depth Attention",
+ * Technical Details, interleaves 3:1 with Gated MLA, whose cache is a latent
+ * and whose keys and values differ in width: that is another operator.)  For
+ * query row i at position p_i of its sequence
  *
  *   o_i = sum_{j <= p_i} w_ij v_j,   w_ij = softmax over j <= p_i of scale q_i . k_j
  *
@@ -542,8 +544,10 @@ kda_status_t kda_prep(const kda_prep_args* args, void* stream);
  * position a row may not attend never reaches that row through its weight,
  * which is exactly 0 there; whatever the cache or the packed tensors hold
  * behind a sequence's end (infinities and NaN among it) changes nothing.  An
- * infinite value makes its channel infinite in the rows that attend it; an
- * infinite or NaN key, or query, may make NaN of the rows that meet it.
+ * infinite value makes its channel infinite in the rows that attend it, or
+ * NaN where the weight it meets is below the least of the kernels' numbers
+ * (2^-126 of the row's largest); an infinite or NaN key, or query, may make
+ * NaN of the rows that meet it, and changes no other row.
  * Softmax statistics and sums are fp32; with bf16 inputs the weights are
  * rounded to bf16 before they multiply v (the tensor cores' operand type),
  * an error of at most 2^-8 of each weight, as o's own rounding to bf16.
@@ -575,7 +579,10 @@ kda_status_t kda_prep(const kda_prep_args* args, void* stream);
 /*
  * Causal attention over packed whole prompts: sequence s holds tokens
  * [cu_seqlens[s], cu_seqlens[s+1]), p_i is the token's index in it.  A
- * malformed sequence (flag 1) is skipped; rows of o behind the last sequence
+ * malformed sequence (flag 1) is skipped: each is judged by its own two
+ * offsets, so that where malformed ones between them make two sequences
+ * overlap, the rows they share hold the output of either, and the last
+ * sequences' rows may stay as they were.  Rows of o behind the last sequence
  * are left as they were.
  */
 typedef struct {
@@ -615,7 +622,9 @@ typedef struct {
   int32_t num_heads, num_kv_heads, head_dim; /* as above                          */
   int64_t total_tokens;        /* T, host-known upper bound of cu_seqlens[N]      */
   const int64_t* cu_seqlens;   /* device [N+1] over the new tokens                */
-  int32_t max_seqlen;          /* host-known upper bound of every L_s; 0 = T      */
+  int32_t max_seqlen;          /* host-known upper bound of every L_s; 0 = T.
+                                  Sets the path: a decode step without it takes
+                                  the row tiles of long chunks                    */
   kda_dtype_t in_dtype;        /* dtype of q, the caches and o                    */
   const void* q;               /* device [T, H, head_dim]                         */
   const void* k_cache;         /* device [num_pages, page_size, H_kv, head_dim]   */
@@ -679,8 +688,8 @@ kda_status_t kda_kv_plan(const kda_kv_plan_args* args, void* ws, size_t ws_bytes
  * in order, its ceil(kv_lens[r] / page_size) pages are appended to free_pages
  * from *free_count on, which advances, and kv_lens[r] becomes 0.  A row named
  * twice is released once; a row outside the pool or with a malformed length,
- * and rows whose pages would pass num_pages, are left alone (flag 32);
- * negative rows are skipped.
+ * and a row whose pages would pass num_pages, are left alone (flag 32), and
+ * the rows behind them go on; negative rows are skipped.
  */
 typedef struct {
   int32_t num_release;         /* M >= 0 entries of rows                          */

@@ -103,7 +103,8 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnParam
     piece = (int)max((int64_t)kMinPiece, share);
   }
   // pieces of an item: how many, and each one's key tiles
-  // (to the nearest: the pieces of like items then fill whole rounds of the SMs)
+  // (to the nearest; the CTAs need not come out even: 64 like items of 258 key
+  // tiles give 320 pieces, three for some of 152 CTAs and two for the others)
   auto pieces = [&](const AttnItem& it) { return split ? max(1, (int)(((int64_t)it.kt1 * 2 + piece) / (2 * (int64_t)piece))) : 1; };
   for (int64_t x = tid; x < n_tiles; x += kPlanThreads) {
     const AttnItem it = tile_item(x);

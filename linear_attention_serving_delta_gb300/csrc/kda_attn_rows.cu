@@ -1,12 +1,12 @@
 // kda_attn_rows.cu -- attention by blocks of at most 16 rows (32 in fp32): single tokens (or
-// a few) over the paged cache in both types, and everything in fp32 or with
-// heads of 256 channels.
+// a few) over the paged cache in both types, all of fp32 with heads of 256
+// channels, and calls of at most 32 rows a key head in fp32 or with 256 channels.
 //
 // A block's rows are those of one key head: row = token * gb + head, with gb
 // = min(G, 16 or 32) of its G query heads and as many tokens (a power of two) as fit
 // a block.  For single tokens that reads every cached key and value once and
-// does little with them, so the kernel is a stream, bound by HBM; fp32 blocks
-// of a prompt are bound by the splitting of their operands instead.
+// does little with them, so the kernel is a stream: bf16 is bound by HBM, fp32
+// by the splitting of its operands and six products for each.
 //
 // The key tiles of all blocks form one line of work, sequence after sequence,
 // head after head, and every CTA of a grid that fills the GPU takes an equal
@@ -24,8 +24,10 @@
 // operand in three bf16 parts.
 //
 // Measured on GB300, 32 query heads over 8 of 128 channels, bf16: one token each
-// of 256 requests over 64..8191 keys 634 us (6.7 TB/s, the measured copy
-// rate), one token over 131,072 keys 90 us (5.9 TB/s).
+// of 256 requests over 64..8191 keys 630..646 us (6.6..6.7 TB/s, the measured copy
+// rate), one token over 131,072 keys 92 us (5.8 TB/s).  fp32, 64 requests over
+// 64..8191 keys: 0.75 ms with 128 channels (2.6 TB/s), 1.79 ms with 256 (2.2 TB/s);
+// one prompt of 4096 tokens with 256 channels 17.1 ms (16 TFLOP/s).
 #include <algorithm>
 
 #include "kda_attn_tc.cuh"
@@ -1083,10 +1085,11 @@ cudaError_t launch_f32(const AttnParams& p, char* w, cudaStream_t stream) {
 
 }  // namespace
 
-// Single tokens, or as few as 16 rows hold, over the cache (more rows of bf16
-// go to the tensor cores' 128-row tiles); all of fp32 and of 256 channels.  A
-// positive finite scale (the running maximum is taken before the scaling),
-// 16-byte aligned bases for the tensor maps.
+// Single tokens, or as few as 16 rows hold, over the cache (more rows go to the
+// tensor cores' 128-row tiles first, where they have a form for the type and head
+// size); all of fp32 and of 256 channels that none of them takes.  A positive
+// finite scale (the running maximum is taken before the scaling), 16-byte aligned
+// bases for the tensor maps.
 bool attn_rows_fits(const AttnParams& p) {
   auto al16 = [](const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15) == 0; };
   return (few_rows(p) || p.dt == KDA_F32 || p.D == 256) && p.scale > 0.f && p.scale <= 3.4e38f && al16(p.q) && al16(p.k) &&

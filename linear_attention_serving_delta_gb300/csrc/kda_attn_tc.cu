@@ -36,9 +36,9 @@
 // into the rows that do attend them (a slow path no finite input takes).
 //
 // Bound by the tensor core and by the softmax between S and P V.  Measured on
-// GB300: one prompt of 8192 tokens, 32 query heads over 8 of 128 channels, 339 us
-// (1.62 PFLOP/s, the tensor pipe 71% busy); 182k tokens of 8 prompts 24.9 ms
-// (1.42 PFLOP/s under the power cap).
+// GB300: one prompt of 8192 tokens, 32 query heads over 8 of 128 channels, 355 us
+// call after call (1.55 PFLOP/s), 324 us with pauses (1.70, the tensor pipe 73%
+// busy); 182k tokens of 8 prompts 24.5 ms (1.44 PFLOP/s under the power cap).
 #include "kda_attn_tc.cuh"
 
 namespace kda {

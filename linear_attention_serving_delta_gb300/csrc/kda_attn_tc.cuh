@@ -17,9 +17,6 @@
 
 namespace kda {
 
-// The SMs the cut into pieces is sized for, the pieces an SM gets (a chunk of 512
-// tokens over 32k keys beside eight requests: one 328 us, two 277, three 297,
-// four 300), and the fewest key tiles a piece has
 // Over the cache, requests of up to kTinyRows rows a key head take the streaming
 // kernel's blocks, and so do a few blocks of rows over short tables: a 128-row
 // tile's chain of steps would take longer (163 requests of 1..40 tokens over
@@ -31,6 +28,9 @@ constexpr int kTinyRows = 16, kShortRows = 64, kShortKeys = 512;
 // the row tiles)
 constexpr int kFewRows = 32;
 constexpr int kRowTile = 128;  // rows of a row tile
+// The SMs the cut into pieces is sized for, the pieces an SM gets (a chunk of 512
+// tokens over 32k keys beside eight requests: one 328 us, two 277, three 297,
+// four 300), and the fewest key tiles a piece has
 constexpr int kSplitSms = 152;
 constexpr int kPiecesPerSm = 2;
 constexpr int kMinPiece = 4;

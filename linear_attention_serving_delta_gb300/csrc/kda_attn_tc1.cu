@@ -11,13 +11,16 @@
 // fp32: x = h + m + l with bf16 parts (split3), and a product of two operands
 // takes the six pairs h h, h m, m h, h l, l h, m m, what is left out being below
 // 2^-22 of it.  A warpgroup splits K and V tiles from a staging ring into the
-// operands' layout (the tensor core takes six times a bf16 tile's time for them,
-// so it hides the splitting), the softmax threads split P.  Bound by the
-// tensor core at six bf16 products a product.
+// operands' layout beside the products, the softmax threads split P.
+//
+// Bound by a chain, not by a unit.  bf16: one warpgroup's TMEM loads, maximum,
+// exponentials and TMEM stores of a key tile.  fp32: P V of a tile, its addition
+// to the sum, P of the next tile and its P V, one after the other (one P, one V
+// and one buffer of what P V gives fit).
 //
 // Measured on GB300, one prompt of 4096 tokens, 32 query heads over 8: bf16 of
-// 256 channels 255 us (1.08 PFLOP/s), fp32 of 128 channels 1.05 ms (131 TFLOP/s,
-// 0.79 PFLOP/s of bf16 products).
+// 256 channels 229 us (1.20 PFLOP/s, the tensor pipe 51% busy), fp32 of 128
+// channels 1.02 ms (134 TFLOP/s, 0.81 PFLOP/s of bf16 products, the tensor pipe 34%).
 #include "kda_attn_tc.cuh"
 
 namespace kda {

@@ -955,8 +955,9 @@ class AttnPaged(_CacheCall):
     the paged cache [num_pages, page_size, H_kv, D] that holds them already.
     block_table [rows, max_pages] int32, kv_lens [rows] int64 (new tokens
     included), rows [N] int32 names each request's row (None: request s is row
-    s).  max_seqlen: a bound on one request's new tokens (0: T); 1 for a decode
-    step."""
+    s).  max_seqlen: a bound on one request's new tokens (0: T), 1 for a decode
+    step; it picks the kernel, and a decode step without it takes that of long
+    chunks, tiles of 256 rows of which a request fills a token's."""
     _name = "kda_attn_paged"
 
     def __init__(self, q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, *, rows=None,
