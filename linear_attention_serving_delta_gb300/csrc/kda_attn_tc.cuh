@@ -376,8 +376,8 @@ __device__ __forceinline__ uint32_t nonfinite8(uint4 x) {
 // Non-finite bf16 values among the 16-byte pieces [from, live) of the `blocks`
 // swizzled blocks of a V tile (`bytes` apart, 64 channels each) become zeros, and
 // their channels' bits of `words` are set: the whole warp, where the search found some.
-static __device__ __noinline__ void take_out_bf16(char* tile, uint32_t bytes, int blocks, int from, int live,
-                                                  uint32_t* words) {
+__device__ __forceinline__ void take_out_bf16(char* tile, uint32_t bytes, int blocks, int from, int live,
+                                              uint32_t* words) {
   for (int c = 0; c < blocks; ++c) {
     uint4* blk = reinterpret_cast<uint4*>(tile + c * bytes);
 #pragma unroll 1

@@ -150,6 +150,12 @@ __device__ void load_k_bf16(const AttnParams& p, const TcArgs& a, const CUtensor
   }
 }
 
+// (out of line: 4096 tokens of 256 channels 229 us, 236 with it in the loop)
+static __device__ __noinline__ void take_out_of(char* tile, uint32_t bytes, int blocks, int from, int live,
+                                                uint32_t* words) {
+  take_out_bf16(tile, bytes, blocks, from, live, words);
+}
+
 template <int DP>
 __device__ void load_v_bf16(const AttnParams& p, const TcArgs& a, const CUtensorMap* mv, char* sm, Bars* b,
                             int64_t total) {
@@ -192,7 +198,7 @@ __device__ void load_v_bf16(const AttnParams& p, const TcArgs& a, const CUtensor
           for (int v = live + lane; v < kKeys * 8; v += 32) blk[v] = make_uint4(0, 0, 0, 0);
         }
         const bool bad = __any_sync(0xffffffffu, (seen & 0x80008000u) != 0);
-        if (bad) take_out_bf16(dst, S::kKBlock, S::NB, from, live, b->poison[slot]);
+        if (bad) take_out_of(dst, S::kKBlock, S::NB, from, live, b->poison[slot]);
         if (bad && lane == 0) {
           if (b->poison_to[slot] < 0) b->poison_from[slot] = max(x0, it.pos0 + 1);
           b->poison_to[slot] = x0 + kKeys - 1;
