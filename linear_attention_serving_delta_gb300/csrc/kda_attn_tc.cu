@@ -37,7 +37,7 @@
 //
 // Bound by the tensor core and by the softmax between S and P V.  Measured on
 // GB300: one prompt of 8192 tokens, 32 query heads over 8 of 128 channels, 355 us
-// call after call (1.55 PFLOP/s), 324 us with pauses (1.70, the tensor pipe 73%
+// call after call (1.55 PFLOP/s), 328 us with pauses (1.68, the tensor pipe 74%
 // busy); 182k tokens of 8 prompts 24.5 ms (1.44 PFLOP/s under the power cap).
 #include "kda_attn_tc.cuh"
 
