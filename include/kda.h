@@ -729,6 +729,178 @@ typedef struct {
 
 kda_status_t kda_kv_write(const kda_kv_write_args* args, void* stream);
 
+/*
+ * Linear attention with a decay for each head, and the states it keeps.
+ *
+ * The recurrence without the delta rule, for stacks whose linear layers write
+ * every key and value as they are: per head, with a state S in R^{dk x dv},
+ *
+ *     log alpha_t = -slope_h softplus(g_t)       (one value per token and head)
+ *     S_t = alpha_t S_{t-1} + k_t v_t^T
+ *     o_t = scale S_t^T q_t
+ *
+ * g [T, H] holds a logit per token and head, slope [H] a rate per head.  Without
+ * slope the rate is 1 (the gate of gate_per_head); without g, softplus(g) is
+ * 1 and alpha = exp(-slope) constant; one of them at least is given.  q and k
+ * are taken as they are, without normalisation.  H heads of v, o and the
+ * states share H_k heads of q and k (H a multiple of H_k, head h reads key
+ * head h / (H / H_k)).  dk and dv are each in {16, 32, 64, 128, 256}.
+ *
+ * alpha is meant to be in [0, 1], slope >= 0.  An alpha below 2^-1024 counts as 0:
+ * what was before such a token is forgotten, and a state that is not finite
+ * becomes NaN there.  Where k, v, a gate or a state is not finite, what it
+ * enters from its token on may be NaN or infinite, in that head alone: an
+ * earlier token's o never changes, nor another channel's where only v's
+ * channel or a column of the state is not finite.
+ *
+ * States are fp32, [num_states, H, dk, dv]; a call reads one pool and writes
+ * another (the same buffer: in place).  state_slots [N] names each
+ * sequence's row in both (NULL: sequence s is row s); a negative slot
+ * skips the sequence, and what it would write stays as it was.  Two sequences
+ * of a call must not share a slot.  States are advanced with products and
+ * sums to fp32 precision for both input types.  o is rounded once; with bf16
+ * inputs the products q.k with their decays, and in prefill and draft the
+ * state that o is read from, are rounded to bf16 before they multiply (the
+ * tensor cores' operand type), each an error of at most 2^-8 of the term.
+ *
+ * One step of a host that drafts tokens:
+ *   kda_lin_draft   o of the drafted tokens, states as they were
+ *   kda_lin_commit  states advanced along the accepted tokens
+ *
+ * `status` of these calls: device int32 or NULL, into which the kernels OR
+ * flags (never cleared by the library): 1 (malformed cu_seqlens), 8 (bounded
+ * wait expired), 32 (a malformed slot, parent or accepted token), 128 (a
+ * request longer than max_seqlen).  Such a sequence is skipped.  Malformed
+ * cu_seqlens are judged as in kda_attn_prefill.
+ */
+
+/*
+ * Packed whole prompts or pieces of them: sequence s holds tokens
+ * [cu_seqlens[s], cu_seqlens[s+1]) and goes on from initial_state (zeros
+ * without one).  A sequence without tokens leaves its initial state as the
+ * final one.  Rows of o behind the last sequence are left as they were.
+ */
+typedef struct {
+  int32_t num_seqs;            /* N >= 1                                          */
+  int32_t num_heads;           /* H heads of v, o and the states                  */
+  int32_t num_key_heads;       /* H_k heads of q and k, divides H                 */
+  int32_t dk, dv;              /* each in {16, 32, 64, 128, 256}                  */
+  int64_t total_tokens;        /* T, host-known upper bound of cu_seqlens[N]      */
+  const int64_t* cu_seqlens;   /* device [N+1], cu[0] = 0, non-decreasing         */
+  kda_dtype_t in_dtype;        /* dtype of q, k, v, g and o                       */
+  const void* q;               /* device [T, H_k, dk]                             */
+  const void* k;               /* device [T, H_k, dk]                             */
+  const void* v;               /* device [T, H, dv]                               */
+  const void* g;               /* device [T, H] or NULL                           */
+  const float* slope;          /* device [H] or NULL (not both NULL)              */
+  float scale;
+  const float* initial_state;  /* device [num_states, H, dk, dv] or NULL (zeros)  */
+  float* final_state;          /* the same shape, or NULL; may be initial_state   */
+  int32_t num_states;          /* rows of either (0 if both are NULL)             */
+  const int32_t* state_slots;  /* device [N] or NULL                              */
+  void* o;                     /* device [T, H, dv]                               */
+  int32_t* status;             /* device int32 or NULL                            */
+} kda_lin_prefill_args;
+
+/* Device workspace bytes (host-side fields only); 0 if the arguments are
+ * invalid.  256-byte aligned; contents need not be initialised; not to be used
+ * by two calls in flight. */
+size_t kda_lin_prefill_workspace_size(const kda_lin_prefill_args* args);
+kda_status_t kda_lin_prefill(const kda_lin_prefill_args* args, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * One token for each of `batch` rows: the row's state is read, advanced by
+ * its token and written, and o follows from the new state.
+ */
+typedef struct {
+  int32_t batch;               /* B >= 0                                          */
+  int32_t num_heads, num_key_heads, dk, dv; /* as above                           */
+  kda_dtype_t in_dtype;
+  const void* q;               /* device [B, H_k, dk]                             */
+  const void* k;               /* device [B, H_k, dk]                             */
+  const void* v;               /* device [B, H, dv]                               */
+  const void* g;               /* device [B, H] or NULL                           */
+  const float* slope;          /* device [H] or NULL                              */
+  float scale;
+  const float* state;          /* device [num_states, H, dk, dv]                  */
+  float* state_out;            /* the same shape; may be state                    */
+  int32_t num_states;
+  const int32_t* state_slots;  /* device [B] or NULL                              */
+  void* o;                     /* device [B, H, dv]                               */
+  int32_t* status;
+} kda_lin_decode_args;
+
+kda_status_t kda_lin_decode(const kda_lin_decode_args* args, void* stream);
+
+/*
+ * Drafted tokens over the states, which stay as they are.  Request s holds
+ * tokens [cu_seqlens[s], cu_seqlens[s+1]), at most KDA_LIN_MAX_DRAFT; parents
+ * [T] gives for each the index within the request of the token it follows,
+ * smaller than its own, or -1 where it follows the state (NULL: each follows
+ * the one before it).  With the path of token i from the state to i and
+ * G_i the sum of log alpha along it,
+ *
+ *   o_i = scale (e^{G_i} S^T q_i + sum_{j on the path of i} e^{G_i - G_j} (q_i . k_j) v_j)
+ *
+ * which is what kda_lin_decode would give along each path by itself.
+ */
+#define KDA_LIN_MAX_DRAFT 64
+typedef struct {
+  int32_t num_seqs;            /* N >= 1                                          */
+  int32_t num_heads, num_key_heads, dk, dv; /* as above                           */
+  int64_t total_tokens;        /* T, host-known upper bound of cu_seqlens[N]      */
+  const int64_t* cu_seqlens;   /* device [N+1]                                    */
+  int32_t max_seqlen;          /* host-known upper bound of a request's tokens, at
+                                  most KDA_LIN_MAX_DRAFT; 0 = KDA_LIN_MAX_DRAFT.
+                                  Smaller ones take smaller tiles                 */
+  kda_dtype_t in_dtype;
+  const void* q;               /* device [T, H_k, dk]                             */
+  const void* k;               /* device [T, H_k, dk]                             */
+  const void* v;               /* device [T, H, dv]                               */
+  const void* g;               /* device [T, H] or NULL                           */
+  const float* slope;          /* device [H] or NULL                              */
+  const int32_t* parents;      /* device [T] or NULL                              */
+  float scale;
+  const float* state;          /* device [num_states, H, dk, dv]                  */
+  int32_t num_states;
+  const int32_t* state_slots;  /* device [N] or NULL                              */
+  void* o;                     /* device [T, H, dv]                               */
+  int32_t* status;
+} kda_lin_draft_args;
+
+kda_status_t kda_lin_draft(const kda_lin_draft_args* args, void* stream);
+
+/*
+ * The states after the accepted tokens of kda_lin_draft: last [N] is the index
+ * within request s of the last accepted token, whose path is what the state
+ * advances by (-1: none, the state stays):
+ *
+ *   S' = e^{G_a} S + sum_{j on the path of a} e^{G_a - G_j} k_j v_j^T,  a = last[s]
+ *
+ * k, v, g, slope, parents and cu_seqlens are those of the draft.
+ */
+typedef struct {
+  int32_t num_seqs;
+  int32_t num_heads, num_key_heads, dk, dv;
+  int64_t total_tokens;
+  const int64_t* cu_seqlens;   /* device [N+1]                                    */
+  int32_t max_seqlen;          /* as in kda_lin_draft_args                        */
+  kda_dtype_t in_dtype;
+  const void* k;               /* device [T, H_k, dk]                             */
+  const void* v;               /* device [T, H, dv]                               */
+  const void* g;               /* device [T, H] or NULL                           */
+  const float* slope;          /* device [H] or NULL                              */
+  const int32_t* parents;      /* device [T] or NULL                              */
+  const int32_t* last;         /* device [N]                                      */
+  const float* state;          /* device [num_states, H, dk, dv]                  */
+  float* state_out;            /* the same shape; may be state                    */
+  int32_t num_states;
+  const int32_t* state_slots;  /* device [N] or NULL                              */
+  int32_t* status;
+} kda_lin_commit_args;
+
+kda_status_t kda_lin_commit(const kda_lin_commit_args* args, void* stream);
+
 /* Static description of a status code. */
 const char* kda_status_string(kda_status_t status);
 

@@ -9,7 +9,9 @@ The names follow the C ABI: ``kda_prefill``, ``kda_prefill_workspace_size``,
 ``kda_prefill_device_status``, ``kda_snapshot_plan``, ``kda_decode_step``,
 ``kda_prep``, ``kda_status_string``, ``kda_prefill_host`` (host buffers), and
 for the full-attention layers ``kda_attn_prefill``, ``kda_attn_paged``,
-``kda_kv_plan``, ``kda_kv_write``, ``kda_kv_release``.
+``kda_kv_plan``, ``kda_kv_write``, ``kda_kv_release``; for linear attention
+with a decay for each head ``kda_lin_prefill``, ``kda_lin_decode``,
+``kda_lin_draft``, ``kda_lin_commit``.
 ``prefill`` and ``prefill_host`` are conveniences that allocate outputs and
 workspace with torch and call ``kda_prefill`` / ``kda_prefill_host``.
 """
@@ -44,7 +46,10 @@ EXPORTED = ("kda_prefill_workspace_size", "kda_prefill", "kda_prefill_noalloc",
             "kda_status_string", "kda_version", "kda_prefill_schedule",
             "kda_attn_prefill_workspace_size", "kda_attn_prefill", "kda_attn_paged_workspace_size",
             "kda_attn_paged", "kda_kv_plan_workspace_size", "kda_kv_plan",
-            "kda_kv_release_workspace_size", "kda_kv_release", "kda_kv_write")
+            "kda_kv_release_workspace_size", "kda_kv_release", "kda_kv_write",
+            "kda_lin_prefill_workspace_size", "kda_lin_prefill", "kda_lin_decode", "kda_lin_draft",
+            "kda_lin_commit")
+LIN_MAX_DRAFT = 64  # KDA_LIN_MAX_DRAFT: drafted tokens of a request
 NOALLOC_SCRATCH_BYTES = 64 << 20  # fixed workspace behind kda_prefill_noalloc
 
 
@@ -142,6 +147,40 @@ class KvWriteArgs(ctypes.Structure):
                 ("num_slots", c_i64), ("k_cache", c_vp), ("v_cache", c_vp), ("status", c_vp)]
 
 
+class LinPrefillArgs(ctypes.Structure):
+    _fields_ = [("num_seqs", c_i32), ("num_heads", c_i32), ("num_key_heads", c_i32), ("dk", c_i32),
+                ("dv", c_i32), ("total_tokens", c_i64), ("cu_seqlens", c_vp),
+                ("in_dtype", ctypes.c_int), ("q", c_vp), ("k", c_vp), ("v", c_vp), ("g", c_vp),
+                ("slope", c_vp), ("scale", c_f32), ("initial_state", c_vp), ("final_state", c_vp),
+                ("num_states", c_i32), ("state_slots", c_vp), ("o", c_vp), ("status", c_vp)]
+
+
+class LinDecodeArgs(ctypes.Structure):
+    _fields_ = [("batch", c_i32), ("num_heads", c_i32), ("num_key_heads", c_i32), ("dk", c_i32),
+                ("dv", c_i32), ("in_dtype", ctypes.c_int), ("q", c_vp), ("k", c_vp), ("v", c_vp),
+                ("g", c_vp), ("slope", c_vp), ("scale", c_f32), ("state", c_vp),
+                ("state_out", c_vp), ("num_states", c_i32), ("state_slots", c_vp), ("o", c_vp),
+                ("status", c_vp)]
+
+
+class LinDraftArgs(ctypes.Structure):
+    _fields_ = [("num_seqs", c_i32), ("num_heads", c_i32), ("num_key_heads", c_i32), ("dk", c_i32),
+                ("dv", c_i32), ("total_tokens", c_i64), ("cu_seqlens", c_vp),
+                ("max_seqlen", c_i32), ("in_dtype", ctypes.c_int), ("q", c_vp), ("k", c_vp),
+                ("v", c_vp), ("g", c_vp), ("slope", c_vp), ("parents", c_vp), ("scale", c_f32),
+                ("state", c_vp), ("num_states", c_i32), ("state_slots", c_vp), ("o", c_vp),
+                ("status", c_vp)]
+
+
+class LinCommitArgs(ctypes.Structure):
+    _fields_ = [("num_seqs", c_i32), ("num_heads", c_i32), ("num_key_heads", c_i32), ("dk", c_i32),
+                ("dv", c_i32), ("total_tokens", c_i64), ("cu_seqlens", c_vp),
+                ("max_seqlen", c_i32), ("in_dtype", ctypes.c_int), ("k", c_vp), ("v", c_vp),
+                ("g", c_vp), ("slope", c_vp), ("parents", c_vp), ("last", c_vp), ("state", c_vp),
+                ("state_out", c_vp), ("num_states", c_i32), ("state_slots", c_vp),
+                ("status", c_vp)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -192,13 +231,16 @@ def lib() -> ctypes.CDLL:
             L.kda_prep.argtypes = [ctypes.POINTER(PrepArgs), c_vp]
             L.kda_prep.restype = ctypes.c_int
             for name, args in (("kda_attn_prefill", AttnPrefillArgs), ("kda_attn_paged", AttnPagedArgs),
-                               ("kda_kv_plan", KvPlanArgs), ("kda_kv_release", KvReleaseArgs)):
+                               ("kda_kv_plan", KvPlanArgs), ("kda_kv_release", KvReleaseArgs),
+                               ("kda_lin_prefill", LinPrefillArgs)):
                 size, call = getattr(L, name + "_workspace_size"), getattr(L, name)
                 size.argtypes, size.restype = [ctypes.POINTER(args)], ctypes.c_size_t
                 call.argtypes = [ctypes.POINTER(args), c_vp, ctypes.c_size_t, c_vp]
                 call.restype = ctypes.c_int
-            L.kda_kv_write.argtypes = [ctypes.POINTER(KvWriteArgs), c_vp]
-            L.kda_kv_write.restype = ctypes.c_int
+            for name, args in (("kda_kv_write", KvWriteArgs), ("kda_lin_decode", LinDecodeArgs),
+                               ("kda_lin_draft", LinDraftArgs), ("kda_lin_commit", LinCommitArgs)):
+                call = getattr(L, name)
+                call.argtypes, call.restype = [ctypes.POINTER(args), c_vp], ctypes.c_int
             L.kda_status_string.argtypes = [ctypes.c_int]
             L.kda_status_string.restype = ctypes.c_char_p
             L.kda_version.restype = ctypes.c_char_p
@@ -869,6 +911,7 @@ class _CacheCall:
     kernels.  Another stream waits for that one before its first run, and two
     runs of one planned call do not overlap (they share its workspace)."""
     _name = ""
+    _sized = True  # the C call takes a workspace
 
     def _plan(self, device, args, keep, status):
         self._device, self.args, self._keep = device, args, keep
@@ -878,7 +921,7 @@ class _CacheCall:
         _same_device(status=self.status, other=keep[0])
         args.status = _ptr(self.status, torch.int32, "status")
         self._fn, self.workspace = getattr(lib(), self._name), None
-        size = getattr(lib(), self._name + "_workspace_size", None) if self._name != "kda_kv_write" else None
+        size = getattr(lib(), self._name + "_workspace_size") if self._sized else None
         if size is not None:
             nbytes = int(size(ctypes.byref(args)))
             if nbytes == 0:
@@ -1072,7 +1115,7 @@ class KvRelease(_CacheCall):
 class KvWrite(_CacheCall):
     """Planned ``kda_kv_write``: k, v [T, H_kv, D] into the slots slot_map [T]
     of the caches [num_pages, page_size, H_kv, D]."""
-    _name = "kda_kv_write"
+    _name, _sized = "kda_kv_write", False
 
     def __init__(self, k, v, slot_map, k_cache, v_cache, *, status=None):
         if k.dim() != 3 or k_cache.dim() != 4:
@@ -1130,3 +1173,177 @@ def kv_release(rows, block_table, kv_lens, free_pages, free_count, *, stream=Non
 def kv_write(k, v, slot_map, k_cache, v_cache, *, stream=None, **kw):
     """Runs kda_kv_write (see KvWrite)."""
     _run_on(lambda: KvWrite(k, v, slot_map, k_cache, v_cache, **kw), stream)
+
+
+# ----------------------------------------------------------------- linear attention, a decay for each head
+def _lin_heads(a, q, k, v, g, slope):
+    """Heads, widths, type and gates of a kda_lin_* argument block (q None for kda_lin_commit).
+    Returns the tokens."""
+    if k.dim() != 3 or v.dim() != 3:
+        raise ValueError(f"k must be [T, H_k, dk] and v [T, H, dv], got {tuple(k.shape)} and {tuple(v.shape)}")
+    (T, H, dv), (Hk, dk), dt = v.shape, k.shape[1:], v.dtype
+    if Hk < 1 or H < 1 or H % Hk:
+        raise ValueError(f"{H} heads are no multiple of {Hk} key heads (v, k)")
+    _shape("k", k, (T, Hk, dk))
+    if q is not None:
+        _shape("q", q, (T, Hk, dk))
+        a.q = _ptr(q, dt, "q")
+    if g is None and slope is None:
+        raise ValueError("g or slope must be given")
+    if g is not None:
+        _shape("g", g, (T, H))
+    if slope is not None:
+        _shape("slope", slope, (H,))
+    a.num_heads, a.num_key_heads, a.dk, a.dv, a.in_dtype = H, Hk, dk, dv, _dtype_code(dt)
+    a.k, a.v, a.g, a.slope = _ptr(k, dt, "k"), _ptr(v, dt, "v"), _ptr(g, dt, "g"), _ptr(slope, torch.float32, "slope")
+    return T
+
+
+def _lin_states(a, rows, slots, **pools):
+    """The state pools (name: tensor or None) and state_slots of a kda_lin_* argument block."""
+    num = None
+    for name, x in pools.items():
+        if x is None:
+            continue
+        if x.dim() != 4 or tuple(x.shape[1:]) != (a.num_heads, a.dk, a.dv):
+            raise ValueError(f"{name} has shape {tuple(x.shape)}, expected [states, {a.num_heads}, {a.dk}, {a.dv}]")
+        if num is not None and x.shape[0] != num:
+            raise ValueError(f"{name} has {x.shape[0]} states, the other pool {num}")
+        num = x.shape[0]
+        setattr(a, name, _ptr(x, torch.float32, name))
+    if slots is not None:
+        _shape("state_slots", slots, (rows,))
+    elif num is not None and num < rows:
+        raise ValueError(f"{rows} sequences but {num} states")
+    a.num_states, a.state_slots = num or 0, _ptr(slots, torch.int32, "state_slots")
+
+
+class LinPrefill(_CacheCall):
+    """Planned ``kda_lin_prefill``: linear attention with a decay for each head
+    over packed prompts, q and k [T, H_k, dk], v [T, H, dv], log alpha = -slope
+    softplus(g) from g [T, H] and slope [H] float32 (either may be left out).
+    Sequence s goes on from row s of initial_state (or row state_slots[s]; None:
+    zeros) and leaves its state in the same row of final_state, [rows, H, dk, dv]
+    float32: True allocates one (zeros where state_slots name no row), None keeps none, and it may be initial_state itself.  ``o``
+    [T, H, dv] is allocated unless given."""
+    _name = "kda_lin_prefill"
+
+    def __init__(self, q, k, v, cu_seqlens, *, g=None, slope=None, scale=1.0, initial_state=None, final_state=True,
+                 state_slots=None, o=None, status=None):
+        a, N = LinPrefillArgs(), _cu(cu_seqlens)
+        dev = _same_device(q=q, k=k, v=v, cu_seqlens=cu_seqlens, g=g, slope=slope, initial_state=initial_state,
+                           final_state=None if final_state is True else final_state, state_slots=state_slots, o=o)
+        T = _lin_heads(a, q, k, v, g, slope)
+        if final_state is True:
+            if initial_state is not None:
+                rows = initial_state.shape[0]
+            elif state_slots is None:
+                rows = N
+            else:
+                raise ValueError("state_slots need a final_state (or None): the pool's rows are not known")
+            make = torch.empty if state_slots is None and rows == N else torch.zeros
+            final_state = make(rows, a.num_heads, a.dk, a.dv, dtype=torch.float32, device=dev)
+        self.final_state = final_state
+        self.o = torch.empty_like(v, memory_format=torch.contiguous_format) if o is None else o
+        _shape("o", self.o, v.shape)
+        a.num_seqs, a.total_tokens, a.scale = N, T, float(scale)
+        a.cu_seqlens = _ptr(cu_seqlens, torch.int64, "cu_seqlens")
+        a.o = _ptr(self.o, v.dtype, "o")
+        _lin_states(a, N, state_slots, initial_state=initial_state, final_state=final_state)
+        self._plan(dev, a, (q, k, v, cu_seqlens, g, slope, initial_state, state_slots), status)
+
+
+class LinDecode(_CacheCall):
+    """Planned ``kda_lin_decode``: one token a row, q and k [B, H_k, dk], v [B, H,
+    dv].  Row r advances row r (or state_slots[r]) of state [rows, H, dk, dv] float32
+    into the same row of state_out (None: in place); ``o`` [B, H, dv] is allocated
+    unless given."""
+    _name, _sized = "kda_lin_decode", False
+
+    def __init__(self, q, k, v, state, *, g=None, slope=None, scale=1.0, state_out=None, state_slots=None, o=None,
+                 status=None):
+        a = LinDecodeArgs()
+        dev = _same_device(q=q, k=k, v=v, state=state, g=g, slope=slope, state_out=state_out, state_slots=state_slots,
+                           o=o)
+        a.batch = _lin_heads(a, q, k, v, g, slope)
+        self.state_out = state if state_out is None else state_out
+        self.o = torch.empty_like(v, memory_format=torch.contiguous_format) if o is None else o
+        _shape("o", self.o, v.shape)
+        a.scale, a.o = float(scale), _ptr(self.o, v.dtype, "o")
+        _lin_states(a, a.batch, state_slots, state=state, state_out=self.state_out)
+        self._plan(dev, a, (q, k, v, state, g, slope, state_slots), status)
+
+
+def _lin_tree(a, T, cu_seqlens, parents, max_seqlen):
+    if parents is not None:
+        _shape("parents", parents, (T,))
+    max_seqlen = int(max_seqlen)
+    if not 0 <= max_seqlen <= LIN_MAX_DRAFT:
+        raise ValueError(f"max_seqlen {max_seqlen} outside 0..{LIN_MAX_DRAFT}")
+    a.num_seqs, a.total_tokens, a.max_seqlen = _cu(cu_seqlens), T, max_seqlen
+    a.cu_seqlens = _ptr(cu_seqlens, torch.int64, "cu_seqlens")
+    a.parents = _ptr(parents, torch.int32, "parents")
+
+
+class LinDraft(_CacheCall):
+    """Planned ``kda_lin_draft``: o of drafted tokens, a tree for each request
+    (parents [T] int32: the index within the request of the token that one
+    follows, -1 for the state; None: a chain), over states that stay as they are.
+    A request holds at most LIN_MAX_DRAFT tokens; max_seqlen (0: that many)
+    bounds them, and smaller bounds take smaller tiles."""
+    _name, _sized = "kda_lin_draft", False
+
+    def __init__(self, q, k, v, cu_seqlens, state, *, parents=None, g=None, slope=None, scale=1.0, state_slots=None,
+                 max_seqlen=0, o=None, status=None):
+        a = LinDraftArgs()
+        dev = _same_device(q=q, k=k, v=v, cu_seqlens=cu_seqlens, state=state, parents=parents, g=g, slope=slope,
+                           state_slots=state_slots, o=o)
+        T = _lin_heads(a, q, k, v, g, slope)
+        _lin_tree(a, T, cu_seqlens, parents, max_seqlen)
+        self.o = torch.empty_like(v, memory_format=torch.contiguous_format) if o is None else o
+        _shape("o", self.o, v.shape)
+        a.scale, a.o = float(scale), _ptr(self.o, v.dtype, "o")
+        _lin_states(a, a.num_seqs, state_slots, state=state)
+        self._plan(dev, a, (q, k, v, cu_seqlens, state, parents, g, slope, state_slots), status)
+
+
+class LinCommit(_CacheCall):
+    """Planned ``kda_lin_commit``: states advanced along the accepted path of the
+    trees that ``LinDraft`` was given; last [N] int32 is the last accepted token's
+    index within its request, -1 for none.  state_out (None: in place) receives
+    the states, rows as in state."""
+    _name, _sized = "kda_lin_commit", False
+
+    def __init__(self, k, v, cu_seqlens, last, state, *, parents=None, g=None, slope=None, state_out=None,
+                 state_slots=None, max_seqlen=0, status=None):
+        a = LinCommitArgs()
+        dev = _same_device(k=k, v=v, cu_seqlens=cu_seqlens, last=last, state=state, parents=parents, g=g, slope=slope,
+                           state_out=state_out, state_slots=state_slots)
+        T = _lin_heads(a, None, k, v, g, slope)
+        _lin_tree(a, T, cu_seqlens, parents, max_seqlen)
+        _shape("last", last, (a.num_seqs,))
+        a.last = _ptr(last, torch.int32, "last")
+        self.state_out = state if state_out is None else state_out
+        _lin_states(a, a.num_seqs, state_slots, state=state, state_out=self.state_out)
+        self._plan(dev, a, (k, v, cu_seqlens, last, state, parents, g, slope, state_slots), status)
+
+
+def lin_prefill(q, k, v, cu_seqlens, *, stream=None, **kw):
+    """Allocates, runs and returns (o, final_state) (see LinPrefill)."""
+    c = _run_on(lambda: LinPrefill(q, k, v, cu_seqlens, **kw), stream)
+    return c.o, c.final_state
+
+
+def lin_decode(q, k, v, state, *, stream=None, **kw):
+    """Allocates, runs and returns o; state advances in place unless state_out is given (see LinDecode)."""
+    return _run_on(lambda: LinDecode(q, k, v, state, **kw), stream).o
+
+
+def lin_draft(q, k, v, cu_seqlens, state, *, stream=None, **kw):
+    """Allocates, runs and returns o (see LinDraft)."""
+    return _run_on(lambda: LinDraft(q, k, v, cu_seqlens, state, **kw), stream).o
+
+
+def lin_commit(k, v, cu_seqlens, last, state, *, stream=None, **kw):
+    """Runs kda_lin_commit and returns the states (see LinCommit)."""
+    return _run_on(lambda: LinCommit(k, v, cu_seqlens, last, state, **kw), stream).state_out
