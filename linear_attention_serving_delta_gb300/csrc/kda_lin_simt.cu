@@ -105,9 +105,4 @@ cudaError_t launch_lin_simt(const LinParams& p, cudaStream_t stream) {
   return p.dt == KDA_BF16 ? launch_t<__nv_bfloat16>(p, stream) : launch_t<float>(p, stream);
 }
 
-// (the tensor cores' form is not there yet)
-bool lin_tc_fits(const LinParams&) { return false; }
-size_t lin_tc_workspace(const LinParams&) { return 256; }
-cudaError_t launch_lin_tc(const LinParams&, void*, cudaStream_t) { return cudaErrorInvalidValue; }
-
 }  // namespace kda
