@@ -5,8 +5,9 @@
 //
 //   P = Q K^T                          tcgen05
 //   P~_ij = 2^{G_i - G_j} P_ij, j <= i rounded to bf16, into P's columns of TMEM
-//   O = 2^{G_i} (Q S) + P~ V           tcgen05, S rounded to bf16 for this alone
-//   S <- 2^{G_C} S + K~^T V            K~_j = 2^{G_C - G_j} k_j in two bf16 parts
+//   Q~_i = 2^{G_i} q_i                 the same, beside them
+//   O = Q~ S + P~ V                    tcgen05, A from TMEM; S rounded to bf16 for this alone
+//   S <- 2^{G_C} S + K~^T V            K~_j = 2^{G_C - G_j} k_j in two bf16 parts, A from TMEM
 //
 // K~ = hi + lo leaves out less than 2^-16 of a term, so states keep fp32's
 // precision to about 1e-6 in norm (hi alone: 1e-3); the product starts from zero in each
@@ -15,18 +16,30 @@
 // are <= 0 and taken as differences before the exponential.
 //
 // A CTA runs one chain: a sequence (or a segment of one) of a head and DV columns
-// of its state, chunk after chunk.  Warps 0-3: P~ and the outputs, a thread a
-// row.  Warps 4-11: the state, DV / 2 columns of a row in a thread's registers; they
-// also look through V and make K~ in place: hi over K, lo over Q, which the
-// products before have read.  Warp 12 copies, 13 issues the MMAs, 14 sums the gates.
+// of its state, chunk after chunk.  Warp 0 copies, 1 issues the products of the
+// outputs, 2 those of the state (the lowest warps, which the schedulers prefer: all
+// others wait for what these do).  Warps 4-7 look through V and make P~, a thread a
+// row.  Warps 8-11: the outputs.  Warps 12-19: the state, DV / 2 columns of a row in
+// a thread's registers, and K~, whose transposition ldmatrix and the 16-lane stores
+// to TMEM make.  The gates' sums of each (chunk, head) are a record in the workspace
+// (kda_lin_tc.cuh), made before: as a role of their own they took the longest.
 //
-// Bytes of a chunk at 128 x 128: 128 KB, 2.9 us of an SM's share of HBM; the chain
-// through the state (Q S, K~, K~^T V, S) takes about half of that.
+// Roles run side by side on the schedulers' small instruction caches: unrolled ones of
+// 140 KB together issued an instruction in 6 to 10 cycles.  What waits for shared
+// memory or TMEM is unrolled as far as its latency asks, the rest is not.
+//
+// Shared memory is what an SM runs short of: its copies, the MMAs' operands and the
+// threads' accesses are 480 KB a chunk at 128 x 128 (3,750 cycles at 128 bytes each)
+// beside the 5,500 that HBM takes for the chunk's 128 KB.  Hence A from TMEM wherever
+// a thread has to rewrite the operand anyway, and the outputs' rows through the
+// query tile, which is done with by then (32-byte pieces of rows straight to
+// global memory took 2,700 cycles a chunk).
 //
 // Values that are not finite.  P~ is exactly 0 at later tokens, which would
 // still turn their infinities and NaN into NaN: V's are taken out in shared
 // memory, and a channel is NaN in o from that token on, and in the state.  Rows
 // of V and K~ behind the sequence are zeroed.
+#include <algorithm>
 #include <cstddef>
 
 #include "kda_lin_tc.cuh"
@@ -37,8 +50,9 @@ namespace {
 using namespace tc;
 
 constexpr int C = kLinChunk;
-constexpr int kThreads = 480;
+constexpr int kThreads = 640;
 constexpr uint32_t kTmemCols = 512;
+constexpr int kAhead = 2;         // chunks that the prefetch into L2 is ahead
 constexpr uint32_t kBlock = C * 128;  // bytes of 64 channels of a tile
 
 template <int DK, int DV>
@@ -54,53 +68,144 @@ struct Shape {
   static constexpr uint32_t kTail = kS + kSop;
   static constexpr uint32_t kBytes = kTail + 3072;
   static constexpr int kSCols = MB == 1 ? DV / 2 : DV;     // columns of a state thread
-  // TMEM columns
-  static constexpr int tP = 0, tOI = C, tOA = C + DV, tKV = C + 2 * DV;
-  static_assert(tKV + MB * DV <= (int)kTmemCols && kStages >= 1 && kBytes <= 232448, "fits an SM");
+  // K~ goes through TMEM kTok tokens of one row tile at a time
+  static constexpr int kTok = MB == 1 ? C : C / 2, kPhases = MB * (C / kTok);
+  // TMEM columns: P (P~ over its first half, Q~ over its second or behind it), O, K~^T V,
+  // then hi and lo, twice where there is room
+  static constexpr int tP = 0, tQ = DK <= 128 ? 64 : C, tO = DK <= 128 ? C : C + DK / 2, tKV = tO + DV,
+                       tHi = tKV + MB * DV, tLo = tHi + kTok / 2;
+  static constexpr int kKBuf = kPhases == 1 && tHi + 2 * kTok <= (int)kTmemCols ? 2 : 1;
+  static_assert(tLo + kTok / 2 <= (int)kTmemCols && kStages >= 1 && kBytes <= 232448, "fits an SM");
 };
 
 struct Tail {
-  uint64_t qk_full[4], v_full[4], empty[4];
-  uint64_t p_full, qs_done, o_full, kv_full;               // committed by the MMA warp
-  uint64_t s_ready, p_ready, v_ready, k_ready, o_free, g_full, g_free, meet, drain;
+  uint64_t q_full[4], k_full[4], v_full[4], v_ready[4], q_empty[4], k_empty[4], v_empty[4];
+  uint64_t p_full, o_full, kv_full;                        // committed by the MMA warp
+  uint64_t s_ready, p_ready, k_ready, o_free, g_full[2], g_free[2], drain[2];
   uint32_t dead, tmem;
-  uint32_t poisoned;      // some channel's nan_from is set
-  float total;            // log2 of the chunk's decay
-  float block_total[4];   // and of its blocks of 32 tokens
-  // (the outputs read these two four at a time)
-  alignas(16) float g32[C];     // sum of log2 alpha from the start of the token's block of 32
-  alignas(16) float to_end[C];  // 2^ of the sum over what follows it in its block
-  float w[C];             // 2^{G_C - G_j}
-  int32_t nan_from[128];  // first token of the chain with a value that is not finite, per channel
+  int32_t poisoned;       // the CTA's chain that nan_from speaks of, -1: none so far
+  int32_t scaled_q;       // the chunk is strong, for the MMAs
+  LinItem only;           // the CTA's chain where there is no plan
+  int32_t num_items, pad;
+  alignas(16) LinGateHead gates[2];  // the records of two chunks
+  // per channel the first token with a value that is not finite in the latest chain
+  // that had one, counted through the CTA's chunks
+  uint32_t nan_from[128];
 };
-static_assert(sizeof(Tail) <= 3072 && offsetof(Tail, g32) % 16 == 0 && offsetof(Tail, to_end) % 16 == 0, "tail block");
-
-struct Chain {
-  int32_t tok0, len, head, tile, from, to;
-  bool any;
-};
+static_assert(sizeof(Tail) <= 3072 && offsetof(Tail, gates) % 16 == 0, "tail block");
 
 // The CTA's i-th chain, for every role alike
-__device__ __forceinline__ bool chain_at(const LinParams& p, const LinTcArgs& a, int i, Chain* ch) {
-  if (a.items) {
-    const int64_t w = nth_item(i);
-    if (w >= *a.num_items) return false;
-    const LinItem it = a.items[w];
-    *ch = Chain{it.tok0, it.len, it.head, it.tile, it.from, it.to, true};
-    return true;
+__device__ __forceinline__ bool chain_at(const LinParams& p, const LinTcArgs& a, const Tail* b, int i, LinItem* ch) {
+  if (!a.items) {
+    *ch = b->only;
+    return i == 0 && ch->len >= 0;
   }
-  if (i > 0) return false;
+  const int64_t w = nth_item(i);
+  if (w >= b->num_items) return false;
+  const int per = p.H * a.tiles, r = (int)(w % per);
+  *ch = a.items[w / per];
+  ch->head = r / a.tiles;
+  ch->tile = r % a.tiles;
+  return true;
+}
+// Without a plan CTA b takes chain b of sequence, head, tile (len -1: skipped)
+__device__ __forceinline__ LinItem own_chain(const LinParams& p, const LinTcArgs& a, int64_t* sum) {
   const int per = p.H * a.tiles, s = (int)(blockIdx.x / per), r = (int)(blockIdx.x % per);
   const LinSeq seq = lin_seq(p, s);
-  if (seq.flag && r == 0 && threadIdx.x == 0) attn_flag(p.status, seq.flag);
+  const int64_t rec = seq_records(p, s, kThreads, sum), chunks = (seq.len + C - 1) / C;
+  // (sequences that overlap between malformed ones may have more chunks than there are records)
+  const bool ok = seq.ok && rec + chunks <= a.max_records;
+  const int32_t flag = seq.ok && !ok ? kFlagBadSeqlens : seq.flag;
+  if (flag && r == 0 && threadIdx.x == 0) attn_flag(p.status, flag);
   const int row = -2 - seq.slot;
-  *ch = Chain{(int32_t)seq.tok0, (int32_t)seq.len, r / a.tiles, r % a.tiles, p.state_in ? row : -1,
-              p.state_out ? row : -1, seq.ok};
-  return seq.ok;
+  return LinItem{(int32_t)seq.tok0, ok ? (int32_t)seq.len : -1, r / a.tiles, r % a.tiles, p.state_in ? row : -1,
+                 p.state_out ? row : -1, (int32_t)rec, -1};
+}
+// wait_or_dead for a whole warp.  The hint lets the hardware hold the warp for up to
+// 10 us at a time: 20 warps that poll took half of the SM's issue slots.
+__device__ __forceinline__ bool mbar_hold(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(10000u)
+      : "memory");
+  return done != 0;
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t* dead) {
+  if (__all_sync(0xffffffffu, mbar_hold(bar, parity))) return true;
+  const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
+  while (!__all_sync(0xffffffffu, mbar_hold(bar, parity))) {
+    if (__any_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(dead) != 0 || globaltimer_ns() - t0 > kWaitLimitNs)) {
+      *reinterpret_cast<volatile uint32_t*>(dead) = 1;
+      return false;
+    }
+  }
+  return true;
+}
+// Whether token `token` of a chain has one before or at it; n: the CTA's chunks before the chain
+__device__ __forceinline__ bool nan_at(const Tail* b, int channel, uint32_t n, int token) {
+  const uint32_t x = reinterpret_cast<const volatile uint32_t*>(b->nan_from)[channel];
+  return x >= n * C && x <= n * C + (uint32_t)token;
+}
+__device__ __noinline__ void nan_note(Tail* b, int channel, uint32_t n, int token) {
+  uint32_t *at = &b->nan_from[channel], x = *reinterpret_cast<volatile uint32_t*>(at);
+  while (x < n * C || x > n * C + (uint32_t)token) {
+    const uint32_t y = atomicCAS_block(at, x, n * C + (uint32_t)token);
+    if (y == x) break;
+    x = y;
+  }
 }
 // A state of the pool or the workspace
 __device__ __forceinline__ int64_t state_at(const LinParams& p, int32_t place, int head) {
   return ((int64_t)(place >= 0 ? place : -2 - place) * p.H + head) * p.dk * p.dv;
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack2(float2 x) { return tc::pack2(x.x, x.y); }
+
+// Four 8 x 8 blocks of bf16, transposed: the thread gets column l / 4, rows 2 (l % 4) and + 1 of each
+__device__ __forceinline__ void ldsm4t(uint32_t* r, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// 16 lanes of TMEM, N blocks of four 32-bit columns: of each block the thread gives
+// column l % 4 of lanes l / 4 and l / 4 + 8
+template <int N>
+__device__ __forceinline__ void tmem_st_16x128(uint32_t taddr, const uint32_t* v) {
+  static_assert(N == 4 || N == 8, "blocks");
+  if constexpr (N == 8)
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+  else
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, const void* src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(m), "r"(x), "r"(y),
+               "r"(z), "r"(smem_u32(src))
+               : "memory");
+}
+// The same box as tma_3d's, into L2 alone
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* m, int x, int y, int z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(m), "r"(x), "r"(y), "r"(z)
+               : "memory");
 }
 
 // ------------------------------------------------------------------ copies
@@ -109,279 +214,432 @@ __device__ void copy_role(const LinParams& p, const LinTcArgs& a, const CUtensor
                           const CUtensorMap* mv, char* sm, Tail* b) {
   using S = Shape<DK, DV>;
   Ring<S::kStages> ring;
-  uint32_t n = 0;
+  uint32_t n = 0, nv = 0, nq = 0, ng = 0;  // copies of K, V, Q and gates under way
   bool ok = true;
-  Chain ch;
-  for (int i = 0; ok && chain_at(p, a, i, &ch); ++i) {
+  LinItem ch;
+  for (int i = 0; ok && chain_at(p, a, b, i, &ch); ++i) {
     const int kh = ch.head / p.R;
-    for (int t = 0; t < ch.len; t += C) {
-      if (!(ok = wait_or_dead(&b->empty[ring.st], ring.ph ^ 1, &b->dead))) break;
-      mbar_arrive_expect_tx(&b->qk_full[ring.st], kLocal ? S::kQK : 2 * S::kQK);
-#pragma unroll
+    // Tiles come to L2 two chunks before the stages have room for them: with two stages
+    // that are given back late HBM's latency would show in every chunk
+    auto prefetch = [&](int t) {
+      if (t >= ch.len) return;
+#pragma unroll 1
       for (int c = 0; c < DK / 64; ++c) {
-        if (!kLocal) tma_3d(sm + ring.st * S::kQK + c * kBlock, mq, 64 * c, kh, ch.tok0 + t, &b->qk_full[ring.st]);
-        tma_3d(sm + S::kK + ring.st * S::kQK + c * kBlock, mk, 64 * c, kh, ch.tok0 + t, &b->qk_full[ring.st]);
+        if (!kLocal) tma_prefetch_3d(mq, 64 * c, kh, ch.tok0 + t);
+        tma_prefetch_3d(mk, 64 * c, kh, ch.tok0 + t);
       }
-      mbar_arrive_expect_tx(&b->v_full[ring.st], S::kVb);
+#pragma unroll 1
+      for (int c = 0; c < DV / 64; ++c) tma_prefetch_3d(mv, ch.tile * DV + 64 * c, ch.head, ch.tok0 + t);
+    };
+    if (kAhead > 1) prefetch(C);
+    for (int t = 0; t < ch.len; t += C) {
+      prefetch(t + kAhead * C);
+      const uint32_t st = ring.st, g = ng & 1;
+      if (!(ok = wait_or_dead(&b->g_free[g], ((ng >> 1) & 1) ^ 1, &b->dead))) break;
+      mbar_arrive_expect_tx(&b->g_full[g], sizeof(LinGateHead));
+      bulk_g2s(&b->gates[g], &a.records[((int64_t)ch.rec + t / C) * p.H + ch.head].head, sizeof(LinGateHead), &b->g_full[g]);
+      ++ng;
+      if (!(ok = wait_or_dead(&b->k_empty[st], ring.ph ^ 1, &b->dead))) break;
+      mbar_arrive_expect_tx(&b->k_full[st], S::kQK);
+#pragma unroll
+      for (int c = 0; c < DK / 64; ++c)
+        tma_3d(sm + S::kK + st * S::kQK + c * kBlock, mk, 64 * c, kh, ch.tok0 + t, &b->k_full[st]);
+      ++n;
+      if (!(ok = wait_or_dead(&b->v_empty[st], ring.ph ^ 1, &b->dead))) break;
+      mbar_arrive_expect_tx(&b->v_full[st], S::kVb);
 #pragma unroll
       for (int c = 0; c < DV / 64; ++c)
-        tma_3d(sm + S::kV + ring.st * S::kVb + c * kBlock, mv, ch.tile * DV + 64 * c, ch.head, ch.tok0 + t,
-               &b->v_full[ring.st]);
+        tma_3d(sm + S::kV + st * S::kVb + c * kBlock, mv, ch.tile * DV + 64 * c, ch.head, ch.tok0 + t, &b->v_full[st]);
+      ++nv;
+      if (!kLocal) {
+        if (!(ok = wait_or_dead(&b->q_empty[st], ring.ph ^ 1, &b->dead))) break;
+        mbar_arrive_expect_tx(&b->q_full[st], S::kQK);
+#pragma unroll
+        for (int c = 0; c < DK / 64; ++c)
+          tma_3d(sm + st * S::kQK + c * kBlock, mq, 64 * c, kh, ch.tok0 + t, &b->q_full[st]);
+        ++nq;
+      }
       ring.next();
-      ++n;
     }
   }
   // no copy of its own is in flight when a CTA that gave up exits
-  if (!ok)
-    for (uint32_t k = n > S::kStages ? n - S::kStages : 0; k < n; ++k) {
-      mbar_wait(&b->qk_full[k % S::kStages], (k / S::kStages) & 1, kWaitLimitNs);
-      mbar_wait(&b->v_full[k % S::kStages], (k / S::kStages) & 1, kWaitLimitNs);
-    }
+  if (!ok) {
+    auto drain = [&](uint64_t* full, uint32_t count, uint32_t stages) {
+      for (uint32_t k = count > stages ? count - stages : 0; k < count; ++k)
+        mbar_wait(&full[k % stages], (k / stages) & 1, kWaitLimitNs);
+    };
+    drain(b->k_full, n, S::kStages);
+    drain(b->v_full, nv, S::kStages);
+    drain(b->q_full, nq, S::kStages);
+    drain(b->g_full, ng, 2);
+  }
 }
 
 // ------------------------------------------------------------------ MMAs
-template <int DK, int DV, bool kLocal>
-__device__ void mma_role(const LinParams& p, const LinTcArgs& a, char* sm, Tail* b) {
+// The products of the outputs: Q K^T, then P~ V and Q~ S over it.  P's columns take
+// the next chunk once both have been issued: an issuer's MMAs execute in order.
+template <int DK, int DV>
+__device__ void mma_out_role(const LinParams& p, const LinTcArgs& a, const CUtensorMap* mo, char* sm, Tail* b) {
   using S = Shape<DK, DV>;
   const uint32_t tmem = __shfl_sync(0xffffffffu, b->tmem, 0);
-  constexpr uint32_t id_qk = idesc_bf16(C, C), id_n = idesc_bf16(C, DV, 0, 1), id_kv = idesc_bf16(C, DV, 1, 1);
-  // K-major Q and K; channels of Q and K as rows of K~^T; V and S by rows of the contraction
+  constexpr uint32_t id_qk = idesc_bf16(C, C), id_n = idesc_bf16(C, DV, 0, 1);
+  // K-major Q and K; V and S by rows of the contraction
   const uint64_t q0 = sdesc_sw128(smem_u32(sm), 16, 1024), k0 = sdesc_sw128(smem_u32(sm + S::kK), 16, 1024),
-                 lo0 = sdesc_sw128(smem_u32(sm), kBlock, 1024), hi0 = sdesc_sw128(smem_u32(sm + S::kK), kBlock, 1024),
                  v0 = sdesc_sw128(smem_u32(sm + S::kV), kBlock, 1024),
                  s0 = sdesc_sw128(smem_u32(sm + S::kS), DK * 128, 1024);
   const bool issue = elect_one();
+  uint32_t n = 0;
   Ring<S::kStages> ring;
-  uint32_t n = 0, ns = 0;
-  uint32_t* dead = &b->dead;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, wait_or_dead(bar, parity, dead)) != 0;
+    return warp_wait(bar, parity, &b->dead);
   };
   bool ok = true;
-  Chain ch;
-  for (int i = 0; ok && chain_at(p, a, i, &ch); ++i) {
-    bool has = ch.from != -1;  // a state to read o from
-    for (int t = 0; t < ch.len; t += C, ++n, has = true) {
-      const uint64_t qd = q0 + (uint64_t)(ring.st * (S::kQK >> 4)), kd = k0 + (uint64_t)(ring.st * (S::kQK >> 4)),
-                     vd = v0 + (uint64_t)(ring.st * (S::kVb >> 4));
-      if (!(ok = wait(&b->qk_full[ring.st], ring.ph))) break;
-      if (!kLocal) {
-        fence_after_sync();
-        if (issue) {
-#pragma unroll
-          for (int s = 0; s < DK / 16; ++s) {
-            const uint32_t off = ((s / 4) * kBlock + (s % 4) * 32) >> 4;
-            mma_bf16(tmem + S::tP, qd + off, kd + off, id_qk, s > 0);
-          }
-          mma_commit(&b->p_full);
-        }
-        // the outputs of the chunk before have been read
-        if (n > 0 && !(ok = wait(&b->o_free, (n - 1) & 1))) break;
-        if (has) {
-          if (!(ok = wait(&b->s_ready, ns & 1))) break;
-          ++ns;
-          fence_after_sync();
-          if (issue) {
-#pragma unroll
-            for (int s = 0; s < DK / 16; ++s)
-              mma_bf16(tmem + S::tOI, qd + (((s / 4) * kBlock + (s % 4) * 32) >> 4), s0 + (uint64_t)(s * (2048 >> 4)),
-                       id_n, s > 0);
-          }
-        }
-        if (issue) mma_commit(&b->qs_done);
-        if (!(ok = wait(&b->v_ready, n & 1)) || !(ok = wait(&b->p_ready, n & 1))) break;
-        fence_after_sync();
-        if (issue) {
-#pragma unroll
-          for (int s = 0; s < C / 16; ++s)
-            mma_bf16_ts(tmem + S::tOA, tmem + S::tP + s * 8, vd + (uint64_t)(s * (2048 >> 4)), id_n, s > 0);
-          mma_commit(&b->o_full);
-        }
-      } else {
-        if (!(ok = wait(&b->v_ready, n & 1))) break;
-      }
-      if (!(ok = wait(&b->k_ready, n & 1))) break;
+  LinItem ch;
+  for (int i = 0; ok && chain_at(p, a, b, i, &ch); ++i) {
+    for (int t = 0; t < ch.len; t += C, ++n) {
+      if (!(ok = wait(&b->k_full[ring.st], ring.ph)) || !(ok = wait(&b->q_full[ring.st], ring.ph))) break;
       fence_after_sync();
       if (issue) {
-        const uint64_t hd = hi0 + (uint64_t)(ring.st * (S::kQK >> 4)), ld = lo0 + (uint64_t)(ring.st * (S::kQK >> 4));
-#pragma unroll
-        for (int m = 0; m < S::MB; ++m)
-#pragma unroll
-          for (int s = 0; s < C / 16; ++s) {
-            const uint32_t off = (2 * m * kBlock + s * 2048) >> 4;
-            mma_bf16(tmem + S::tKV + m * DV, ld + off, vd + (uint64_t)(s * (2048 >> 4)), id_kv, s > 0);
-            mma_bf16(tmem + S::tKV + m * DV, hd + off, vd + (uint64_t)(s * (2048 >> 4)), id_kv, 1);
+        const uint64_t qd = q0 + (uint64_t)(ring.st * (S::kQK >> 4)), kd = k0 + (uint64_t)(ring.st * (S::kQK >> 4));
+#pragma unroll 1
+        for (int s = 0; s < DK / 16; ++s) {
+          const uint32_t off = ((s / 4) * kBlock + (s % 4) * 32) >> 4;
+          mma_bf16(tmem + S::tP, qd + off, kd + off, id_qk, s > 0);
+        }
+        mma_commit(&b->p_full);
+        mma_commit(&b->k_empty[ring.st]);
+      }
+      // the outputs of the chunk before have been read
+      if (n > 0 && !(ok = wait(&b->o_free, (n - 1) & 1))) break;
+      if (!(ok = wait(&b->v_ready[ring.st], ring.ph)) || !(ok = wait(&b->p_ready, n & 1))) break;
+      fence_after_sync();
+      if (issue) {
+        const uint64_t vd = v0 + (uint64_t)(ring.st * (S::kVb >> 4));
+#pragma unroll 1
+        for (int s = 0; s < C / 16; ++s)
+          mma_bf16_ts(tmem + S::tO, tmem + S::tP + s * 8, vd + (uint64_t)(s * (2048 >> 4)), id_n, s > 0);
+        mma_commit(&b->v_empty[ring.st]);
+      }
+      if (!(ok = wait(&b->s_ready, n & 1))) break;
+      fence_after_sync();
+      if (issue) {
+        if (t > 0 || ch.from != -1) {
+          const bool scaled = *reinterpret_cast<volatile int32_t*>(&b->scaled_q) != 0;
+          const uint64_t qd = q0 + (uint64_t)(ring.st * (S::kQK >> 4));
+#pragma unroll 1
+          for (int s = 0; s < DK / 16; ++s) {
+            const uint64_t sd = s0 + (uint64_t)(s * (2048 >> 4));
+            if (scaled) mma_bf16_ts(tmem + S::tO, tmem + S::tQ + s * 8, sd, id_n, 1);
+            else mma_bf16(tmem + S::tO, qd + (((s / 4) * kBlock + (s % 4) * 32) >> 4), sd, id_n, 1);
           }
-        mma_commit(&b->kv_full);
-        mma_commit(&b->empty[ring.st]);
+        }
+        mma_commit(&b->o_full);
       }
       ring.next();
     }
   }
   // no MMA and no arrival of one is left in flight
-  if (issue) mma_commit(&b->drain);
-  mbar_wait(&b->drain, 0, kWaitLimitNs);
+  if (issue) mma_commit(&b->drain[0]);
+  mbar_wait(&b->drain[0], 0, kWaitLimitNs);
 }
 
-// ------------------------------------------------------------------ gates
-// A warp, four neighbouring tokens a lane; the logits of the next chunk are
-// read before this one's sums are waited for.
-template <bool kLocal>
-__device__ void gate_role(const LinParams& p, const LinTcArgs& a, Tail* b) {
-  const int lane = threadIdx.x & 31;
-  uint32_t n = 0;
-  Chain ch;
-  for (int i = 0; chain_at(p, a, i, &ch); ++i) {
-    float x[4];
-    auto fetch = [&](int t) {
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        x[u] = t + 4 * lane + u < ch.len ? lin_log2_alpha<__nv_bfloat16>(p, (int64_t)ch.tok0 + t + 4 * lane + u, ch.head)
-                                         : 0.f;
-    };
-    if (ch.len > 0) fetch(0);
-    for (int t = 0; t < ch.len; t += C, ++n) {
-      LogSum g[4];
-      g[0] = log_sum(x[0]);
-#pragma unroll
-      for (int u = 1; u < 4; ++u) g[u] = g[u - 1] + log_sum(x[u]);
-      LogSum before = g[3];  // of the lanes up to this one, then of those before it
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const LogSum y{__shfl_up_sync(0xffffffffu, before.i, o), __shfl_up_sync(0xffffffffu, before.f, o)};
-        if (lane >= o) before = y + before;
+// Those of the state: K~^T V from zero, lo and hi in turn
+template <int DK, int DV>
+__device__ void mma_state_role(const LinParams& p, const LinTcArgs& a, char* sm, Tail* b) {
+  using S = Shape<DK, DV>;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, b->tmem, 0);
+  constexpr uint32_t id_n = idesc_bf16(C, DV, 0, 1);
+  const uint64_t v0 = sdesc_sw128(smem_u32(sm + S::kV), kBlock, 1024);
+  const bool issue = elect_one();
+  uint32_t n = 0;  // phases
+  Ring<S::kStages> ring;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return warp_wait(bar, parity, &b->dead);
+  };
+  bool ok = true;
+  LinItem ch;
+  for (int i = 0; ok && chain_at(p, a, b, i, &ch); ++i) {
+    for (int t = 0; ok && t < ch.len; t += C) {
+      const uint64_t vd = v0 + (uint64_t)(ring.st * (S::kVb >> 4));
+      if (!(ok = wait(&b->v_ready[ring.st], ring.ph))) break;
+#pragma unroll 1
+      for (int ph = 0; ph < S::kPhases; ++ph, ++n) {
+        if (!(ok = wait(&b->k_ready, n & 1))) break;
+        fence_after_sync();
+        if (issue) {
+          constexpr int kPer = C / S::kTok;
+          const int tok = ph % kPer * S::kTok;
+          const uint32_t buf = tmem + (S::kKBuf == 2 ? (n & 1) * S::kTok : 0);
+#pragma unroll 1
+          for (int s = 0; s < S::kTok / 16; ++s) {
+            const uint64_t vs = vd + (uint64_t)((tok / 16 + s) * (2048 >> 4));
+            mma_bf16_ts(tmem + S::tKV + ph / kPer * DV, buf + S::tLo + s * 8, vs, id_n, tok > 0 || s > 0);
+            mma_bf16_ts(tmem + S::tKV + ph / kPer * DV, buf + S::tHi + s * 8, vs, id_n, 1);
+          }
+          mma_commit(&b->kv_full);
+          if (ph + 1 == S::kPhases) mma_commit(&b->v_empty[ring.st]);
+        }
       }
-      auto from = [&](int src) {
-        return LogSum{__shfl_sync(0xffffffffu, before.i, src), __shfl_sync(0xffffffffu, before.f, src)};
-      };
-      const LogSum end = from(lane | 7), all = from(31), prev = from(lane > 0 ? lane - 1 : 0),
-                   start = from(lane >= 8 ? (lane & ~7) - 1 : 0);
-      const bool first = lane == 0, first_block = lane < 8;
-      if (t + C < ch.len) fetch(t + C);
-      if (!__all_sync(0xffffffffu, wait_or_dead(&b->g_free, (n & 1) ^ 1, &b->dead))) return;
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const LogSum G = first ? g[u] : prev + g[u];
-        const int j = 4 * lane + u;
-        b->g32[j] = first_block ? G.i + G.f : log_diff(G, start);
-        b->to_end[j] = exp2f(log_diff(end, G));
-        b->w[j] = exp2f(log_diff(all, G));
-      }
-      if ((lane & 7) == 7) b->block_total[lane >> 3] = first_block ? end.i + end.f : log_diff(end, start);
-      if (lane == 31) b->total = all.i + all.f;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&b->g_full);
+      ring.next();
     }
   }
+  if (issue) mma_commit(&b->drain[1]);
+  mbar_wait(&b->drain[1], 0, kWaitLimitNs);
 }
 
-// ------------------------------------------------------------------ outputs
-template <int DK, int DV>
-__device__ void out_role(const LinParams& p, const LinTcArgs& a, Tail* b) {
+// ------------------------------------------------------------------ values, P~ and Q~
+// V before the products read it: rows behind the sequence to zero, values that are
+// not finite out (r: the thread's row of the tile).
+// These are noted once nothing of an earlier chunk is left to be written.
+template <int DK, int DV, bool kLocal>
+__device__ __forceinline__ bool look_through(char* vt, int r, int live, int chain, int token, uint32_t n, Tail* b) {
   using S = Shape<DK, DV>;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = 32 * warp + lane;
-  const uint32_t lanes = (uint32_t)(32 * warp) << 16, tp = b->tmem + lanes + S::tP;
-  uint32_t* dead = &b->dead;
-  uint32_t n = 0;
-  Chain ch;
-  for (int i = 0; chain_at(p, a, i, &ch); ++i) {
-    bool has = ch.from != -1;
-    for (int t = 0; t < ch.len; t += C, ++n, has = true) {
-      if (!__all_sync(0xffffffffu, wait_or_dead(&b->g_full, n & 1, dead))) return;
-      if (!__all_sync(0xffffffffu, wait_or_dead(&b->p_full, n & 1, dead))) return;
-      fence_after_sync();
-      const float gi = b->g32[row];
-      // 2^{G_i - G_j}: within the row's own block of 32 tokens from the difference,
-      // for an earlier block as 2^{G_i - G_e} 2^{G_e - G_j}, e the block's last token
-      float since = gi;  // from the end of block c to the row
-      float back[4];
-#pragma unroll
-      for (int c = 3; c >= 0; --c) {
-        if (c >= warp) {
-          back[c] = 0.f;
-        } else {
-          back[c] = exp2_fast(since);
-          since += b->block_total[c];
-        }
+  constexpr int P = DV / 8;
+  uint32_t seen = 0;
+  if (r >= live) {
+#pragma unroll 1
+    for (int c = 0; c < P; ++c) *reinterpret_cast<uint4*>(vt + sw_off(r, c, kBlock)) = make_uint4(0, 0, 0, 0);
+  } else {
+#pragma unroll 8
+    for (int c = 0; c < P; ++c) seen |= exponents_full(*reinterpret_cast<const uint4*>(vt + sw_off(r, c, kBlock)));
+  }
+  if (__any_sync(0xffffffffu, (seen & 0x80008000u) != 0)) {
+    if (!warp_wait(&b->k_ready, (n * S::kPhases) & 1, &b->dead)) return false;
+    if (!kLocal && n > 0 && !warp_wait(&b->o_free, (n - 1) & 1, &b->dead)) return false;
+    if (seen & 0x80008000u) {
+#pragma unroll 1
+      for (int c = 0; c < P; ++c) {
+        uint4* at = reinterpret_cast<uint4*>(vt + sw_off(r, c, kBlock));
+        const uint4 z = *at;
+        const uint32_t bad = nonfinite8(z);
+#pragma unroll 1
+        for (int e = 0; e < 8; ++e)
+          if (bad >> e & 1)
+            nan_note(b, 8 * c + e, n - token / C, token);
+        *at = make_uint4(finite_only(z.x), finite_only(z.y), finite_only(z.z), finite_only(z.w));
       }
-      const float from_start = exp2f(since);  // 2^{G_i}
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t pk[16];
-        if (c <= warp) {
-          float s[32];
-          tmem_ld32(tp + 32 * c, s);
+      *reinterpret_cast<volatile int32_t*>(&b->poisoned) = chain;
+    }
+  }
+  return true;
+}
+
+template <int DK, int DV, bool kLocal>
+__device__ void weight_role(const LinParams& p, const LinTcArgs& a, char* sm, Tail* b) {
+  using S = Shape<DK, DV>;
+  const int warp = (threadIdx.x >> 5) - 4, lane = threadIdx.x & 31, row = 32 * warp + lane;
+  const uint32_t lanes = b->tmem + ((uint32_t)(32 * warp) << 16), tp = lanes + S::tP;
+  uint32_t* dead = &b->dead;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return warp_wait(bar, parity, dead);
+  };
+  uint32_t n = 0;
+  Ring<S::kStages> ring;
+  LinItem ch;
+  for (int i = 0; chain_at(p, a, b, i, &ch); ++i) {
+    for (int t = 0; t < ch.len; t += C, ++n) {
+      if (!wait(&b->v_full[ring.st], ring.ph)) return;
+      if (!look_through<DK, DV, kLocal>(sm + S::kV + ring.st * S::kVb, row, min(C, ch.len - t), i, t + row, n, b)) return;
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&b->v_ready[ring.st]);
+      if (kLocal) {
+        ring.next();
+        continue;
+      }
+      const LinGateHead& gh = b->gates[n & 1];
+      if (!wait(&b->g_full[n & 1], (n >> 1) & 1) || !wait(&b->p_full, n & 1)) return;
+      fence_after_sync();
+      const bool strong = gh.strong != 0;
+      if (row == 0) b->scaled_q = strong;
+      if (!strong) {
+        // 2^{-G_j} P_ij for j <= i; 64 columns at a time, over columns that have been read
+        auto convert = [&](int c, auto masked) {
+          float x[64];
+          uint32_t pk[32];
+          tmem_ld32(tp + c, x);
+          tmem_ld32(tp + c + 32, x + 32);
           tmem_ld_wait();
-          if (c < warp) {
 #pragma unroll
-            for (int u = 0; u < 32; u += 4) {
-              const float4 e = *reinterpret_cast<const float4*>(&b->to_end[32 * c + u]);
-              pk[u / 2] = pack2(s[u] * (back[c] * e.x), s[u + 1] * (back[c] * e.y));
-              pk[u / 2 + 1] = pack2(s[u + 2] * (back[c] * e.z), s[u + 3] * (back[c] * e.w));
+          for (int u = 0; u < 64; u += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(&gh.col[c + u]);
+            float2 y = mul2(make_float2(x[u], x[u + 1]), make_float2(f.x, f.y)),
+                   z = mul2(make_float2(x[u + 2], x[u + 3]), make_float2(f.z, f.w));
+            if (decltype(masked)::value) {
+              const int last = row - c - u;
+              y = make_float2(last >= 0 ? y.x : 0.f, last >= 1 ? y.y : 0.f);
+              z = make_float2(last >= 2 ? z.x : 0.f, last >= 3 ? z.y : 0.f);
             }
-          } else {
-#pragma unroll
-            for (int u = 0; u < 32; u += 4) {
-              const float4 g = *reinterpret_cast<const float4*>(&b->g32[32 * c + u]);
-              const float y0 = u <= lane ? s[u] * exp2_fast(gi - g.x) : 0.f,
-                          y1 = u + 1 <= lane ? s[u + 1] * exp2_fast(gi - g.y) : 0.f,
-                          y2 = u + 2 <= lane ? s[u + 2] * exp2_fast(gi - g.z) : 0.f,
-                          y3 = u + 3 <= lane ? s[u + 3] * exp2_fast(gi - g.w) : 0.f;
-              pk[u / 2] = pack2(y0, y1);
-              pk[u / 2 + 1] = pack2(y2, y3);
-            }
+            pk[u / 2] = pack2(y);
+            pk[u / 2 + 1] = pack2(z);
           }
+          tmem_st32(tp + c / 2, pk);
+        };
+        if (warp >= 2) {
+          convert(0, std::false_type{});
+          convert(64, std::true_type{});
         } else {
+          convert(0, std::true_type{});
+          uint32_t pk[32];
+#pragma unroll
+          for (int u = 0; u < 32; ++u) pk[u] = 0;
+          tmem_st32(tp + 32, pk);
+        }
+      } else {
+        // 2^{G_i - G_j}.  For an earlier block of 32 tokens as 2^{G_i - G_e} 2^{G_e - G_j},
+        // e the block's last token
+        const float* g32 = a.records[((int64_t)ch.rec + t / C) * p.H + ch.head].row;
+        const float gi = g32[row];
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
 #pragma unroll
           for (int u = 0; u < 16; ++u) pk[u] = 0;
+          if (c <= warp) {
+            float since = gi;
+#pragma unroll 1
+            for (int y = c + 1; y < warp; ++y) since += gh.block[y];
+            const float back = exp2_fast(since);
+            float x[32];
+            tmem_ld32(tp + 32 * c, x);
+            tmem_ld_wait();
+#pragma unroll
+            for (int u = 0; u < 32; u += 2) {
+              float f[2];
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {
+                const int j = 32 * c + u + z;
+                f[z] = c < warp ? back * gh.col[j] : exp2_fast(gi - g32[j]);
+                x[u + z] = j <= row ? x[u + z] * f[z] : 0.f;
+              }
+              pk[u / 2] = tc::pack2(x[u], x[u + 1]);
+            }
+          }
+          tmem_st16(tp + 16 * c, reinterpret_cast<const float*>(pk));
         }
-        tmem_st16(tp + 16 * c, reinterpret_cast<const float*>(pk));
+        // 2^{G_i} q_i
+        if (!wait(&b->q_full[ring.st], ring.ph)) return;
+        const char* qt = sm + ring.st * S::kQK;
+        float since = gi;
+#pragma unroll 1
+        for (int y = 0; y < warp; ++y) since += gh.block[y];
+        const float f = exp2f(since);
+        const float2 f2 = make_float2(f, f);
+        auto part = [&](uint32_t q2) { return pack2(mul2(make_float2(bf_lo(q2), bf_hi(q2)), f2)); };
+#pragma unroll 1
+        for (int c = 0; c < DK / 32; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const uint4 q4 = *reinterpret_cast<const uint4*>(qt + sw_off(row, 4 * c + u, kBlock));
+            pk[4 * u] = part(q4.x);
+            pk[4 * u + 1] = part(q4.y);
+            pk[4 * u + 2] = part(q4.z);
+            pk[4 * u + 3] = part(q4.w);
+          }
+          tmem_st16(lanes + S::tQ + 16 * c, reinterpret_cast<const float*>(pk));
+        }
       }
       tmem_st_wait();
       fence_before_sync();
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&b->p_ready);
-        mbar_arrive(&b->g_free);
+        mbar_arrive(&b->g_free[n & 1]);
       }
-      if (!__all_sync(0xffffffffu, wait_or_dead(&b->o_full, n & 1, dead))) return;
-      fence_after_sync();
-      const bool mine = t + row < ch.len;
-      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) +
-                         ((int64_t)(ch.tok0 + t + row) * p.H + ch.head) * p.dv + ch.tile * DV;
-      const bool poisoned = *reinterpret_cast<volatile uint32_t*>(&b->poisoned) != 0;
-      const int width = min(DV, p.dv - ch.tile * DV);
-#pragma unroll 1
-      for (int c = 0; c < width; c += 32) {
-        float x[32];
-        tmem_ld32(tp + (S::tOA - S::tP) + c, x);
-        if (has) {
-          float y[32];
-          tmem_ld32(tp + (S::tOI - S::tP) + c, y);
-          tmem_ld_wait();
-#pragma unroll
-          for (int u = 0; u < 32; ++u) x[u] = fmaf(from_start, y[u], x[u]);
-        } else {
-          tmem_ld_wait();
-        }
-        if (poisoned)
-#pragma unroll
-          for (int u = 0; u < 32; ++u)
-            if (reinterpret_cast<const volatile int32_t*>(b->nan_from)[c + u] <= t + row) x[u] = NAN;
-        if (mine) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int u = 0; u < 16; ++u) pk[u] = pack2(x[2 * u] * p.scale, x[2 * u + 1] * p.scale);
-          st_32b(o + c, pk, a.o_wide);
-          if (c + 16 < width) st_32b(o + c + 16, pk + 8, a.o_wide);
-        }
-        __syncwarp();
-      }
-      fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&b->o_free);
+      ring.next();
     }
   }
+}
+
+// ------------------------------------------------------------------ outputs
+template <int DK, int DV>
+__device__ void out_role(const LinParams& p, const LinTcArgs& a, const CUtensorMap* mo, char* sm, Tail* b) {
+  using S = Shape<DK, DV>;
+  const int warp = (threadIdx.x >> 5) - 8, lane = threadIdx.x & 31, row = 32 * warp + lane;
+  const uint32_t to = b->tmem + ((uint32_t)(32 * warp) << 16) + S::tO;
+  uint32_t n = 0;
+  Ring<S::kStages> ring;
+  LinItem ch;
+  for (int i = 0; chain_at(p, a, b, i, &ch); ++i) {
+    const int width = min(DV, p.dv - ch.tile * DV);
+    const int64_t stride = (int64_t)p.H * p.dv;
+    const LinGates* rec = a.records + (int64_t)ch.rec * p.H + ch.head;
+    for (int t = 0; t < ch.len; t += C, rec += p.H) {
+      const float own = rec->row[row];
+      const int32_t strong = rec->head.strong;
+      char* qt = sm + ring.st * S::kQK;
+      if (!warp_wait(&b->o_full, n & 1, &b->dead)) return;
+      fence_after_sync();
+      const int live = min(C, ch.len - t) - 32 * warp;  // rows of the warp that are tokens
+      const bool poisoned = *reinterpret_cast<volatile int32_t*>(&b->poisoned) == i;
+      // Through the warp's rows of the query tile, which nothing reads any more, as
+      // many blocks of 64 channels as it has: then whole rows of them to global memory
+      constexpr int kHold = DV < DK ? DV : DK;
+      const float f = p.scale * (strong ? 1.f : own);
+      const float2 f2 = make_float2(f, f);
+#pragma unroll 1
+      for (int c0 = 0; c0 < DV; c0 += kHold) {
+        __syncwarp();
+#pragma unroll 1
+        for (int c = 0; c < kHold && c < DV; c += 64) {
+          float x[64];
+          tmem_ld32(to + c0 + c, x);
+          tmem_ld32(to + c0 + c + 32, x + 32);
+          tmem_ld_wait();
+          if (c0 + c + 64 == DV) {
+            fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&b->o_free);
+          }
+#pragma unroll
+          for (int u = 0; u < 64; u += 8) {
+            uint32_t pk[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) pk[z] = pack2(mul2(make_float2(x[u + 2 * z], x[u + 2 * z + 1]), f2));
+            *reinterpret_cast<uint4*>(qt + sw_off(row, (c + u) / 8, kBlock)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          }
+        }
+        if (poisoned)
+#pragma unroll 1
+          for (int u = 0; u < kHold; ++u)
+            if (nan_at(b, c0 + u, n - t / C, t + row))
+              *reinterpret_cast<uint16_t*>(qt + sw_off(row, u / 8, kBlock) + 2 * (u % 8)) = 0x7fff;
+        fence_async_smem();
+        __syncwarp();
+        constexpr int kB = kHold / 64;
+        if (live >= 32) {
+          // 32 rows of 64 channels a copy (stores of the threads took 2,700 cycles a chunk)
+          if (lane == 0) {
+#pragma unroll
+            for (int c = 0; c < kB; ++c)
+              if (c0 + 64 * c < width)
+                tma_store_3d(mo, qt + c * kBlock + warp * 4096, ch.tile * DV + c0 + 64 * c, ch.head,
+                             ch.tok0 + t + 32 * warp);
+            bulk_commit();
+            bulk_wait_read_all();
+          }
+          __syncwarp();
+        } else {
+          const int piece = lane & 7, r0 = lane >> 3;
+          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) +
+                             ((int64_t)(ch.tok0 + t + 32 * warp + r0) * p.H + ch.head) * p.dv + ch.tile * DV + c0 + 8 * piece;
+#pragma unroll 1
+          for (int r = r0; r < live; r += 4, o += 4 * stride)
+#pragma unroll
+            for (int c = 0; c < kB; ++c)
+              if (c0 + 64 * c + 8 * piece < width)
+                *reinterpret_cast<uint4*>(o + 64 * c) =
+                    *reinterpret_cast<const uint4*>(qt + sw_off(32 * warp + r, 8 * c + piece, kBlock));
+          __syncwarp();
+        }
+      }
+      if (lane == 0) mbar_arrive(&b->q_empty[ring.st]);
+      ring.next();
+      ++n;
+    }
+  }
+  if (lane == 0) bulk_wait_all();
 }
 
 // ------------------------------------------------------------------ the state
@@ -389,24 +647,20 @@ template <int DK, int DV, bool kLocal>
 __device__ void state_role(const LinParams& p, const LinTcArgs& a, char* sm, Tail* b) {
   using S = Shape<DK, DV>;
   constexpr int N = S::kSCols;
-  const int x = threadIdx.x - 128, lane = x & 31, quarter = (x >> 5) & 3, half = x >> 7;
+  constexpr int TH = S::kTok / 2;  // tokens of K~ that a warp makes at a time, for 32 channels
+  const int x = threadIdx.x - 384, lane = x & 31, quarter = (x >> 5) & 3, half = x >> 7;
   // the state: row d, columns [col, col + N)
   const int d = 32 * quarter + lane + (S::MB > 1 ? 128 * half : 0), col = S::MB > 1 ? 0 : half * N;
   const bool holds = d < DK;
-  const uint32_t kv = b->tmem + ((uint32_t)(32 * quarter) << 16) + S::tKV + half * N;
-  // copies: row r of a tile, half of its 16-byte pieces
-  const int r = x & 127;
+  const uint32_t lanes = b->tmem + ((uint32_t)(32 * quarter) << 16), kv = lanes + S::tKV + half * N;
   uint32_t* dead = &b->dead;
-  uint32_t n = 0, met = 0;
+  uint32_t n = 0;
   Ring<S::kStages> ring;
-  // the state's threads meet (a wait with a limit, as all others)
-  auto meet = [&]() -> bool {
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&b->meet);
-    return __all_sync(0xffffffffu, wait_or_dead(&b->meet, met++ & 1, dead)) != 0;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return warp_wait(bar, parity, dead);
   };
-  Chain ch;
-  for (int i = 0; chain_at(p, a, i, &ch); ++i) {
+  LinItem ch;
+  for (int i = 0; chain_at(p, a, b, i, &ch); ++i) {
     float s[N];
     const int c0 = ch.tile * DV + col;  // of the head's columns
     const bool mine = holds && d < p.dk;
@@ -420,136 +674,137 @@ __device__ void state_role(const LinParams& p, const LinTcArgs& a, char* sm, Tai
         s[u + 1] = y.y;
         s[u + 2] = y.z;
         s[u + 3] = y.w;
+        if (kLocal && ch.copy >= 0 && mine && c0 + u < p.dv)
+          *reinterpret_cast<float4*>(a.states + state_at(p, ch.copy, ch.head) + (int64_t)d * p.dv + c0 + u) = y;
       }
     }
-    // what was noted in the chain before is dropped once its last outputs are written
-    if (!meet()) return;
-    if (!kLocal && n > 0 && *reinterpret_cast<volatile uint32_t*>(&b->poisoned) &&
-        !__all_sync(0xffffffffu, wait_or_dead(&b->o_free, (n - 1) & 1, dead)))
-      return;
-    if (!meet()) return;
-    if (x < DV) b->nan_from[x] = INT32_MAX;
-    if (x == 0) b->poisoned = 0;
-    if (!meet()) return;
     LinDecay decay{0.f, true};
-    bool has = ch.from != -1;
-    // S <- decay S + K~^T V of the chunk before, which ended at token t
-    auto advance = [&](int t) -> bool {
-      if (!__all_sync(0xffffffffu, wait_or_dead(&b->kv_full, (n - 1) & 1, dead))) return false;
+    // S <- decay S + K~^T V of the chunk before
+    auto advance = [&]() -> bool {
+      if (!wait(&b->kv_full, (n * S::kPhases - 1) & 1)) return false;
       fence_after_sync();
       if (holds) {
+        const float one = decay.near_one ? 1.f : 0.f;
+        const float2 m = make_float2(decay.m, decay.m), keep = make_float2(one, one);
 #pragma unroll
         for (int c = 0; c < N; c += 32) {
           float y[32];
           tmem_ld32(kv + c, y);
           tmem_ld_wait();
-          if (decay.near_one) {
 #pragma unroll
-            for (int u = 0; u < 32; ++u) s[c + u] = fmaf(decay.m, s[c + u], s[c + u]) + y[u];
-          } else {
-#pragma unroll
-            for (int u = 0; u < 32; ++u) s[c + u] = fmaf(decay.m, s[c + u], y[u]);
+          for (int u = 0; u < 32; u += 2) {
+            const float2 old = make_float2(s[c + u], s[c + u + 1]);
+            const float2 z = fma2(keep, old, fma2(m, old, make_float2(y[u], y[u + 1])));
+            s[c + u] = z.x;
+            s[c + u + 1] = z.y;
           }
         }
-        if (*reinterpret_cast<volatile uint32_t*>(&b->poisoned))
-#pragma unroll
-          for (int u = 0; u < N; ++u)
-            if (reinterpret_cast<volatile int32_t*>(b->nan_from)[col + u] < t) s[u] = NAN;
       }
       fence_before_sync();
       return true;
     };
-    for (int t = 0; t < ch.len; t += C, ++n, has = true) {
+    for (int t = 0; t < ch.len; t += C, ++n) {
       const int live = min(C, ch.len - t);
-      // V: rows behind the sequence to zero, values that are not finite out
-      if (!__all_sync(0xffffffffu, wait_or_dead(&b->v_full[ring.st], ring.ph, dead))) return;
-      {
-        char* vt = sm + S::kV + ring.st * S::kVb;
-        constexpr int P = DV / 16;
-        if (r >= live) {
-#pragma unroll
-          for (int c = 0; c < P; ++c) *reinterpret_cast<uint4*>(vt + sw_off(r, half * P + c, kBlock)) = make_uint4(0, 0, 0, 0);
-        } else {
-          uint32_t seen = 0;
-#pragma unroll
-          for (int c = 0; c < P; ++c) seen |= exponents_full(*reinterpret_cast<const uint4*>(vt + sw_off(r, half * P + c, kBlock)));
-          if (seen & 0x80008000u) {
+      const bool has = t > 0 || ch.from != -1;
+      LinDecay next;
+      // K~ of a phase: 32 channels and TH tokens, transposed on the way to TMEM
+      auto make_k = [&](int ph) {
+        const int m = ph / (C / S::kTok), tok0 = ph % (C / S::kTok) * S::kTok + half * TH;
+        const uint32_t kt = smem_u32(sm + S::kK + ring.st * S::kQK);
+        if (32 * quarter < DK) {
 #pragma unroll 1
-            for (int c = 0; c < P; ++c) {
-              uint4* at = reinterpret_cast<uint4*>(vt + sw_off(r, half * P + c, kBlock));
-              const uint4 y = *at;
-              const uint32_t bad = nonfinite8(y);
-              if (!bad) continue;
-              for (int e = 0; e < 8; ++e)
-                if (bad >> e & 1) atomicMin_block(&b->nan_from[8 * (half * P + c) + e], t + r);
-              *at = make_uint4(finite_only(y.x), finite_only(y.y), finite_only(y.z), finite_only(y.w));
+          for (int g = 0; g < 2; ++g) {
+            const int ch0 = 128 * m + 32 * quarter + 16 * g;
+            uint32_t hi[TH / 4], lo[TH / 4];
+#pragma unroll
+            for (int c = 0; c < TH / 16; ++c)
+              ldsm4t(lo + 4 * c, kt + sw_off(tok0 + 16 * c + (lane & 7) + (lane >> 4) * 8, ch0 / 8 + ((lane >> 3) & 1), kBlock));
+            if (live < C)  // rows behind the sequence
+#pragma unroll
+              for (int u = 0; u < TH / 4; ++u) {
+                const int y = tok0 + (u >> 1) * 8 + 2 * (lane & 3);
+                if (y >= live) lo[u] = 0;
+                else if (y + 1 >= live) lo[u] &= 0xffffu;
+              }
+#pragma unroll
+            for (int u = 0; u < TH / 4; ++u) {
+              const float2 w = *reinterpret_cast<const float2*>(&b->gates[n & 1].w[tok0 + (u >> 1) * 8 + 2 * (lane & 3)]);
+              const float2 f = mul2(make_float2(bf_lo(lo[u]), bf_hi(lo[u])), w);
+              hi[u] = pack2(f);
+              lo[u] = pack2(fma2(make_float2(bf_lo(hi[u]), bf_hi(hi[u])), make_float2(-1.f, -1.f), f));
             }
-            *reinterpret_cast<volatile uint32_t*>(&b->poisoned) = 1;
+            const uint32_t at = lanes + ((uint32_t)(16 * g) << 16) + half * (TH / 2) +
+                                (S::kKBuf == 2 ? (n & 1) * S::kTok : 0);
+            tmem_st_16x128<TH / 8>(at + S::tHi, hi);
+            tmem_st_16x128<TH / 8>(at + S::tLo, lo);
+          }
+          tmem_st_wait();
+        }
+        fence_before_sync();
+      };
+      auto gates = [&]() -> bool {
+        if (!wait(&b->g_full[n & 1], (n >> 1) & 1) || !wait(&b->k_full[ring.st], ring.ph)) return false;
+        next = lin_decay(b->gates[n & 1].total);
+        return true;
+      };
+      // with two buffers K~ beside the product of the chunk before, else behind it
+      if (S::kKBuf == 2) {
+        if (!gates()) return;
+        make_k(0);
+        if (t > 0 && !advance()) return;
+      } else {
+        if (t > 0 && !advance()) return;
+        if (!gates()) return;
+      }
+      decay = next;
+#pragma unroll 1
+      for (int ph = 0; ph < S::kPhases; ++ph) {
+        if (ph > 0) {
+          if (!wait(&b->kv_full, (n * S::kPhases + ph - 1) & 1)) return;
+          fence_after_sync();
+        }
+        if (S::kKBuf == 1) make_k(ph);
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&b->k_ready);
+          if (ph + 1 == S::kPhases) {
+            mbar_arrive(&b->k_empty[ring.st]);
+            mbar_arrive(&b->g_free[n & 1]);
           }
         }
       }
-      fence_async_smem();
-      // the state after the chunk before, also as an operand
-      if (t > 0 && !advance(t)) return;
-      __syncwarp();
-      // (behind kv_full, so that the MMA warp has passed the arrival of the chunk before)
-      if (lane == 0) mbar_arrive(&b->v_ready);
-      if (!kLocal && has) {
-        if (holds) {
+      // the state as an operand, once the product with the one before is done
+      if (!kLocal) {
+        if (n > 0 && !wait(&b->o_full, (n - 1) & 1)) return;
+        if (has && holds) {
           char* st = sm + S::kS;
 #pragma unroll
           for (int u = 0; u < N; u += 8)
             *reinterpret_cast<uint4*>(st + sw_off(d, (col + u) / 8, DK * 128)) =
-                make_uint4(pack2(s[u], s[u + 1]), pack2(s[u + 2], s[u + 3]), pack2(s[u + 4], s[u + 5]), pack2(s[u + 6], s[u + 7]));
+                make_uint4(tc::pack2(s[u], s[u + 1]), tc::pack2(s[u + 2], s[u + 3]), tc::pack2(s[u + 4], s[u + 5]),
+                           tc::pack2(s[u + 6], s[u + 7]));
+          if (*reinterpret_cast<volatile int32_t*>(&b->poisoned) == i)
+#pragma unroll 1
+            for (int u = 0; u < N; ++u)
+              if (nan_at(b, col + u, n - t / C, t - 1))
+                *reinterpret_cast<uint16_t*>(st + sw_off(d, (col + u) / 8, DK * 128) + 2 * (u % 8)) = 0x7fff;
         }
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&b->s_ready);
       }
-      // K~
-      if (!__all_sync(0xffffffffu, wait_or_dead(&b->g_full, n & 1, dead))) return;
-      const float w = b->w[r];
-      decay = lin_decay(b->total);
-      if (!__all_sync(0xffffffffu, wait_or_dead(&b->qk_full[ring.st], ring.ph, dead))) return;
-      if (!kLocal && !__all_sync(0xffffffffu, wait_or_dead(&b->qs_done, n & 1, dead))) return;
-      fence_after_sync();
-      {
-        char *lo = sm + ring.st * S::kQK, *hi = sm + S::kK + ring.st * S::kQK;
-        constexpr int P = DK / 16;
-#pragma unroll 4
-        for (int c = 0; c < P; ++c) {
-          const uint32_t off = sw_off(r, half * P + c, kBlock);
-          uint4 h4 = make_uint4(0, 0, 0, 0), l4 = h4;
-          if (r < live) {
-            const uint4 k4 = *reinterpret_cast<const uint4*>(hi + off);
-            auto part = [&](uint32_t k2, uint32_t* h2, uint32_t* l2) {
-              const float k0 = bf_lo(k2), k1 = bf_hi(k2);
-              *h2 = pack2(k0 * w, k1 * w);
-              *l2 = pack2(fmaf(k0, w, -bf_lo(*h2)), fmaf(k1, w, -bf_hi(*h2)));
-            };
-            part(k4.x, &h4.x, &l4.x);
-            part(k4.y, &h4.y, &l4.y);
-            part(k4.z, &h4.z, &l4.z);
-            part(k4.w, &h4.w, &l4.w);
-          }
-          *reinterpret_cast<uint4*>(hi + off) = h4;
-          *reinterpret_cast<uint4*>(lo + off) = l4;
-        }
-      }
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&b->k_ready);
-        mbar_arrive(&b->g_free);
-      }
       ring.next();
     }
-    if (ch.len > 0 && !advance(ch.len)) return;
+    if (ch.len > 0 && !advance()) return;
     if (ch.to != -1 && mine) {
       float* to = (ch.to >= 0 ? a.states : p.state_out) + state_at(p, ch.to, ch.head) + (int64_t)d * p.dv + c0;
 #pragma unroll
       for (int u = 0; u < N; u += 4)
         if (c0 + u < p.dv) *reinterpret_cast<float4*>(to + u) = make_float4(s[u], s[u + 1], s[u + 2], s[u + 3]);
+      if (ch.len > 0 && *reinterpret_cast<volatile int32_t*>(&b->poisoned) == i)
+#pragma unroll 1
+        for (int u = 0; u < N; ++u)
+          if (c0 + u < p.dv && nan_at(b, col + u, n - (ch.len + C - 1) / C, ch.len - 1)) to[u] = NAN;
     }
   }
 }
@@ -557,63 +812,86 @@ __device__ void state_role(const LinParams& p, const LinTcArgs& a, char* sm, Tai
 template <int DK, int DV, bool kLocal>
 __global__ void __launch_bounds__(kThreads, 1)
     lin_tc(const LinParams p, const LinTcArgs a, const __grid_constant__ CUtensorMap mq,
-           const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+           const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+           const __grid_constant__ CUtensorMap mo) {
   using S = Shape<DK, DV>;
   extern __shared__ __align__(1024) char sm[];
   Tail* b = reinterpret_cast<Tail*>(sm + S::kTail);
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     for (int s = 0; s < 4; ++s) {
-      mbar_init(&b->qk_full[s], 1);
-      mbar_init(&b->v_full[s], 1);
-      mbar_init(&b->empty[s], 1);
+      for (uint64_t* x : {&b->q_full[s], &b->k_full[s], &b->v_full[s]}) mbar_init(x, 1);
+      mbar_init(&b->v_ready[s], 4);
+      mbar_init(&b->q_empty[s], 4);
+      mbar_init(&b->k_empty[s], kLocal ? 8 : 9);
+      mbar_init(&b->v_empty[s], kLocal ? 1 : 2);
     }
-    for (uint64_t* x : {&b->p_full, &b->qs_done, &b->o_full, &b->kv_full, &b->g_full, &b->drain}) mbar_init(x, 1);
-    for (uint64_t* x : {&b->s_ready, &b->v_ready, &b->k_ready, &b->meet}) mbar_init(x, 8);
-    mbar_init(&b->p_ready, 4);
-    mbar_init(&b->o_free, 4);
-    mbar_init(&b->g_free, kLocal ? 8 : 12);
+    for (uint64_t* x : {&b->p_full, &b->o_full, &b->kv_full, &b->drain[0], &b->drain[1], &b->g_full[0], &b->g_full[1]})
+      mbar_init(x, 1);
+    for (uint64_t* x : {&b->s_ready, &b->k_ready}) mbar_init(x, 8);
+    for (uint64_t* x : {&b->p_ready, &b->o_free}) mbar_init(x, 4);
+    for (uint64_t* x : {&b->g_free[0], &b->g_free[1]}) mbar_init(x, kLocal ? 8 : 12);
     b->dead = 0;
+    b->poisoned = -1;
     mbar_init_fence();
   }
   if (threadIdx.x == 32) {
     if (!kLocal) prefetch_map(&mq);
+    if (!kLocal) prefetch_map(&mo);
     prefetch_map(&mk);
     prefetch_map(&mv);
   }
-  if (warp == 13) tmem_alloc(&b->tmem, kTmemCols);
+  if (threadIdx.x >= 64 && threadIdx.x < 64 + 128) b->nan_from[threadIdx.x - 64] = ~0u;
+  if (warp == 1) tmem_alloc(&b->tmem, kTmemCols);
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
   pdl_wait();  // the plan, or what came before
-  if (warp < 4) {
-    if (!kLocal) out_role<DK, DV>(p, a, b);
-  } else if (warp < 12) {
-    state_role<DK, DV, kLocal>(p, a, sm, b);
-  } else if (warp == 12) {
-    if ((threadIdx.x & 31) == 0) copy_role<DK, DV, kLocal>(p, a, &mq, &mk, &mv, sm, b);
-  } else if (warp == 13) {
-    mma_role<DK, DV, kLocal>(p, a, sm, b);
+  if (a.items) {
+    if (threadIdx.x == 0) b->num_items = *a.num_items;
   } else {
-    gate_role<kLocal>(p, a, b);
+    // a chain of the CTA's own, and its records (the tiles of a head all make them, alike)
+    const LinItem own = own_chain(p, a, reinterpret_cast<int64_t*>(sm));
+    if (threadIdx.x == 0) b->only = own;
+    for (int c = warp; c * C < own.len; c += kThreads / 32)
+      make_gates(p, own.tok0, own.len, c * C, own.head, &a.records[((int64_t)own.rec + c) * p.H + own.head]);
+    fence_proxy_async_global();
+  }
+  __syncthreads();
+  // registers: 96 a thread at launch (640 x 96 = 61,440); 128 x (48 + 104 + 88 + 2 x 120)
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    if (warp == 0) {
+      if ((threadIdx.x & 31) == 0) copy_role<DK, DV, kLocal>(p, a, &mq, &mk, &mv, sm, b);
+    } else if (warp == 1) {
+      if (!kLocal) mma_out_role<DK, DV>(p, a, &mo, sm, b);
+    } else if (warp == 2) {
+      mma_state_role<DK, DV>(p, a, sm, b);
+    }
+  } else if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    weight_role<DK, DV, kLocal>(p, a, sm, b);
+  } else if (warp < 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (!kLocal) out_role<DK, DV>(p, a, &mo, sm, b);
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
+    state_role<DK, DV, kLocal>(p, a, sm, b);
   }
   __syncwarp();
   fence_before_sync();
   __syncthreads();
   if (threadIdx.x == 0 && b->dead) attn_flag(p.status, kFlagTimeout);
-  if (warp == 13) tmem_dealloc(b->tmem, kTmemCols);
+  if (warp == 1) tmem_dealloc(b->tmem, kTmemCols);
 }
 
 // ------------------------------------------------------------------ host
-// Column tiles: 128 wide, 64 where the keys are 256 or the values no wider
-int tile_width(const LinParams& p) { return p.dk > 128 || p.dv <= 64 ? 64 : 128; }
-
-bool lin_map(CUtensorMap* m, const void* base, int64_t tokens, int heads, int d) {
+bool lin_map(CUtensorMap* m, const void* base, int64_t tokens, int heads, int d, int box_tokens) {
   const EncodeTiledFn enc = encode_tiled();
   if (!enc) return false;
   const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)tokens};
   const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)d * 2 * heads};
-  const cuuint32_t box[3] = {64, 1, (cuuint32_t)C}, elem[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {64, 1, (cuuint32_t)box_tokens}, elem[3] = {1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, elem,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -622,19 +900,49 @@ bool lin_map(CUtensorMap* m, const void* base, int64_t tokens, int heads, int d)
 template <int DK, int DV>
 cudaError_t launch_shape(const LinParams& p, void* ws, cudaStream_t stream) {
   using S = Shape<DK, DV>;
-  CUtensorMap mq, mk, mv;
-  if (!lin_map(&mq, p.q, p.total_tokens, p.Hk, p.dk) || !lin_map(&mk, p.k, p.total_tokens, p.Hk, p.dk) ||
-      !lin_map(&mv, p.v, p.total_tokens, p.H, p.dv))
+  CUtensorMap mq, mk, mv, mo;
+  if (!lin_map(&mq, p.q, p.total_tokens, p.Hk, p.dk, C) || !lin_map(&mk, p.k, p.total_tokens, p.Hk, p.dk, C) ||
+      !lin_map(&mv, p.v, p.total_tokens, p.H, p.dv, C) || !lin_map(&mo, p.o, p.total_tokens, p.H, p.dv, 32))
     return cudaErrorInvalidValue;
+  char* w = static_cast<char*>(ws);
+  const LinLayout L = lin_layout(p);
   LinTcArgs a{};
   a.tiles = (p.dv + DV - 1) / DV;
-  a.o_wide = (reinterpret_cast<uintptr_t>(p.o) & 31) == 0;
-  cudaError_t e =
-      cudaFuncSetAttribute(lin_tc<DK, DV, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kBytes);
+  a.records = reinterpret_cast<LinGates*>(w + L.records);
+  a.max_records = lin_max_records(p);
+  auto run = [&](auto kernel, int64_t ctas) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kBytes);
+    if (e != cudaSuccess) return e;
+    return launch_maybe_dependent(true, kernel, dim3((unsigned)ctas), dim3(kThreads), (size_t)S::kBytes, stream, p, a, mq,
+                                  mk, mv, mo);
+  };
+  const int64_t per = (int64_t)p.H * a.tiles;
+  if (L.direct) return run(lin_tc<DK, DV, false>, p.num_seqs * per);
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  const int64_t chains = (int64_t)p.num_seqs * p.H * a.tiles;
-  return launch_maybe_dependent(true, lin_tc<DK, DV, false>, dim3((unsigned)chains), dim3(kThreads), (size_t)S::kBytes,
-                                stream, p, a, mq, mk, mv);
+  LinPlan plan{};
+  plan.head = reinterpret_cast<LinHead*>(w + L.head);
+  plan.seq_rec = reinterpret_cast<int32_t*>(w + L.seq_rec);
+  plan.items = reinterpret_cast<LinItem*>(w + L.items);
+  plan.locals = reinterpret_cast<LinItem*>(w + L.locals);
+  plan.splits = reinterpret_cast<LinSplit*>(w + L.splits);
+  plan.tiles = a.tiles;
+  plan.max_records = a.max_records;
+  plan.may_split = L.may_split;
+  a.states = reinterpret_cast<float*>(w + L.states);
+  if ((e = launch_lin_plan(p, plan, stream)) != cudaSuccess) return e;
+  if ((e = launch_lin_gates(p, plan, a.records, stream)) != cudaSuccess) return e;
+  if (L.may_split) {
+    a.items = plan.locals;
+    a.num_items = &plan.head->locals;
+    if ((e = run(lin_tc<DK, DV, true>, std::min<int64_t>(sms, L.places * per))) != cudaSuccess) return e;
+    if ((e = launch_lin_combine(p, plan, a.records, a.states, stream)) != cudaSuccess) return e;
+  }
+  a.items = plan.items;
+  a.num_items = &plan.head->items;
+  return run(lin_tc<DK, DV, false>, std::min<int64_t>(sms, (p.num_seqs + L.places) * per));
 }
 
 }  // namespace
@@ -645,9 +953,9 @@ bool lin_tc_fits(const LinParams& p) {
   return p.dt == KDA_BF16 && p.total_tokens > 0 && al16(p.q) && al16(p.k) && al16(p.v) && al16(p.o) &&
          (int64_t)p.num_seqs * p.H * 4 < INT32_MAX;
 }
-size_t lin_tc_workspace(const LinParams&) { return 256; }
+size_t lin_tc_workspace(const LinParams& p) { return lin_layout(p).total; }
 cudaError_t launch_lin_tc(const LinParams& p, void* ws, cudaStream_t stream) {
-  const int w = tile_width(p);
+  const int w = lin_tile_width(p);
   if (p.dk > 128) return launch_shape<256, 64>(p, ws, stream);
   if (p.dk > 64) return w == 64 ? launch_shape<128, 64>(p, ws, stream) : launch_shape<128, 128>(p, ws, stream);
   return w == 64 ? launch_shape<64, 64>(p, ws, stream) : launch_shape<64, 128>(p, ws, stream);

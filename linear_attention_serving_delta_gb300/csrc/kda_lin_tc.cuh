@@ -1,5 +1,5 @@
-// kda_lin_tc.cuh -- work items and workspace of the tensor-core prompts of the
-// linear attention with a decay for each head.
+// kda_lin_tc.cuh -- what the tensor-core prompts of the linear attention with a decay
+// for each head share: work items, gate records, workspace.
 #pragma once
 
 #include "kda_attn_tc.cuh"
@@ -11,17 +11,152 @@ constexpr int kLinChunk = 128;  // tokens of a chunk: the rows of a tensor-core 
 
 // One chain: tokens [tok0, tok0 + len) of a head's columns [tile * DV, ...).
 // from, to: the state it starts from and leaves, a place of the workspace's
-// states (>= 0), row -2 - x of the pool (<= -2), or none (-1).
+// states (>= 0), row -2 - x of the pool (<= -2), or none (-1).  rec: its first record.
+// copy: where the state it starts from goes too, or -1.  A plan holds one for all
+// heads and tiles.
 struct LinItem {
-  int32_t tok0, len, head, tile, from, to;
+  int32_t tok0, len, head, tile, from, to, rec, copy;
 };
+
+// A sequence cut into segments, whose start states are at place, place + 1, ...
+struct LinSplit {
+  int32_t place, segments, rec, chunks;
+};
+// Segment i of n chunks cut into k: its first chunk
+__host__ __device__ __forceinline__ int32_t lin_cut(int32_t n, int32_t k, int32_t i) { return (int32_t)((int64_t)n * i / k); }
+
+struct LinHead {
+  int32_t items, locals, splits;  // entries of the lists
+};
+// The CTAs that chains are shared out to, and the fewest chunks of a segment
+constexpr int kLinSlots = 152;
+constexpr int kLinMinSegment = 8;
+constexpr int kLinDirectTokens = 2048;
+
+// The gates of a chunk of one head, with G_i the sum of log2 alpha up to token i.  A
+// chunk is weak while |G| <= kLinWeak: weights are then split as 2^{G_i} 2^{-G_j}.
+constexpr float kLinWeak = 64.f;
+struct LinGateHead {
+  float w[kLinChunk];    // 2^{G_C - G_j}
+  // weak: 2^{-G_j}; strong: 2^ of the sum over what follows the token in its block of 32
+  float col[kLinChunk];
+  float total;           // G_C
+  int32_t strong;
+  int32_t pad[2];
+  float block[4];        // the sums over the blocks of 32
+};
+struct LinGates {
+  LinGateHead head;
+  float row[kLinChunk];  // weak: 2^{G_i}; strong: the sum from the block's start on
+};
+static_assert(sizeof(LinGateHead) % 16 == 0 && sizeof(LinGates) % 16 == 0, "bulk copies");
 
 struct LinTcArgs {
   const LinItem* items;    // null: CTA b takes chain b of sequence, head, tile
   const int32_t* num_items;
   float* states;           // [places][H][dk][dv]
+  LinGates* records;       // [max_records][H]
+  int64_t max_records;
   int32_t tiles;           // column tiles of a head
-  int32_t o_wide;          // o is 32-byte aligned
 };
+
+// What the plan leaves in the workspace
+struct LinPlan {
+  LinHead* head;
+  int32_t* seq_rec;        // [N] a sequence's first record, or -1: skipped
+  LinItem* items;          // costliest first
+  LinItem* locals;         // the segments whose own end states come first
+  LinSplit* splits;
+  int32_t tiles;
+  int64_t max_records;
+  int32_t may_split;
+};
+
+struct LinLayout {
+  size_t head, seq_rec, items, locals, splits, states, records, total;
+  int64_t places;
+  bool direct, may_split;
+};
+int lin_tile_width(const LinParams& p);
+LinLayout lin_layout(const LinParams& p);
+cudaError_t launch_lin_plan(const LinParams& p, const LinPlan& a, cudaStream_t stream);
+cudaError_t launch_lin_gates(const LinParams& p, const LinPlan& a, LinGates* records, cudaStream_t stream);
+cudaError_t launch_lin_combine(const LinParams& p, const LinPlan& a, const LinGates* records, float* states,
+                               cudaStream_t stream);
+
+// Chunks of all sequences of a well-formed call, at most
+inline int64_t lin_max_records(const LinParams& p) { return p.total_tokens / kLinChunk + p.num_seqs; }
+
+// The chunks of the valid sequences before s, for the whole block (sum: shared, free before and after)
+__device__ __forceinline__ int64_t seq_records(const LinParams& p, int s, int threads, int64_t* sum) {
+  unsigned long long* at = reinterpret_cast<unsigned long long*>(sum);
+  if (threadIdx.x == 0) *at = 0;
+  __syncthreads();
+  long long x = 0;
+  for (int y = threadIdx.x; y < s; y += threads) {
+    const LinSeq q = lin_seq(p, y);
+    if (q.ok) x += (q.len + kLinChunk - 1) / kLinChunk;
+  }
+  if (x) atomicAdd_block(at, (unsigned long long)x);
+  __syncthreads();
+  const int64_t r = (int64_t)*at;
+  tc::fence_async_smem();
+  __syncthreads();
+  return r;
+}
+
+// The record of the chunk at token t of a sequence of len tokens from tok0 on, by a
+// warp, four neighbouring tokens a lane (bf16 gates).
+__device__ __forceinline__ void make_gates(const LinParams& p, int64_t tok0, int len, int t, int head, LinGates* out) {
+  const int lane = threadIdx.x & 31;
+  LogSum G[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int x = t + 4 * lane + u;
+    const LogSum la = log_sum(x < len ? lin_log2_alpha<__nv_bfloat16>(p, tok0 + x, head) : 0.f);
+    G[u] = u == 0 ? la : G[u - 1] + la;
+  }
+  // within the lane's block of 32 tokens, then over the blocks
+  LogSum upto = G[3];
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) {
+    const LogSum y{__shfl_up_sync(0xffffffffu, upto.i, o), __shfl_up_sync(0xffffffffu, upto.f, o)};
+    if ((lane & 7) >= o) upto = y + upto;
+  }
+  auto from = [&](LogSum v, int src) {
+    return LogSum{__shfl_sync(0xffffffffu, v.i, src), __shfl_sync(0xffffffffu, v.f, src)};
+  };
+  const LogSum prev = from(upto, lane > 0 ? lane - 1 : 0), t0 = from(upto, 7), t1 = from(upto, 15),
+               t2 = from(upto, 23), t3 = from(upto, 31), end = from(upto, lane | 7);
+  LogSum before{0.f, 0.f};
+  if (lane >= 8) before = t0;
+  if (lane >= 16) before = before + t1;
+  if (lane >= 24) before = before + t2;
+  const LogSum all = (t0 + t1) + (t2 + t3);
+  float from_start[4], w[4], col[4], row[4];
+  bool far = false;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    if ((lane & 7) != 0) G[u] = prev + G[u];
+    const LogSum x = before + G[u];
+    from_start[u] = x.i + x.f;
+    w[u] = exp2f(log_diff(all, x));
+    far |= fabsf(from_start[u]) > kLinWeak;  // (a NaN is not: it leaves the tokens before it as they are)
+  }
+  const bool strong = __any_sync(0xffffffffu, far);
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    col[u] = exp2f(strong ? log_diff(end, G[u]) : -from_start[u]);
+    row[u] = strong ? G[u].i + G[u].f : exp2f(from_start[u]);
+  }
+  reinterpret_cast<float4*>(out->head.w)[lane] = make_float4(w[0], w[1], w[2], w[3]);
+  reinterpret_cast<float4*>(out->head.col)[lane] = make_float4(col[0], col[1], col[2], col[3]);
+  reinterpret_cast<float4*>(out->row)[lane] = make_float4(row[0], row[1], row[2], row[3]);
+  if (lane == 0) {
+    out->head.total = all.i + all.f;
+    out->head.strong = strong;
+  }
+  if ((lane & 7) == 7) out->head.block[lane >> 3] = end.i + end.f;
+}
 
 }  // namespace kda

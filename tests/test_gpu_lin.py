@@ -264,6 +264,93 @@ def test_prefill_same_bits_every_time_and_in_a_graph():
     assert call.device_status() == 0
 
 
+# Long prompts: cut into segments where the chains would not fill the GPU, and planned in any case
+LONG = [([5000], 2, 2, 64, 64, "g"), ([3000, 0, 1, 2500], 2, 1, 128, 128, "slope"), ([4100], 1, 1, 256, 128, "both"),
+        ([2600, 1300, 17], 3, 3, 64, 128, "strong"), ([2300, 900], 40, 8, 32, 16, "keep"), ([6000], 4, 4, 128, 64, "g")]
+
+
+@pytest.mark.parametrize("lens,H,Hk,dk,dv,gate", LONG)
+def test_prefill_long(lens, H, Hk, dk, dv, gate):
+    d = inputs(60 + dk, sum(lens), H, Hk, dk, dv, "bf16", gate, n=len(lens))
+    o, final = kda.lin_prefill(d["q"], d["k"], d["v"], offsets(lens), g=d["g"], slope=d["slope"], scale=dk ** -0.5,
+                               initial_state=d["state"])
+    check_prefill(d, lens, H, dk, "bf16", o, final, dk ** -0.5)
+
+
+def test_prefill_long_slots_in_place():
+    lens, slots, H, dk = [2500, 40, 1200, 0], [4, -1, 0, 2], 2, 64
+    T = sum(lens)
+    d = inputs(71, T, H, H, dk, dk, "bf16", "g", n=6)
+    pool = d["state"].clone()
+    o = torch.full((T, H, dk), 7.0, device="cuda", dtype=torch.bfloat16)
+    call = kda.LinPrefill(d["q"], d["k"], d["v"], offsets(lens), g=d["g"], initial_state=pool, final_state=pool, o=o,
+                          state_slots=torch.tensor(slots, device="cuda", dtype=torch.int32))
+    call.run()
+    check_prefill(d, lens, H, dk, "bf16", o, pool, 1.0, slots)
+    assert call.device_status() == 0 and bool((o[2500:2540] == 7).all())
+    for row in (1, 2, 3, 5):
+        assert torch.equal(pool[row], d["state"][row])
+
+
+def test_prefill_many_sequences():
+    """More chains than the CTAs take at once; a long prompt among short ones."""
+    lens = [(37 * i) % 300 for i in range(90)] + [2000]
+    d = inputs(81, sum(lens), 4, 2, 64, 64, "bf16", "g")
+    o, final = kda.lin_prefill(d["q"], d["k"], d["v"], offsets(lens), g=d["g"])
+    check_prefill(d, lens, 4, 64, "bf16", o, final, 1.0)
+
+
+@pytest.mark.parametrize("H", [2, 40])
+def test_prefill_long_values_that_are_not_finite(H):
+    lens, dk = [2600, 400], 64
+    d = inputs(14, 3000, H, H, dk, dk, "bf16", "g")
+    clean, fc = kda.lin_prefill(d["q"], d["k"], d["v"], offsets(lens), g=d["g"])
+    d["v"][60, 0, 5] = float("inf")
+    d["v"][2500, 1, 9] = float("nan")
+    o, final = kda.lin_prefill(d["q"], d["k"], d["v"], offsets(lens), g=d["g"])
+    same = torch.ones(3000, H, dk, dtype=torch.bool, device="cuda")
+    same[60:2600, 0, 5] = same[2500:2600, 1, 9] = False
+    assert torch.equal(o[same], clean[same]) and not torch.isfinite(o[~same].float()).any()
+    cols = torch.ones(2, H, dk, dk, dtype=torch.bool, device="cuda")
+    cols[0, 0, :, 5] = cols[0, 1, :, 9] = False
+    assert torch.equal(final[cols], fc[cols]) and not torch.isfinite(final[~cols]).any()
+
+
+def test_prefill_long_malformed_offsets():
+    """What two sequences that overlap between malformed ones add up to is refused past the call's room."""
+    H, dk, T = 2, 64, 2560
+    d = inputs(32, T, H, H, dk, dk, "bf16", "g")
+    cut = torch.tensor([0, T, 100, T, 200, T], device="cuda")
+    final = torch.full((5, H, dk, dk), 7.0, device="cuda")
+    call = kda.LinPrefill(d["q"], d["k"], d["v"], cut, g=d["g"], final_state=final).run()
+    assert call.device_status() == 1
+    loga = log_alpha(d["g"], None, T, H)
+    _, _, S, A = walk(None, spread(d["k"], H), d["v"].double(), loga,
+                      torch.zeros(H, dk, dk, device="cuda", dtype=torch.float64), 1.0, range(T))
+    close(final[0], S, A, "bf16", T, dk, 0, state=True)
+    assert all(bool((final[s] == 7).all()) for s in (1, 3))
+
+
+def test_prefill_long_same_bits_every_time_and_in_a_graph():
+    lens, H = [2500, 1300], 4
+    d = inputs(18, sum(lens), H, 2, 128, 128, "bf16", "both", n=2)
+    call = kda.LinPrefill(d["q"], d["k"], d["v"], offsets(lens), g=d["g"], slope=d["slope"], initial_state=d["state"]).run()
+    o, f = call.o.clone(), call.final_state.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        call.run(side)
+    for _ in range(3):
+        call.o.zero_()
+        call.final_state.zero_()
+        call.workspace.fill_(255)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(call.o, o) and torch.equal(call.final_state, f)
+    assert call.device_status() == 0
+
+
 # ------------------------------------------------------------------ single tokens
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("dk,dv", SIZES)
