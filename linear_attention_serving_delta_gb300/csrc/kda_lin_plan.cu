@@ -63,6 +63,7 @@ __global__ void __launch_bounds__(kPlanThreads) lin_plan(const LinParams p, cons
   // chunks and records
   auto chunks_of = [](const LinSeq& q) { return (int32_t)((q.len + kLinChunk - 1) / kLinChunk); };
   int64_t chunks = 0, active = 0, total;
+  int32_t mine_n = 0;  // the thread's first sequence, for the search below
   for (int base = 0; base < p.num_seqs; base += kPlanThreads) {
     const int s = base + tid;
     LinSeq q{};
@@ -78,6 +79,7 @@ __global__ void __launch_bounds__(kPlanThreads) lin_plan(const LinParams p, cons
     if (q.flag) attn_flag(p.status, q.flag);
     if (s < p.num_seqs) a.seq_rec[s] = q.ok ? (int32_t)rec : -1;
     active += __syncthreads_count(q.ok);
+    if (base == 0) mine_n = q.ok ? max(n, 1) : 0;
   }
   // chunks of a segment: the least with which all chains fit the CTAs at once, or where
   // there are more chains than CTAs twice a CTA's share, so that only what would
@@ -88,8 +90,8 @@ __global__ void __launch_bounds__(kPlanThreads) lin_plan(const LinParams p, cons
       int64_t lo = kLinMinSegment, hi = chunks > kLinMinSegment ? chunks : kLinMinSegment;
       while (lo < hi) {
         const int64_t mid = (lo + hi) >> 1;
-        int64_t x = 0;
-        for (int s = tid; s < p.num_seqs; s += kPlanThreads)
+        int64_t x = (mine_n + mid - 1) / mid;
+        for (int s = tid + kPlanThreads; s < p.num_seqs; s += kPlanThreads)
           if (a.seq_rec[s] >= 0) x += max((int64_t)1, (chunks_of(lin_seq(p, s)) + mid - 1) / mid);
         scan(x, part, &total);
         if (total * per <= kLinSlots) hi = mid;
@@ -172,7 +174,7 @@ __global__ void __launch_bounds__(kPlanThreads) lin_plan(const LinParams p, cons
   }
 }
 
-// A CTA per chunk, a warp for every eighth head
+// A CTA per chunk and eight heads, a warp each
 __global__ void __launch_bounds__(256) lin_gates(const LinParams p, const LinPlan a, LinGates* records) {
   pdl_launch_dependents();
   pdl_wait();
@@ -197,8 +199,8 @@ __global__ void __launch_bounds__(256) lin_gates(const LinParams p, const LinPla
   const LinSeq q = lin_seq(p, found);
   const int64_t c = x - a.seq_rec[found];
   if (c * kLinChunk >= q.len) return;
-  for (int h = threadIdx.x >> 5; h < p.H; h += 8)
-    make_gates(p, q.tok0, (int)q.len, (int)(c * kLinChunk), h, &records[x * p.H + h]);
+  const int h = blockIdx.y * 8 + (threadIdx.x >> 5);
+  if (h < p.H) make_gates(p, q.tok0, (int)q.len, (int)(c * kLinChunk), h, &records[x * p.H + h]);
 }
 
 // Start states of segments 2, 3, ...: a thread four elements
@@ -278,7 +280,7 @@ cudaError_t launch_lin_plan(const LinParams& p, const LinPlan& a, cudaStream_t s
   return launch_maybe_dependent(true, lin_plan, dim3(1), dim3(kPlanThreads), 0, stream, p, a);
 }
 cudaError_t launch_lin_gates(const LinParams& p, const LinPlan& a, LinGates* records, cudaStream_t stream) {
-  return launch_maybe_dependent(true, lin_gates, dim3((unsigned)a.max_records), dim3(256), 0, stream, p, a, records);
+  return launch_maybe_dependent(true, lin_gates, dim3((unsigned)a.max_records, (unsigned)((p.H + 7) / 8)), dim3(256), 0, stream, p, a, records);
 }
 cudaError_t launch_lin_combine(const LinParams& p, const LinPlan& a, const LinGates* records, float* states,
                                cudaStream_t stream) {

@@ -100,12 +100,12 @@ __device__ __forceinline__ bool chain_at(const LinParams& p, const LinTcArgs& a,
     *ch = b->only;
     return i == 0 && ch->len >= 0;
   }
-  const int64_t w = nth_item(i);
-  if (w >= b->num_items) return false;
-  const int per = p.H * a.tiles, r = (int)(w % per);
-  *ch = a.items[w / per];
-  ch->head = r / a.tiles;
-  ch->tile = r % a.tiles;
+  const uint32_t g = gridDim.x, c = blockIdx.x, w = (uint32_t)i * g + ((i & 1) ? g - 1 - c : c);  // (see nth_item)
+  if (w >= (uint32_t)b->num_items) return false;
+  const uint32_t per = (uint32_t)(p.H * a.tiles), pair = w / per, r = w - pair * per;
+  *ch = a.items[pair];
+  ch->head = (int32_t)(r >> a.tile_shift);
+  ch->tile = (int32_t)(r & ((1u << a.tile_shift) - 1));
   return true;
 }
 // Without a plan CTA b takes chain b of sequence, head, tile (len -1: skipped)
@@ -121,30 +121,38 @@ __device__ __forceinline__ LinItem own_chain(const LinParams& p, const LinTcArgs
   return LinItem{(int32_t)seq.tok0, ok ? (int32_t)seq.len : -1, r / a.tiles, r % a.tiles, p.state_in ? row : -1,
                  p.state_out ? row : -1, (int32_t)rec, -1};
 }
-// wait_or_dead for a whole warp.  The hint lets the hardware hold the warp for up to
-// 10 us at a time: 20 warps that poll took half of the SM's issue slots.
+// Waits for `parity` of `bar`, for a second of an SM's fastest clock at most; false, with
+// *dead set, once that is over.  Few instructions, as 20 warps do it (a time limit of
+// try_wait's own makes the compiler sleep between polls, and wake late).
+constexpr uint32_t kWaitClocks = 2070000000u;
 __device__ __forceinline__ bool mbar_hold(uint64_t* bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 t, u;\n\t"
+      "mov.u32 t, %%clock;\n"
+      "WAIT_%=:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra DONE_%=;\n\t"
+      "mov.u32 u, %%clock;\n\t"
+      "sub.u32 u, u, t;\n\t"
+      "setp.lt.u32 q, u, %3;\n\t"
+      "@q bra WAIT_%=;\n"
+      "DONE_%=:\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}\n"
       : "=r"(done)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(10000u)
+      : "r"(smem_u32(bar)), "r"(parity), "n"(kWaitClocks)
       : "memory");
   return done != 0;
 }
+__device__ __forceinline__ bool thread_wait(uint64_t* bar, uint32_t parity, uint32_t* dead) {
+  if (mbar_hold(bar, parity)) return true;
+  *reinterpret_cast<volatile uint32_t*>(dead) = 1;
+  return false;
+}
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t* dead) {
   if (__all_sync(0xffffffffu, mbar_hold(bar, parity))) return true;
-  const uint64_t t0 = globaltimer_ns();
-#pragma unroll 1
-  while (!__all_sync(0xffffffffu, mbar_hold(bar, parity))) {
-    if (__any_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(dead) != 0 || globaltimer_ns() - t0 > kWaitLimitNs)) {
-      *reinterpret_cast<volatile uint32_t*>(dead) = 1;
-      return false;
-    }
-  }
-  return true;
+  *reinterpret_cast<volatile uint32_t*>(dead) = 1;
+  return false;
 }
 // Whether token `token` of a chain has one before or at it; n: the CTA's chunks before the chain
 __device__ __forceinline__ bool nan_at(const Tail* b, int channel, uint32_t n, int token) {
@@ -235,24 +243,24 @@ __device__ void copy_role(const LinParams& p, const LinTcArgs& a, const CUtensor
     for (int t = 0; t < ch.len; t += C) {
       prefetch(t + kAhead * C);
       const uint32_t st = ring.st, g = ng & 1;
-      if (!(ok = wait_or_dead(&b->g_free[g], ((ng >> 1) & 1) ^ 1, &b->dead))) break;
+      if (!(ok = thread_wait(&b->g_free[g], ((ng >> 1) & 1) ^ 1, &b->dead))) break;
       mbar_arrive_expect_tx(&b->g_full[g], sizeof(LinGateHead));
       bulk_g2s(&b->gates[g], &a.records[((int64_t)ch.rec + t / C) * p.H + ch.head].head, sizeof(LinGateHead), &b->g_full[g]);
       ++ng;
-      if (!(ok = wait_or_dead(&b->k_empty[st], ring.ph ^ 1, &b->dead))) break;
+      if (!(ok = thread_wait(&b->k_empty[st], ring.ph ^ 1, &b->dead))) break;
       mbar_arrive_expect_tx(&b->k_full[st], S::kQK);
 #pragma unroll
       for (int c = 0; c < DK / 64; ++c)
         tma_3d(sm + S::kK + st * S::kQK + c * kBlock, mk, 64 * c, kh, ch.tok0 + t, &b->k_full[st]);
       ++n;
-      if (!(ok = wait_or_dead(&b->v_empty[st], ring.ph ^ 1, &b->dead))) break;
+      if (!(ok = thread_wait(&b->v_empty[st], ring.ph ^ 1, &b->dead))) break;
       mbar_arrive_expect_tx(&b->v_full[st], S::kVb);
 #pragma unroll
       for (int c = 0; c < DV / 64; ++c)
         tma_3d(sm + S::kV + st * S::kVb + c * kBlock, mv, ch.tile * DV + 64 * c, ch.head, ch.tok0 + t, &b->v_full[st]);
       ++nv;
       if (!kLocal) {
-        if (!(ok = wait_or_dead(&b->q_empty[st], ring.ph ^ 1, &b->dead))) break;
+        if (!(ok = thread_wait(&b->q_empty[st], ring.ph ^ 1, &b->dead))) break;
         mbar_arrive_expect_tx(&b->q_full[st], S::kQK);
 #pragma unroll
         for (int c = 0; c < DK / 64; ++c)
@@ -400,7 +408,7 @@ __device__ __forceinline__ bool look_through(char* vt, int r, int live, int chai
 #pragma unroll 1
     for (int c = 0; c < P; ++c) *reinterpret_cast<uint4*>(vt + sw_off(r, c, kBlock)) = make_uint4(0, 0, 0, 0);
   } else {
-#pragma unroll 8
+#pragma unroll 4
     for (int c = 0; c < P; ++c) seen |= exponents_full(*reinterpret_cast<const uint4*>(vt + sw_off(r, c, kBlock)));
   }
   if (__any_sync(0xffffffffu, (seen & 0x80008000u) != 0)) {
@@ -454,36 +462,28 @@ __device__ void weight_role(const LinParams& p, const LinTcArgs& a, char* sm, Ta
       if (row == 0) b->scaled_q = strong;
       if (!strong) {
         // 2^{-G_j} P_ij for j <= i; 64 columns at a time, over columns that have been read
-        auto convert = [&](int c, auto masked) {
-          float x[64];
+#pragma unroll 1
+        for (int c = 0; c < C; c += 64) {
           uint32_t pk[32];
-          tmem_ld32(tp + c, x);
-          tmem_ld32(tp + c + 32, x + 32);
-          tmem_ld_wait();
+          if (c <= 32 * warp) {
+            float x[64];
+            tmem_ld32(tp + c, x);
+            tmem_ld32(tp + c + 32, x + 32);
+            tmem_ld_wait();
+            const int last = row - c;
 #pragma unroll
-          for (int u = 0; u < 64; u += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(&gh.col[c + u]);
-            float2 y = mul2(make_float2(x[u], x[u + 1]), make_float2(f.x, f.y)),
-                   z = mul2(make_float2(x[u + 2], x[u + 3]), make_float2(f.z, f.w));
-            if (decltype(masked)::value) {
-              const int last = row - c - u;
-              y = make_float2(last >= 0 ? y.x : 0.f, last >= 1 ? y.y : 0.f);
-              z = make_float2(last >= 2 ? z.x : 0.f, last >= 3 ? z.y : 0.f);
+            for (int u = 0; u < 64; u += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(&gh.col[c + u]);
+              const float2 y = mul2(make_float2(x[u], x[u + 1]), make_float2(f.x, f.y)),
+                           z = mul2(make_float2(x[u + 2], x[u + 3]), make_float2(f.z, f.w));
+              pk[u / 2] = tc::pack2(last >= u ? y.x : 0.f, last >= u + 1 ? y.y : 0.f);
+              pk[u / 2 + 1] = tc::pack2(last >= u + 2 ? z.x : 0.f, last >= u + 3 ? z.y : 0.f);
             }
-            pk[u / 2] = pack2(y);
-            pk[u / 2 + 1] = pack2(z);
+          } else {
+#pragma unroll
+            for (int u = 0; u < 32; ++u) pk[u] = 0;
           }
           tmem_st32(tp + c / 2, pk);
-        };
-        if (warp >= 2) {
-          convert(0, std::false_type{});
-          convert(64, std::true_type{});
-        } else {
-          convert(0, std::true_type{});
-          uint32_t pk[32];
-#pragma unroll
-          for (int u = 0; u < 32; ++u) pk[u] = 0;
-          tmem_st32(tp + 32, pk);
         }
       } else {
         // 2^{G_i - G_j}.  For an earlier block of 32 tokens as 2^{G_i - G_e} 2^{G_e - G_j},
@@ -908,6 +908,7 @@ cudaError_t launch_shape(const LinParams& p, void* ws, cudaStream_t stream) {
   const LinLayout L = lin_layout(p);
   LinTcArgs a{};
   a.tiles = (p.dv + DV - 1) / DV;
+  a.tile_shift = a.tiles == 4 ? 2 : a.tiles - 1;
   a.records = reinterpret_cast<LinGates*>(w + L.records);
   a.max_records = lin_max_records(p);
   auto run = [&](auto kernel, int64_t ctas) {

@@ -57,7 +57,8 @@ struct LinTcArgs {
   float* states;           // [places][H][dk][dv]
   LinGates* records;       // [max_records][H]
   int64_t max_records;
-  int32_t tiles;           // column tiles of a head
+  int32_t tiles;           // column tiles of a head: 1, 2 or 4
+  int32_t tile_shift;
 };
 
 // What the plan leaves in the workspace
