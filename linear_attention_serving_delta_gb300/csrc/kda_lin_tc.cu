@@ -31,9 +31,8 @@
 // Shared memory is what an SM runs short of: its copies, the MMAs' operands and the
 // threads' accesses are 480 KB a chunk at 128 x 128 (3,750 cycles at 128 bytes each)
 // beside the 5,500 that HBM takes for the chunk's 128 KB.  Hence A from TMEM wherever
-// a thread has to rewrite the operand anyway, and the outputs' rows through the
-// query tile, which is done with by then (32-byte pieces of rows straight to
-// global memory took 2,700 cycles a chunk).
+// a thread has to rewrite the operand anyway, and the outputs go through the value
+// tile, which is needed again last.
 //
 // Values that are not finite.  P~ is exactly 0 at later tokens, which would
 // still turn their infinities and NaN into NaN: V's are taken out in shared
@@ -68,20 +67,19 @@ struct Shape {
   static constexpr uint32_t kTail = kS + kSop;
   static constexpr uint32_t kBytes = kTail + 3072;
   static constexpr int kSCols = MB == 1 ? DV / 2 : DV;     // columns of a state thread
-  // K~ goes through TMEM kTok tokens of one row tile at a time
-  static constexpr int kTok = MB == 1 ? C : C / 2, kPhases = MB * (C / kTok);
-  // TMEM columns: P (P~ over its first half, Q~ over its second or behind it), O, K~^T V,
-  // then hi and lo, twice where there is room
+  // K~ goes through TMEM half a chunk of one row tile at a time, a place for each half
+  // where there is room: one is made while the other is multiplied
+  static constexpr int kTok = C / 2, kPhases = 2 * MB, kKBuf = MB == 1 ? 2 : 1;
+  // TMEM columns: P (P~ over its first half, Q~ over its second or behind it), O, K~^T V, hi and lo
   static constexpr int tP = 0, tQ = DK <= 128 ? 64 : C, tO = DK <= 128 ? C : C + DK / 2, tKV = tO + DV,
                        tHi = tKV + MB * DV, tLo = tHi + kTok / 2;
-  static constexpr int kKBuf = kPhases == 1 && tHi + 2 * kTok <= (int)kTmemCols ? 2 : 1;
-  static_assert(tLo + kTok / 2 <= (int)kTmemCols && kStages >= 1 && kBytes <= 232448, "fits an SM");
+  static_assert(tHi + kKBuf * kTok <= (int)kTmemCols && kStages >= 1 && kBytes <= 232448, "fits an SM");
 };
 
 struct Tail {
-  uint64_t q_full[4], k_full[4], v_full[4], v_ready[4], q_empty[4], k_empty[4], v_empty[4];
-  uint64_t p_full, o_full, kv_full;                        // committed by the MMA warp
-  uint64_t s_ready, p_ready, k_ready, o_free, g_full[2], g_free[2], drain[2];
+  uint64_t q_full[4], k_full[4], v_full[4], v_ready[4], q_empty[4], k_empty[4], v_done[4], v_empty[4];
+  uint64_t p_full, o_full, kv_full[2];                     // committed by the MMA warps
+  uint64_t s_ready, p_ready, k_ready[2], o_free, g_full[2], g_free[2], drain[2];
   uint32_t dead, tmem;
   int32_t poisoned;       // the CTA's chain that nan_from speaks of, -1: none so far
   int32_t scaled_q;       // the chunk is strong, for the MMAs
@@ -326,7 +324,7 @@ __device__ void mma_out_role(const LinParams& p, const LinTcArgs& a, const CUten
 #pragma unroll 1
         for (int s = 0; s < C / 16; ++s)
           mma_bf16_ts(tmem + S::tO, tmem + S::tP + s * 8, vd + (uint64_t)(s * (2048 >> 4)), id_n, s > 0);
-        mma_commit(&b->v_empty[ring.st]);
+        mma_commit(&b->v_done[ring.st]);
       }
       if (!(ok = wait(&b->s_ready, n & 1))) break;
       fence_after_sync();
@@ -342,6 +340,7 @@ __device__ void mma_out_role(const LinParams& p, const LinTcArgs& a, const CUten
           }
         }
         mma_commit(&b->o_full);
+        mma_commit(&b->q_empty[ring.st]);
       }
       ring.next();
     }
@@ -352,7 +351,7 @@ __device__ void mma_out_role(const LinParams& p, const LinTcArgs& a, const CUten
 }
 
 // Those of the state: K~^T V from zero, lo and hi in turn
-template <int DK, int DV>
+template <int DK, int DV, bool kLocal>
 __device__ void mma_state_role(const LinParams& p, const LinTcArgs& a, char* sm, Tail* b) {
   using S = Shape<DK, DV>;
   const uint32_t tmem = __shfl_sync(0xffffffffu, b->tmem, 0);
@@ -372,20 +371,20 @@ __device__ void mma_state_role(const LinParams& p, const LinTcArgs& a, char* sm,
       if (!(ok = wait(&b->v_ready[ring.st], ring.ph))) break;
 #pragma unroll 1
       for (int ph = 0; ph < S::kPhases; ++ph, ++n) {
-        if (!(ok = wait(&b->k_ready, n & 1))) break;
+        if (!(ok = wait(&b->k_ready[n & 1], (n >> 1) & 1))) break;
         fence_after_sync();
         if (issue) {
           constexpr int kPer = C / S::kTok;
           const int tok = ph % kPer * S::kTok;
-          const uint32_t buf = tmem + (S::kKBuf == 2 ? (n & 1) * S::kTok : 0);
+          const uint32_t buf = tmem + (n & (S::kKBuf - 1)) * S::kTok;
 #pragma unroll 1
           for (int s = 0; s < S::kTok / 16; ++s) {
             const uint64_t vs = vd + (uint64_t)((tok / 16 + s) * (2048 >> 4));
             mma_bf16_ts(tmem + S::tKV + ph / kPer * DV, buf + S::tLo + s * 8, vs, id_n, tok > 0 || s > 0);
             mma_bf16_ts(tmem + S::tKV + ph / kPer * DV, buf + S::tHi + s * 8, vs, id_n, 1);
           }
-          mma_commit(&b->kv_full);
-          if (ph + 1 == S::kPhases) mma_commit(&b->v_empty[ring.st]);
+          mma_commit(&b->kv_full[n & 1]);
+          if (ph + 1 == S::kPhases) mma_commit(kLocal ? &b->v_empty[ring.st] : &b->v_done[ring.st]);
         }
       }
       ring.next();
@@ -412,7 +411,7 @@ __device__ __forceinline__ bool look_through(char* vt, int r, int live, int chai
     for (int c = 0; c < P; ++c) seen |= exponents_full(*reinterpret_cast<const uint4*>(vt + sw_off(r, c, kBlock)));
   }
   if (__any_sync(0xffffffffu, (seen & 0x80008000u) != 0)) {
-    if (!warp_wait(&b->k_ready, (n * S::kPhases) & 1, &b->dead)) return false;
+    if (!warp_wait(&b->k_ready[0], (n * S::kPhases >> 1) & 1, &b->dead)) return false;
     if (!kLocal && n > 0 && !warp_wait(&b->o_free, (n - 1) & 1, &b->dead)) return false;
     if (seen & 0x80008000u) {
 #pragma unroll 1
@@ -568,73 +567,65 @@ __device__ void out_role(const LinParams& p, const LinTcArgs& a, const CUtensorM
     for (int t = 0; t < ch.len; t += C, rec += p.H) {
       const float own = rec->row[row];
       const int32_t strong = rec->head.strong;
-      char* qt = sm + ring.st * S::kQK;
+      char* vt = sm + S::kV + ring.st * S::kVb;
       if (!warp_wait(&b->o_full, n & 1, &b->dead)) return;
       fence_after_sync();
       const int live = min(C, ch.len - t) - 32 * warp;  // rows of the warp that are tokens
       const bool poisoned = *reinterpret_cast<volatile int32_t*>(&b->poisoned) == i;
-      // Through the warp's rows of the query tile, which nothing reads any more, as
-      // many blocks of 64 channels as it has: then whole rows of them to global memory
-      constexpr int kHold = DV < DK ? DV : DK;
       const float f = p.scale * (strong ? 1.f : own);
       const float2 f2 = make_float2(f, f);
+      // Through the warp's rows of the value tile, once no product reads it any more
+      if (!warp_wait(&b->v_done[ring.st], ring.ph, &b->dead)) return;
 #pragma unroll 1
-      for (int c0 = 0; c0 < DV; c0 += kHold) {
-        __syncwarp();
-#pragma unroll 1
-        for (int c = 0; c < kHold && c < DV; c += 64) {
-          float x[64];
-          tmem_ld32(to + c0 + c, x);
-          tmem_ld32(to + c0 + c + 32, x + 32);
-          tmem_ld_wait();
-          if (c0 + c + 64 == DV) {
-            fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&b->o_free);
-          }
-#pragma unroll
-          for (int u = 0; u < 64; u += 8) {
-            uint32_t pk[4];
-#pragma unroll
-            for (int z = 0; z < 4; ++z) pk[z] = pack2(mul2(make_float2(x[u + 2 * z], x[u + 2 * z + 1]), f2));
-            *reinterpret_cast<uint4*>(qt + sw_off(row, (c + u) / 8, kBlock)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-          }
+      for (int c = 0; c < DV; c += 64) {
+        float x[64];
+        tmem_ld32(to + c, x);
+        tmem_ld32(to + c + 32, x + 32);
+        tmem_ld_wait();
+        if (c + 64 == DV) {
+          fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&b->o_free);
         }
-        if (poisoned)
-#pragma unroll 1
-          for (int u = 0; u < kHold; ++u)
-            if (nan_at(b, c0 + u, n - t / C, t + row))
-              *reinterpret_cast<uint16_t*>(qt + sw_off(row, u / 8, kBlock) + 2 * (u % 8)) = 0x7fff;
-        fence_async_smem();
-        __syncwarp();
-        constexpr int kB = kHold / 64;
-        if (live >= 32) {
-          // 32 rows of 64 channels a copy (stores of the threads took 2,700 cycles a chunk)
-          if (lane == 0) {
 #pragma unroll
-            for (int c = 0; c < kB; ++c)
-              if (c0 + 64 * c < width)
-                tma_store_3d(mo, qt + c * kBlock + warp * 4096, ch.tile * DV + c0 + 64 * c, ch.head,
-                             ch.tok0 + t + 32 * warp);
-            bulk_commit();
-            bulk_wait_read_all();
-          }
-          __syncwarp();
-        } else {
-          const int piece = lane & 7, r0 = lane >> 3;
-          __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) +
-                             ((int64_t)(ch.tok0 + t + 32 * warp + r0) * p.H + ch.head) * p.dv + ch.tile * DV + c0 + 8 * piece;
-#pragma unroll 1
-          for (int r = r0; r < live; r += 4, o += 4 * stride)
+        for (int u = 0; u < 64; u += 8) {
+          uint32_t pk[4];
 #pragma unroll
-            for (int c = 0; c < kB; ++c)
-              if (c0 + 64 * c + 8 * piece < width)
-                *reinterpret_cast<uint4*>(o + 64 * c) =
-                    *reinterpret_cast<const uint4*>(qt + sw_off(32 * warp + r, 8 * c + piece, kBlock));
-          __syncwarp();
+          for (int z = 0; z < 4; ++z) pk[z] = pack2(mul2(make_float2(x[u + 2 * z], x[u + 2 * z + 1]), f2));
+          *reinterpret_cast<uint4*>(vt + sw_off(row, (c + u) / 8, kBlock)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
         }
       }
-      if (lane == 0) mbar_arrive(&b->q_empty[ring.st]);
+      if (poisoned)
+#pragma unroll 1
+        for (int u = 0; u < DV; ++u)
+          if (nan_at(b, u, n - t / C, t + row))
+            *reinterpret_cast<uint16_t*>(vt + sw_off(row, u / 8, kBlock) + 2 * (u % 8)) = 0x7fff;
+      fence_async_smem();
+      __syncwarp();
+      if (live >= 32) {
+        // 32 rows of 64 channels a copy (stores of the threads took 2,700 cycles a chunk)
+        if (lane == 0) {
+#pragma unroll
+          for (int c = 0; c < DV; c += 64)
+            if (c < width)
+              tma_store_3d(mo, vt + c / 64 * kBlock + warp * 4096, ch.tile * DV + c, ch.head, ch.tok0 + t + 32 * warp);
+          bulk_commit();
+          bulk_wait_read_all();
+        }
+      } else {
+        const int piece = lane & 7, r0 = lane >> 3;
+        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) +
+                           ((int64_t)(ch.tok0 + t + 32 * warp + r0) * p.H + ch.head) * p.dv + ch.tile * DV + 8 * piece;
+#pragma unroll 1
+        for (int r = r0; r < live; r += 4, o += 4 * stride)
+#pragma unroll
+          for (int c = 0; c < DV; c += 64)
+            if (c + 8 * piece < width)
+              *reinterpret_cast<uint4*>(o + c) =
+                  *reinterpret_cast<const uint4*>(vt + sw_off(32 * warp + r, c / 8 + piece, kBlock));
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&b->v_empty[ring.st]);
       ring.next();
       ++n;
     }
@@ -681,7 +672,7 @@ __device__ void state_role(const LinParams& p, const LinTcArgs& a, char* sm, Tai
     LinDecay decay{0.f, true};
     // S <- decay S + K~^T V of the chunk before
     auto advance = [&]() -> bool {
-      if (!wait(&b->kv_full, (n * S::kPhases - 1) & 1)) return false;
+      if (!wait(&b->kv_full[1], ((n * S::kPhases - 1) >> 1) & 1)) return false;
       fence_after_sync();
       if (holds) {
         const float one = decay.near_one ? 1.f : 0.f;
@@ -734,7 +725,7 @@ __device__ void state_role(const LinParams& p, const LinTcArgs& a, char* sm, Tai
               lo[u] = pack2(fma2(make_float2(bf_lo(hi[u]), bf_hi(hi[u])), make_float2(-1.f, -1.f), f));
             }
             const uint32_t at = lanes + ((uint32_t)(16 * g) << 16) + half * (TH / 2) +
-                                (S::kKBuf == 2 ? (n & 1) * S::kTok : 0);
+                                (ph & (S::kKBuf - 1)) * S::kTok;
             tmem_st_16x128<TH / 8>(at + S::tHi, hi);
             tmem_st_16x128<TH / 8>(at + S::tLo, lo);
           }
@@ -747,31 +738,34 @@ __device__ void state_role(const LinParams& p, const LinTcArgs& a, char* sm, Tai
         next = lin_decay(b->gates[n & 1].total);
         return true;
       };
-      // with two buffers K~ beside the product of the chunk before, else behind it
+      // with two places the first half of K~ beside the product of the chunk before, else behind it
       if (S::kKBuf == 2) {
         if (!gates()) return;
+        if (t > 0 && !wait(&b->kv_full[0], (n - 1) & 1)) return;
+        fence_after_sync();
         make_k(0);
         if (t > 0 && !advance()) return;
       } else {
         if (t > 0 && !advance()) return;
         if (!gates()) return;
+        make_k(0);
       }
       decay = next;
 #pragma unroll 1
-      for (int ph = 0; ph < S::kPhases; ++ph) {
-        if (ph > 0) {
-          if (!wait(&b->kv_full, (n * S::kPhases + ph - 1) & 1)) return;
+      for (int ph = 0;;) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b->k_ready[ph & 1]);
+        if (++ph == S::kPhases) break;
+        // (the second half's place: its product of the chunk before is done, as the state has it)
+        if (S::kKBuf == 1) {
+          if (!wait(&b->kv_full[(ph - 1) & 1], ((n * S::kPhases + ph - 1) >> 1) & 1)) return;
           fence_after_sync();
         }
-        if (S::kKBuf == 1) make_k(ph);
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&b->k_ready);
-          if (ph + 1 == S::kPhases) {
-            mbar_arrive(&b->k_empty[ring.st]);
-            mbar_arrive(&b->g_free[n & 1]);
-          }
-        }
+        make_k(ph);
+      }
+      if (lane == 0) {
+        mbar_arrive(&b->k_empty[ring.st]);
+        mbar_arrive(&b->g_free[n & 1]);
       }
       // the state as an operand, once the product with the one before is done
       if (!kLocal) {
@@ -822,13 +816,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < 4; ++s) {
       for (uint64_t* x : {&b->q_full[s], &b->k_full[s], &b->v_full[s]}) mbar_init(x, 1);
       mbar_init(&b->v_ready[s], 4);
-      mbar_init(&b->q_empty[s], 4);
+      mbar_init(&b->q_empty[s], 1);
       mbar_init(&b->k_empty[s], kLocal ? 8 : 9);
-      mbar_init(&b->v_empty[s], kLocal ? 1 : 2);
+      mbar_init(&b->v_done[s], 2);
+      mbar_init(&b->v_empty[s], kLocal ? 1 : 4);
     }
-    for (uint64_t* x : {&b->p_full, &b->o_full, &b->kv_full, &b->drain[0], &b->drain[1], &b->g_full[0], &b->g_full[1]})
+    for (uint64_t* x : {&b->p_full, &b->o_full, &b->kv_full[0], &b->kv_full[1], &b->drain[0], &b->drain[1], &b->g_full[0], &b->g_full[1]})
       mbar_init(x, 1);
-    for (uint64_t* x : {&b->s_ready, &b->k_ready}) mbar_init(x, 8);
+    for (uint64_t* x : {&b->s_ready, &b->k_ready[0], &b->k_ready[1]}) mbar_init(x, 8);
     for (uint64_t* x : {&b->p_ready, &b->o_free}) mbar_init(x, 4);
     for (uint64_t* x : {&b->g_free[0], &b->g_free[1]}) mbar_init(x, kLocal ? 8 : 12);
     b->dead = 0;
@@ -866,7 +861,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
       if (!kLocal) mma_out_role<DK, DV>(p, a, &mo, sm, b);
     } else if (warp == 2) {
-      mma_state_role<DK, DV>(p, a, sm, b);
+      mma_state_role<DK, DV, kLocal>(p, a, sm, b);
     }
   } else if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
