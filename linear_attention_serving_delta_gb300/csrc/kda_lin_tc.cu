@@ -51,7 +51,6 @@ using namespace tc;
 constexpr int C = kLinChunk;
 constexpr int kThreads = 640;
 constexpr uint32_t kTmemCols = 512;
-constexpr int kAhead = 2;         // chunks that the prefetch into L2 is ahead
 constexpr uint32_t kBlock = C * 128;  // bytes of 64 channels of a tile
 
 template <int DK, int DV>
@@ -208,12 +207,6 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, const void* s
                "r"(z), "r"(smem_u32(src))
                : "memory");
 }
-// The same box as tma_3d's, into L2 alone
-__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* m, int x, int y, int z) {
-  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(m), "r"(x), "r"(y), "r"(z)
-               : "memory");
-}
-
 // ------------------------------------------------------------------ copies
 template <int DK, int DV, bool kLocal>
 __device__ void copy_role(const LinParams& p, const LinTcArgs& a, const CUtensorMap* mq, const CUtensorMap* mk,
@@ -225,21 +218,7 @@ __device__ void copy_role(const LinParams& p, const LinTcArgs& a, const CUtensor
   LinItem ch;
   for (int i = 0; ok && chain_at(p, a, b, i, &ch); ++i) {
     const int kh = ch.head / p.R;
-    // Tiles come to L2 two chunks before the stages have room for them: with two stages
-    // that are given back late HBM's latency would show in every chunk
-    auto prefetch = [&](int t) {
-      if (t >= ch.len) return;
-#pragma unroll 1
-      for (int c = 0; c < DK / 64; ++c) {
-        if (!kLocal) tma_prefetch_3d(mq, 64 * c, kh, ch.tok0 + t);
-        tma_prefetch_3d(mk, 64 * c, kh, ch.tok0 + t);
-      }
-#pragma unroll 1
-      for (int c = 0; c < DV / 64; ++c) tma_prefetch_3d(mv, ch.tile * DV + 64 * c, ch.head, ch.tok0 + t);
-    };
-    if (kAhead > 1) prefetch(C);
     for (int t = 0; t < ch.len; t += C) {
-      prefetch(t + kAhead * C);
       const uint32_t st = ring.st, g = ng & 1;
       if (!(ok = thread_wait(&b->g_free[g], ((ng >> 1) & 1) ^ 1, &b->dead))) break;
       mbar_arrive_expect_tx(&b->g_full[g], sizeof(LinGateHead));
