@@ -45,7 +45,7 @@ __device__ __forceinline__ LinSeq lin_seq(const LinParams& p, int32_t s) {
   LinSeq r;
   r.flag = 0;
   r.ok = false;
-  r.slot = s;
+  r.slot = p.slots ? p.slots[s] : s;  // (beside the offsets: one wait for all three)
   if (p.cu_seqlens) {
     r.tok0 = p.cu_seqlens[s];
     const int64_t end = p.cu_seqlens[s + 1];
@@ -63,7 +63,6 @@ __device__ __forceinline__ LinSeq lin_seq(const LinParams& p, int32_t s) {
     r.len = 1;
   }
   if (p.slots) {
-    r.slot = p.slots[s];
     if (r.slot < 0) return r;
     if (r.slot >= p.num_states) {
       r.flag = kFlagBadCache;

@@ -14,11 +14,14 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxDraft = KDA_LIN_MAX_DRAFT;
+constexpr int kLinSms = 152;
 
 // A CTA's slice of a state: DK x DVS elements, a float4 of VPT for each thread
-template <int DK, int DV>
+// (narrow: at most 32 columns, for calls too small to fill the GPU otherwise)
+template <int DK, int DV, bool kNarrow = false>
 struct Tile {
-  static constexpr int DVS = DK * DV > 16384 ? 16384 / DK : DV;  // columns
+  static constexpr int kWide = DK * DV > 16384 ? 16384 / DK : DV;
+  static constexpr int DVS = kNarrow && kWide > 32 ? 32 : kWide;  // columns
   static constexpr int QPR = DVS / 4;                            // float4 of a row
   static constexpr int NT = DK * QPR < kThreads ? DK * QPR : kThreads;
   static constexpr int NRG = NT / QPR;                           // rows that the threads cover at once
@@ -42,12 +45,14 @@ __device__ __forceinline__ void decay_all(LinDecay a, float4 (&s)[N]) {
 }
 
 // ------------------------------------------------------------------ decode
-template <typename T, int DK, int DV>
-__global__ void __launch_bounds__(Tile<DK, DV>::NT) lin_decode(const LinParams p) {
-  using L = Tile<DK, DV>;
+template <typename T, int DK, int DV, bool kNarrow>
+__global__ void __launch_bounds__(Tile<DK, DV, kNarrow>::NT) lin_decode(const LinParams p) {
+  using L = Tile<DK, DV, kNarrow>;
   __shared__ float sq[DK], sk[DK];
   __shared__ __align__(16) float sv[L::DVS];
   __shared__ __align__(16) float part[L::NRG][L::DVS];
+  pdl_launch_dependents();
+  pdl_wait();
   const int tid = threadIdx.x, row = blockIdx.x, h = blockIdx.y, c0 = blockIdx.z * L::DVS;
   const LinSeq seq = lin_seq(p, row);
   if (seq.flag && tid == 0 && h == 0 && c0 == 0) attn_flag(p.status, seq.flag);
@@ -100,76 +105,346 @@ __device__ __forceinline__ bool load_parents(const LinParams& p, const LinSeq& s
 
 // Commit.  Token j of the path contributes 2^{G_a - G_j} k_j v_j^T, G_a - G_j
 // being the sum of log2 alpha over what follows j on the path: taken from the
-// accepted token upwards, so that no difference of far sums appears.
-constexpr int kBatch = 16;  // tokens of the path in shared memory at a time
+// accepted token upwards, so that no difference of far sums appears.  Every warp
+// walks the path for itself, with the tokens' logarithms in its lanes; the keys
+// and values of the first kBatch tokens are on their way beside the state, whether
+// on the path or not (a wait for them behind the walk took a quarter of the time).
+constexpr int kBatch = 16;  // tokens in shared memory at a time
 
 template <typename T, int DK, int DV>
-__global__ void __launch_bounds__(Tile<DK, DV>::NT) lin_commit(const LinParams p) {
+__global__ void __launch_bounds__(Tile<DK, DV>::NT, 3) lin_commit(const LinParams p) {
   using L = Tile<DK, DV>;
   constexpr int kB = DK == 256 ? kBatch / 2 : kBatch;
   __shared__ float sk[kB][DK];
   __shared__ __align__(16) float sv[kB][L::DVS];
-  __shared__ float la[kMaxDraft], w[kMaxDraft];
-  __shared__ int8_t par[kMaxDraft], path[kMaxDraft];
-  __shared__ int32_t n_path;
-  __shared__ LinDecay decay;
-  const int tid = threadIdx.x, h = blockIdx.y, c0 = blockIdx.z * L::DVS;
+  __shared__ float la[kMaxDraft];
+  __shared__ int8_t par[kMaxDraft];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int tid = threadIdx.x, lane = tid & 31, h = blockIdx.y, c0 = blockIdx.z * L::DVS;
+  const int a = p.last[blockIdx.x];
   const LinSeq seq = lin_seq(p, blockIdx.x);
   const bool first = tid == 0 && h == 0 && c0 == 0;
   if (seq.flag && first) attn_flag(p.status, seq.flag);
   if (!seq.ok) return;
-  const int a = p.last[blockIdx.x];
-  const bool good = load_parents(p, seq, par) && a >= -1 && a < seq.len;
-  if (!good) {
-    if (first) attn_flag(p.status, kFlagBadCache);
-    return;
-  }
-  if (a < 0 && p.state_in == p.state_out) return;
+  const int n = (int)seq.len;
   const int cq = tid % L::QPR, rg = tid / L::QPR;
   const int64_t at = ((int64_t)seq.slot * p.H + h) * DK * DV + c0 + 4 * cq;
   float4 s[L::VPT];
+  const bool moves = a >= -1 && a < n && !(a < 0 && p.state_in == p.state_out);
+  if (moves)
 #pragma unroll
-  for (int i = 0; i < L::VPT; ++i) s[i] = *reinterpret_cast<const float4*>(p.state_in + at + (int64_t)(rg + i * L::NRG) * DV);
-  for (int i = tid; i <= a; i += L::NT) la[i] = lin_log2_alpha<T>(p, seq.tok0 + i, h);
-  __syncthreads();
-  if (tid == 0) {
-    int n = 0;
-    float sum = 0.f;
-    for (int j = a; j >= 0; j = par[j]) {
-      path[n] = (int8_t)j;
-      w[n++] = exp2f(sum);
-      sum += la[j];
-    }
-    n_path = n;
-    decay = lin_decay(sum);
+    for (int i = 0; i < L::VPT; ++i)
+      s[i] = *reinterpret_cast<const float4*>(p.state_in + at + (int64_t)(rg + i * L::NRG) * DV);
+  auto fetch = [&](int b) {  // tokens b .. b + kB - 1 up to the accepted one
+    const int m = min(kB, a + 1 - b);
+    for (int i = tid; i < m * DK; i += L::NT)
+      sk[i / DK][i % DK] = ld_in(static_cast<const T*>(p.k), ((seq.tok0 + b + i / DK) * p.Hk + h / p.R) * DK + i % DK);
+    for (int i = tid; i < m * L::DVS; i += L::NT)
+      sv[i / L::DVS][i % L::DVS] =
+          ld_in(static_cast<const T*>(p.v), ((seq.tok0 + b + i / L::DVS) * p.H + h) * DV + c0 + i % L::DVS);
+  };
+  if (moves) {
+    for (int i = tid; i <= a; i += L::NT) la[i] = lin_log2_alpha<T>(p, seq.tok0 + i, h);
+    fetch(0);
   }
-  __syncthreads();
-  const int n = n_path;
-  if (n > 0) decay_all(decay, s);
-  for (int b = n - 1; b >= 0; b -= kB) {  // from the root on
-    const int m = min(kB, b + 1);
-    for (int i = tid; i < m * DK; i += L::NT) {
-      const int j = i / DK, d = i % DK;
-      sk[j][d] = w[b - j] * ld_in(static_cast<const T*>(p.k), ((seq.tok0 + path[b - j]) * p.Hk + h / p.R) * DK + d);
+  if (!load_parents(p, seq, par) || a < -1 || a >= n) {
+    if (first) attn_flag(p.status, kFlagBadCache);
+    return;
+  }
+  if (!moves) return;
+  // the path, and of the lane's tokens (lane, lane + 32) the sum over what follows them
+  const float l0 = lane <= a ? la[lane] : 0.f, l1 = lane + 32 <= a ? la[lane + 32] : 0.f;
+  unsigned long long path = 0;
+  float sum = 0.f, w0 = 0.f, w1 = 0.f;
+  for (int j = a; j >= 0; j = par[j]) {
+    path |= 1ull << j;
+    if (lane == (j & 31)) (j < 32 ? w0 : w1) = sum;
+    sum += __shfl_sync(0xffffffffu, j < 32 ? l0 : l1, j & 31);
+  }
+  w0 = exp2f(w0);
+  w1 = exp2f(w1);
+  if (a >= 0) decay_all(lin_decay(sum), s);
+  for (int b = 0; b <= a; b += kB) {
+    if (b > 0) {
+      if (!(path >> b & ((1ull << kB) - 1))) continue;
+      __syncthreads();
+      fetch(b);
+      __syncthreads();
     }
-    for (int i = tid; i < m * L::DVS; i += L::NT) {
-      const int j = i / L::DVS, c = i % L::DVS;
-      sv[j][c] = ld_in(static_cast<const T*>(p.v), ((seq.tok0 + path[b - j]) * p.H + h) * DV + c0 + c);
-    }
-    __syncthreads();
-    for (int j = 0; j < m; ++j) {
-      const float4 v4 = *reinterpret_cast<const float4*>(&sv[j][4 * cq]);
+    for (int j = 0; j < kB; ++j) {
+      if (!(path >> (b + j) & 1)) continue;
+      const float w = __shfl_sync(0xffffffffu, b + j < 32 ? w0 : w1, (b + j) & 31);
+      const float4 v4 = mul4(w, *reinterpret_cast<const float4*>(&sv[j][4 * cq]));
 #pragma unroll
       for (int i = 0; i < L::VPT; ++i) s[i] = fma4(sk[j][rg + i * L::NRG], v4, s[i]);
     }
-    __syncthreads();
   }
 #pragma unroll
   for (int i = 0; i < L::VPT; ++i) *reinterpret_cast<float4*>(p.state_out + at + (int64_t)(rg + i * L::NRG) * DV) = s[i];
 }
 
-// Draft.  A CTA per (request, head, 32 columns): the columns of the state in
-// shared memory, a warp per token, lane = column.
+// Draft, bf16.  A CTA per (request, head), a warp per 32 columns of the state, on
+// mma.sync: up to MT tiles of 16 tokens as rows, so a 128-row tcgen05 tile would be
+// mostly padding, and the state is read once either way -- the kernel is bound by it.
+//
+// A product's contraction may run over its index in any order, so the fragments take
+// whole 16-byte loads: of a block of 16 key channels the thread's four slots are
+// channels 4 (l % 4) + 0..3, and of a warp's 32 columns column n of tile j is 4 n + j.
+// States are rounded to bf16 on the way; o = 2^{G_i} (Q S) in fp32, then + (weights) V
+// with the weights 2^{G_i - G_j} q.k of the token's path, 0 elsewhere, rounded to
+// bf16.  Values that are not finite are taken out before they meet a weight of 0
+// and make NaN of their channel in the tokens whose path holds them.
+__device__ __forceinline__ void mma16816(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ bool finite2(uint32_t w) { return (w & 0x7f80u) != 0x7f80u && (w & 0x7f800000u) != 0x7f800000u; }
+
+// Ancestors (itself included) and sums of log2 alpha along the path of every token
+struct Tree {
+  unsigned long long path[kMaxDraft];
+  LogSum G[kMaxDraft];
+  int8_t par[kMaxDraft];
+};
+// By doubling: after round r a token knows the 2^r nearest of its path.  For the whole
+// CTA, at least kMaxDraft threads or as many rounds over them.
+template <typename T>
+__device__ __forceinline__ bool make_tree(const LinParams& p, const LinSeq& seq, int h, Tree* t) {
+  const int n = (int)seq.len;
+  if (!load_parents(p, seq, t->par)) return false;
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    t->path[i] = 1ull << i;
+    t->G[i] = log_sum(lin_log2_alpha<T>(p, seq.tok0 + i, h));
+  }
+  __syncthreads();
+  constexpr int kPer = kMaxDraft / 32;  // tokens of a thread, at most
+  for (int d = 1; d < n; d *= 2) {
+    unsigned long long path[kPer];
+    LogSum G[kPer];
+    int8_t up[kPer];
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      const int i = threadIdx.x + u * blockDim.x;
+      if (i >= n) continue;
+      const int y = t->par[i];
+      path[u] = t->path[i];
+      G[u] = t->G[i];
+      up[u] = (int8_t)y;
+      if (y >= 0) {
+        path[u] |= t->path[y];
+        G[u] = G[u] + t->G[y];
+        up[u] = t->par[y];
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      const int i = threadIdx.x + u * blockDim.x;
+      if (i >= n) continue;
+      t->path[i] = path[u];
+      t->G[i] = G[u];
+      t->par[i] = up[u];
+    }
+    __syncthreads();
+  }
+  return true;
+}
+
+// Rows of queries, keys and values in shared memory are 32 bytes apart beyond their own
+// bytes: the fragments' 8-byte reads of eight rows then fall on different banks.
+constexpr int kRowPad = 16;  // elements
+
+template <int DK, int MT>
+__global__ void __launch_bounds__(256) lin_draft_mma(const LinParams p) {
+  using T = __nv_bfloat16;
+  constexpr int KB = DK / 16, NB = KB < 4 ? KB : 4;
+  extern __shared__ __align__(16) char dyn[];
+  __shared__ Tree tree;
+  __shared__ unsigned long long bad[256];  // tokens whose value is not finite, per column
+  __shared__ int32_t any_bad;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gi = lane >> 2, ti = lane & 3;
+  const int h = blockIdx.y, cb = 32 * warp + 4 * gi, co = 32 * warp + 8 * ti;  // columns: of loads, of outputs
+  const LinSeq seq = lin_seq(p, blockIdx.x);
+  const bool first = threadIdx.x == 0 && h == 0;
+  if (seq.flag && first) attn_flag(p.status, seq.flag);
+  if (!seq.ok || seq.len == 0) return;
+  const int n = (int)seq.len, mt = (n + 15) / 16;
+  constexpr int kPitch = DK + kRowPad;
+  const int pv = p.dv + kRowPad;
+  T *sq = reinterpret_cast<T*>(dyn), *sk = sq + 16 * MT * kPitch, *sv = sk + 16 * MT * kPitch;
+  const float* S = p.state_in + ((int64_t)seq.slot * p.H + h) * DK * p.dv + cb;
+  float4 s[NB][4];
+  auto load = [&](int k0) {
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        s[b][e] = cb < p.dv ? *reinterpret_cast<const float4*>(S + (int64_t)(16 * (k0 + b) + 4 * ti + e) * p.dv)
+                            : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  load(0);
+  // queries, keys and values of the request, rows behind it zero; 16 bytes at a time
+  for (int i = threadIdx.x; i < p.dv; i += blockDim.x) bad[i] = 0;
+  if (threadIdx.x == 0) any_bad = 0;
+  for (int i = threadIdx.x; i < 16 * mt * (DK / 8); i += blockDim.x) {
+    const int t = i / (DK / 8), c = i % (DK / 8) * 8;
+    const int64_t at = ((seq.tok0 + t) * p.Hk + h / p.R) * DK + c;
+    uint4 x = make_uint4(0, 0, 0, 0), y = x;
+    if (t < n) {
+      x = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + at);
+      y = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.k) + at);
+    }
+    *reinterpret_cast<uint4*>(sq + t * kPitch + c) = x;
+    *reinterpret_cast<uint4*>(sk + t * kPitch + c) = y;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 16 * mt * (p.dv / 8); i += blockDim.x) {
+    const int t = i / (p.dv / 8), c = i % (p.dv / 8) * 8;
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (t < n) x = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.v) + ((seq.tok0 + t) * p.H + h) * p.dv + c);
+    if (!finite2(x.x) || !finite2(x.y) || !finite2(x.z) || !finite2(x.w)) {
+      uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t ones = e & 1 ? 0x7f800000u : 0x7f80u;
+        if ((w[e / 2] & ones) != ones) continue;
+        atomicOr(&bad[c + e], 1ull << t);
+        w[e / 2] &= e & 1 ? 0xffffu : 0xffff0000u;
+      }
+      x = make_uint4(w[0], w[1], w[2], w[3]);
+      any_bad = 1;
+    }
+    *reinterpret_cast<uint4*>(sv + t * pv + c) = x;
+  }
+  if (!make_tree<T>(p, seq, h, &tree)) {  // (its barriers are those of the rows too)
+    if (first) attn_flag(p.status, kFlagBadCache);
+    return;
+  }
+  const bool found = any_bad != 0;
+  // four channels of a token's query or key
+  auto four = [&](const T* x, int tok, int kb) { return *reinterpret_cast<const uint2*>(x + tok * kPitch + 16 * kb + 4 * ti); };
+  float acc[MT][4][4];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[m][j][e] = 0.f;
+#pragma unroll
+  for (int k0 = 0; k0 < KB; k0 += NB) {
+    uint32_t b0[NB][4], b1[NB][4];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      b0[b][0] = pack2(s[b][0].x, s[b][1].x);
+      b1[b][0] = pack2(s[b][2].x, s[b][3].x);
+      b0[b][1] = pack2(s[b][0].y, s[b][1].y);
+      b1[b][1] = pack2(s[b][2].y, s[b][3].y);
+      b0[b][2] = pack2(s[b][0].z, s[b][1].z);
+      b1[b][2] = pack2(s[b][2].z, s[b][3].z);
+      b0[b][3] = pack2(s[b][0].w, s[b][1].w);
+      b1[b][3] = pack2(s[b][2].w, s[b][3].w);
+    }
+    if (k0 + NB < KB) load(k0 + NB);  // beside this part's products
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        if (m >= mt) continue;
+        const uint2 x = four(sq, 16 * m + gi, k0 + b), y = four(sq, 16 * m + gi + 8, k0 + b);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mma16816(acc[m][j], x.x, y.x, x.y, y.y, b0[b][j], b1[b][j]);
+      }
+  }
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    if (m >= mt) continue;
+    const int r0 = 16 * m + gi, r1 = r0 + 8;  // the thread's two tokens
+    const LogSum none{0.f, 0.f};
+    const LogSum g0 = r0 < n ? tree.G[r0] : none, g1 = r1 < n ? tree.G[r1] : none;
+    const unsigned long long p0 = r0 < n ? tree.path[r0] : 0, p1 = r1 < n ? tree.path[r1] : 0;
+    {
+      const float f0 = exp2f(g0.i + g0.f), f1 = exp2f(g1.i + g1.f);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        acc[m][j][0] *= f0;
+        acc[m][j][1] *= f0;
+        acc[m][j][2] *= f1;
+        acc[m][j][3] *= f1;
+      }
+    }
+    // sixteen earlier tokens at a time: their weights are the next product's fragments
+#pragma unroll 1
+    for (int t = 0; t <= m; ++t) {
+      float w[2][4];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[u][e] = 0.f;
+#pragma unroll 4
+      for (int kb = 0; kb < KB; ++kb) {
+        const uint2 x = four(sq, r0, kb), y = four(sq, r1, kb);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint2 z = four(sk, 16 * t + 8 * u + gi, kb);
+          mma16816(w[u], x.x, y.x, x.y, y.y, z.x, z.y);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int j = 16 * t + 8 * u + 2 * ti + (e & 1);
+          const bool on = ((e < 2 ? p0 : p1) >> j & 1) != 0;
+          w[u][e] = on ? w[u][e] * exp2f(log_diff(e < 2 ? g0 : g1, tree.G[j])) : 0.f;
+        }
+      // V: rows 2 ti, + 1, + 8, + 9 of the sixteen, the thread's four columns
+      uint2 v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        v[e] = cb < p.dv ? *reinterpret_cast<const uint2*>(sv + (16 * t + 2 * ti + (e & 1) + 8 * (e >> 1)) * pv + cb)
+                         : make_uint2(0, 0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t pick = j & 1 ? 0x7632u : 0x5410u;
+        const uint32_t b0 = __byte_perm(j < 2 ? v[0].x : v[0].y, j < 2 ? v[1].x : v[1].y, pick),
+                       b1 = __byte_perm(j < 2 ? v[2].x : v[2].y, j < 2 ? v[3].x : v[3].y, pick);
+        mma16816(acc[m][j], pack2(w[0][0], w[0][1]), pack2(w[0][2], w[0][3]), pack2(w[1][0], w[1][1]),
+                 pack2(w[1][2], w[1][3]), b0, b1);
+      }
+    }
+    // columns co .. co + 7 of the two tokens: n = 2 ti of the tiles, then n = 2 ti + 1
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int i = r ? r1 : r0;
+      if (i >= n || co >= p.dv) continue;
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x[j] = acc[m][j][2 * r] * p.scale;
+        x[4 + j] = acc[m][j][2 * r + 1] * p.scale;
+      }
+      if (found)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (bad[co + j] & (r ? p1 : p0)) x[j] = NAN;
+      *reinterpret_cast<uint4*>(static_cast<T*>(p.o) + ((seq.tok0 + i) * p.H + h) * p.dv + co) =
+          make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
+    }
+  }
+}
+
+// Draft in fp32, and where the tensors are not aligned.  A CTA per (request, head, 32
+// columns): the columns of the state in shared memory, a warp per token, lane = column.
 template <typename T, int DK>
 __global__ void __launch_bounds__(kThreads) lin_draft(const LinParams p) {
   constexpr int kCols = 32;
@@ -222,13 +497,17 @@ __global__ void __launch_bounds__(kThreads) lin_draft(const LinParams p) {
 }
 
 // ------------------------------------------------------------------ launches
+// Launched as the dependents of what is before them on the stream, as the cache's calls are
 template <typename T, int DK, int DV, bool kCommit>
 cudaError_t launch_state(const LinParams& p, cudaStream_t stream) {
   using L = Tile<DK, DV>;
-  const dim3 grid((unsigned)p.num_seqs, (unsigned)p.H, DV / L::DVS);
-  if (kCommit) lin_commit<T, DK, DV><<<grid, L::NT, 0, stream>>>(p);
-  else lin_decode<T, DK, DV><<<grid, L::NT, 0, stream>>>(p);
-  return cudaGetLastError();
+  using N = Tile<DK, DV, true>;
+  const dim3 grid((unsigned)p.num_seqs, (unsigned)p.H, DV / L::DVS), narrow(grid.x, grid.y, DV / N::DVS);
+  if (kCommit) return launch_maybe_dependent(true, lin_commit<T, DK, DV>, grid, dim3(L::NT), 0, stream, p);
+  // fewer CTAs than SMs (one row of 32 heads of 128 x 128: 6.1 us in whole states)
+  if (N::DVS < L::DVS && (int64_t)grid.x * grid.y * grid.z < kLinSms)
+    return launch_maybe_dependent(true, lin_decode<T, DK, DV, true>, narrow, dim3(N::NT), 0, stream, p);
+  return launch_maybe_dependent(true, lin_decode<T, DK, DV, false>, grid, dim3(L::NT), 0, stream, p);
 }
 template <typename T, int DK, bool kCommit>
 cudaError_t launch_dv(const LinParams& p, cudaStream_t stream) {
@@ -251,6 +530,19 @@ cudaError_t launch_dk(const LinParams& p, cudaStream_t stream) {
     case 256: return launch_dv<T, 256, kCommit>(p, stream);
   }
   return cudaErrorInvalidValue;
+}
+
+template <int DK>
+cudaError_t launch_draft_mma(const LinParams& p, cudaStream_t stream) {
+  const dim3 grid((unsigned)p.num_seqs, (unsigned)p.H);
+  const int threads = 32 * ((p.dv + 31) / 32);
+  auto run = [&](auto kernel, int tokens) {
+    const size_t smem = (size_t)tokens * (2 * (DK + kRowPad) + p.dv + kRowPad) * sizeof(__nv_bfloat16);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    return e != cudaSuccess ? e : launch_maybe_dependent(true, kernel, grid, dim3(threads), smem, stream, p);
+  };
+  return p.max_seqlen <= 16 ? run(lin_draft_mma<DK, 1>, 16)
+                            : p.max_seqlen <= 32 ? run(lin_draft_mma<DK, 2>, 32) : run(lin_draft_mma<DK, 4>, 64);
 }
 
 template <typename T>
@@ -276,6 +568,16 @@ cudaError_t launch_lin_commit(const LinParams& p, cudaStream_t stream) {
   return p.dt == KDA_BF16 ? launch_dk<__nv_bfloat16, true>(p, stream) : launch_dk<float, true>(p, stream);
 }
 cudaError_t launch_lin_draft(const LinParams& p, cudaStream_t stream) {
+  auto al16 = [](const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15) == 0; };
+  if (p.dt == KDA_BF16 && al16(p.q) && al16(p.k) && al16(p.v) && al16(p.o)) {
+    switch (p.dk) {
+      case 16: return launch_draft_mma<16>(p, stream);
+      case 32: return launch_draft_mma<32>(p, stream);
+      case 64: return launch_draft_mma<64>(p, stream);
+      case 128: return launch_draft_mma<128>(p, stream);
+      case 256: return launch_draft_mma<256>(p, stream);
+    }
+  }
   return p.dt == KDA_BF16 ? launch_draft_t<__nv_bfloat16>(p, stream) : launch_draft_t<float>(p, stream);
 }
 
