@@ -18,12 +18,12 @@ constexpr int kLinSms = 152;
 
 // A CTA's slice of a state: DK x DVS elements, a float4 of VPT for each thread
 // (narrow: at most 32 columns, for calls too small to fill the GPU otherwise)
-template <int DK, int DV, bool kNarrow = false>
+template <int DK, int DV, bool kNarrow = false, int kMost = kThreads>
 struct Tile {
   static constexpr int kWide = DK * DV > 16384 ? 16384 / DK : DV;
   static constexpr int DVS = kNarrow && kWide > 32 ? 32 : kWide;  // columns
   static constexpr int QPR = DVS / 4;                            // float4 of a row
-  static constexpr int NT = DK * QPR < kThreads ? DK * QPR : kThreads;
+  static constexpr int NT = DK * QPR < kMost ? DK * QPR : kMost;
   static constexpr int NRG = NT / QPR;                           // rows that the threads cover at once
   static constexpr int VPT = DK / NRG;
   static_assert(NT % QPR == 0 && DK % NRG == 0, "threads tile the slice");
@@ -111,9 +111,12 @@ __device__ __forceinline__ bool load_parents(const LinParams& p, const LinSeq& s
 // on the path or not (a wait for them behind the walk took a quarter of the time).
 constexpr int kBatch = 16;  // tokens in shared memory at a time
 
+// (512 threads a slice of 64 KB: with 256 the state left too few registers for the rest)
+template <int DK, int DV>
+using CommitTile = Tile<DK, DV, false, 2 * kThreads>;
 template <typename T, int DK, int DV>
-__global__ void __launch_bounds__(Tile<DK, DV>::NT, 3) lin_commit(const LinParams p) {
-  using L = Tile<DK, DV>;
+__global__ void __launch_bounds__(CommitTile<DK, DV>::NT, 2) lin_commit(const LinParams p) {
+  using L = CommitTile<DK, DV>;
   constexpr int kB = DK == 256 ? kBatch / 2 : kBatch;
   __shared__ float sk[kB][DK];
   __shared__ __align__(16) float sv[kB][L::DVS];
@@ -157,9 +160,11 @@ __global__ void __launch_bounds__(Tile<DK, DV>::NT, 3) lin_commit(const LinParam
   const float l0 = lane <= a ? la[lane] : 0.f, l1 = lane + 32 <= a ? la[lane + 32] : 0.f;
   unsigned long long path = 0;
   float sum = 0.f, w0 = 0.f, w1 = 0.f;
+#pragma unroll 1
   for (int j = a; j >= 0; j = par[j]) {
     path |= 1ull << j;
-    if (lane == (j & 31)) (j < 32 ? w0 : w1) = sum;
+    if (lane == j) w0 = sum;
+    if (lane + 32 == j) w1 = sum;
     sum += __shfl_sync(0xffffffffu, j < 32 ? l0 : l1, j & 31);
   }
   w0 = exp2f(w0);
@@ -172,8 +177,9 @@ __global__ void __launch_bounds__(Tile<DK, DV>::NT, 3) lin_commit(const LinParam
       fetch(b);
       __syncthreads();
     }
-    for (int j = 0; j < kB; ++j) {
-      if (!(path >> (b + j) & 1)) continue;
+#pragma unroll 1
+    for (unsigned long long left = path >> b & ((1ull << kB) - 1); left; left &= left - 1) {
+      const int j = __ffsll((long long)left) - 1;
       const float w = __shfl_sync(0xffffffffu, b + j < 32 ? w0 : w1, (b + j) & 31);
       const float4 v4 = mul4(w, *reinterpret_cast<const float4*>(&sv[j][4 * cq]));
 #pragma unroll
@@ -503,7 +509,7 @@ cudaError_t launch_state(const LinParams& p, cudaStream_t stream) {
   using L = Tile<DK, DV>;
   using N = Tile<DK, DV, true>;
   const dim3 grid((unsigned)p.num_seqs, (unsigned)p.H, DV / L::DVS), narrow(grid.x, grid.y, DV / N::DVS);
-  if (kCommit) return launch_maybe_dependent(true, lin_commit<T, DK, DV>, grid, dim3(L::NT), 0, stream, p);
+  if (kCommit) return launch_maybe_dependent(true, lin_commit<T, DK, DV>, grid, dim3(CommitTile<DK, DV>::NT), 0, stream, p);
   // fewer CTAs than SMs (one row of 32 heads of 128 x 128: 6.1 us in whole states)
   if (N::DVS < L::DVS && (int64_t)grid.x * grid.y * grid.z < kLinSms)
     return launch_maybe_dependent(true, lin_decode<T, DK, DV, true>, narrow, dim3(N::NT), 0, stream, p);
