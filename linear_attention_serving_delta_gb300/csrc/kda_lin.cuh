@@ -77,14 +77,20 @@ constexpr float kLinLog2e = 1.4426950408889634f;
 // An alpha below 2^-kLinMaxDecay counts as 0 (so the sums of logarithms stay finite)
 constexpr float kLinMaxDecay = 1024.f;
 
-// log2 alpha of token t, head h
+// The gate of token t, head h, and log2 alpha of it
 template <typename T>
-__device__ __forceinline__ float lin_log2_alpha(const LinParams& p, int64_t t, int h) {
-  float x = -1.f;
-  if (p.g) x = log_alpha_of(ld_in(static_cast<const T*>(p.g), t * p.H + h));
+__device__ __forceinline__ float lin_gate(const LinParams& p, int64_t t, int h) {
+  return p.g ? ld_in(static_cast<const T*>(p.g), t * p.H + h) : 0.f;
+}
+__device__ __forceinline__ float lin_log2_alpha(const LinParams& p, float gate, int h) {
+  float x = p.g ? log_alpha_of(gate) : -1.f;
   if (p.slope) x *= p.slope[h];
   x *= kLinLog2e;
   return x < -kLinMaxDecay ? -kLinMaxDecay : x;  // (a NaN stays)
+}
+template <typename T>
+__device__ __forceinline__ float lin_log2_alpha(const LinParams& p, int64_t t, int h) {
+  return lin_log2_alpha(p, lin_gate<T>(p, t, h), h);
 }
 
 // A sum of logarithms kept as a whole number and a fraction of at most a half,
@@ -123,7 +129,8 @@ size_t lin_tc_workspace(const LinParams& p);
 cudaError_t launch_lin_tc(const LinParams& p, void* ws, cudaStream_t stream);
 
 // Prompts token by token on the CUDA cores: every type, size and alignment
-cudaError_t launch_lin_simt(const LinParams& p, cudaStream_t stream);
+size_t lin_simt_workspace(const LinParams& p);
+cudaError_t launch_lin_simt(const LinParams& p, void* ws, cudaStream_t stream);
 
 cudaError_t launch_lin_decode(const LinParams& p, cudaStream_t stream);
 cudaError_t launch_lin_draft(const LinParams& p, cudaStream_t stream);

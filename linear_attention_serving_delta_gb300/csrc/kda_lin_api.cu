@@ -1,6 +1,8 @@
 // kda_lin_api.cu -- the extern "C" entry points of the linear attention with a
 // decay for each head: argument validation, workspace sizes and the choice of
 // path.  Declarations and contracts are in include/kda.h.
+#include <algorithm>
+
 #include "kda_lin.cuh"
 
 namespace kda {
@@ -137,7 +139,8 @@ extern "C" {
 size_t kda_lin_prefill_workspace_size(const kda_lin_prefill_args* a) {
   if (validate(a) != KDA_OK) return 0;
   const LinParams p = params(a);
-  return lin_tc_fits(p) ? lin_tc_workspace(p) : 256;
+  // (enough for either path: a call's pointers may be aligned otherwise than these)
+  return p.dt == KDA_BF16 ? std::max(lin_tc_workspace(p), lin_simt_workspace(p)) : lin_simt_workspace(p);
 }
 
 kda_status_t kda_lin_prefill(const kda_lin_prefill_args* a, void* ws, size_t ws_bytes, void* stream) {
@@ -145,9 +148,9 @@ kda_status_t kda_lin_prefill(const kda_lin_prefill_args* a, void* ws, size_t ws_
   if (st != KDA_OK) return st;
   const LinParams p = params(a);
   const bool tc = lin_tc_fits(p);
-  if (!ws || ws_bytes < (tc ? lin_tc_workspace(p) : 256) || misaligned(ws, 256)) return KDA_ERR_WORKSPACE;
+  if (!ws || ws_bytes < (tc ? lin_tc_workspace(p) : lin_simt_workspace(p)) || misaligned(ws, 256)) return KDA_ERR_WORKSPACE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return from_cuda(tc ? launch_lin_tc(p, ws, s) : launch_lin_simt(p, s));
+  return from_cuda(tc ? launch_lin_tc(p, ws, s) : launch_lin_simt(p, ws, s));
 }
 
 kda_status_t kda_lin_decode(const kda_lin_decode_args* a, void* stream) {

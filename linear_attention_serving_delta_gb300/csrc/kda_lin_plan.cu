@@ -23,6 +23,12 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kBuckets = 2560;
+constexpr int kLinMostSegments = 640;  // slots of any path, and two
+
+// A sequence as its segments need it
+struct LinMine {
+  int32_t tok0, len, rec, place, local, row;
+};
 
 // lengths up to 255 chunks keep their own bucket, longer ones their seven leading bits
 __device__ __forceinline__ int bucket_of(int n) {
@@ -56,14 +62,15 @@ __device__ int64_t scan(int64_t x, int64_t* part, int64_t* total) {
 __global__ void __launch_bounds__(kPlanThreads) lin_plan(const LinParams p, const LinPlan a) {
   __shared__ int64_t part[32];
   __shared__ int32_t hist[kBuckets];
+  __shared__ LinMine mine_of[kPlanThreads];
+  __shared__ int32_t first_n[kPlanThreads];  // chunks of the first sequences, for the search
   const int tid = threadIdx.x, per = p.H * a.tiles;
   pdl_launch_dependents();
   pdl_wait();
   for (int i = tid; i < kBuckets; i += kPlanThreads) hist[i] = 0;
   // chunks and records
-  auto chunks_of = [](const LinSeq& q) { return (int32_t)((q.len + kLinChunk - 1) / kLinChunk); };
+  auto chunks_of = [&](const LinSeq& q) { return (int32_t)((q.len + a.chunk - 1) / a.chunk); };
   int64_t chunks = 0, active = 0, total;
-  int32_t mine_n = 0;  // the thread's first sequence, for the search below
   for (int base = 0; base < p.num_seqs; base += kPlanThreads) {
     const int s = base + tid;
     LinSeq q{};
@@ -78,36 +85,59 @@ __global__ void __launch_bounds__(kPlanThreads) lin_plan(const LinParams p, cons
     }
     if (q.flag) attn_flag(p.status, q.flag);
     if (s < p.num_seqs) a.seq_rec[s] = q.ok ? (int32_t)rec : -1;
+    if (base == 0) first_n[tid] = q.ok ? max(n, 1) : 0;
     active += __syncthreads_count(q.ok);
-    if (base == 0) mine_n = q.ok ? max(n, 1) : 0;
   }
   // chunks of a segment: the least with which all chains fit the CTAs at once, or where
   // there are more chains than CTAs twice a CTA's share, so that only what would
   // outlast the others is cut
   int32_t limit = INT32_MAX;
   if (a.may_split && chunks > 0) {
-    if (active * per <= kLinSlots) {
-      int64_t lo = kLinMinSegment, hi = chunks > kLinMinSegment ? chunks : kLinMinSegment;
+    if (active * per <= a.slots) {
+      // 32 candidates at once, a warp each; the first that fits ends a round
+      const int lane = tid & 31, warp = tid >> 5;
+      int64_t lo = a.min_segment, hi = chunks > a.min_segment ? chunks : a.min_segment;
       while (lo < hi) {
-        const int64_t mid = (lo + hi) >> 1;
-        int64_t x = (mine_n + mid - 1) / mid;
-        for (int s = tid + kPlanThreads; s < p.num_seqs; s += kPlanThreads)
-          if (a.seq_rec[s] >= 0) x += max((int64_t)1, (chunks_of(lin_seq(p, s)) + mid - 1) / mid);
-        scan(x, part, &total);
-        if (total * per <= kLinSlots) hi = mid;
-        else lo = mid + 1;
+        const int64_t step = (hi - lo + 31) / 32, mid = lo + warp * step;
+        const int32_t m = (int32_t)min(mid, hi);
+        int64_t x = 0;
+        for (int s = lane; s < p.num_seqs; s += 32) {
+          int32_t n = s < kPlanThreads ? first_n[s] : 0;
+          if (s >= kPlanThreads && a.seq_rec[s] >= 0) n = max(chunks_of(lin_seq(p, s)), 1);
+          x += n > 0 ? (n - 1) / m + 1 : 0;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        if (lane == 0) part[warp] = x * per <= a.slots;
+        __syncthreads();
+        const int fit = __ffs(__ballot_sync(0xffffffffu, part[lane] != 0)) - 1;
+        __syncthreads();
+        if (fit != 0) lo = min(hi, lo + (fit < 0 ? 31 : fit - 1) * step + 1);
+        if (fit >= 0) hi = fit == 0 ? lo : min(hi, lo - 1 + step);
       }
       limit = (int32_t)min(lo, (int64_t)INT32_MAX);
     } else {
-      limit = (int32_t)min(max((int64_t)kLinMinSegment, (2 * chunks * per + kLinSlots - 1) / kLinSlots), (int64_t)INT32_MAX);
+      limit = (int32_t)min(max((int64_t)a.min_segment, (2 * chunks * per + a.slots - 1) / a.slots), (int64_t)INT32_MAX);
     }
   }
   auto segments_of = [&](int32_t n) { return n > limit ? (n - 1) / limit + 1 : 1; };
   __syncthreads();
-  for (int s = tid; s < p.num_seqs; s += kPlanThreads) {
-    if (a.seq_rec[s] < 0) continue;
-    const int32_t n = chunks_of(lin_seq(p, s)), k = segments_of(n);
-    for (int i = 0; i < k; ++i) atomicAdd(&hist[bucket_of(lin_cut(n, k, i + 1) - lin_cut(n, k, i))], 1);
+  // A thread a sequence; the segments of one that is cut by all lanes of its warp
+  auto each_segment = [&](int32_t n, int32_t k, auto one) {
+    if (k == 1) one(tid & 31, n, 1, 0);
+    for (uint32_t cut = __ballot_sync(0xffffffffu, k > 1); cut; cut &= cut - 1) {
+      const int from = __ffs(cut) - 1;
+      const int32_t n_of = __shfl_sync(0xffffffffu, n, from), k_of = __shfl_sync(0xffffffffu, k, from);
+      for (int i = tid & 31; i < k_of; i += 32) one(from, n_of, k_of, i);
+    }
+  };
+  for (int base = 0; base < p.num_seqs; base += kPlanThreads) {
+    const int s = base + tid;
+    const bool ok = s < p.num_seqs && a.seq_rec[s] >= 0;
+    const int32_t n = ok ? chunks_of(lin_seq(p, s)) : 0;
+    each_segment(n, ok ? segments_of(n) : 0, [&](int, int32_t n, int32_t k, int32_t i) {
+      atomicAdd(&hist[bucket_of(lin_cut(n, k, i + 1) - lin_cut(n, k, i))], 1);
+    });
   }
   __syncthreads();
   // hist[b] becomes the first place of bucket b: longer ones first
@@ -129,7 +159,7 @@ __global__ void __launch_bounds__(kPlanThreads) lin_plan(const LinParams p, cons
     at += mine[i];
   }
   __syncthreads();
-  int64_t places = 0, splits = 0, locals = 0;
+  int64_t before = 0;
   for (int base = 0; base < p.num_seqs; base += kPlanThreads) {
     const int s = base + tid;
     LinSeq q{};
@@ -140,37 +170,39 @@ __global__ void __launch_bounds__(kPlanThreads) lin_plan(const LinParams p, cons
       k = segments_of(n_s);
     }
     const bool cut = k > 1;
-    const int64_t place = places + scan(cut ? k : 0, part, &total) - (cut ? k : 0);
-    places += total;
-    const int64_t split = splits + scan(cut, part, &total) - cut;
-    splits += total;
-    const int64_t local = locals + scan(cut ? k - 1 : 0, part, &total) - (cut ? k - 1 : 0);
-    locals += total;
-    const int32_t row = -2 - q.slot, from = p.state_in ? row : -1, to = p.state_out ? row : -1;
+    // sequences cut and their segments before this one, in one sum
+    const int64_t both = cut ? ((int64_t)1 << 32) + k : 0, sum = before + scan(both, part, &total) - both;
+    before += total;
+    const int64_t split = sum >> 32, place = sum & 0xffffffff, local = place - split;
     if (cut) a.splits[split] = LinSplit{(int32_t)place, k, rec, n_s};
-    for (int i = 0; i < k; ++i) {
-      const int32_t c0 = lin_cut(n_s, k, i), c1 = lin_cut(n_s, k, i + 1);
+    mine_of[tid] = LinMine{(int32_t)q.tok0, (int32_t)q.len, rec, (int32_t)place, (int32_t)local, -2 - q.slot};
+    __syncwarp();
+    each_segment(n_s, k, [&](int lane, int32_t n, int32_t k, int32_t i) {
+      const LinMine m = mine_of[(tid & ~31) + lane];
+      const int32_t c0 = lin_cut(n, k, i), c1 = lin_cut(n, k, i + 1);
+      const int32_t from = p.state_in ? m.row : -1, to = p.state_out ? m.row : -1;
       LinItem it{};
-      it.tok0 = (int32_t)q.tok0 + c0 * kLinChunk;
-      it.len = (int32_t)min((int64_t)(c1 - c0) * kLinChunk, q.len - (int64_t)c0 * kLinChunk);
-      it.rec = rec + c0;
+      it.tok0 = m.tok0 + c0 * a.chunk;
+      it.len = min((c1 - c0) * a.chunk, m.len - c0 * a.chunk);
+      it.rec = m.rec + c0;
       it.copy = -1;
       // (the first segment starts from a copy: the last one may write the pool in place meanwhile)
-      it.from = !cut || (i == 0 && !p.state_in) ? from : (int32_t)place + i;
+      it.from = k == 1 || (i == 0 && !p.state_in) ? from : m.place + i;
       it.to = i + 1 == k ? to : -1;
       a.items[atomicAdd(&hist[bucket_of(c1 - c0)], 1)] = it;
       if (i + 1 < k) {
         it.from = i == 0 ? from : -1;
-        it.copy = i == 0 && p.state_in ? (int32_t)place : -1;
-        it.to = (int32_t)place + i + 1;
-        a.locals[local + i] = it;
+        it.copy = i == 0 && p.state_in ? m.place : -1;
+        it.to = m.place + i + 1;
+        a.locals[m.local + i] = it;
       }
-    }
+    });
+    __syncwarp();
   }
   if (tid == 0) {
-    a.head->items = (int32_t)(items * per);
-    a.head->locals = (int32_t)(locals * per);
-    a.head->splits = (int32_t)splits;
+    a.head->items = (int32_t)items;
+    a.head->locals = (int32_t)((before & 0xffffffff) - (before >> 32));
+    a.head->splits = (int32_t)(before >> 32);
   }
 }
 
@@ -204,9 +236,8 @@ __global__ void __launch_bounds__(256) lin_gates(const LinParams p, const LinPla
 }
 
 // Start states of segments 2, 3, ...: a thread four elements
-__global__ void __launch_bounds__(256) lin_combine(const LinParams p, const LinPlan a, const LinGates* records,
-                                                   float* states) {
-  __shared__ float decay[kLinSlots + 2];
+__global__ void __launch_bounds__(256) lin_combine(const LinParams p, const LinPlan a) {
+  __shared__ float decay[kLinMostSegments];
   pdl_launch_dependents();
   pdl_wait();
   const int h = blockIdx.y;
@@ -216,9 +247,13 @@ __global__ void __launch_bounds__(256) lin_combine(const LinParams p, const LinP
     __syncthreads();
     // log2 of each segment's decay, a warp a segment
     for (int i = 1 + (threadIdx.x >> 5); i < sp.segments - 1; i += 8) {
+      if (a.logs) {
+        if ((threadIdx.x & 31) == 0) decay[i] = a.logs[((int64_t)sp.place + i + 1) * p.H + h];
+        continue;
+      }
       LogSum g{0.f, 0.f};
       for (int c = lin_cut(sp.chunks, sp.segments, i) + (threadIdx.x & 31); c < lin_cut(sp.chunks, sp.segments, i + 1); c += 32)
-        g = g + log_sum(records[((int64_t)sp.rec + c) * p.H + h].head.total);
+        g = g + log_sum(a.records[((int64_t)sp.rec + c) * p.H + h].head.total);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1)
         g = g + LogSum{__shfl_xor_sync(0xffffffffu, g.i, o), __shfl_xor_sync(0xffffffffu, g.f, o)};
@@ -226,18 +261,27 @@ __global__ void __launch_bounds__(256) lin_combine(const LinParams p, const LinP
     }
     __syncthreads();
     if (e >= size) continue;
-    float4* at = reinterpret_cast<float4*>(states + ((int64_t)sp.place * p.H + h) * size + e);
+    float4* at = reinterpret_cast<float4*>(a.states + ((int64_t)sp.place * p.H + h) * size + e);
     const int64_t step = (int64_t)p.H * size / 4;
     float4 s = at[step];
-    for (int i = 2; i < sp.segments; ++i) {
-      const LinDecay d = lin_decay(decay[i - 1]);
-      const float one = d.near_one ? 1.f : 0.f;
-      float4 y = at[i * step];
-      y.x = fmaf(one, s.x, fmaf(d.m, s.x, y.x));
-      y.y = fmaf(one, s.y, fmaf(d.m, s.y, y.y));
-      y.z = fmaf(one, s.z, fmaf(d.m, s.z, y.z));
-      y.w = fmaf(one, s.w, fmaf(d.m, s.w, y.w));
-      at[i * step] = s = y;
+    // (eight loads at a time: one after the other they would be a chain of waits)
+    constexpr int kAhead = 8;
+    for (int i0 = 2; i0 < sp.segments; i0 += kAhead) {
+      float4 y[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        if (i0 + u < sp.segments) y[u] = at[(i0 + u) * step];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        if (i0 + u >= sp.segments) break;
+        const LinDecay d = lin_decay(decay[i0 + u - 1]);
+        const float one = d.near_one ? 1.f : 0.f;
+        y[u].x = fmaf(one, s.x, fmaf(d.m, s.x, y[u].x));
+        y[u].y = fmaf(one, s.y, fmaf(d.m, s.y, y[u].y));
+        y[u].z = fmaf(one, s.z, fmaf(d.m, s.z, y[u].z));
+        y[u].w = fmaf(one, s.w, fmaf(d.m, s.w, y[u].w));
+        at[(i0 + u) * step] = s = y[u];
+      }
     }
   }
 }
@@ -247,16 +291,20 @@ __global__ void __launch_bounds__(256) lin_combine(const LinParams p, const LinP
 // Column tiles: 128 wide, 64 where the keys are 256 or the values no wider
 int lin_tile_width(const LinParams& p) { return p.dk > 128 || p.dv <= 64 ? 64 : 128; }
 
-LinLayout lin_layout(const LinParams& p) {
-  LinLayout L{};
+LinShare lin_tc_share(const LinParams& p) {
   const int w = lin_tile_width(p);
-  const int64_t per = (int64_t)p.H * ((p.dv + w - 1) / w), chunks = lin_max_records(p);
+  return LinShare{(p.dv + w - 1) / w, kLinSlots, kLinChunk, kLinMinSegment, kLinDirectTokens, true};
+}
+
+LinLayout lin_layout(const LinParams& p, const LinShare& sh) {
+  LinLayout L{};
+  const int64_t per = (int64_t)p.H * sh.tiles, chunks = lin_max_records(p, sh.chunk);
   // Short prompts that the CTAs hold at once need no plan: a chain each, which makes its
   // gates itself
-  L.direct = p.total_tokens <= kLinDirectTokens && p.num_seqs * per <= 2 * kLinSlots;
+  L.direct = p.total_tokens <= sh.direct_tokens && p.num_seqs * per <= 2 * sh.slots;
   // with more than half as many chains a sequence as CTAs no cut would fit
-  L.may_split = !L.direct && 2 * per <= kLinSlots && p.total_tokens > kLinMinSegment * kLinChunk;
-  L.places = L.may_split ? kLinSlots / per + 2 : 0;
+  L.may_split = !L.direct && 2 * per <= sh.slots && p.total_tokens > sh.min_segment * sh.chunk;
+  L.places = L.may_split ? sh.slots / per + 2 : 0;
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t at = off;
@@ -270,10 +318,31 @@ LinLayout lin_layout(const LinParams& p) {
     L.locals = take(sizeof(LinItem) * (size_t)L.places);
     L.splits = take(sizeof(LinSplit) * (size_t)L.places);
     L.states = take(sizeof(float) * (size_t)L.places * p.H * p.dk * p.dv);
+    if (!sh.records) L.logs = take(sizeof(float) * (size_t)L.places * p.H);
   }
-  L.records = take(sizeof(LinGates) * (size_t)chunks * p.H);
-  L.total = off;
+  if (sh.records) L.records = take(sizeof(LinGates) * (size_t)chunks * p.H);
+  L.total = off > 0 ? off : 256;
   return L;
+}
+
+LinPlan lin_plan_of(const LinParams& p, const LinShare& sh, const LinLayout& L, void* ws) {
+  char* w = static_cast<char*>(ws);
+  LinPlan a{};
+  a.head = reinterpret_cast<LinHead*>(w + L.head);
+  a.seq_rec = reinterpret_cast<int32_t*>(w + L.seq_rec);
+  a.items = reinterpret_cast<LinItem*>(w + L.items);
+  a.locals = reinterpret_cast<LinItem*>(w + L.locals);
+  a.splits = reinterpret_cast<LinSplit*>(w + L.splits);
+  a.tiles = sh.tiles;
+  a.slots = sh.slots;
+  a.min_segment = sh.min_segment;
+  a.chunk = sh.chunk;
+  a.max_records = lin_max_records(p, sh.chunk);
+  a.may_split = L.may_split;
+  a.states = reinterpret_cast<float*>(w + L.states);
+  a.records = sh.records ? reinterpret_cast<const LinGates*>(w + L.records) : nullptr;
+  a.logs = sh.records ? nullptr : reinterpret_cast<float*>(w + L.logs);
+  return a;
 }
 
 cudaError_t launch_lin_plan(const LinParams& p, const LinPlan& a, cudaStream_t stream) {
@@ -282,11 +351,10 @@ cudaError_t launch_lin_plan(const LinParams& p, const LinPlan& a, cudaStream_t s
 cudaError_t launch_lin_gates(const LinParams& p, const LinPlan& a, LinGates* records, cudaStream_t stream) {
   return launch_maybe_dependent(true, lin_gates, dim3((unsigned)a.max_records, (unsigned)((p.H + 7) / 8)), dim3(256), 0, stream, p, a, records);
 }
-cudaError_t launch_lin_combine(const LinParams& p, const LinPlan& a, const LinGates* records, float* states,
-                               cudaStream_t stream) {
+cudaError_t launch_lin_combine(const LinParams& p, const LinPlan& a, cudaStream_t stream) {
   const int64_t size = (int64_t)p.dk * p.dv;
-  const dim3 grid((unsigned)std::max(1, kLinSlots / (2 * p.H)), (unsigned)p.H, (unsigned)((size + 1023) / 1024));
-  return launch_maybe_dependent(true, lin_combine, grid, dim3(256), 0, stream, p, a, records, states);
+  const dim3 grid((unsigned)std::max(1, a.slots / (2 * p.H * a.tiles)), (unsigned)p.H, (unsigned)((size + 1023) / 1024));
+  return launch_maybe_dependent(true, lin_combine, grid, dim3(256), 0, stream, p, a);
 }
 
 }  // namespace kda

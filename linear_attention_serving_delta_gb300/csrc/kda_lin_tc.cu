@@ -64,7 +64,7 @@ struct Shape {
   static constexpr uint32_t kV = 2 * kStages * kQK;
   static constexpr uint32_t kS = kStages * kStage;
   static constexpr uint32_t kTail = kS + kSop;
-  static constexpr uint32_t kBytes = kTail + 3072;
+  static constexpr uint32_t kBytes = kTail + 3 * 1024;
   static constexpr int kSCols = MB == 1 ? DV / 2 : DV;     // columns of a state thread
   // K~ goes through TMEM half a chunk of one row tile at a time, a place for each half
   // where there is room: one is made while the other is multiplied
@@ -89,7 +89,7 @@ struct Tail {
   // that had one, counted through the CTA's chunks
   uint32_t nan_from[128];
 };
-static_assert(sizeof(Tail) <= 3072 && offsetof(Tail, gates) % 16 == 0, "tail block");
+static_assert(sizeof(Tail) <= 3 * 1024 && offsetof(Tail, gates) % 16 == 0, "tail block");
 
 // The CTA's i-th chain, for every role alike
 __device__ __forceinline__ bool chain_at(const LinParams& p, const LinTcArgs& a, const Tail* b, int i, LinItem* ch) {
@@ -822,7 +822,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_after_sync();
   pdl_wait();  // the plan, or what came before
   if (a.items) {
-    if (threadIdx.x == 0) b->num_items = *a.num_items;
+    if (threadIdx.x == 0) b->num_items = *a.num_items * p.H * a.tiles;  // (lin_tc_fits)
   } else {
     // a chain of the CTA's own, and its records (the tiles of a head all make them, alike)
     const LinItem own = own_chain(p, a, reinterpret_cast<int64_t*>(sm));
@@ -879,7 +879,8 @@ cudaError_t launch_shape(const LinParams& p, void* ws, cudaStream_t stream) {
       !lin_map(&mv, p.v, p.total_tokens, p.H, p.dv, C) || !lin_map(&mo, p.o, p.total_tokens, p.H, p.dv, 32))
     return cudaErrorInvalidValue;
   char* w = static_cast<char*>(ws);
-  const LinLayout L = lin_layout(p);
+  const LinShare sh = lin_tc_share(p);
+  const LinLayout L = lin_layout(p, sh);
   LinTcArgs a{};
   a.tiles = (p.dv + DV - 1) / DV;
   a.tile_shift = a.tiles == 4 ? 2 : a.tiles - 1;
@@ -897,23 +898,15 @@ cudaError_t launch_shape(const LinParams& p, void* ws, cudaStream_t stream) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  LinPlan plan{};
-  plan.head = reinterpret_cast<LinHead*>(w + L.head);
-  plan.seq_rec = reinterpret_cast<int32_t*>(w + L.seq_rec);
-  plan.items = reinterpret_cast<LinItem*>(w + L.items);
-  plan.locals = reinterpret_cast<LinItem*>(w + L.locals);
-  plan.splits = reinterpret_cast<LinSplit*>(w + L.splits);
-  plan.tiles = a.tiles;
-  plan.max_records = a.max_records;
-  plan.may_split = L.may_split;
-  a.states = reinterpret_cast<float*>(w + L.states);
+  const LinPlan plan = lin_plan_of(p, sh, L, ws);
+  a.states = plan.states;
   if ((e = launch_lin_plan(p, plan, stream)) != cudaSuccess) return e;
   if ((e = launch_lin_gates(p, plan, a.records, stream)) != cudaSuccess) return e;
   if (L.may_split) {
     a.items = plan.locals;
     a.num_items = &plan.head->locals;
     if ((e = run(lin_tc<DK, DV, true>, std::min<int64_t>(sms, L.places * per))) != cudaSuccess) return e;
-    if ((e = launch_lin_combine(p, plan, a.records, a.states, stream)) != cudaSuccess) return e;
+    if ((e = launch_lin_combine(p, plan, stream)) != cudaSuccess) return e;
   }
   a.items = plan.items;
   a.num_items = &plan.head->items;
@@ -928,7 +921,7 @@ bool lin_tc_fits(const LinParams& p) {
   return p.dt == KDA_BF16 && p.total_tokens > 0 && al16(p.q) && al16(p.k) && al16(p.v) && al16(p.o) &&
          (int64_t)p.num_seqs * p.H * 4 < INT32_MAX;
 }
-size_t lin_tc_workspace(const LinParams& p) { return lin_layout(p).total; }
+size_t lin_tc_workspace(const LinParams& p) { return lin_layout(p, lin_tc_share(p)).total; }
 cudaError_t launch_lin_tc(const LinParams& p, void* ws, cudaStream_t stream) {
   const int w = lin_tile_width(p);
   if (p.dk > 128) return launch_shape<256, 64>(p, ws, stream);

@@ -23,7 +23,10 @@ struct LinSplit {
   int32_t place, segments, rec, chunks;
 };
 // Segment i of n chunks cut into k: its first chunk
-__host__ __device__ __forceinline__ int32_t lin_cut(int32_t n, int32_t k, int32_t i) { return (int32_t)((int64_t)n * i / k); }
+__host__ __device__ __forceinline__ int32_t lin_cut(int32_t n, int32_t k, int32_t i) {
+  const int32_t each = n / k, more = n - each * k;  // the first `more` have one more
+  return i * each + (i < more ? i : more);
+}
 
 struct LinHead {
   int32_t items, locals, splits;  // entries of the lists
@@ -68,25 +71,39 @@ struct LinPlan {
   LinItem* items;          // costliest first
   LinItem* locals;         // the segments whose own end states come first
   LinSplit* splits;
-  int32_t tiles;
+  int32_t tiles;           // column tiles of a head
+  int32_t slots;           // CTAs that the chains are shared out to
+  int32_t chunk;           // tokens of a chunk
+  int32_t min_segment;     // fewest chunks of a segment
   int64_t max_records;
   int32_t may_split;
+  float* states;           // [places][H][dk][dv] start states of segments
+  // log2 of the decay of the segment before a place: from the records, or [places][H]
+  const LinGates* records;
+  float* logs;
 };
 
+// How a path plans: its column tiles, CTAs, tokens of a chunk, shortest segment in
+// chunks, up to how many tokens its chains need no plan, whether it has gate records
+struct LinShare {
+  int32_t tiles, slots, chunk, min_segment, direct_tokens;
+  bool records;
+};
 struct LinLayout {
-  size_t head, seq_rec, items, locals, splits, states, records, total;
+  size_t head, seq_rec, items, locals, splits, states, records, logs, total;
   int64_t places;
   bool direct, may_split;
 };
 int lin_tile_width(const LinParams& p);
-LinLayout lin_layout(const LinParams& p);
+LinShare lin_tc_share(const LinParams& p);
+LinLayout lin_layout(const LinParams& p, const LinShare& sh);
+LinPlan lin_plan_of(const LinParams& p, const LinShare& sh, const LinLayout& L, void* ws);
 cudaError_t launch_lin_plan(const LinParams& p, const LinPlan& a, cudaStream_t stream);
 cudaError_t launch_lin_gates(const LinParams& p, const LinPlan& a, LinGates* records, cudaStream_t stream);
-cudaError_t launch_lin_combine(const LinParams& p, const LinPlan& a, const LinGates* records, float* states,
-                               cudaStream_t stream);
+cudaError_t launch_lin_combine(const LinParams& p, const LinPlan& a, cudaStream_t stream);
 
 // Chunks of all sequences of a well-formed call, at most
-inline int64_t lin_max_records(const LinParams& p) { return p.total_tokens / kLinChunk + p.num_seqs; }
+inline int64_t lin_max_records(const LinParams& p, int chunk = kLinChunk) { return p.total_tokens / chunk + p.num_seqs; }
 
 // The chunks of the valid sequences before s, for the whole block (sum: shared, free before and after)
 __device__ __forceinline__ int64_t seq_records(const LinParams& p, int s, int threads, int64_t* sum) {

@@ -351,6 +351,54 @@ def test_prefill_long_same_bits_every_time_and_in_a_graph():
     assert call.device_status() == 0
 
 
+# Token by token, in segments too: every size with and without a second column a lane
+@pytest.mark.parametrize("lens,H,Hk,dk,dv,gate", [
+    ([1500], 2, 2, 64, 64, "g"), ([700, 0, 1, 33, 400], 2, 1, 128, 128, "slope"), ([900], 1, 1, 256, 128, "both"),
+    ([600, 300, 17], 3, 3, 16, 256, "strong"), ([800, 90], 6, 2, 32, 16, "keep"), ([1000], 4, 4, 128, 32, "g")])
+def test_prefill_f32_long(lens, H, Hk, dk, dv, gate):
+    d = inputs(160 + dk, sum(lens), H, Hk, dk, dv, "f32", gate, n=len(lens))
+    o, final = kda.lin_prefill(d["q"], d["k"], d["v"], offsets(lens), g=d["g"], slope=d["slope"], scale=dk ** -0.5,
+                               initial_state=d["state"])
+    check_prefill(d, lens, H, dk, "f32", o, final, dk ** -0.5)
+
+
+def test_prefill_f32_long_slots_in_place_and_in_a_graph():
+    lens, slots, H, dk = [900, 40, 500, 0], [4, -1, 0, 2], 2, 64
+    T = sum(lens)
+    d = inputs(171, T, H, H, dk, dk, "f32", "g", n=6)
+    pool = d["state"].clone()
+    o = torch.full((T, H, dk), 7.0, device="cuda")
+    call = kda.LinPrefill(d["q"], d["k"], d["v"], offsets(lens), g=d["g"], initial_state=pool, final_state=pool, o=o,
+                          state_slots=torch.tensor(slots, device="cuda", dtype=torch.int32))
+    call.run()
+    check_prefill(d, lens, H, dk, "f32", o, pool, 1.0, slots)
+    assert call.device_status() == 0 and bool((o[900:940] == 7).all())
+    for row in (1, 2, 3, 5):
+        assert torch.equal(pool[row], d["state"][row])
+    first, after = o.clone(), pool.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        call.run(side)
+    for _ in range(2):
+        pool.copy_(d["state"])
+        call.workspace.fill_(255)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, first) and torch.equal(pool, after)
+
+
+def test_prefill_long_unaligned():
+    lens, H, dk = [1100, 20], 2, 64
+    d = inputs(19, sum(lens), H, H, dk, dk, "bf16", "g")
+    for x in ("q", "k", "v", "g"):
+        y = torch.empty(d[x].numel() + 1, device="cuda", dtype=d[x].dtype)[1:].view(d[x].shape)
+        d[x] = y.copy_(d[x])
+    o, final = kda.lin_prefill(d["q"], d["k"], d["v"], offsets(lens), g=d["g"])
+    check_prefill(d, lens, H, dk, "bf16", o, final, 1.0)
+
+
 # ------------------------------------------------------------------ single tokens
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("dk,dv", SIZES)
