@@ -131,6 +131,13 @@ __global__ void __launch_bounds__(CommitTile<DK, DV>::NT, 2) lin_commit(const Li
   if (seq.flag && first) attn_flag(p.status, seq.flag);
   if (!seq.ok) return;
   const int n = (int)seq.len;
+  static_assert(L::NT >= kMaxDraft, "a thread a token");
+  int parent = tid - 1;
+  float gate = 0.f;
+  if (tid < n) {
+    if (p.parents) parent = p.parents[seq.tok0 + tid];
+    gate = lin_gate<T>(p, seq.tok0 + tid, h);
+  }
   const int cq = tid % L::QPR, rg = tid / L::QPR;
   const int64_t at = ((int64_t)seq.slot * p.H + h) * DK * DV + c0 + 4 * cq;
   float4 s[L::VPT];
@@ -147,11 +154,12 @@ __global__ void __launch_bounds__(CommitTile<DK, DV>::NT, 2) lin_commit(const Li
       sv[i / L::DVS][i % L::DVS] =
           ld_in(static_cast<const T*>(p.v), ((seq.tok0 + b + i / L::DVS) * p.H + h) * DV + c0 + i % L::DVS);
   };
-  if (moves) {
-    for (int i = tid; i <= a; i += L::NT) la[i] = lin_log2_alpha<T>(p, seq.tok0 + i, h);
-    fetch(0);
+  if (moves) fetch(0);
+  if (tid < n) {
+    la[tid] = lin_log2_alpha(p, gate, h);
+    par[tid] = (int8_t)parent;
   }
-  if (!load_parents(p, seq, par) || a < -1 || a >= n) {
+  if (!__syncthreads_and(parent >= -1 && parent < tid || tid >= n) || a < -1 || a >= n) {
     if (first) attn_flag(p.status, kFlagBadCache);
     return;
   }
@@ -220,18 +228,39 @@ struct Tree {
   LogSum G[kMaxDraft];
   int8_t par[kMaxDraft];
 };
-// By doubling: after round r a token knows the 2^r nearest of its path.  For the whole
-// CTA, at least kMaxDraft threads or as many rounds over them.
+constexpr int kPer = kMaxDraft / 32;  // tokens of a thread, at most
+// What a tree is made from, on its way beside the other loads
+struct TreeIn {
+  int32_t parent[kPer];
+  float gate[kPer];
+};
 template <typename T>
-__device__ __forceinline__ bool make_tree(const LinParams& p, const LinSeq& seq, int h, Tree* t) {
-  const int n = (int)seq.len;
-  if (!load_parents(p, seq, t->par)) return false;
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    t->path[i] = 1ull << i;
-    t->G[i] = log_sum(lin_log2_alpha<T>(p, seq.tok0 + i, h));
+__device__ __forceinline__ TreeIn tree_in(const LinParams& p, const LinSeq& seq, int h) {
+  TreeIn in;
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) {
+    const int i = threadIdx.x + u * blockDim.x;
+    if (i >= seq.len) continue;
+    in.parent[u] = p.parents ? p.parents[seq.tok0 + i] : i - 1;
+    in.gate[u] = lin_gate<T>(p, seq.tok0 + i, h);
   }
-  __syncthreads();
-  constexpr int kPer = kMaxDraft / 32;  // tokens of a thread, at most
+  return in;
+}
+// By doubling: after round r a token knows the 2^r nearest of its path.  For the whole
+// CTA; false if a parent is malformed.
+__device__ __forceinline__ bool make_tree(const LinParams& p, const LinSeq& seq, const TreeIn& in, int h, Tree* t) {
+  const int n = (int)seq.len;
+  bool good = true;
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) {
+    const int i = threadIdx.x + u * blockDim.x;
+    if (i >= n) continue;
+    good = good && in.parent[u] >= -1 && in.parent[u] < i;
+    t->par[i] = (int8_t)in.parent[u];
+    t->path[i] = 1ull << i;
+    t->G[i] = log_sum(lin_log2_alpha(p, in.gate[u], h));
+  }
+  if (!__syncthreads_and(good)) return false;
   for (int d = 1; d < n; d *= 2) {
     unsigned long long path[kPer];
     LogSum G[kPer];
@@ -264,12 +293,22 @@ __device__ __forceinline__ bool make_tree(const LinParams& p, const LinSeq& seq,
   return true;
 }
 
+// 16 bytes from global to shared memory, or zeros
+__device__ __forceinline__ void copy16(void* to, const void* from, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from),
+               "r"(there ? 16 : 0)
+               : "memory");
+}
+
 // Rows of queries, keys and values in shared memory are 32 bytes apart beyond their own
 // bytes: the fragments' 8-byte reads of eight rows then fall on different banks.
 constexpr int kRowPad = 16;  // elements
 
-template <int DK, int MT>
-__global__ void __launch_bounds__(256) lin_draft_mma(const LinParams p) {
+// MT tiles of 16 tokens in MT / MW groups of warps, which all read the state: for calls too
+// small to fill the GPU, where the products one after the other are what takes the time.
+template <int DK, int MT, int MW>
+__global__ void __launch_bounds__(256, DK <= 128 && MW == 1 ? 2 : 1)
+    lin_draft_mma(const LinParams p) {
   using T = __nv_bfloat16;
   constexpr int KB = DK / 16, NB = KB < 4 ? KB : 4;
   extern __shared__ __align__(16) char dyn[];
@@ -278,7 +317,11 @@ __global__ void __launch_bounds__(256) lin_draft_mma(const LinParams p) {
   __shared__ int32_t any_bad;
   pdl_launch_dependents();
   pdl_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gi = lane >> 2, ti = lane & 3;
+  constexpr int kGroups = MT / MW;
+  const int lane = threadIdx.x & 31, wide = (p.dv + 31) / 32, gi = lane >> 2, ti = lane & 3;
+  const int warp = (threadIdx.x >> 5) % wide, group = (threadIdx.x >> 5) / wide;
+  // a warp's tile u: every second row of groups backwards, as later tiles have more to add up
+  auto tile_of = [&](int u) { return u * kGroups + (u & 1 ? kGroups - 1 - group : group); };
   const int h = blockIdx.y, cb = 32 * warp + 4 * gi, co = 32 * warp + 8 * ti;  // columns: of loads, of outputs
   const LinSeq seq = lin_seq(p, blockIdx.x);
   const bool first = threadIdx.x == 0 && h == 0;
@@ -295,57 +338,60 @@ __global__ void __launch_bounds__(256) lin_draft_mma(const LinParams p) {
     for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        s[b][e] = cb < p.dv ? *reinterpret_cast<const float4*>(S + (int64_t)(16 * (k0 + b) + 4 * ti + e) * p.dv)
+        s[b][e] = cb < p.dv && tile_of(0) < mt ? *reinterpret_cast<const float4*>(S + (int64_t)(16 * (k0 + b) + 4 * ti + e) * p.dv)
                             : make_float4(0.f, 0.f, 0.f, 0.f);
   };
   load(0);
-  // queries, keys and values of the request, rows behind it zero; 16 bytes at a time
-  for (int i = threadIdx.x; i < p.dv; i += blockDim.x) bad[i] = 0;
-  if (threadIdx.x == 0) any_bad = 0;
+  // queries, keys and values of the request, rows behind it zero, 16 bytes at a time and
+  // without a wait in between: what a call's loads wait for one after the other, a CTA
+  // waits for with its state half loaded
   for (int i = threadIdx.x; i < 16 * mt * (DK / 8); i += blockDim.x) {
     const int t = i / (DK / 8), c = i % (DK / 8) * 8;
-    const int64_t at = ((seq.tok0 + t) * p.Hk + h / p.R) * DK + c;
-    uint4 x = make_uint4(0, 0, 0, 0), y = x;
-    if (t < n) {
-      x = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + at);
-      y = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.k) + at);
-    }
-    *reinterpret_cast<uint4*>(sq + t * kPitch + c) = x;
-    *reinterpret_cast<uint4*>(sk + t * kPitch + c) = y;
+    const int64_t at = t < n ? ((seq.tok0 + t) * p.Hk + h / p.R) * DK + c : 0;
+    copy16(sq + t * kPitch + c, static_cast<const T*>(p.q) + at, t < n);
+    copy16(sk + t * kPitch + c, static_cast<const T*>(p.k) + at, t < n);
   }
-  __syncthreads();
   for (int i = threadIdx.x; i < 16 * mt * (p.dv / 8); i += blockDim.x) {
     const int t = i / (p.dv / 8), c = i % (p.dv / 8) * 8;
-    uint4 x = make_uint4(0, 0, 0, 0);
-    if (t < n) x = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.v) + ((seq.tok0 + t) * p.H + h) * p.dv + c);
-    if (!finite2(x.x) || !finite2(x.y) || !finite2(x.z) || !finite2(x.w)) {
-      uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t ones = e & 1 ? 0x7f800000u : 0x7f80u;
-        if ((w[e / 2] & ones) != ones) continue;
-        atomicOr(&bad[c + e], 1ull << t);
-        w[e / 2] &= e & 1 ? 0xffffu : 0xffff0000u;
-      }
-      x = make_uint4(w[0], w[1], w[2], w[3]);
-      any_bad = 1;
-    }
-    *reinterpret_cast<uint4*>(sv + t * pv + c) = x;
+    const int64_t at = t < n ? ((seq.tok0 + t) * p.H + h) * p.dv + c : 0;
+    copy16(sv + t * pv + c, static_cast<const T*>(p.v) + at, t < n);
   }
-  if (!make_tree<T>(p, seq, h, &tree)) {  // (its barriers are those of the rows too)
+  const TreeIn in = tree_in<T>(p, seq, h);
+  for (int i = threadIdx.x; i < p.dv; i += blockDim.x) bad[i] = 0;
+  if (threadIdx.x == 0) any_bad = 0;
+  if (!make_tree(p, seq, in, h, &tree)) {
     if (first) attn_flag(p.status, kFlagBadCache);
+    asm volatile("cp.async.wait_all;" ::: "memory");
     return;
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  for (int i = threadIdx.x; i < 16 * mt * (p.dv / 8); i += blockDim.x) {  // (the thread's own copies)
+    const int t = i / (p.dv / 8), c = i % (p.dv / 8) * 8;
+    uint4* at = reinterpret_cast<uint4*>(sv + t * pv + c);
+    const uint4 x = *at;
+    if (finite2(x.x) && finite2(x.y) && finite2(x.z) && finite2(x.w)) continue;
+    uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t ones = e & 1 ? 0x7f800000u : 0x7f80u;
+      if ((w[e / 2] & ones) != ones) continue;
+      atomicOr(&bad[c + e], 1ull << t);
+      w[e / 2] &= e & 1 ? 0xffffu : 0xffff0000u;
+    }
+    *at = make_uint4(w[0], w[1], w[2], w[3]);
+    any_bad = 1;
+  }
+  __syncthreads();
   const bool found = any_bad != 0;
   // four channels of a token's query or key
   auto four = [&](const T* x, int tok, int kb) { return *reinterpret_cast<const uint2*>(x + tok * kPitch + 16 * kb + 4 * ti); };
-  float acc[MT][4][4];
+  float acc[MW][4][4];
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int u = 0; u < MW; ++u)
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[m][j][e] = 0.f;
+      for (int e = 0; e < 4; ++e) acc[u][j][e] = 0.f;
 #pragma unroll
   for (int k0 = 0; k0 < KB; k0 += NB) {
     uint32_t b0[NB][4], b1[NB][4];
@@ -364,15 +410,17 @@ __global__ void __launch_bounds__(256) lin_draft_mma(const LinParams p) {
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
+      for (int u = 0; u < MW; ++u) {
+        const int m = tile_of(u);
         if (m >= mt) continue;
         const uint2 x = four(sq, 16 * m + gi, k0 + b), y = four(sq, 16 * m + gi + 8, k0 + b);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) mma16816(acc[m][j], x.x, y.x, x.y, y.y, b0[b][j], b1[b][j]);
+        for (int j = 0; j < 4; ++j) mma16816(acc[u][j], x.x, y.x, x.y, y.y, b0[b][j], b1[b][j]);
       }
   }
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
+  for (int um = 0; um < MW; ++um) {
+    const int m = tile_of(um);
     if (m >= mt) continue;
     const int r0 = 16 * m + gi, r1 = r0 + 8;  // the thread's two tokens
     const LogSum none{0.f, 0.f};
@@ -382,10 +430,10 @@ __global__ void __launch_bounds__(256) lin_draft_mma(const LinParams p) {
       const float f0 = exp2f(g0.i + g0.f), f1 = exp2f(g1.i + g1.f);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        acc[m][j][0] *= f0;
-        acc[m][j][1] *= f0;
-        acc[m][j][2] *= f1;
-        acc[m][j][3] *= f1;
+        acc[um][j][0] *= f0;
+        acc[um][j][1] *= f0;
+        acc[um][j][2] *= f1;
+        acc[um][j][3] *= f1;
       }
     }
     // sixteen earlier tokens at a time: their weights are the next product's fragments
@@ -424,7 +472,7 @@ __global__ void __launch_bounds__(256) lin_draft_mma(const LinParams p) {
         const uint32_t pick = j & 1 ? 0x7632u : 0x5410u;
         const uint32_t b0 = __byte_perm(j < 2 ? v[0].x : v[0].y, j < 2 ? v[1].x : v[1].y, pick),
                        b1 = __byte_perm(j < 2 ? v[2].x : v[2].y, j < 2 ? v[3].x : v[3].y, pick);
-        mma16816(acc[m][j], pack2(w[0][0], w[0][1]), pack2(w[0][2], w[0][3]), pack2(w[1][0], w[1][1]),
+        mma16816(acc[um][j], pack2(w[0][0], w[0][1]), pack2(w[0][2], w[0][3]), pack2(w[1][0], w[1][1]),
                  pack2(w[1][2], w[1][3]), b0, b1);
       }
     }
@@ -436,8 +484,8 @@ __global__ void __launch_bounds__(256) lin_draft_mma(const LinParams p) {
       float x[8];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        x[j] = acc[m][j][2 * r] * p.scale;
-        x[4 + j] = acc[m][j][2 * r + 1] * p.scale;
+        x[j] = acc[um][j][2 * r] * p.scale;
+        x[4 + j] = acc[um][j][2 * r + 1] * p.scale;
       }
       if (found)
 #pragma unroll
@@ -541,14 +589,21 @@ cudaError_t launch_dk(const LinParams& p, cudaStream_t stream) {
 template <int DK>
 cudaError_t launch_draft_mma(const LinParams& p, cudaStream_t stream) {
   const dim3 grid((unsigned)p.num_seqs, (unsigned)p.H);
-  const int threads = 32 * ((p.dv + 31) / 32);
-  auto run = [&](auto kernel, int tokens) {
+  const int wide = (p.dv + 31) / 32;
+  auto run = [&](auto kernel, int tokens, int groups) {
+    const int threads = 32 * wide * groups;
     const size_t smem = (size_t)tokens * (2 * (DK + kRowPad) + p.dv + kRowPad) * sizeof(__nv_bfloat16);
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     return e != cudaSuccess ? e : launch_maybe_dependent(true, kernel, grid, dim3(threads), smem, stream, p);
   };
-  return p.max_seqlen <= 16 ? run(lin_draft_mma<DK, 1>, 16)
-                            : p.max_seqlen <= 32 ? run(lin_draft_mma<DK, 2>, 32) : run(lin_draft_mma<DK, 4>, 64);
+  if (p.max_seqlen <= 16) return run(lin_draft_mma<DK, 1, 1>, 16, 1);
+  // as many groups as eight warps allow while the CTAs are at most two an SM: nine trees of
+  // 60 tokens, 32 heads and 64 columns 23.2 -> 19.1 us, but 64 trees and 128 columns 134 -> 165
+  const bool split = (int64_t)p.num_seqs * p.H <= 2 * kLinSms;
+  if (p.max_seqlen <= 32)
+    return split && wide <= 4 ? run(lin_draft_mma<DK, 2, 1>, 32, 2) : run(lin_draft_mma<DK, 2, 2>, 32, 1);
+  if (split && wide <= 2) return run(lin_draft_mma<DK, 4, 1>, 64, 4);
+  return split && wide <= 4 ? run(lin_draft_mma<DK, 4, 2>, 64, 2) : run(lin_draft_mma<DK, 4, 4>, 64, 1);
 }
 
 template <typename T>
