@@ -18,12 +18,12 @@ constexpr int kLinSms = 152;
 
 // A CTA's slice of a state: DK x DVS elements, a float4 of VPT for each thread
 // (narrow: at most 32 columns, for calls too small to fill the GPU otherwise)
-template <int DK, int DV, bool kNarrow = false, int kMost = kThreads>
+template <int DK, int DV, bool kNarrow = false, int kElems = 16384>
 struct Tile {
-  static constexpr int kWide = DK * DV > 16384 ? 16384 / DK : DV;
+  static constexpr int kWide = DK * DV > kElems ? kElems / DK : DV;
   static constexpr int DVS = kNarrow && kWide > 32 ? 32 : kWide;  // columns
   static constexpr int QPR = DVS / 4;                            // float4 of a row
-  static constexpr int NT = DK * QPR < kMost ? DK * QPR : kMost;
+  static constexpr int NT = DK * QPR < kThreads ? DK * QPR : kThreads;
   static constexpr int NRG = NT / QPR;                           // rows that the threads cover at once
   static constexpr int VPT = DK / NRG;
   static_assert(NT % QPR == 0 && DK % NRG == 0, "threads tile the slice");
@@ -111,11 +111,11 @@ __device__ __forceinline__ bool load_parents(const LinParams& p, const LinSeq& s
 // on the path or not (a wait for them behind the walk took a quarter of the time).
 constexpr int kBatch = 16;  // tokens in shared memory at a time
 
-// (512 threads a slice of 64 KB: with 256 the state left too few registers for the rest)
+// (slices of 32 KB: with 64 KB the state left too few registers for the rest)
 template <int DK, int DV>
-using CommitTile = Tile<DK, DV, false, 2 * kThreads>;
+using CommitTile = Tile<DK, DV, false, 8192>;
 template <typename T, int DK, int DV>
-__global__ void __launch_bounds__(CommitTile<DK, DV>::NT, 2) lin_commit(const LinParams p) {
+__global__ void __launch_bounds__(CommitTile<DK, DV>::NT, 4) lin_commit(const LinParams p) {
   using L = CommitTile<DK, DV>;
   constexpr int kB = DK == 256 ? kBatch / 2 : kBatch;
   __shared__ float sk[kB][DK];
@@ -557,7 +557,10 @@ cudaError_t launch_state(const LinParams& p, cudaStream_t stream) {
   using L = Tile<DK, DV>;
   using N = Tile<DK, DV, true>;
   const dim3 grid((unsigned)p.num_seqs, (unsigned)p.H, DV / L::DVS), narrow(grid.x, grid.y, DV / N::DVS);
-  if (kCommit) return launch_maybe_dependent(true, lin_commit<T, DK, DV>, grid, dim3(CommitTile<DK, DV>::NT), 0, stream, p);
+  if (kCommit) {
+    using M = CommitTile<DK, DV>;
+    return launch_maybe_dependent(true, lin_commit<T, DK, DV>, dim3(grid.x, grid.y, DV / M::DVS), dim3(M::NT), 0, stream, p);
+  }
   // fewer CTAs than SMs (one row of 32 heads of 128 x 128: 6.1 us in whole states)
   if (N::DVS < L::DVS && (int64_t)grid.x * grid.y * grid.z < kLinSms)
     return launch_maybe_dependent(true, lin_decode<T, DK, DV, true>, narrow, dim3(N::NT), 0, stream, p);
