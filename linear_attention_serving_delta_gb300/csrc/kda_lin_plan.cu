@@ -59,6 +59,50 @@ __device__ int64_t scan(int64_t x, int64_t* part, int64_t* total) {
   return warp > 0 ? x + before : x;
 }
 
+// Sequence base + thread, with its chunks and its first record, and *before moved on by all of them
+struct LinCounted {
+  LinSeq seq;
+  int32_t chunks;
+  int64_t rec;
+};
+__device__ LinCounted count_chunks(const LinParams& p, const LinPlan& a, int base, int64_t* part, int64_t* before) {
+  const int s = base + threadIdx.x;
+  LinCounted c{};
+  if (s < p.num_seqs) c.seq = lin_seq(p, s);
+  c.chunks = c.seq.ok ? (int32_t)((c.seq.len + a.chunk - 1) / a.chunk) : 0;
+  int64_t total;
+  c.rec = *before + scan(c.chunks, part, &total) - c.chunks;
+  *before += total;
+  // (sequences that overlap between malformed ones may have more chunks than there are records)
+  if (c.seq.ok && c.rec + c.chunks > a.max_records) {
+    c.seq.ok = false;
+    c.seq.flag = kFlagBadSeqlens;
+  }
+  return c;
+}
+
+// The gate records of a CTA: of some chunks where there are fewer than 32 heads, a warp
+// each, otherwise of one chunk and 32 heads.  It counts the chunks for itself, so that it
+// runs beside the plan.
+__device__ __forceinline__ int gate_chunks(int H) { return H < 32 ? 32 / H : 1; }
+__device__ void gates_role(const LinParams& p, const LinPlan& a, int64_t x0, int h0, int64_t* part) {
+  __shared__ LinMine of[32];  // the chunks' tokens
+  const int mine = gate_chunks(p.H), warp = threadIdx.x >> 5;
+  if (threadIdx.x < 32) of[threadIdx.x].len = 0;
+  int64_t before = 0;
+  for (int base = 0; base < p.num_seqs && before <= x0 + mine - 1; base += kPlanThreads) {
+    const LinCounted c = count_chunks(p, a, base, part, &before);
+    if (!c.seq.ok) continue;
+    for (int64_t x = max(x0, c.rec); x < min(x0 + mine, c.rec + c.chunks); ++x)
+      of[x - x0] = LinMine{(int32_t)c.seq.tok0, (int32_t)c.seq.len, (int32_t)(x - c.rec), 0, 0, 0};
+  }
+  __syncthreads();
+  const int c = p.H < 32 ? warp / p.H : 0, h = p.H < 32 ? warp % p.H : h0 + warp;
+  if (c >= mine || h >= p.H || of[c].len == 0) return;
+  make_gates(p, of[c].tok0, of[c].len, of[c].rec * kLinChunk, h, &a.records[(x0 + c) * p.H + h]);
+}
+
+// Block 0 plans, the others make the gate records
 __global__ void __launch_bounds__(kPlanThreads) lin_plan(const LinParams p, const LinPlan a) {
   __shared__ int64_t part[32];
   __shared__ int32_t hist[kBuckets];
@@ -67,25 +111,22 @@ __global__ void __launch_bounds__(kPlanThreads) lin_plan(const LinParams p, cons
   const int tid = threadIdx.x, per = p.H * a.tiles;
   pdl_launch_dependents();
   pdl_wait();
+  if (blockIdx.x > 0) {
+    gates_role(p, a, (int64_t)(blockIdx.x - 1) * gate_chunks(p.H), blockIdx.y * 32, part);
+    return;
+  }
+  if (blockIdx.y > 0) return;
   for (int i = tid; i < kBuckets; i += kPlanThreads) hist[i] = 0;
   // chunks and records
   auto chunks_of = [&](const LinSeq& q) { return (int32_t)((q.len + a.chunk - 1) / a.chunk); };
   int64_t chunks = 0, active = 0, total;
   for (int base = 0; base < p.num_seqs; base += kPlanThreads) {
     const int s = base + tid;
-    LinSeq q{};
-    if (s < p.num_seqs) q = lin_seq(p, s);
-    const int32_t n = q.ok ? chunks_of(q) : 0;
-    const int64_t rec = chunks + scan(n, part, &total) - n;
-    chunks += total;
-    // (sequences that overlap between malformed ones may have more chunks than there are records)
-    if (q.ok && rec + n > a.max_records) {
-      q.ok = false;
-      q.flag = kFlagBadSeqlens;
-    }
+    const LinCounted c = count_chunks(p, a, base, part, &chunks);
+    const LinSeq& q = c.seq;
     if (q.flag) attn_flag(p.status, q.flag);
-    if (s < p.num_seqs) a.seq_rec[s] = q.ok ? (int32_t)rec : -1;
-    if (base == 0) first_n[tid] = q.ok ? max(n, 1) : 0;
+    if (s < p.num_seqs) a.seq_rec[s] = q.ok ? (int32_t)c.rec : -1;
+    if (base == 0) first_n[tid] = q.ok ? max(c.chunks, 1) : 0;
     active += __syncthreads_count(q.ok);
   }
   // chunks of a segment: the least with which all chains fit the CTAs at once, or where
@@ -206,35 +247,6 @@ __global__ void __launch_bounds__(kPlanThreads) lin_plan(const LinParams p, cons
   }
 }
 
-// A CTA per chunk and eight heads, a warp each
-__global__ void __launch_bounds__(256) lin_gates(const LinParams p, const LinPlan a, LinGates* records) {
-  pdl_launch_dependents();
-  pdl_wait();
-  const int64_t x = blockIdx.x;
-  // the last sequence whose records start at or before x (skipped ones: found by those before them)
-  int lo = 0, hi = p.num_seqs - 1, found = -1;
-  while (lo <= hi) {
-    int mid = (lo + hi) >> 1, y = mid;
-    while (y >= lo && a.seq_rec[y] < 0) --y;
-    if (y < lo) {
-      lo = mid + 1;
-      continue;
-    }
-    if (a.seq_rec[y] <= x) {
-      found = y;
-      lo = mid + 1;
-    } else {
-      hi = y - 1;
-    }
-  }
-  if (found < 0) return;
-  const LinSeq q = lin_seq(p, found);
-  const int64_t c = x - a.seq_rec[found];
-  if (c * kLinChunk >= q.len) return;
-  const int h = blockIdx.y * 8 + (threadIdx.x >> 5);
-  if (h < p.H) make_gates(p, q.tok0, (int)q.len, (int)(c * kLinChunk), h, &records[x * p.H + h]);
-}
-
 // Start states of segments 2, 3, ...: a thread four elements
 __global__ void __launch_bounds__(256) lin_combine(const LinParams p, const LinPlan a) {
   __shared__ float decay[kLinMostSegments];
@@ -340,16 +352,18 @@ LinPlan lin_plan_of(const LinParams& p, const LinShare& sh, const LinLayout& L, 
   a.max_records = lin_max_records(p, sh.chunk);
   a.may_split = L.may_split;
   a.states = reinterpret_cast<float*>(w + L.states);
-  a.records = sh.records ? reinterpret_cast<const LinGates*>(w + L.records) : nullptr;
+  a.records = sh.records ? reinterpret_cast<LinGates*>(w + L.records) : nullptr;
   a.logs = sh.records ? nullptr : reinterpret_cast<float*>(w + L.logs);
   return a;
 }
 
 cudaError_t launch_lin_plan(const LinParams& p, const LinPlan& a, cudaStream_t stream) {
-  return launch_maybe_dependent(true, lin_plan, dim3(1), dim3(kPlanThreads), 0, stream, p, a);
-}
-cudaError_t launch_lin_gates(const LinParams& p, const LinPlan& a, LinGates* records, cudaStream_t stream) {
-  return launch_maybe_dependent(true, lin_gates, dim3((unsigned)a.max_records, (unsigned)((p.H + 7) / 8)), dim3(256), 0, stream, p, a, records);
+  dim3 grid(1);
+  if (a.records) {
+    const int64_t each = p.H < 32 ? 32 / p.H : 1;
+    grid = dim3((unsigned)(1 + (a.max_records + each - 1) / each), (unsigned)((p.H + 31) / 32));
+  }
+  return launch_maybe_dependent(true, lin_plan, grid, dim3(kPlanThreads), 0, stream, p, a);
 }
 cudaError_t launch_lin_combine(const LinParams& p, const LinPlan& a, cudaStream_t stream) {
   const int64_t size = (int64_t)p.dk * p.dv;

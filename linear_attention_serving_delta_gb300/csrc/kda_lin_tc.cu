@@ -901,7 +901,6 @@ cudaError_t launch_shape(const LinParams& p, void* ws, cudaStream_t stream) {
   const LinPlan plan = lin_plan_of(p, sh, L, ws);
   a.states = plan.states;
   if ((e = launch_lin_plan(p, plan, stream)) != cudaSuccess) return e;
-  if ((e = launch_lin_gates(p, plan, a.records, stream)) != cudaSuccess) return e;
   if (L.may_split) {
     a.items = plan.locals;
     a.num_items = &plan.head->locals;

@@ -79,7 +79,7 @@ struct LinPlan {
   int32_t may_split;
   float* states;           // [places][H][dk][dv] start states of segments
   // log2 of the decay of the segment before a place: from the records, or [places][H]
-  const LinGates* records;
+  LinGates* records;
   float* logs;
 };
 
@@ -99,7 +99,6 @@ LinShare lin_tc_share(const LinParams& p);
 LinLayout lin_layout(const LinParams& p, const LinShare& sh);
 LinPlan lin_plan_of(const LinParams& p, const LinShare& sh, const LinLayout& L, void* ws);
 cudaError_t launch_lin_plan(const LinParams& p, const LinPlan& a, cudaStream_t stream);
-cudaError_t launch_lin_gates(const LinParams& p, const LinPlan& a, LinGates* records, cudaStream_t stream);
 cudaError_t launch_lin_combine(const LinParams& p, const LinPlan& a, cudaStream_t stream);
 
 // Chunks of all sequences of a well-formed call, at most
