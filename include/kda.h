@@ -760,8 +760,12 @@ kda_status_t kda_kv_write(const kda_kv_write_args* args, void* stream);
  * of a call must not share a slot.  States are advanced with products and
  * sums to fp32 precision for both input types.  o is rounded once; with bf16
  * inputs the products q.k with their decays, and in prefill and draft the
- * state that o is read from, are rounded to bf16 before they multiply (the
- * tensor cores' operand type), each an error of at most 2^-8 of the term.
+ * state that o is read from (where a prompt's decays span more than 2^64 within
+ * 128 tokens, the queries with their decays too), are rounded to bf16 before
+ * they multiply (the tensor cores' operand type), each an error of at most 2^-8
+ * of the term.  Which of the two forms is taken, and so how an o rounds, may
+ * depend on the gates of later tokens of the sequence; results are the same
+ * bits for the same call every time.
  *
  * One step of a host that drafts tokens:
  *   kda_lin_draft   o of the drafted tokens, states as they were

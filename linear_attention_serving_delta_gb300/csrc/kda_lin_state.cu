@@ -3,10 +3,12 @@
 // (commit), drafted tokens over the states as they are (draft).  Formulas in
 // include/kda.h.
 //
-// Decode and commit read every state once and write it once and do little
-// else, so they are bound by HBM: a CTA takes one (row, head) -- or a slice
-// of 16,384 elements of a wide one -- with 16-byte loads straight into
-// registers, all issued before anything waits, and writes them back from there.
+// All three are bound by HBM.  Decode and commit read every state once, write it once and do
+// little else: a CTA takes one (row, head), or a slice of a wide one, with 16-byte loads
+// straight into registers, all issued before anything waits, and writes them back from
+// there.  256 rows of 32 heads of 128 x 128: 158 us, 6.85 TB/s, what a copy reaches; one row
+// 2.9 us, a launch.  The commit of 64 trees of 8 tokens takes 51 us, 5.3 TB/s (the path comes
+// between its reads and its writes); their draft, which only reads, 36 us, 4.2 TB/s.
 #include "kda_lin.cuh"
 
 namespace kda {

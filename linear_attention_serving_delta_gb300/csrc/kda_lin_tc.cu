@@ -4,16 +4,19 @@
 // Chunks of C = 128 tokens, with G_i = sum_{m <= i} log2 alpha_m within a chunk:
 //
 //   P = Q K^T                          tcgen05
-//   P~_ij = 2^{G_i - G_j} P_ij, j <= i rounded to bf16, into P's columns of TMEM
-//   Q~_i = 2^{G_i} q_i                 the same, beside them
-//   O = Q~ S + P~ V                    tcgen05, A from TMEM; S rounded to bf16 for this alone
+//   P~_ij = 2^{-G_j} P_ij, j <= i      rounded to bf16, into P's columns of TMEM
+//   O = 2^{G_i} (Q S + P~ V)           tcgen05, P~ from TMEM; S rounded to bf16 for this alone
 //   S <- 2^{G_C} S + K~^T V            K~_j = 2^{G_C - G_j} k_j in two bf16 parts, A from TMEM
+//
+// That is for a weak chunk, |G| <= 64: both factors stay within fp32 and bf16 by far, and
+// one of them is left to the epilogue.  In a strong one P~_ij = 2^{G_i - G_j} P_ij, the
+// difference taken before the exponential (over whole blocks of 32 tokens as a product of two
+// factors <= 1), and the queries are multiplied by theirs, Q~_i = 2^{G_i} q_i in bf16 beside P~.
 //
 // K~ = hi + lo leaves out less than 2^-16 of a term, so states keep fp32's
 // precision to about 1e-6 in norm (hi alone: 1e-3); the product starts from zero in each
 // chunk and is added to S in registers, rounded to nearest (the tensor cores'
-// own accumulation cuts, a bias that grows with the chunks).  All exponents
-// are <= 0 and taken as differences before the exponential.
+// own accumulation cuts, a bias that grows with the chunks).
 //
 // A CTA runs one chain: a sequence (or a segment of one) of a head and DV columns
 // of its state, chunk after chunk.  Warp 0 copies, 1 issues the products of the
@@ -23,6 +26,14 @@
 // a thread's registers, and K~, whose transposition ldmatrix and the 16-lane stores
 // to TMEM make.  The gates' sums of each (chunk, head) are a record in the workspace
 // (kda_lin_tc.cuh), made before: as a role of their own they took the longest.
+//
+// What it takes (a copy reaches 6.8 TB/s): 8,192 tokens of 32 heads of 128 x 128 in
+// 111 us, of which the plan 9, the segments' own states 37, the combination 6 and the
+// outputs 63, each traced by itself; eight prompts of 1,024 to 32,768 tokens in 1.28 ms, 4.5 TB/s.
+// An SM does a chunk in 3.1 to 3.9 us there, against 2.9 of HBM for its 128 KB at an
+// SM's share; what is beyond that is 256 chains that 152 SMs cannot share evenly.  64
+// columns a chain take 3 us a chunk all the same: then a chunk's chain of waits -- products,
+// state, operand, products, outputs -- bounds it, one chain an SM.
 //
 // Roles run side by side on the schedulers' small instruction caches: unrolled ones of
 // 140 KB together issued an instruction in 6 to 10 cycles.  What waits for shared

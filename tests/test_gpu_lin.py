@@ -389,6 +389,39 @@ def test_prefill_f32_long_slots_in_place_and_in_a_graph():
         assert torch.equal(o, first) and torch.equal(pool, after)
 
 
+@pytest.mark.parametrize("dtype,lens", [("bf16", [130, 7]), ("bf16", [2500, 130]), ("f32", [90]), ("f32", [700, 33])])
+def test_prefill_rows_behind_the_last_sequence(dtype, lens):
+    H, dk, more = 2, 64, 70
+    T = sum(lens)
+    d = inputs(23, T + more, H, H, dk, dk, dtype, "g")
+    for x in ("q", "k", "v", "g"):
+        d[x][T:] = float("nan")
+    o = torch.full((T + more, H, dk), 7.0, device="cuda", dtype=DT[dtype])
+    call = kda.LinPrefill(d["q"], d["k"], d["v"], offsets(lens), g=d["g"], o=o).run()
+    check_prefill({**d, "v": d["v"][:T], "q": d["q"][:T], "k": d["k"][:T], "g": d["g"][:T]}, lens, H, dk, dtype, o[:T],
+                  call.final_state, 1.0)
+    assert bool((o[T:] == 7).all()) and call.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_prefills_at_once_on_two_streams(dtype):
+    lens, H, dk = [1500, 400], 4, 64
+    calls, want = [], []
+    for i in range(2):
+        d = inputs(200 + i, sum(lens), H, 2, dk, dk, dtype, "g", n=2)
+        calls.append(kda.LinPrefill(d["q"], d["k"], d["v"], offsets(lens), g=d["g"], initial_state=d["state"]))
+        calls[i].run()
+        want.append((calls[i].o.clone(), calls[i].final_state.clone()))
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for c, s in zip(calls, streams):
+            c.run(s)
+    torch.cuda.synchronize()
+    for c, (o, f) in zip(calls, want):
+        assert torch.equal(c.o, o) and torch.equal(c.final_state, f)
+
+
 def test_prefill_long_unaligned():
     lens, H, dk = [1100, 20], 2, 64
     d = inputs(19, sum(lens), H, H, dk, dk, "bf16", "g")
@@ -516,6 +549,17 @@ def test_draft_and_commit_sizes(dtype, dk, dv):
     c.run()
     assert c.device_status() == 0
     check_commit(d, lens, par, H, dk, pool, last, slots)
+
+
+@pytest.mark.parametrize("most,dv", [(30, 32), (60, 64), (60, 128)])
+def test_draft_many_requests(most, dv):
+    """More CTAs than the small calls' split of a tree's tiles allows."""
+    H, dk, n = 8, 64, 40
+    lens = [(7 * i + 3) % (most + 1) for i in range(n)]
+    d = inputs(most + dv, sum(lens), H, 2, dk, dv, "bf16", "g", n=n)
+    par = make_tree("tree", lens, 5)
+    o = kda.lin_draft(d["q"], d["k"], d["v"], offsets(lens), d["state"], parents=par.cuda(), g=d["g"], max_seqlen=most)
+    check_draft(d, lens, par, H, dk, "bf16", o, 1.0)
 
 
 def check_commit(d, lens, par, H, dk, pool, last, slots, untouched=True):
