@@ -4,16 +4,18 @@
 // path, and the start states of the segments.
 //
 // A chain is a walk over its chunks, and a call with few sequences and heads has
-// fewer chains than the GPU has SMs.  Then sequences are cut into segments of equal
-// length: a first pass leaves the end state of every segment but the last one,
-// B_i, from zeros (the first from the initial state); with the decay D_i of a
-// segment its start state follows as
+// fewer chains than the GPU has SMs.  Then sequences are cut into segments: a first pass
+// leaves the end state B_i of every segment but the last one, of the first segment from the
+// initial state and with its outputs, of the others from zeros and without; with the
+// decay D_i of a segment the start states follow as
 //
-//   S_0 = S,   S_1 = B_0,   S_{i+1} = D_i S_i + B_i
+//   S_1 = B_0,   S_{i+1} = D_i S_i + B_i
 //
 // (the recurrence is affine in S, and its linear part one factor), and a
-// second pass gives the outputs of all segments side by side.  Keys and values are
-// read twice, from L2 where the call's fit it.  One block plans, in 9 us for one
+// second pass gives the outputs of the other segments side by side.  So k segments are
+// k - 1 chains of either pass, and the first is as much shorter as its outputs take longer.
+// Keys and values of those between the first and the last are read twice, from L2 where
+// the call's fit it.  One block plans, in 9 us for one
 // prompt as for ninety: lengths, scans over the block, and a search for the length of
 // the segments that tries 32 at a time (one after the other took 4 us more, and
 // writing a prompt's segments by one thread 6 us).
@@ -148,7 +150,7 @@ __global__ void __launch_bounds__(kPlanThreads) lin_plan(const LinParams p, cons
         for (int s = lane; s < p.num_seqs; s += 32) {
           int32_t n = s < kPlanThreads ? first_n[s] : 0;
           if (s >= kPlanThreads && a.seq_rec[s] >= 0) n = max(chunks_of(lin_seq(p, s)), 1);
-          x += n > 0 ? (n - 1) / m + 1 : 0;
+          x += n > 0 ? lin_chains(n, m, a.first) : 0;
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
@@ -164,7 +166,7 @@ __global__ void __launch_bounds__(kPlanThreads) lin_plan(const LinParams p, cons
       limit = (int32_t)min(max((int64_t)a.min_segment, (2 * chunks * per + a.slots - 1) / a.slots), (int64_t)INT32_MAX);
     }
   }
-  auto segments_of = [&](int32_t n) { return n > limit ? (n - 1) / limit + 1 : 1; };
+  auto segments_of = [&](int32_t n) { return n > limit ? lin_chains(n, limit, a.first) + 1 : 1; };
   __syncthreads();
   // A thread a sequence; the segments of one that is cut by all lanes of its warp
   auto each_segment = [&](int32_t n, int32_t k, auto one) {
@@ -180,7 +182,8 @@ __global__ void __launch_bounds__(kPlanThreads) lin_plan(const LinParams p, cons
     const bool ok = s < p.num_seqs && a.seq_rec[s] >= 0;
     const int32_t n = ok ? chunks_of(lin_seq(p, s)) : 0;
     each_segment(n, ok ? segments_of(n) : 0, [&](int, int32_t n, int32_t k, int32_t i) {
-      atomicAdd(&hist[bucket_of(lin_cut(n, k, i + 1) - lin_cut(n, k, i))], 1);
+      if (k > 1 && i == 0) return;  // (the first pass has done it)
+      atomicAdd(&hist[bucket_of(lin_cut(n, k, i + 1, a.first) - lin_cut(n, k, i, a.first))], 1);
     });
   }
   __syncthreads();
@@ -223,21 +226,22 @@ __global__ void __launch_bounds__(kPlanThreads) lin_plan(const LinParams p, cons
     __syncwarp();
     each_segment(n_s, k, [&](int lane, int32_t n, int32_t k, int32_t i) {
       const LinMine m = mine_of[(tid & ~31) + lane];
-      const int32_t c0 = lin_cut(n, k, i), c1 = lin_cut(n, k, i + 1);
+      const int32_t c0 = lin_cut(n, k, i, a.first), c1 = lin_cut(n, k, i + 1, a.first);
       const int32_t from = p.state_in ? m.row : -1, to = p.state_out ? m.row : -1;
       LinItem it{};
       it.tok0 = m.tok0 + c0 * a.chunk;
       it.len = min((c1 - c0) * a.chunk, m.len - c0 * a.chunk);
       it.rec = m.rec + c0;
-      it.copy = -1;
-      // (the first segment starts from a copy: the last one may write the pool in place meanwhile)
-      it.from = k == 1 || (i == 0 && !p.state_in) ? from : m.place + i;
-      it.to = i + 1 == k ? to : -1;
-      a.items[atomicAdd(&hist[bucket_of(c1 - c0)], 1)] = it;
+      it.outputs = 1;
+      if (k == 1 || i > 0) {
+        it.from = k == 1 ? from : m.place + i;
+        it.to = i + 1 == k ? to : -1;
+        a.items[atomicAdd(&hist[bucket_of(c1 - c0)], 1)] = it;
+      }
       if (i + 1 < k) {
         it.from = i == 0 ? from : -1;
-        it.copy = i == 0 && p.state_in ? m.place : -1;
         it.to = m.place + i + 1;
+        it.outputs = i == 0;
         a.locals[m.local + i] = it;
       }
     });
@@ -267,7 +271,8 @@ __global__ void __launch_bounds__(256) lin_combine(const LinParams p, const LinP
         continue;
       }
       LogSum g{0.f, 0.f};
-      for (int c = lin_cut(sp.chunks, sp.segments, i) + (threadIdx.x & 31); c < lin_cut(sp.chunks, sp.segments, i + 1); c += 32)
+      for (int c = lin_cut(sp.chunks, sp.segments, i, a.first) + (threadIdx.x & 31);
+           c < lin_cut(sp.chunks, sp.segments, i + 1, a.first); c += 32)
         g = g + log_sum(a.records[((int64_t)sp.rec + c) * p.H + h].head.total);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1)
@@ -308,7 +313,7 @@ int lin_tile_width(const LinParams& p) { return p.dk > 128 || p.dv <= 64 ? 64 : 
 
 LinShare lin_tc_share(const LinParams& p) {
   const int w = lin_tile_width(p);
-  return LinShare{(p.dv + w - 1) / w, kLinSlots, kLinChunk, kLinMinSegment, kLinDirectTokens, true};
+  return LinShare{(p.dv + w - 1) / w, kLinSlots, kLinChunk, kLinMinSegment, kLinFirst, kLinDirectTokens, true};
 }
 
 LinLayout lin_layout(const LinParams& p, const LinShare& sh) {
@@ -319,7 +324,8 @@ LinLayout lin_layout(const LinParams& p, const LinShare& sh) {
   L.direct = p.total_tokens <= sh.direct_tokens && p.num_seqs * per <= 2 * sh.slots;
   // with more than half as many chains a sequence as CTAs no cut would fit
   L.may_split = !L.direct && 2 * per <= sh.slots && p.total_tokens > sh.min_segment * sh.chunk;
-  L.places = L.may_split ? sh.slots / per + 2 : 0;
+  // (a segment more than chains of a pass for each sequence that is cut)
+  L.places = L.may_split ? 2 * (sh.slots / per) + 2 : 0;
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t at = off;
@@ -351,6 +357,7 @@ LinPlan lin_plan_of(const LinParams& p, const LinShare& sh, const LinLayout& L, 
   a.tiles = sh.tiles;
   a.slots = sh.slots;
   a.min_segment = sh.min_segment;
+  a.first = sh.first;
   a.chunk = sh.chunk;
   a.max_records = lin_max_records(p, sh.chunk);
   a.may_split = L.may_split;

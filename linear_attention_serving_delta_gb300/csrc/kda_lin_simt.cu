@@ -28,15 +28,15 @@ constexpr int kThreads = 256, kWarps = 8;
 // key channels leave no registers for two)
 int cols_of(const LinParams& p) { return p.dk == 256 ? 1 : (p.dv > 32 ? 2 : 1); }
 
-// kLocal: segments' own end states alone, no outputs
-template <typename T, int DK, int NC, bool kLocal>
+// kFirst: the first pass over segments, most of which leave their end states alone
+template <typename T, int DK, int NC, bool kFirst>
 __global__ void __launch_bounds__(kThreads, 3) lin_simt(const LinParams p, const LinPlan a, const bool planned) {
   constexpr int R = DK / kWarps, kCols = 32 * NC;      // key channels of a thread, columns of the CTA
   constexpr int kTok = DK > 64 ? 8 : 16;               // tokens of a block: 48 KB hold them
   constexpr int kQK = kTok * DK / kThreads, kV = kTok * kCols / kThreads;  // a thread's share
   static_assert(kQK * kThreads == kTok * DK && kV * kThreads == kTok * kCols, "whole shares");
   __shared__ __align__(16) float sq[kTok][DK], sk[kTok][DK];
-  __shared__ __align__(16) float sv[kTok][kCols], so[kLocal ? 1 : kWarps][kTok][kCols];
+  __shared__ __align__(16) float sv[kTok][kCols], so[kWarps][kTok][kCols];
   __shared__ LinDecay sa[kTok];
   __shared__ float sl[kTok];
   pdl_launch_dependents();
@@ -45,15 +45,16 @@ __global__ void __launch_bounds__(kThreads, 3) lin_simt(const LinParams p, const
   const int h = blockIdx.y, c0 = blockIdx.z * kCols, cols = min(kCols, p.dv - c0);
   LinItem it{};
   if (planned) {
-    if ((int)blockIdx.x >= (kLocal ? a.head->locals : a.head->items)) return;
-    it = (kLocal ? a.locals : a.items)[blockIdx.x];
+    if ((int)blockIdx.x >= (kFirst ? a.head->locals : a.head->items)) return;
+    it = (kFirst ? a.locals : a.items)[blockIdx.x];
   } else {
     const LinSeq seq = lin_seq(p, blockIdx.x);
     if (seq.flag && tid == 0 && h == 0 && c0 == 0) attn_flag(p.status, seq.flag);
     if (!seq.ok) return;
     const int row = -2 - seq.slot;
-    it = LinItem{(int32_t)seq.tok0, (int32_t)seq.len, h, 0, p.state_in ? row : -1, p.state_out ? row : -1, 0, -1};
+    it = LinItem{(int32_t)seq.tok0, (int32_t)seq.len, h, 0, p.state_in ? row : -1, p.state_out ? row : -1, 0, 1};
   }
+  const bool local = kFirst && !it.outputs;
   // element i of the thread's columns: lane + 32 i
   float S[R][NC];
   auto state_at = [&](int32_t place) {
@@ -72,7 +73,6 @@ __global__ void __launch_bounds__(kThreads, 3) lin_simt(const LinParams p, const
     for (int i = 0; i < R; ++i)
 #pragma unroll
       for (int j = 0; j < NC; ++j) S[i][j] = from && lane + 32 * j < cols ? from[(int64_t)i * p.dv + 32 * j] : 0.f;
-    if (kLocal && it.copy >= 0) put_state(a.states + state_at(it.copy));
   }
   // the next block of tokens, in registers: element u of a thread is kThreads on
   const int64_t row_k = (int64_t)p.Hk * DK, row_v = (int64_t)p.H * p.dv;
@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kThreads, 3) lin_simt(const LinParams p, const
     for (int u = 0; u < kQK; ++u) {
       const int t = u * (kThreads / DK);
       if (tk + t >= n) continue;
-      if (!kLocal) rq[u] = ld_in(q, (t0 + t) * row_k);
+      if (!local) rq[u] = ld_in(q, (t0 + t) * row_k);
       rk[u] = ld_in(k, (t0 + t) * row_k);
     }
 #pragma unroll
@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kThreads, 3) lin_simt(const LinParams p, const
     const int n = min(kTok, it.len - t0);
 #pragma unroll
     for (int u = 0; u < kQK; ++u) {
-      if (!kLocal) (&sq[0][0])[tid + u * kThreads] = rq[u];
+      if (!local) (&sq[0][0])[tid + u * kThreads] = rq[u];
       (&sk[0][0])[tid + u * kThreads] = rk[u];
     }
 #pragma unroll
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, 3) lin_simt(const LinParams p, const
     }
     __syncthreads();
     if (t0 + kTok < it.len) fetch(t0 + kTok);
-    if (kLocal && tid == 0)
+    if (local && tid == 0)
       for (int t = 0; t < n; ++t) sum = sum + log_sum(sl[t]);
 #pragma unroll 2
     for (int t = 0; t < n; ++t) {
@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, 3) lin_simt(const LinParams p, const
 #pragma unroll
           for (int j = 0; j < NC; ++j) S[i][j] = fmaf(d.m, S[i][j], sk[t][warp * R + i] * x[j]);
       }
-      if (kLocal) continue;
+      if (local) continue;
 #pragma unroll
       for (int i = 0; i < R; ++i)
 #pragma unroll
@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, 3) lin_simt(const LinParams p, const
       for (int j = 0; j < NC; ++j) so[warp][t][lane + 32 * j] = y[j];
     }
     __syncthreads();
-    if (kLocal) continue;
+    if (local) continue;
 #pragma unroll
     for (int u = 0; u < kV; ++u) {
       const int t = u * (kThreads / kCols);
@@ -158,14 +158,14 @@ __global__ void __launch_bounds__(kThreads, 3) lin_simt(const LinParams p, const
     }
   }
   if (it.to != -1) put_state((it.to >= 0 ? a.states : p.state_out) + state_at(it.to));
-  if (kLocal && c0 == 0 && tid == 0) a.logs[(int64_t)it.to * p.H + h] = sum.i + sum.f;
+  if (local && c0 == 0 && tid == 0) a.logs[(int64_t)it.to * p.H + h] = sum.i + sum.f;
 }
 
 // Three CTAs an SM (chains for four, with registers for two: 108 us where three with
 // registers for three took 87), in segments of 32 tokens and up (of 128: 87 us, of 32: 70)
 LinShare share(const LinParams& p) {
   const int cols = 32 * cols_of(p);
-  return LinShare{(p.dv + cols - 1) / cols, 3 * kLinSlots, 32, 1, 32, false};
+  return LinShare{(p.dv + cols - 1) / cols, 3 * kLinSlots, 32, 1, 8, 32, false};
 }
 
 template <typename T, int DK, int NC>

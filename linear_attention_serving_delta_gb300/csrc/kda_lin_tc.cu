@@ -51,6 +51,7 @@
 // of V and K~ behind the sequence are zeroed.
 #include <algorithm>
 #include <cstddef>
+#include <type_traits>
 
 #include "kda_lin_tc.cuh"
 
@@ -94,7 +95,7 @@ struct Tail {
   int32_t poisoned;       // the CTA's chain that nan_from speaks of, -1: none so far
   int32_t scaled_q;       // the chunk is strong, for the MMAs
   LinItem only;           // the CTA's chain where there is no plan
-  int32_t num_items, pad;
+  int32_t num_items, local;  // local: the CTA's chain leaves its end state alone
   alignas(16) LinGateHead gates[2];  // the records of two chunks
   // per channel the first token with a value that is not finite in the latest chain
   // that had one, counted through the CTA's chunks
@@ -127,7 +128,7 @@ __device__ __forceinline__ LinItem own_chain(const LinParams& p, const LinTcArgs
   if (flag && r == 0 && threadIdx.x == 0) attn_flag(p.status, flag);
   const int row = -2 - seq.slot;
   return LinItem{(int32_t)seq.tok0, ok ? (int32_t)seq.len : -1, r / a.tiles, r % a.tiles, p.state_in ? row : -1,
-                 p.state_out ? row : -1, (int32_t)rec, -1};
+                 p.state_out ? row : -1, (int32_t)rec, 1};
 }
 // Waits for `parity` of `bar`, for a second of an SM's fastest clock at most; false, with
 // *dead set, once that is over.  Few instructions, as 20 warps do it (a time limit of
@@ -655,8 +656,6 @@ __device__ void state_role(const LinParams& p, const LinTcArgs& a, char* sm, Tai
         s[u + 1] = y.y;
         s[u + 2] = y.z;
         s[u + 3] = y.w;
-        if (kLocal && ch.copy >= 0 && mine && c0 + u < p.dv)
-          *reinterpret_cast<float4*>(a.states + state_at(p, ch.copy, ch.head) + (int64_t)d * p.dv + c0 + u) = y;
       }
     }
     LinDecay decay{0.f, true};
@@ -793,7 +792,8 @@ __device__ void state_role(const LinParams& p, const LinTcArgs& a, char* sm, Tai
   }
 }
 
-template <int DK, int DV, bool kLocal>
+// kFirst: the first pass over segments, a chain a CTA, most of which leave their end states alone
+template <int DK, int DV, bool kFirst>
 __global__ void __launch_bounds__(kThreads, 1)
     lin_tc(const LinParams p, const LinTcArgs a, const __grid_constant__ CUtensorMap mq,
            const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
@@ -807,22 +807,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (uint64_t* x : {&b->q_full[s], &b->k_full[s], &b->v_full[s]}) mbar_init(x, 1);
       mbar_init(&b->v_ready[s], 4);
       mbar_init(&b->q_empty[s], 1);
-      mbar_init(&b->k_empty[s], kLocal ? 8 : 9);
       mbar_init(&b->v_done[s], 2);
-      mbar_init(&b->v_empty[s], kLocal ? 1 : 4);
     }
     for (uint64_t* x : {&b->p_full, &b->o_full, &b->kv_full[0], &b->kv_full[1], &b->drain[0], &b->drain[1], &b->g_full[0], &b->g_full[1]})
       mbar_init(x, 1);
     for (uint64_t* x : {&b->s_ready, &b->k_ready[0], &b->k_ready[1]}) mbar_init(x, 8);
     for (uint64_t* x : {&b->p_ready, &b->o_free}) mbar_init(x, 4);
-    for (uint64_t* x : {&b->g_free[0], &b->g_free[1]}) mbar_init(x, kLocal ? 8 : 12);
     b->dead = 0;
     b->poisoned = -1;
-    mbar_init_fence();
+    b->local = 0;
   }
   if (threadIdx.x == 32) {
-    if (!kLocal) prefetch_map(&mq);
-    if (!kLocal) prefetch_map(&mo);
+    prefetch_map(&mq);
+    prefetch_map(&mo);
     prefetch_map(&mk);
     prefetch_map(&mv);
   }
@@ -833,7 +830,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_after_sync();
   pdl_wait();  // the plan, or what came before
   if (a.items) {
-    if (threadIdx.x == 0) b->num_items = *a.num_items * p.H * a.tiles;  // (lin_tc_fits)
+    if (threadIdx.x == 0) {
+      const int32_t per = p.H * a.tiles, n = *a.num_items * per;  // (lin_tc_fits)
+      b->num_items = n;
+      if (kFirst && (int)blockIdx.x < n) b->local = !a.items[blockIdx.x / per].outputs;
+    }
   } else {
     // a chain of the CTA's own, and its records (the tiles of a head all make them, alike)
     const LinItem own = own_chain(p, a, reinterpret_cast<int64_t*>(sm));
@@ -842,27 +843,42 @@ __global__ void __launch_bounds__(kThreads, 1)
       make_gates(p, own.tok0, own.len, c * C, own.head, &a.records[((int64_t)own.rec + c) * p.H + own.head]);
     fence_proxy_async_global();
   }
+  if (threadIdx.x == 0) {
+    // what is not free for others before all who read it are done with it
+    const bool local = kFirst && b->local;
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&b->k_empty[s], local ? 8 : 9);
+      mbar_init(&b->v_empty[s], local ? 1 : 4);
+    }
+    for (uint64_t* x : {&b->g_free[0], &b->g_free[1]}) mbar_init(x, local ? 8 : 12);
+    mbar_init_fence();
+  }
   __syncthreads();
   // registers: 96 a thread at launch (640 x 96 = 61,440); 128 x (48 + 104 + 88 + 2 x 120)
-  if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-    if (warp == 0) {
-      if ((threadIdx.x & 31) == 0) copy_role<DK, DV, kLocal>(p, a, &mq, &mk, &mv, sm, b);
-    } else if (warp == 1) {
-      if (!kLocal) mma_out_role<DK, DV>(p, a, &mo, sm, b);
-    } else if (warp == 2) {
-      mma_state_role<DK, DV, kLocal>(p, a, sm, b);
+  auto roles = [&](auto kind) {
+    constexpr bool kLocal = decltype(kind)::value;
+    if (warp < 4) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+      if (warp == 0) {
+        if ((threadIdx.x & 31) == 0) copy_role<DK, DV, kLocal>(p, a, &mq, &mk, &mv, sm, b);
+      } else if (warp == 1) {
+        if (!kLocal) mma_out_role<DK, DV>(p, a, &mo, sm, b);
+      } else if (warp == 2) {
+        mma_state_role<DK, DV, kLocal>(p, a, sm, b);
+      }
+    } else if (warp < 8) {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+      weight_role<DK, DV, kLocal>(p, a, sm, b);
+    } else if (warp < 12) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+      if (!kLocal) out_role<DK, DV>(p, a, &mo, sm, b);
+    } else {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
+      state_role<DK, DV, kLocal>(p, a, sm, b);
     }
-  } else if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
-    weight_role<DK, DV, kLocal>(p, a, sm, b);
-  } else if (warp < 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (!kLocal) out_role<DK, DV>(p, a, &mo, sm, b);
-  } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
-    state_role<DK, DV, kLocal>(p, a, sm, b);
-  }
+  };
+  if (kFirst && b->local) roles(std::true_type{});
+  else roles(std::false_type{});
   __syncwarp();
   fence_before_sync();
   __syncthreads();
@@ -915,7 +931,7 @@ cudaError_t launch_shape(const LinParams& p, void* ws, cudaStream_t stream) {
   if (L.may_split) {
     a.items = plan.locals;
     a.num_items = &plan.head->locals;
-    if ((e = run(lin_tc<DK, DV, true>, std::min<int64_t>(sms, L.places * per))) != cudaSuccess) return e;
+    if ((e = run(lin_tc<DK, DV, true>, sh.slots / per * per)) != cudaSuccess) return e;
     if ((e = launch_lin_combine(p, plan, stream)) != cudaSuccess) return e;
   }
   a.items = plan.items;

@@ -12,20 +12,31 @@ constexpr int kLinChunk = 128;  // tokens of a chunk: the rows of a tensor-core 
 // One chain: tokens [tok0, tok0 + len) of a head's columns [tile * DV, ...).
 // from, to: the state it starts from and leaves, a place of the workspace's
 // states (>= 0), row -2 - x of the pool (<= -2), or none (-1).  rec: its first record.
-// copy: where the state it starts from goes too, or -1.  A plan holds one for all
-// heads and tiles.
+// outputs: whether the first pass makes its outputs too.  A plan holds one for all heads
+// and tiles.
 struct LinItem {
-  int32_t tok0, len, head, tile, from, to, rec, copy;
+  int32_t tok0, len, head, tile, from, to, rec, outputs;
 };
 
 // A sequence cut into segments, whose start states are at place, place + 1, ...
 struct LinSplit {
   int32_t place, segments, rec, chunks;
 };
-// Segment i of n chunks cut into k: its first chunk
-__host__ __device__ __forceinline__ int32_t lin_cut(int32_t n, int32_t k, int32_t i) {
-  const int32_t each = n / k, more = n - each * k;  // the first `more` have one more
-  return i * each + (i < more ? i : more);
+// Segment i of n chunks cut into k: its first chunk.  The first segment is shorter, `first`
+// tenths of another: the first pass makes its outputs too.
+__host__ __device__ __forceinline__ int32_t lin_cut(int32_t n, int32_t k, int32_t i, int32_t first) {
+  if (k == 1 || i == 0) return i == 0 ? 0 : n;
+  int32_t a = n * first / (10 * (k - 1) + first);
+  a = a > 1 ? a : 1;
+  const int32_t rest = n - a, each = rest / (k - 1), more = rest - each * (k - 1);  // `more` have one more
+  return a + (i - 1) * each + (i - 1 < more ? i - 1 : more);
+}
+// The chains of either pass that n chunks in segments of m give
+__host__ __device__ __forceinline__ int32_t lin_chains(int32_t n, int32_t m, int32_t first) {
+  if (n <= m) return 1;
+  int32_t a = (int32_t)((int64_t)m * first / 10);
+  a = a > 1 ? a : 1;
+  return n - a > m ? (n - a - 1) / m + 1 : 1;
 }
 
 struct LinHead {
@@ -34,6 +45,8 @@ struct LinHead {
 // The CTAs that chains are shared out to, and the fewest chunks of a segment
 constexpr int kLinSlots = 152;
 constexpr int kLinMinSegment = 8;
+// A chunk without its outputs takes 2.3 us where one with them takes 3.9
+constexpr int kLinFirst = 6;
 constexpr int kLinDirectTokens = 2048;
 
 // The gates of a chunk of one head, with G_i the sum of log2 alpha up to token i.  A
@@ -75,6 +88,7 @@ struct LinPlan {
   int32_t slots;           // CTAs that the chains are shared out to
   int32_t chunk;           // tokens of a chunk
   int32_t min_segment;     // fewest chunks of a segment
+  int32_t first;           // of lin_cut
   int64_t max_records;
   int32_t may_split;
   float* states;           // [places][H][dk][dv] start states of segments
@@ -84,9 +98,10 @@ struct LinPlan {
 };
 
 // How a path plans: its column tiles, CTAs, tokens of a chunk, shortest segment in
-// chunks, up to how many tokens its chains need no plan, whether it has gate records
+// chunks, the share of the first one, up to how many tokens its chains need no plan,
+// whether it has gate records
 struct LinShare {
-  int32_t tiles, slots, chunk, min_segment, direct_tokens;
+  int32_t tiles, slots, chunk, min_segment, first, direct_tokens;
   bool records;
 };
 struct LinLayout {
