@@ -6,15 +6,15 @@
 //   P = Q K^T                          tcgen05
 //   P~_ij = 2^{-G_j} P_ij, j <= i      rounded to bf16, into P's columns of TMEM
 //   O = 2^{G_i} (Q S + P~ V)           tcgen05, P~ from TMEM; S rounded to bf16 for this alone
-//   S <- 2^{G_C} S + K~^T V            K~_j = 2^{G_C - G_j} k_j in two bf16 parts, A from TMEM
+//   S <- 2^{G_C} S + K~^T V            K~_j = 2^{G_C - G_j} k_j in three bf16 parts, A from TMEM
 //
 // That is for a weak chunk, |G| <= 64: both factors stay within fp32 and bf16 by far, and
 // one of them is left to the epilogue.  In a strong one P~_ij = 2^{G_i - G_j} P_ij, the
 // difference taken before the exponential (over whole blocks of 32 tokens as a product of two
 // factors <= 1), and the queries are multiplied by theirs, Q~_i = 2^{G_i} q_i in bf16 beside P~.
 //
-// K~ = hi + lo leaves out less than 2^-16 of a term, so states keep fp32's
-// precision to about 1e-6 in norm (hi alone: 1e-3); the product starts from zero in each
+// Three parts of K~ leave out less than 2^-25 of a term, so states keep fp32's
+// precision (two: 2.3e-6 in norm, one: 1e-3); the product starts from zero in each
 // chunk and is added to S in registers, rounded to nearest (the tensor cores'
 // own accumulation cuts, a bias that grows with the chunks).
 //
@@ -78,13 +78,14 @@ struct Shape {
   static constexpr uint32_t kTail = kS + kSop;
   static constexpr uint32_t kBytes = kTail + 3 * 1024;
   static constexpr int kSCols = MB == 1 ? DV / 2 : DV;     // columns of a state thread
-  // K~ goes through TMEM half a chunk of one row tile at a time, a place for each half
+  // K~ goes through TMEM a quarter of a chunk of one row tile at a time, in two places
   // where there is room: one is made while the other is multiplied
-  static constexpr int kTok = C / 2, kPhases = 2 * MB, kKBuf = MB == 1 ? 2 : 1;
-  // TMEM columns: P (P~ over its first half, Q~ over its second or behind it), O, K~^T V, hi and lo
+  static constexpr int kTok = C / 4, kPhases = 4 * MB, kKBuf = MB == 1 ? 2 : 1;
+  static constexpr int kKPart = kTok / 2, kKPlace = 3 * kKPart;  // TMEM columns of a part, of a place
+  // TMEM columns: P (P~ over its first half, Q~ over its second or behind it), O, K~^T V, K~
   static constexpr int tP = 0, tQ = DK <= 128 ? 64 : C, tO = DK <= 128 ? C : C + DK / 2, tKV = tO + DV,
-                       tHi = tKV + MB * DV, tLo = tHi + kTok / 2;
-  static_assert(tHi + kKBuf * kTok <= (int)kTmemCols && kStages >= 1 && kBytes <= 232448, "fits an SM");
+                       tK = tKV + MB * DV;
+  static_assert(tK + kKBuf * kKPlace <= (int)kTmemCols && kStages >= 1 && kBytes <= 232448, "fits an SM");
 };
 
 struct Tail {
@@ -201,17 +202,10 @@ __device__ __forceinline__ void ldsm4t(uint32_t* r, uint32_t addr) {
 // column l % 4 of lanes l / 4 and l / 4 + 8
 template <int N>
 __device__ __forceinline__ void tmem_st_16x128(uint32_t taddr, const uint32_t* v) {
-  static_assert(N == 4 || N == 8, "blocks");
-  if constexpr (N == 8)
-    asm volatile(
-        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-        : "memory");
-  else
-    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
-                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
+  static_assert(N == 2, "blocks");
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3])
+               : "memory");
 }
 
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, const void* src, int x, int y, int z) {
@@ -341,7 +335,7 @@ __device__ void mma_out_role(const LinParams& p, const LinTcArgs& a, const CUten
   mbar_wait(&b->drain[0], 0, kWaitLimitNs);
 }
 
-// Those of the state: K~^T V from zero, lo and hi in turn
+// Those of the state: K~^T V from zero, the parts of K~ in turn, smallest first
 template <int DK, int DV, bool kLocal>
 __device__ void mma_state_role(const LinParams& p, const LinTcArgs& a, char* sm, Tail* b) {
   using S = Shape<DK, DV>;
@@ -367,12 +361,14 @@ __device__ void mma_state_role(const LinParams& p, const LinTcArgs& a, char* sm,
         if (issue) {
           constexpr int kPer = C / S::kTok;
           const int tok = ph % kPer * S::kTok;
-          const uint32_t buf = tmem + (n & (S::kKBuf - 1)) * S::kTok;
+          const uint32_t buf = tmem + S::tK + (n & (S::kKBuf - 1)) * S::kKPlace;
 #pragma unroll 1
           for (int s = 0; s < S::kTok / 16; ++s) {
             const uint64_t vs = vd + (uint64_t)((tok / 16 + s) * (2048 >> 4));
-            mma_bf16_ts(tmem + S::tKV + ph / kPer * DV, buf + S::tLo + s * 8, vs, id_n, tok > 0 || s > 0);
-            mma_bf16_ts(tmem + S::tKV + ph / kPer * DV, buf + S::tHi + s * 8, vs, id_n, 1);
+            const uint32_t to = tmem + S::tKV + ph / kPer * DV;
+            mma_bf16_ts(to, buf + 2 * S::kKPart + s * 8, vs, id_n, tok > 0 || s > 0);
+            mma_bf16_ts(to, buf + S::kKPart + s * 8, vs, id_n, 1);
+            mma_bf16_ts(to, buf + s * 8, vs, id_n, 1);
           }
           mma_commit(&b->kv_full[n & 1]);
           if (ph + 1 == S::kPhases) mma_commit(kLocal ? &b->v_empty[ring.st] : &b->v_done[ring.st]);
@@ -695,7 +691,7 @@ __device__ void state_role(const LinParams& p, const LinTcArgs& a, char* sm, Tai
 #pragma unroll 1
           for (int g = 0; g < 2; ++g) {
             const int ch0 = 128 * m + 32 * quarter + 16 * g;
-            uint32_t hi[TH / 4], lo[TH / 4];
+            uint32_t hi[TH / 4], mid[TH / 4], lo[TH / 4];
 #pragma unroll
             for (int c = 0; c < TH / 16; ++c)
               ldsm4t(lo + 4 * c, kt + sw_off(tok0 + 16 * c + (lane & 7) + (lane >> 4) * 8, ch0 / 8 + ((lane >> 3) & 1), kBlock));
@@ -711,12 +707,15 @@ __device__ void state_role(const LinParams& p, const LinTcArgs& a, char* sm, Tai
               const float2 w = *reinterpret_cast<const float2*>(&b->gates[n & 1].w[tok0 + (u >> 1) * 8 + 2 * (lane & 3)]);
               const float2 f = mul2(make_float2(bf_lo(lo[u]), bf_hi(lo[u])), w);
               hi[u] = pack2(f);
-              lo[u] = pack2(fma2(make_float2(bf_lo(hi[u]), bf_hi(hi[u])), make_float2(-1.f, -1.f), f));
+              const float2 minus = make_float2(-1.f, -1.f), rest = fma2(make_float2(bf_lo(hi[u]), bf_hi(hi[u])), minus, f);
+              mid[u] = pack2(rest);
+              lo[u] = pack2(fma2(make_float2(bf_lo(mid[u]), bf_hi(mid[u])), minus, rest));
             }
-            const uint32_t at = lanes + ((uint32_t)(16 * g) << 16) + half * (TH / 2) +
-                                (ph & (S::kKBuf - 1)) * S::kTok;
-            tmem_st_16x128<TH / 8>(at + S::tHi, hi);
-            tmem_st_16x128<TH / 8>(at + S::tLo, lo);
+            const uint32_t at = lanes + ((uint32_t)(16 * g) << 16) + half * (TH / 2) + S::tK +
+                                (ph & (S::kKBuf - 1)) * S::kKPlace;
+            tmem_st_16x128<TH / 8>(at, hi);
+            tmem_st_16x128<TH / 8>(at + S::kKPart, mid);
+            tmem_st_16x128<TH / 8>(at + 2 * S::kKPart, lo);
           }
           tmem_st_wait();
         }
@@ -727,10 +726,10 @@ __device__ void state_role(const LinParams& p, const LinTcArgs& a, char* sm, Tai
         next = lin_decay(b->gates[n & 1].total);
         return true;
       };
-      // with two places the first half of K~ beside the product of the chunk before, else behind it
+      // with two places the first quarter of K~ beside the product of the chunk before, else behind it
       if (S::kKBuf == 2) {
         if (!gates()) return;
-        if (t > 0 && !wait(&b->kv_full[0], (n - 1) & 1)) return;
+        if (t > 0 && !wait(&b->kv_full[0], ((n * S::kPhases - 2) >> 1) & 1)) return;
         fence_after_sync();
         make_k(0);
         if (t > 0 && !advance()) return;
@@ -745,9 +744,9 @@ __device__ void state_role(const LinParams& p, const LinTcArgs& a, char* sm, Tai
         __syncwarp();
         if (lane == 0) mbar_arrive(&b->k_ready[ph & 1]);
         if (++ph == S::kPhases) break;
-        // (the second half's place: its product of the chunk before is done, as the state has it)
-        if (S::kKBuf == 1) {
-          if (!wait(&b->kv_full[(ph - 1) & 1], ((n * S::kPhases + ph - 1) >> 1) & 1)) return;
+        // its place, once multiplied (the second quarter's was the chunk before's last, which the state has)
+        if (ph >= S::kKBuf) {
+          if (!wait(&b->kv_full[(ph - S::kKBuf) & 1], ((n * S::kPhases + ph - S::kKBuf) >> 1) & 1)) return;
           fence_after_sync();
         }
         make_k(ph);
