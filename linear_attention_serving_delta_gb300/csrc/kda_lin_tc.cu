@@ -78,10 +78,10 @@ struct Shape {
   static constexpr uint32_t kTail = kS + kSop;
   static constexpr uint32_t kBytes = kTail + 3 * 1024;
   static constexpr int kSCols = MB == 1 ? DV / 2 : DV;     // columns of a state thread
-  // K~ goes through TMEM a quarter of a chunk of one row tile at a time, in two places
-  // where there is room: one is made while the other is multiplied
-  static constexpr int kTok = C / 4, kPhases = 4 * MB, kKBuf = MB == 1 ? 2 : 1;
-  static constexpr int kKPart = kTok / 2, kKPlace = 3 * kKPart;  // TMEM columns of a part, of a place
+  // K~ goes through TMEM a half or a quarter of a chunk of one row tile at a time, in two
+  // places where there is room: one is made while the other is multiplied
+  static constexpr int kTok = DK <= 128 && DV <= 64 ? C / 2 : C / 4, kPhases = C / kTok * MB, kKBuf = MB == 1 ? 2 : 1;
+  static constexpr int kKStep = 24, kKPlace = kTok / 16 * kKStep;  // TMEM columns of 16 tokens' three parts, of a place
   // TMEM columns: P (P~ over its first half, Q~ over its second or behind it), O, K~^T V, K~
   static constexpr int tP = 0, tQ = DK <= 128 ? 64 : C, tO = DK <= 128 ? C : C + DK / 2, tKV = tO + DV,
                        tK = tKV + MB * DV;
@@ -202,10 +202,15 @@ __device__ __forceinline__ void ldsm4t(uint32_t* r, uint32_t addr) {
 // column l % 4 of lanes l / 4 and l / 4 + 8
 template <int N>
 __device__ __forceinline__ void tmem_st_16x128(uint32_t taddr, const uint32_t* v) {
-  static_assert(N == 2, "blocks");
-  asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-               "r"(v[3])
-               : "memory");
+  static_assert(N == 2 || N == 4, "blocks");
+  if constexpr (N == 4)
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  else
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3])
+                 : "memory");
 }
 
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, const void* src, int x, int y, int z) {
@@ -366,9 +371,9 @@ __device__ void mma_state_role(const LinParams& p, const LinTcArgs& a, char* sm,
           for (int s = 0; s < S::kTok / 16; ++s) {
             const uint64_t vs = vd + (uint64_t)((tok / 16 + s) * (2048 >> 4));
             const uint32_t to = tmem + S::tKV + ph / kPer * DV;
-            mma_bf16_ts(to, buf + 2 * S::kKPart + s * 8, vs, id_n, tok > 0 || s > 0);
-            mma_bf16_ts(to, buf + S::kKPart + s * 8, vs, id_n, 1);
-            mma_bf16_ts(to, buf + s * 8, vs, id_n, 1);
+            mma_bf16_ts(to, buf + s * S::kKStep + 16, vs, id_n, tok > 0 || s > 0);
+            mma_bf16_ts(to, buf + s * S::kKStep + 8, vs, id_n, 1);
+            mma_bf16_ts(to, buf + s * S::kKStep, vs, id_n, 1);
           }
           mma_commit(&b->kv_full[n & 1]);
           if (ph + 1 == S::kPhases) mma_commit(kLocal ? &b->v_empty[ring.st] : &b->v_done[ring.st]);
@@ -625,7 +630,7 @@ template <int DK, int DV, bool kLocal>
 __device__ void state_role(const LinParams& p, const LinTcArgs& a, char* sm, Tail* b) {
   using S = Shape<DK, DV>;
   constexpr int N = S::kSCols;
-  constexpr int TH = S::kTok / 2;  // tokens of K~ that a warp makes at a time, for 32 channels
+  constexpr int TH = S::kTok / 2;  // tokens of K~ that a warp makes at a time, of 32 channels
   const int x = threadIdx.x - 384, lane = x & 31, quarter = (x >> 5) & 3, half = x >> 7;
   // the state: row d, columns [col, col + N)
   const int d = 32 * quarter + lane + (S::MB > 1 ? 128 * half : 0), col = S::MB > 1 ? 0 : half * N;
@@ -688,34 +693,36 @@ __device__ void state_role(const LinParams& p, const LinTcArgs& a, char* sm, Tai
         const int m = ph / (C / S::kTok), tok0 = ph % (C / S::kTok) * S::kTok + half * TH;
         const uint32_t kt = smem_u32(sm + S::kK + ring.st * S::kQK);
         if (32 * quarter < DK) {
-#pragma unroll 1
+#pragma unroll
           for (int g = 0; g < 2; ++g) {
             const int ch0 = 128 * m + 32 * quarter + 16 * g;
-            uint32_t hi[TH / 4], mid[TH / 4], lo[TH / 4];
 #pragma unroll
-            for (int c = 0; c < TH / 16; ++c)
-              ldsm4t(lo + 4 * c, kt + sw_off(tok0 + 16 * c + (lane & 7) + (lane >> 4) * 8, ch0 / 8 + ((lane >> 3) & 1), kBlock));
-            if (live < C)  // rows behind the sequence
+            for (int c = 0; c < TH / 16; ++c) {
+              // the tokens' keys, then the parts of K~: largest, middle, smallest
+              uint32_t part[12], *key = part + 8;
+              ldsm4t(key, kt + sw_off(tok0 + 16 * c + (lane & 7) + (lane >> 4) * 8, ch0 / 8 + ((lane >> 3) & 1), kBlock));
+              if (live < C)  // rows behind the sequence
 #pragma unroll
-              for (int u = 0; u < TH / 4; ++u) {
-                const int y = tok0 + (u >> 1) * 8 + 2 * (lane & 3);
-                if (y >= live) lo[u] = 0;
-                else if (y + 1 >= live) lo[u] &= 0xffffu;
+                for (int u = 0; u < 4; ++u) {
+                  const int y = tok0 + 16 * c + (u >> 1) * 8 + 2 * (lane & 3);
+                  if (y >= live) key[u] = 0;
+                  else if (y + 1 >= live) key[u] &= 0xffffu;
+                }
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                const float2 w =
+                    *reinterpret_cast<const float2*>(&b->gates[n & 1].w[tok0 + 16 * c + (u >> 1) * 8 + 2 * (lane & 3)]);
+                const float2 f = mul2(make_float2(bf_lo(key[u]), bf_hi(key[u])), w), minus = make_float2(-1.f, -1.f);
+                part[u] = pack2(f);
+                const float2 rest = fma2(make_float2(bf_lo(part[u]), bf_hi(part[u])), minus, f);
+                part[4 + u] = pack2(rest);
+                part[8 + u] = pack2(fma2(make_float2(bf_lo(part[4 + u]), bf_hi(part[4 + u])), minus, rest));
               }
-#pragma unroll
-            for (int u = 0; u < TH / 4; ++u) {
-              const float2 w = *reinterpret_cast<const float2*>(&b->gates[n & 1].w[tok0 + (u >> 1) * 8 + 2 * (lane & 3)]);
-              const float2 f = mul2(make_float2(bf_lo(lo[u]), bf_hi(lo[u])), w);
-              hi[u] = pack2(f);
-              const float2 minus = make_float2(-1.f, -1.f), rest = fma2(make_float2(bf_lo(hi[u]), bf_hi(hi[u])), minus, f);
-              mid[u] = pack2(rest);
-              lo[u] = pack2(fma2(make_float2(bf_lo(mid[u]), bf_hi(mid[u])), minus, rest));
+              const uint32_t at = lanes + ((uint32_t)(16 * g) << 16) + S::tK + (ph & (S::kKBuf - 1)) * S::kKPlace +
+                                  (half * (TH / 16) + c) * S::kKStep;
+              tmem_st_16x128<4>(at, part);
+              tmem_st_16x128<2>(at + 16, part + 8);
             }
-            const uint32_t at = lanes + ((uint32_t)(16 * g) << 16) + half * (TH / 2) + S::tK +
-                                (ph & (S::kKBuf - 1)) * S::kKPlace;
-            tmem_st_16x128<TH / 8>(at, hi);
-            tmem_st_16x128<TH / 8>(at + S::kKPart, mid);
-            tmem_st_16x128<TH / 8>(at + 2 * S::kKPart, lo);
           }
           tmem_st_wait();
         }
