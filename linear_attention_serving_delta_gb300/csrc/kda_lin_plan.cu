@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kPlanThreads) lin_plan(const LinParams p, cons
 
 // Start states of segments 2, 3, ...: a thread four elements
 __global__ void __launch_bounds__(256) lin_combine(const LinParams p, const LinPlan a) {
-  __shared__ float decay[kLinMostSegments];
+  __shared__ LinDecay decay[kLinMostSegments];
   pdl_launch_dependents();
   pdl_wait();
   const int h = blockIdx.y;
@@ -264,12 +264,11 @@ __global__ void __launch_bounds__(256) lin_combine(const LinParams p, const LinP
   for (int x = blockIdx.x; x < a.head->splits; x += gridDim.x) {
     const LinSplit sp = a.splits[x];
     __syncthreads();
-    // log2 of each segment's decay, a warp a segment
-    for (int i = 1 + (threadIdx.x >> 5); i < sp.segments - 1; i += 8) {
-      if (a.logs) {
-        if ((threadIdx.x & 31) == 0) decay[i] = a.logs[((int64_t)sp.place + i + 1) * p.H + h];
-        continue;
-      }
+    // each segment's decay: from the first pass, or from the records, a warp a segment
+    if (a.logs)
+      for (int i = 1 + threadIdx.x; i < sp.segments - 1; i += 256)
+        decay[i] = lin_decay(a.logs[((int64_t)sp.place + i + 1) * p.H + h]);
+    for (int i = 1 + (threadIdx.x >> 5); !a.logs && i < sp.segments - 1; i += 8) {
       LogSum g{0.f, 0.f};
       for (int c = lin_cut(sp.chunks, sp.segments, i, a.first) + (threadIdx.x & 31);
            c < lin_cut(sp.chunks, sp.segments, i + 1, a.first); c += 32)
@@ -277,7 +276,7 @@ __global__ void __launch_bounds__(256) lin_combine(const LinParams p, const LinP
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1)
         g = g + LogSum{__shfl_xor_sync(0xffffffffu, g.i, o), __shfl_xor_sync(0xffffffffu, g.f, o)};
-      if ((threadIdx.x & 31) == 0) decay[i] = g.i + g.f;
+      if ((threadIdx.x & 31) == 0) decay[i] = lin_decay(g.i + g.f);
     }
     __syncthreads();
     if (e >= size) continue;
@@ -294,7 +293,7 @@ __global__ void __launch_bounds__(256) lin_combine(const LinParams p, const LinP
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
         if (i0 + u >= sp.segments) break;
-        const LinDecay d = lin_decay(decay[i0 + u - 1]);
+        const LinDecay d = decay[i0 + u - 1];
         const float one = d.near_one ? 1.f : 0.f;
         y[u].x = fmaf(one, s.x, fmaf(d.m, s.x, y[u].x));
         y[u].y = fmaf(one, s.y, fmaf(d.m, s.y, y[u].y));

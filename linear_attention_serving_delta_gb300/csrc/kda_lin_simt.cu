@@ -178,10 +178,11 @@ cudaError_t launch_nc(const LinParams& p, void* ws, cudaStream_t stream) {
                                   stream, p, plan, planned);
   };
   if (!L.may_split) return run(lin_simt<T, DK, NC, false>, p.num_seqs, false);
+  const int64_t chains = sh.slots / ((int64_t)p.H * sh.tiles);  // of cut sequences, at most, in either pass
   cudaError_t e = launch_lin_plan(p, plan, stream);
-  if (e == cudaSuccess) e = run(lin_simt<T, DK, NC, true>, L.places, true);
+  if (e == cudaSuccess) e = run(lin_simt<T, DK, NC, true>, chains, true);
   if (e == cudaSuccess) e = launch_lin_combine(p, plan, stream);
-  return e != cudaSuccess ? e : run(lin_simt<T, DK, NC, false>, p.num_seqs + L.places, true);
+  return e != cudaSuccess ? e : run(lin_simt<T, DK, NC, false>, p.num_seqs + chains, true);
 }
 
 template <typename T, int DK>

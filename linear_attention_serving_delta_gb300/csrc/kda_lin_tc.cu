@@ -942,7 +942,7 @@ cudaError_t launch_shape(const LinParams& p, void* ws, cudaStream_t stream) {
   }
   a.items = plan.items;
   a.num_items = &plan.head->items;
-  return run(lin_tc<DK, DV, false>, std::min<int64_t>(sms, (p.num_seqs + L.places) * per));
+  return run(lin_tc<DK, DV, false>, std::min<int64_t>(sms, (p.num_seqs + sh.slots / per) * per));
 }
 
 }  // namespace

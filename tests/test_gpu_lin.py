@@ -8,9 +8,8 @@ to fp32 by 2^-24.
     read from: |error| <= 2^-8 |o| + 2 (2^-8 + 2^-16) o_abs.  The roundings being
     independent and of either sign, the norm of the error is below 2^-8 of the
     norm of o (each has a root mean square of at most 2^-8 / sqrt 3).
-  states, bf16 inputs: keys with their decays are split into two bf16, what is
-    left out below 2^-16 of a term: |error| <= (2^-16 + (T + 64) 2^-24) S_abs, and the
-    norm below 2^-16 (+ the fp32 part).
+  states, bf16 inputs: keys with their decays are split into three bf16, what is
+    left out below 2^-25 of a term: the bounds of fp32.
   fp32: a sum of T tokens, then of dk channels: |error| <= (T + dk + 64) 2^-24 of the
     sum over absolute values, the 64 for the decays' logarithms and exponentials; in
     norm, roundings of either sign add up like a random walk: 2^-18.
@@ -24,7 +23,7 @@ pytestmark = pytest.mark.gpu
 
 DT = {"bf16": torch.bfloat16, "f32": torch.float32}
 NORM_O = {"bf16": 2.0 ** -8, "f32": 2.0 ** -18}
-NORM_S = {"bf16": 2.0 ** -16 + 2.0 ** -18, "f32": 2.0 ** -18}
+NORM_S = {"bf16": 2.0 ** -18, "f32": 2.0 ** -18}
 
 
 def log_alpha(g, slope, T, H):
@@ -53,7 +52,7 @@ def walk(q, k, v, loga, S, scale, order):
 def close(got, want, total, dtype, T, dk, what, state=False):
     got, err = got.double(), (got.double() - want).abs()
     if state:
-        lim = ((2.0 ** -16 if dtype == "bf16" else 0.0) + (T + 64) * 2.0 ** -24) * total
+        lim = (T + 64) * 2.0 ** -24 * total
         norm = NORM_S[dtype]
     elif dtype == "bf16":
         lim, norm = 2.0 ** -8 * want.abs() + 2 * (2.0 ** -8 + 2.0 ** -16) * total, NORM_O[dtype]
