@@ -129,6 +129,12 @@ LinParams tree_params(const A* a) {
   return p;
 }
 
+// Enough for either path: a call's pointers may be aligned otherwise than those that the
+// size was asked with
+size_t prefill_workspace(const LinParams& p) {
+  return p.dt == KDA_BF16 ? std::max(lin_tc_workspace(p), lin_simt_workspace(p)) : lin_simt_workspace(p);
+}
+
 }  // namespace
 }  // namespace kda
 
@@ -138,9 +144,7 @@ extern "C" {
 
 size_t kda_lin_prefill_workspace_size(const kda_lin_prefill_args* a) {
   if (validate(a) != KDA_OK) return 0;
-  const LinParams p = params(a);
-  // (enough for either path: a call's pointers may be aligned otherwise than these)
-  return p.dt == KDA_BF16 ? std::max(lin_tc_workspace(p), lin_simt_workspace(p)) : lin_simt_workspace(p);
+  return prefill_workspace(params(a));
 }
 
 kda_status_t kda_lin_prefill(const kda_lin_prefill_args* a, void* ws, size_t ws_bytes, void* stream) {
@@ -148,7 +152,7 @@ kda_status_t kda_lin_prefill(const kda_lin_prefill_args* a, void* ws, size_t ws_
   if (st != KDA_OK) return st;
   const LinParams p = params(a);
   const bool tc = lin_tc_fits(p);
-  if (!ws || ws_bytes < (tc ? lin_tc_workspace(p) : lin_simt_workspace(p)) || misaligned(ws, 256)) return KDA_ERR_WORKSPACE;
+  if (!ws || ws_bytes < prefill_workspace(p) || misaligned(ws, 256)) return KDA_ERR_WORKSPACE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return from_cuda(tc ? launch_lin_tc(p, ws, s) : launch_lin_simt(p, ws, s));
 }

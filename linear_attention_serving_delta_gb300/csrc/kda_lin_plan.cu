@@ -15,10 +15,9 @@
 // second pass gives the outputs of the other segments side by side.  So k segments are
 // k - 1 chains of either pass, and the first is as much shorter as its outputs take longer.
 // Keys and values of those between the first and the last are read twice, from L2 where
-// the call's fit it.  One block plans, in 9 us for one
-// prompt as for ninety: lengths, scans over the block, and a search for the length of
-// the segments that tries 32 at a time (one after the other took 4 us more, and
-// writing a prompt's segments by one thread 6 us).
+// the call's fit it.  One block plans, in about 10 us: lengths, scans over the block,
+// and a search for the length of the segments that tries 32 at a time (one after the
+// other took 4 us more, and writing a prompt's segments by one thread 6 us).
 #include <algorithm>
 
 #include "kda_lin_tc.cuh"

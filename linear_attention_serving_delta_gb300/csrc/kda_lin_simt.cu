@@ -14,7 +14,7 @@
 // which no tensor core does to fp32 precision at a better rate.  Two prompts of 500 to
 // 1,500 tokens, 8 heads of 64 x 64: 217 us as one chain a sequence and 32 columns, 67 in
 // segments of 32 tokens and up, 53 with two columns a lane (an element of k or q
-// from shared memory serves both) -- 9 the plan, 8 the combination, 16 and 20 the two passes.
+// from shared memory serves both), 47 with segments in steps of 16 tokens.
 #include <algorithm>
 
 #include "kda_lin_tc.cuh"
@@ -162,10 +162,11 @@ __global__ void __launch_bounds__(kThreads, 3) lin_simt(const LinParams p, const
 }
 
 // Three CTAs an SM (chains for four, with registers for two: 108 us where three with
-// registers for three took 87), in segments of 32 tokens and up (of 128: 87 us, of 32: 70)
+// registers for three took 87), in segments of 32 tokens and up (of 128 and up: 87 us where
+// these took 70) in steps of 16 (of 32: 55 us where these took 47)
 LinShare share(const LinParams& p) {
   const int cols = 32 * cols_of(p);
-  return LinShare{(p.dv + cols - 1) / cols, 3 * kLinSlots, 32, 1, 8, 32, false};
+  return LinShare{(p.dv + cols - 1) / cols, 3 * kLinSlots, 16, 2, 8, 32, false};
 }
 
 template <typename T, int DK, int NC>

@@ -28,12 +28,13 @@
 // (kda_lin_tc.cuh), made before: as a role of their own they took the longest.
 //
 // What it takes (a copy reaches 6.8 TB/s): 8,192 tokens of 32 heads of 128 x 128 in
-// 111 us, of which the plan 9, the segments' own states 37, the combination 6 and the
-// outputs 63, each traced by itself; eight prompts of 1,024 to 32,768 tokens in 1.28 ms, 4.5 TB/s.
-// An SM does a chunk in 3.1 to 3.9 us there, against 2.9 of HBM for its 128 KB at an
-// SM's share; what is beyond that is 256 chains that 152 SMs cannot share evenly.  64
-// columns a chain take 3 us a chunk all the same: then a chunk's chain of waits -- products,
-// state, operand, products, outputs -- bounds it, one chain an SM.
+// 123 us, of which the plan 10, the first pass 46, the joining of its states 8 and the second
+// pass 64, each traced by itself; eight prompts of 1,024 to 32,768 tokens in 1.37 ms, 4.2 TB/s.
+// An SM does a chunk in 3.9 to 4.6 us there, against 2.9 of HBM for its 128 KB at an
+// SM's share; what is beyond that is 256 chains that 152 SMs cannot share evenly.  (With two
+// parts of K~ for three: 108 us and 1.29 ms.)  64 columns a chain take 3.5 us a chunk all the
+// same: then a chunk's chain of waits -- products, state, operand, products, outputs --
+// bounds it, one chain an SM.
 //
 // Roles run side by side on the schedulers' small instruction caches: unrolled ones of
 // 140 KB together issued an instruction in 6 to 10 cycles.  What waits for shared

@@ -116,6 +116,15 @@ def test_workspace_is_checked(kda, over):
     assert L.kda_lin_prefill(ctypes.byref(a), 0x140, n, None) == WORKSPACE
 
 
+@pytest.mark.parametrize("tokens", [100, 5000, 100000])
+def test_workspace_is_enough_for_any_alignment(kda, tokens):
+    size = kda.lib().kda_lin_prefill_workspace_size
+    args = [block(kda.LinPrefillArgs, kda, total_tokens=tokens, q=PTR + off) for off in (0, 2)]
+    assert size(ctypes.byref(args[0])) == size(ctypes.byref(args[1])) > 0
+    # and a call that takes the other path still refuses less than that
+    assert kda.lib().kda_lin_prefill(ctypes.byref(args[1]), 0x100, size(ctypes.byref(args[0])) - 1, None) == WORKSPACE
+
+
 def test_binding_refuses(kda, monkeypatch):
     # (shapes and numbers are looked at before anything that needs a GPU)
     monkeypatch.setattr(kda, "_same_device", lambda **t: torch.device("cpu"))
