@@ -388,6 +388,33 @@ def test_prefill_f32_long_slots_in_place_and_in_a_graph():
         assert torch.equal(o, first) and torch.equal(pool, after)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_prefill_few_of_many_sequences(dtype):
+    """More sequences than the plan takes at once, nearly all skipped, three cut into segments."""
+    n, H, dk = 1500, 2, 32
+    lens = [i % 2 for i in range(n)]
+    lens[0], lens[1200], lens[1499] = 2300, 900, 1
+    slots = [-1] * n
+    slots[0], slots[1200], slots[1499], slots[700] = 3, 0, 1, 2
+    T = sum(lens)
+    d = inputs(41, T, H, H, dk, dk, dtype, "g", n=4)
+    o = torch.full((T, H, dk), 7.0, device="cuda", dtype=DT[dtype])
+    pool = d["state"].clone()
+    call = kda.LinPrefill(d["q"], d["k"], d["v"], offsets(lens), g=d["g"], initial_state=pool, final_state=pool, o=o,
+                          state_slots=torch.tensor(slots, device="cuda", dtype=torch.int32)).run()
+    check_prefill(d, lens, H, dk, dtype, o, pool, 1.0, slots)
+    at = offsets(lens).tolist()
+    assert call.device_status() == 0 and all(bool((o[at[s]:at[s + 1]] == 7).all()) for s in range(n) if slots[s] < 0)
+
+
+@pytest.mark.parametrize("dtype,T,H,dk,dv", [("bf16", 9000, 1, 64, 64), ("f32", 3000, 1, 32, 32), ("bf16", 3500, 38, 64, 128)])
+def test_prefill_most_segments(dtype, T, H, dk, dv):
+    d = inputs(43, T, H, 1, dk, dv, dtype, "both", n=1)
+    o, final = kda.lin_prefill(d["q"], d["k"], d["v"], offsets([T]), g=d["g"], slope=d["slope"], scale=dk ** -0.5,
+                               initial_state=d["state"])
+    check_prefill(d, [T], H, dk, dtype, o, final, dk ** -0.5)
+
+
 @pytest.mark.parametrize("dtype,lens", [("bf16", [130, 7]), ("bf16", [2500, 130]), ("f32", [90]), ("f32", [700, 33])])
 def test_prefill_rows_behind_the_last_sequence(dtype, lens):
     H, dk, more = 2, 64, 70
