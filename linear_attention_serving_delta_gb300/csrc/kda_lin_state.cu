@@ -63,7 +63,8 @@ __global__ void __launch_bounds__(Tile<DK, DV, kNarrow>::NT) lin_decode(const Li
   const int64_t at = ((int64_t)seq.slot * p.H + h) * DK * DV + c0 + 4 * cq;
   float4 s[L::VPT];
 #pragma unroll
-  for (int i = 0; i < L::VPT; ++i) s[i] = *reinterpret_cast<const float4*>(p.state_in + at + (int64_t)(rg + i * L::NRG) * DV);
+  for (int i = 0; i < L::VPT; ++i)
+    s[i] = *reinterpret_cast<const float4*>(p.state_in + at + (int64_t)(rg + i * L::NRG) * DV);
   const int64_t tk = ((int64_t)row * p.Hk + h / p.R) * DK, tv = ((int64_t)row * p.H + h) * DV + c0;
   for (int i = tid; i < DK; i += L::NT) {
     sq[i] = ld_in(static_cast<const T*>(p.q), tk + i);
@@ -340,8 +341,9 @@ __global__ void __launch_bounds__(256, DK <= 128 && MW == 1 ? 2 : 1)
     for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        s[b][e] = cb < p.dv && tile_of(0) < mt ? *reinterpret_cast<const float4*>(S + (int64_t)(16 * (k0 + b) + 4 * ti + e) * p.dv)
-                            : make_float4(0.f, 0.f, 0.f, 0.f);
+        s[b][e] = cb < p.dv && tile_of(0) < mt
+                      ? *reinterpret_cast<const float4*>(S + (int64_t)(16 * (k0 + b) + 4 * ti + e) * p.dv)
+                      : make_float4(0.f, 0.f, 0.f, 0.f);
   };
   load(0);
   // queries, keys and values of the request, rows behind it zero, 16 bytes at a time and
@@ -386,7 +388,9 @@ __global__ void __launch_bounds__(256, DK <= 128 && MW == 1 ? 2 : 1)
   __syncthreads();
   const bool found = any_bad != 0;
   // four channels of a token's query or key
-  auto four = [&](const T* x, int tok, int kb) { return *reinterpret_cast<const uint2*>(x + tok * kPitch + 16 * kb + 4 * ti); };
+  auto four = [&](const T* x, int tok, int kb) {
+    return *reinterpret_cast<const uint2*>(x + tok * kPitch + 16 * kb + 4 * ti);
+  };
   float acc[MW][4][4];
 #pragma unroll
   for (int u = 0; u < MW; ++u)
@@ -535,7 +539,9 @@ __global__ void __launch_bounds__(kThreads) lin_draft(const LinParams p) {
     float q[(DK + 31) / 32];
 #pragma unroll
     for (int u = 0; u < (DK + 31) / 32; ++u)
-      q[u] = 32 * u + lane < DK ? ld_in(static_cast<const T*>(p.q), ((seq.tok0 + i) * p.Hk + h / p.R) * DK + 32 * u + lane) : 0.f;
+      q[u] = 32 * u + lane < DK
+                 ? ld_in(static_cast<const T*>(p.q), ((seq.tok0 + i) * p.Hk + h / p.R) * DK + 32 * u + lane)
+                 : 0.f;
     float y = 0.f;
 #pragma unroll
     for (int d = 0; d < DK; ++d) y = fmaf(__shfl_sync(0xffffffffu, q[d / 32], d % 32), S[d][lane], y);

@@ -816,7 +816,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&b->q_empty[s], 1);
       mbar_init(&b->v_done[s], 2);
     }
-    for (uint64_t* x : {&b->p_full, &b->o_full, &b->kv_full[0], &b->kv_full[1], &b->drain[0], &b->drain[1], &b->g_full[0], &b->g_full[1]})
+    for (uint64_t* x : {&b->p_full, &b->o_full, &b->kv_full[0], &b->kv_full[1], &b->drain[0], &b->drain[1],
+                        &b->g_full[0], &b->g_full[1]})
       mbar_init(x, 1);
     for (uint64_t* x : {&b->s_ready, &b->k_ready[0], &b->k_ready[1]}) mbar_init(x, 8);
     for (uint64_t* x : {&b->p_ready, &b->o_free}) mbar_init(x, 4);

@@ -40,7 +40,7 @@ __host__ __device__ __forceinline__ int32_t lin_chains(int32_t n, int32_t m, int
 }
 
 struct LinHead {
-  int32_t items, locals, splits;  // entries of the lists
+  int32_t items, locals, splits;  // entries of the lists, for one head and tile
 };
 // The CTAs that chains are shared out to, and the fewest chunks of a segment
 constexpr int kLinSlots = 152;
@@ -82,7 +82,7 @@ struct LinPlan {
   LinHead* head;
   int32_t* seq_rec;        // [N] a sequence's first record, or -1: skipped
   LinItem* items;          // costliest first
-  LinItem* locals;         // the segments whose own end states come first
+  LinItem* locals;         // the first pass's segments
   LinSplit* splits;
   int32_t tiles;           // column tiles of a head
   int32_t slots;           // CTAs that the chains are shared out to

@@ -1224,8 +1224,9 @@ class LinPrefill(_CacheCall):
     softplus(g) from g [T, H] and slope [H] float32 (either may be left out).
     Sequence s goes on from row s of initial_state (or row state_slots[s]; None:
     zeros) and leaves its state in the same row of final_state, [rows, H, dk, dv]
-    float32: True allocates one (zeros where state_slots name no row), None keeps none, and it may be initial_state itself.  ``o``
-    [T, H, dv] is allocated unless given."""
+    float32: True allocates one (zeros where state_slots name no row), None keeps
+    none, and it may be initial_state itself.  ``o`` [T, H, dv] is allocated unless
+    given."""
     _name = "kda_lin_prefill"
 
     def __init__(self, q, k, v, cu_seqlens, *, g=None, slope=None, scale=1.0, initial_state=None, final_state=True,
