@@ -165,7 +165,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32
   *reinterpret_cast<volatile uint32_t*>(dead) = 1;
   return false;
 }
-// Whether token `token` of a chain has one before or at it; n: the CTA's chunks before the chain
+// Whether token `token` >= 0 of a chain has one before or at it; n: the CTA's chunks before the chain
 __device__ __forceinline__ bool nan_at(const Tail* b, int channel, uint32_t n, int token) {
   const uint32_t x = reinterpret_cast<const volatile uint32_t*>(b->nan_from)[channel];
   return x >= n * C && x <= n * C + (uint32_t)token;
@@ -773,7 +773,8 @@ __device__ void state_role(const LinParams& p, const LinTcArgs& a, char* sm, Tai
             *reinterpret_cast<uint4*>(st + sw_off(d, (col + u) / 8, DK * 128)) =
                 make_uint4(tc::pack2(s[u], s[u + 1]), tc::pack2(s[u + 2], s[u + 3]), tc::pack2(s[u + 4], s[u + 5]),
                            tc::pack2(s[u + 6], s[u + 7]));
-          if (*reinterpret_cast<volatile int32_t*>(&b->poisoned) == i)
+          // (nothing of the chain precedes its first chunk)
+          if (t > 0 && *reinterpret_cast<volatile int32_t*>(&b->poisoned) == i)
 #pragma unroll 1
             for (int u = 0; u < N; ++u)
               if (nan_at(b, col + u, n - t / C, t - 1))

@@ -1,0 +1,62 @@
+"""Linear attention with a decay for each head where values that are not finite meet
+the borders of chunks, segments and chains: corners beside those of test_gpu_lin.py,
+with its inputs and bounds.
+"""
+import pytest
+import torch
+
+from linear_attention_serving_delta_gb300 import kda
+from test_gpu_lin import inputs, offsets
+
+pytestmark = pytest.mark.gpu
+
+# every shape of the tensor-core prompts
+SHAPES = [(64, 64), (128, 128), (256, 128), (64, 128), (128, 64)]
+
+
+def poison(d, lens, at):
+    """Infinities and NaN into v at (sequence, token, head, channel); which elements of o and of the states
+    may keep their bits."""
+    T, H, dv = d["v"].shape
+    o, s = torch.ones(T, H, dv, dtype=torch.bool), torch.ones(len(lens), H, d["k"].shape[2], dv, dtype=torch.bool)
+    cu = offsets(lens).tolist()
+    v = d["v"].cpu()
+    for i, (seq, t, h, c) in enumerate(at):
+        v[cu[seq] + t, h, c] = (float("inf"), float("nan"), float("-inf"))[i % 3]
+        o[cu[seq] + t:cu[seq + 1], h, c] = False
+        s[seq, h, :, c] = False
+    return dict(d, v=v.cuda()), o.cuda(), s.cuda()
+
+
+def check_poisoned(got, clean, same_o, same_s):
+    assert torch.equal(got[0][same_o], clean[0][same_o])
+    assert not torch.isfinite(got[0][~same_o].float()).any()
+    assert torch.equal(got[1][same_s], clean[1][same_s])
+    assert not torch.isfinite(got[1][~same_s]).any()
+
+
+def prompts(d, lens):
+    return kda.lin_prefill(d["q"], d["k"], d["v"], offsets(lens), g=d["g"], initial_state=d["state"])
+
+
+# ------------------------------------------------------------------ values that are not finite
+@pytest.mark.parametrize("dk,dv", SHAPES)
+@pytest.mark.parametrize("at", [0, 60, 127])
+def test_first_chunk_behind_a_state(dk, dv, at):
+    """Nothing of a chain precedes its first chunk, so the state that it starts from stays as it is."""
+    lens, H = [200, 150], 2
+    d = inputs(dk + dv + at, 350, H, H, dk, dv, "bf16", "g", n=2)
+    clean = prompts(d, lens)
+    bad, same_o, same_s = poison(d, lens, [(0, at, 0, 5), (1, at, 1, dv - 1), (1, at, 1, 8)])
+    check_poisoned(prompts(bad, lens), clean, same_o, same_s)
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128), (256, 64)])
+def test_first_chunk_of_a_later_segment(dk, dv):
+    """A long prompt is cut into segments: a value in each of its chunks in turn."""
+    lens, H = [2600], 2
+    d = inputs(dk + dv, 2600, H, H, dk, dv, "bf16", "g")
+    clean = prompts(d, lens)
+    for t in range(5, 2600, 128):
+        bad, same_o, same_s = poison(d, lens, [(0, t, 1, 9)])
+        check_poisoned(prompts(bad, lens), clean, same_o, same_s)
