@@ -92,7 +92,7 @@ struct Shape {
 struct Tail {
   uint64_t q_full[4], k_full[4], v_full[4], v_ready[4], q_empty[4], k_empty[4], v_done[4], v_empty[4];
   uint64_t p_full, o_full, kv_full[2];                     // committed by the MMA warps
-  uint64_t s_ready, p_ready, k_ready[2], o_free, g_full[2], g_free[2], drain[2];
+  uint64_t s_ready[2], p_ready, k_ready[2], o_free[2], g_full[2], g_free[2], drain[2];  // [2]: chunks in turn, k_ready phases
   uint32_t dead, tmem;
   int32_t poisoned;       // the CTA's chain that nan_from speaks of, -1: none so far
   int32_t scaled_q;       // the chunk is strong, for the MMAs
@@ -307,7 +307,7 @@ __device__ void mma_out_role(const LinParams& p, const LinTcArgs& a, const CUten
         mma_commit(&b->k_empty[ring.st]);
       }
       // the outputs of the chunk before have been read
-      if (n > 0 && !(ok = wait(&b->o_free, (n - 1) & 1))) break;
+      if (n > 0 && !(ok = wait(&b->o_free[(n - 1) & 1], ((n - 1) >> 1) & 1))) break;
       if (!(ok = wait(&b->v_ready[ring.st], ring.ph)) || !(ok = wait(&b->p_ready, n & 1))) break;
       fence_after_sync();
       if (issue) {
@@ -317,7 +317,7 @@ __device__ void mma_out_role(const LinParams& p, const LinTcArgs& a, const CUten
           mma_bf16_ts(tmem + S::tO, tmem + S::tP + s * 8, vd + (uint64_t)(s * (2048 >> 4)), id_n, s > 0);
         mma_commit(&b->v_done[ring.st]);
       }
-      if (!(ok = wait(&b->s_ready, n & 1))) break;
+      if (!(ok = wait(&b->s_ready[n & 1], (n >> 1) & 1))) break;
       fence_after_sync();
       if (issue) {
         if (t > 0 || ch.from != -1) {
@@ -390,7 +390,7 @@ __device__ void mma_state_role(const LinParams& p, const LinTcArgs& a, char* sm,
 // ------------------------------------------------------------------ values, P~ and Q~
 // V before the products read it: rows behind the sequence to zero, values that are
 // not finite out (r: the thread's row of the tile).
-// These are noted once nothing of an earlier chunk is left to be written.
+// These are noted once nothing of an earlier chain asks for its own.
 template <int DK, int DV, bool kLocal>
 __device__ __forceinline__ bool look_through(char* vt, int r, int live, int chain, int token, uint32_t n, Tail* b) {
   using S = Shape<DK, DV>;
@@ -404,8 +404,20 @@ __device__ __forceinline__ bool look_through(char* vt, int r, int live, int chai
     for (int c = 0; c < P; ++c) seen |= exponents_full(*reinterpret_cast<const uint4*>(vt + sw_off(r, c, kBlock)));
   }
   if (__any_sync(0xffffffffu, (seen & 0x80008000u) != 0)) {
-    if (!warp_wait(&b->k_ready[0], (n * S::kPhases >> 1) & 1, &b->dead)) return false;
-    if (!kLocal && n > 0 && !warp_wait(&b->o_free, (n - 1) & 1, &b->dead)) return false;
+    // A note of this chain may take the place of one of an earlier chain: not before all that
+    // asks for that is over, the outputs of the chunk before being read and the states' warps
+    // being in this chunk.  A wait by parity holds only where the phase before is known to be
+    // over and the next one is not.  p_full of the chunk before (weight_role) says so of s_ready
+    // two chunks back and of o_free three back, hence two barriers of each in turn; s_ready of
+    // the chunk before then says so of k_ready.  (A CTA whose chain leaves its end state alone
+    // has no earlier one.)
+    if (!kLocal) {
+      const uint32_t m = n - 1;
+      if (n > 0 && (!warp_wait(&b->o_free[m & 1], (m >> 1) & 1, &b->dead) ||
+                    !warp_wait(&b->s_ready[m & 1], (m >> 1) & 1, &b->dead)))
+        return false;
+      if (!warp_wait(&b->k_ready[0], (n * S::kPhases >> 1) & 1, &b->dead)) return false;
+    }
     if (seen & 0x80008000u) {
 #pragma unroll 1
       for (int c = 0; c < P; ++c) {
@@ -564,7 +576,7 @@ __device__ void out_role(const LinParams& p, const LinTcArgs& a, const CUtensorM
       if (!warp_wait(&b->o_full, n & 1, &b->dead)) return;
       fence_after_sync();
       const int live = min(C, ch.len - t) - 32 * warp;  // rows of the warp that are tokens
-      const bool poisoned = *reinterpret_cast<volatile int32_t*>(&b->poisoned) == i;
+      const bool poisoned = __any_sync(0xffffffffu, *reinterpret_cast<volatile int32_t*>(&b->poisoned) == i);
       const float f = p.scale * (strong ? 1.f : own);
       const float2 f2 = make_float2(f, f);
       // Through the warp's rows of the value tile, once no product reads it any more
@@ -575,10 +587,10 @@ __device__ void out_role(const LinParams& p, const LinTcArgs& a, const CUtensorM
         tmem_ld32(to + c, x);
         tmem_ld32(to + c + 32, x + 32);
         tmem_ld_wait();
-        if (c + 64 == DV) {
+        if (c + 64 == DV && !poisoned) {
           fence_before_sync();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&b->o_free);
+          if (lane == 0) mbar_arrive(&b->o_free[n & 1]);
         }
 #pragma unroll
         for (int u = 0; u < 64; u += 8) {
@@ -588,11 +600,16 @@ __device__ void out_role(const LinParams& p, const LinTcArgs& a, const CUtensorM
           *reinterpret_cast<uint4*>(vt + sw_off(row, (c + u) / 8, kBlock)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
         }
       }
-      if (poisoned)
+      if (poisoned) {
 #pragma unroll 1
         for (int u = 0; u < DV; ++u)
           if (nan_at(b, u, n - t / C, t + row))
             *reinterpret_cast<uint16_t*>(vt + sw_off(row, u / 8, kBlock) + 2 * (u % 8)) = 0x7fff;
+        // (only now: then the next chunk's notes may take the place of these)
+        fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b->o_free[n & 1]);
+      }
       fence_async_smem();
       __syncwarp();
       if (live >= 32) {
@@ -782,7 +799,7 @@ __device__ void state_role(const LinParams& p, const LinTcArgs& a, char* sm, Tai
         }
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&b->s_ready);
+        if (lane == 0) mbar_arrive(&b->s_ready[n & 1]);
       }
       ring.next();
     }
@@ -820,8 +837,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (uint64_t* x : {&b->p_full, &b->o_full, &b->kv_full[0], &b->kv_full[1], &b->drain[0], &b->drain[1],
                         &b->g_full[0], &b->g_full[1]})
       mbar_init(x, 1);
-    for (uint64_t* x : {&b->s_ready, &b->k_ready[0], &b->k_ready[1]}) mbar_init(x, 8);
-    for (uint64_t* x : {&b->p_ready, &b->o_free}) mbar_init(x, 4);
+    for (uint64_t* x : {&b->s_ready[0], &b->s_ready[1], &b->k_ready[0], &b->k_ready[1]}) mbar_init(x, 8);
+    for (uint64_t* x : {&b->p_ready, &b->o_free[0], &b->o_free[1]}) mbar_init(x, 4);
     b->dead = 0;
     b->poisoned = -1;
     b->local = 0;

@@ -36,7 +36,9 @@ def check_poisoned(got, clean, same_o, same_s):
 
 
 def prompts(d, lens):
-    return kda.lin_prefill(d["q"], d["k"], d["v"], offsets(lens), g=d["g"], initial_state=d["state"])
+    call = kda.LinPrefill(d["q"], d["k"], d["v"], offsets(lens), g=d["g"], initial_state=d["state"]).run()
+    assert call.device_status() == 0
+    return call.o, call.final_state
 
 
 # ------------------------------------------------------------------ values that are not finite
@@ -60,3 +62,28 @@ def test_first_chunk_of_a_later_segment(dk, dv):
     for t in range(5, 2600, 128):
         bad, same_o, same_s = poison(d, lens, [(0, t, 1, 9)])
         check_poisoned(prompts(bad, lens), clean, same_o, same_s)
+
+
+@pytest.mark.parametrize("dk,dv", SHAPES)
+@pytest.mark.parametrize("most", [120, 390])
+def test_chains_of_a_cta_one_after_the_other(dk, dv, most):
+    """Many more chains than CTAs, and in each channels whose values are not finite in its first and its last
+    chunk: what one chain notes must not hide what the chain before it is still asked for."""
+    n, H = 240, 4
+    g = torch.Generator().manual_seed(dk + dv + most)
+    lens = torch.randint(1, most + 1, (n,), generator=g).tolist()
+    d = inputs(dk + 2 * dv + most, sum(lens), H, 2, dk, dv, "bf16", "g", n=n)
+    clean = prompts(d, lens)
+    at = []
+    for s in range(n):
+        for h in range(H):
+            if (s + h) % 5 == 4:  # (and some chains without any)
+                continue
+            at += [(s, lens[s] - 1, h, dv - 1), (s, 0, h, dv - 1), (s, lens[s] - 1, h, dv - 2),
+                   (s, max(0, lens[s] - 9), h, dv // 2), (s, int(lens[s] * 0.7), h, 0)]
+    bad, same_o, same_s = poison(d, lens, at)
+    call = kda.LinPrefill(bad["q"], bad["k"], bad["v"], offsets(lens), g=bad["g"], initial_state=bad["state"])
+    for _ in range(5):
+        call.run()
+        check_poisoned((call.o, call.final_state), clean, same_o, same_s)
+    assert call.device_status() == 0
