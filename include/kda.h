@@ -765,7 +765,10 @@ kda_status_t kda_kv_write(const kda_kv_write_args* args, void* stream);
  * they multiply (the tensor cores' operand type), each an error of at most 2^-8
  * of the term.  Which of the two forms is taken, and so how an o rounds, may
  * depend on the gates of later tokens of the sequence; results are the same
- * bits for the same call every time.
+ * bits for the same call every time.  In prompts of bf16 whose decays span up
+ * to 2^64 within 128 tokens the products q.k and their sums with v carry a
+ * factor of up to 2^33 either way: they are meant to stay below 2^94, and lose
+ * bits below 2^-92.
  *
  * One step of a host that drafts tokens:
  *   kda_lin_draft   o of the drafted tokens, states as they were

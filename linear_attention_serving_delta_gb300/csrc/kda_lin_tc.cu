@@ -4,11 +4,11 @@
 // Chunks of C = 128 tokens, with G_i = sum_{m <= i} log2 alpha_m within a chunk:
 //
 //   P = Q K^T                          tcgen05
-//   P~_ij = 2^{-G_j} P_ij, j <= i      rounded to bf16, into P's columns of TMEM
-//   O = 2^{G_i} (Q S + P~ V)           tcgen05, P~ from TMEM; S rounded to bf16 for this alone
+//   P~_ij = 2^{M - G_j} P_ij, j <= i   rounded to bf16, into P's columns of TMEM
+//   O = 2^{G_i - M} (Q 2^M S + P~ V)   tcgen05, P~ from TMEM; 2^M S rounded to bf16 for this alone
 //   S <- 2^{G_C} S + K~^T V            K~_j = 2^{G_C - G_j} k_j in three bf16 parts, A from TMEM
 //
-// That is for a weak chunk, |G| <= 64: both factors stay within fp32 and bf16 by far, and
+// That is for a weak chunk, |G| <= 64, with M the middle of the G: no factor is above 2^33, and
 // one of them is left to the epilogue.  In a strong one P~_ij = 2^{G_i - G_j} P_ij, the
 // difference taken before the exponential (over whole blocks of 32 tokens as a product of two
 // factors <= 1), and the queries are multiplied by theirs, Q~_i = 2^{G_i} q_i in bf16 beside P~.
@@ -465,7 +465,7 @@ __device__ void weight_role(const LinParams& p, const LinTcArgs& a, char* sm, Ta
       const bool strong = gh.strong != 0;
       if (row == 0) b->scaled_q = strong;
       if (!strong) {
-        // 2^{-G_j} P_ij for j <= i; 64 columns at a time, over columns that have been read
+        // 2^{M - G_j} P_ij for j <= i; 64 columns at a time, over columns that have been read
 #pragma unroll 1
         for (int c = 0; c < C; c += 64) {
           uint32_t pk[32];
@@ -706,6 +706,7 @@ __device__ void state_role(const LinParams& p, const LinTcArgs& a, char* sm, Tai
       const int live = min(C, ch.len - t);
       const bool has = t > 0 || ch.from != -1;
       LinDecay next;
+      float lift;
       // K~ of a phase: 32 channels and TH tokens, transposed on the way to TMEM
       auto make_k = [&](int ph) {
         const int m = ph / (C / S::kTok), tok0 = ph % (C / S::kTok) * S::kTok + half * TH;
@@ -749,6 +750,7 @@ __device__ void state_role(const LinParams& p, const LinTcArgs& a, char* sm, Tai
       auto gates = [&]() -> bool {
         if (!wait(&b->g_full[n & 1], (n >> 1) & 1) || !wait(&b->k_full[ring.st], ring.ph)) return false;
         next = lin_decay(b->gates[n & 1].total);
+        lift = b->gates[n & 1].lift;
         return true;
       };
       // with two places the first quarter of K~ beside the product of the chunk before, else behind it
@@ -785,11 +787,14 @@ __device__ void state_role(const LinParams& p, const LinTcArgs& a, char* sm, Tai
         if (n > 0 && !wait(&b->o_full, (n - 1) & 1)) return;
         if (has && holds) {
           char* st = sm + S::kS;
+          const float2 lift2 = make_float2(lift, lift);
 #pragma unroll
-          for (int u = 0; u < N; u += 8)
-            *reinterpret_cast<uint4*>(st + sw_off(d, (col + u) / 8, DK * 128)) =
-                make_uint4(tc::pack2(s[u], s[u + 1]), tc::pack2(s[u + 2], s[u + 3]), tc::pack2(s[u + 4], s[u + 5]),
-                           tc::pack2(s[u + 6], s[u + 7]));
+          for (int u = 0; u < N; u += 8) {
+            uint32_t pk[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) pk[z] = pack2(mul2(make_float2(s[u + 2 * z], s[u + 2 * z + 1]), lift2));
+            *reinterpret_cast<uint4*>(st + sw_off(d, (col + u) / 8, DK * 128)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          }
           // (nothing of the chain precedes its first chunk)
           if (t > 0 && *reinterpret_cast<volatile int32_t*>(&b->poisoned) == i)
 #pragma unroll 1

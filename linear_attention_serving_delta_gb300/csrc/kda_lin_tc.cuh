@@ -50,20 +50,23 @@ constexpr int kLinFirst = 6;
 constexpr int kLinDirectTokens = 2048;
 
 // The gates of a chunk of one head, with G_i the sum of log2 alpha up to token i.  A
-// chunk is weak while |G| <= kLinWeak: weights are then split as 2^{G_i} 2^{-G_j}.
+// chunk is weak while |G| <= kLinWeak: weights are then split as 2^{G_i - M} 2^{M - G_j}, with
+// M the middle of the G, a whole number, so that neither factor is above 2^33 (2^{-G_j} by itself
+// would take products from 2^64 on out of fp32) and M scales without rounding.
 constexpr float kLinWeak = 64.f;
 struct LinGateHead {
   float w[kLinChunk];    // 2^{G_C - G_j}
-  // weak: 2^{-G_j}; strong: 2^ of the sum over what follows the token in its block of 32
+  // weak: 2^{M - G_j}; strong: 2^ of the sum over what follows the token in its block of 32
   float col[kLinChunk];
   float total;           // G_C
   int32_t strong;
-  int32_t pad[2];
+  float lift;            // weak: 2^M; strong: 1
+  int32_t pad;
   float block[4];        // the sums over the blocks of 32
 };
 struct LinGates {
   LinGateHead head;
-  float row[kLinChunk];  // weak: 2^{G_i}; strong: the sum from the block's start on
+  float row[kLinChunk];  // weak: 2^{G_i - M}; strong: the sum from the block's start on
 };
 static_assert(sizeof(LinGateHead) % 16 == 0 && sizeof(LinGates) % 16 == 0, "bulk copies");
 
@@ -165,21 +168,29 @@ __device__ __forceinline__ void make_gates(const LinParams& p, int64_t tok0, int
   if (lane >= 16) before = before + t1;
   if (lane >= 24) before = before + t2;
   const LogSum all = (t0 + t1) + (t2 + t3);
-  float from_start[4], w[4], col[4], row[4];
+  LogSum from_start[4];
+  float w[4], col[4], row[4], low = 0.f;
   bool far = false;
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     if ((lane & 7) != 0) G[u] = prev + G[u];
-    const LogSum x = before + G[u];
-    from_start[u] = x.i + x.f;
+    const LogSum x = from_start[u] = before + G[u];
     w[u] = exp2f(log_diff(all, x));
-    far |= fabsf(from_start[u]) > kLinWeak;  // (a NaN is not: it leaves the tokens before it as they are)
+    // (a NaN is not far, nor the lowest: it leaves the tokens before it as they are)
+    far |= fabsf(x.i + x.f) > kLinWeak;
+    low = fminf(low, x.i + x.f);
   }
   const bool strong = __any_sync(0xffffffffu, far);
 #pragma unroll
+  for (int o = 16; o > 0; o >>= 1) low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
+  const float mid = strong ? 0.f : rintf(0.5f * low);
+  // 2^n for whole n (NaN: 1, beside a factor that is NaN)
+  auto octaves = [](float n) { return __int_as_float(((int)n + 127) << 23); };
+#pragma unroll
   for (int u = 0; u < 4; ++u) {
-    col[u] = exp2f(strong ? log_diff(end, G[u]) : -from_start[u]);
-    row[u] = strong ? G[u].i + G[u].f : exp2f(from_start[u]);
+    const LogSum x = from_start[u];
+    col[u] = strong ? exp2f(log_diff(end, G[u])) : exp2f(-x.f) * octaves(mid - x.i);
+    row[u] = strong ? G[u].i + G[u].f : exp2f(x.f) * octaves(x.i - mid);
   }
   reinterpret_cast<float4*>(out->head.w)[lane] = make_float4(w[0], w[1], w[2], w[3]);
   reinterpret_cast<float4*>(out->head.col)[lane] = make_float4(col[0], col[1], col[2], col[3]);
@@ -187,6 +198,7 @@ __device__ __forceinline__ void make_gates(const LinParams& p, int64_t tok0, int
   if (lane == 0) {
     out->head.total = all.i + all.f;
     out->head.strong = strong;
+    out->head.lift = octaves(mid);
   }
   if ((lane & 7) == 7) out->head.block[lane >> 3] = end.i + end.f;
 }

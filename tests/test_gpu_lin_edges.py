@@ -1,12 +1,14 @@
 """Linear attention with a decay for each head where values that are not finite meet
-the borders of chunks, segments and chains: corners beside those of test_gpu_lin.py,
-with its inputs and bounds.
+the borders of chunks, segments and chains, and where products are far from 1: corners
+beside those of test_gpu_lin.py, with its inputs and bounds.
 """
+import math
+
 import pytest
 import torch
 
 from linear_attention_serving_delta_gb300 import kda
-from test_gpu_lin import inputs, offsets
+from test_gpu_lin import check_prefill, inputs, offsets
 
 pytestmark = pytest.mark.gpu
 
@@ -87,3 +89,41 @@ def test_chains_of_a_cta_one_after_the_other(dk, dv, most):
         call.run()
         check_poisoned((call.o, call.final_state), clean, same_o, same_s)
     assert call.device_status() == 0
+
+
+# ------------------------------------------------------------------ range
+@pytest.mark.parametrize("dk,dv", SHAPES)
+def test_large_products_in_decaying_chunks(dk, dv):
+    """Chunks that decay by nearly 2^64 and products q.k of some 2^70: o of 2^70 is well within bf16 and fp32."""
+    lens, H = [300, 128, 40], 2
+    d = inputs(3 * dk + dv, sum(lens), H, H, dk, dv, "bf16", None, n=3)
+    d["q"], d["k"], d["state"] = d["q"] * 2.0 ** 33, d["k"] * 2.0 ** 33, d["state"] * 2.0 ** 33
+    d["slope"] = torch.tensor([63.0, 40.0], device="cuda") / 128 * math.log(2.0)
+    o, final = kda.lin_prefill(d["q"], d["k"], d["v"], offsets(lens), slope=d["slope"], initial_state=d["state"])
+    check_prefill(d, lens, H, dk, "bf16", o, final, 1.0)
+
+
+@pytest.mark.parametrize("dk,dv", SHAPES)
+def test_small_products_in_decaying_chunks(dk, dv):
+    """And products of some 2^-60, which the factors of such a chunk must not push out of bf16."""
+    lens, H = [300, 128, 40], 2
+    d = inputs(5 * dk + dv, sum(lens), H, H, dk, dv, "bf16", None, n=3)
+    d["q"], d["k"], d["state"] = d["q"] * 2.0 ** -32, d["k"] * 2.0 ** -32, d["state"] * 2.0 ** -32
+    d["slope"] = torch.tensor([63.0, 40.0], device="cuda") / 128 * math.log(2.0)
+    o, final = kda.lin_prefill(d["q"], d["k"], d["v"], offsets(lens), slope=d["slope"], initial_state=d["state"])
+    check_prefill(d, lens, H, dk, "bf16", o, final, 1.0)
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128), (256, 64)])
+def test_gates_that_are_not_numbers_in_decaying_chunks(dk, dv):
+    """Tokens before one whose gate is NaN keep their bits, whatever their chunk decays by."""
+    lens, H, t = [300], 2, 240
+    d = inputs(dk, 300, H, H, dk, dv, "bf16", "g", n=1)
+    d["g"] = torch.full_like(d["g"], -1.1)  # log2 alpha -0.41: 53 in a chunk
+    clean = prompts(d, lens)
+    d["g"][t, 1] = float("nan")
+    o, final = prompts(d, lens)
+    same = torch.ones(300, H, dtype=torch.bool, device="cuda")
+    same[t:, 1] = False
+    assert torch.equal(o[same], clean[0][same]) and torch.equal(final[:, 0], clean[1][:, 0])
+    assert not torch.isfinite(o[t:, 1].float()).any() and not torch.isfinite(final[:, 1]).any()
