@@ -73,6 +73,10 @@ __device__ __forceinline__ LinSeq lin_seq(const LinParams& p, int32_t s) {
   return r;
 }
 
+// SMs of a GB300, which grids are sized by.  On a part with fewer of them results are the
+// same, in more waves.
+constexpr int kLinSms = 152;
+
 constexpr float kLinLog2e = 1.4426950408889634f;
 // An alpha below 2^-kLinMaxDecay counts as 0 (so the sums of logarithms stay finite)
 constexpr float kLinMaxDecay = 1024.f;

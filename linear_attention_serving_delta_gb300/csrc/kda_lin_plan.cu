@@ -27,7 +27,6 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kBuckets = 2560;
-constexpr int kLinMostSegments = 640;  // slots of any path, and two
 
 // A sequence as its segments need it
 struct LinMine {
@@ -311,7 +310,7 @@ int lin_tile_width(const LinParams& p) { return p.dk > 128 || p.dv <= 64 ? 64 : 
 
 LinShare lin_tc_share(const LinParams& p) {
   const int w = lin_tile_width(p);
-  return LinShare{(p.dv + w - 1) / w, kLinSlots, kLinChunk, kLinMinSegment, kLinFirst, kLinDirectTokens, true};
+  return LinShare{(p.dv + w - 1) / w, kLinTcSlots, kLinChunk, kLinMinSegment, kLinFirst, kLinDirectTokens, true};
 }
 
 LinLayout lin_layout(const LinParams& p, const LinShare& sh) {

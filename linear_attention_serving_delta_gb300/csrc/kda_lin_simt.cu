@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 3) lin_simt(const LinParams p, const
 // these took 70) in steps of 16 (of 32: 55 us where these took 47)
 LinShare share(const LinParams& p) {
   const int cols = 32 * cols_of(p);
-  return LinShare{(p.dv + cols - 1) / cols, 3 * kLinSlots, 16, 2, 8, 32, false};
+  return LinShare{(p.dv + cols - 1) / cols, kLinSimtSlots, 16, 2, 8, 32, false};
 }
 
 template <typename T, int DK, int NC>

@@ -16,7 +16,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxDraft = KDA_LIN_MAX_DRAFT;
-constexpr int kLinSms = 152;
 
 // A CTA's slice of a state: DK x DVS elements, a float4 of VPT for each thread
 // (narrow: at most 32 columns, for calls too small to fill the GPU otherwise)

@@ -276,7 +276,7 @@ __device__ void copy_role(const LinParams& p, const LinTcArgs& a, const CUtensor
 // The products of the outputs: Q K^T, then P~ V and Q~ S over it.  P's columns take
 // the next chunk once both have been issued: an issuer's MMAs execute in order.
 template <int DK, int DV>
-__device__ void mma_out_role(const LinParams& p, const LinTcArgs& a, const CUtensorMap* mo, char* sm, Tail* b) {
+__device__ void mma_out_role(const LinParams& p, const LinTcArgs& a, char* sm, Tail* b) {
   using S = Shape<DK, DV>;
   const uint32_t tmem = __shfl_sync(0xffffffffu, b->tmem, 0);
   constexpr uint32_t id_qk = idesc_bf16(C, C), id_n = idesc_bf16(C, DV, 0, 1);
@@ -893,7 +893,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (warp == 0) {
         if ((threadIdx.x & 31) == 0) copy_role<DK, DV, kLocal>(p, a, &mq, &mk, &mv, sm, b);
       } else if (warp == 1) {
-        if (!kLocal) mma_out_role<DK, DV>(p, a, &mo, sm, b);
+        if (!kLocal) mma_out_role<DK, DV>(p, a, sm, b);
       } else if (warp == 2) {
         mma_state_role<DK, DV, kLocal>(p, a, sm, b);
       }

@@ -42,8 +42,11 @@ __host__ __device__ __forceinline__ int32_t lin_chains(int32_t n, int32_t m, int
 struct LinHead {
   int32_t items, locals, splits;  // entries of the lists, for one head and tile
 };
-// The CTAs that chains are shared out to, and the fewest chunks of a segment
-constexpr int kLinSlots = 152;
+// The CTAs that chains are shared out to: one an SM on the tensor cores, three on the CUDA cores
+constexpr int kLinTcSlots = kLinSms, kLinSimtSlots = 3 * kLinSms;
+// Segments of one sequence at most: one for each CTA of the second pass, and the first
+constexpr int kLinMostSegments = kLinSimtSlots + 1;
+// The fewest chunks of a segment
 constexpr int kLinMinSegment = 8;
 // A chunk without its outputs takes 2.3 us where one with them takes 3.9
 constexpr int kLinFirst = 6;
