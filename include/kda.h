@@ -849,7 +849,9 @@ kda_status_t kda_lin_decode(const kda_lin_decode_args* args, void* stream);
  *
  *   o_i = scale (e^{G_i} S^T q_i + sum_{j on the path of i} e^{G_i - G_j} (q_i . k_j) v_j)
  *
- * which is what kda_lin_decode would give along each path by itself.
+ * which is what kda_lin_decode would give along each path by itself, but for the
+ * roundings above: decode reads o from the state in fp32, so with bf16 inputs a
+ * drafted token's o and the same token's decoded one are not the same bits.
  */
 #define KDA_LIN_MAX_DRAFT 64
 typedef struct {

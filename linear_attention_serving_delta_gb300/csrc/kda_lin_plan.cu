@@ -15,7 +15,7 @@
 // second pass gives the outputs of the other segments side by side.  So k segments are
 // k - 1 chains of either pass, and the first is as much shorter as its outputs take longer.
 // Keys and values of those between the first and the last are read twice, from L2 where
-// the call's fit it.  One block plans, in about 10 us: lengths, scans over the block,
+// the call's fit it.  One block plans, in about 11 us: lengths, scans over the block,
 // and a search for the length of the segments that tries 32 at a time (one after the
 // other took 4 us more, and writing a prompt's segments by one thread 6 us).
 #include <algorithm>

@@ -3,12 +3,15 @@
 // (commit), drafted tokens over the states as they are (draft).  Formulas in
 // include/kda.h.
 //
-// All three are bound by HBM.  Decode and commit read every state once, write it once and do
-// little else: a CTA takes one (row, head), or a slice of a wide one, with 16-byte loads
+// Decode and commit are bound by HBM: they read every state once, write it once and do
+// little else.  A CTA takes one (row, head), or a slice of a wide one, with 16-byte loads
 // straight into registers, all issued before anything waits, and writes them back from
 // there.  256 rows of 32 heads of 128 x 128: 158 us, 6.85 TB/s, what a copy reaches; one row
-// 2.9 us, a launch.  The commit of 64 trees of 8 tokens takes 51 us, 5.3 TB/s (the path comes
-// between its reads and its writes); their draft, which only reads, 36 us, 4.2 TB/s.
+// 3.3 us, a launch.  The commit of 64 trees of 8 tokens takes 51 us, 5.3 TB/s (the path comes
+// between its reads and its writes).  Their draft, which only reads, takes 36 us, 4.2 TB/s, and
+// is bound by the loads that four CTAs an SM keep in flight (DRAM 50% busy); fp32 drafts go
+// token by token and are bound by instructions (64 chains of 8 tokens, 16 heads of 128 x 128:
+// 72 us, where bf16 takes 21).
 #include "kda_lin.cuh"
 
 namespace kda {
@@ -608,7 +611,7 @@ cudaError_t launch_draft_mma(const LinParams& p, cudaStream_t stream) {
   };
   if (p.max_seqlen <= 16) return run(lin_draft_mma<DK, 1, 1>, 16, 1);
   // as many groups as eight warps allow while the CTAs are at most two an SM: nine trees of
-  // 60 tokens, 32 heads and 64 columns 23.2 -> 19.1 us, but 64 trees and 128 columns 134 -> 165
+  // 60 tokens, 32 heads of 128 x 64 21.9 -> 14.4 us, but 64 trees and 128 x 128 131 -> 168
   const bool split = (int64_t)p.num_seqs * p.H <= 2 * kLinSms;
   if (p.max_seqlen <= 32)
     return split && wide <= 4 ? run(lin_draft_mma<DK, 2, 1>, 32, 2) : run(lin_draft_mma<DK, 2, 2>, 32, 1);

@@ -28,12 +28,12 @@
 // (kda_lin_tc.cuh), made before: as a role of their own they took the longest.
 //
 // What it takes (a copy reaches 6.8 TB/s): 8,192 tokens of 32 heads of 128 x 128 in
-// 123 us, of which the plan 10, the first pass 46, the joining of its states 8 and the second
-// pass 64, each traced by itself; eight prompts of 1,024 to 32,768 tokens in 1.37 ms, 4.2 TB/s.
+// 124 us, of which the plan 11, the first pass 46, the joining of its states 8 and the second
+// pass 67, each traced by itself; eight prompts of 1,024 to 32,768 tokens in 1.39 ms, 4.1 TB/s.
 // An SM does a chunk in 3.9 to 4.6 us there, against 2.9 of HBM for its 128 KB at an
-// SM's share; what is beyond that is 256 chains that 152 SMs cannot share evenly.  (With two
-// parts of K~ for three: 108 us and 1.29 ms.)  64 columns a chain take 3.5 us a chunk all the
-// same: then a chunk's chain of waits -- products, state, operand, products, outputs --
+// SM's share; what is beyond that is 256 chains that 152 SMs cannot share evenly.  (Of
+// these the third part of K~ takes 15 us and 80 us, 2^M 1.5 and 18.)  64 columns a chain take
+// 3.5 us a chunk all the same: then a chunk's chain of waits -- products, state, operand, products, outputs --
 // bounds it, one chain an SM.
 //
 // Roles run side by side on the schedulers' small instruction caches: unrolled ones of
